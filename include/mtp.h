@@ -330,6 +330,147 @@ mtp_status spec_verify_noalloc(mtp_stream stream, int32_t rows, int32_t depth, i
 mtp_status kv_rollback(mtp_t h, mtp_stream stream, int32_t rows, const int32_t* d_n_acc,
                        int32_t* d_target_len, int32_t depth, int32_t zero_tail);
 
+/*
+ * ------------------------------------------------ paged 4-bit KV cache
+ *
+ * A cache for the model that verifies the drafts: it appends a block of
+ * positions per row and round, is trimmed by the round's device-side counts,
+ * and is read by every query of the block. Pages are planned on the GPU from
+ * device-side lengths, so a round needs no host read before its next one.
+ *
+ * Layout. K and V are two arrays [n_pages][n_kv][page][kv_q4_row_bytes(dh)] of
+ * bytes, page a multiple of 16 slots, dh in {64, 128, 256}. A row holds one
+ * slot of one head: dh/2 bytes of codes (element 2i in the low half of byte i,
+ * 2i+1 in the high half), then dh/16 bytes of scales. A code is e2m1 (sign,
+ * then 0, .5, 1, 1.5, 2, 3, 4, 6), a scale e4m3 for 16 elements:
+ *   element = e2m1(code) * e4m3(scale of its 16) * 2^exp[head]
+ * with an optional exponent per head, which puts the head's range into the
+ * scales' (2^-9 to 448). Slot s is slot s % page of page s / page.
+ */
+typedef struct {
+  void* k;               /* device, 16-byte aligned */
+  void* v;
+  const int32_t* k_exp;  /* device [n_kv], in [-64, 64]; NULL = 0 */
+  const int32_t* v_exp;
+  int32_t n_kv, head_dim, page, n_pages; /* n_pages * page < 2^31 */
+} kv_q4_cache;
+
+/* Bytes of one slot of one head, dh/2 + dh/16; 0 if head_dim is not supported. */
+size_t kv_q4_row_bytes(int32_t head_dim);
+
+/*
+ * kv_page_plan — block tables and slot maps from the rows' lengths.
+ * Row r's pages cover d_cover[r] positions; the caller keeps the first
+ * d_keep[r] <= d_cover[r] of them (the rest were rejected) and appends
+ * d_new[r] >= 0. With held = ceil(cover / page) and
+ * want = ceil((keep + new) / page), the row gives held - want pages back or
+ * takes want - held more.
+ *   d_table [rows][max_pages] in/out: the pages of row r are its first
+ *       ceil(cover / page) entries; entries past them carry no meaning.
+ *   d_free [n_pages] in/out: the free pages, a stack of
+ *       n_free = n_pages - sum_r held entries (every page is a row's or free).
+ *   d_cover_out [rows] out: keep + new, the d_cover of the next call and the
+ *       cache length that kv_q4_attend takes; d_cover where the row is refused.
+ *       Must not overlap d_cover.
+ *   d_start [rows + 1] out: the rows' appended positions are packed, row r's at
+ *       [start[r], start[r + 1]).
+ *   d_slot, d_pos [max_tokens] out: slot and position of every packed position;
+ *       -1 past the last one, and d_slot -1 for a refused row.
+ * Order: pages given back go onto the stack from the last row's last page to
+ * the first row's first, then pages are taken off it from the first row on, so
+ * a plan that undoes another leaves the stack as it was. The lengths are inputs
+ * only and no entry that is read is written: a call repeated on the same
+ * lengths gives the same result.
+ * A row is refused (its pages stay) with 1 << MTP_ERR_KV_CAPACITY in d_status
+ * when the stack runs out before it (in row order) or it would need more than
+ * max_pages, and with 1 << MTP_ERR_BAD_ARG when its lengths are invalid, its
+ * positions pass max_tokens; d_slot is -1 (and BAD_ARG set) also where an entry
+ * of the table or of the stack is no page. d_status may be NULL.
+ * Errors: BAD_ARG (rows outside 1..4096, page not a multiple of 16,
+ * rows * max_pages or n_pages * page of 2^31 and more, a null pointer).
+ */
+mtp_status kv_page_plan(mtp_stream stream, int32_t rows, int32_t page, int32_t max_pages, int32_t n_pages,
+                        int32_t max_tokens, const int32_t* d_cover, const int32_t* d_keep, const int32_t* d_new,
+                        int32_t* d_table, int32_t* d_free, int32_t* d_cover_out, int32_t* d_start, int32_t* d_slot,
+                        int32_t* d_pos, int32_t* d_status);
+
+/*
+ * kv_q4_append — round K and V rows to 4 bits and write them to their slots.
+ *   d_k, d_v: element (t, head, i) at t * tok_stride + head * head_stride + i,
+ *       strides in elements (a slice of a fused q/k/v projection will do)
+ *   d_slot [tokens]: kv_page_plan's; -1 skips the position, any other value
+ *       outside [0, n_pages * page) skips it and sets 1 << MTP_ERR_BAD_ARG in
+ *       d_status. Two positions with the same slot leave either's row.
+ * Rounding, per 16 elements y = x * 2^-exp: scale = e4m3(max|y| / 6) (fp32
+ * quotient, to nearest even, at most 448), code = the e2m1 value nearest to
+ * |y| / scale (exact, the even code when two are as near, 6 beyond 6); a zero
+ * scale gives zero codes. 16 elements with a NaN or an infinity among them are
+ * stored as NaN (scale 0x7F) and set 1 << MTP_ERR_NONFINITE.
+ * kv_q4_read — the values of slots, [tokens][n_kv][head_dim] contiguous in
+ * dtype; zeros where d_slot skips. Errors of both: BAD_ARG.
+ */
+mtp_status kv_q4_append(mtp_stream stream, const kv_q4_cache* cache, int32_t tokens, const void* d_k,
+                        int64_t k_tok_stride, int64_t k_head_stride, const void* d_v, int64_t v_tok_stride,
+                        int64_t v_head_stride, int32_t dtype, const int32_t* d_slot, int32_t* d_status);
+mtp_status kv_q4_read(mtp_stream stream, const kv_q4_cache* cache, int32_t tokens, const int32_t* d_slot, void* d_k,
+                      void* d_v, int32_t dtype, int32_t* d_status);
+
+/*
+ * kv_q4_attend — attention of each row's newest positions over its pages.
+ * Row r has queries [start[r], start[r + 1]) of the packed d_q and
+ * L = d_len[r] cached positions, its own among them: its i-th query stands at
+ * position L - n + i (n its query count) and sees the positions up to its own,
+ * with window > 0 only the last `window` of those. Per query head (n_q / n_kv
+ * of them share a KV head):
+ *   s_j = scale * q . k_j,  out = sum_j softmax(s)_j v_j,  lse = log sum_j exp(s_j)
+ * A query that sees nothing gets zeros and lse = -inf.
+ *   d_q: element (t, head, i) at t * tok_stride + head * head_stride + i
+ *   d_out [tokens][n_q][head_dim] contiguous in dtype; d_lse [tokens][n_q] float
+ *       (optional)
+ *   d_table [rows][max_pages], d_start [rows + 1], d_len [rows]: kv_page_plan's
+ *   max_q: the most queries of a row, as the caller knows it; it chooses the
+ *       kernel's shape. Rows that have more are still computed.
+ *   d_workspace: kv_q4_attend_workspace_bytes(...) bytes, 16-byte aligned.
+ * Scores and sums are fp32. q enters as f16 after a power-of-two scaling per
+ * query and head (exact for bf16 but for elements 2^-16 below the largest);
+ * fp32 q as two f16 parts (22 bits), and the softmax weights likewise.
+ * A page entry outside [0, n_pages) sets 1 << MTP_ERR_BAD_ARG in d_status and
+ * its positions are not read; a bounded wait that ran out sets
+ * 1 << MTP_ERR_TIMEOUT. Errors: BAD_ARG.
+ */
+size_t kv_q4_attend_workspace_bytes(const kv_q4_cache* cache, int32_t n_q, int32_t max_q, int32_t dtype);
+mtp_status kv_q4_attend(mtp_stream stream, const kv_q4_cache* cache, int32_t rows, int32_t n_q, int32_t tokens,
+                        const void* d_q, int64_t tok_stride, int64_t head_stride, int32_t dtype,
+                        const int32_t* d_table, int32_t max_pages, const int32_t* d_start, const int32_t* d_len,
+                        int32_t max_q, float scale, int32_t window, void* d_out, float* d_lse, int32_t* d_status,
+                        void* d_workspace);
+
+/*
+ * spec_logprobs — log probabilities of given tokens under raw logits (no
+ * transforms), with their ranks, the entropy and the likeliest alternatives.
+ *   d_logits [n] rows of vocab logits (dtype), row_stride elements apart: for
+ *       a verified block, spec_verify's d_logits as rows * (depth + 1) rows
+ *   d_tok [n]: the given tokens; -1 (d_out_tok past a row's committed tokens)
+ *       gives log probability 0 and rank -1, any other id outside [0, vocab)
+ *       the same with 1 << MTP_ERR_BAD_ARG in d_status
+ *   d_logprob [n] out: x_t - log sum_j exp(x_j)
+ *   d_rank [n] out (optional): tokens before t in the order (logit descending,
+ *       id ascending)
+ *   d_entropy [n] out (optional): -sum_j p_j log p_j, in nats
+ *   d_top_id, d_top_lp [n][top] out: the first `top` (0..64) tokens of that
+ *       order and their log probabilities; id -1 and -inf past the last token
+ *       with p > 0 possible (logit above -inf)
+ * Logits of -inf are masked tokens; a row with nothing else gives -inf (0 for
+ * entropy). A NaN or +inf sets 1 << MTP_ERR_NONFINITE; the row's outputs then
+ * carry no meaning, ids stay in range. d_workspace:
+ * spec_logprobs_workspace_bytes(n, vocab, top) bytes, 16-byte aligned.
+ * Errors: BAD_ARG.
+ */
+size_t spec_logprobs_workspace_bytes(int32_t n, int32_t vocab, int32_t top);
+mtp_status spec_logprobs(mtp_stream stream, int32_t n, int32_t vocab, const void* d_logits, int64_t row_stride,
+                         int32_t dtype, const int32_t* d_tok, int32_t top, float* d_logprob, int32_t* d_rank,
+                         float* d_entropy, int32_t* d_top_id, float* d_top_lp, int32_t* d_status, void* d_workspace);
+
 /* Test hook of the streaming verify's bounded waits: the next spec_verify
  * call that takes the streaming path leaves ring stage `stage` of every task
  * unfilled (a copy that never lands) and gives each wait `wait_polls` polls,

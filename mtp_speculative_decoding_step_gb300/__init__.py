@@ -34,6 +34,8 @@ EXPORTS = (
     "mtp_profile_read", "mtp_kernel_launches", "spec_verify_noalloc",
     "mtp_depth_ctl_create", "mtp_depth_ctl_free", "mtp_depth_ctl_next", "mtp_depth_ctl_observe",
     "mtp_depth_ctl_state", "mtp_set_draft_head", "mtp_test_verify_stall",
+    "kv_q4_row_bytes", "kv_page_plan", "kv_q4_append", "kv_q4_read", "kv_q4_attend_workspace_bytes",
+    "kv_q4_attend", "spec_logprobs_workspace_bytes", "spec_logprobs",
 )
 
 
@@ -63,6 +65,12 @@ class Sampling(ctypes.Structure):
 
 class KV(ctypes.Structure):
     _fields_ = [("k", ctypes.c_void_p), ("v", ctypes.c_void_p), ("len", ctypes.c_void_p)]
+
+
+class Q4Cache(ctypes.Structure):
+    _fields_ = [("k", ctypes.c_void_p), ("v", ctypes.c_void_p), ("k_exp", ctypes.c_void_p),
+                ("v_exp", ctypes.c_void_p), ("n_kv", ctypes.c_int32), ("head_dim", ctypes.c_int32),
+                ("page", ctypes.c_int32), ("n_pages", ctypes.c_int32)]
 
 
 _lib = None
@@ -104,9 +112,23 @@ def lib():
         L.mtp_profile_kind_name.restype = ctypes.c_char_p
         L.mtp_profile_read.argtypes = [vp, vp, vp]
         L.mtp_kernel_launches.restype = ctypes.c_int64
+        i64, cache = ctypes.c_int64, ctypes.POINTER(Q4Cache)
+        L.kv_q4_row_bytes.argtypes = [i32]
+        L.kv_q4_row_bytes.restype = sz
+        L.kv_page_plan.argtypes = [vp, i32, i32, i32, i32, i32] + [vp] * 10
+        L.kv_q4_append.argtypes = [vp, cache, i32, vp, i64, i64, vp, i64, i64, i32, vp, vp]
+        L.kv_q4_read.argtypes = [vp, cache, i32, vp, vp, vp, i32, vp]
+        L.kv_q4_attend_workspace_bytes.argtypes = [cache, i32, i32, i32]
+        L.kv_q4_attend_workspace_bytes.restype = sz
+        L.kv_q4_attend.argtypes = [vp, cache, i32, i32, i32, vp, i64, i64, i32, vp, i32, vp, vp, i32,
+                                   ctypes.c_float, i32, vp, vp, vp, vp]
+        L.spec_logprobs_workspace_bytes.argtypes = [i32, i32, i32]
+        L.spec_logprobs_workspace_bytes.restype = sz
+        L.spec_logprobs.argtypes = [vp, i32, i32, vp, i64, i32, vp, i32] + [vp] * 7
         for name in ("mtp_load", "mtp_free", "mtp_get_lengths", "mtp_set_lengths", "mtp_flush", "mtp_draft",
                      "spec_verify", "spec_verify_noalloc", "kv_rollback", "mtp_profile_enable",
-                     "mtp_profile_read", "mtp_test_verify_stall"):
+                     "mtp_profile_read", "mtp_test_verify_stall", "kv_page_plan", "kv_q4_append", "kv_q4_read",
+                     "kv_q4_attend", "spec_logprobs"):
             getattr(L, name).restype = ctypes.c_int
         _lib = L
     return _lib
@@ -304,6 +326,139 @@ def kv_rollback(h: Handle, rows: int, depth: int, n_acc=None, target_len=None, z
     rc = lib().kv_rollback(h.ptr, _stream(stream), rows, _ptr(n_acc), _ptr(target_len), depth,
                            1 if zero_tail else 0)
     _check(rc, "kv_rollback")
+
+
+def _want(ok: bool, where: str):
+    """Checks that the C side cannot make (shapes, element types): a bad argument like its own."""
+    if not ok:
+        raise MTPError(9, where)
+
+
+def _whole(where: str, *tensors, n=None):
+    """Contiguous int32 tensors (None passes), of n elements if n is given."""
+    for t in tensors:
+        if t is not None and (t.element_size() != 4 or t.is_floating_point() or not t.is_contiguous()
+                              or (n is not None and t.numel() != n)):
+            raise MTPError(9, where)
+
+
+def kv_q4_row_bytes(head_dim: int) -> int:
+    return lib().kv_q4_row_bytes(head_dim)
+
+
+class PagedCache:
+    """A kv_q4_cache and the tensors it points to."""
+
+    def __init__(self, c, keep):
+        self.c = c
+        self.ref = ctypes.byref(c)
+        self._keep = keep
+
+
+def kv_q4_cache(k, v, k_exp=None, v_exp=None) -> PagedCache:
+    """k, v: uint8 [n_pages, n_kv, page, kv_q4_row_bytes(head_dim)]; k_exp, v_exp: int32 [n_kv] exponents."""
+    n_pages, n_kv, page, row = k.shape
+    _want(k.shape == v.shape and k.element_size() == v.element_size() == 1 and k.is_contiguous()
+          and v.is_contiguous() and row in (36, 72, 144), "kv_q4_cache")
+    _whole("kv_q4_cache", k_exp, v_exp, n=n_kv)
+    return PagedCache(Q4Cache(_ptr(k), _ptr(v), _ptr(k_exp), _ptr(v_exp), n_kv, row * 16 // 9, page, n_pages),
+                      (k, v, k_exp, v_exp))
+
+
+def kv_page_plan(cover, keep, new, table, free, cover_out, start, slot, pos, page: int, status=None, stream=None):
+    """cover, keep, new, cover_out [rows]; table [rows, max_pages]; free [n_pages]; start [rows + 1];
+    slot, pos [max_tokens]; all int32. See kv_page_plan in include/mtp.h."""
+    rows, max_pages = table.shape
+    _whole("kv_page_plan", cover, keep, new, cover_out, n=rows)
+    _whole("kv_page_plan", table, free, start, slot, pos)
+    _want(start.numel() == rows + 1 and slot.numel() == pos.numel(), "kv_page_plan")
+    rc = lib().kv_page_plan(_stream(stream), rows, page, max_pages, free.numel(), slot.numel(), _ptr(cover),
+                            _ptr(keep), _ptr(new), _ptr(table), _ptr(free), _ptr(cover_out), _ptr(start), _ptr(slot),
+                            _ptr(pos), _ptr(status))
+    _check(rc, "kv_page_plan")
+
+
+def _dtype_q4(where: str, *tensors) -> int:
+    """The dtype code of tensors of one type, fp32 or bf16."""
+    import torch
+    dt = tensors[0].dtype
+    _want(dt in (torch.bfloat16, torch.float32) and all(t.dtype == dt for t in tensors), where)
+    return MTP_DTYPE_BF16 if dt == torch.bfloat16 else MTP_DTYPE_F32
+
+
+def kv_q4_append(cache: PagedCache, k, v, slot, status=None, stream=None):
+    """k, v: [tokens, n_kv, head_dim], fp32 or bf16, the last dimension contiguous; slot [tokens] int32."""
+    c = cache.c
+    shape = (slot.numel(), c.n_kv, c.head_dim)
+    _want(tuple(k.shape) == shape and tuple(v.shape) == shape and k.stride(2) == 1 and v.stride(2) == 1, "kv_q4_append")
+    _whole("kv_q4_append", slot)
+    rc = lib().kv_q4_append(_stream(stream), cache.ref, shape[0], _ptr(k), k.stride(0), k.stride(1), _ptr(v), v.stride(0),
+                            v.stride(1), _dtype_q4("kv_q4_append", k, v), _ptr(slot), _ptr(status))
+    _check(rc, "kv_q4_append")
+
+
+def kv_q4_read(cache: PagedCache, slot, k, v, status=None, stream=None):
+    """slot [tokens] int32; k, v: [tokens, n_kv, head_dim] out, contiguous, fp32 or bf16."""
+    c = cache.c
+    shape = (slot.numel(), c.n_kv, c.head_dim)
+    _want(tuple(k.shape) == shape and tuple(v.shape) == shape and k.is_contiguous() and v.is_contiguous(), "kv_q4_read")
+    _whole("kv_q4_read", slot)
+    rc = lib().kv_q4_read(_stream(stream), cache.ref, shape[0], _ptr(slot), _ptr(k), _ptr(v),
+                          _dtype_q4("kv_q4_read", k, v), _ptr(status))
+    _check(rc, "kv_q4_read")
+
+
+def kv_q4_attend_workspace_bytes(cache: PagedCache, n_q: int, max_q: int, dtype) -> int:
+    """dtype: the queries' torch dtype."""
+    import torch
+    return lib().kv_q4_attend_workspace_bytes(cache.ref, n_q, max_q, MTP_DTYPE_BF16 if dtype == torch.bfloat16
+                                              else MTP_DTYPE_F32)
+
+
+def kv_q4_attend(cache: PagedCache, q, table, start, length, out, workspace, max_q: int, scale: float, window: int = 0,
+                 lse=None, status=None, stream=None):
+    """q: [tokens, n_q, head_dim], fp32 or bf16, the last dimension contiguous; table [rows, max_pages], start [rows + 1],
+    length [rows] int32; out [tokens, n_q, head_dim]; lse [tokens, n_q] float; workspace:
+    kv_q4_attend_workspace_bytes(cache, n_q, max_q, q.dtype) bytes."""
+    tokens, n_q, dh = q.shape
+    rows, max_pages = table.shape
+    _want(dh == cache.c.head_dim and q.stride(2) == 1 and out.shape == q.shape and out.is_contiguous()
+          and (lse is None or (lse.element_size() == 4 and lse.numel() == tokens * n_q and lse.is_contiguous())),
+          "kv_q4_attend")
+    _whole("kv_q4_attend", table, start, length)
+    _want(start.numel() == rows + 1 and length.numel() == rows, "kv_q4_attend")
+    dt = _dtype_q4("kv_q4_attend", q, out)
+    _want(workspace.numel() * workspace.element_size()
+          >= lib().kv_q4_attend_workspace_bytes(cache.ref, n_q, max_q, dt), "kv_q4_attend")
+    rc = lib().kv_q4_attend(_stream(stream), cache.ref, rows, n_q, tokens, _ptr(q), q.stride(0), q.stride(1), dt,
+                            _ptr(table), max_pages, _ptr(start), _ptr(length), max_q, scale, window, _ptr(out), _ptr(lse),
+                            _ptr(status), _ptr(workspace))
+    _check(rc, "kv_q4_attend")
+
+
+def spec_logprobs_workspace_bytes(n: int, vocab: int, top: int) -> int:
+    return lib().spec_logprobs_workspace_bytes(n, vocab, top)
+
+
+def spec_logprobs(logits, tok, logprob, workspace, rank=None, entropy=None, top_id=None, top_lp=None, status=None,
+                  stream=None):
+    """logits [n, V] fp32 or bf16, rows contiguous; tok [n] int32; logprob [n] float out; optional outputs rank [n]
+    int32, entropy [n] float, top_id [n, top] int32 and top_lp [n, top] float; workspace:
+    spec_logprobs_workspace_bytes(n, V, top) bytes."""
+    n, V = logits.shape
+    top = 0 if top_id is None else top_id.shape[1]
+    _whole("spec_logprobs", tok, rank, n=n)
+    _whole("spec_logprobs", top_id, n=n * top)
+    for t, size in ((logprob, n), (entropy, n), (top_lp, n * top)):
+        _want(t is None or (t.element_size() == 4 and t.is_floating_point() and t.is_contiguous() and t.numel() == size),
+              "spec_logprobs")
+    _want(logits.stride(1) == 1 and (top_id is None) == (top_lp is None)
+          and workspace.numel() * workspace.element_size() >= lib().spec_logprobs_workspace_bytes(n, V, top),
+          "spec_logprobs")
+    rc = lib().spec_logprobs(_stream(stream), n, V, _ptr(logits), logits.stride(0), _dtype_q4("spec_logprobs", logits),
+                             _ptr(tok), top, _ptr(logprob), _ptr(rank), _ptr(entropy), _ptr(top_id), _ptr(top_lp),
+                             _ptr(status), _ptr(workspace))
+    _check(rc, "spec_logprobs")
 
 
 PROFILE_KINDS = ("fc", "qkv", "qkv_post", "attention", "o_proj", "gate_up", "down", "lm_head", "sample",

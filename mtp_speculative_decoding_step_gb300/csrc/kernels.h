@@ -416,6 +416,9 @@ bool launch_verify_greedy_flat(const VerifyArgs& a, void* d_part, size_t part_by
 constexpr int kMaxDevices = 64;
 int device_sm_count();
 
+// Whether a paged 4-bit cache's description is in order.
+bool q4_cache_ok(const kv_q4_cache* c);
+
 // spec_verify with the streaming path allowed or not (the workspace of
 // spec_verify_workspace_bytes holds its lists; a descriptors-only scratch does not).
 mtp_status spec_verify_impl(mtp_stream stream, int32_t rows, int32_t depth, int32_t vocab, const float* d_logits,
