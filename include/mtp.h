@@ -433,7 +433,9 @@ mtp_status kv_q4_read(mtp_stream stream, const kv_q4_cache* cache, int32_t token
  *   d_workspace: kv_q4_attend_workspace_bytes(...) bytes, 16-byte aligned.
  * Scores and sums are fp32. q enters as f16 after a power-of-two scaling per
  * query and head (exact for bf16 but for elements 2^-16 below the largest);
- * fp32 q as two f16 parts (22 bits), and the softmax weights likewise.
+ * fp32 q as two f16 parts (22 bits). The softmax weights are f16 (11 bits;
+ * fp32 q: two parts, 22 bits) down to 2^-21 of the largest, below that in steps
+ * of 2^-31 of it.
  * A page entry outside [0, n_pages) sets 1 << MTP_ERR_BAD_ARG in d_status and
  * its positions are not read; a bounded wait that ran out sets
  * 1 << MTP_ERR_TIMEOUT. Errors: BAD_ARG.

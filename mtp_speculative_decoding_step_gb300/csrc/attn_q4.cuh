@@ -1,0 +1,1092 @@
+// Attention over the paged 4-bit cache (kv_q4_attend) on the 5th-generation
+// tensor cores.
+//
+//   s_jt = c_j q_j . k_t,  out_j = sum_t softmax(s)_jt v_t
+//
+// for the query rows j of one KV head (positions x the query heads that share
+// it), c_j = scale log2 e 2^(exponents). Both products are formed transposed,
+// with 128 cached positions (or 128 head dimensions) as the MMA's M and the
+// query rows as its N, so that a block of a few queries costs N = 16..64
+// columns instead of a padded 128-row tile, and one kernel serves single
+// tokens, verify blocks and prompts:
+//
+//   S^T[128 positions][N] = K[128][DH] . Q^T      A = K in tensor memory
+//   O^T[DH][N]           += V^T[DH][128] . P^T    A = V in shared memory
+//
+// A block owns an equal run of (row, KV head, query tile, 128-position tile)
+// tasks, whatever the rows' lengths are; a (row, head, query tile) that its run
+// does not hold whole leaves a partial (O, running maximum, sum) that a second
+// kernel joins. 16 warps:
+//   warp 0        copies the tile's 4-bit rows (cp.async.bulk) into two rings
+//   warp 1        issues the MMAs; S of tile i+1 goes before P.V of tile i
+//   dequantisers  thread = position: codes x scale as f16, exact (at most six
+//                 significant bits). K goes to tensor memory (the thread's row
+//                 is the operand's lane), V to 128B-swizzled shared memory
+//                 (position-major, read by the MMA as an M-major operand)
+//   softmax       reads S^T in the MMA fragment layout (a thread holds 8 rows x
+//                 2 columns of a 16 x 8 patch), so column sums stay in registers
+//                 and stmatrix.trans lays P^T out for the MMA
+// The running maximum is lazy: weights are 2^(y - m) with m seven below a
+// maximum seen, and m moves (O is rescaled in tensor memory) only when some y
+// passes m + 15; until then a tile needs one vote and no reduction. f16 holds
+// weights up to 2^15 and, 2^-14 being its smallest normal number, rounds all
+// within 2^21 of the largest to 11 bits.
+//
+// fp32 queries: q and the weights each enter as two f16 parts in separate
+// columns (22 bits), N / 2 rows a tile.
+//
+// Every wait is bounded: on expiry the block raises the status word, waits for
+// its copies, frees its tensor memory and returns.
+#pragma once
+#include <mutex>
+
+#include "common.cuh"
+#include "kernels.h"
+#include "q4.cuh"
+#include "tc_common.cuh"
+
+namespace mtp {
+
+constexpr int kT = 128;          // positions per tile
+constexpr int kAttnThreads = 512;
+constexpr float kUnset = -INFINITY;
+constexpr unsigned kQ4WaitLimit = 1u << 20;  // polls: 10 ms at the least, where a tile takes about a microsecond
+
+struct Q4AttnArgs {
+  const uint8_t *kc, *vc;
+  const int32_t *k_exp, *v_exp, *table, *start, *len;
+  const void* q;
+  long long ts, hs;
+  void* out;
+  float* lse;
+  int32_t* status;
+  int4* part_meta;               // [2 * blocks] (row, head, query tile, 1 = a start | 2 = an end | 4 = present)
+  float2* part_ml;               // [2 * blocks][rows of a tile] (m, sum)
+  float* part_o;                 // [2 * blocks][rows of a tile][DH]
+  int rows, n_q, n_kv, page, n_pages, max_pages, tokens, window;
+  int q_vec;                     // 16-byte loads of q are aligned
+  float scale;
+};
+
+// ------------------------------------------------------------ task walk
+
+// One (row, KV head, query tile): `rows_tile` query rows of position-major
+// order (position i, head h of the group) -> i * G + h.
+struct Seg {
+  int r, g, j;     // row, KV head, query tile
+  int a0, n, L;    // first packed position, positions, cached length
+  int lo, end;     // cached positions that some query row sees: [lo, end)
+  int t0, cnt;     // their tiles
+  int p0, p1;      // positions of the first and the last query row
+
+  // whether some (row, position) pair of a tile may be out of sight
+  __device__ bool edge(int tile, int window) const {
+    return tile * kT + kT - 1 > p0 || (window > 0 && tile * kT <= p1 - window);
+  }
+  // its number among the run's edge tiles: p0 and p1 lie less than kT apart,
+  // so two tiles at most hold a causal border, and two a window's
+  __device__ int edge_index(int tile) const {
+    return tile * kT + kT - 1 > p0 ? min(max(tile - p0 / kT, 0), 1) : 2 + min(tile - t0, 1);
+  }
+};
+
+struct Walk {
+  const Q4AttnArgs* a;
+  int G, RT;       // query heads per KV head, query rows per tile
+
+  __device__ void row(int r, int& a0, int& n, int& L) const {
+    a0 = min(max(__ldg(a->start + r), 0), a->tokens);
+    n = min(max(__ldg(a->start + r + 1), a0), a->tokens) - a0;
+    L = min(max(__ldg(a->len + r), 0), a->max_pages * a->page);
+  }
+  __device__ int tiles(int n) const { return (n * G + RT - 1) / RT; }
+  __device__ void span(int n, int L, int j, int& lo, int& end, int& t0, int& cnt) const {
+    const int i0 = j * RT / G, i1 = (min(n * G, (j + 1) * RT) - 1) / G;
+    end = max(L - n + i1 + 1, 0);
+    lo = a->window > 0 ? max(0, L - n + i0 - a->window + 1) : 0;
+    t0 = 0;
+    cnt = 1;  // one tile at least: rows that see nothing are written too
+    if (lo < end) {
+      t0 = lo / kT;
+      cnt = (end - 1) / kT - t0 + 1;
+    } else {
+      end = lo;
+    }
+  }
+  __device__ int per_head(int n, int L) const {
+    int sum = 0;
+    for (int j = 0; j < tiles(n); ++j) {
+      int lo, end, t0, cnt;
+      span(n, L, j, lo, end, t0, cnt);
+      sum += cnt;
+    }
+    return sum;
+  }
+  __device__ void load(Seg& s, int r, int g, int j) const {
+    s.r = r;
+    s.g = g;
+    s.j = j;
+    row(r, s.a0, s.n, s.L);
+    span(s.n, s.L, j, s.lo, s.end, s.t0, s.cnt);
+    s.p0 = s.L - s.n + j * RT / G;
+    s.p1 = s.L - s.n + (min(s.n * G, (j + 1) * RT) - 1) / G;
+  }
+  __device__ void next(Seg& s) const {
+    int r = s.r, g = s.g, j = s.j + 1;
+    if (j == tiles(s.n)) {
+      j = 0;
+      if (++g == a->n_kv) {
+        g = 0;
+        int a0, n, L;
+        do {
+          if (++r >= a->rows) return;
+          row(r, a0, n, L);
+        } while (n == 0);
+      }
+    }
+    load(s, r, g, j);
+  }
+};
+
+// ------------------------------------------------------------ PTX
+
+__device__ __forceinline__ uint64_t sdesc_mn(uint32_t addr, uint32_t lbo) {
+  // M-major operand in 128B-swizzled atoms of 64 elements x 8 k: `lbo` bytes
+  // between atoms along M, 1024 between groups of eight k
+  uint64_t d = 0;
+  d |= (uint64_t)((addr >> 4) & 0x3FFF);
+  d |= (uint64_t)((lbo >> 4) & 0x3FFF) << 16;
+  d |= (uint64_t)(1024 >> 4) << 32;
+  d |= (uint64_t)1 << 46;
+  d |= (uint64_t)2 << 61;
+  return d;
+}
+
+// kind::f16 with f16 operands and fp32 accumulators; `a_mn`: A is M-major
+__host__ __device__ constexpr uint32_t idesc_f16(int m, int n, bool a_mn) {
+  return (1u << 4) | ((a_mn ? 1u : 0u) << 15) | ((uint32_t)(n >> 3) << 17) | ((uint32_t)(m >> 4) << 24);
+}
+
+__device__ __forceinline__ void mma_f16_ss(uint32_t d, uint64_t a, uint64_t b, uint32_t idesc, uint32_t acc) {
+  tc::mma_bf16(d, a, b, idesc, acc);  // the descriptor names the types
+}
+__device__ __forceinline__ void mma_f16_ts(uint32_t d, uint32_t a, uint64_t b, uint32_t idesc, uint32_t acc) {
+  asm volatile(
+      "{\n\t.reg .pred p;\n\t"
+      "setp.ne.b32 p, %4, 0;\n\t"
+      "tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, p;\n\t}" ::"r"(d),
+      "r"(a), "l"(b), "r"(idesc), "r"(acc)
+      : "memory");
+}
+
+__device__ __forceinline__ void tc_fence_before() { asm volatile("tcgen05.fence::before_thread_sync;" ::: "memory"); }
+__device__ __forceinline__ void tc_fence_after() { asm volatile("tcgen05.fence::after_thread_sync;" ::: "memory"); }
+__device__ __forceinline__ void tc_wait_ld() { asm volatile("tcgen05.wait::ld.sync.aligned;" ::: "memory"); }
+__device__ __forceinline__ void tc_wait_st() { asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory"); }
+__device__ __forceinline__ void fence_async() { asm volatile("fence.proxy.async.shared::cta;" ::: "memory"); }
+
+// 16 lanes x 8 C columns in the MMA fragment layout: registers 4b..4b+3 hold
+// (row l/4, columns 8b + 2(l%4), +1) and the same of row l/4 + 8.
+template <int C>
+__device__ __forceinline__ void tmem_ld_frag(uint32_t t, uint32_t* r);
+template <>
+__device__ __forceinline__ void tmem_ld_frag<1>(uint32_t t, uint32_t* r) {
+  asm volatile("tcgen05.ld.sync.aligned.16x256b.x1.b32 {%0,%1,%2,%3}, [%4];"
+               : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]) : "r"(t));
+}
+template <>
+__device__ __forceinline__ void tmem_ld_frag<2>(uint32_t t, uint32_t* r) {
+  asm volatile("tcgen05.ld.sync.aligned.16x256b.x2.b32 {%0,%1,%2,%3,%4,%5,%6,%7}, [%8];"
+               : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7])
+               : "r"(t));
+}
+template <>
+__device__ __forceinline__ void tmem_ld_frag<4>(uint32_t t, uint32_t* r) {
+  asm volatile("tcgen05.ld.sync.aligned.16x256b.x4.b32 {%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15}, [%16];"
+               : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7]),
+                 "=r"(r[8]), "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]), "=r"(r[14]), "=r"(r[15])
+               : "r"(t));
+}
+template <>
+__device__ __forceinline__ void tmem_ld_frag<8>(uint32_t t, uint32_t* r) {
+  tmem_ld_frag<4>(t, r);
+  tmem_ld_frag<4>(t + 32, r + 16);
+}
+
+__device__ __forceinline__ void tmem_ld_rows16(uint32_t t, uint32_t (&r)[16]) {  // lane's 16 columns
+  asm volatile("tcgen05.ld.sync.aligned.32x32b.x16.b32 {%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15}, [%16];"
+               : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7]),
+                 "=r"(r[8]), "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]), "=r"(r[14]), "=r"(r[15])
+               : "r"(t));
+}
+__device__ __forceinline__ void tmem_st_rows16(uint32_t t, const uint32_t (&r)[16]) {
+  asm volatile("tcgen05.st.sync.aligned.32x32b.x16.b32 [%16], {%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15};" ::"r"(r[0]),
+               "r"(r[1]), "r"(r[2]), "r"(r[3]), "r"(r[4]), "r"(r[5]), "r"(r[6]), "r"(r[7]), "r"(r[8]), "r"(r[9]),
+               "r"(r[10]), "r"(r[11]), "r"(r[12]), "r"(r[13]), "r"(r[14]), "r"(r[15]), "r"(t)
+               : "memory");
+}
+
+__device__ __forceinline__ void stmatrix_x4_t(uint32_t addr, uint32_t a, uint32_t b, uint32_t c, uint32_t d) {
+  asm volatile("stmatrix.sync.aligned.m8n8.x4.trans.shared.b16 [%0], {%1,%2,%3,%4};" ::"r"(addr), "r"(a), "r"(b),
+               "r"(c), "r"(d)
+               : "memory");
+}
+
+__device__ __forceinline__ float ex2(float x) {
+  float y;
+  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+  return y;
+}
+__device__ __forceinline__ uint32_t pack_f16(float lo, float hi) {
+  uint32_t d;
+  asm("cvt.rn.f16x2.f32 %0, %1, %2;" : "=r"(d) : "f"(hi), "f"(lo));
+  return d;
+}
+
+// Barrier over the 128 threads of a softmax warpgroup, and a vote over them.
+__device__ __forceinline__ void group_sync(int id) { asm volatile("barrier.cta.sync.aligned %0, 128;" ::"r"(id) : "memory"); }
+__device__ __forceinline__ bool group_any(int id, bool p) {
+  uint32_t any;
+  asm volatile(
+      "{\n\t.reg .pred p, q;\n\t"
+      "setp.ne.b32 p, %2, 0;\n\t"
+      "barrier.cta.red.or.aligned.pred q, %1, 128, p;\n\t"
+      "selp.u32 %0, 1, 0, q;\n\t}"
+      : "=r"(any)
+      : "r"(id), "r"((uint32_t)p)
+      : "memory");
+  return any != 0;
+}
+
+// ------------------------------------------------------------ shape
+
+template <int DH, int N, bool WIDE>
+struct Shape {
+  static constexpr int kRow = q4_row_bytes(DH);
+  static constexpr int RT = WIDE ? N / 2 : N;            // query rows per tile
+  static constexpr int SG = N == 128 ? 2 : 1;            // softmax warpgroups
+  static constexpr int NW = N / SG;                      // columns per softmax warpgroup
+  static constexpr int NC = WIDE ? NW / 2 : NW;          // query rows per softmax warpgroup
+  static constexpr int MB = DH == 256 ? 2 : 1;           // M blocks of O^T (64 dims: duplicated rows)
+  static constexpr int KC = DH / 2;                      // tensor-memory columns of a K operand
+  static constexpr int SB = MB * N + 2 * N + 2 * KC <= 512 ? 2 : 1;  // S and K buffers
+  static constexpr uint32_t cO = 0, cS = MB * N, cK = cS + SB * N, cEnd = cK + SB * KC;
+  static constexpr uint32_t kCols = cEnd <= 128 ? 128 : (cEnd <= 256 ? 256 : 512);
+  // shared memory
+  static constexpr int kRaw = kT * kRow;                 // a tile's rows of K or V
+  static constexpr int kV = kT * DH * 2, kQ = N * DH * 2, kP = N * kT * 2;
+  static constexpr int kMetaBytes = 8192;
+  static constexpr int kRoom = (227 * 1024 - 1024 - kMetaBytes - kV - kQ - kP) / kRaw;
+  static constexpr int KS = kRoom >= 16 ? 8 : (kRoom + 1) / 2;  // ring stages
+  static constexpr int VS = kRoom >= 16 ? 8 : kRoom / 2;
+  static constexpr int oV = 0, oQ = kV, oP = oQ + kQ, oRawK = oP + kP, oRawV = oRawK + KS * kRaw;
+  static constexpr int oMeta = (oRawV + VS * kRaw + 127) / 128 * 128;
+  static constexpr int kSmem = oMeta + kMetaBytes + 1024;
+  static_assert(VS >= 1 && cEnd <= 512, "shape");
+};
+
+// Small state of a block.
+template <int DH>
+struct Meta {
+  uint64_t rawk_full[8], rawk_empty[8], rawv_full[8], rawv_empty[8];
+  uint64_t k_full[2], k_empty[2], s_full[2], s_empty[2];
+  uint64_t v_full[2], v_empty[2], p_full, p_empty, q_full;
+  uint32_t valid_k[8], valid_v[8];   // bit p: piece p of the stage was copied
+  uint32_t tmem;
+  int fail;
+  int w_r, w_g, w_j, w_o;            // the block's first task
+  long long w_n;                     // its tasks
+  long long scan[kAttnThreads / 32];
+  alignas(16) float cm[128][2];      // per query row: c, m
+  float f[128];                      // per query row: factor of a moved m, then 1 / sum
+  alignas(16) int lim[128];          // per query row: its position
+  long long dst[128];                // per query row: row of out and lse, or -1
+  float red[4][128];                 // per warp of a softmax group and query row
+  uint32_t copied[2];                // tiles of K and of V whose copies were issued
+  uint64_t drain;                    // the MMAs of a run that gave up
+  uint32_t nan_run[2];               // by the run's parity: 1 + the last run that noted something in nan_bits
+  uint32_t nan_bits[2][4][DH / 16][4];  // edge tile, 16 dimensions: positions whose V is NaN there
+};
+static_assert(sizeof(Meta<256>) <= 8192, "meta");
+
+// Bounded wait that gives up as soon as another role has failed.
+__device__ __forceinline__ bool wait(uint64_t* bar, uint32_t parity, volatile int* fail) {
+  const uint32_t b = smem_u32(bar);
+  for (unsigned i = 0; i < kQ4WaitLimit; ++i) {
+    if (mbar_try(b, parity)) return true;
+    if ((i & 1023) == 1023 && *fail) return false;
+  }
+  *fail = 1;
+  return false;
+}
+
+// Keeps a value read from tensor memory behind the wait that completes it.
+__device__ __forceinline__ void pin(uint32_t& x) { asm volatile("" : "+r"(x)); }
+
+// Whether a query at `pos` sees a position of an edge tile whose V is NaN in
+// 16-dimension block b.
+template <int B>
+__device__ __noinline__ bool sees_nan(int t0, int cnt, int p0, int p1, const uint32_t (*bits)[B][4], int b, int pos,
+                                      int window) {
+  Seg s;
+  s.t0 = t0;
+  s.p0 = p0;
+  s.p1 = p1;
+  for (int tile = t0; tile < t0 + cnt; ++tile) {
+    if (!s.edge(tile, window)) continue;
+    for (int w = 0; w < 4; ++w) {
+      uint32_t m = bits[s.edge_index(tile)][b][w];
+      while (m) {
+        const int t = tile * kT + 32 * w + __ffs(m) - 1;
+        m &= m - 1;
+        if (t <= pos && (window == 0 || pos - t < window)) return true;
+      }
+    }
+  }
+  return false;
+}
+
+// The same for a whole warp, with one answer.
+__device__ __forceinline__ bool wait_warp(uint64_t* bar, uint32_t parity, volatile int* fail) {
+  return __all_sync(0xFFFFFFFFu, wait(bar, parity, fail));
+}
+
+template <int DH, int N, bool WIDE>
+__global__ void __launch_bounds__(kAttnThreads, 1) k_q4_attn(const __grid_constant__ Q4AttnArgs a) {
+  using S = Shape<DH, N, WIDE>;
+  extern __shared__ uint8_t smem_raw[];
+  uint8_t* base = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
+  auto& M = *reinterpret_cast<Meta<DH>*>(base + S::oMeta);
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  constexpr bool kOneDq = S::SG == 2;                    // one warpgroup dequantises K and V
+  constexpr int kSoftWarp = kOneDq ? 8 : 12;             // first softmax warp
+  constexpr int kSoftWarps = 4 * S::SG;
+
+  if (threadIdx.x == 0) {
+    for (int i = 0; i < 8; ++i) {
+      mbar_init(smem_u32(&M.rawk_full[i]), 1);
+      mbar_init(smem_u32(&M.rawv_full[i]), 1);
+      mbar_init(smem_u32(&M.rawk_empty[i]), 4);
+      mbar_init(smem_u32(&M.rawv_empty[i]), 4);
+    }
+    for (int i = 0; i < 2; ++i) {
+      mbar_init(smem_u32(&M.k_full[i]), 4);
+      mbar_init(smem_u32(&M.k_empty[i]), 1);
+      mbar_init(smem_u32(&M.s_full[i]), 1);
+      mbar_init(smem_u32(&M.s_empty[i]), kSoftWarps);
+      mbar_init(smem_u32(&M.v_full[i]), 4);
+      mbar_init(smem_u32(&M.v_empty[i]), 1);
+    }
+    mbar_init(smem_u32(&M.p_full), kSoftWarps);
+    mbar_init(smem_u32(&M.p_empty), 1);
+    mbar_init(smem_u32(&M.q_full), kSoftWarps);
+    M.fail = 0;
+    M.w_n = 0;
+    M.copied[0] = M.copied[1] = 0;
+    M.nan_run[0] = M.nan_run[1] = 0;
+    mbar_init(smem_u32(&M.drain), 1);
+    asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
+  }
+  if (warp == 0) {
+    asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(smem_u32(&M.tmem)),
+                 "r"(S::kCols)
+                 : "memory");
+    asm volatile("tcgen05.relinquish_alloc_permit.cta_group::1.sync.aligned;" ::: "memory");
+  }
+  pdl_wait();
+  pdl_trigger();
+  if (threadIdx.x < 2) a.part_meta[2 * blockIdx.x + threadIdx.x] = make_int4(0, 0, 0, 0);
+
+  // the block's run of tasks: rows' task counts scanned, consecutive rows per thread
+  Walk walk{&a, a.n_q / a.n_kv, S::RT};
+  {
+    const int per = (a.rows + kAttnThreads - 1) / kAttnThreads;
+    const int r0 = min((int)threadIdx.x * per, a.rows), r1 = min(r0 + per, a.rows);
+    long long sum = 0;
+    for (int r = r0; r < r1; ++r) {
+      int a0, n, L;
+      walk.row(r, a0, n, L);
+      if (blockIdx.x == 0 && L != a.len[r]) flag_status(a.status, MTP_ERR_BAD_ARG);
+      sum += (long long)walk.per_head(n, L) * a.n_kv;
+    }
+    long long inc = sum;
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+      const long long u = __shfl_up_sync(0xFFFFFFFFu, inc, o);
+      if (lane >= o) inc += u;
+    }
+    if (lane == 31) M.scan[warp] = inc;
+    tc_fence_before();
+    __syncthreads();
+    tc_fence_after();
+    long long all = 0;
+    for (int w = 0; w < kAttnThreads / 32; ++w) {
+      if (w == warp) inc += all;
+      all += M.scan[w];
+    }
+    // equal runs; with fewer tasks than blocks the first blocks take one each
+    const long long nb = max(1LL, min((long long)gridDim.x, all)), b = min((long long)blockIdx.x, nb);
+    const long long w0 = all * b / nb, w1 = min(all * (b + 1) / nb, all);
+    long long at = inc - sum;
+    if (w0 < w1 && at <= w0 && w0 < at + sum) {
+      for (int r = r0; r < r1; ++r) {
+        int a0, n, L;
+        walk.row(r, a0, n, L);
+        const int ph = walk.per_head(n, L);
+        if (w0 < at + (long long)ph * a.n_kv) {
+          int o = (int)((w0 - at) % ph), j = 0;
+          const int g = (int)((w0 - at) / ph);
+          for (;; ++j) {
+            int lo, end, t0, cnt;
+            walk.span(n, L, j, lo, end, t0, cnt);
+            if (o < cnt) break;
+            o -= cnt;
+          }
+          M.w_r = r;
+          M.w_g = g;
+          M.w_j = j;
+          M.w_o = o;
+          M.w_n = w1 - w0;
+          break;
+        }
+        at += (long long)ph * a.n_kv;
+      }
+    }
+    __syncthreads();
+  }
+  const uint32_t tmem = M.tmem;
+  volatile int* fail = &M.fail;
+  const long long todo = M.w_n;
+  Seg s;
+  int off = 0;
+  if (todo > 0) {
+    walk.load(s, M.w_r, M.w_g, M.w_j);
+    off = M.w_o;
+  }
+  long long left = todo;
+  const int ps = a.page % kT == 0 ? kT : (a.page % 64 == 0 ? 64 : (a.page % 32 == 0 ? 32 : 16));  // slots per copy
+
+  if (warp == 0) {
+    // ---------------------------------------------------------- copies
+    uint32_t it = 0;
+    bool ok = true;
+    while (left > 0 && ok) {
+      const int nt = (int)min((long long)(s.cnt - off), left);
+      const int32_t* tab = a.table + (long long)s.r * a.max_pages;
+      for (int i = 0; i < nt && ok; ++i, ++it) {
+        const int t0 = (s.t0 + off + i) * kT + lane * ps;  // lane p: piece p of the tile
+        const bool need = lane * ps < kT && t0 < s.end && t0 + ps > s.lo;
+        int id = need ? __ldg(tab + t0 / a.page) : 0;
+        const bool good = need && id >= 0 && id < a.n_pages;
+        if (need && !good) flag_status(a.status, MTP_ERR_BAD_ARG);
+        const uint32_t mask = __ballot_sync(0xFFFFFFFFu, good);
+        const long long src = good ? (((long long)id * a.n_kv + s.g) * a.page + t0 % a.page) * S::kRow : 0;
+        const uint32_t bytes = ps * S::kRow;
+#pragma unroll
+        for (int kv = 0; kv < 2; ++kv) {
+          const int st = it % (kv ? S::VS : S::KS), round = it / (kv ? S::VS : S::KS);
+          uint64_t* full = kv ? &M.rawv_full[st] : &M.rawk_full[st];
+          if (round > 0) ok = wait(kv ? &M.rawv_empty[st] : &M.rawk_empty[st], (round - 1) & 1, fail);
+          ok = __all_sync(0xFFFFFFFFu, ok);
+          if (!ok) break;
+          if (lane == 0) {
+            (kv ? M.valid_v : M.valid_k)[st] = mask;
+            mbar_expect_tx(smem_u32(full), bytes * __popc(mask));
+            M.copied[kv] = it + 1;
+          }
+          __syncwarp();
+          if (good)
+            bulk_g2s(smem_u32(base + (kv ? S::oRawV : S::oRawK) + st * S::kRaw + lane * bytes), (kv ? a.vc : a.kc) + src,
+                     bytes, smem_u32(full));
+        }
+      }
+      left -= nt;
+      off = 0;
+      if (left > 0) walk.next(s);
+    }
+  } else if (warp == 1) {
+    // ---------------------------------------------------------- MMAs
+    if (lane == 0) {
+      constexpr uint32_t idS = idesc_f16(128, N, false), idO = idesc_f16(128, N, true);
+      const uint32_t q = smem_u32(base + S::oQ), p = smem_u32(base + S::oP), v = smem_u32(base + S::oV);
+      uint32_t it = 0, seg = 0;
+      bool ok = true;
+      auto pv = [&](uint32_t i, bool first) {
+        if (!wait(&M.p_full, i & 1, fail)) return false;
+#pragma unroll 1
+        for (int h = 0; h < 2; ++h) {
+          if (!wait(&M.v_full[h], i & 1, fail)) return false;
+          tc_fence_after();
+#pragma unroll
+          for (int k = 0; k < 4; ++k)
+#pragma unroll
+            for (int mb = 0; mb < S::MB; ++mb)
+              mma_f16_ss(tmem + S::cO + mb * N,
+                         sdesc_mn(v + h * (S::kV / 2) + mb * 2 * 8192 + k * 2048, DH == 64 ? 0 : 8192),
+                         tc::sdesc(p + h * N * 128 + k * 32), idO, (first && h == 0 && k == 0) ? 0u : 1u);
+          tc::mma_commit(smem_u32(&M.v_empty[h]));
+        }
+        tc::mma_commit(smem_u32(&M.p_empty));
+        return true;
+      };
+      while (left > 0 && ok) {
+        const int nt = (int)min((long long)(s.cnt - off), left);
+        ok = wait(&M.q_full, seg & 1, fail);
+        for (int i = 0; i < nt && ok; ++i, ++it) {
+          const uint32_t b = it % S::SB, round = it / S::SB;
+          ok = wait(&M.k_full[b], round & 1, fail) && (round == 0 || wait(&M.s_empty[b], (round - 1) & 1, fail));
+          if (!ok) break;
+          tc_fence_after();
+#pragma unroll
+          for (int k = 0; k < DH / 16; ++k)
+            mma_f16_ts(tmem + S::cS + b * N, tmem + S::cK + b * S::KC + k * 8,
+                       tc::sdesc(q + (k / 4) * N * 128 + (k % 4) * 32), idS, k > 0 ? 1u : 0u);
+          tc::mma_commit(smem_u32(&M.k_empty[b]));
+          tc::mma_commit(smem_u32(&M.s_full[b]));
+          if (i > 0) ok = pv(it - 1, i == 1);
+        }
+        if (ok) ok = pv(it - 1, nt == 1);
+        left -= nt;
+        off = 0;
+        ++seg;
+        if (left > 0) walk.next(s);
+      }
+      if (!ok) {  // what was issued ends before its operands and tensor memory go
+        tc::mma_commit(smem_u32(&M.drain));
+        mbar_wait(smem_u32(&M.drain), 0, kQ4WaitLimit);
+      }
+    }
+    __syncwarp();
+  } else if (warp >= 4 && warp < kSoftWarp) {
+    // ---------------------------------------------------------- dequantisers
+    const int quarter = warp & 3, tid = threadIdx.x & 127;
+    const bool do_k = kOneDq || warp < 8, do_v = kOneDq || warp >= 8;
+
+    // position `tid` of tile `i` to tensor memory, as f16
+    auto deq_k = [&](uint32_t i, const Seg& sg, int tile) {
+      const int st = i % S::KS;
+      const uint32_t b = i % S::SB, round = i / S::SB;
+      if (!wait_warp(&M.rawk_full[st], (i / S::KS) & 1, fail)) return false;
+      if (round > 0 && !wait_warp(&M.k_empty[b], (round - 1) & 1, fail)) return false;
+      tc_fence_after();
+      const int t = tile * kT + tid;
+      const bool live = t >= sg.lo && t < sg.end && (M.valid_k[st] >> (tid / ps) & 1);
+      const uint8_t* row = base + S::oRawK + st * S::kRaw + tid * S::kRow;
+      uint32_t sc[DH / 64];  // four scales a word
+#pragma unroll
+      for (int w = 0; w < DH / 64; ++w) sc[w] = reinterpret_cast<const uint32_t*>(row + DH / 2)[w];
+#pragma unroll
+      for (int c = 0; c < DH / 32; ++c) {  // 32 elements: 16 bytes, two scales
+        uint32_t code[4], x[16];
+#pragma unroll
+        for (int w = 0; w < 4; ++w) code[w] = reinterpret_cast<const uint32_t*>(row + 16 * c)[w];
+        const uint32_t s2 = e4m3x2_to_f16x2(sc[c / 2] >> (16 * (c & 1)));
+        const uint32_t slo = __byte_perm(s2, s2, 0x1010), shi = __byte_perm(s2, s2, 0x3232);
+#pragma unroll
+        for (int w = 0; w < 4; ++w) {
+          uint32_t h[4];
+          e2m1x8_to_f16(code[w], h);
+#pragma unroll
+          for (int e = 0; e < 4; ++e) x[4 * w + e] = live ? hmul2_bits(h[e], w < 2 ? slo : shi) : 0u;
+        }
+        tmem_st_rows16(tmem + S::cK + b * S::KC + 16 * c + ((uint32_t)(32 * quarter) << 16), x);
+      }
+      tc_wait_st();
+      tc_fence_before();
+      __syncwarp();
+      if (lane == 0) {
+        mbar_arrive(smem_u32(&M.rawk_empty[st]));
+        mbar_arrive(smem_u32(&M.k_full[b]));
+      }
+      return true;
+    };
+    // tile `i`'s V in two halves of 64 positions; a thread takes half a row
+    auto deq_v = [&](uint32_t i, const Seg& sg, int tile, uint32_t run, bool first) {
+      const int st = i % S::VS;
+      // 0 x NaN would reach rows that do not see the position: where a tile
+      // has such rows, NaN is kept out of the product and noted for the end
+      const bool edge = sg.edge(tile, a.window);
+      if (!wait_warp(&M.rawv_full[st], (i / S::VS) & 1, fail)) return false;
+      const int tt = tid & 63, part = tid >> 6;
+      constexpr int kD = DH / 2;  // elements of a thread
+#pragma unroll 1
+      for (int h = 0; h < 2; ++h) {
+        if (i > 0 && !wait_warp(&M.v_empty[h], (i - 1) & 1, fail)) return false;
+        if (first && h == 0) {
+          // this warp's words, two runs old: their reader is done with them,
+          // since the last run's products are
+          for (int e = lane; e < 4 * (kD / 16) * 2; e += 32)
+            M.nan_bits[run & 1][e / (kD / 8)][part * (kD / 16) + e / 2 % (kD / 16)][(e & 1) * 2 + (quarter & 1)] = 0;
+          __syncwarp();
+        }
+        const int tr = h * 64 + tt, t = tile * kT + tr;
+        const bool live = t >= sg.lo && t < sg.end && (M.valid_v[st] >> (tr / ps) & 1);
+        const uint8_t* row = base + S::oRawV + st * S::kRaw + tr * S::kRow;
+#pragma unroll
+        for (int c = 0; c < kD / 16; ++c) {  // 16 elements: two words, one scale
+          const int d = part * kD + 16 * c;
+          uint32_t sb = row[DH / 2 + d / 16];
+          if (edge && live && (sb & 0x7F) == 0x7F) {
+            sb = 0;
+            atomicOr(&M.nan_bits[run & 1][sg.edge_index(tile)][d / 16][tr >> 5], 1u << (tr & 31));
+            M.nan_run[run & 1] = run + 1;
+          }
+          const uint32_t s2 = e4m3x2_to_f16x2(sb);
+          const uint32_t sv = __byte_perm(s2, s2, 0x1010);
+          uint32_t x[8];
+#pragma unroll
+          for (int w = 0; w < 2; ++w) {
+            uint32_t hh[4];
+            e2m1x8_to_f16(reinterpret_cast<const uint32_t*>(row + d / 2)[w], hh);
+#pragma unroll
+            for (int e = 0; e < 4; ++e) x[4 * w + e] = live ? hmul2_bits(hh[e], sv) : 0u;
+          }
+          uint8_t* dst = base + S::oV + h * (S::kV / 2) + (d / 64) * 8192 + tt * 128;
+#pragma unroll
+          for (int w = 0; w < 2; ++w)
+            *reinterpret_cast<uint4*>(dst + ((((d & 63) / 8 + w) ^ (tt & 7)) << 4)) =
+                make_uint4(x[4 * w], x[4 * w + 1], x[4 * w + 2], x[4 * w + 3]);
+        }
+        fence_async();
+        __syncwarp();
+        if (lane == 0) mbar_arrive(smem_u32(&M.v_full[h]));
+      }
+      if (lane == 0) mbar_arrive(smem_u32(&M.rawv_empty[st]));
+      return true;
+    };
+    uint32_t it = 0, run = 0;
+    bool ok = true;
+    Seg sv = s;        // V lags K by one tile where one group does both
+    int tv = -1;
+    uint32_t rv = 0;
+    bool fv = false;
+    while (left > 0 && ok) {
+      const int nt = (int)min((long long)(s.cnt - off), left);
+      for (int i = 0; i < nt && ok; ++i, ++it) {
+        const int tile = s.t0 + off + i;
+        if (do_k) ok = deq_k(it, s, tile);
+        if (do_v && ok) {
+          if (!kOneDq) {
+            ok = deq_v(it, s, tile, run, i == 0);
+          } else {
+            if (tv >= 0) ok = deq_v(it - 1, sv, tv, rv, fv);
+            sv = s;
+            tv = tile;
+            rv = run;
+            fv = i == 0;
+          }
+        }
+        ok = __all_sync(0xFFFFFFFFu, ok);
+      }
+      left -= nt;
+      off = 0;
+      ++run;
+      if (left > 0) walk.next(s);
+    }
+    if (kOneDq && ok && tv >= 0) deq_v(it - 1, sv, tv, rv, fv);
+  } else if (warp >= kSoftWarp) {
+    // ---------------------------------------------------------- softmax
+    const int sg = (warp - kSoftWarp) >> 2, quarter = warp & 3, bar = 1 + sg;
+    constexpr int NC = S::NC, NB = NC / 8;      // query rows and 8-row blocks of the group
+    const int c0 = sg * NC;                     // its first query row (= column)
+    const int pr = 2 * (lane & 3);              // the thread's column pair in a block
+    const uint32_t lanes = (uint32_t)(32 * quarter) << 16;
+    const int G = walk.G;
+    uint32_t it = 0, run = 0;
+    bool ok = true;  // (a warp that fails leaves with its group, at a vote)
+    while (left > 0) {
+      const int nt = (int)min((long long)(s.cnt - off), left);
+      const bool begins = off == 0, ends = off + nt == s.cnt;
+      // ---- queries: one warp per row, scaled by a power of two to [2^13, 2^14)
+      const int kexp = head_exp(a.k_exp, s.g);
+      for (int j = c0 + quarter; j < c0 + NC; j += 4) {
+        const int f = s.j * S::RT + j, i = f / G, h = s.g * G + f % G;
+        const bool real = f < s.n * G;
+        constexpr int E = DH / 32;
+        float x[E];
+#pragma unroll
+        for (int e = 0; e < E; ++e) x[e] = 0.f;
+        if (real) {
+          const long long at = (long long)(s.a0 + i) * a.ts + (long long)h * a.hs + lane * E;
+          if (WIDE) {
+            const float* src = static_cast<const float*>(a.q) + at;
+            if (a.q_vec && E >= 4) {
+#pragma unroll
+              for (int e = 0; e < E / 4; ++e) {
+                const float4 v = reinterpret_cast<const float4*>(src)[e];
+                x[4 * e] = v.x;
+                x[4 * e + 1] = v.y;
+                x[4 * e + 2] = v.z;
+                x[4 * e + 3] = v.w;
+              }
+            } else {
+#pragma unroll
+              for (int e = 0; e < E; ++e) x[e] = src[e];
+            }
+          } else {
+            const uint16_t* src = static_cast<const uint16_t*>(a.q) + at;
+            if (a.q_vec) {
+              uint32_t u[4];
+              if (E == 8) {
+                const uint4 v = *reinterpret_cast<const uint4*>(src);
+                u[0] = v.x;
+                u[1] = v.y;
+                u[2] = v.z;
+                u[3] = v.w;
+              } else {
+                u[0] = reinterpret_cast<const uint32_t*>(src)[0];
+                if (E == 4) u[1] = reinterpret_cast<const uint32_t*>(src)[1];
+              }
+#pragma unroll
+              for (int e = 0; e < E / 2; ++e) {
+                x[2 * e] = bf16lo(u[e]);
+                x[2 * e + 1] = bf16hi(u[e]);
+              }
+            } else {
+#pragma unroll
+              for (int e = 0; e < E; ++e) x[e] = bf16_to_f(src[e]);
+            }
+          }
+        }
+        float mx = 0.f;
+#pragma unroll
+        for (int e = 0; e < E; ++e) mx = fmaxf(mx, fabsf(x[e]));
+        mx = warp_max(mx);
+        // the exponent of the largest; an infinity or a NaN stays one (and its
+        // row's scores become NaN)
+        const int ex = mx > 0.f && mx < INFINITY ? max((int)(__float_as_uint(mx) >> 23) - 127, -107) : 13;
+        const float up = pow2i(13 - ex);
+        uint32_t hi[E / 2], lo[E / 2];
+#pragma unroll
+        for (int e = 0; e < E / 2; ++e) {
+          const float y0 = x[2 * e] * up, y1 = x[2 * e + 1] * up;
+          hi[e] = pack_f16(y0, y1);
+          const float2 b = f16x2_to_f(hi[e]);
+          lo[e] = pack_f16(y0 - b.x, y1 - b.y);
+        }
+        auto put = [&](int row, const uint32_t (&u)[E / 2]) {
+          const int d = lane * E;
+          uint8_t* p = base + S::oQ + (d / 64) * N * 128 + row * 128 + ((((d & 63) / 8) ^ (row & 7)) << 4) + (d & 7) * 2;
+#pragma unroll
+          for (int e = 0; e < E / 2; ++e) reinterpret_cast<uint32_t*>(p)[e] = u[e];
+        };
+        put(j, hi);
+        if (WIDE) put(N / 2 + j, lo);
+        if (lane == 0) {
+          M.cm[j][0] = ldexpf(a.scale * 1.44269504f, kexp - (13 - ex));
+          M.cm[j][1] = kUnset;
+          M.lim[j] = real ? s.L - s.n + i : -1;
+          M.dst[j] = real ? (long long)(s.a0 + i) * a.n_q + h : -1;
+        }
+      }
+      fence_async();
+      group_sync(bar);
+      if (lane == 0) mbar_arrive(smem_u32(&M.q_full));
+
+      float sum[2 * NB];
+#pragma unroll
+      for (int b = 0; b < 2 * NB; ++b) sum[b] = 0.f;
+
+      bool broken = false;
+      for (int i = 0; i < nt; ++i, ++it) {
+        const uint32_t sb = it % S::SB;
+        ok = wait(&M.s_full[sb], (it / S::SB) & 1, fail) && ok;
+        tc_fence_after();
+        const int t0 = (s.t0 + off + i) * kT;
+        const bool edge = s.edge(s.t0 + off + i, a.window);
+        uint32_t v[2][4 * NB];
+        auto fetch = [&]() {
+#pragma unroll
+          for (int hh = 0; hh < 2; ++hh) {
+            const uint32_t t = tmem + S::cS + sb * N + c0 + lanes + ((uint32_t)(16 * hh) << 16);
+            tmem_ld_frag<NB>(t, v[hh]);
+          }
+          if (WIDE) {
+            uint32_t u[2][4 * NB];
+#pragma unroll
+            for (int hh = 0; hh < 2; ++hh)
+              tmem_ld_frag<NB>(tmem + S::cS + sb * N + c0 + N / 2 + lanes + ((uint32_t)(16 * hh) << 16), u[hh]);
+            tc_wait_ld();
+#pragma unroll
+            for (int hh = 0; hh < 2; ++hh)
+#pragma unroll
+              for (int e = 0; e < 4 * NB; ++e) {
+                pin(v[hh][e]);
+                pin(u[hh][e]);
+                v[hh][e] = __float_as_uint(__uint_as_float(v[hh][e]) + __uint_as_float(u[hh][e]));
+              }
+          } else {
+            tc_wait_ld();
+#pragma unroll
+            for (int hh = 0; hh < 2; ++hh)
+#pragma unroll
+              for (int e = 0; e < 4 * NB; ++e) pin(v[hh][e]);
+          }
+        };
+        // v <- c v - (m or 0), -inf where out of sight; the largest is returned
+        auto apply = [&](bool sub) {
+          float mx = -INFINITY;
+#pragma unroll
+          for (int b = 0; b < NB; ++b) {
+            const float4 cm = *reinterpret_cast<const float4*>(&M.cm[c0 + 8 * b + pr][0]);
+            const float m0 = sub ? cm.y : 0.f, m1 = sub ? cm.w : 0.f;
+            int2 lim = make_int2(0, 0);
+            if (edge) lim = *reinterpret_cast<const int2*>(&M.lim[c0 + 8 * b + pr]);
+#pragma unroll
+            for (int hh = 0; hh < 2; ++hh)
+#pragma unroll
+              for (int e = 0; e < 2; ++e) {
+                float x0 = fmaf(__uint_as_float(v[hh][4 * b + 2 * e]), cm.x, -m0);
+                float x1 = fmaf(__uint_as_float(v[hh][4 * b + 2 * e + 1]), cm.z, -m1);
+                if (edge) {
+                  const int t = t0 + 32 * quarter + 16 * hh + 8 * e + (lane >> 2);
+                  const int w = a.window > 0 ? a.window : 0x7FFFFFFF;
+                  if (t > lim.x || lim.x - t >= w) x0 = -INFINITY;
+                  if (t > lim.y || lim.y - t >= w) x1 = -INFINITY;
+                }
+                mx = fmaxf(mx, fmaxf(x0, x1));
+                v[hh][4 * b + 2 * e] = __float_as_uint(x0);
+                v[hh][4 * b + 2 * e + 1] = __float_as_uint(x1);
+              }
+          }
+          return mx;
+        };
+        fetch();
+        const float mx = apply(true);
+        if (group_any(bar, mx > 15.f || !ok)) {
+          if (group_any(bar, !ok)) { broken = true; break; }
+          // move the maxima: the tile's column maxima over the group's 128 positions
+          fetch();
+          apply(false);
+#pragma unroll
+          for (int b = 0; b < NB; ++b)
+#pragma unroll
+            for (int c = 0; c < 2; ++c) {
+              float y = fmaxf(fmaxf(__uint_as_float(v[0][4 * b + c]), __uint_as_float(v[0][4 * b + 2 + c])),
+                              fmaxf(__uint_as_float(v[1][4 * b + c]), __uint_as_float(v[1][4 * b + 2 + c])));
+#pragma unroll
+              for (int o = 4; o < 32; o <<= 1) y = fmaxf(y, __shfl_xor_sync(0xFFFFFFFFu, y, o));
+              if (lane < 4) M.red[quarter][c0 + 8 * b + pr + c] = y;
+            }
+          group_sync(bar);
+          const int me = threadIdx.x & 127;
+          if (me < NC) {
+            const int col = c0 + me;
+            const float y = fmaxf(fmaxf(M.red[0][col], M.red[1][col]), fmaxf(M.red[2][col], M.red[3][col]));
+            const float m = M.cm[col][1];
+            float nm = m;
+            if (y > -INFINITY && !(y - m <= 15.f)) nm = y - 7.f;
+            M.f[col] = nm == m ? 1.f : (m == kUnset ? 0.f : ex2(m - nm));
+            M.cm[col][1] = nm;
+          }
+          group_sync(bar);
+#pragma unroll
+          for (int b = 0; b < NB; ++b)
+#pragma unroll
+            for (int c = 0; c < 2; ++c) sum[2 * b + c] *= M.f[c0 + 8 * b + pr + c];
+          if (i > 0) {
+            // O holds tiles before this one: rescale its columns once they are all in
+            ok = wait(&M.p_empty, (it - 1) & 1, fail);
+            if (group_any(bar, !ok)) { broken = true; break; }
+            tc_fence_after();
+#pragma unroll 1
+            for (int part = 0; part < (WIDE ? 2 : 1); ++part)
+#pragma unroll 1
+              for (int mb = 0; mb < S::MB; ++mb)
+#pragma unroll 1
+                for (int c = 0; c < NC; c += NC < 16 ? 8 : 16) {
+                  const uint32_t t = tmem + S::cO + mb * N + part * (N / 2) + c0 + c + lanes;
+                  uint32_t o[16];
+                  if (NC < 16) {
+                    float o8[8];
+                    tc::tmem_ld8(t, o8);
+#pragma unroll
+                    for (int e = 0; e < 8; ++e) o[e] = __float_as_uint(o8[e] * M.f[c0 + c + e]);
+                    asm volatile("tcgen05.st.sync.aligned.32x32b.x8.b32 [%8], {%0,%1,%2,%3,%4,%5,%6,%7};" ::"r"(o[0]),
+                                 "r"(o[1]), "r"(o[2]), "r"(o[3]), "r"(o[4]), "r"(o[5]), "r"(o[6]), "r"(o[7]), "r"(t)
+                                 : "memory");
+                  } else {
+                    tmem_ld_rows16(t, o);
+                    tc_wait_ld();
+#pragma unroll
+                    for (int e = 0; e < 16; ++e) pin(o[e]);
+#pragma unroll
+                    for (int e = 0; e < 16; ++e) o[e] = __float_as_uint(__uint_as_float(o[e]) * M.f[c0 + c + e]);
+                    tmem_st_rows16(t, o);
+                  }
+                }
+            tc_wait_st();
+          }
+          fetch();
+          apply(true);
+        }
+        tc_fence_before();
+        __syncwarp();
+        if (lane == 0) mbar_arrive(smem_u32(&M.s_empty[sb]));
+        // weights, their sums, and P^T once the last tile's P has been read
+        uint32_t w[NB][4], wl[WIDE ? NB : 1][4];
+#pragma unroll
+        for (int b = 0; b < NB; ++b)
+#pragma unroll
+          for (int k = 0; k < 4; ++k) {  // k = 2 hh + e
+            const float p0 = ex2(__uint_as_float(v[k >> 1][4 * b + 2 * (k & 1)]));
+            const float p1 = ex2(__uint_as_float(v[k >> 1][4 * b + 2 * (k & 1) + 1]));
+            sum[2 * b] += p0;
+            sum[2 * b + 1] += p1;
+            w[b][k] = pack_f16(p0, p1);
+            if (WIDE) {
+              const float2 h = f16x2_to_f(w[b][k]);
+              wl[WIDE ? b : 0][k] = pack_f16(p0 - h.x, p1 - h.y);
+            }
+          }
+        if (it > 0) ok = wait(&M.p_empty, (it - 1) & 1, fail) && ok;
+        __syncwarp();
+        {
+          const int row = lane & 7, mi = lane >> 3;
+          const uint32_t p = smem_u32(base + S::oP) + (quarter >> 1) * N * 128 + (c0 + row) * 128 +
+                             (((4 * (quarter & 1) + mi) ^ row) << 4);
+#pragma unroll
+          for (int b = 0; b < NB; ++b) {
+            stmatrix_x4_t(p + b * 1024, w[b][0], w[b][1], w[b][2], w[b][3]);
+            if (WIDE) {
+              const int k = WIDE ? b : 0;
+              stmatrix_x4_t(p + b * 1024 + N / 2 * 128, wl[k][0], wl[k][1], wl[k][2], wl[k][3]);
+            }
+          }
+        }
+        fence_async();
+        tc_fence_before();
+        __syncwarp();
+        if (lane == 0) mbar_arrive(smem_u32(&M.p_full));
+      }
+      // ---- the run's share of this (row, head, query tile) is in O
+      if (broken) break;
+      ok = wait(&M.p_empty, (it - 1) & 1, fail) && ok;
+      if (group_any(bar, !ok)) break;
+      tc_fence_after();
+#pragma unroll
+      for (int b = 0; b < 2 * NB; ++b) {
+        float y = sum[b];
+#pragma unroll
+        for (int o = 4; o < 32; o <<= 1) y += __shfl_xor_sync(0xFFFFFFFFu, y, o);
+        if (lane < 4) M.red[quarter][c0 + 8 * (b >> 1) + pr + (b & 1)] = y;
+      }
+      group_sync(bar);
+      const bool whole = begins && ends;
+      const int slot = 2 * blockIdx.x + (begins ? 1 : 0);
+      const int me = threadIdx.x & 127;
+      if (me < NC) {
+        const int col = c0 + me;
+        const float l = M.red[0][col] + M.red[1][col] + M.red[2][col] + M.red[3][col];
+        const float m = M.cm[col][1];
+        if (whole) {
+          M.f[col] = l != 0.f ? pow2i(head_exp(a.v_exp, s.g)) / l : 0.f;
+          if (a.lse && M.dst[col] >= 0) a.lse[M.dst[col]] = l != 0.f ? (m + log2f(l)) * 0.693147181f : -INFINITY;
+        } else {
+          a.part_ml[(long long)slot * S::RT + col] = make_float2(m, l);
+        }
+      }
+      if (!whole && sg == 0 && me == 0)
+        a.part_meta[slot] = make_int4(s.r, s.g, s.j, (begins ? 1 : 0) | (ends ? 2 : 0) | 4);
+      group_sync(bar);
+      if (DH > 64 || quarter < 2) {
+#pragma unroll 1
+        for (int mb = 0; mb < S::MB; ++mb)
+#pragma unroll 1
+          for (int c = 0; c < NC; c += 8) {
+            float o[8];
+            tc::tmem_ld8(tmem + S::cO + mb * N + c0 + c + lanes, o);
+            if (WIDE) {
+              float o2[8];
+              tc::tmem_ld8(tmem + S::cO + mb * N + N / 2 + c0 + c + lanes, o2);
+#pragma unroll
+              for (int e = 0; e < 8; ++e) o[e] += o2[e];
+            }
+            const int d = mb * 128 + 32 * quarter + lane;
+            if (M.nan_run[run & 1] == run + 1) {
+#pragma unroll
+              for (int e = 0; e < 8; ++e)
+                if (sees_nan<DH / 16>(s.t0, s.cnt, s.p0, s.p1, M.nan_bits[run & 1], d / 16, M.lim[c0 + c + e], a.window))
+                  o[e] = __int_as_float(0x7FC00000);
+            }
+#pragma unroll
+            for (int e = 0; e < 8; ++e) {
+              const int col = c0 + c + e;
+              const long long dst = M.dst[col];
+              if (dst < 0) continue;
+              if (whole) store_elem(a.out, WIDE ? MTP_DTYPE_F32 : MTP_DTYPE_BF16, dst * DH + d, o[e] * M.f[col]);
+              else a.part_o[((long long)slot * S::RT + col) * DH + d] = o[e];
+            }
+          }
+      }
+      tc_fence_before();
+      left -= nt;
+      off = 0;
+      if (left > 0) walk.next(s);
+      group_sync(bar);
+      ++run;
+    }
+  }
+
+  tc_fence_before();
+  __syncthreads();
+  tc_fence_after();
+  if (threadIdx.x == 0) {
+    if (M.fail) {
+      flag_status(a.status, MTP_ERR_TIMEOUT);
+      // let copies still in flight land before the shared memory is released
+      for (uint32_t i = 0; i < (uint32_t)S::KS && i < M.copied[0]; ++i)
+        mbar_wait(smem_u32(&M.rawk_full[i]), ((M.copied[0] - 1 - i) / S::KS) & 1, kQ4WaitLimit);
+      for (uint32_t i = 0; i < (uint32_t)S::VS && i < M.copied[1]; ++i)
+        mbar_wait(smem_u32(&M.rawv_full[i]), ((M.copied[1] - 1 - i) / S::VS) & 1, kQ4WaitLimit);
+    }
+  }
+  __syncthreads();
+  if (warp == 0)
+    asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, %1;" ::"r"(tmem), "r"(S::kCols) : "memory");
+}
+
+template <int DH, int N, bool WIDE>
+cudaError_t launch_q4_attn_t(const Q4AttnArgs& a, int blocks, cudaStream_t s) {
+  using S = Shape<DH, N, WIDE>;
+  auto k = k_q4_attn<DH, N, WIDE>;
+  {
+    // the dynamic shared memory limit, raised once per device
+    static std::mutex mu;
+    static bool set[kMaxDevices] = {};
+    int dev = 0;
+    cudaGetDevice(&dev);
+    if (dev < 0 || dev >= kMaxDevices) dev = 0;
+    std::lock_guard<std::mutex> lock(mu);
+    if (!set[dev]) {
+      const cudaError_t e = cudaFuncSetAttribute(k, cudaFuncAttributeMaxDynamicSharedMemorySize, S::kSmem);
+      if (e != cudaSuccess) {
+        cudaGetLastError();
+        return e;
+      }
+      set[dev] = true;
+    }
+  }
+  count_launch();
+  return launch_pdl(k, dim3(blocks), dim3(kAttnThreads), (size_t)S::kSmem, s, a);
+}
+
+template <int DH>
+cudaError_t launch_q4_attn(const Q4AttnArgs& a, int n, bool wide, int blocks, cudaStream_t s) {
+  if (wide) {
+    if (n == 16) return launch_q4_attn_t<DH, 16, true>(a, blocks, s);
+    if (n == 32) return launch_q4_attn_t<DH, 32, true>(a, blocks, s);
+    return launch_q4_attn_t<DH, 64, true>(a, blocks, s);
+  }
+  if (n == 16) return launch_q4_attn_t<DH, 16, false>(a, blocks, s);
+  if (n == 32) return launch_q4_attn_t<DH, 32, false>(a, blocks, s);
+  if (n == 64) return launch_q4_attn_t<DH, 64, false>(a, blocks, s);
+  return launch_q4_attn_t<DH, 128, false>(a, blocks, s);
+}
+
+// One head dimension's kernels each (their own translation units).
+cudaError_t launch_q4_attn_64(const Q4AttnArgs& a, int n, bool wide, int blocks, cudaStream_t s);
+cudaError_t launch_q4_attn_128(const Q4AttnArgs& a, int n, bool wide, int blocks, cudaStream_t s);
+cudaError_t launch_q4_attn_256(const Q4AttnArgs& a, int n, bool wide, int blocks, cudaStream_t s);
+
+}  // namespace mtp

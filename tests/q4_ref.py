@@ -105,12 +105,13 @@ def values(raw, dh):
 # ------------------------------------------------------------------ attention
 
 def attend(q, kc, vc, table, start, length, scale, window=0, k_exp=None, v_exp=None):
-    """q [T, n_q, dh] float64; caches as bytes. Returns (out, lse, spread, reach): spread = sum_j p_j |v_j| per
-    element, reach = scale * max_j sum_i |q_i k_ji| per query, the sizes that the tolerances go by."""
+    """q [T, n_q, dh] float64; caches as bytes. Returns (out, lse, spread, reach, flat): spread = sum_j p_j |v_j|
+    and flat = sum_j |v_j| per element, reach = scale * max_j sum_i |q_i k_ji| per query, the sizes that the
+    tolerances go by."""
     T, nq, dh = q.shape
     nkv, page = kc.shape[1], kc.shape[2]
     G = nq // nkv
-    out, spread = torch.zeros(T, nq, dh, dtype=torch.float64), torch.zeros(T, nq, dh, dtype=torch.float64)
+    out, spread, flat = (torch.zeros(T, nq, dh, dtype=torch.float64) for _ in range(3))
     lse = torch.full((T, nq), -math.inf, dtype=torch.float64)
     reach = torch.zeros(T, nq, dtype=torch.float64)
     for r in range(len(length)):
@@ -132,9 +133,10 @@ def attend(q, kc, vc, table, start, length, scale, window=0, k_exp=None, v_exp=N
                 p = torch.softmax(s, -1)
                 out[i, h * G:(h + 1) * G] = p @ vv
                 spread[i, h * G:(h + 1) * G] = p @ vv.abs()
+                flat[i, h * G:(h + 1) * G] = vv.abs().sum(0)
                 lse[i, h * G:(h + 1) * G] = torch.logsumexp(s, -1)
                 reach[i, h * G:(h + 1) * G] = abs(scale) * (qi.abs() @ kk.abs().T).amax(-1)
-    return out, lse, spread, reach
+    return out, lse, spread, reach, flat
 
 
 # ------------------------------------------------------------------ log probabilities

@@ -6,7 +6,11 @@ of it; fp32: two parts, 2^-22), so it is off by at most
   d = (2^-16 or 2^-21 + dh 2^-24) scale sum |q k|,
 a softmax weight by 2 d + 2^-21 of itself and, for bf16, its own f16 rounding
 (2^-11; fp32: two parts, 2^-22), an output element by that times sum p |v|, and
-finally by its type's half step; lse by d + 2^-20 and its own half step."""
+finally by its type's half step; lse by d + 2^-20 and its own half step.
+Weights are held as 2^(y - m) with the largest at 2^7 at the least, so f16's
+smallest spacing of 2^-24 moves each by up to 2^-25, 2^-32 of the largest: an
+output element by 2^-32 sum |v|, which shows only where the positions that carry
+the weight have v = 0."""
 import math
 
 import pytest
@@ -62,13 +66,13 @@ def call(c, scale, window=0, max_q=None, q_dev=None, want_lse=True, stream=None)
 def check(c, scale, window=0, **kw):
     out, lse, status = call(c, scale, window, **kw)
     assert status == 0
-    ref, rlse, spread, reach = q4_ref.attend(c["q"].double(), c["kc"], c["vc"], c["table"], c["start"], c["length"], scale,
-                                             window, c["k_exp"], c["v_exp"])
+    ref, rlse, spread, reach, flat = q4_ref.attend(c["q"].double(), c["kc"], c["vc"], c["table"], c["start"], c["length"],
+                                                   scale, window, c["k_exp"], c["v_exp"])
     wide = c["q"].dtype == torch.float32
     dh = c["q"].shape[2]
     d = ((2.0 ** -21 if wide else 2.0 ** -16) + dh * 2.0 ** -24) * reach
     rel = 2 * d + 2.0 ** -21 + (2.0 ** -22 if wide else 2.0 ** -11)
-    tol = ref.abs() * (2.0 ** -24 if wide else 2.0 ** -8) + rel[..., None] * spread * (1 + 2.0 ** -8) + 1e-30
+    tol = ref.abs() * (2.0 ** -24 if wide else 2.0 ** -8) + rel[..., None] * spread * (1 + 2.0 ** -8) + 1e-30 + 2.0 ** -32 * flat
     off = (out.double() - ref).abs()
     assert (off <= tol).all(), (float((off / tol).max()), (off > tol).nonzero()[:5])
     empty = rlse == -math.inf
@@ -163,6 +167,41 @@ def test_a_nan_query_or_cache_row_shows():
     assert status == 0
     assert out[0, 1].isnan().all() and not out[0, 0].isnan().any() and not out[1].isnan().any()
     assert out[2, 2:].isnan().all() and not out[2, :2].isnan().any()
+
+
+@pytest.mark.parametrize("nq,nkv,dh", HEADS)
+@pytest.mark.parametrize("dtype", [torch.bfloat16, torch.float32])
+@pytest.mark.parametrize("window", [0, 3, 200])
+def test_nan_out_of_sight_stays_out(nq, nkv, dh, dtype, window):
+    """K and V that are NaN at positions after some of a block's queries, and before the window of others."""
+    kv, n = 389, 7
+    c = build(2, [n, 2], [kv, 300], nq, nkv, dh, 64, dtype, 29)
+    clean, _ = check(c, 0.1, window)
+
+    def poison(pos, which, head, block):
+        c[which][c["table"][0][pos // 64], head, pos % 64, dh // 2 + block] = 0x7F if pos % 2 else 0xFF
+    poison(kv - 3, "vc", 0, 1)               # the fifth query on sees it
+    poison(kv - 1, "kc", 0, 0)               # only the last one does
+    if window == 3:
+        poison(kv - n - 1, "vc", nkv - 1, 2)  # only the first and the second one do
+    out, _, status = call(c, 0.1, window)
+    assert status == 0
+    G = nq // nkv
+    for i in range(n):
+        bad = torch.zeros(nq, dh, dtype=torch.bool)
+        if i >= 4:
+            bad[:G, 16:32] = True
+        if i == 6:
+            bad[:G] = True
+        if window == 3 and i <= 1:
+            bad[nq - G:, 32:48] = True
+        assert torch.equal(out[i].isnan(), bad), i
+        assert torch.equal(out[i][~bad], clean[i][~bad])
+    assert torch.equal(out[n:], clean[n:])
+    if window == 0:
+        poison(5, "vc", nkv - 1, 3)          # far from any border: every query sees it
+        out, _, _ = call(c, 0.1, window)
+        assert out[:n, nq - G:, 48:64].isnan().all() and not out[:4, nq - G:, :16].isnan().any()
 
 
 def test_strided_queries_and_a_small_hint():
