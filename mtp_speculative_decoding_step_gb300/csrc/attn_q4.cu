@@ -9,44 +9,79 @@ namespace mtp {
 
 namespace {
 
-constexpr int kJoinRows = 4;  // query rows per block of the join
+constexpr int kJoinThreads = 256;
 
 // Block (b, y): the query tile that block b of the attention began and did not
-// end, its rows y * kJoinRows on. Block b + 1 holds the next part of it, and
-// so on up to the block that ended it. Thread = head dimension.
+// end; blocks b + 1 to `last` hold the rest of it. Row by row (y, y + gridDim.y,
+// ...): the parts' weights, one thread per part, then their sum, a group of
+// DH / 4 threads per part.
 template <int DH, int DT>
-__global__ void __launch_bounds__(DH) k_q4_join(const __grid_constant__ Q4AttnArgs a, int RT, int blocks) {
+__global__ void __launch_bounds__(kJoinThreads) k_q4_join(const __grid_constant__ Q4AttnArgs a, int RT) {
+  constexpr int kG = kJoinThreads / (DH / 4);
+  __shared__ float s_w[kJoinThreads], s_red[2][kJoinThreads / 32];
+  __shared__ float4 s_o[kG][DH / 4];
   pdl_wait();
   pdl_trigger();
-  const int b = blockIdx.x;
+  const int b = blockIdx.x, tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
   const int4 me = a.part_meta[2 * b + 1];
-  if (me.w != (1 | 4)) return;
-  int last = b + 1;
-  while (last < blocks && (a.part_meta[2 * last].w & 6) == 4) ++last;
-  if (last == blocks || (a.part_meta[2 * last].w & 6) != 6) return;  // (a run that gave up: the status word says so)
-  const int G = a.n_q / a.n_kv;
+  if (me.w <= b) return;  // it began nothing that others went on with
+  const int parts = me.w - b + 1, G = a.n_q / a.n_kv;
   const int a0 = min(max(a.start[me.x], 0), a.tokens);
   const int n = min(max(a.start[me.x + 1], a0), a.tokens) - a0;
   const float up = pow2i(head_exp(a.v_exp, me.y));
-  for (int j = blockIdx.y * kJoinRows; j < min(RT, (int)(blockIdx.y + 1) * kJoinRows); ++j) {
+  const int grp = tid / (DH / 4), d4 = tid % (DH / 4);
+  for (int j = blockIdx.y; j < RT; j += gridDim.y) {
     const int f = me.z * RT + j;
     if (f >= n * G) return;
+    // a part that saw nothing has m = -inf and the sum 0; one whose scores were
+    // all NaN has m = -inf and the sum NaN
+    auto at = [&](int p) { return (long long)(2 * (b + p) + (p == 0)) * RT + j; };
     float m = -INFINITY;
-    for (int p = b; p <= last; ++p) m = fmaxf(m, a.part_ml[(long long)(2 * p + (p == b)) * RT + j].x);
-    float l = 0.f, o = 0.f;
+    for (int p = tid; p < parts; p += kJoinThreads) m = fmaxf(m, a.part_ml[at(p)].x);
+    m = warp_max(m);
+    __syncthreads();
+    if (lane == 0) s_red[0][warp] = m;
+    __syncthreads();
+#pragma unroll
+    for (int w = 0; w < kJoinThreads / 32; ++w) m = fmaxf(m, s_red[0][w]);
+    float l = 0.f;
+    float4 o = make_float4(0.f, 0.f, 0.f, 0.f);
+    for (int p0 = 0; p0 < parts; p0 += kJoinThreads) {  // (one turn up to 256 blocks)
+      if (p0 + tid < parts) {
+        const float2 ml = a.part_ml[at(p0 + tid)];
+        const float w = ml.x == -INFINITY ? (ml.y == 0.f ? 0.f : 1.f) : exp2f(ml.x - m);
+        s_w[tid] = w;
+        l = fmaf(w, ml.y, l);
+      }
+      __syncthreads();
 #pragma unroll 4
-    for (int p = b; p <= last; ++p) {
-      const long long at = (long long)(2 * p + (p == b)) * RT + j;
-      const float2 ml = a.part_ml[at];
-      // (a part that saw nothing has m = -inf and adds nothing; one whose
-      // scores were all NaN has m = -inf and the sum NaN)
-      const float w = ml.x == -INFINITY ? (ml.y == 0.f ? 0.f : 1.f) : exp2f(ml.x - m);
-      l = fmaf(w, ml.y, l);
-      o = fmaf(w, w == 0.f ? 0.f : a.part_o[at * DH + threadIdx.x], o);
+      for (int p = grp; p < min(parts - p0, kJoinThreads); p += kG) {
+        const float w = s_w[p];
+        const float4 v = reinterpret_cast<const float4*>(a.part_o + at(p0 + p) * DH)[d4];
+        if (w != 0.f) {
+          o.x = fmaf(w, v.x, o.x);
+          o.y = fmaf(w, v.y, o.y);
+          o.z = fmaf(w, v.z, o.z);
+          o.w = fmaf(w, v.w, o.w);
+        }
+      }
+      __syncthreads();
     }
+    l = warp_sum(l);
+    if (lane == 0) s_red[1][warp] = l;
+    s_o[grp][d4] = o;
+    __syncthreads();
+    l = 0.f;
+#pragma unroll
+    for (int w = 0; w < kJoinThreads / 32; ++w) l += s_red[1][w];
     const long long dst = (long long)(a0 + f / G) * a.n_q + me.y * G + f % G;
-    store_elem(a.out, DT, dst * DH + threadIdx.x, l != 0.f ? o * (up / l) : 0.f);
-    if (threadIdx.x == 0 && a.lse) a.lse[dst] = l != 0.f ? (m + log2f(l)) * 0.693147181f : -INFINITY;
+    if (tid < DH) {
+      float y = 0.f;
+#pragma unroll
+      for (int g = 0; g < kG; ++g) y += reinterpret_cast<const float*>(s_o[g])[tid];
+      store_elem(a.out, DT, dst * DH + tid, l != 0.f ? y * (up / l) : 0.f);
+    }
+    if (tid == 0 && a.lse) a.lse[dst] = l != 0.f ? (m + log2f(l)) * 0.693147181f : -INFINITY;
   }
 }
 
@@ -108,11 +143,11 @@ mtp_status kv_q4_attend(mtp_stream stream, const kv_q4_cache* c, int32_t rows, i
                   : c->head_dim == 128 ? launch_q4_attn_128(a, n, wide, blocks, s)
                                        : launch_q4_attn_256(a, n, wide, blocks, s);
   if (e != cudaSuccess) return MTP_ERR_CUDA;
-  void (*join)(Q4AttnArgs, int, int) =
+  void (*join)(Q4AttnArgs, int) =
       c->head_dim == 64    ? (wide ? k_q4_join<64, MTP_DTYPE_F32> : k_q4_join<64, MTP_DTYPE_BF16>)
       : c->head_dim == 128 ? (wide ? k_q4_join<128, MTP_DTYPE_F32> : k_q4_join<128, MTP_DTYPE_BF16>)
                            : (wide ? k_q4_join<256, MTP_DTYPE_F32> : k_q4_join<256, MTP_DTYPE_BF16>);
-  e = launch_pdl(join, dim3(blocks, (rt + kJoinRows - 1) / kJoinRows), dim3(c->head_dim), 0, s, a, rt, blocks);
+  e = launch_pdl(join, dim3(blocks, std::min(rt, 32)), dim3(kJoinThreads), 0, s, a, rt);
   count_launch();
   return e == cudaSuccess ? MTP_OK : MTP_ERR_CUDA;
 }

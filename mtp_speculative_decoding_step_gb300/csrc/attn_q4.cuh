@@ -60,7 +60,7 @@ struct Q4AttnArgs {
   void* out;
   float* lse;
   int32_t* status;
-  int4* part_meta;               // [2 * blocks] (row, head, query tile, 1 = a start | 2 = an end | 4 = present)
+  int4* part_meta;               // [2 * blocks] (row, head, query tile, block that ends it; -1 if it began elsewhere; 0 if none)
   float2* part_ml;               // [2 * blocks][rows of a tile] (m, sum)
   float* part_o;                 // [2 * blocks][rows of a tile][DH]
   int rows, n_q, n_kv, page, n_pages, max_pages, tokens, window;
@@ -213,17 +213,10 @@ __device__ __forceinline__ void tmem_ld_frag<8>(uint32_t t, uint32_t* r) {
   tmem_ld_frag<4>(t + 32, r + 16);
 }
 
-__device__ __forceinline__ void tmem_ld_rows16(uint32_t t, uint32_t (&r)[16]) {  // lane's 16 columns
-  asm volatile("tcgen05.ld.sync.aligned.32x32b.x16.b32 {%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15}, [%16];"
-               : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7]),
-                 "=r"(r[8]), "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]), "=r"(r[14]), "=r"(r[15])
-               : "r"(t));
-}
 __device__ __forceinline__ void tmem_st_rows16(uint32_t t, const uint32_t (&r)[16]) {
   asm volatile("tcgen05.st.sync.aligned.32x32b.x16.b32 [%16], {%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15};" ::"r"(r[0]),
                "r"(r[1]), "r"(r[2]), "r"(r[3]), "r"(r[4]), "r"(r[5]), "r"(r[6]), "r"(r[7]), "r"(r[8]), "r"(r[9]),
-               "r"(r[10]), "r"(r[11]), "r"(r[12]), "r"(r[13]), "r"(r[14]), "r"(r[15]), "r"(t)
-               : "memory");
+               "r"(r[10]), "r"(r[11]), "r"(r[12]), "r"(r[13]), "r"(r[14]), "r"(r[15]), "r"(t));
 }
 
 __device__ __forceinline__ void stmatrix_x4_t(uint32_t addr, uint32_t a, uint32_t b, uint32_t c, uint32_t d) {
@@ -295,12 +288,13 @@ struct Meta {
   uint32_t tmem;
   int fail;
   int w_r, w_g, w_j, w_o;            // the block's first task
-  long long w_n;                     // its tasks
+  long long w_n, w_q, w_end;         // its tasks, a run's tasks (w_more runs have one more), the end of its run
+  int w_more;
   long long scan[kAttnThreads / 32];
   alignas(16) float cm[128][2];      // per query row: c, m
   float f[128];                      // per query row: factor of a moved m, then 1 / sum
   alignas(16) int lim[128];          // per query row: its position
-  long long dst[128];                // per query row: row of out and lse, or -1
+  int dst[128];                      // per query row: row of out and lse, or -1
   float red[4][128];                 // per warp of a softmax group and query row
   uint32_t copied[2];                // tiles of K and of V whose copies were issued
   uint64_t drain;                    // the MMAs of a run that gave up
@@ -308,6 +302,32 @@ struct Meta {
   uint32_t nan_bits[2][4][DH / 16][4];  // edge tile, 16 dimensions: positions whose V is NaN there
 };
 static_assert(sizeof(Meta<256>) <= 8192, "meta");
+
+// NW words of a cache row in shared memory, in the widest loads that rows of
+// kRow bytes are aligned for.
+template <int NW, int kRow>
+__device__ __forceinline__ void load_words(const uint8_t* p, uint32_t (&w)[NW]) {
+  if (kRow % 16 == 0 && NW % 4 == 0) {
+#pragma unroll
+    for (int i = 0; i < NW / 4; ++i) {
+      const uint4 v = reinterpret_cast<const uint4*>(p)[i];
+      w[4 * i] = v.x;
+      w[4 * i + 1] = v.y;
+      w[4 * i + 2] = v.z;
+      w[4 * i + 3] = v.w;
+    }
+  } else if (kRow % 8 == 0 && NW % 2 == 0) {
+#pragma unroll
+    for (int i = 0; i < NW / 2; ++i) {
+      const uint2 v = reinterpret_cast<const uint2*>(p)[i];
+      w[2 * i] = v.x;
+      w[2 * i + 1] = v.y;
+    }
+  } else {
+#pragma unroll
+    for (int i = 0; i < NW; ++i) w[i] = reinterpret_cast<const uint32_t*>(p)[i];
+  }
+}
 
 // Bounded wait that gives up as soon as another role has failed.
 __device__ __forceinline__ bool wait(uint64_t* bar, uint32_t parity, volatile int* fail) {
@@ -318,6 +338,13 @@ __device__ __forceinline__ bool wait(uint64_t* bar, uint32_t parity, volatile in
   }
   *fail = 1;
   return false;
+}
+
+// The block whose run holds the last of the `rest` tasks that follow this one's run.
+template <class M>
+__device__ __forceinline__ int part_end(const M& m, int rest) {
+  const long long e = m.w_end + rest - 1, longer = (m.w_q + 1) * m.w_more;
+  return (int)(e < longer ? e / (m.w_q + 1) : m.w_more + (e - longer) / m.w_q);
 }
 
 // Keeps a value read from tensor memory behind the wait that completes it.
@@ -403,11 +430,13 @@ __global__ void __launch_bounds__(kAttnThreads, 1) k_q4_attn(const __grid_consta
     const int per = (a.rows + kAttnThreads - 1) / kAttnThreads;
     const int r0 = min((int)threadIdx.x * per, a.rows), r1 = min(r0 + per, a.rows);
     long long sum = 0;
+    int ph = 0;
     for (int r = r0; r < r1; ++r) {
       int a0, n, L;
       walk.row(r, a0, n, L);
       if (blockIdx.x == 0 && L != a.len[r]) flag_status(a.status, MTP_ERR_BAD_ARG);
-      sum += (long long)walk.per_head(n, L) * a.n_kv;
+      ph = walk.per_head(n, L);
+      sum += (long long)ph * a.n_kv;
     }
     long long inc = sum;
 #pragma unroll
@@ -419,23 +448,27 @@ __global__ void __launch_bounds__(kAttnThreads, 1) k_q4_attn(const __grid_consta
     tc_fence_before();
     __syncthreads();
     tc_fence_after();
-    long long all = 0;
+    long long all = 0, before = 0;
+#pragma unroll
     for (int w = 0; w < kAttnThreads / 32; ++w) {
-      if (w == warp) inc += all;
+      if (w < warp) before += M.scan[w];
       all += M.scan[w];
     }
-    // equal runs; with fewer tasks than blocks the first blocks take one each
-    const long long nb = max(1LL, min((long long)gridDim.x, all)), b = min((long long)blockIdx.x, nb);
-    const long long w0 = all * b / nb, w1 = min(all * (b + 1) / nb, all);
-    long long at = inc - sum;
+    // equal runs, the first ones a task longer; with fewer tasks than blocks
+    // the first blocks take one each
+    const int nb = (int)max(1LL, min((long long)gridDim.x, all)), b = blockIdx.x;
+    const long long q = all < (1LL << 31) ? (long long)((unsigned)all / (unsigned)nb) : all / nb;
+    const int more = (int)(all - q * nb);
+    const long long w0 = b < nb ? b * q + min(b, more) : all, w1 = w0 + (b < nb ? q + (b < more) : 0);
+    long long at = before + inc - sum;
     if (w0 < w1 && at <= w0 && w0 < at + sum) {
       for (int r = r0; r < r1; ++r) {
         int a0, n, L;
         walk.row(r, a0, n, L);
-        const int ph = walk.per_head(n, L);
+        if (per > 1) ph = walk.per_head(n, L);
         if (w0 < at + (long long)ph * a.n_kv) {
-          int o = (int)((w0 - at) % ph), j = 0;
-          const int g = (int)((w0 - at) / ph);
+          const unsigned x = (unsigned)(w0 - at), g = x / (unsigned)ph;  // (a row has fewer than 2^32 tasks)
+          int o = (int)(x - g * ph), j = 0;
           for (;; ++j) {
             int lo, end, t0, cnt;
             walk.span(n, L, j, lo, end, t0, cnt);
@@ -443,10 +476,13 @@ __global__ void __launch_bounds__(kAttnThreads, 1) k_q4_attn(const __grid_consta
             o -= cnt;
           }
           M.w_r = r;
-          M.w_g = g;
+          M.w_g = (int)g;
           M.w_j = j;
           M.w_o = o;
           M.w_n = w1 - w0;
+          M.w_q = q;
+          M.w_more = more;
+          M.w_end = w1;
           break;
         }
         at += (long long)ph * a.n_kv;
@@ -562,42 +598,40 @@ __global__ void __launch_bounds__(kAttnThreads, 1) k_q4_attn(const __grid_consta
     const int quarter = warp & 3, tid = threadIdx.x & 127;
     const bool do_k = kOneDq || warp < 8, do_v = kOneDq || warp >= 8;
 
-    // position `tid` of tile `i` to tensor memory, as f16
+    // position `tid` of tile `i` to tensor memory, as f16; the row is read
+    // whole before the first store, and its stage given back there
     auto deq_k = [&](uint32_t i, const Seg& sg, int tile) {
       const int st = i % S::KS;
       const uint32_t b = i % S::SB, round = i / S::SB;
       if (!wait_warp(&M.rawk_full[st], (i / S::KS) & 1, fail)) return false;
+      const int t = tile * kT + tid;
+      const uint32_t live = t >= sg.lo && t < sg.end && (M.valid_k[st] >> (tid / ps) & 1) ? ~0u : 0u;
+      const uint8_t* row = base + S::oRawK + st * S::kRaw + tid * S::kRow;
+      uint32_t code[DH / 8], sc[DH / 64];
+      load_words<DH / 8, S::kRow>(row, code);
+      load_words<DH / 64, S::kRow>(row + DH / 2, sc);
+      __syncwarp();
+      if (lane == 0) mbar_arrive(smem_u32(&M.rawk_empty[st]));
       if (round > 0 && !wait_warp(&M.k_empty[b], (round - 1) & 1, fail)) return false;
       tc_fence_after();
-      const int t = tile * kT + tid;
-      const bool live = t >= sg.lo && t < sg.end && (M.valid_k[st] >> (tid / ps) & 1);
-      const uint8_t* row = base + S::oRawK + st * S::kRaw + tid * S::kRow;
-      uint32_t sc[DH / 64];  // four scales a word
-#pragma unroll
-      for (int w = 0; w < DH / 64; ++w) sc[w] = reinterpret_cast<const uint32_t*>(row + DH / 2)[w];
 #pragma unroll
       for (int c = 0; c < DH / 32; ++c) {  // 32 elements: 16 bytes, two scales
-        uint32_t code[4], x[16];
-#pragma unroll
-        for (int w = 0; w < 4; ++w) code[w] = reinterpret_cast<const uint32_t*>(row + 16 * c)[w];
-        const uint32_t s2 = e4m3x2_to_f16x2(sc[c / 2] >> (16 * (c & 1)));
+        uint32_t x[16];
+        const uint32_t s2 = e4m3x2_to_f16x2((sc[c / 2] & live) >> (16 * (c & 1)));
         const uint32_t slo = __byte_perm(s2, s2, 0x1010), shi = __byte_perm(s2, s2, 0x3232);
 #pragma unroll
         for (int w = 0; w < 4; ++w) {
           uint32_t h[4];
-          e2m1x8_to_f16(code[w], h);
+          e2m1x8_to_f16(code[4 * c + w] & live, h);
 #pragma unroll
-          for (int e = 0; e < 4; ++e) x[4 * w + e] = live ? hmul2_bits(h[e], w < 2 ? slo : shi) : 0u;
+          for (int e = 0; e < 4; ++e) x[4 * w + e] = hmul2_bits(h[e], w < 2 ? slo : shi);
         }
         tmem_st_rows16(tmem + S::cK + b * S::KC + 16 * c + ((uint32_t)(32 * quarter) << 16), x);
       }
       tc_wait_st();
       tc_fence_before();
       __syncwarp();
-      if (lane == 0) {
-        mbar_arrive(smem_u32(&M.rawk_empty[st]));
-        mbar_arrive(smem_u32(&M.k_full[b]));
-      }
+      if (lane == 0) mbar_arrive(smem_u32(&M.k_full[b]));
       return true;
     };
     // tile `i`'s V in two halves of 64 positions; a thread takes half a row
@@ -608,9 +642,23 @@ __global__ void __launch_bounds__(kAttnThreads, 1) k_q4_attn(const __grid_consta
       const bool edge = sg.edge(tile, a.window);
       if (!wait_warp(&M.rawv_full[st], (i / S::VS) & 1, fail)) return false;
       const int tt = tid & 63, part = tid >> 6;
-      constexpr int kD = DH / 2;  // elements of a thread
+      constexpr int kD = DH / 2;                // elements of a thread
+      constexpr int kS = kD >= 64 ? kD / 64 : 1;  // words of its scales
 #pragma unroll 1
       for (int h = 0; h < 2; ++h) {
+        const int tr = h * 64 + tt, t = tile * kT + tr;
+        const uint32_t live = t >= sg.lo && t < sg.end && (M.valid_v[st] >> (tr / ps) & 1) ? ~0u : 0u;
+        const uint8_t* row = base + S::oRawV + st * S::kRaw + tr * S::kRow;
+        uint32_t code[kD / 8], sc[kS];
+        load_words<kD / 8, S::kRow>(row + part * (kD / 2), code);
+        if (kD >= 64) load_words<kS, S::kRow>(row + DH / 2 + part * (kD / 16), sc);
+        else sc[0] = *reinterpret_cast<const uint16_t*>(row + DH / 2 + part * (kD / 16));
+#pragma unroll
+        for (int w = 0; w < kS; ++w) sc[w] &= live;
+        if (h == 1) {
+          __syncwarp();
+          if (lane == 0) mbar_arrive(smem_u32(&M.rawv_empty[st]));
+        }
         if (i > 0 && !wait_warp(&M.v_empty[h], (i - 1) & 1, fail)) return false;
         if (first && h == 0) {
           // this warp's words, two runs old: their reader is done with them,
@@ -619,39 +667,39 @@ __global__ void __launch_bounds__(kAttnThreads, 1) k_q4_attn(const __grid_consta
             M.nan_bits[run & 1][e / (kD / 8)][part * (kD / 16) + e / 2 % (kD / 16)][(e & 1) * 2 + (quarter & 1)] = 0;
           __syncwarp();
         }
-        const int tr = h * 64 + tt, t = tile * kT + tr;
-        const bool live = t >= sg.lo && t < sg.end && (M.valid_v[st] >> (tr / ps) & 1);
-        const uint8_t* row = base + S::oRawV + st * S::kRaw + tr * S::kRow;
+        if (edge) {
 #pragma unroll
-        for (int c = 0; c < kD / 16; ++c) {  // 16 elements: two words, one scale
-          const int d = part * kD + 16 * c;
-          uint32_t sb = row[DH / 2 + d / 16];
-          if (edge && live && (sb & 0x7F) == 0x7F) {
-            sb = 0;
-            atomicOr(&M.nan_bits[run & 1][sg.edge_index(tile)][d / 16][tr >> 5], 1u << (tr & 31));
-            M.nan_run[run & 1] = run + 1;
+          for (int w = 0; w < kS; ++w) {
+            uint32_t nan = __vcmpeq4(sc[w] & 0x7F7F7F7Fu, 0x7F7F7F7Fu);
+            sc[w] &= ~nan;
+            while (nan) {
+              const int q = (__ffs(nan) - 1) / 8;
+              nan &= ~(0xFFu << (8 * q));
+              atomicOr(&M.nan_bits[run & 1][sg.edge_index(tile)][part * (kD / 16) + 4 * w + q][tr >> 5], 1u << (tr & 31));
+              M.nan_run[run & 1] = run + 1;
+            }
           }
-          const uint32_t s2 = e4m3x2_to_f16x2(sb);
-          const uint32_t sv = __byte_perm(s2, s2, 0x1010);
-          uint32_t x[8];
+        }
+        uint8_t* dst = base + S::oV + h * (S::kV / 2) + tt * 128;
 #pragma unroll
-          for (int w = 0; w < 2; ++w) {
+        for (int c = 0; c < kD / 32; ++c) {  // 32 elements: four words, two scales
+          const uint32_t s2 = e4m3x2_to_f16x2(sc[c / 2] >> (16 * (c & 1)));
+          const uint32_t slo = __byte_perm(s2, s2, 0x1010), shi = __byte_perm(s2, s2, 0x3232);
+          const int d = part * kD + 32 * c;
+#pragma unroll
+          for (int w = 0; w < 4; ++w) {
             uint32_t hh[4];
-            e2m1x8_to_f16(reinterpret_cast<const uint32_t*>(row + d / 2)[w], hh);
+            e2m1x8_to_f16(code[4 * c + w] & live, hh);
 #pragma unroll
-            for (int e = 0; e < 4; ++e) x[4 * w + e] = live ? hmul2_bits(hh[e], sv) : 0u;
+            for (int e = 0; e < 4; ++e) hh[e] = hmul2_bits(hh[e], w < 2 ? slo : shi);
+            *reinterpret_cast<uint4*>(dst + (d / 64) * 8192 + ((((d & 63) / 8 + w) ^ (tt & 7)) << 4)) =
+                make_uint4(hh[0], hh[1], hh[2], hh[3]);
           }
-          uint8_t* dst = base + S::oV + h * (S::kV / 2) + (d / 64) * 8192 + tt * 128;
-#pragma unroll
-          for (int w = 0; w < 2; ++w)
-            *reinterpret_cast<uint4*>(dst + ((((d & 63) / 8 + w) ^ (tt & 7)) << 4)) =
-                make_uint4(x[4 * w], x[4 * w + 1], x[4 * w + 2], x[4 * w + 3]);
         }
         fence_async();
         __syncwarp();
         if (lane == 0) mbar_arrive(smem_u32(&M.v_full[h]));
       }
-      if (lane == 0) mbar_arrive(smem_u32(&M.rawv_empty[st]));
       return true;
     };
     uint32_t it = 0, run = 0;
@@ -697,86 +745,78 @@ __global__ void __launch_bounds__(kAttnThreads, 1) k_q4_attn(const __grid_consta
     while (left > 0) {
       const int nt = (int)min((long long)(s.cnt - off), left);
       const bool begins = off == 0, ends = off + nt == s.cnt;
-      // ---- queries: one warp per row, scaled by a power of two to [2^13, 2^14)
+      // ---- queries: eight lanes per row, scaled by a power of two to [2^13, 2^14)
       const int kexp = head_exp(a.k_exp, s.g);
-      for (int j = c0 + quarter; j < c0 + NC; j += 4) {
+#pragma unroll 1
+      for (int j0 = 4 * quarter; j0 < (NC + 15) / 16 * 16; j0 += 16) {
+        const int j = c0 + j0 + (lane >> 3), d0 = (lane & 7) * 8;  // its elements: d0 + 64 k .. + 7
+        const bool mine = j0 + (lane >> 3) < NC;
         const int f = s.j * S::RT + j, i = f / G, h = s.g * G + f % G;
-        const bool real = f < s.n * G;
-        constexpr int E = DH / 32;
-        float x[E];
+        const bool real = mine && f < s.n * G;
+        const long long at = (long long)(s.a0 + i) * a.ts + (long long)h * a.hs + d0;
+        float x[DH / 8];
 #pragma unroll
-        for (int e = 0; e < E; ++e) x[e] = 0.f;
-        if (real) {
-          const long long at = (long long)(s.a0 + i) * a.ts + (long long)h * a.hs + lane * E;
-          if (WIDE) {
-            const float* src = static_cast<const float*>(a.q) + at;
-            if (a.q_vec && E >= 4) {
+        for (int k = 0; k < DH / 64; ++k) {
+          uint32_t u[WIDE ? 8 : 4];
 #pragma unroll
-              for (int e = 0; e < E / 4; ++e) {
-                const float4 v = reinterpret_cast<const float4*>(src)[e];
-                x[4 * e] = v.x;
-                x[4 * e + 1] = v.y;
-                x[4 * e + 2] = v.z;
-                x[4 * e + 3] = v.w;
-              }
-            } else {
-#pragma unroll
-              for (int e = 0; e < E; ++e) x[e] = src[e];
-            }
-          } else {
-            const uint16_t* src = static_cast<const uint16_t*>(a.q) + at;
+          for (int e = 0; e < (WIDE ? 8 : 4); ++e) u[e] = 0u;
+          if (real) {
+            const uint8_t* p = static_cast<const uint8_t*>(a.q) + (at + 64 * k) * (WIDE ? 4 : 2);
             if (a.q_vec) {
-              uint32_t u[4];
-              if (E == 8) {
-                const uint4 v = *reinterpret_cast<const uint4*>(src);
-                u[0] = v.x;
-                u[1] = v.y;
-                u[2] = v.z;
-                u[3] = v.w;
-              } else {
-                u[0] = reinterpret_cast<const uint32_t*>(src)[0];
-                if (E == 4) u[1] = reinterpret_cast<const uint32_t*>(src)[1];
-              }
 #pragma unroll
-              for (int e = 0; e < E / 2; ++e) {
-                x[2 * e] = bf16lo(u[e]);
-                x[2 * e + 1] = bf16hi(u[e]);
+              for (int e = 0; e < (WIDE ? 2 : 1); ++e) {
+                const uint4 v = reinterpret_cast<const uint4*>(p)[e];
+                u[4 * e] = v.x;
+                u[4 * e + 1] = v.y;
+                u[4 * e + 2] = v.z;
+                u[4 * e + 3] = v.w;
               }
+            } else if (WIDE) {
+#pragma unroll
+              for (int e = 0; e < 8; ++e) u[WIDE ? e : 0] = reinterpret_cast<const uint32_t*>(p)[e];
             } else {
 #pragma unroll
-              for (int e = 0; e < E; ++e) x[e] = bf16_to_f(src[e]);
+              for (int e = 0; e < 4; ++e)
+                u[e] = (uint32_t)reinterpret_cast<const uint16_t*>(p)[2 * e] |
+                       ((uint32_t)reinterpret_cast<const uint16_t*>(p)[2 * e + 1] << 16);
             }
           }
+#pragma unroll
+          for (int e = 0; e < 8; ++e)
+            x[8 * k + e] = WIDE ? __uint_as_float(u[WIDE ? e : 0]) : ((e & 1) ? bf16hi(u[e / 2]) : bf16lo(u[e / 2]));
         }
         float mx = 0.f;
 #pragma unroll
-        for (int e = 0; e < E; ++e) mx = fmaxf(mx, fabsf(x[e]));
-        mx = warp_max(mx);
+        for (int e = 0; e < DH / 8; ++e) mx = fmaxf(mx, fabsf(x[e]));
+#pragma unroll
+        for (int o = 1; o < 8; o <<= 1) mx = fmaxf(mx, __shfl_xor_sync(0xFFFFFFFFu, mx, o));
         // the exponent of the largest; an infinity or a NaN stays one (and its
         // row's scores become NaN)
         const int ex = mx > 0.f && mx < INFINITY ? max((int)(__float_as_uint(mx) >> 23) - 127, -107) : 13;
         const float up = pow2i(13 - ex);
-        uint32_t hi[E / 2], lo[E / 2];
+        if (mine) {
 #pragma unroll
-        for (int e = 0; e < E / 2; ++e) {
-          const float y0 = x[2 * e] * up, y1 = x[2 * e + 1] * up;
-          hi[e] = pack_f16(y0, y1);
-          const float2 b = f16x2_to_f(hi[e]);
-          lo[e] = pack_f16(y0 - b.x, y1 - b.y);
-        }
-        auto put = [&](int row, const uint32_t (&u)[E / 2]) {
-          const int d = lane * E;
-          uint8_t* p = base + S::oQ + (d / 64) * N * 128 + row * 128 + ((((d & 63) / 8) ^ (row & 7)) << 4) + (d & 7) * 2;
+          for (int k = 0; k < DH / 64; ++k) {
+            uint32_t hi[4], lo[4];
 #pragma unroll
-          for (int e = 0; e < E / 2; ++e) reinterpret_cast<uint32_t*>(p)[e] = u[e];
-        };
-        put(j, hi);
-        if (WIDE) put(N / 2 + j, lo);
-        if (lane == 0) {
-          M.cm[j][0] = ldexpf(a.scale * 1.44269504f, kexp - (13 - ex));
-          M.cm[j][1] = kUnset;
-          M.lim[j] = real ? s.L - s.n + i : -1;
-          M.dst[j] = real ? (long long)(s.a0 + i) * a.n_q + h : -1;
+            for (int e = 0; e < 4; ++e) {
+              const float y0 = x[8 * k + 2 * e] * up, y1 = x[8 * k + 2 * e + 1] * up;
+              hi[e] = pack_f16(y0, y1);
+              if (WIDE) {
+                const float2 b = f16x2_to_f(hi[e]);
+                lo[e] = pack_f16(y0 - b.x, y1 - b.y);
+              }
+            }
+            uint8_t* p = base + S::oQ + k * N * 128 + (((lane & 7) ^ (j & 7)) << 4);
+            *reinterpret_cast<uint4*>(p + j * 128) = make_uint4(hi[0], hi[1], hi[2], hi[3]);
+            if (WIDE) *reinterpret_cast<uint4*>(p + (N / 2 + j) * 128) = make_uint4(lo[0], lo[1], lo[2], lo[3]);
+          }
+          if ((lane & 7) == 0) {
+            M.cm[j][0] = ldexpf(a.scale * 1.44269504f, kexp - (13 - ex));
+            M.cm[j][1] = kUnset;
+            M.lim[j] = real ? s.L - s.n + i : -1;
+            M.dst[j] = real ? (s.a0 + i) * a.n_q + h : -1;
+          }
         }
       }
       fence_async();
@@ -795,12 +835,14 @@ __global__ void __launch_bounds__(kAttnThreads, 1) k_q4_attn(const __grid_consta
         const int t0 = (s.t0 + off + i) * kT;
         const bool edge = s.edge(s.t0 + off + i, a.window);
         uint32_t v[2][4 * NB];
-        auto fetch = [&]() {
+        // y = c s - m, the vote, and where some y passes 15 a move of the maxima
+        // and y once more (the code is there once: it has to stay in the
+        // instruction cache beside the other roles')
+#pragma unroll 1
+        for (bool moved = false;; moved = true) {
 #pragma unroll
-          for (int hh = 0; hh < 2; ++hh) {
-            const uint32_t t = tmem + S::cS + sb * N + c0 + lanes + ((uint32_t)(16 * hh) << 16);
-            tmem_ld_frag<NB>(t, v[hh]);
-          }
+          for (int hh = 0; hh < 2; ++hh)
+            tmem_ld_frag<NB>(tmem + S::cS + sb * N + c0 + lanes + ((uint32_t)(16 * hh) << 16), v[hh]);
           if (WIDE) {
             uint32_t u[2][4 * NB];
 #pragma unroll
@@ -822,52 +864,71 @@ __global__ void __launch_bounds__(kAttnThreads, 1) k_q4_attn(const __grid_consta
 #pragma unroll
               for (int e = 0; e < 4 * NB; ++e) pin(v[hh][e]);
           }
-        };
-        // v <- c v - (m or 0), -inf where out of sight; the largest is returned
-        auto apply = [&](bool sub) {
           float mx = -INFINITY;
 #pragma unroll
           for (int b = 0; b < NB; ++b) {
             const float4 cm = *reinterpret_cast<const float4*>(&M.cm[c0 + 8 * b + pr][0]);
-            const float m0 = sub ? cm.y : 0.f, m1 = sub ? cm.w : 0.f;
-            int2 lim = make_int2(0, 0);
-            if (edge) lim = *reinterpret_cast<const int2*>(&M.lim[c0 + 8 * b + pr]);
 #pragma unroll
-            for (int hh = 0; hh < 2; ++hh)
-#pragma unroll
-              for (int e = 0; e < 2; ++e) {
-                float x0 = fmaf(__uint_as_float(v[hh][4 * b + 2 * e]), cm.x, -m0);
-                float x1 = fmaf(__uint_as_float(v[hh][4 * b + 2 * e + 1]), cm.z, -m1);
-                if (edge) {
-                  const int t = t0 + 32 * quarter + 16 * hh + 8 * e + (lane >> 2);
-                  const int w = a.window > 0 ? a.window : 0x7FFFFFFF;
-                  if (t > lim.x || lim.x - t >= w) x0 = -INFINITY;
-                  if (t > lim.y || lim.y - t >= w) x1 = -INFINITY;
-                }
-                mx = fmaxf(mx, fmaxf(x0, x1));
-                v[hh][4 * b + 2 * e] = __float_as_uint(x0);
-                v[hh][4 * b + 2 * e + 1] = __float_as_uint(x1);
-              }
-          }
-          return mx;
-        };
-        fetch();
-        const float mx = apply(true);
-        if (group_any(bar, mx > 15.f || !ok)) {
-          if (group_any(bar, !ok)) { broken = true; break; }
-          // move the maxima: the tile's column maxima over the group's 128 positions
-          fetch();
-          apply(false);
-#pragma unroll
-          for (int b = 0; b < NB; ++b)
-#pragma unroll
-            for (int c = 0; c < 2; ++c) {
-              float y = fmaxf(fmaxf(__uint_as_float(v[0][4 * b + c]), __uint_as_float(v[0][4 * b + 2 + c])),
-                              fmaxf(__uint_as_float(v[1][4 * b + c]), __uint_as_float(v[1][4 * b + 2 + c])));
-#pragma unroll
-              for (int o = 4; o < 32; o <<= 1) y = fmaxf(y, __shfl_xor_sync(0xFFFFFFFFu, y, o));
-              if (lane < 4) M.red[quarter][c0 + 8 * b + pr + c] = y;
+            for (int k = 0; k < 4; ++k) {
+              uint32_t &x0 = v[k >> 1][4 * b + 2 * (k & 1)], &x1 = v[k >> 1][4 * b + 2 * (k & 1) + 1];
+              x0 = __float_as_uint(fmaf(__uint_as_float(x0), cm.x, -cm.y));
+              x1 = __float_as_uint(fmaf(__uint_as_float(x1), cm.z, -cm.w));
             }
+            if (edge) {
+              const int2 lim = *reinterpret_cast<const int2*>(&M.lim[c0 + 8 * b + pr]);
+              const unsigned w = a.window > 0 ? (unsigned)a.window : 0x80000000u;
+#pragma unroll
+              for (int k = 0; k < 4; ++k) {
+                const int t = t0 + 32 * quarter + 8 * k + (lane >> 2);
+                uint32_t &x0 = v[k >> 1][4 * b + 2 * (k & 1)], &x1 = v[k >> 1][4 * b + 2 * (k & 1) + 1];
+                if ((unsigned)(lim.x - t) >= w) x0 = 0xFF800000u;  // -inf: out of sight
+                if ((unsigned)(lim.y - t) >= w) x1 = 0xFF800000u;
+              }
+            }
+#pragma unroll
+            for (int k = 0; k < 4; ++k)
+              mx = fmaxf(mx, fmaxf(__uint_as_float(v[k >> 1][4 * b + 2 * (k & 1)]),
+                                   __uint_as_float(v[k >> 1][4 * b + 2 * (k & 1) + 1])));
+          }
+          if (moved || !group_any(bar, mx > 15.f || !ok)) break;
+          if (group_any(bar, !ok)) { broken = true; break; }
+          // column maxima of c s over the group's 128 positions
+#pragma unroll 1
+          for (int b = 0; b < NB; ++b) {
+            const float4 cm = *reinterpret_cast<const float4*>(&M.cm[c0 + 8 * b + pr][0]);
+            const int2 lim = *reinterpret_cast<const int2*>(&M.lim[c0 + 8 * b + pr]);
+            const unsigned w = a.window > 0 ? (unsigned)a.window : 0x80000000u;
+            float y0 = -INFINITY, y1 = -INFINITY;
+            uint32_t r[2][4], u[2][4];
+#pragma unroll
+            for (int hh = 0; hh < 2; ++hh) {
+              const uint32_t t = tmem + S::cS + sb * N + c0 + 8 * b + lanes + ((uint32_t)(16 * hh) << 16);
+              tmem_ld_frag<1>(t, r[hh]);
+              if (WIDE) tmem_ld_frag<1>(t + N / 2, u[hh]);
+            }
+            tc_wait_ld();
+#pragma unroll
+            for (int k = 0; k < 4; ++k) {
+              const int t = t0 + 32 * quarter + 8 * k + (lane >> 2), e = 2 * (k & 1);
+              pin(r[k >> 1][e]);
+              pin(r[k >> 1][e + 1]);
+              float z0 = __uint_as_float(r[k >> 1][e]), z1 = __uint_as_float(r[k >> 1][e + 1]);
+              if (WIDE) {
+                pin(u[k >> 1][e]);
+                pin(u[k >> 1][e + 1]);
+                z0 += __uint_as_float(u[k >> 1][e]);
+                z1 += __uint_as_float(u[k >> 1][e + 1]);
+              }
+              if (!edge || (unsigned)(lim.x - t) < w) y0 = fmaxf(y0, z0 * cm.x);
+              if (!edge || (unsigned)(lim.y - t) < w) y1 = fmaxf(y1, z1 * cm.z);
+            }
+#pragma unroll
+            for (int o = 4; o < 32; o <<= 1) {
+              y0 = fmaxf(y0, __shfl_xor_sync(0xFFFFFFFFu, y0, o));
+              y1 = fmaxf(y1, __shfl_xor_sync(0xFFFFFFFFu, y1, o));
+            }
+            if (lane < 4) *reinterpret_cast<float2*>(&M.red[quarter][c0 + 8 * b + pr]) = make_float2(y0, y1);
+          }
           group_sync(bar);
           const int me = threadIdx.x & 127;
           if (me < NC) {
@@ -880,46 +941,33 @@ __global__ void __launch_bounds__(kAttnThreads, 1) k_q4_attn(const __grid_consta
             M.cm[col][1] = nm;
           }
           group_sync(bar);
+          if (i == 0) continue;
 #pragma unroll
-          for (int b = 0; b < NB; ++b)
-#pragma unroll
-            for (int c = 0; c < 2; ++c) sum[2 * b + c] *= M.f[c0 + 8 * b + pr + c];
-          if (i > 0) {
-            // O holds tiles before this one: rescale its columns once they are all in
-            ok = wait(&M.p_empty, (it - 1) & 1, fail);
-            if (group_any(bar, !ok)) { broken = true; break; }
-            tc_fence_after();
-#pragma unroll 1
-            for (int part = 0; part < (WIDE ? 2 : 1); ++part)
-#pragma unroll 1
-              for (int mb = 0; mb < S::MB; ++mb)
-#pragma unroll 1
-                for (int c = 0; c < NC; c += NC < 16 ? 8 : 16) {
-                  const uint32_t t = tmem + S::cO + mb * N + part * (N / 2) + c0 + c + lanes;
-                  uint32_t o[16];
-                  if (NC < 16) {
-                    float o8[8];
-                    tc::tmem_ld8(t, o8);
-#pragma unroll
-                    for (int e = 0; e < 8; ++e) o[e] = __float_as_uint(o8[e] * M.f[c0 + c + e]);
-                    asm volatile("tcgen05.st.sync.aligned.32x32b.x8.b32 [%8], {%0,%1,%2,%3,%4,%5,%6,%7};" ::"r"(o[0]),
-                                 "r"(o[1]), "r"(o[2]), "r"(o[3]), "r"(o[4]), "r"(o[5]), "r"(o[6]), "r"(o[7]), "r"(t)
-                                 : "memory");
-                  } else {
-                    tmem_ld_rows16(t, o);
-                    tc_wait_ld();
-#pragma unroll
-                    for (int e = 0; e < 16; ++e) pin(o[e]);
-#pragma unroll
-                    for (int e = 0; e < 16; ++e) o[e] = __float_as_uint(__uint_as_float(o[e]) * M.f[c0 + c + e]);
-                    tmem_st_rows16(t, o);
-                  }
-                }
-            tc_wait_st();
+          for (int b = 0; b < NB; ++b) {
+            const float2 f = *reinterpret_cast<const float2*>(&M.f[c0 + 8 * b + pr]);
+            sum[2 * b] *= f.x;
+            sum[2 * b + 1] *= f.y;
           }
-          fetch();
-          apply(true);
+          // O holds tiles before this one: rescale its columns once they are all in
+          ok = wait(&M.p_empty, (it - 1) & 1, fail);
+          if (group_any(bar, !ok)) { broken = true; break; }
+          tc_fence_after();
+#pragma unroll 1
+          for (int q = 0; q < (WIDE ? 2 : 1) * S::MB * NC / 8; ++q) {
+            const int c = q % (NC / 8) * 8, mb = q / (NC / 8) % S::MB, part = q / (NC / 8 * S::MB);
+            const uint32_t t = tmem + S::cO + mb * N + part * (N / 2) + c0 + c + lanes;
+            float o[8];
+            tc::tmem_ld8(t, o);
+#pragma unroll
+            for (int e = 0; e < 8; ++e) o[e] *= M.f[c0 + c + e];
+            asm volatile("tcgen05.st.sync.aligned.32x32b.x8.b32 [%8], {%0,%1,%2,%3,%4,%5,%6,%7};" ::"r"(__float_as_uint(o[0])),
+                         "r"(__float_as_uint(o[1])), "r"(__float_as_uint(o[2])), "r"(__float_as_uint(o[3])),
+                         "r"(__float_as_uint(o[4])), "r"(__float_as_uint(o[5])), "r"(__float_as_uint(o[6])),
+                         "r"(__float_as_uint(o[7])), "r"(t));
+          }
+          tc_wait_st();
         }
+        if (broken) break;
         tc_fence_before();
         __syncwarp();
         if (lane == 0) mbar_arrive(smem_u32(&M.s_empty[sb]));
@@ -987,7 +1035,7 @@ __global__ void __launch_bounds__(kAttnThreads, 1) k_q4_attn(const __grid_consta
         }
       }
       if (!whole && sg == 0 && me == 0)
-        a.part_meta[slot] = make_int4(s.r, s.g, s.j, (begins ? 1 : 0) | (ends ? 2 : 0) | 4);
+        a.part_meta[slot] = make_int4(s.r, s.g, s.j, begins ? part_end(M, s.cnt - nt) : -1);
       group_sync(bar);
       if (DH > 64 || quarter < 2) {
 #pragma unroll 1
@@ -1012,9 +1060,9 @@ __global__ void __launch_bounds__(kAttnThreads, 1) k_q4_attn(const __grid_consta
 #pragma unroll
             for (int e = 0; e < 8; ++e) {
               const int col = c0 + c + e;
-              const long long dst = M.dst[col];
+              const int dst = M.dst[col];
               if (dst < 0) continue;
-              if (whole) store_elem(a.out, WIDE ? MTP_DTYPE_F32 : MTP_DTYPE_BF16, dst * DH + d, o[e] * M.f[col]);
+              if (whole) store_elem(a.out, WIDE ? MTP_DTYPE_F32 : MTP_DTYPE_BF16, (long long)dst * DH + d, o[e] * M.f[col]);
               else a.part_o[((long long)slot * S::RT + col) * DH + d] = o[e];
             }
           }
