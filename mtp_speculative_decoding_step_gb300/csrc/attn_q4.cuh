@@ -40,6 +40,8 @@
 #pragma once
 #include <mutex>
 
+#include <cuda_bf16.h>
+
 #include "common.cuh"
 #include "kernels.h"
 #include "q4.cuh"
@@ -70,23 +72,26 @@ struct Q4AttnArgs {
 
 // ------------------------------------------------------------ task walk
 
-// One (row, KV head, query tile): `rows_tile` query rows of position-major
-// order (position i, head h of the group) -> i * G + h.
-struct Seg {
-  int r, g, j;     // row, KV head, query tile
-  int a0, n, L;    // first packed position, positions, cached length
-  int lo, end;     // cached positions that some query row sees: [lo, end)
-  int t0, cnt;     // their tiles
-  int p0, p1;      // positions of the first and the last query row
+// A block's share of one (row, KV head, query tile). Query row f of the row's
+// position-major order is (position f / G, head f % G of the KV head's G); tile
+// j holds f in [j RT, (j + 1) RT).
+struct Run {
+  int r, g, j;         // row, KV head, query tile
+  int a0, n, pos;      // first packed position, positions, the first one's place in the cache
+  int lo, end;         // cached positions that some query row sees: [lo, end)
+  int first, tile, nt; // the query tile's first 128-position tile; this share's tiles
+  int p0, p1;          // places of the first and the last query row
+  int flags;           // 1: begins here, 2: ends here, 4: the block's last share
+  int last;            // the block that ends it
 
   // whether some (row, position) pair of a tile may be out of sight
-  __device__ bool edge(int tile, int window) const {
-    return tile * kT + kT - 1 > p0 || (window > 0 && tile * kT <= p1 - window);
+  __device__ bool edge(int t, int window) const {
+    return t * kT + kT - 1 > p0 || (window > 0 && t * kT <= p1 - window);
   }
-  // its number among the run's edge tiles: p0 and p1 lie less than kT apart,
-  // so two tiles at most hold a causal border, and two a window's
-  __device__ int edge_index(int tile) const {
-    return tile * kT + kT - 1 > p0 ? min(max(tile - p0 / kT, 0), 1) : 2 + min(tile - t0, 1);
+  // its number among the edge tiles: p0 and p1 lie less than kT apart, so two
+  // tiles at most hold a causal border, and two a window's
+  __device__ int edge_index(int t) const {
+    return t * kT + kT - 1 > p0 ? min(max(t - p0 / kT, 0), 1) : 2 + min(t - first, 1);
   }
 };
 
@@ -115,36 +120,13 @@ struct Walk {
   }
   __device__ int per_head(int n, int L) const {
     int sum = 0;
+#pragma unroll 1
     for (int j = 0; j < tiles(n); ++j) {
       int lo, end, t0, cnt;
       span(n, L, j, lo, end, t0, cnt);
       sum += cnt;
     }
     return sum;
-  }
-  __device__ void load(Seg& s, int r, int g, int j) const {
-    s.r = r;
-    s.g = g;
-    s.j = j;
-    row(r, s.a0, s.n, s.L);
-    span(s.n, s.L, j, s.lo, s.end, s.t0, s.cnt);
-    s.p0 = s.L - s.n + j * RT / G;
-    s.p1 = s.L - s.n + (min(s.n * G, (j + 1) * RT) - 1) / G;
-  }
-  __device__ void next(Seg& s) const {
-    int r = s.r, g = s.g, j = s.j + 1;
-    if (j == tiles(s.n)) {
-      j = 0;
-      if (++g == a->n_kv) {
-        g = 0;
-        int a0, n, L;
-        do {
-          if (++r >= a->rows) return;
-          row(r, a0, n, L);
-        } while (n == 0);
-      }
-    }
-    load(s, r, g, j);
   }
 };
 
@@ -278,6 +260,8 @@ struct Shape {
   static_assert(VS >= 1 && cEnd <= 512, "shape");
 };
 
+constexpr int kRuns = 4;
+
 // Small state of a block.
 template <int DH>
 struct Meta {
@@ -287,10 +271,8 @@ struct Meta {
   uint32_t valid_k[8], valid_v[8];   // bit p: piece p of the stage was copied
   uint32_t tmem;
   int fail;
-  int w_r, w_g, w_j, w_o;            // the block's first task
-  long long w_n, w_q, w_end;         // its tasks, a run's tasks (w_more runs have one more), the end of its run
-  int w_more;
-  long long scan[kAttnThreads / 32];
+  uint64_t run_full[kRuns], run_empty[kRuns];
+  Run run[kRuns];                    // the shares, written by one warp ahead of the other roles
   alignas(16) float cm[128][2];      // per query row: c, m
   float f[128];                      // per query row: factor of a moved m, then 1 / sum
   alignas(16) int lim[128];          // per query row: its position
@@ -330,21 +312,18 @@ __device__ __forceinline__ void load_words(const uint8_t* p, uint32_t (&w)[NW]) 
 }
 
 // Bounded wait that gives up as soon as another role has failed.
-__device__ __forceinline__ bool wait(uint64_t* bar, uint32_t parity, volatile int* fail) {
-  const uint32_t b = smem_u32(bar);
+static __device__ __noinline__ bool wait_on(uint32_t bar, uint32_t parity, volatile int* fail) {
+#pragma unroll 1
   for (unsigned i = 0; i < kQ4WaitLimit; ++i) {
-    if (mbar_try(b, parity)) return true;
+    if (mbar_try(bar, parity)) return true;
     if ((i & 1023) == 1023 && *fail) return false;
   }
   *fail = 1;
   return false;
 }
-
-// The block whose run holds the last of the `rest` tasks that follow this one's run.
-template <class M>
-__device__ __forceinline__ int part_end(const M& m, int rest) {
-  const long long e = m.w_end + rest - 1, longer = (m.w_q + 1) * m.w_more;
-  return (int)(e < longer ? e / (m.w_q + 1) : m.w_more + (e - longer) / m.w_q);
+__device__ __forceinline__ bool wait(uint64_t* bar, uint32_t parity, volatile int* fail) {
+  const uint32_t b = smem_u32(bar);
+  return mbar_try(b, parity) || wait_on(b, parity, fail);
 }
 
 // Keeps a value read from tensor memory behind the wait that completes it.
@@ -355,8 +334,8 @@ __device__ __forceinline__ void pin(uint32_t& x) { asm volatile("" : "+r"(x)); }
 template <int B>
 __device__ __noinline__ bool sees_nan(int t0, int cnt, int p0, int p1, const uint32_t (*bits)[B][4], int b, int pos,
                                       int window) {
-  Seg s;
-  s.t0 = t0;
+  Run s;
+  s.first = t0;
   s.p0 = p0;
   s.p1 = p1;
   for (int tile = t0; tile < t0 + cnt; ++tile) {
@@ -408,10 +387,13 @@ __global__ void __launch_bounds__(kAttnThreads, 1) k_q4_attn(const __grid_consta
     mbar_init(smem_u32(&M.p_empty), 1);
     mbar_init(smem_u32(&M.q_full), kSoftWarps);
     M.fail = 0;
-    M.w_n = 0;
     M.copied[0] = M.copied[1] = 0;
     M.nan_run[0] = M.nan_run[1] = 0;
     mbar_init(smem_u32(&M.drain), 1);
+    for (int i = 0; i < kRuns; ++i) {
+      mbar_init(smem_u32(&M.run_full[i]), 1);
+      mbar_init(smem_u32(&M.run_empty[i]), 14);  // copies, MMAs, 12 warps of the other roles
+    }
     asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
   }
   if (warp == 0) {
@@ -420,23 +402,38 @@ __global__ void __launch_bounds__(kAttnThreads, 1) k_q4_attn(const __grid_consta
                  : "memory");
     asm volatile("tcgen05.relinquish_alloc_permit.cta_group::1.sync.aligned;" ::: "memory");
   }
+  tc_fence_before();
+  __syncthreads();
+  tc_fence_after();
+  const uint32_t tmem = M.tmem;
+  volatile int* fail = &M.fail;
+  const int ps = a.page % kT == 0 ? kT : (a.page % 64 == 0 ? 64 : (a.page % 32 == 0 ? 32 : 16));  // slots per copy
   pdl_wait();
   pdl_trigger();
-  if (threadIdx.x < 2) a.part_meta[2 * blockIdx.x + threadIdx.x] = make_int4(0, 0, 0, 0);
 
-  // the block's run of tasks: rows' task counts scanned, consecutive rows per thread
-  Walk walk{&a, a.n_q / a.n_kv, S::RT};
-  {
-    const int per = (a.rows + kAttnThreads - 1) / kAttnThreads;
-    const int r0 = min((int)threadIdx.x * per, a.rows), r1 = min(r0 + per, a.rows);
+  // the shares in turn: `next` waits for share `k` and hands it out, `done` gives its slot back
+  auto next = [&](uint32_t k, Run& s) {
+    if (!wait(&M.run_full[k % kRuns], (k / kRuns) & 1, fail)) return false;
+    s = M.run[k % kRuns];
+    return true;
+  };
+  auto done = [&](uint32_t k) { mbar_arrive(smem_u32(&M.run_empty[k % kRuns])); };
+
+  if (warp == 2) {
+    // ---------------------------------------------------------- shares
+    // Every (row, KV head, query tile, 128-position tile) is a task; each block
+    // owns an equal stretch of them. The rows' task counts are scanned, rows
+    // in consecutive groups per lane.
+    const Walk walk{&a, a.n_q / a.n_kv, S::RT};
+    if (lane < 2) a.part_meta[2 * blockIdx.x + lane] = make_int4(0, 0, 0, 0);
+    const int per = (a.rows + 31) / 32, r0 = min(lane * per, a.rows), r1 = min(r0 + per, a.rows);
     long long sum = 0;
-    int ph = 0;
+#pragma unroll 1
     for (int r = r0; r < r1; ++r) {
       int a0, n, L;
       walk.row(r, a0, n, L);
       if (blockIdx.x == 0 && L != a.len[r]) flag_status(a.status, MTP_ERR_BAD_ARG);
-      ph = walk.per_head(n, L);
-      sum += (long long)ph * a.n_kv;
+      sum += (long long)walk.per_head(n, L) * a.n_kv;
     }
     long long inc = sum;
 #pragma unroll
@@ -444,73 +441,104 @@ __global__ void __launch_bounds__(kAttnThreads, 1) k_q4_attn(const __grid_consta
       const long long u = __shfl_up_sync(0xFFFFFFFFu, inc, o);
       if (lane >= o) inc += u;
     }
-    if (lane == 31) M.scan[warp] = inc;
-    tc_fence_before();
-    __syncthreads();
-    tc_fence_after();
-    long long all = 0, before = 0;
-#pragma unroll
-    for (int w = 0; w < kAttnThreads / 32; ++w) {
-      if (w < warp) before += M.scan[w];
-      all += M.scan[w];
-    }
-    // equal runs, the first ones a task longer; with fewer tasks than blocks
-    // the first blocks take one each
+    const long long all = __shfl_sync(0xFFFFFFFFu, inc, 31);
+    // equal stretches, the first ones a task longer; with fewer tasks than
+    // blocks the first blocks take one each
     const int nb = (int)max(1LL, min((long long)gridDim.x, all)), b = blockIdx.x;
-    const long long q = all < (1LL << 31) ? (long long)((unsigned)all / (unsigned)nb) : all / nb;
-    const int more = (int)(all - q * nb);
-    const long long w0 = b < nb ? b * q + min(b, more) : all, w1 = w0 + (b < nb ? q + (b < more) : 0);
-    long long at = before + inc - sum;
-    if (w0 < w1 && at <= w0 && w0 < at + sum) {
-      for (int r = r0; r < r1; ++r) {
-        int a0, n, L;
+    long long q = 0;
+    unsigned rem = 0;
+#pragma unroll 1
+    for (int d = 48; d >= 0; d -= 16) {  // all / nb, 16 bits a step (nb < 2^16)
+      const unsigned part = rem << 16 | (unsigned)(all >> d & 0xFFFF), x = part / (unsigned)nb;
+      q = q << 16 | x;
+      rem = part - x * nb;
+    }
+    const int more = (int)rem;
+    const long long w0 = b < nb ? b * q + min(b, more) : all;
+    long long left = b < nb ? q + (b < more) : 0;
+    // the lane whose rows hold the first task
+    const unsigned who = __ballot_sync(0xFFFFFFFFu, left > 0 && inc - sum <= w0 && w0 < inc);
+    const int owner = who ? __ffs(who) - 1 : 0;
+    long long at = __shfl_sync(0xFFFFFFFFu, inc - sum, owner);
+    int r = __shfl_sync(0xFFFFFFFFu, r0, owner), g = 0, j = 0, o = 0, a0 = 0, n = 0, L = 0;
+    if (left > 0) {
+#pragma unroll 1
+      for (;; ++r) {
         walk.row(r, a0, n, L);
-        if (per > 1) ph = walk.per_head(n, L);
+        const int ph = walk.per_head(n, L);
         if (w0 < at + (long long)ph * a.n_kv) {
-          const unsigned x = (unsigned)(w0 - at), g = x / (unsigned)ph;  // (a row has fewer than 2^32 tasks)
-          int o = (int)(x - g * ph), j = 0;
-          for (;; ++j) {
-            int lo, end, t0, cnt;
-            walk.span(n, L, j, lo, end, t0, cnt);
-            if (o < cnt) break;
-            o -= cnt;
-          }
-          M.w_r = r;
-          M.w_g = (int)g;
-          M.w_j = j;
-          M.w_o = o;
-          M.w_n = w1 - w0;
-          M.w_q = q;
-          M.w_more = more;
-          M.w_end = w1;
+          const unsigned x = (unsigned)(w0 - at);  // (a row has fewer than 2^32 tasks)
+          g = (int)(x / (unsigned)ph);
+          o = (int)(x % (unsigned)ph);
           break;
         }
         at += (long long)ph * a.n_kv;
       }
     }
-    __syncthreads();
-  }
-  const uint32_t tmem = M.tmem;
-  volatile int* fail = &M.fail;
-  const long long todo = M.w_n;
-  Seg s;
-  int off = 0;
-  if (todo > 0) {
-    walk.load(s, M.w_r, M.w_g, M.w_j);
-    off = M.w_o;
-  }
-  long long left = todo;
-  const int ps = a.page % kT == 0 ? kT : (a.page % 64 == 0 ? 64 : (a.page % 32 == 0 ? 32 : 16));  // slots per copy
-
-  if (warp == 0) {
+    bool found = false;
+    uint32_t k = 0;
+    if (left == 0 && lane == 0) {  // nothing: an empty last share
+      M.run[0].nt = 0;
+      M.run[0].flags = 4;
+      mbar_arrive(smem_u32(&M.run_full[0]));
+    }
+#pragma unroll 1
+    while (left > 0) {
+      Run s;
+      int cnt;
+      walk.span(n, L, j, s.lo, s.end, s.first, cnt);
+      if (!found && o >= cnt) {  // still before the first task
+        o -= cnt;
+        ++j;
+        continue;
+      }
+      found = true;
+      s.r = r;
+      s.g = g;
+      s.j = j;
+      s.a0 = a0;
+      s.n = n;
+      s.pos = L - n;
+      s.p0 = s.pos + j * S::RT / walk.G;
+      s.p1 = s.pos + (min(n * walk.G, (j + 1) * S::RT) - 1) / walk.G;
+      s.tile = s.first + o;
+      s.nt = (int)min((long long)(cnt - o), left);
+      s.flags = (o == 0 ? 1 : 0) | (o + s.nt == cnt ? 2 : 0) | (s.nt == left ? 4 : 0);
+      s.last = b;
+#pragma unroll 1
+      for (long long rest = cnt - o - s.nt; rest > 0; rest -= q + (s.last < more)) ++s.last;
+      left -= s.nt;
+      o = 0;
+      if (k >= kRuns && !wait_warp(&M.run_empty[k % kRuns], (k / kRuns - 1) & 1, fail)) break;
+      if (lane == 0) {
+        M.run[k % kRuns] = s;
+        mbar_arrive(smem_u32(&M.run_full[k % kRuns]));
+      }
+      ++k;
+      if (left > 0 && ++j == walk.tiles(n)) {
+        j = 0;
+        if (++g == a.n_kv) {
+          g = 0;
+#pragma unroll 1
+          do walk.row(++r, a0, n, L);
+          while (n == 0);
+        }
+      }
+    }
+  } else if (warp == 0) {
     // ---------------------------------------------------------- copies
     uint32_t it = 0;
     bool ok = true;
-    while (left > 0 && ok) {
-      const int nt = (int)min((long long)(s.cnt - off), left);
+    Run s;
+    s.flags = 0;
+#pragma unroll 1
+    for (uint32_t k = 0; ok && !(s.flags & 4); ++k) {
+      ok = __all_sync(0xFFFFFFFFu, next(k, s));
+      if (!ok) break;
       const int32_t* tab = a.table + (long long)s.r * a.max_pages;
-      for (int i = 0; i < nt && ok; ++i, ++it) {
-        const int t0 = (s.t0 + off + i) * kT + lane * ps;  // lane p: piece p of the tile
+#pragma unroll 1
+      for (int i = 0; i < s.nt && ok; ++i, ++it) {
+        const int t0 = (s.tile + i) * kT + lane * ps;  // lane p: piece p of the tile
         const bool need = lane * ps < kT && t0 < s.end && t0 + ps > s.lo;
         int id = need ? __ldg(tab + t0 / a.page) : 0;
         const bool good = need && id >= 0 && id < a.n_pages;
@@ -536,56 +564,67 @@ __global__ void __launch_bounds__(kAttnThreads, 1) k_q4_attn(const __grid_consta
                      bytes, smem_u32(full));
         }
       }
-      left -= nt;
-      off = 0;
-      if (left > 0) walk.next(s);
+      __syncwarp();
+      if (lane == 0) done(k);
     }
   } else if (warp == 1) {
     // ---------------------------------------------------------- MMAs
     if (lane == 0) {
       constexpr uint32_t idS = idesc_f16(128, N, false), idO = idesc_f16(128, N, true);
-      const uint32_t q = smem_u32(base + S::oQ), p = smem_u32(base + S::oP), v = smem_u32(base + S::oV);
-      uint32_t it = 0, seg = 0;
+      // descriptors grow by their operand's offset / 16
+      const uint64_t dq = tc::sdesc(smem_u32(base + S::oQ)), dp = tc::sdesc(smem_u32(base + S::oP));
+      const uint64_t dv = sdesc_mn(smem_u32(base + S::oV), DH == 64 ? 0 : 8192);
+      uint32_t it = 0;
       bool ok = true;
       auto pv = [&](uint32_t i, bool first) {
         if (!wait(&M.p_full, i & 1, fail)) return false;
+        uint32_t acc = first ? 0u : 1u;
 #pragma unroll 1
         for (int h = 0; h < 2; ++h) {
           if (!wait(&M.v_full[h], i & 1, fail)) return false;
           tc_fence_after();
+          const uint64_t vh = dv + h * (S::kV / 32), ph = dp + h * (N * 8);
 #pragma unroll
-          for (int k = 0; k < 4; ++k)
+          for (int k = 0; k < 4; ++k) {
 #pragma unroll
             for (int mb = 0; mb < S::MB; ++mb)
-              mma_f16_ss(tmem + S::cO + mb * N,
-                         sdesc_mn(v + h * (S::kV / 2) + mb * 2 * 8192 + k * 2048, DH == 64 ? 0 : 8192),
-                         tc::sdesc(p + h * N * 128 + k * 32), idO, (first && h == 0 && k == 0) ? 0u : 1u);
+              mma_f16_ss(tmem + S::cO + mb * N, vh + mb * 1024 + k * 128, ph + k * 2, idO, acc);
+            acc = 1u;
+          }
           tc::mma_commit(smem_u32(&M.v_empty[h]));
         }
         tc::mma_commit(smem_u32(&M.p_empty));
         return true;
       };
-      while (left > 0 && ok) {
-        const int nt = (int)min((long long)(s.cnt - off), left);
-        ok = wait(&M.q_full, seg & 1, fail);
-        for (int i = 0; i < nt && ok; ++i, ++it) {
-          const uint32_t b = it % S::SB, round = it / S::SB;
-          ok = wait(&M.k_full[b], round & 1, fail) && (round == 0 || wait(&M.s_empty[b], (round - 1) & 1, fail));
-          if (!ok) break;
-          tc_fence_after();
+      int flags = 0;
+#pragma unroll 1
+      for (uint32_t k = 0; ok && !(flags & 4); ++k) {
+        ok = wait(&M.run_full[k % kRuns], (k / kRuns) & 1, fail);
+        if (!ok) break;
+        const int nt = M.run[k % kRuns].nt;
+        flags = M.run[k % kRuns].flags;
+        done(k);
+        if (nt > 0) ok = wait(&M.q_full, k & 1, fail);
+        // S of tile i, then P.V of the tile before
+#pragma unroll 1
+        for (int i = 0; i <= nt && nt > 0 && ok; ++i) {
+          if (i < nt) {
+            const uint32_t b = it % S::SB, round = it / S::SB;
+            ok = wait(&M.k_full[b], round & 1, fail) && (round == 0 || wait(&M.s_empty[b], (round - 1) & 1, fail));
+            if (!ok) break;
+            tc_fence_after();
+#pragma unroll 1
+            for (int c = 0; c < DH / 64; ++c)
 #pragma unroll
-          for (int k = 0; k < DH / 16; ++k)
-            mma_f16_ts(tmem + S::cS + b * N, tmem + S::cK + b * S::KC + k * 8,
-                       tc::sdesc(q + (k / 4) * N * 128 + (k % 4) * 32), idS, k > 0 ? 1u : 0u);
-          tc::mma_commit(smem_u32(&M.k_empty[b]));
-          tc::mma_commit(smem_u32(&M.s_full[b]));
-          if (i > 0) ok = pv(it - 1, i == 1);
+              for (int e = 0; e < 4; ++e)
+                mma_f16_ts(tmem + S::cS + b * N, tmem + S::cK + b * S::KC + c * 32 + e * 8, dq + c * (N * 8) + e * 2, idS,
+                           (c | e) > 0 ? 1u : 0u);
+            tc::mma_commit(smem_u32(&M.k_empty[b]));
+            tc::mma_commit(smem_u32(&M.s_full[b]));
+            ++it;
+          }
+          if (i > 0) ok = pv(i < nt ? it - 2 : it - 1, i == 1);
         }
-        if (ok) ok = pv(it - 1, nt == 1);
-        left -= nt;
-        off = 0;
-        ++seg;
-        if (left > 0) walk.next(s);
       }
       if (!ok) {  // what was issued ends before its operands and tensor memory go
         tc::mma_commit(smem_u32(&M.drain));
@@ -598,35 +637,41 @@ __global__ void __launch_bounds__(kAttnThreads, 1) k_q4_attn(const __grid_consta
     const int quarter = warp & 3, tid = threadIdx.x & 127;
     const bool do_k = kOneDq || warp < 8, do_v = kOneDq || warp >= 8;
 
-    // position `tid` of tile `i` to tensor memory, as f16; the row is read
-    // whole before the first store, and its stage given back there
-    auto deq_k = [&](uint32_t i, const Seg& sg, int tile) {
+    // position `tid` of tile `i` to tensor memory, as f16; half a row is read
+    // before its first store, and the stage given back once all is read
+    constexpr int kKW = DH == 64 ? 1 : DH / 128;
+    auto deq_k = [&](uint32_t i, const Run& sg, int tile) {
       const int st = i % S::KS;
       const uint32_t b = i % S::SB, round = i / S::SB;
       if (!wait_warp(&M.rawk_full[st], (i / S::KS) & 1, fail)) return false;
       const int t = tile * kT + tid;
       const uint32_t live = t >= sg.lo && t < sg.end && (M.valid_k[st] >> (tid / ps) & 1) ? ~0u : 0u;
       const uint8_t* row = base + S::oRawK + st * S::kRaw + tid * S::kRow;
-      uint32_t code[DH / 8], sc[DH / 64];
-      load_words<DH / 8, S::kRow>(row, code);
-      load_words<DH / 64, S::kRow>(row + DH / 2, sc);
-      __syncwarp();
-      if (lane == 0) mbar_arrive(smem_u32(&M.rawk_empty[st]));
       if (round > 0 && !wait_warp(&M.k_empty[b], (round - 1) & 1, fail)) return false;
       tc_fence_after();
-#pragma unroll
-      for (int c = 0; c < DH / 32; ++c) {  // 32 elements: 16 bytes, two scales
-        uint32_t x[16];
-        const uint32_t s2 = e4m3x2_to_f16x2((sc[c / 2] & live) >> (16 * (c & 1)));
-        const uint32_t slo = __byte_perm(s2, s2, 0x1010), shi = __byte_perm(s2, s2, 0x3232);
-#pragma unroll
-        for (int w = 0; w < 4; ++w) {
-          uint32_t h[4];
-          e2m1x8_to_f16(code[4 * c + w] & live, h);
-#pragma unroll
-          for (int e = 0; e < 4; ++e) x[4 * w + e] = hmul2_bits(h[e], w < 2 ? slo : shi);
+#pragma unroll 1
+      for (int p = 0; p < DH / 64; p += kKW) {  // kKW x 64 elements
+        uint32_t code[8 * kKW], sc[kKW];
+        load_words<8 * kKW, S::kRow>(row + 32 * p, code);
+        load_words<kKW, S::kRow>(row + DH / 2 + 4 * p, sc);
+        if (p + kKW == DH / 64) {
+          __syncwarp();
+          if (lane == 0) mbar_arrive(smem_u32(&M.rawk_empty[st]));
         }
-        tmem_st_rows16(tmem + S::cK + b * S::KC + 16 * c + ((uint32_t)(32 * quarter) << 16), x);
+#pragma unroll
+        for (int c = 0; c < 2 * kKW; ++c) {  // 32 elements: 16 bytes, two scales
+          uint32_t x[16];
+          const uint32_t s2 = e4m3x2_to_f16x2((sc[c / 2] & live) >> (16 * (c & 1)));
+          const uint32_t slo = __byte_perm(s2, s2, 0x1010), shi = __byte_perm(s2, s2, 0x3232);
+#pragma unroll
+          for (int w = 0; w < 4; ++w) {
+            uint32_t h[4];
+            e2m1x8_to_f16(code[4 * c + w] & live, h);
+#pragma unroll
+            for (int e = 0; e < 4; ++e) x[4 * w + e] = hmul2_bits(h[e], w < 2 ? slo : shi);
+          }
+          tmem_st_rows16(tmem + S::cK + b * S::KC + 32 * p + 16 * c + ((uint32_t)(32 * quarter) << 16), x);
+        }
       }
       tc_wait_st();
       tc_fence_before();
@@ -635,7 +680,7 @@ __global__ void __launch_bounds__(kAttnThreads, 1) k_q4_attn(const __grid_consta
       return true;
     };
     // tile `i`'s V in two halves of 64 positions; a thread takes half a row
-    auto deq_v = [&](uint32_t i, const Seg& sg, int tile, uint32_t run, bool first) {
+    auto deq_v = [&](uint32_t i, const Run& sg, int tile, uint32_t run, bool first) {
       const int st = i % S::VS;
       // 0 x NaN would reach rows that do not see the position: where a tile
       // has such rows, NaN is kept out of the product and noted for the end
@@ -702,36 +747,38 @@ __global__ void __launch_bounds__(kAttnThreads, 1) k_q4_attn(const __grid_consta
       }
       return true;
     };
-    uint32_t it = 0, run = 0;
+    uint32_t it = 0;
     bool ok = true;
-    Seg sv = s;        // V lags K by one tile where one group does both
+    Run s, sv;         // V lags K by one tile where one group does both
     int tv = -1;
     uint32_t rv = 0;
     bool fv = false;
-    while (left > 0 && ok) {
-      const int nt = (int)min((long long)(s.cnt - off), left);
-      for (int i = 0; i < nt && ok; ++i, ++it) {
-        const int tile = s.t0 + off + i;
-        if (do_k) ok = deq_k(it, s, tile);
+    s.flags = 0;
+#pragma unroll 1
+    for (uint32_t k = 0; ok && !(s.flags & 4); ++k) {
+      ok = __all_sync(0xFFFFFFFFu, next(k, s));
+      __syncwarp();
+      if (!ok) break;
+      if (lane == 0) done(k);
+      // (where both are done, one more turn after the last tile for its V)
+#pragma unroll 1
+      for (int i = 0; ok && (i < s.nt || (kOneDq && i == s.nt && (s.flags & 4) && it > 0)); ++i) {
+        const int tile = s.tile + i;
+        if (do_k && i < s.nt) ok = deq_k(it, s, tile);
         if (do_v && ok) {
           if (!kOneDq) {
-            ok = deq_v(it, s, tile, run, i == 0);
+            ok = deq_v(it, s, tile, k, i == 0);
           } else {
             if (tv >= 0) ok = deq_v(it - 1, sv, tv, rv, fv);
             sv = s;
             tv = tile;
-            rv = run;
+            rv = k;
             fv = i == 0;
           }
         }
-        ok = __all_sync(0xFFFFFFFFu, ok);
+        ++it;
       }
-      left -= nt;
-      off = 0;
-      ++run;
-      if (left > 0) walk.next(s);
     }
-    if (kOneDq && ok && tv >= 0) deq_v(it - 1, sv, tv, rv, fv);
   } else if (warp >= kSoftWarp) {
     // ---------------------------------------------------------- softmax
     const int sg = (warp - kSoftWarp) >> 2, quarter = warp & 3, bar = 1 + sg;
@@ -739,12 +786,19 @@ __global__ void __launch_bounds__(kAttnThreads, 1) k_q4_attn(const __grid_consta
     const int c0 = sg * NC;                     // its first query row (= column)
     const int pr = 2 * (lane & 3);              // the thread's column pair in a block
     const uint32_t lanes = (uint32_t)(32 * quarter) << 16;
-    const int G = walk.G;
+    const int G = a.n_q / a.n_kv;
     uint32_t it = 0, run = 0;
     bool ok = true;  // (a warp that fails leaves with its group, at a vote)
-    while (left > 0) {
-      const int nt = (int)min((long long)(s.cnt - off), left);
-      const bool begins = off == 0, ends = off + nt == s.cnt;
+    Run s;
+    s.flags = 0;
+#pragma unroll 1
+    for (; !(s.flags & 4); ++run) {
+      ok = next(run, s);
+      if (group_any(bar, !ok)) break;
+      if (lane == 0) done(run);
+      if (s.nt == 0) break;
+      const int nt = s.nt;
+      const bool begins = s.flags & 1, ends = s.flags & 2;
       // ---- queries: eight lanes per row, scaled by a power of two to [2^13, 2^14)
       const int kexp = head_exp(a.k_exp, s.g);
 #pragma unroll 1
@@ -814,7 +868,7 @@ __global__ void __launch_bounds__(kAttnThreads, 1) k_q4_attn(const __grid_consta
           if ((lane & 7) == 0) {
             M.cm[j][0] = ldexpf(a.scale * 1.44269504f, kexp - (13 - ex));
             M.cm[j][1] = kUnset;
-            M.lim[j] = real ? s.L - s.n + i : -1;
+            M.lim[j] = real ? s.pos + i : -1;
             M.dst[j] = real ? (s.a0 + i) * a.n_q + h : -1;
           }
         }
@@ -832,8 +886,8 @@ __global__ void __launch_bounds__(kAttnThreads, 1) k_q4_attn(const __grid_consta
         const uint32_t sb = it % S::SB;
         ok = wait(&M.s_full[sb], (it / S::SB) & 1, fail) && ok;
         tc_fence_after();
-        const int t0 = (s.t0 + off + i) * kT;
-        const bool edge = s.edge(s.t0 + off + i, a.window);
+        const int t0 = (s.tile + i) * kT;
+        const bool edge = s.edge(s.tile + i, a.window);
         uint32_t v[2][4 * NB];
         // y = c s - m, the vote, and where some y passes 15 a move of the maxima
         // and y once more (the code is there once: it has to stay in the
@@ -1028,15 +1082,19 @@ __global__ void __launch_bounds__(kAttnThreads, 1) k_q4_attn(const __grid_consta
         const float l = M.red[0][col] + M.red[1][col] + M.red[2][col] + M.red[3][col];
         const float m = M.cm[col][1];
         if (whole) {
-          M.f[col] = l != 0.f ? pow2i(head_exp(a.v_exp, s.g)) / l : 0.f;
-          if (a.lse && M.dst[col] >= 0) a.lse[M.dst[col]] = l != 0.f ? (m + log2f(l)) * 0.693147181f : -INFINITY;
+          M.f[col] = l != 0.f ? pow2i(head_exp(a.v_exp, s.g)) * __frcp_rn(l) : 0.f;
+          if (a.lse && M.dst[col] >= 0) a.lse[M.dst[col]] = l != 0.f ? (m + __log2f(l)) * 0.693147181f : -INFINITY;
         } else {
           a.part_ml[(long long)slot * S::RT + col] = make_float2(m, l);
         }
       }
       if (!whole && sg == 0 && me == 0)
-        a.part_meta[slot] = make_int4(s.r, s.g, s.j, begins ? part_end(M, s.cnt - nt) : -1);
+        a.part_meta[slot] = make_int4(s.r, s.g, s.j, begins ? s.last : -1);
       group_sync(bar);
+      auto put = [](void* out, long long at, float y) {
+        if (WIDE) static_cast<float*>(out)[at] = y;
+        else static_cast<__nv_bfloat16*>(out)[at] = __float2bfloat16_rn(y);
+      };
       if (DH > 64 || quarter < 2) {
 #pragma unroll 1
         for (int mb = 0; mb < S::MB; ++mb)
@@ -1052,27 +1110,30 @@ __global__ void __launch_bounds__(kAttnThreads, 1) k_q4_attn(const __grid_consta
             }
             const int d = mb * 128 + 32 * quarter + lane;
             if (M.nan_run[run & 1] == run + 1) {
+              uint32_t nan = 0;
+#pragma unroll 1
+              for (int e = 0; e < 8; ++e)
+                nan |= (uint32_t)sees_nan<DH / 16>(s.first, s.tile + nt - s.first, s.p0, s.p1, M.nan_bits[run & 1], d / 16,
+                                                   M.lim[c0 + c + e], a.window) << e;
 #pragma unroll
               for (int e = 0; e < 8; ++e)
-                if (sees_nan<DH / 16>(s.t0, s.cnt, s.p0, s.p1, M.nan_bits[run & 1], d / 16, M.lim[c0 + c + e], a.window))
-                  o[e] = __int_as_float(0x7FC00000);
+                if (nan >> e & 1) o[e] = __int_as_float(0x7FC00000);
             }
+            if (whole) {
 #pragma unroll
-            for (int e = 0; e < 8; ++e) {
-              const int col = c0 + c + e;
-              const int dst = M.dst[col];
-              if (dst < 0) continue;
-              if (whole) store_elem(a.out, WIDE ? MTP_DTYPE_F32 : MTP_DTYPE_BF16, (long long)dst * DH + d, o[e] * M.f[col]);
-              else a.part_o[((long long)slot * S::RT + col) * DH + d] = o[e];
+              for (int e = 0; e < 8; ++e) {
+                const int dst = M.dst[c0 + c + e];
+                if (dst >= 0) put(a.out, (long long)dst * DH + d, o[e] * M.f[c0 + c + e]);
+              }
+            } else {
+              float* p = a.part_o + ((long long)slot * S::RT + c0 + c) * DH + d;
+#pragma unroll
+              for (int e = 0; e < 8; ++e) p[e * DH] = o[e];
             }
           }
       }
       tc_fence_before();
-      left -= nt;
-      off = 0;
-      if (left > 0) walk.next(s);
       group_sync(bar);
-      ++run;
     }
   }
 
