@@ -149,15 +149,33 @@ __host__ __device__ constexpr uint32_t idesc_f16(int m, int n, bool a_mn) {
   return (1u << 4) | ((a_mn ? 1u : 0u) << 15) | ((uint32_t)(n >> 3) << 17) | ((uint32_t)(m >> 4) << 24);
 }
 
+// Issued by a converged warp, one lane elected in the instruction's own
+// predicate: operands that are the same for the warp then live in uniform
+// registers. (A branch on one lane costs moves into them for every MMA: 54
+// cycles each where the tensor core needs 20 to 40 at N = 32.)
 __device__ __forceinline__ void mma_f16_ss(uint32_t d, uint64_t a, uint64_t b, uint32_t idesc, uint32_t acc) {
-  tc::mma_bf16(d, a, b, idesc, acc);  // the descriptor names the types
+  asm volatile(
+      "{\n\t.reg .pred p, q;\n\t"
+      "elect.sync _|q, 0xffffffff;\n\t"
+      "setp.ne.b32 p, %4, 0;\n\t"
+      "@q tcgen05.mma.cta_group::1.kind::f16 [%0], %1, %2, %3, p;\n\t}" ::"r"(d),
+      "l"(a), "l"(b), "r"(idesc), "r"(acc)
+      : "memory");
 }
 __device__ __forceinline__ void mma_f16_ts(uint32_t d, uint32_t a, uint64_t b, uint32_t idesc, uint32_t acc) {
   asm volatile(
-      "{\n\t.reg .pred p;\n\t"
+      "{\n\t.reg .pred p, q;\n\t"
+      "elect.sync _|q, 0xffffffff;\n\t"
       "setp.ne.b32 p, %4, 0;\n\t"
-      "tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, p;\n\t}" ::"r"(d),
+      "@q tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, p;\n\t}" ::"r"(d),
       "r"(a), "l"(b), "r"(idesc), "r"(acc)
+      : "memory");
+}
+__device__ __forceinline__ void mma_commit_elect(uint32_t bar) {
+  asm volatile(
+      "{\n\t.reg .pred q;\n\t"
+      "elect.sync _|q, 0xffffffff;\n\t"
+      "@q tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.b64 [%0];\n\t}" ::"r"(bar)
       : "memory");
 }
 
@@ -251,12 +269,12 @@ struct Shape {
   static constexpr int kRaw = kT * kRow;                 // a tile's rows of K or V
   static constexpr int kV = kT * DH * 2, kQ = N * DH * 2, kP = N * kT * 2;
   static constexpr int kMetaBytes = 8192;
-  static constexpr int kRoom = (227 * 1024 - 1024 - kMetaBytes - kV - kQ - kP) / kRaw;
+  static constexpr int kRoom = (227 * 1024 - kMetaBytes - kV - kQ - kP) / kRaw;
   static constexpr int KS = kRoom >= 16 ? 8 : (kRoom + 1) / 2;  // ring stages
   static constexpr int VS = kRoom >= 16 ? 8 : kRoom / 2;
   static constexpr int oV = 0, oQ = kV, oP = oQ + kQ, oRawK = oP + kP, oRawV = oRawK + KS * kRaw;
   static constexpr int oMeta = (oRawV + VS * kRaw + 127) / 128 * 128;
-  static constexpr int kSmem = oMeta + kMetaBytes + 1024;
+  static constexpr int kSmem = oMeta + kMetaBytes;
   static_assert(VS >= 1 && cEnd <= 512, "shape");
 };
 
@@ -360,10 +378,10 @@ __device__ __forceinline__ bool wait_warp(uint64_t* bar, uint32_t parity, volati
 template <int DH, int N, bool WIDE>
 __global__ void __launch_bounds__(kAttnThreads, 1) k_q4_attn(const __grid_constant__ Q4AttnArgs a) {
   using S = Shape<DH, N, WIDE>;
-  extern __shared__ uint8_t smem_raw[];
-  uint8_t* base = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
+  extern __shared__ __align__(1024) uint8_t smem_raw[];  // (swizzled operands go by address bits 7 to 9)
+  uint8_t* const base = smem_raw;
   auto& M = *reinterpret_cast<Meta<DH>*>(base + S::oMeta);
-  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const int warp = __shfl_sync(0xFFFFFFFFu, (int)threadIdx.x >> 5, 0), lane = threadIdx.x & 31;
   constexpr bool kOneDq = S::SG == 2;                    // one warpgroup dequantises K and V
   constexpr int kSoftWarp = kOneDq ? 8 : 12;             // first softmax warp
   constexpr int kSoftWarps = 4 * S::SG;
@@ -569,67 +587,67 @@ __global__ void __launch_bounds__(kAttnThreads, 1) k_q4_attn(const __grid_consta
     }
   } else if (warp == 1) {
     // ---------------------------------------------------------- MMAs
-    if (lane == 0) {
-      constexpr uint32_t idS = idesc_f16(128, N, false), idO = idesc_f16(128, N, true);
-      // descriptors grow by their operand's offset / 16
-      const uint64_t dq = tc::sdesc(smem_u32(base + S::oQ)), dp = tc::sdesc(smem_u32(base + S::oP));
-      const uint64_t dv = sdesc_mn(smem_u32(base + S::oV), DH == 64 ? 0 : 8192);
-      uint32_t it = 0;
-      bool ok = true;
-      auto pv = [&](uint32_t i, bool first) {
-        if (!wait(&M.p_full, i & 1, fail)) return false;
-        uint32_t acc = first ? 0u : 1u;
+    constexpr uint32_t idS = idesc_f16(128, N, false), idO = idesc_f16(128, N, true);
+    // descriptors grow by their operand's offset / 16
+    const uint32_t sm = smem_u32(smem_raw), tm = __shfl_sync(0xFFFFFFFFu, tmem, 0);
+    const uint64_t dq = tc::sdesc(sm + S::oQ), dp = tc::sdesc(sm + S::oP);
+    const uint64_t dv = sdesc_mn(sm + S::oV, DH == 64 ? 0 : 8192);
+    uint32_t it = 0;
+    bool ok = true;
+    auto pv = [&](uint32_t i, bool first) {
+      if (!wait_warp(&M.p_full, i & 1, fail)) return false;
+      uint32_t acc = first ? 0u : 1u;
 #pragma unroll 1
-        for (int h = 0; h < 2; ++h) {
-          if (!wait(&M.v_full[h], i & 1, fail)) return false;
+      for (int h = 0; h < 2; ++h) {
+        if (!wait_warp(&M.v_full[h], i & 1, fail)) return false;
+        tc_fence_after();
+        const uint64_t vh = dv + h * (S::kV / 32), ph = dp + h * (N * 8);
+#pragma unroll
+        for (int k = 0; k < 4; ++k) {
+#pragma unroll
+          for (int mb = 0; mb < S::MB; ++mb)
+            mma_f16_ss(tm + S::cO + mb * N, vh + mb * 1024 + k * 128, ph + k * 2, idO, acc);
+          acc = 1u;
+        }
+        mma_commit_elect(smem_u32(&M.v_empty[h]));
+      }
+      mma_commit_elect(smem_u32(&M.p_empty));
+      return true;
+    };
+    int flags = 0;
+#pragma unroll 1
+    for (uint32_t k = 0; ok && !(flags & 4); ++k) {
+      ok = wait_warp(&M.run_full[k % kRuns], (k / kRuns) & 1, fail);
+      if (!ok) break;
+      const int nt = __shfl_sync(0xFFFFFFFFu, M.run[k % kRuns].nt, 0);
+      flags = __shfl_sync(0xFFFFFFFFu, M.run[k % kRuns].flags, 0);
+      if (lane == 0) done(k);
+      __syncwarp();
+      if (nt > 0) ok = wait_warp(&M.q_full, k & 1, fail);
+      // S of tile i, then P.V of the tile before
+#pragma unroll 1
+      for (int i = 0; i <= nt && nt > 0 && ok; ++i) {
+        if (i < nt) {
+          const uint32_t b = it % S::SB, round = it / S::SB;
+          ok = wait_warp(&M.k_full[b], round & 1, fail) && (round == 0 || wait_warp(&M.s_empty[b], (round - 1) & 1, fail));
+          if (!ok) break;
           tc_fence_after();
-          const uint64_t vh = dv + h * (S::kV / 32), ph = dp + h * (N * 8);
+#pragma unroll 1
+          for (int c = 0; c < DH / 64; ++c)
 #pragma unroll
-          for (int k = 0; k < 4; ++k) {
-#pragma unroll
-            for (int mb = 0; mb < S::MB; ++mb)
-              mma_f16_ss(tmem + S::cO + mb * N, vh + mb * 1024 + k * 128, ph + k * 2, idO, acc);
-            acc = 1u;
-          }
-          tc::mma_commit(smem_u32(&M.v_empty[h]));
+            for (int e = 0; e < 4; ++e)
+              mma_f16_ts(tm + S::cS + b * N, tm + S::cK + b * S::KC + c * 32 + e * 8, dq + c * (N * 8) + e * 2, idS,
+                         (c | e) > 0 ? 1u : 0u);
+          mma_commit_elect(smem_u32(&M.k_empty[b]));
+          mma_commit_elect(smem_u32(&M.s_full[b]));
+          ++it;
         }
-        tc::mma_commit(smem_u32(&M.p_empty));
-        return true;
-      };
-      int flags = 0;
-#pragma unroll 1
-      for (uint32_t k = 0; ok && !(flags & 4); ++k) {
-        ok = wait(&M.run_full[k % kRuns], (k / kRuns) & 1, fail);
-        if (!ok) break;
-        const int nt = M.run[k % kRuns].nt;
-        flags = M.run[k % kRuns].flags;
-        done(k);
-        if (nt > 0) ok = wait(&M.q_full, k & 1, fail);
-        // S of tile i, then P.V of the tile before
-#pragma unroll 1
-        for (int i = 0; i <= nt && nt > 0 && ok; ++i) {
-          if (i < nt) {
-            const uint32_t b = it % S::SB, round = it / S::SB;
-            ok = wait(&M.k_full[b], round & 1, fail) && (round == 0 || wait(&M.s_empty[b], (round - 1) & 1, fail));
-            if (!ok) break;
-            tc_fence_after();
-#pragma unroll 1
-            for (int c = 0; c < DH / 64; ++c)
-#pragma unroll
-              for (int e = 0; e < 4; ++e)
-                mma_f16_ts(tmem + S::cS + b * N, tmem + S::cK + b * S::KC + c * 32 + e * 8, dq + c * (N * 8) + e * 2, idS,
-                           (c | e) > 0 ? 1u : 0u);
-            tc::mma_commit(smem_u32(&M.k_empty[b]));
-            tc::mma_commit(smem_u32(&M.s_full[b]));
-            ++it;
-          }
-          if (i > 0) ok = pv(i < nt ? it - 2 : it - 1, i == 1);
-        }
+        if (i > 0) ok = pv(i < nt ? it - 2 : it - 1, i == 1);
       }
-      if (!ok) {  // what was issued ends before its operands and tensor memory go
-        tc::mma_commit(smem_u32(&M.drain));
-        mbar_wait(smem_u32(&M.drain), 0, kQ4WaitLimit);
-      }
+    }
+    if (!ok) {  // what was issued ends before its operands and tensor memory go
+      mma_commit_elect(smem_u32(&M.drain));
+      mbar_wait(smem_u32(&M.drain), 0, kQ4WaitLimit);
     }
     __syncwarp();
   } else if (warp >= 4 && warp < kSoftWarp) {
@@ -637,9 +655,7 @@ __global__ void __launch_bounds__(kAttnThreads, 1) k_q4_attn(const __grid_consta
     const int quarter = warp & 3, tid = threadIdx.x & 127;
     const bool do_k = kOneDq || warp < 8, do_v = kOneDq || warp >= 8;
 
-    // position `tid` of tile `i` to tensor memory, as f16; half a row is read
-    // before its first store, and the stage given back once all is read
-    constexpr int kKW = DH == 64 ? 1 : DH / 128;
+    // position `tid` of tile `i` to tensor memory, as f16
     auto deq_k = [&](uint32_t i, const Run& sg, int tile) {
       const int st = i % S::KS;
       const uint32_t b = i % S::SB, round = i / S::SB;
@@ -649,30 +665,32 @@ __global__ void __launch_bounds__(kAttnThreads, 1) k_q4_attn(const __grid_consta
       const uint8_t* row = base + S::oRawK + st * S::kRaw + tid * S::kRow;
       if (round > 0 && !wait_warp(&M.k_empty[b], (round - 1) & 1, fail)) return false;
       tc_fence_after();
+      // 32 elements (16 bytes, two scales) a turn, the next ones' words in
+      // flight: a short loop, since the roles share the instruction cache
+      uint32_t code[4], sc = *reinterpret_cast<const uint16_t*>(row + DH / 2);
+      load_words<4, S::kRow>(row, code);
+      uint32_t at = tmem + S::cK + b * S::KC + ((uint32_t)(32 * quarter) << 16);
 #pragma unroll 1
-      for (int p = 0; p < DH / 64; p += kKW) {  // kKW x 64 elements
-        uint32_t code[8 * kKW], sc[kKW];
-        load_words<8 * kKW, S::kRow>(row + 32 * p, code);
-        load_words<kKW, S::kRow>(row + DH / 2 + 4 * p, sc);
-        if (p + kKW == DH / 64) {
-          __syncwarp();
-          if (lane == 0) mbar_arrive(smem_u32(&M.rawk_empty[st]));
+      for (int c = 0; c < DH / 32; ++c, at += 16) {
+        uint32_t x[16], s2 = e4m3x2_to_f16x2(sc & live);
+        const uint32_t slo = __byte_perm(s2, s2, 0x1010), shi = __byte_perm(s2, s2, 0x3232);
+#pragma unroll
+        for (int w = 0; w < 4; ++w) {
+          uint32_t h[4];
+          e2m1x8_to_f16(code[w] & live, h);
+#pragma unroll
+          for (int e = 0; e < 4; ++e) x[4 * w + e] = h[e];
+        }
+        if (c + 1 < DH / 32) {
+          sc = *reinterpret_cast<const uint16_t*>(row + DH / 2 + 2 * (c + 1));
+          load_words<4, S::kRow>(row + 16 * (c + 1), code);
         }
 #pragma unroll
-        for (int c = 0; c < 2 * kKW; ++c) {  // 32 elements: 16 bytes, two scales
-          uint32_t x[16];
-          const uint32_t s2 = e4m3x2_to_f16x2((sc[c / 2] & live) >> (16 * (c & 1)));
-          const uint32_t slo = __byte_perm(s2, s2, 0x1010), shi = __byte_perm(s2, s2, 0x3232);
-#pragma unroll
-          for (int w = 0; w < 4; ++w) {
-            uint32_t h[4];
-            e2m1x8_to_f16(code[4 * c + w] & live, h);
-#pragma unroll
-            for (int e = 0; e < 4; ++e) x[4 * w + e] = hmul2_bits(h[e], w < 2 ? slo : shi);
-          }
-          tmem_st_rows16(tmem + S::cK + b * S::KC + 32 * p + 16 * c + ((uint32_t)(32 * quarter) << 16), x);
-        }
+        for (int e = 0; e < 16; ++e) x[e] = hmul2_bits(x[e], e < 8 ? slo : shi);
+        tmem_st_rows16(at, x);
       }
+      __syncwarp();
+      if (lane == 0) mbar_arrive(smem_u32(&M.rawk_empty[st]));
       tc_wait_st();
       tc_fence_before();
       __syncwarp();
@@ -694,16 +712,13 @@ __global__ void __launch_bounds__(kAttnThreads, 1) k_q4_attn(const __grid_consta
         const int tr = h * 64 + tt, t = tile * kT + tr;
         const uint32_t live = t >= sg.lo && t < sg.end && (M.valid_v[st] >> (tr / ps) & 1) ? ~0u : 0u;
         const uint8_t* row = base + S::oRawV + st * S::kRaw + tr * S::kRow;
-        uint32_t code[kD / 8], sc[kS];
-        load_words<kD / 8, S::kRow>(row + part * (kD / 2), code);
+        uint32_t code[4], sc[kS];
+        const uint8_t* from = row + part * (kD / 2);
+        load_words<4, S::kRow>(from, code);
         if (kD >= 64) load_words<kS, S::kRow>(row + DH / 2 + part * (kD / 16), sc);
         else sc[0] = *reinterpret_cast<const uint16_t*>(row + DH / 2 + part * (kD / 16));
 #pragma unroll
         for (int w = 0; w < kS; ++w) sc[w] &= live;
-        if (h == 1) {
-          __syncwarp();
-          if (lane == 0) mbar_arrive(smem_u32(&M.rawv_empty[st]));
-        }
         if (i > 0 && !wait_warp(&M.v_empty[h], (i - 1) & 1, fail)) return false;
         if (first && h == 0) {
           // this warp's words, two runs old: their reader is done with them,
@@ -725,21 +740,34 @@ __global__ void __launch_bounds__(kAttnThreads, 1) k_q4_attn(const __grid_consta
             }
           }
         }
-        uint8_t* dst = base + S::oV + h * (S::kV / 2) + tt * 128;
-#pragma unroll
+        uint8_t* dst = base + S::oV + h * (S::kV / 2) + tt * 128 + part * kD / 64 * 8192;
+        int chunk = (part * kD & 63) / 8;
+        uint64_t scales = kS == 2 ? (uint64_t)sc[kS - 1] << 32 | sc[0] : sc[0];
+#pragma unroll 1
         for (int c = 0; c < kD / 32; ++c) {  // 32 elements: four words, two scales
-          const uint32_t s2 = e4m3x2_to_f16x2(sc[c / 2] >> (16 * (c & 1)));
+          const uint32_t s2 = e4m3x2_to_f16x2((uint32_t)scales);
           const uint32_t slo = __byte_perm(s2, s2, 0x1010), shi = __byte_perm(s2, s2, 0x3232);
-          const int d = part * kD + 32 * c;
+          scales >>= 16;
+          uint32_t x[16];
 #pragma unroll
           for (int w = 0; w < 4; ++w) {
             uint32_t hh[4];
-            e2m1x8_to_f16(code[4 * c + w] & live, hh);
+            e2m1x8_to_f16(code[w] & live, hh);
 #pragma unroll
-            for (int e = 0; e < 4; ++e) hh[e] = hmul2_bits(hh[e], w < 2 ? slo : shi);
-            *reinterpret_cast<uint4*>(dst + (d / 64) * 8192 + ((((d & 63) / 8 + w) ^ (tt & 7)) << 4)) =
-                make_uint4(hh[0], hh[1], hh[2], hh[3]);
+            for (int e = 0; e < 4; ++e) x[4 * w + e] = hh[e];
           }
+          if (c + 1 < kD / 32) load_words<4, S::kRow>(from + 16 * (c + 1), code);
+#pragma unroll
+          for (int w = 0; w < 4; ++w)
+            *reinterpret_cast<uint4*>(dst + (((chunk + w) ^ (tt & 7)) << 4)) =
+                make_uint4(hmul2_bits(x[4 * w], w < 2 ? slo : shi), hmul2_bits(x[4 * w + 1], w < 2 ? slo : shi),
+                           hmul2_bits(x[4 * w + 2], w < 2 ? slo : shi), hmul2_bits(x[4 * w + 3], w < 2 ? slo : shi));
+          chunk ^= 4;
+          if (chunk == 0) dst += 8192;
+        }
+        if (h == 1) {
+          __syncwarp();
+          if (lane == 0) mbar_arrive(smem_u32(&M.rawv_empty[st]));
         }
         fence_async();
         __syncwarp();
