@@ -41,6 +41,7 @@
 #include <mutex>
 
 #include <cuda_bf16.h>
+#include <cuda_fp16.h>
 
 #include "common.cuh"
 #include "kernels.h"
@@ -296,12 +297,16 @@ struct Meta {
   alignas(16) int lim[128];          // per query row: its position
   int dst[128];                      // per query row: row of out and lse, or -1
   float red[4][128];                 // per warp of a softmax group and query row
+  alignas(16) uint8_t zero[144];     // a row of zeros, read in the place of positions out of sight
   uint32_t copied[2];                // tiles of K and of V whose copies were issued
   uint64_t drain;                    // the MMAs of a run that gave up
   uint32_t nan_run[2];               // by the run's parity: 1 + the last run that noted something in nan_bits
   uint32_t nan_bits[2][4][DH / 16][4];  // edge tile, 16 dimensions: positions whose V is NaN there
 };
 static_assert(sizeof(Meta<256>) <= 8192, "meta");
+
+__device__ __forceinline__ __half2 as_half2(uint32_t u) { return *reinterpret_cast<const __half2*>(&u); }
+__device__ __forceinline__ uint32_t as_bits(__half2 h) { return *reinterpret_cast<const uint32_t*>(&h); }
 
 // NW words of a cache row in shared memory, in the widest loads that rows of
 // kRow bytes are aligned for.
@@ -382,19 +387,19 @@ __global__ void __launch_bounds__(kAttnThreads, 1) k_q4_attn(const __grid_consta
   uint8_t* const base = smem_raw;
   auto& M = *reinterpret_cast<Meta<DH>*>(base + S::oMeta);
   const int warp = __shfl_sync(0xFFFFFFFFu, (int)threadIdx.x >> 5, 0), lane = threadIdx.x & 31;
-  constexpr bool kOneDq = S::SG == 2;                    // one warpgroup dequantises K and V
-  constexpr int kSoftWarp = kOneDq ? 8 : 12;             // first softmax warp
+  constexpr int kDq = S::SG == 2 ? 1 : 2;                // dequantising warpgroups
+  constexpr int kSoftWarp = 4 + 4 * kDq;                 // first softmax warp
   constexpr int kSoftWarps = 4 * S::SG;
 
   if (threadIdx.x == 0) {
     for (int i = 0; i < 8; ++i) {
       mbar_init(smem_u32(&M.rawk_full[i]), 1);
       mbar_init(smem_u32(&M.rawv_full[i]), 1);
-      mbar_init(smem_u32(&M.rawk_empty[i]), 4);
-      mbar_init(smem_u32(&M.rawv_empty[i]), 4);
+      mbar_init(smem_u32(&M.rawk_empty[i]), 4 * kDq);
+      mbar_init(smem_u32(&M.rawv_empty[i]), 4 * kDq);
     }
     for (int i = 0; i < 2; ++i) {
-      mbar_init(smem_u32(&M.k_full[i]), 4);
+      mbar_init(smem_u32(&M.k_full[i]), 4 * kDq);
       mbar_init(smem_u32(&M.k_empty[i]), 1);
       mbar_init(smem_u32(&M.s_full[i]), 1);
       mbar_init(smem_u32(&M.s_empty[i]), kSoftWarps);
@@ -414,6 +419,7 @@ __global__ void __launch_bounds__(kAttnThreads, 1) k_q4_attn(const __grid_consta
     }
     asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
   }
+  if (threadIdx.x >= 64 && threadIdx.x < 64 + S::kRow / 4) reinterpret_cast<uint32_t*>(M.zero)[threadIdx.x - 64] = 0u;
   if (warp == 0) {
     asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(smem_u32(&M.tmem)),
                  "r"(S::kCols)
@@ -446,9 +452,9 @@ __global__ void __launch_bounds__(kAttnThreads, 1) k_q4_attn(const __grid_consta
     if (lane < 2) a.part_meta[2 * blockIdx.x + lane] = make_int4(0, 0, 0, 0);
     const int per = (a.rows + 31) / 32, r0 = min(lane * per, a.rows), r1 = min(r0 + per, a.rows);
     long long sum = 0;
+    int a0 = 0, n = 0, L = 0;
 #pragma unroll 1
     for (int r = r0; r < r1; ++r) {
-      int a0, n, L;
       walk.row(r, a0, n, L);
       if (blockIdx.x == 0 && L != a.len[r]) flag_status(a.status, MTP_ERR_BAD_ARG);
       sum += (long long)walk.per_head(n, L) * a.n_kv;
@@ -478,11 +484,14 @@ __global__ void __launch_bounds__(kAttnThreads, 1) k_q4_attn(const __grid_consta
     const unsigned who = __ballot_sync(0xFFFFFFFFu, left > 0 && inc - sum <= w0 && w0 < inc);
     const int owner = who ? __ffs(who) - 1 : 0;
     long long at = __shfl_sync(0xFFFFFFFFu, inc - sum, owner);
-    int r = __shfl_sync(0xFFFFFFFFu, r0, owner), g = 0, j = 0, o = 0, a0 = 0, n = 0, L = 0;
+    int r = __shfl_sync(0xFFFFFFFFu, r0, owner), g = 0, j = 0, o = 0;
+    a0 = __shfl_sync(0xFFFFFFFFu, a0, owner);  // (the last row that the lane looked at: its only one, mostly)
+    n = __shfl_sync(0xFFFFFFFFu, n, owner);
+    L = __shfl_sync(0xFFFFFFFFu, L, owner);
     if (left > 0) {
 #pragma unroll 1
       for (;; ++r) {
-        walk.row(r, a0, n, L);
+        if (per > 1) walk.row(r, a0, n, L);
         const int ph = walk.per_head(n, L);
         if (w0 < at + (long long)ph * a.n_kv) {
           const unsigned x = (unsigned)(w0 - at);  // (a row has fewer than 2^32 tasks)
@@ -652,84 +661,95 @@ __global__ void __launch_bounds__(kAttnThreads, 1) k_q4_attn(const __grid_consta
     __syncwarp();
   } else if (warp >= 4 && warp < kSoftWarp) {
     // ---------------------------------------------------------- dequantisers
-    const int quarter = warp & 3, tid = threadIdx.x & 127;
-    const bool do_k = kOneDq || warp < 8, do_v = kOneDq || warp >= 8;
+    // Two groups (one beside 128-column softmax) share every tile: of K each
+    // takes its part of the head dimension, of V its 64 positions. Bound by the
+    // ALU pipe (a conversion per two elements goes there, so all else is kept
+    // off it: rows out of sight point at zeros, addresses are made once).
+    const int quarter = warp & 3, tid = threadIdx.x & 127, group = (warp - 4) >> 2;
+    constexpr int kKC = DH / 32 / kDq;  // 32-element chunks of a thread's share of a K row
+    constexpr int kD = DH / 2;          // elements of a thread's share of a V row
+    const int tt = tid & 63, part = tid >> 6;
+    uint32_t vdst[kD >= 64 ? 8 : 4];    // where its 8-element chunks go, in atoms of 64 dimensions
+#pragma unroll
+    for (int w = 0; w < (kD >= 64 ? 8 : 4); ++w)
+      vdst[w] = smem_u32(smem_raw) + S::oV + part * kD / 64 * 8192 + tt * 128 +
+                ((((part * kD & 63) / 8 + w) ^ (tt & 7)) << 4);
 
-    // position `tid` of tile `i` to tensor memory, as f16
+    // NC chunks of 32 elements and their scales, from one row
+    auto load_row = [&](const uint8_t* codes, const uint8_t* scales, auto& code, auto& sc) {
+      constexpr int NC = sizeof(code) / 16;
+      load_words<4 * NC, S::kRow>(codes, code);
+      if constexpr (NC >= 2) load_words<NC / 2, S::kRow>(scales, sc);
+      else sc[0] = *reinterpret_cast<const uint16_t*>(scales);
+    };
+    // one chunk's 32 elements as f16 pairs: code x scale, exact
+    auto expand = [](const uint32_t* code, uint32_t scales, uint32_t (&x)[16]) {
+      const __half2 s2 = as_half2(e4m3x2_to_f16x2(scales));
+      const __half2 lo = __low2half2(s2), hi = __high2half2(s2);
+#pragma unroll
+      for (int w = 0; w < 4; ++w) {
+        uint32_t h[4];
+        e2m1x8_to_f16(code[w], h);
+#pragma unroll
+        for (int e = 0; e < 4; ++e) x[4 * w + e] = as_bits(__hmul2(as_half2(h[e]), w < 2 ? lo : hi));
+      }
+    };
+
+    // position `tid` of tile `i` to tensor memory
     auto deq_k = [&](uint32_t i, const Run& sg, int tile) {
       const int st = i % S::KS;
       const uint32_t b = i % S::SB, round = i / S::SB;
       if (!wait_warp(&M.rawk_full[st], (i / S::KS) & 1, fail)) return false;
       const int t = tile * kT + tid;
-      const uint32_t live = t >= sg.lo && t < sg.end && (M.valid_k[st] >> (tid / ps) & 1) ? ~0u : 0u;
-      const uint8_t* row = base + S::oRawK + st * S::kRaw + tid * S::kRow;
-      if (round > 0 && !wait_warp(&M.k_empty[b], (round - 1) & 1, fail)) return false;
-      tc_fence_after();
-      // 32 elements (16 bytes, two scales) a turn, the next ones' words in
-      // flight: a short loop, since the roles share the instruction cache
-      uint32_t code[4], sc = *reinterpret_cast<const uint16_t*>(row + DH / 2);
-      load_words<4, S::kRow>(row, code);
-      uint32_t at = tmem + S::cK + b * S::KC + ((uint32_t)(32 * quarter) << 16);
-#pragma unroll 1
-      for (int c = 0; c < DH / 32; ++c, at += 16) {
-        uint32_t x[16], s2 = e4m3x2_to_f16x2(sc & live);
-        const uint32_t slo = __byte_perm(s2, s2, 0x1010), shi = __byte_perm(s2, s2, 0x3232);
-#pragma unroll
-        for (int w = 0; w < 4; ++w) {
-          uint32_t h[4];
-          e2m1x8_to_f16(code[w] & live, h);
-#pragma unroll
-          for (int e = 0; e < 4; ++e) x[4 * w + e] = h[e];
-        }
-        if (c + 1 < DH / 32) {
-          sc = *reinterpret_cast<const uint16_t*>(row + DH / 2 + 2 * (c + 1));
-          load_words<4, S::kRow>(row + 16 * (c + 1), code);
-        }
-#pragma unroll
-        for (int e = 0; e < 16; ++e) x[e] = hmul2_bits(x[e], e < 8 ? slo : shi);
-        tmem_st_rows16(at, x);
-      }
+      const bool live = t >= sg.lo && t < sg.end && (M.valid_k[st] >> (tid / ps) & 1);
+      const uint8_t* row = live ? base + S::oRawK + st * S::kRaw + tid * S::kRow : M.zero;
+      uint32_t code[4 * kKC], sc[(kKC + 1) / 2];
+      load_row(row + group * kKC * 16, row + DH / 2 + group * kKC * 2, code, sc);
       __syncwarp();
       if (lane == 0) mbar_arrive(smem_u32(&M.rawk_empty[st]));
+      if (round > 0 && !wait_warp(&M.k_empty[b], (round - 1) & 1, fail)) return false;
+      tc_fence_after();
+#pragma unroll
+      for (int c = 0; c < kKC; ++c) {
+        uint32_t x[16];
+        expand(code + 4 * c, sc[c / 2] >> (16 * (c & 1)), x);
+        tmem_st_rows16(tmem + S::cK + b * S::KC + (group * kKC + c) * 16 + ((uint32_t)(32 * quarter) << 16), x);
+      }
       tc_wait_st();
       tc_fence_before();
       __syncwarp();
       if (lane == 0) mbar_arrive(smem_u32(&M.k_full[b]));
       return true;
     };
-    // tile `i`'s V in two halves of 64 positions; a thread takes half a row
+    // tile `i`'s V in halves of 64 positions; a thread takes half a row
     auto deq_v = [&](uint32_t i, const Run& sg, int tile, uint32_t run, bool first) {
       const int st = i % S::VS;
       // 0 x NaN would reach rows that do not see the position: where a tile
       // has such rows, NaN is kept out of the product and noted for the end
       const bool edge = sg.edge(tile, a.window);
       if (!wait_warp(&M.rawv_full[st], (i / S::VS) & 1, fail)) return false;
-      const int tt = tid & 63, part = tid >> 6;
-      constexpr int kD = DH / 2;                // elements of a thread
-      constexpr int kS = kD >= 64 ? kD / 64 : 1;  // words of its scales
 #pragma unroll 1
-      for (int h = 0; h < 2; ++h) {
+      for (int h = group; h < 2; h += kDq) {
         const int tr = h * 64 + tt, t = tile * kT + tr;
-        const uint32_t live = t >= sg.lo && t < sg.end && (M.valid_v[st] >> (tr / ps) & 1) ? ~0u : 0u;
-        const uint8_t* row = base + S::oRawV + st * S::kRaw + tr * S::kRow;
-        uint32_t code[4], sc[kS];
-        const uint8_t* from = row + part * (kD / 2);
-        load_words<4, S::kRow>(from, code);
-        if (kD >= 64) load_words<kS, S::kRow>(row + DH / 2 + part * (kD / 16), sc);
-        else sc[0] = *reinterpret_cast<const uint16_t*>(row + DH / 2 + part * (kD / 16));
-#pragma unroll
-        for (int w = 0; w < kS; ++w) sc[w] &= live;
+        const bool live = t >= sg.lo && t < sg.end && (M.valid_v[st] >> (tr / ps) & 1);
+        const uint8_t* row = live ? base + S::oRawV + st * S::kRaw + tr * S::kRow : M.zero;
+        uint32_t code[kD / 8], sc[(kD / 32 + 1) / 2];
+        load_row(row + part * (kD / 2), row + DH / 2 + part * (kD / 16), code, sc);
+        if (h + kDq >= 2) {
+          __syncwarp();
+          if (lane == 0) mbar_arrive(smem_u32(&M.rawv_empty[st]));
+        }
         if (i > 0 && !wait_warp(&M.v_empty[h], (i - 1) & 1, fail)) return false;
-        if (first && h == 0) {
-          // this warp's words, two runs old: their reader is done with them,
-          // since the last run's products are
-          for (int e = lane; e < 4 * (kD / 16) * 2; e += 32)
-            M.nan_bits[run & 1][e / (kD / 8)][part * (kD / 16) + e / 2 % (kD / 16)][(e & 1) * 2 + (quarter & 1)] = 0;
+        if (first) {
+          // this warp's words, two shares old: their reader is done with them,
+          // since the last share's products are
+          if (lane < 4 * (kD / 16))
+            M.nan_bits[run & 1][lane / (kD / 16)][part * (kD / 16) + lane % (kD / 16)][tr >> 5] = 0;
           __syncwarp();
         }
         if (edge) {
 #pragma unroll
-          for (int w = 0; w < kS; ++w) {
+          for (int w = 0; w < (kD / 32 + 1) / 2; ++w) {
             uint32_t nan = __vcmpeq4(sc[w] & 0x7F7F7F7Fu, 0x7F7F7F7Fu);
             sc[w] &= ~nan;
             while (nan) {
@@ -740,34 +760,16 @@ __global__ void __launch_bounds__(kAttnThreads, 1) k_q4_attn(const __grid_consta
             }
           }
         }
-        uint8_t* dst = base + S::oV + h * (S::kV / 2) + tt * 128 + part * kD / 64 * 8192;
-        int chunk = (part * kD & 63) / 8;
-        uint64_t scales = kS == 2 ? (uint64_t)sc[kS - 1] << 32 | sc[0] : sc[0];
-#pragma unroll 1
-        for (int c = 0; c < kD / 32; ++c) {  // 32 elements: four words, two scales
-          const uint32_t s2 = e4m3x2_to_f16x2((uint32_t)scales);
-          const uint32_t slo = __byte_perm(s2, s2, 0x1010), shi = __byte_perm(s2, s2, 0x3232);
-          scales >>= 16;
+        const uint32_t to = h * (S::kV / 2);
+#pragma unroll
+        for (int c = 0; c < kD / 32; ++c) {
           uint32_t x[16];
-#pragma unroll
-          for (int w = 0; w < 4; ++w) {
-            uint32_t hh[4];
-            e2m1x8_to_f16(code[w] & live, hh);
-#pragma unroll
-            for (int e = 0; e < 4; ++e) x[4 * w + e] = hh[e];
-          }
-          if (c + 1 < kD / 32) load_words<4, S::kRow>(from + 16 * (c + 1), code);
+          expand(code + 4 * c, sc[c / 2] >> (16 * (c & 1)), x);
 #pragma unroll
           for (int w = 0; w < 4; ++w)
-            *reinterpret_cast<uint4*>(dst + (((chunk + w) ^ (tt & 7)) << 4)) =
-                make_uint4(hmul2_bits(x[4 * w], w < 2 ? slo : shi), hmul2_bits(x[4 * w + 1], w < 2 ? slo : shi),
-                           hmul2_bits(x[4 * w + 2], w < 2 ? slo : shi), hmul2_bits(x[4 * w + 3], w < 2 ? slo : shi));
-          chunk ^= 4;
-          if (chunk == 0) dst += 8192;
-        }
-        if (h == 1) {
-          __syncwarp();
-          if (lane == 0) mbar_arrive(smem_u32(&M.rawv_empty[st]));
+            asm volatile("st.shared.v4.b32 [%0], {%1, %2, %3, %4};" ::"r"(vdst[(4 * c + w) & 7] + to + (4 * c + w) / 8 * 8192),
+                         "r"(x[4 * w]), "r"(x[4 * w + 1]), "r"(x[4 * w + 2]), "r"(x[4 * w + 3])
+                         : "memory");
         }
         fence_async();
         __syncwarp();
@@ -777,7 +779,7 @@ __global__ void __launch_bounds__(kAttnThreads, 1) k_q4_attn(const __grid_consta
     };
     uint32_t it = 0;
     bool ok = true;
-    Run s, sv;         // V lags K by one tile where one group does both
+    Run s, sv;         // V goes one tile behind K
     int tv = -1;
     uint32_t rv = 0;
     bool fv = false;
@@ -788,23 +790,15 @@ __global__ void __launch_bounds__(kAttnThreads, 1) k_q4_attn(const __grid_consta
       __syncwarp();
       if (!ok) break;
       if (lane == 0) done(k);
-      // (where both are done, one more turn after the last tile for its V)
+      // (one more turn after the last tile, for its V)
 #pragma unroll 1
-      for (int i = 0; ok && (i < s.nt || (kOneDq && i == s.nt && (s.flags & 4) && it > 0)); ++i) {
-        const int tile = s.tile + i;
-        if (do_k && i < s.nt) ok = deq_k(it, s, tile);
-        if (do_v && ok) {
-          if (!kOneDq) {
-            ok = deq_v(it, s, tile, k, i == 0);
-          } else {
-            if (tv >= 0) ok = deq_v(it - 1, sv, tv, rv, fv);
-            sv = s;
-            tv = tile;
-            rv = k;
-            fv = i == 0;
-          }
-        }
-        ++it;
+      for (int i = 0; ok && (i < s.nt || (i == s.nt && (s.flags & 4) && it > 0)); ++i, ++it) {
+        if (i < s.nt) ok = deq_k(it, s, s.tile + i);
+        if (tv >= 0 && ok) ok = deq_v(it - 1, sv, tv, rv, fv);
+        if (i == 0) sv = s;
+        tv = s.tile + i;
+        rv = k;
+        fv = i == 0;
       }
     }
   } else if (warp >= kSoftWarp) {
