@@ -268,12 +268,12 @@ struct Shape {
   static constexpr uint32_t kCols = cEnd <= 128 ? 128 : (cEnd <= 256 ? 256 : 512);
   // shared memory
   static constexpr int kRaw = kT * kRow;                 // a tile's rows of K or V
-  static constexpr int kV = kT * DH * 2, kQ = N * DH * 2, kP = N * kT * 2;
+  static constexpr int kV = kT * DH * 2, kQ = N * DH * 2, kP = N * kT * 2;  // (SB buffers of P)
   static constexpr int kMetaBytes = 8192;
-  static constexpr int kRoom = (227 * 1024 - kMetaBytes - kV - kQ - kP) / kRaw;
+  static constexpr int kRoom = (227 * 1024 - kMetaBytes - kV - kQ - SB * kP) / kRaw;
   static constexpr int KS = kRoom >= 16 ? 8 : (kRoom + 1) / 2;  // ring stages
   static constexpr int VS = kRoom >= 16 ? 8 : kRoom / 2;
-  static constexpr int oV = 0, oQ = kV, oP = oQ + kQ, oRawK = oP + kP, oRawV = oRawK + KS * kRaw;
+  static constexpr int oV = 0, oQ = kV, oP = oQ + kQ, oRawK = oP + SB * kP, oRawV = oRawK + KS * kRaw;
   static constexpr int oMeta = (oRawV + VS * kRaw + 127) / 128 * 128;
   static constexpr int kSmem = oMeta + kMetaBytes;
   static_assert(VS >= 1 && cEnd <= 512, "shape");
@@ -286,7 +286,7 @@ template <int DH>
 struct Meta {
   uint64_t rawk_full[8], rawk_empty[8], rawv_full[8], rawv_empty[8];
   uint64_t k_full[2], k_empty[2], s_full[2], s_empty[2];
-  uint64_t v_full[2], v_empty[2], p_full, p_empty, q_full;
+  uint64_t v_full[2], v_empty[2], p_full[2], p_empty[2], q_full;
   uint32_t valid_k[8], valid_v[8];   // bit p: piece p of the stage was copied
   uint32_t tmem;
   int fail;
@@ -334,19 +334,19 @@ __device__ __forceinline__ void load_words(const uint8_t* p, uint32_t (&w)[NW]) 
   }
 }
 
-// Bounded wait that gives up as soon as another role has failed.
-static __device__ __noinline__ bool wait_on(uint32_t bar, uint32_t parity, volatile int* fail) {
+// Bounded wait that gives up as soon as another role has failed. For whole,
+// converged warps: a ready wait costs some 80 cycles then, 230 where one lane
+// looks for the others, and lanes that wait for barriers of their own slow
+// every role threefold.
+__device__ __forceinline__ bool wait(uint64_t* bar, uint32_t parity, volatile int* fail) {
+  const uint32_t b = smem_u32(bar);
 #pragma unroll 1
   for (unsigned i = 0; i < kQ4WaitLimit; ++i) {
-    if (mbar_try(bar, parity)) return true;
+    if (mbar_try(b, parity)) return true;
     if ((i & 1023) == 1023 && *fail) return false;
   }
   *fail = 1;
   return false;
-}
-__device__ __forceinline__ bool wait(uint64_t* bar, uint32_t parity, volatile int* fail) {
-  const uint32_t b = smem_u32(bar);
-  return mbar_try(b, parity) || wait_on(b, parity, fail);
 }
 
 // Keeps a value read from tensor memory behind the wait that completes it.
@@ -375,11 +375,6 @@ __device__ __noinline__ bool sees_nan(int t0, int cnt, int p0, int p1, const uin
   return false;
 }
 
-// The same for a whole warp, with one answer.
-__device__ __forceinline__ bool wait_warp(uint64_t* bar, uint32_t parity, volatile int* fail) {
-  return __all_sync(0xFFFFFFFFu, wait(bar, parity, fail));
-}
-
 template <int DH, int N, bool WIDE>
 __global__ void __launch_bounds__(kAttnThreads, 1) k_q4_attn(const __grid_constant__ Q4AttnArgs a) {
   using S = Shape<DH, N, WIDE>;
@@ -405,9 +400,9 @@ __global__ void __launch_bounds__(kAttnThreads, 1) k_q4_attn(const __grid_consta
       mbar_init(smem_u32(&M.s_empty[i]), kSoftWarps);
       mbar_init(smem_u32(&M.v_full[i]), 4);
       mbar_init(smem_u32(&M.v_empty[i]), 1);
+      mbar_init(smem_u32(&M.p_full[i]), kSoftWarps);
+      mbar_init(smem_u32(&M.p_empty[i]), 1);
     }
-    mbar_init(smem_u32(&M.p_full), kSoftWarps);
-    mbar_init(smem_u32(&M.p_empty), 1);
     mbar_init(smem_u32(&M.q_full), kSoftWarps);
     M.fail = 0;
     M.copied[0] = M.copied[1] = 0;
@@ -536,7 +531,7 @@ __global__ void __launch_bounds__(kAttnThreads, 1) k_q4_attn(const __grid_consta
       for (long long rest = cnt - o - s.nt; rest > 0; rest -= q + (s.last < more)) ++s.last;
       left -= s.nt;
       o = 0;
-      if (k >= kRuns && !wait_warp(&M.run_empty[k % kRuns], (k / kRuns - 1) & 1, fail)) break;
+      if (k >= kRuns && !wait(&M.run_empty[k % kRuns], (k / kRuns - 1) & 1, fail)) break;
       if (lane == 0) {
         M.run[k % kRuns] = s;
         mbar_arrive(smem_u32(&M.run_full[k % kRuns]));
@@ -578,7 +573,6 @@ __global__ void __launch_bounds__(kAttnThreads, 1) k_q4_attn(const __grid_consta
           const int st = it % (kv ? S::VS : S::KS), round = it / (kv ? S::VS : S::KS);
           uint64_t* full = kv ? &M.rawv_full[st] : &M.rawk_full[st];
           if (round > 0) ok = wait(kv ? &M.rawv_empty[st] : &M.rawk_empty[st], (round - 1) & 1, fail);
-          ok = __all_sync(0xFFFFFFFFu, ok);
           if (!ok) break;
           if (lane == 0) {
             (kv ? M.valid_v : M.valid_k)[st] = mask;
@@ -601,16 +595,25 @@ __global__ void __launch_bounds__(kAttnThreads, 1) k_q4_attn(const __grid_consta
     const uint32_t sm = smem_u32(smem_raw), tm = __shfl_sync(0xFFFFFFFFu, tmem, 0);
     const uint64_t dq = tc::sdesc(sm + S::oQ), dp = tc::sdesc(sm + S::oP);
     const uint64_t dv = sdesc_mn(sm + S::oV, DH == 64 ? 0 : 8192);
-    uint32_t it = 0;
-    bool ok = true;
-    auto pv = [&](uint32_t i, bool first) {
-      if (!wait_warp(&M.p_full, i & 1, fail)) return false;
+    auto issue_s = [&](uint32_t i) {
+      const uint32_t b = i % S::SB;
+#pragma unroll 1
+      for (int c = 0; c < DH / 64; ++c)
+#pragma unroll
+        for (int e = 0; e < 4; ++e)
+          mma_f16_ts(tm + S::cS + b * N, tm + S::cK + b * S::KC + c * 32 + e * 8, dq + c * (N * 8) + e * 2, idS,
+                     (c | e) > 0 ? 1u : 0u);
+      mma_commit_elect(smem_u32(&M.k_empty[b]));
+      mma_commit_elect(smem_u32(&M.s_full[b]));
+    };
+    auto issue_pv = [&](uint32_t i, bool first) {
       uint32_t acc = first ? 0u : 1u;
+      const uint64_t dpb = dp + (i % S::SB) * (S::kP / 16);
 #pragma unroll 1
       for (int h = 0; h < 2; ++h) {
-        if (!wait_warp(&M.v_full[h], i & 1, fail)) return false;
+        if (!wait(&M.v_full[h], i & 1, fail)) return false;
         tc_fence_after();
-        const uint64_t vh = dv + h * (S::kV / 32), ph = dp + h * (N * 8);
+        const uint64_t vh = dv + h * (S::kV / 32), ph = dpb + h * (N * 8);
 #pragma unroll
         for (int k = 0; k < 4; ++k) {
 #pragma unroll
@@ -620,39 +623,53 @@ __global__ void __launch_bounds__(kAttnThreads, 1) k_q4_attn(const __grid_consta
         }
         mma_commit_elect(smem_u32(&M.v_empty[h]));
       }
-      mma_commit_elect(smem_u32(&M.p_empty));
+      mma_commit_elect(smem_u32(&M.p_empty[i % S::SB]));
       return true;
     };
+    uint32_t it = 0;  // tiles before the share
+    bool ok = true;
     int flags = 0;
 #pragma unroll 1
     for (uint32_t k = 0; ok && !(flags & 4); ++k) {
-      ok = wait_warp(&M.run_full[k % kRuns], (k / kRuns) & 1, fail);
+      ok = wait(&M.run_full[k % kRuns], (k / kRuns) & 1, fail);
       if (!ok) break;
       const int nt = __shfl_sync(0xFFFFFFFFu, M.run[k % kRuns].nt, 0);
       flags = __shfl_sync(0xFFFFFFFFu, M.run[k % kRuns].flags, 0);
       if (lane == 0) done(k);
       __syncwarp();
-      if (nt > 0) ok = wait_warp(&M.q_full, k & 1, fail);
-      // S of tile i, then P.V of the tile before
+      if (nt == 0) break;
+      // With two buffers S runs two tiles ahead of P.V: a tile's softmax has
+      // the other tile's products to hide behind. (The softmax that fills P of
+      // tile i has read S of tile i, so S of tile i + 2 may follow P.V of tile
+      // i without a wait of its own.) With one, S of tile i + 1 goes before
+      // P.V of tile i, as soon as S of tile i has been read.
+      const int ahead = min(S::SB, nt);
 #pragma unroll 1
-      for (int i = 0; i <= nt && nt > 0 && ok; ++i) {
-        if (i < nt) {
-          const uint32_t b = it % S::SB, round = it / S::SB;
-          ok = wait_warp(&M.k_full[b], round & 1, fail) && (round == 0 || wait_warp(&M.s_empty[b], (round - 1) & 1, fail));
-          if (!ok) break;
-          tc_fence_after();
-#pragma unroll 1
-          for (int c = 0; c < DH / 64; ++c)
-#pragma unroll
-            for (int e = 0; e < 4; ++e)
-              mma_f16_ts(tm + S::cS + b * N, tm + S::cK + b * S::KC + c * 32 + e * 8, dq + c * (N * 8) + e * 2, idS,
-                         (c | e) > 0 ? 1u : 0u);
-          mma_commit_elect(smem_u32(&M.k_empty[b]));
-          mma_commit_elect(smem_u32(&M.s_full[b]));
-          ++it;
-        }
-        if (i > 0) ok = pv(i < nt ? it - 2 : it - 1, i == 1);
+      for (int i = 0; i < ahead && ok; ++i) {
+        const uint32_t t = it + i;
+        ok = wait(&M.q_full, k & 1, fail) && wait(&M.k_full[t % S::SB], t / S::SB & 1, fail) &&
+             (t < S::SB || wait(&M.s_empty[t % S::SB], (t / S::SB - 1) & 1, fail));
+        tc_fence_after();
+        if (ok) issue_s(t);
       }
+#pragma unroll 1
+      for (int i = 0; i < nt && ok; ++i) {
+        const uint32_t t = it + i, n = t + S::SB;
+        const bool more = i + S::SB < nt;
+        if (S::SB == 1 && more) {
+          ok = wait(&M.k_full[0], n & 1, fail) && wait(&M.s_empty[0], (n - 1) & 1, fail);
+          tc_fence_after();
+          if (!ok) break;
+          issue_s(n);
+        }
+        ok = wait(&M.p_full[t % S::SB], t / S::SB & 1, fail) && issue_pv(t, i == 0);
+        if (S::SB == 2 && more && ok) {
+          ok = wait(&M.k_full[n % S::SB], n / S::SB & 1, fail);
+          tc_fence_after();
+          if (ok) issue_s(n);
+        }
+      }
+      it += nt;
     }
     if (!ok) {  // what was issued ends before its operands and tensor memory go
       mma_commit_elect(smem_u32(&M.drain));
@@ -699,7 +716,7 @@ __global__ void __launch_bounds__(kAttnThreads, 1) k_q4_attn(const __grid_consta
     auto deq_k = [&](uint32_t i, const Run& sg, int tile) {
       const int st = i % S::KS;
       const uint32_t b = i % S::SB, round = i / S::SB;
-      if (!wait_warp(&M.rawk_full[st], (i / S::KS) & 1, fail)) return false;
+      if (!wait(&M.rawk_full[st], (i / S::KS) & 1, fail)) return false;
       const int t = tile * kT + tid;
       const bool live = t >= sg.lo && t < sg.end && (M.valid_k[st] >> (tid / ps) & 1);
       const uint8_t* row = live ? base + S::oRawK + st * S::kRaw + tid * S::kRow : M.zero;
@@ -707,7 +724,7 @@ __global__ void __launch_bounds__(kAttnThreads, 1) k_q4_attn(const __grid_consta
       load_row(row + group * kKC * 16, row + DH / 2 + group * kKC * 2, code, sc);
       __syncwarp();
       if (lane == 0) mbar_arrive(smem_u32(&M.rawk_empty[st]));
-      if (round > 0 && !wait_warp(&M.k_empty[b], (round - 1) & 1, fail)) return false;
+      if (round > 0 && !wait(&M.k_empty[b], (round - 1) & 1, fail)) return false;
       tc_fence_after();
 #pragma unroll
       for (int c = 0; c < kKC; ++c) {
@@ -727,7 +744,7 @@ __global__ void __launch_bounds__(kAttnThreads, 1) k_q4_attn(const __grid_consta
       // 0 x NaN would reach rows that do not see the position: where a tile
       // has such rows, NaN is kept out of the product and noted for the end
       const bool edge = sg.edge(tile, a.window);
-      if (!wait_warp(&M.rawv_full[st], (i / S::VS) & 1, fail)) return false;
+      if (!wait(&M.rawv_full[st], (i / S::VS) & 1, fail)) return false;
 #pragma unroll 1
       for (int h = group; h < 2; h += kDq) {
         const int tr = h * 64 + tt, t = tile * kT + tr;
@@ -739,7 +756,7 @@ __global__ void __launch_bounds__(kAttnThreads, 1) k_q4_attn(const __grid_consta
           __syncwarp();
           if (lane == 0) mbar_arrive(smem_u32(&M.rawv_empty[st]));
         }
-        if (i > 0 && !wait_warp(&M.v_empty[h], (i - 1) & 1, fail)) return false;
+        if (i > 0 && !wait(&M.v_empty[h], (i - 1) & 1, fail)) return false;
         if (first) {
           // this warp's words, two shares old: their reader is done with them,
           // since the last share's products are
@@ -1025,7 +1042,7 @@ __global__ void __launch_bounds__(kAttnThreads, 1) k_q4_attn(const __grid_consta
             sum[2 * b + 1] *= f.y;
           }
           // O holds tiles before this one: rescale its columns once they are all in
-          ok = wait(&M.p_empty, (it - 1) & 1, fail);
+          ok = wait(&M.p_empty[(it - 1) % S::SB], (it - 1) / S::SB & 1, fail);
           if (group_any(bar, !ok)) { broken = true; break; }
           tc_fence_after();
 #pragma unroll 1
@@ -1063,11 +1080,10 @@ __global__ void __launch_bounds__(kAttnThreads, 1) k_q4_attn(const __grid_consta
               wl[WIDE ? b : 0][k] = pack_f16(p0 - h.x, p1 - h.y);
             }
           }
-        if (it > 0) ok = wait(&M.p_empty, (it - 1) & 1, fail) && ok;
-        __syncwarp();
+        if (it >= S::SB) ok = wait(&M.p_empty[it % S::SB], (it / S::SB - 1) & 1, fail) && ok;
         {
           const int row = lane & 7, mi = lane >> 3;
-          const uint32_t p = smem_u32(base + S::oP) + (quarter >> 1) * N * 128 + (c0 + row) * 128 +
+          const uint32_t p = smem_u32(base + S::oP) + sb * S::kP + (quarter >> 1) * N * 128 + (c0 + row) * 128 +
                              (((4 * (quarter & 1) + mi) ^ row) << 4);
 #pragma unroll
           for (int b = 0; b < NB; ++b) {
@@ -1081,11 +1097,11 @@ __global__ void __launch_bounds__(kAttnThreads, 1) k_q4_attn(const __grid_consta
         fence_async();
         tc_fence_before();
         __syncwarp();
-        if (lane == 0) mbar_arrive(smem_u32(&M.p_full));
+        if (lane == 0) mbar_arrive(smem_u32(&M.p_full[sb]));
       }
       // ---- the run's share of this (row, head, query tile) is in O
       if (broken) break;
-      ok = wait(&M.p_empty, (it - 1) & 1, fail) && ok;
+      ok = wait(&M.p_empty[(it - 1) % S::SB], (it - 1) / S::SB & 1, fail) && ok;
       if (group_any(bar, !ok)) break;
       tc_fence_after();
 #pragma unroll
