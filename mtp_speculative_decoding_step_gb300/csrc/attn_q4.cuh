@@ -17,8 +17,9 @@
 // tasks, whatever the rows' lengths are; a (row, head, query tile) that its run
 // does not hold whole leaves a partial (O, running maximum, sum) that a second
 // kernel joins. 16 warps:
-//   warp 0        copies the tile's 4-bit rows (cp.async.bulk) into two rings
-//   warp 1        issues the MMAs; S of tile i+1 goes before P.V of tile i
+//   warps 0, 3    copy the tile's 4-bit K and V rows (cp.async.bulk) into a ring each
+//   warp 1        issues the MMAs; S runs one or two tiles ahead of P.V
+//   warp 2        hands out the block's shares
 //   dequantisers  thread = position: codes x scale as f16, exact (at most six
 //                 significant bits). K goes to tensor memory (the thread's row
 //                 is the operand's lane), V to 128B-swizzled shared memory
@@ -254,6 +255,8 @@ __device__ __forceinline__ bool group_any(int id, bool p) {
 
 // ------------------------------------------------------------ shape
 
+constexpr int least(int a, int b) { return a < b ? a : b; }
+
 template <int DH, int N, bool WIDE>
 struct Shape {
   static constexpr int kRow = q4_row_bytes(DH);
@@ -268,15 +271,19 @@ struct Shape {
   static constexpr uint32_t kCols = cEnd <= 128 ? 128 : (cEnd <= 256 ? 256 : 512);
   // shared memory
   static constexpr int kRaw = kT * kRow;                 // a tile's rows of K or V
+  static constexpr int VB = DH == 256 ? 1 : 2;           // V tiles in shared memory
   static constexpr int kV = kT * DH * 2, kQ = N * DH * 2, kP = N * kT * 2;  // (SB buffers of P)
   static constexpr int kMetaBytes = 8192;
-  static constexpr int kRoom = (227 * 1024 - kMetaBytes - kV - kQ - SB * kP) / kRaw;
-  static constexpr int KS = kRoom >= 16 ? 8 : (kRoom + 1) / 2;  // ring stages
-  static constexpr int VS = kRoom >= 16 ? 8 : kRoom / 2;
-  static constexpr int oV = 0, oQ = kV, oP = oQ + kQ, oRawK = oP + SB * kP, oRawV = oRawK + KS * kRaw;
+  static constexpr int kRoom = (227 * 1024 - kMetaBytes - VB * kV - kQ - SB * kP) / kRaw;
+  // ring stages; even counts for two dequantising groups, so that each group
+  // meets every phase of its stages' barriers
+  static constexpr int kMost = 8;
+  static constexpr int KS = least(kMost, SG == 2 ? (kRoom + 1) / 2 : (kRoom >= 8 ? kRoom / 4 * 2 : 2));
+  static constexpr int VS = least(kMost, SG == 2 ? kRoom / 2 : (kRoom - KS) / 2 * 2);  // V waits longer than K
+  static constexpr int oV = 0, oQ = VB * kV, oP = oQ + kQ, oRawK = oP + SB * kP, oRawV = oRawK + KS * kRaw;
   static constexpr int oMeta = (oRawV + VS * kRaw + 127) / 128 * 128;
   static constexpr int kSmem = oMeta + kMetaBytes;
-  static_assert(VS >= 1 && cEnd <= 512, "shape");
+  static_assert(VS >= 1 && KS <= kMost && VS <= kMost && KS + VS <= kRoom && cEnd <= 512 && (SG == 2 || (KS % 2 == 0 && VS % 2 == 0)), "shape");
 };
 
 constexpr int kRuns = 4;
@@ -286,7 +293,9 @@ template <int DH>
 struct Meta {
   uint64_t rawk_full[8], rawk_empty[8], rawv_full[8], rawv_empty[8];
   uint64_t k_full[2], k_empty[2], s_full[2], s_empty[2];
-  uint64_t v_full[2], v_empty[2], p_full[2], p_empty[2], q_full;
+  // (a waiter has to meet every phase of its barrier, since a parity tells only
+  // neighbouring ones apart: v_empty goes by the tile's parity, as the groups do)
+  uint64_t v_full[4], v_empty[4], p_full[2], p_empty[2], q_full;
   uint32_t valid_k[8], valid_v[8];   // bit p: piece p of the stage was copied
   uint32_t tmem;
   int fail;
@@ -355,10 +364,10 @@ __device__ __forceinline__ void pin(uint32_t& x) { asm volatile("" : "+r"(x)); }
 // Whether a query at `pos` sees a position of an edge tile whose V is NaN in
 // 16-dimension block b.
 template <int B>
-__device__ __noinline__ bool sees_nan(int t0, int cnt, int p0, int p1, const uint32_t (*bits)[B][4], int b, int pos,
+__device__ __noinline__ bool sees_nan(int first, int t0, int cnt, int p0, int p1, const uint32_t (*bits)[B][4], int b, int pos,
                                       int window) {
   Run s;
-  s.first = t0;
+  s.first = first;
   s.p0 = p0;
   s.p1 = p1;
   for (int tile = t0; tile < t0 + cnt; ++tile) {
@@ -390,16 +399,18 @@ __global__ void __launch_bounds__(kAttnThreads, 1) k_q4_attn(const __grid_consta
     for (int i = 0; i < 8; ++i) {
       mbar_init(smem_u32(&M.rawk_full[i]), 1);
       mbar_init(smem_u32(&M.rawv_full[i]), 1);
-      mbar_init(smem_u32(&M.rawk_empty[i]), 4 * kDq);
-      mbar_init(smem_u32(&M.rawv_empty[i]), 4 * kDq);
+      mbar_init(smem_u32(&M.rawk_empty[i]), 4);
+      mbar_init(smem_u32(&M.rawv_empty[i]), 4);
+    }
+    for (int i = 0; i < 4; ++i) {
+      mbar_init(smem_u32(&M.v_full[i]), 4);
+      mbar_init(smem_u32(&M.v_empty[i]), 1);
     }
     for (int i = 0; i < 2; ++i) {
-      mbar_init(smem_u32(&M.k_full[i]), 4 * kDq);
+      mbar_init(smem_u32(&M.k_full[i]), 4);
       mbar_init(smem_u32(&M.k_empty[i]), 1);
       mbar_init(smem_u32(&M.s_full[i]), 1);
       mbar_init(smem_u32(&M.s_empty[i]), kSoftWarps);
-      mbar_init(smem_u32(&M.v_full[i]), 4);
-      mbar_init(smem_u32(&M.v_empty[i]), 1);
       mbar_init(smem_u32(&M.p_full[i]), kSoftWarps);
       mbar_init(smem_u32(&M.p_empty[i]), 1);
     }
@@ -410,7 +421,7 @@ __global__ void __launch_bounds__(kAttnThreads, 1) k_q4_attn(const __grid_consta
     mbar_init(smem_u32(&M.drain), 1);
     for (int i = 0; i < kRuns; ++i) {
       mbar_init(smem_u32(&M.run_full[i]), 1);
-      mbar_init(smem_u32(&M.run_empty[i]), 14);  // copies, MMAs, 12 warps of the other roles
+      mbar_init(smem_u32(&M.run_empty[i]), 3 + 4 * kDq + kSoftWarps);  // copies (2), MMAs, the warps of the others
     }
     asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
   }
@@ -547,42 +558,55 @@ __global__ void __launch_bounds__(kAttnThreads, 1) k_q4_attn(const __grid_consta
         }
       }
     }
-  } else if (warp == 0) {
-    // ---------------------------------------------------------- copies
-    uint32_t it = 0;
+  } else if (warp == 0 || warp == 3) {
+    // ---------------------------------------------------------- copies: K, V
+    const bool is_v = warp == 3;
+    const int stages = is_v ? S::VS : S::KS;
+    uint64_t *full = is_v ? M.rawv_full : M.rawk_full, *empty = is_v ? M.rawv_empty : M.rawk_empty;
+    uint32_t *valid = is_v ? M.valid_v : M.valid_k, *copied = &M.copied[is_v];
+    const uint8_t* cache = is_v ? a.vc : a.kc;
+    const uint32_t ring = smem_u32(smem_raw) + (is_v ? S::oRawV : S::oRawK), bytes = ps * S::kRow;
+    uint32_t it = 0, st = 0, round = 0;
     bool ok = true;
     Run s;
     s.flags = 0;
 #pragma unroll 1
     for (uint32_t k = 0; ok && !(s.flags & 4); ++k) {
-      ok = __all_sync(0xFFFFFFFFu, next(k, s));
+      ok = next(k, s);
       if (!ok) break;
+      // lane 8 q + p holds the place of piece p of tile 4 g + q, a group of four
+      // tiles ahead of the copies: the look-up would cost each tile an L2 trip
       const int32_t* tab = a.table + (long long)s.r * a.max_pages;
+      auto places = [&](int g) {
+        const int q = 4 * g + (lane >> 3), p0 = (lane & 7) * ps, t0 = (s.tile + q) * kT + p0;
+        if (p0 >= kT || q >= s.nt || t0 >= s.end || t0 + ps <= s.lo) return -1LL;
+        const int page = t0 / a.page, id = __ldg(tab + page);
+        if (id >= 0 && id < a.n_pages) return (((long long)id * a.n_kv + s.g) * a.page + (t0 - page * a.page)) * S::kRow;
+        flag_status(a.status, MTP_ERR_BAD_ARG);
+        return -1LL;
+      };
+      long long at = places(0), ahead = places(1);
 #pragma unroll 1
       for (int i = 0; i < s.nt && ok; ++i, ++it) {
-        const int t0 = (s.tile + i) * kT + lane * ps;  // lane p: piece p of the tile
-        const bool need = lane * ps < kT && t0 < s.end && t0 + ps > s.lo;
-        int id = need ? __ldg(tab + t0 / a.page) : 0;
-        const bool good = need && id >= 0 && id < a.n_pages;
-        if (need && !good) flag_status(a.status, MTP_ERR_BAD_ARG);
-        const uint32_t mask = __ballot_sync(0xFFFFFFFFu, good);
-        const long long src = good ? (((long long)id * a.n_kv + s.g) * a.page + t0 % a.page) * S::kRow : 0;
-        const uint32_t bytes = ps * S::kRow;
-#pragma unroll
-        for (int kv = 0; kv < 2; ++kv) {
-          const int st = it % (kv ? S::VS : S::KS), round = it / (kv ? S::VS : S::KS);
-          uint64_t* full = kv ? &M.rawv_full[st] : &M.rawk_full[st];
-          if (round > 0) ok = wait(kv ? &M.rawv_empty[st] : &M.rawk_empty[st], (round - 1) & 1, fail);
-          if (!ok) break;
-          if (lane == 0) {
-            (kv ? M.valid_v : M.valid_k)[st] = mask;
-            mbar_expect_tx(smem_u32(full), bytes * __popc(mask));
-            M.copied[kv] = it + 1;
-          }
-          __syncwarp();
-          if (good)
-            bulk_g2s(smem_u32(base + (kv ? S::oRawV : S::oRawK) + st * S::kRaw + lane * bytes), (kv ? a.vc : a.kc) + src,
-                     bytes, smem_u32(full));
+        if (i > 0 && (i & 3) == 0) {
+          at = ahead;
+          ahead = places((i >> 2) + 1);
+        }
+        long long src = __shfl_sync(0xFFFFFFFFu, at, (i & 3) * 8 + (lane & 7));
+        if (lane >= 8) src = -1;
+        const uint32_t mask = __ballot_sync(0xFFFFFFFFu, src >= 0);
+        if (round > 0) ok = wait(&empty[st], (round - 1) & 1, fail);
+        if (!ok) break;
+        if (lane == 0) {
+          valid[st] = mask;
+          mbar_expect_tx(smem_u32(&full[st]), bytes * __popc(mask));
+          *copied = it + 1;
+        }
+        __syncwarp();
+        if (src >= 0) bulk_g2s(ring + st * S::kRaw + lane * bytes, cache + src, bytes, smem_u32(&full[st]));
+        if (++st == stages) {
+          st = 0;
+          ++round;
         }
       }
       __syncwarp();
@@ -611,9 +635,10 @@ __global__ void __launch_bounds__(kAttnThreads, 1) k_q4_attn(const __grid_consta
       const uint64_t dpb = dp + (i % S::SB) * (S::kP / 16);
 #pragma unroll 1
       for (int h = 0; h < 2; ++h) {
-        if (!wait(&M.v_full[h], i & 1, fail)) return false;
+        const uint32_t vs = i % S::VB * 2 + h;
+        if (!wait(&M.v_full[vs], i / S::VB & 1, fail)) return false;
         tc_fence_after();
-        const uint64_t vh = dv + h * (S::kV / 32), ph = dpb + h * (N * 8);
+        const uint64_t vh = dv + vs * (S::kV / 32), ph = dpb + h * (N * 8);
 #pragma unroll
         for (int k = 0; k < 4; ++k) {
 #pragma unroll
@@ -621,7 +646,7 @@ __global__ void __launch_bounds__(kAttnThreads, 1) k_q4_attn(const __grid_consta
             mma_f16_ss(tm + S::cO + mb * N, vh + mb * 1024 + k * 128, ph + k * 2, idO, acc);
           acc = 1u;
         }
-        mma_commit_elect(smem_u32(&M.v_empty[h]));
+        mma_commit_elect(smem_u32(&M.v_empty[(i & 1) * 2 + h]));
       }
       mma_commit_elect(smem_u32(&M.p_empty[i % S::SB]));
       return true;
@@ -678,12 +703,12 @@ __global__ void __launch_bounds__(kAttnThreads, 1) k_q4_attn(const __grid_consta
     __syncwarp();
   } else if (warp >= 4 && warp < kSoftWarp) {
     // ---------------------------------------------------------- dequantisers
-    // Two groups (one beside 128-column softmax) share every tile: of K each
-    // takes its part of the head dimension, of V its 64 positions. Bound by the
-    // ALU pipe (a conversion per two elements goes there, so all else is kept
+    // Two groups (one beside 128-column softmax) take the tiles in turn. Bound by
+    // the ALU pipe (a conversion per two elements goes there, so all else is kept
     // off it: rows out of sight point at zeros, addresses are made once).
     const int quarter = warp & 3, tid = threadIdx.x & 127, group = (warp - 4) >> 2;
-    constexpr int kKC = DH / 32 / kDq;  // 32-element chunks of a thread's share of a K row
+    const int psh = 31 - __clz(ps);
+    constexpr int kKC = DH / 32;        // 32-element chunks of a K row
     constexpr int kD = DH / 2;          // elements of a thread's share of a V row
     const int tt = tid & 63, part = tid >> 6;
     uint32_t vdst[kD >= 64 ? 8 : 4];    // where its 8-element chunks go, in atoms of 64 dimensions
@@ -718,10 +743,10 @@ __global__ void __launch_bounds__(kAttnThreads, 1) k_q4_attn(const __grid_consta
       const uint32_t b = i % S::SB, round = i / S::SB;
       if (!wait(&M.rawk_full[st], (i / S::KS) & 1, fail)) return false;
       const int t = tile * kT + tid;
-      const bool live = t >= sg.lo && t < sg.end && (M.valid_k[st] >> (tid / ps) & 1);
+      const bool live = t >= sg.lo && t < sg.end && (M.valid_k[st] >> (tid >> psh) & 1);
       const uint8_t* row = live ? base + S::oRawK + st * S::kRaw + tid * S::kRow : M.zero;
       uint32_t code[4 * kKC], sc[(kKC + 1) / 2];
-      load_row(row + group * kKC * 16, row + DH / 2 + group * kKC * 2, code, sc);
+      load_row(row, row + DH / 2, code, sc);
       __syncwarp();
       if (lane == 0) mbar_arrive(smem_u32(&M.rawk_empty[st]));
       if (round > 0 && !wait(&M.k_empty[b], (round - 1) & 1, fail)) return false;
@@ -730,7 +755,7 @@ __global__ void __launch_bounds__(kAttnThreads, 1) k_q4_attn(const __grid_consta
       for (int c = 0; c < kKC; ++c) {
         uint32_t x[16];
         expand(code + 4 * c, sc[c / 2] >> (16 * (c & 1)), x);
-        tmem_st_rows16(tmem + S::cK + b * S::KC + (group * kKC + c) * 16 + ((uint32_t)(32 * quarter) << 16), x);
+        tmem_st_rows16(tmem + S::cK + b * S::KC + c * 16 + ((uint32_t)(32 * quarter) << 16), x);
       }
       tc_wait_st();
       tc_fence_before();
@@ -739,32 +764,31 @@ __global__ void __launch_bounds__(kAttnThreads, 1) k_q4_attn(const __grid_consta
       return true;
     };
     // tile `i`'s V in halves of 64 positions; a thread takes half a row
-    auto deq_v = [&](uint32_t i, const Run& sg, int tile, uint32_t run, bool first) {
+    auto deq_v = [&](uint32_t i, const Run& sg, int tile, uint32_t run) {
       const int st = i % S::VS;
       // 0 x NaN would reach rows that do not see the position: where a tile
       // has such rows, NaN is kept out of the product and noted for the end
       const bool edge = sg.edge(tile, a.window);
       if (!wait(&M.rawv_full[st], (i / S::VS) & 1, fail)) return false;
 #pragma unroll 1
-      for (int h = group; h < 2; h += kDq) {
+      for (int h = 0; h < 2; ++h) {
         const int tr = h * 64 + tt, t = tile * kT + tr;
-        const bool live = t >= sg.lo && t < sg.end && (M.valid_v[st] >> (tr / ps) & 1);
+        const bool live = t >= sg.lo && t < sg.end && (M.valid_v[st] >> (tr >> psh) & 1);
         const uint8_t* row = live ? base + S::oRawV + st * S::kRaw + tr * S::kRow : M.zero;
         uint32_t code[kD / 8], sc[(kD / 32 + 1) / 2];
         load_row(row + part * (kD / 2), row + DH / 2 + part * (kD / 16), code, sc);
-        if (h + kDq >= 2) {
+        if (h == 1) {
           __syncwarp();
           if (lane == 0) mbar_arrive(smem_u32(&M.rawv_empty[st]));
         }
-        if (i > 0 && !wait(&M.v_empty[h], (i - 1) & 1, fail)) return false;
-        if (first) {
-          // this warp's words, two shares old: their reader is done with them,
-          // since the last share's products are
-          if (lane < 4 * (kD / 16))
-            M.nan_bits[run & 1][lane / (kD / 16)][part * (kD / 16) + lane % (kD / 16)][tr >> 5] = 0;
-          __syncwarp();
-        }
+        const uint32_t vs = i % S::VB * 2 + h;
+        if (i >= S::VB && !wait(&M.v_empty[(i - S::VB & 1) * 2 + h], (i - S::VB) / 2 & 1, fail)) return false;
         if (edge) {
+          // (the words hold an older share's notes, whose reader is done: the
+          // products of the share between are)
+          auto& notes = M.nan_bits[run & 1][sg.edge_index(tile)];
+          if (lane < kD / 16) notes[part * (kD / 16) + lane][tr >> 5] = 0;
+          __syncwarp();
 #pragma unroll
           for (int w = 0; w < (kD / 32 + 1) / 2; ++w) {
             uint32_t nan = __vcmpeq4(sc[w] & 0x7F7F7F7Fu, 0x7F7F7F7Fu);
@@ -772,12 +796,12 @@ __global__ void __launch_bounds__(kAttnThreads, 1) k_q4_attn(const __grid_consta
             while (nan) {
               const int q = (__ffs(nan) - 1) / 8;
               nan &= ~(0xFFu << (8 * q));
-              atomicOr(&M.nan_bits[run & 1][sg.edge_index(tile)][part * (kD / 16) + 4 * w + q][tr >> 5], 1u << (tr & 31));
+              atomicOr(&notes[part * (kD / 16) + 4 * w + q][tr >> 5], 1u << (tr & 31));
               M.nan_run[run & 1] = run + 1;
             }
           }
         }
-        const uint32_t to = h * (S::kV / 2);
+        const uint32_t to = vs * (S::kV / 2);
 #pragma unroll
         for (int c = 0; c < kD / 32; ++c) {
           uint32_t x[16];
@@ -790,32 +814,36 @@ __global__ void __launch_bounds__(kAttnThreads, 1) k_q4_attn(const __grid_consta
         }
         fence_async();
         __syncwarp();
-        if (lane == 0) mbar_arrive(smem_u32(&M.v_full[h]));
+        if (lane == 0) mbar_arrive(smem_u32(&M.v_full[vs]));
       }
       return true;
     };
     uint32_t it = 0;
     bool ok = true;
-    Run s, sv;         // V goes one tile behind K
+    Run s, sv;         // V goes one of the group's tiles behind K
     int tv = -1;
-    uint32_t rv = 0;
-    bool fv = false;
+    uint32_t rv = 0, iv = 0;
     s.flags = 0;
 #pragma unroll 1
     for (uint32_t k = 0; ok && !(s.flags & 4); ++k) {
-      ok = __all_sync(0xFFFFFFFFu, next(k, s));
+      ok = next(k, s);
       __syncwarp();
       if (!ok) break;
       if (lane == 0) done(k);
-      // (one more turn after the last tile, for its V)
 #pragma unroll 1
-      for (int i = 0; ok && (i < s.nt || (i == s.nt && (s.flags & 4) && it > 0)); ++i, ++it) {
-        if (i < s.nt) ok = deq_k(it, s, s.tile + i);
-        if (tv >= 0 && ok) ok = deq_v(it - 1, sv, tv, rv, fv);
-        if (i == 0) sv = s;
+      for (int i = 0; i <= s.nt && ok; ++i) {
+        const bool flush = i == s.nt;  // after the last tile, its V
+        if (flush ? !(s.flags & 4) : kDq == 2 && (it & 1) != group) {
+          it += !flush;
+          continue;
+        }
+        if (!flush) ok = deq_k(it, s, s.tile + i);
+        if (tv >= 0 && ok) ok = deq_v(iv, sv, tv, rv);
+        sv = s;
         tv = s.tile + i;
         rv = k;
-        fv = i == 0;
+        iv = it;
+        it += !flush;
       }
     }
   } else if (warp >= kSoftWarp) {
@@ -1151,7 +1179,7 @@ __global__ void __launch_bounds__(kAttnThreads, 1) k_q4_attn(const __grid_consta
               uint32_t nan = 0;
 #pragma unroll 1
               for (int e = 0; e < 8; ++e)
-                nan |= (uint32_t)sees_nan<DH / 16>(s.first, s.tile + nt - s.first, s.p0, s.p1, M.nan_bits[run & 1], d / 16,
+                nan |= (uint32_t)sees_nan<DH / 16>(s.first, s.tile, nt, s.p0, s.p1, M.nan_bits[run & 1], d / 16,
                                                    M.lim[c0 + c + e], a.window) << e;
 #pragma unroll
               for (int e = 0; e < 8; ++e)
