@@ -1,9 +1,21 @@
 // Log probabilities of given tokens, ranks, entropy and alternatives
-// (spec_logprobs).
+// (spec_logprobs), in one read of the logits.
 //
-// One block per row: the maximum, then the sums
-//   S = sum e^(x-m),  T = sum (x-m) e^(x-m),  rank = #{j before t},
-// then the alternatives one by one.
+// With m = max x:  S = sum e^(x-m),  T = sum (x-m) e^(x-m),
+//   log p_t = x_t - m - log S,   H = log S - T / S,
+//   rank = #{j : (x_j, j) before (x_t, t)},  and the first k of that order.
+//
+// k_lp_part: a row is cut into parts, one block each. A thread keeps its own
+// running (m, S, T); when m grows by d, S and T become f S and f (T - d S) with
+// f = e^-d. Alternatives: at least k elements reach the k-th largest of the
+// maxima that groups of threads saw, so only threads whose own maximum reaches
+// that bound look at their elements again (from L2) and collect what does: some
+// 25 elements for k = 20. A collection that overflows is cut to its k best as it
+// goes. Elements go by 64-bit keys (value descending, id ascending), so ties
+// need no care anywhere.
+// k_lp_join: a block per row adds up the parts and merges their k keys.
+//
+// HBM-bound for many rows: 9 instructions an element, one of them an exponential.
 #include <algorithm>
 
 #include "common.cuh"
@@ -13,8 +25,12 @@ namespace mtp {
 
 namespace {
 
-constexpr int kLpThreads = 512;
+constexpr int kLpThreads = 256;
+constexpr int kLpBlocksPerSM = 4;
 constexpr int kLpMaxTop = 64;
+constexpr int kLpCap = 1024;        // collected keys of a block
+constexpr int kLpKeys = 4096;       // keys of a row's parts together
+constexpr int kLpMaxParts = 128;
 
 struct LpArgs {
   const void* x;
@@ -22,79 +38,540 @@ struct LpArgs {
   const int32_t* tok;
   float *lp, *ent, *top_lp;
   int32_t *rank, *top_id, *status;
-  int n, V, top;
+  int n, V, top, parts;
+  float4* sums;                     // [n][parts] m, S, T, rank count (bits)
+  unsigned long long* keys;         // [n][parts][top], descending; 0 = none
 };
 
+// Order key: larger value first, then lower id; -0 counts as +0.
+__device__ __forceinline__ uint32_t value_key(float x) {
+  const uint32_t u = __float_as_uint(x + 0.0f);
+  return u & 0x80000000u ? ~u : u | 0x80000000u;
+}
+__device__ __forceinline__ unsigned long long lp_key(float x, int id) {
+  return (unsigned long long)value_key(x) << 32 | (0xFFFFFFFFu - (uint32_t)id);
+}
+__device__ __forceinline__ float key_value(unsigned long long k) {
+  const uint32_t u = (uint32_t)(k >> 32);
+  return __uint_as_float(u & 0x80000000u ? u & 0x7FFFFFFFu : ~u);
+}
+
+// max that keeps a NaN
+__device__ __forceinline__ float max_nan(float a, float b) {
+  float y;
+  asm("max.NaN.f32 %0, %1, %2;" : "=f"(y) : "f"(a), "f"(b));
+  return y;
+}
+__device__ __forceinline__ float exp2_fast(float x) {
+  float y;
+  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+  return y;
+}
+constexpr float kLog2e = 1.44269504f;
+constexpr float kFloor = -110.f;    // e^-110 is zero in fp32
+
+// (m, S, T) of two disjoint sets.
+struct LpSum {
+  float m, S, T;
+  __device__ void raise(float to) {  // to >= m
+    if (m == -INFINITY) {
+      m = to;
+      return;
+    }
+    const float d = to - m, f = exp2_fast(-d * kLog2e);
+    T = f == 0.f ? 0.f : f * (T - d * S);
+    S *= f;
+    m = to;
+  }
+  __device__ void add(LpSum o) {
+    if (o.m == -INFINITY && o.S == o.S) return;
+    if (o.m > m) raise(o.m);
+    else o.raise(m);
+    S += o.S;
+    T += o.T;
+  }
+};
+
+// Two fp32 values side by side (one instruction for both).
+__device__ __forceinline__ uint64_t pair(float a, float b) {
+  uint64_t d;
+  asm("mov.b64 %0, {%1, %2};" : "=l"(d) : "f"(a), "f"(b));
+  return d;
+}
+__device__ __forceinline__ void unpair(uint64_t d, float& a, float& b) {
+  asm("mov.b64 {%0, %1}, %2;" : "=f"(a), "=f"(b) : "l"(d));
+}
+__device__ __forceinline__ uint64_t add2(uint64_t a, uint64_t b) {
+  uint64_t d;
+  asm("add.rn.f32x2 %0, %1, %2;" : "=l"(d) : "l"(a), "l"(b));
+  return d;
+}
+__device__ __forceinline__ uint64_t mul2(uint64_t a, uint64_t b) {
+  uint64_t d;
+  asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(d) : "l"(a), "l"(b));
+  return d;
+}
+__device__ __forceinline__ uint64_t fma2(uint64_t a, uint64_t b, uint64_t c) {
+  uint64_t d;
+  asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(d) : "l"(a), "l"(b), "l"(c));
+  return d;
+}
+// Moves paired sums into (m, S, T).
+__device__ __forceinline__ void fold(LpSum& s, uint64_t& S2, uint64_t& T2) {
+  float a, b;
+  unpair(S2, a, b);
+  s.S += a + b;
+  unpair(T2, a, b);
+  s.T += a + b;
+  S2 = T2 = 0;
+}
+
+struct LpShared {
+  alignas(16) unsigned long long group[128];
+  unsigned long long key[kLpCap], live[kLpCap], bound, kth;
+  int n, n_live;
+  float red[4][kLpThreads / 32];
+};
+
+// The k-th largest (k = top) of the block's group maxima of the threads' keys,
+// into sh.kth: groups of 4 threads up to 24 alternatives, else of 2. (Whole
+// keys, not values: where thousands of logits are equal, as a mask's are, the
+// ids keep the bound sharp.)
+__device__ __forceinline__ void kth_bound(LpShared& sh, unsigned long long v, int top) {
+  const int tid = threadIdx.x, g = top <= 24 ? 4 : 2, ng = kLpThreads / g;
+  v = max(v, __shfl_xor_sync(0xFFFFFFFFu, v, 1));
+  if (g == 4) v = max(v, __shfl_xor_sync(0xFFFFFFFFu, v, 2));
+  if (tid % g == 0) sh.group[tid / g] = v;
+  __syncthreads();
+  // a group's rank, counted by its g threads a slice each
+  const int me = tid / g, share = ng / g, from = tid % g * share;
+  const unsigned long long mine = sh.group[me];
+  int before = 0;
+#pragma unroll 4
+  for (int i = from; i < from + share; i += 2) {
+    const ulonglong2 o = *reinterpret_cast<const ulonglong2*>(&sh.group[i]);
+    before += (o.x > mine || (o.x == mine && i < me)) + (o.y > mine || (o.y == mine && i + 1 < me));
+  }
+  before += __shfl_xor_sync(0xFFFFFFFFu, before, 1);
+  if (g == 4) before += __shfl_xor_sync(0xFFFFFFFFu, before, 2);
+  if (before == top - 1) sh.kth = mine;
+  __syncthreads();
+}
+
+// Cuts sh.key[0, n) to its `top` best in descending order, sh.n of them; where
+// there were that many, the last one is the new bound.
+__device__ __noinline__ void cut(LpShared& sh, int top) {
+  const int tid = threadIdx.x;
+  __syncthreads();
+  const int n = min(sh.n, kLpCap);
+  unsigned long long bound = 0;
+  if (n > 64) {
+    unsigned long long v = 0;
+    for (int i = tid; i < n; i += kLpThreads) v = max(v, sh.key[i]);
+    kth_bound(sh, v, top);
+    bound = sh.kth;
+  }
+  if (tid == 0) sh.n_live = 0;
+  __syncthreads();
+  for (int i = tid; i < n; i += kLpThreads) {
+    const unsigned long long k = sh.key[i];
+    if (k >= bound) sh.live[atomicAdd(&sh.n_live, 1)] = k;
+  }
+  __syncthreads();
+  const int live = sh.n_live;
+  for (int i = tid; i < live; i += kLpThreads) {
+    const unsigned long long k = sh.live[i];
+    int before = 0;
+#pragma unroll 4
+    for (int j = 0; j < live; ++j) before += sh.live[j] > k;
+    if (before < top) sh.key[before] = k;
+    if (before == top - 1) sh.bound = k;
+  }
+  if (tid == 0) sh.n = min(live, top);
+  __syncthreads();
+}
+
 template <int DT>
-__global__ void __launch_bounds__(kLpThreads) k_logprobs(const __grid_constant__ LpArgs a) {
-  __shared__ float s_v[32];
-  __shared__ int s_i[32];
-  __shared__ float red[32];
+__global__ void __launch_bounds__(kLpThreads, kLpBlocksPerSM) k_lp_part(const __grid_constant__ LpArgs a) {
+  constexpr int W = DT == MTP_DTYPE_BF16 ? 8 : 4;  // elements of a 16-byte load
+  constexpr int kLpVec = 16 / W;  // 16-byte loads of a thread and batch: 16 elements
+  __shared__ LpShared sh;
+  const int tid = threadIdx.x, part = blockIdx.x, r = blockIdx.y;
+  const uint8_t* row = static_cast<const uint8_t*>(a.x) + (long long)r * a.stride * (16 / W);
+  // whole vectors from the row's first 16-byte boundary on, and the elements
+  // before and after them
+  const int head = min((int)((16 - (reinterpret_cast<uintptr_t>(row) & 15)) & 15) / (16 / W), a.V);
+  const int n_vec = (a.V - head) / W, tail = (a.V - head) % W;
+  const int v0 = (int)((long long)n_vec * part / a.parts), v1 = (int)((long long)n_vec * (part + 1) / a.parts);
+  const uint8_t* body = row + head * (16 / W);
+  if (tid == 0) sh.n = 0;
   pdl_wait();
   pdl_trigger();
-  const int r = blockIdx.x, lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-  const long long base = r * a.stride;
-  // argmax of the elements after (v, id) in the order
-  auto next = [&](float lv, int li, float& bv, int& bi) {
-    bv = -INFINITY;
-    bi = -1;
-    for (int j = threadIdx.x; j < a.V; j += kLpThreads) {
-      const float x = load_elem(a.x, DT, base + j);
-      if (li >= 0 && !better(lv, li, x, j)) continue;
-      if (bi < 0 ? x > -INFINITY : better(x, j, bv, bi)) { bv = x; bi = j; }
+  uint4 w[kLpVec], nw[kLpVec];
+  auto load = [&](int v, uint4 (&to)[kLpVec]) {
+#pragma unroll
+    for (int q = 0; q < kLpVec; ++q) {
+      const int i = v + q * kLpThreads + tid;
+      if (i < v1) to[q] = __ldg(reinterpret_cast<const uint4*>(body) + i);
     }
-    if (bi < 0) bi = 0x7FFFFFFF;
-    warp_argmax(bv, bi);
-    __syncthreads();
-    if (lane == 0) { s_v[warp] = bv; s_i[warp] = bi; }
-    __syncthreads();
-    bv = lane < kLpThreads / 32 ? s_v[lane] : -INFINITY;
-    bi = lane < kLpThreads / 32 ? s_i[lane] : 0x7FFFFFFF;
-    warp_argmax(bv, bi);
-    if (bi == 0x7FFFFFFF) bi = -1;
   };
-  float m;
-  int mi;
-  next(0.f, -1, m, mi);
+  load(v0, w);
   const int t = a.tok[r];
   const bool given = t >= 0 && t < a.V;
-  if (!given && t != -1 && threadIdx.x == 0) flag_status(a.status, MTP_ERR_BAD_ARG);
-  const float xt = given ? load_elem(a.x, DT, base + t) : 0.f;
-  float S = 0.f, T = 0.f, cnt = 0.f;
-  bool bad = false;
-  for (int j = threadIdx.x; j < a.V; j += kLpThreads) {
-    const float x = load_elem(a.x, DT, base + j);
-    bad |= !(x < INFINITY);
-    const float e = mi < 0 ? 0.f : expf(x - m);
-    S += e;
-    if (e > 0.f) T += (x - m) * e;
-    cnt += better(x, j, xt, t) ? 1.f : 0.f;
-  }
-  S = block_sum(S, red);
-  T = block_sum(T, red);
-  cnt = block_sum(cnt, red);
-  if (bad) flag_status(a.status, MTP_ERR_NONFINITE);
-  const float ls = logf(S);
-  if (threadIdx.x == 0) {
-    a.lp[r] = given ? (mi < 0 ? -INFINITY : xt - m - ls) : 0.f;
-    if (a.rank) a.rank[r] = given ? (int)cnt : -1;
-    if (a.ent) a.ent[r] = mi < 0 ? 0.f : ls - T / S;
-  }
-  float v = m;
-  int id = mi;
-  for (int k = 0; k < a.top; ++k) {
-    if (threadIdx.x == 0) {
-      a.top_id[(long long)r * a.top + k] = id;
-      a.top_lp[(long long)r * a.top + k] = id < 0 ? -INFINITY : v - m - ls;
-    }
-    if (id >= 0 && k + 1 < a.top) {
-      float nv;
-      int ni;
-      next(v, id, nv, ni);
-      v = nv;
-      id = ni;
+  const float xt = given ? load_elem(row, DT, t) : INFINITY;
+  const uint32_t xt_bits = __float_as_uint(xt);
+  const float below = xt == 0.f ? -__uint_as_float(1) : __uint_as_float(xt_bits & 0x80000000u ? xt_bits + 1 : xt_bits - 1);
+  __syncthreads();
+
+  LpSum s{-INFINITY, 0.f, 0.f};
+  int before = 0;
+  // thread t's share of the elements outside the vectors: one at most
+  unsigned long long lone = 0, best = 0;  // its key; a key that some element of the thread reaches
+  {
+    int id = -1;
+    if (part == 0 && tid < head) id = tid;
+    if (part == a.parts - 1 && tid >= 8 && tid - 8 < tail) id = head + n_vec * W + tid - 8;
+    if (id >= 0) {
+      const float x = load_elem(row, DT, id);
+      if (!(x == -INFINITY)) {
+        s.m = x;
+        s.S = x < INFINITY ? 1.f : x - x;  // (a NaN or +inf makes the sum NaN)
+        lone = best = lp_key(x, id);
+      }
+      before += x > xt || (x == xt && id < t);
     }
   }
+
+  float seen = -INFINITY;  // the largest of the vectors, and the first one that had it
+  int seen_at = v0;
+  uint64_t S2 = 0, T2 = 0;  // even and odd elements' sums
+#pragma unroll 2
+  for (int v = v0; v < v1; v += kLpVec * kLpThreads) {
+    const bool whole = v + kLpVec * kLpThreads <= v1;
+    if (v + kLpVec * kLpThreads < v1) load(v + kLpVec * kLpThreads, nw);
+    if (!whole) {
+#pragma unroll
+      for (int q = 0; q < kLpVec; ++q)
+        if (v + q * kLpThreads + tid >= v1) {  // -inf past the part's end
+          const uint32_t none = W == 8 ? 0xFF80FF80u : 0xFF800000u;
+          w[q] = make_uint4(none, none, none, none);
+        }
+    }
+    // element e of load q
+    auto elem = [&](int q, int e) {
+      const uint32_t u[4] = {w[q].x, w[q].y, w[q].z, w[q].w};
+      return W == 8 ? ((e & 1) ? bf16hi(u[e / 2]) : bf16lo(u[e / 2])) : __uint_as_float(u[W == 8 ? 0 : e]);
+    };
+    float most[kLpVec], top = -INFINITY;
+#pragma unroll
+    for (int q = 0; q < kLpVec; ++q) {
+      most[q] = elem(q, 0);
+#pragma unroll
+      for (int e = 1; e < W; ++e) most[q] = fmaxf(most[q], elem(q, e));
+      top = fmaxf(top, most[q]);
+    }
+    if (top > seen) {
+      seen = top;
+#pragma unroll
+      for (int q = kLpVec - 1; q >= 0; --q)
+        if (most[q] == top) seen_at = v + q * kLpThreads + tid;
+      if (top > s.m) {
+        fold(s, S2, T2);
+        s.raise(top);
+      }
+    }
+    // before t an equal logit comes first too: x >= xt is x > the float below
+    // xt (below -inf: a NaN, which nothing is at most)
+    const int id0 = head + v * W, id1 = id0 + kLpVec * kLpThreads * W;
+    const bool mixed = id0 <= t && t < id1;
+    const float m = s.m == -INFINITY ? 0.f : s.m, over = mixed ? INFINITY : (id1 <= t ? below : xt);
+    const uint64_t minus_m = pair(-m, -m), l2e = pair(kLog2e, kLog2e);
+    int count = 0;
+#pragma unroll
+    for (int q = 0; q < kLpVec; ++q)
+#pragma unroll
+      for (int e = 0; e < W; e += 2) {
+        const float x0 = elem(q, e), x1 = elem(q, e + 1);
+        float d0, d1, p0, p1;
+        unpair(add2(pair(x0, x1), minus_m), d0, d1);
+        const uint64_t d = pair(max_nan(d0, kFloor), max_nan(d1, kFloor));
+        unpair(mul2(d, l2e), p0, p1);
+        const uint64_t p = pair(exp2_fast(p0), exp2_fast(p1));
+        S2 = add2(S2, p);
+        T2 = fma2(d, p, T2);
+        count += !(x0 <= over);
+        count += !(x1 <= over);
+      }
+    // (what was filled in past the part's end is -inf: over a NaN, not counted)
+    if (!whole && over != over) {
+      count = 0;
+#pragma unroll
+      for (int q = 0; q < kLpVec; ++q) count += v + q * kLpThreads + tid < v1 ? W : 0;
+    }
+    before += count;
+    if (mixed) {
+#pragma unroll
+      for (int q = 0; q < kLpVec; ++q)
+#pragma unroll
+        for (int e = 0; e < W; ++e) {
+          const int i = v + q * kLpThreads + tid, id = head + i * W + e;
+          const float x = elem(q, e);
+          before += i < v1 && (x > xt || (x == xt && id < t));
+        }
+    }
+#pragma unroll
+    for (int q = 0; q < kLpVec; ++q) w[q] = nw[q];
+  }
+  fold(s, S2, T2);
+
+  // the block's sums
+  const int lane = tid & 31, warp = tid >> 5;
+#pragma unroll
+  for (int o = 16; o > 0; o >>= 1) {
+    LpSum x;
+    x.m = __shfl_xor_sync(0xFFFFFFFFu, s.m, o);
+    x.S = __shfl_xor_sync(0xFFFFFFFFu, s.S, o);
+    x.T = __shfl_xor_sync(0xFFFFFFFFu, s.T, o);
+    s.add(x);
+    before += __shfl_xor_sync(0xFFFFFFFFu, before, o);
+  }
+  if (lane == 0) {
+    sh.red[0][warp] = s.m;
+    sh.red[1][warp] = s.S;
+    sh.red[2][warp] = s.T;
+    sh.red[3][warp] = __int_as_float(before);
+  }
+  __syncthreads();
+  const long long at = (long long)r * a.parts + part;
+  if (tid == 0) {
+    for (int i = 1; i < kLpThreads / 32; ++i) {
+      s.add(LpSum{sh.red[0][i], sh.red[1][i], sh.red[2][i]});
+      before += __float_as_int(sh.red[3][i]);
+    }
+    a.sums[at] = make_float4(s.m, s.S, s.T, __int_as_float(before));
+  }
+  if (a.top == 0) return;
+
+  // the alternatives (`each` hands the thread's elements of batch v on)
+  auto each = [&](int v, auto&& f) {
+#pragma unroll
+    for (int q = 0; q < kLpVec; ++q) {
+      const int i = v + q * kLpThreads + tid;
+      if (i >= v1) continue;
+      const uint4 u4 = __ldg(reinterpret_cast<const uint4*>(body) + i);
+      const uint32_t u[4] = {u4.x, u4.y, u4.z, u4.w};
+#pragma unroll
+      for (int e = 0; e < W; ++e)
+        f(W == 8 ? ((e & 1) ? bf16hi(u[e / 2]) : bf16lo(u[e / 2])) : __uint_as_float(u[W == 8 ? 0 : e]), head + i * W + e);
+    }
+  };
+  // (the last id of the vector that has it: a key not above the element's own)
+  if (seen > -INFINITY) best = max(best, lp_key(seen, head + seen_at * W + W - 1));
+  kth_bound(sh, best, a.top);
+  unsigned long long bound = sh.kth;  // 0 where fewer groups than alternatives saw anything
+  float least = bound ? key_value(bound) : -INFINITY;
+  auto push = [&](unsigned long long k) {
+    const int at = atomicAdd(&sh.n, 1);
+    if (at < kLpCap) sh.key[at] = k;
+    return at < kLpCap;
+  };
+  if (lone >= bound && lone) push(lone);
+  // threads that may hold some: their elements, by the whole warp (a lane per
+  // vector), four threads' loads in flight
+  unsigned who = __ballot_sync(0xFFFFFFFFu, best >= bound && seen >= least && seen > -INFINITY);
+#pragma unroll 1
+  while (who) {
+    int from[4];
+#pragma unroll
+    for (int c = 0; c < 4; ++c) {
+      from[c] = who ? v0 + (tid & ~31) + __ffs(who) - 1 : v1;
+      who &= who - 1;
+    }
+#pragma unroll 1
+    for (int step = (tid & 31) * kLpThreads; v0 + step < v1; step += 32 * kLpThreads) {
+      uint4 u4[4];
+#pragma unroll
+      for (int c = 0; c < 4; ++c)
+        if (from[c] + step < v1) u4[c] = __ldg(reinterpret_cast<const uint4*>(body) + from[c] + step);
+#pragma unroll
+      for (int c = 0; c < 4; ++c) {
+        if (from[c] + step >= v1) continue;
+        const uint32_t u[4] = {u4[c].x, u4[c].y, u4[c].z, u4[c].w};
+#pragma unroll
+        for (int e = 0; e < W; ++e) {
+          const float x = W == 8 ? ((e & 1) ? bf16hi(u[e / 2]) : bf16lo(u[e / 2])) : __uint_as_float(u[W == 8 ? 0 : e]);
+          if (x >= least && x > -INFINITY) {
+            const unsigned long long k = lp_key(x, head + (from[c] + step) * W + e);
+            if (k >= bound) push(k);
+          }
+        }
+      }
+    }
+  }
+  __syncthreads();
+  if (sh.n > kLpCap) {
+    // too many (a few threads hold the top of the row): again, batch by batch
+    // with a cut and a sharper bound whenever the collection is full
+    __syncthreads();
+    if (tid == 0) sh.n = 0;
+    __syncthreads();
+    if (lone >= bound && lone) push(lone);
+#pragma unroll 1
+    for (int v = v0; v < v1; v += kLpVec * kLpThreads) {
+      uint32_t bits = 0xFFFF;  // the thread's elements that are still to be looked at
+      int e = 0;
+      while (__syncthreads_or(bits != 0)) {
+        e = 0;
+        uint32_t left = 0;
+        each(v, [&](float x, int id) {
+          const unsigned long long k = lp_key(x, id);
+          if ((bits >> e & 1) && x > -INFINITY && k >= bound && !push(k)) left |= 1u << e;
+          ++e;
+        });
+        bits = left;
+        if (__syncthreads_or(left != 0)) {
+          cut(sh, a.top);
+          bound = sh.bound + 1;
+        }
+      }
+    }
+  }
+  cut(sh, a.top);
+  for (int i = tid; i < a.top; i += kLpThreads) a.keys[at * a.top + i] = i < sh.n ? sh.key[i] : 0ull;
+}
+
+__global__ void __launch_bounds__(kLpThreads) k_lp_join(const __grid_constant__ LpArgs a, int dt) {
+  __shared__ unsigned long long s_key[kLpKeys];
+  __shared__ unsigned long long s_bound, s_live[kLpThreads];
+  __shared__ int s_n;
+  __shared__ float s_red[4][kLpThreads / 32];
+  pdl_wait();
+  pdl_trigger();
+  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, r = blockIdx.x, P = a.parts, top = a.top;
+  for (int i = tid; i < P * top; i += kLpThreads) s_key[i] = a.keys[(long long)r * P * top + i];
+  LpSum s{-INFINITY, 0.f, 0.f};
+  int before = 0;
+  for (int p = tid; p < P; p += kLpThreads) {
+    const float4 f = a.sums[(long long)r * P + p];
+    s.add(LpSum{f.x, f.y, f.z});
+    before += __float_as_int(f.w);
+  }
+#pragma unroll
+  for (int o = 16; o > 0; o >>= 1) {
+    LpSum x;
+    x.m = __shfl_xor_sync(0xFFFFFFFFu, s.m, o);
+    x.S = __shfl_xor_sync(0xFFFFFFFFu, s.S, o);
+    x.T = __shfl_xor_sync(0xFFFFFFFFu, s.T, o);
+    s.add(x);
+    before += __shfl_xor_sync(0xFFFFFFFFu, before, o);
+  }
+  if (lane == 0) {
+    s_red[0][warp] = s.m;
+    s_red[1][warp] = s.S;
+    s_red[2][warp] = s.T;
+    s_red[3][warp] = __int_as_float(before);
+  }
+  if (tid == 0) {
+    s_bound = 1ull;
+    s_n = 0;
+  }
+  __syncthreads();
+  s = LpSum{-INFINITY, 0.f, 0.f};
+  before = 0;
+  for (int i = 0; i < kLpThreads / 32; ++i) {
+    s.add(LpSum{s_red[0][i], s_red[1][i], s_red[2][i]});
+    before += __float_as_int(s_red[3][i]);
+  }
+  const bool none = s.m == -INFINITY && s.S == s.S;  // every logit is -inf
+  const float ls = none ? 0.f : logf(s.S);
+  if (tid == 0) {
+    if (!(s.S == s.S)) flag_status(a.status, MTP_ERR_NONFINITE);
+    const int t = a.tok[r];
+    const bool given = t >= 0 && t < a.V;
+    if (!given && t != -1) flag_status(a.status, MTP_ERR_BAD_ARG);
+    const float xt = given ? load_elem(a.x, dt, (long long)r * a.stride + t) : 0.f;
+    a.lp[r] = given ? (none ? -INFINITY : (xt - s.m) - ls) : 0.f;
+    if (a.rank) a.rank[r] = given ? before : -1;
+    if (a.ent) a.ent[r] = none ? 0.f : ls - s.T / s.S;
+  }
+  if (top == 0) return;
+  // with as many parts as alternatives, the top-th largest of the parts'
+  // first keys bounds what can be among them
+  if (P >= top && tid < P) {
+    const unsigned long long mine = s_key[tid * top];
+    int rank = 0;
+#pragma unroll 4
+    for (int p = 0; p < P; ++p) {
+      const unsigned long long o = s_key[p * top];
+      rank += o > mine || (o == mine && p < tid);
+    }
+    if (rank == top - 1 && mine > 0) s_bound = mine;
+  }
+  __syncthreads();
+  for (int i = tid; i < top; i += kLpThreads) {  // (overwritten below where there are that many)
+    a.top_id[(long long)r * top + i] = -1;
+    a.top_lp[(long long)r * top + i] = -INFINITY;
+  }
+  __syncthreads();
+  const unsigned long long bound = s_bound;
+  auto put = [&](unsigned long long k, int rank) {
+    a.top_id[(long long)r * top + rank] = (int32_t)(0xFFFFFFFFu - (uint32_t)k);
+    a.top_lp[(long long)r * top + rank] = (key_value(k) - s.m) - ls;
+  };
+  if (P >= top) {
+    // few keys are left: ranked by counting
+    for (int i = tid; i < P * top; i += kLpThreads)
+      if (s_key[i] >= bound) {
+        const int at = atomicAdd(&s_n, 1);
+        if (at < kLpThreads) s_live[at] = s_key[i];
+      }
+    __syncthreads();
+    if (s_n <= kLpThreads) {
+      if (tid < s_n) {
+        const unsigned long long k = s_live[tid];
+        int rank = 0;
+#pragma unroll 4
+        for (int i = 0; i < s_n; ++i) rank += s_live[i] > k;
+        if (rank < top) put(k, rank);
+      }
+      return;
+    }
+  }
+  for (int i = tid; i < P * top; i += kLpThreads) {
+    const unsigned long long k = s_key[i];
+    if (k < bound) continue;
+    int rank = i % top;
+    for (int p = 0; p < P && rank < top; ++p) {  // keys above k in part p's descending list
+      if (p == i / top) continue;
+      const unsigned long long* list = s_key + p * top;
+      int lo = 0, hi = top;
+      while (lo < hi) {
+        const int mid = (lo + hi) >> 1;
+        if (list[mid] > k) lo = mid + 1;
+        else hi = mid;
+      }
+      rank += lo;
+    }
+    if (rank < top) put(k, rank);
+  }
+}
+
+// Parts per row: the count with the least (waves of resident blocks) x (a
+// part's elements + a block's fixed cost, counted in elements), the join's cost
+// per part added. Many rows: whole waves; few rows: short parts.
+int lp_parts(int n, int V, int top) {
+  const long long slots = (long long)kLpBlocksPerSM * device_sm_count();
+  const int most = std::min({kLpMaxParts, std::max(1, V / 2048), top > 0 ? kLpKeys / top : kLpMaxParts});
+  int best = 1;
+  double least = 0;
+  for (int p = 1; p <= most; ++p) {
+    const double cost = (double)(((long long)n * p + slots - 1) / slots) * ((double)V / p + 8000.0) + 30.0 * p;
+    if (p == 1 || cost < least) {
+      least = cost;
+      best = p;
+    }
+  }
+  return best;
 }
 
 }  // namespace
@@ -106,13 +583,14 @@ extern "C" {
 
 size_t spec_logprobs_workspace_bytes(int32_t n, int32_t vocab, int32_t top) {
   if (n < 1 || vocab < 1 || top < 0 || top > kLpMaxTop) return 0;
-  return 256;
+  const size_t parts = (size_t)n * lp_parts(n, vocab, top);
+  return parts * (sizeof(float4) + sizeof(unsigned long long) * top);
 }
 
 mtp_status spec_logprobs(mtp_stream stream, int32_t n, int32_t vocab, const void* d_logits, int64_t row_stride,
                          int32_t dtype, const int32_t* d_tok, int32_t top, float* d_logprob, int32_t* d_rank,
                          float* d_entropy, int32_t* d_top_id, float* d_top_lp, int32_t* d_status, void* d_workspace) {
-  if (n < 0 || vocab < 1 || vocab > (1 << 20) || top < 0 || top > kLpMaxTop ||
+  if (n < 0 || n > 65535 || vocab < 1 || vocab > (1 << 20) || top < 0 || top > kLpMaxTop ||
       (dtype != MTP_DTYPE_BF16 && dtype != MTP_DTYPE_F32))
     return MTP_ERR_BAD_ARG;
   if (n == 0) return MTP_OK;
@@ -121,11 +599,14 @@ mtp_status spec_logprobs(mtp_stream stream, int32_t n, int32_t vocab, const void
       (n > 1 && row_stride < vocab) || (reinterpret_cast<uintptr_t>(d_logits) & (es - 1)) != 0 ||
       (reinterpret_cast<uintptr_t>(d_workspace) & 15) != 0)
     return MTP_ERR_BAD_ARG;
-  LpArgs a{d_logits, row_stride, d_tok, d_logprob, d_entropy, d_top_lp, d_rank, d_top_id, d_status, n, vocab, top};
+  LpArgs a{d_logits, row_stride, d_tok, d_logprob, d_entropy, d_top_lp, d_rank, d_top_id, d_status, n, vocab, top,
+           lp_parts(n, vocab, top), static_cast<float4*>(d_workspace), nullptr};
+  a.keys = reinterpret_cast<unsigned long long*>(a.sums + (size_t)n * a.parts);
   cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
-  const cudaError_t e = launch_pdl(dtype == MTP_DTYPE_BF16 ? k_logprobs<MTP_DTYPE_BF16> : k_logprobs<MTP_DTYPE_F32>,
-                                   dim3(n), dim3(kLpThreads), 0, s, a);
-  count_launch();
+  cudaError_t e = launch_pdl(dtype == MTP_DTYPE_BF16 ? k_lp_part<MTP_DTYPE_BF16> : k_lp_part<MTP_DTYPE_F32>,
+                             dim3(a.parts, n), dim3(kLpThreads), 0, s, a);
+  if (e == cudaSuccess) e = launch_pdl(k_lp_join, dim3(n), dim3(kLpThreads), 0, s, a, dtype);
+  count_launch(2);
   return e == cudaSuccess ? MTP_OK : MTP_ERR_CUDA;
 }
 
