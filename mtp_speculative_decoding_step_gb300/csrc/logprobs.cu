@@ -25,12 +25,15 @@ namespace mtp {
 
 namespace {
 
-constexpr int kLpThreads = 256;
+constexpr int kLpThreads = 256;     // (and a warp more that copies)
 constexpr int kLpBlocksPerSM = 4;
 constexpr int kLpMaxTop = 64;
 constexpr int kLpCap = 1024;        // collected keys of a block
-constexpr int kLpKeys = 4096;       // keys of a row's parts together
+constexpr int kLpList = 128;        // keys that a part hands on
 constexpr int kLpMaxParts = 128;
+constexpr int kLpStages = 4;
+constexpr int kLpStage = 8192;      // bytes: two 16-byte vectors a thread
+constexpr unsigned kLpWaitLimit = 1u << 20;
 
 struct LpArgs {
   const void* x;
@@ -40,7 +43,8 @@ struct LpArgs {
   int32_t *rank, *top_id, *status;
   int n, V, top, parts;
   float4* sums;                     // [n][parts] m, S, T, rank count (bits)
-  unsigned long long* keys;         // [n][parts][top], descending; 0 = none
+  uint4* heads;                     // [n][parts] a bound (key), keys handed on
+  unsigned long long* keys;         // [n][parts][kLpList], in no order
 };
 
 // Order key: larger value first, then lower id; -0 counts as +0.
@@ -127,11 +131,29 @@ __device__ __forceinline__ void fold(LpSum& s, uint64_t& S2, uint64_t& T2) {
 }
 
 struct LpShared {
+  union {
+    alignas(128) uint8_t ring[kLpStages][kLpStage];
+    unsigned long long key[2][kLpCap];  // collected keys, and those left of them (once the ring is done)
+  };
   alignas(16) unsigned long long group[128];
-  unsigned long long key[kLpCap], live[kLpCap], bound, kth;
-  int n, n_live;
+  unsigned long long bound, kth;
+  uint64_t full[kLpStages], empty[kLpStages];
+  int n, n_live, fail;
   float red[4][kLpThreads / 32];
 };
+
+// Barrier of the 256 threads that compute.
+__device__ __forceinline__ void lp_sync() { asm volatile("barrier.cta.sync.aligned 1, 256;" ::: "memory"); }
+__device__ __forceinline__ bool lp_any(bool p) {
+  uint32_t any;
+  asm volatile(
+      "{\n\t.reg .pred p, q;\n\tsetp.ne.b32 p, %1, 0;\n\t"
+      "barrier.cta.red.or.aligned.pred q, 1, 256, p;\n\tselp.u32 %0, 1, 0, q;\n\t}"
+      : "=r"(any)
+      : "r"((uint32_t)p)
+      : "memory");
+  return any != 0;
+}
 
 // The k-th largest (k = top) of the block's group maxima of the threads' keys,
 // into sh.kth: groups of 4 threads up to 24 alternatives, else of 2. (Whole
@@ -142,7 +164,7 @@ __device__ __forceinline__ void kth_bound(LpShared& sh, unsigned long long v, in
   v = max(v, __shfl_xor_sync(0xFFFFFFFFu, v, 1));
   if (g == 4) v = max(v, __shfl_xor_sync(0xFFFFFFFFu, v, 2));
   if (tid % g == 0) sh.group[tid / g] = v;
-  __syncthreads();
+  lp_sync();
   // a group's rank, counted by its g threads a slice each
   const int me = tid / g, share = ng / g, from = tid % g * share;
   const unsigned long long mine = sh.group[me];
@@ -155,46 +177,47 @@ __device__ __forceinline__ void kth_bound(LpShared& sh, unsigned long long v, in
   before += __shfl_xor_sync(0xFFFFFFFFu, before, 1);
   if (g == 4) before += __shfl_xor_sync(0xFFFFFFFFu, before, 2);
   if (before == top - 1) sh.kth = mine;
-  __syncthreads();
+  lp_sync();
 }
 
-// Cuts sh.key[0, n) to its `top` best in descending order, sh.n of them; where
+// Cuts sh.key[0][0, n) to its `top` best in descending order, sh.n of them; where
 // there were that many, the last one is the new bound.
 __device__ __noinline__ void cut(LpShared& sh, int top) {
   const int tid = threadIdx.x;
-  __syncthreads();
+  lp_sync();
   const int n = min(sh.n, kLpCap);
   unsigned long long bound = 0;
   if (n > 64) {
     unsigned long long v = 0;
-    for (int i = tid; i < n; i += kLpThreads) v = max(v, sh.key[i]);
+    for (int i = tid; i < n; i += kLpThreads) v = max(v, sh.key[0][i]);
     kth_bound(sh, v, top);
     bound = sh.kth;
   }
   if (tid == 0) sh.n_live = 0;
-  __syncthreads();
+  lp_sync();
   for (int i = tid; i < n; i += kLpThreads) {
-    const unsigned long long k = sh.key[i];
-    if (k >= bound) sh.live[atomicAdd(&sh.n_live, 1)] = k;
+    const unsigned long long k = sh.key[0][i];
+    if (k >= bound) sh.key[1][atomicAdd(&sh.n_live, 1)] = k;
   }
-  __syncthreads();
+  lp_sync();
   const int live = sh.n_live;
   for (int i = tid; i < live; i += kLpThreads) {
-    const unsigned long long k = sh.live[i];
+    const unsigned long long k = sh.key[1][i];
     int before = 0;
 #pragma unroll 4
-    for (int j = 0; j < live; ++j) before += sh.live[j] > k;
-    if (before < top) sh.key[before] = k;
+    for (int j = 0; j < live; ++j) before += sh.key[1][j] > k;
+    if (before < top) sh.key[0][before] = k;
     if (before == top - 1) sh.bound = k;
   }
   if (tid == 0) sh.n = min(live, top);
-  __syncthreads();
+  lp_sync();
 }
 
 template <int DT>
-__global__ void __launch_bounds__(kLpThreads, kLpBlocksPerSM) k_lp_part(const __grid_constant__ LpArgs a) {
-  constexpr int W = DT == MTP_DTYPE_BF16 ? 8 : 4;  // elements of a 16-byte load
-  constexpr int kLpVec = 16 / W;  // 16-byte loads of a thread and batch: 16 elements
+__global__ void __launch_bounds__(kLpThreads + 32, kLpBlocksPerSM) k_lp_part(const __grid_constant__ LpArgs a) {
+  constexpr int W = DT == MTP_DTYPE_BF16 ? 8 : 4;   // elements of a 16-byte vector
+  constexpr int Q = kLpStage / 16 / kLpThreads;     // vectors of a thread and stage
+  constexpr int kVecs = kLpStage / 16;              // vectors of a stage
   __shared__ LpShared sh;
   const int tid = threadIdx.x, part = blockIdx.x, r = blockIdx.y;
   const uint8_t* row = static_cast<const uint8_t*>(a.x) + (long long)r * a.stride * (16 / W);
@@ -204,24 +227,55 @@ __global__ void __launch_bounds__(kLpThreads, kLpBlocksPerSM) k_lp_part(const __
   const int n_vec = (a.V - head) / W, tail = (a.V - head) % W;
   const int v0 = (int)((long long)n_vec * part / a.parts), v1 = (int)((long long)n_vec * (part + 1) / a.parts);
   const uint8_t* body = row + head * (16 / W);
-  if (tid == 0) sh.n = 0;
+  if (tid == 0) {
+    sh.n = sh.fail = 0;
+    for (int i = 0; i < kLpStages; ++i) {
+      mbar_init(smem_u32(&sh.full[i]), 1);
+      mbar_init(smem_u32(&sh.empty[i]), kLpThreads / 32);
+    }
+    asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
+  }
+  __syncthreads();
   pdl_wait();
   pdl_trigger();
-  uint4 w[kLpVec], nw[kLpVec];
-  auto load = [&](int v, uint4 (&to)[kLpVec]) {
+  if (tid >= kLpThreads) {
+    // the copying warp: the part in stages of contiguous bytes
+    int st = 0, round = 0, last[kLpStages];
 #pragma unroll
-    for (int q = 0; q < kLpVec; ++q) {
-      const int i = v + q * kLpThreads + tid;
-      if (i < v1) to[q] = __ldg(reinterpret_cast<const uint4*>(body) + i);
+    for (int i = 0; i < kLpStages; ++i) last[i] = -1;
+#pragma unroll 1
+    for (int v = v0; v < v1; v += kVecs) {
+      if (round > 0 && !mbar_wait(smem_u32(&sh.empty[st]), (round - 1) & 1, kLpWaitLimit)) {
+        sh.fail = 1;
+        break;
+      }
+      if (tid == kLpThreads) {
+        const uint32_t bytes = min(kVecs, v1 - v) * 16;
+        mbar_expect_tx(smem_u32(&sh.full[st]), bytes);
+        bulk_g2s(smem_u32(sh.ring[st]), body + 16LL * v, bytes, smem_u32(&sh.full[st]));
+      }
+      __syncwarp();
+#pragma unroll
+      for (int i = 0; i < kLpStages; ++i)
+        if (i == st) last[i] = round;
+      if (++st == kLpStages) {
+        st = 0;
+        ++round;
+      }
     }
-  };
-  load(v0, w);
+    if (sh.fail)  // copies in flight land before the block's shared memory goes
+#pragma unroll
+      for (int i = 0; i < kLpStages; ++i)
+        if (last[i] >= 0) mbar_wait(smem_u32(&sh.full[i]), last[i] & 1, kLpWaitLimit);
+    return;
+  }
   const int t = a.tok[r];
   const bool given = t >= 0 && t < a.V;
   const float xt = given ? load_elem(row, DT, t) : INFINITY;
   const uint32_t xt_bits = __float_as_uint(xt);
+  // before t an equal logit comes first too: x >= xt is x > the float below xt
+  // (below -inf: a NaN, which nothing is at most)
   const float below = xt == 0.f ? -__uint_as_float(1) : __uint_as_float(xt_bits & 0x80000000u ? xt_bits + 1 : xt_bits - 1);
-  __syncthreads();
 
   LpSum s{-INFINITY, 0.f, 0.f};
   int before = 0;
@@ -245,26 +299,37 @@ __global__ void __launch_bounds__(kLpThreads, kLpBlocksPerSM) k_lp_part(const __
   float seen = -INFINITY;  // the largest of the vectors, and the first one that had it
   int seen_at = v0;
   uint64_t S2 = 0, T2 = 0;  // even and odd elements' sums
-#pragma unroll 2
-  for (int v = v0; v < v1; v += kLpVec * kLpThreads) {
-    const bool whole = v + kLpVec * kLpThreads <= v1;
-    if (v + kLpVec * kLpThreads < v1) load(v + kLpVec * kLpThreads, nw);
+  int st = 0, phase = 0;
+  bool ok = true;
+#pragma unroll 1
+  for (int v = v0; v < v1; v += kVecs) {
+    const bool whole = v + kVecs <= v1;
+    ok = mbar_wait(smem_u32(&sh.full[st]), phase, kLpWaitLimit) && ok;
+    uint4 w[Q];
+#pragma unroll
+    for (int q = 0; q < Q; ++q) w[q] = reinterpret_cast<const uint4*>(sh.ring[st])[q * kLpThreads + tid];
+    __syncwarp();
+    if ((tid & 31) == 0) mbar_arrive(smem_u32(&sh.empty[st]));
+    if (++st == kLpStages) {
+      st = 0;
+      phase ^= 1;
+    }
     if (!whole) {
 #pragma unroll
-      for (int q = 0; q < kLpVec; ++q)
+      for (int q = 0; q < Q; ++q)
         if (v + q * kLpThreads + tid >= v1) {  // -inf past the part's end
           const uint32_t none = W == 8 ? 0xFF80FF80u : 0xFF800000u;
           w[q] = make_uint4(none, none, none, none);
         }
     }
-    // element e of load q
+    // element e of vector q
     auto elem = [&](int q, int e) {
       const uint32_t u[4] = {w[q].x, w[q].y, w[q].z, w[q].w};
       return W == 8 ? ((e & 1) ? bf16hi(u[e / 2]) : bf16lo(u[e / 2])) : __uint_as_float(u[W == 8 ? 0 : e]);
     };
-    float most[kLpVec], top = -INFINITY;
+    float most[Q], top = -INFINITY;
 #pragma unroll
-    for (int q = 0; q < kLpVec; ++q) {
+    for (int q = 0; q < Q; ++q) {
       most[q] = elem(q, 0);
 #pragma unroll
       for (int e = 1; e < W; ++e) most[q] = fmaxf(most[q], elem(q, e));
@@ -273,22 +338,20 @@ __global__ void __launch_bounds__(kLpThreads, kLpBlocksPerSM) k_lp_part(const __
     if (top > seen) {
       seen = top;
 #pragma unroll
-      for (int q = kLpVec - 1; q >= 0; --q)
+      for (int q = Q - 1; q >= 0; --q)
         if (most[q] == top) seen_at = v + q * kLpThreads + tid;
       if (top > s.m) {
         fold(s, S2, T2);
         s.raise(top);
       }
     }
-    // before t an equal logit comes first too: x >= xt is x > the float below
-    // xt (below -inf: a NaN, which nothing is at most)
-    const int id0 = head + v * W, id1 = id0 + kLpVec * kLpThreads * W;
+    const int id0 = head + v * W, id1 = id0 + kVecs * W;
     const bool mixed = id0 <= t && t < id1;
     const float m = s.m == -INFINITY ? 0.f : s.m, over = mixed ? INFINITY : (id1 <= t ? below : xt);
     const uint64_t minus_m = pair(-m, -m), l2e = pair(kLog2e, kLog2e);
     int count = 0;
 #pragma unroll
-    for (int q = 0; q < kLpVec; ++q)
+    for (int q = 0; q < Q; ++q)
 #pragma unroll
       for (int e = 0; e < W; e += 2) {
         const float x0 = elem(q, e), x1 = elem(q, e + 1);
@@ -306,12 +369,12 @@ __global__ void __launch_bounds__(kLpThreads, kLpBlocksPerSM) k_lp_part(const __
     if (!whole && over != over) {
       count = 0;
 #pragma unroll
-      for (int q = 0; q < kLpVec; ++q) count += v + q * kLpThreads + tid < v1 ? W : 0;
+      for (int q = 0; q < Q; ++q) count += v + q * kLpThreads + tid < v1 ? W : 0;
     }
     before += count;
     if (mixed) {
 #pragma unroll
-      for (int q = 0; q < kLpVec; ++q)
+      for (int q = 0; q < Q; ++q)
 #pragma unroll
         for (int e = 0; e < W; ++e) {
           const int i = v + q * kLpThreads + tid, id = head + i * W + e;
@@ -319,10 +382,12 @@ __global__ void __launch_bounds__(kLpThreads, kLpBlocksPerSM) k_lp_part(const __
           before += i < v1 && (x > xt || (x == xt && id < t));
         }
     }
-#pragma unroll
-    for (int q = 0; q < kLpVec; ++q) w[q] = nw[q];
   }
   fold(s, S2, T2);
+  if (!ok) {
+    flag_status(a.status, MTP_ERR_TIMEOUT);
+    sh.fail = 1;
+  }
 
   // the block's sums
   const int lane = tid & 31, warp = tid >> 5;
@@ -341,21 +406,28 @@ __global__ void __launch_bounds__(kLpThreads, kLpBlocksPerSM) k_lp_part(const __
     sh.red[2][warp] = s.T;
     sh.red[3][warp] = __int_as_float(before);
   }
-  __syncthreads();
+  lp_sync();
   const long long at = (long long)r * a.parts + part;
-  if (tid == 0) {
-    for (int i = 1; i < kLpThreads / 32; ++i) {
-      s.add(LpSum{sh.red[0][i], sh.red[1][i], sh.red[2][i]});
-      before += __float_as_int(sh.red[3][i]);
+  if (warp == 0) {
+    s = lane < kLpThreads / 32 ? LpSum{sh.red[0][lane], sh.red[1][lane], sh.red[2][lane]} : LpSum{-INFINITY, 0.f, 0.f};
+    before = lane < kLpThreads / 32 ? __float_as_int(sh.red[3][lane]) : 0;
+#pragma unroll
+    for (int o = kLpThreads / 64; o > 0; o >>= 1) {
+      LpSum x;
+      x.m = __shfl_xor_sync(0xFFFFFFFFu, s.m, o);
+      x.S = __shfl_xor_sync(0xFFFFFFFFu, s.S, o);
+      x.T = __shfl_xor_sync(0xFFFFFFFFu, s.T, o);
+      s.add(x);
+      before += __shfl_xor_sync(0xFFFFFFFFu, before, o);
     }
-    a.sums[at] = make_float4(s.m, s.S, s.T, __int_as_float(before));
+    if (lane == 0) a.sums[at] = make_float4(s.m, s.S, s.T, __int_as_float(before));
   }
   if (a.top == 0) return;
 
   // the alternatives (`each` hands the thread's elements of batch v on)
   auto each = [&](int v, auto&& f) {
 #pragma unroll
-    for (int q = 0; q < kLpVec; ++q) {
+    for (int q = 0; q < Q; ++q) {
       const int i = v + q * kLpThreads + tid;
       if (i >= v1) continue;
       const uint4 u4 = __ldg(reinterpret_cast<const uint4*>(body) + i);
@@ -369,10 +441,11 @@ __global__ void __launch_bounds__(kLpThreads, kLpBlocksPerSM) k_lp_part(const __
   if (seen > -INFINITY) best = max(best, lp_key(seen, head + seen_at * W + W - 1));
   kth_bound(sh, best, a.top);
   unsigned long long bound = sh.kth;  // 0 where fewer groups than alternatives saw anything
-  float least = bound ? key_value(bound) : -INFINITY;
+  unsigned long long known = bound;     // at least `top` of the part's keys reach it (if it is not 0)
+  const float least = bound ? key_value(bound) : -INFINITY;
   auto push = [&](unsigned long long k) {
     const int at = atomicAdd(&sh.n, 1);
-    if (at < kLpCap) sh.key[at] = k;
+    if (at < kLpCap) sh.key[0][at] = k;
     return at < kLpCap;
   };
   if (lone >= bound && lone) push(lone);
@@ -408,19 +481,19 @@ __global__ void __launch_bounds__(kLpThreads, kLpBlocksPerSM) k_lp_part(const __
       }
     }
   }
-  __syncthreads();
+  lp_sync();
   if (sh.n > kLpCap) {
     // too many (a few threads hold the top of the row): again, batch by batch
     // with a cut and a sharper bound whenever the collection is full
-    __syncthreads();
+    lp_sync();
     if (tid == 0) sh.n = 0;
-    __syncthreads();
+    lp_sync();
     if (lone >= bound && lone) push(lone);
 #pragma unroll 1
-    for (int v = v0; v < v1; v += kLpVec * kLpThreads) {
+    for (int v = v0; v < v1; v += kVecs) {
       uint32_t bits = 0xFFFF;  // the thread's elements that are still to be looked at
       int e = 0;
-      while (__syncthreads_or(bits != 0)) {
+      while (lp_any(bits != 0)) {
         e = 0;
         uint32_t left = 0;
         each(v, [&](float x, int id) {
@@ -429,33 +502,55 @@ __global__ void __launch_bounds__(kLpThreads, kLpBlocksPerSM) k_lp_part(const __
           ++e;
         });
         bits = left;
-        if (__syncthreads_or(left != 0)) {
+        if (lp_any(left != 0)) {
           cut(sh, a.top);
-          bound = sh.bound + 1;
+          known = sh.bound;
+          bound = known + 1;
         }
       }
     }
   }
-  cut(sh, a.top);
-  for (int i = tid; i < a.top; i += kLpThreads) a.keys[at * a.top + i] = i < sh.n ? sh.key[i] : 0ull;
+  // the part's bound and what reaches it: the row's join takes the sharpest of
+  // the parts' bounds, so the list needs no order
+  if (sh.n > kLpList || (!known && sh.n >= a.top)) {
+    cut(sh, a.top);
+    if (sh.n == a.top) known = sh.bound;
+  }
+  const int n = sh.n;
+  if (tid < n) a.keys[at * kLpList + tid] = sh.key[0][tid];
+  if (tid == 0) a.heads[at] = make_uint4((uint32_t)known, (uint32_t)(known >> 32), (uint32_t)n, 0u);
 }
 
-__global__ void __launch_bounds__(kLpThreads) k_lp_join(const __grid_constant__ LpArgs a, int dt) {
-  __shared__ unsigned long long s_key[kLpKeys];
-  __shared__ unsigned long long s_bound, s_live[kLpThreads];
+constexpr int kLpJoinThreads = 128;
+constexpr int kLpLive = 1024;
+
+__global__ void __launch_bounds__(kLpJoinThreads) k_lp_join(const __grid_constant__ LpArgs a, int dt) {
+  __shared__ unsigned long long s_live[kLpLive], s_bound;
   __shared__ int s_n;
-  __shared__ float s_red[4][kLpThreads / 32];
+  __shared__ float s_red[4][kLpJoinThreads / 32];
+  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, r = blockIdx.x, P = a.parts, top = a.top;
+  if (tid == 0) {
+    s_bound = 1ull;
+    s_n = 0;
+  }
   pdl_wait();
   pdl_trigger();
-  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, r = blockIdx.x, P = a.parts, top = a.top;
-  for (int i = tid; i < P * top; i += kLpThreads) s_key[i] = a.keys[(long long)r * P * top + i];
+  __syncthreads();
   LpSum s{-INFINITY, 0.f, 0.f};
   int before = 0;
-  for (int p = tid; p < P; p += kLpThreads) {
+  unsigned long long bound = 0;
+  for (int p = tid; p < P; p += kLpJoinThreads) {
     const float4 f = a.sums[(long long)r * P + p];
+    if (top > 0) {
+      const uint4 h = a.heads[(long long)r * P + p];
+      bound = max(bound, (unsigned long long)h.y << 32 | h.x);
+    }
     s.add(LpSum{f.x, f.y, f.z});
     before += __float_as_int(f.w);
   }
+  const int t = a.tok[r];
+  const bool given = t >= 0 && t < a.V;
+  const float xt = given && tid == 0 ? load_elem(a.x, dt, (long long)r * a.stride + t) : 0.f;
 #pragma unroll
   for (int o = 16; o > 0; o >>= 1) {
     LpSum x;
@@ -464,21 +559,20 @@ __global__ void __launch_bounds__(kLpThreads) k_lp_join(const __grid_constant__ 
     x.T = __shfl_xor_sync(0xFFFFFFFFu, s.T, o);
     s.add(x);
     before += __shfl_xor_sync(0xFFFFFFFFu, before, o);
+    bound = max(bound, __shfl_xor_sync(0xFFFFFFFFu, bound, o));
   }
   if (lane == 0) {
     s_red[0][warp] = s.m;
     s_red[1][warp] = s.S;
     s_red[2][warp] = s.T;
     s_red[3][warp] = __int_as_float(before);
-  }
-  if (tid == 0) {
-    s_bound = 1ull;
-    s_n = 0;
+    if (bound > 1) atomicMax(&s_bound, bound);
   }
   __syncthreads();
   s = LpSum{-INFINITY, 0.f, 0.f};
   before = 0;
-  for (int i = 0; i < kLpThreads / 32; ++i) {
+#pragma unroll
+  for (int i = 0; i < kLpJoinThreads / 32; ++i) {
     s.add(LpSum{s_red[0][i], s_red[1][i], s_red[2][i]});
     before += __float_as_int(s_red[3][i]);
   }
@@ -486,82 +580,83 @@ __global__ void __launch_bounds__(kLpThreads) k_lp_join(const __grid_constant__ 
   const float ls = none ? 0.f : logf(s.S);
   if (tid == 0) {
     if (!(s.S == s.S)) flag_status(a.status, MTP_ERR_NONFINITE);
-    const int t = a.tok[r];
-    const bool given = t >= 0 && t < a.V;
     if (!given && t != -1) flag_status(a.status, MTP_ERR_BAD_ARG);
-    const float xt = given ? load_elem(a.x, dt, (long long)r * a.stride + t) : 0.f;
     a.lp[r] = given ? (none ? -INFINITY : (xt - s.m) - ls) : 0.f;
     if (a.rank) a.rank[r] = given ? before : -1;
     if (a.ent) a.ent[r] = none ? 0.f : ls - s.T / s.S;
   }
   if (top == 0) return;
-  // with as many parts as alternatives, the top-th largest of the parts'
-  // first keys bounds what can be among them
-  if (P >= top && tid < P) {
-    const unsigned long long mine = s_key[tid * top];
-    int rank = 0;
-#pragma unroll 4
-    for (int p = 0; p < P; ++p) {
-      const unsigned long long o = s_key[p * top];
-      rank += o > mine || (o == mine && p < tid);
-    }
-    if (rank == top - 1 && mine > 0) s_bound = mine;
-  }
-  __syncthreads();
-  for (int i = tid; i < top; i += kLpThreads) {  // (overwritten below where there are that many)
-    a.top_id[(long long)r * top + i] = -1;
-    a.top_lp[(long long)r * top + i] = -INFINITY;
-  }
-  __syncthreads();
-  const unsigned long long bound = s_bound;
+  // what reaches the sharpest bound, ranked by counting
   auto put = [&](unsigned long long k, int rank) {
     a.top_id[(long long)r * top + rank] = (int32_t)(0xFFFFFFFFu - (uint32_t)k);
     a.top_lp[(long long)r * top + rank] = (key_value(k) - s.m) - ls;
   };
-  if (P >= top) {
-    // few keys are left: ranked by counting
-    for (int i = tid; i < P * top; i += kLpThreads)
-      if (s_key[i] >= bound) {
-        const int at = atomicAdd(&s_n, 1);
-        if (at < kLpThreads) s_live[at] = s_key[i];
+  auto keys = [&](auto&& f) {
+    for (int p = warp; p < P; p += kLpJoinThreads / 32) {
+      const int n = min((int)a.heads[(long long)r * P + p].z, kLpList);
+      for (int i = lane; i < n; i += 32) f(a.keys[((long long)r * P + p) * kLpList + i]);
+    }
+  };
+  auto collect = [&]() {
+    keys([&](unsigned long long k) {
+      if (k >= bound) {
+        const int i = atomicAdd(&s_n, 1);
+        if (i < kLpLive) s_live[i] = k;
       }
+    });
     __syncthreads();
-    if (s_n <= kLpThreads) {
-      if (tid < s_n) {
-        const unsigned long long k = s_live[tid];
-        int rank = 0;
+  };
+  bound = s_bound;
+  collect();
+  if (s_n > kLpJoinThreads) {
+    // many are left, where parts have fewer tokens than alternatives: the
+    // top-th largest of the threads' own maxima is a bound again
+    unsigned long long mine = 0;
+    keys([&](unsigned long long k) { mine = max(mine, k); });
+    __syncthreads();
+    s_live[tid] = mine;
+    if (tid == 0) s_n = 0;
+    __syncthreads();
+    int rank = 0;
 #pragma unroll 4
-        for (int i = 0; i < s_n; ++i) rank += s_live[i] > k;
-        if (rank < top) put(k, rank);
-      }
-      return;
-    }
+    for (int i = 0; i < kLpJoinThreads; ++i) rank += s_live[i] > mine || (s_live[i] == mine && i < tid);
+    if (rank == top - 1 && mine > bound) s_bound = mine;
+    __syncthreads();
+    bound = s_bound;
+    collect();
   }
-  for (int i = tid; i < P * top; i += kLpThreads) {
-    const unsigned long long k = s_key[i];
-    if (k < bound) continue;
-    int rank = i % top;
-    for (int p = 0; p < P && rank < top; ++p) {  // keys above k in part p's descending list
-      if (p == i / top) continue;
-      const unsigned long long* list = s_key + p * top;
-      int lo = 0, hi = top;
-      while (lo < hi) {
-        const int mid = (lo + hi) >> 1;
-        if (list[mid] > k) lo = mid + 1;
-        else hi = mid;
-      }
-      rank += lo;
+  const int n = s_n;
+  if (n <= kLpLive) {
+    for (int i = tid; i < n; i += kLpJoinThreads) {
+      const unsigned long long k = s_live[i];
+      int rank = 0;
+#pragma unroll 4
+      for (int j = 0; j < n; ++j) rank += s_live[j] > k;
+      if (rank < top) put(k, rank);
     }
-    if (rank < top) put(k, rank);
+  } else {
+    // (long lists of many parts without a bound: each key against all)
+    keys([&](unsigned long long k) {
+      int rank = 0;
+      for (int p = 0; p < P; ++p) {
+        const int m = min((int)a.heads[(long long)r * P + p].z, kLpList);
+        for (int i = 0; i < m; ++i) rank += a.keys[((long long)r * P + p) * kLpList + i] > k;
+      }
+      if (rank < top) put(k, rank);
+    });
+  }
+  for (int i = min(n, top) + tid; i < top; i += kLpJoinThreads) {  // past the last token that is possible
+    a.top_id[(long long)r * top + i] = -1;
+    a.top_lp[(long long)r * top + i] = -INFINITY;
   }
 }
 
 // Parts per row: the count with the least (waves of resident blocks) x (a
 // part's elements + a block's fixed cost, counted in elements), the join's cost
 // per part added. Many rows: whole waves; few rows: short parts.
-int lp_parts(int n, int V, int top) {
+int lp_parts(int n, int V) {
   const long long slots = (long long)kLpBlocksPerSM * device_sm_count();
-  const int most = std::min({kLpMaxParts, std::max(1, V / 2048), top > 0 ? kLpKeys / top : kLpMaxParts});
+  const int most = std::min(kLpMaxParts, std::max(1, V / 2048));
   int best = 1;
   double least = 0;
   for (int p = 1; p <= most; ++p) {
@@ -583,8 +678,8 @@ extern "C" {
 
 size_t spec_logprobs_workspace_bytes(int32_t n, int32_t vocab, int32_t top) {
   if (n < 1 || vocab < 1 || top < 0 || top > kLpMaxTop) return 0;
-  const size_t parts = (size_t)n * lp_parts(n, vocab, top);
-  return parts * (sizeof(float4) + sizeof(unsigned long long) * top);
+  const size_t parts = (size_t)n * lp_parts(n, vocab);
+  return parts * (sizeof(float4) + (top > 0 ? sizeof(uint4) + sizeof(unsigned long long) * kLpList : 0));
 }
 
 mtp_status spec_logprobs(mtp_stream stream, int32_t n, int32_t vocab, const void* d_logits, int64_t row_stride,
@@ -600,12 +695,13 @@ mtp_status spec_logprobs(mtp_stream stream, int32_t n, int32_t vocab, const void
       (reinterpret_cast<uintptr_t>(d_workspace) & 15) != 0)
     return MTP_ERR_BAD_ARG;
   LpArgs a{d_logits, row_stride, d_tok, d_logprob, d_entropy, d_top_lp, d_rank, d_top_id, d_status, n, vocab, top,
-           lp_parts(n, vocab, top), static_cast<float4*>(d_workspace), nullptr};
-  a.keys = reinterpret_cast<unsigned long long*>(a.sums + (size_t)n * a.parts);
+           lp_parts(n, vocab), static_cast<float4*>(d_workspace), nullptr, nullptr};
+  a.heads = reinterpret_cast<uint4*>(a.sums + (size_t)n * a.parts);
+  a.keys = reinterpret_cast<unsigned long long*>(a.heads + (size_t)n * a.parts);
   cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
   cudaError_t e = launch_pdl(dtype == MTP_DTYPE_BF16 ? k_lp_part<MTP_DTYPE_BF16> : k_lp_part<MTP_DTYPE_F32>,
-                             dim3(a.parts, n), dim3(kLpThreads), 0, s, a);
-  if (e == cudaSuccess) e = launch_pdl(k_lp_join, dim3(n), dim3(kLpThreads), 0, s, a, dtype);
+                             dim3(a.parts, n), dim3(kLpThreads + 32), 0, s, a);
+  if (e == cudaSuccess) e = launch_pdl(k_lp_join, dim3(n), dim3(kLpJoinThreads), 0, s, a, dtype);
   count_launch(2);
   return e == cudaSuccess ? MTP_OK : MTP_ERR_CUDA;
 }

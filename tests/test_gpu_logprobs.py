@@ -82,6 +82,30 @@ def test_ties_masks_and_empty_rows(dtype):
     check(x, [17, 5, 4321, 4995, 4999, 50, 2500, 3, 4998], top)
 
 
+@pytest.mark.parametrize("keep,V,top", [(70, 152064, 64), (5000, 152064, 64), (5000, 152064, 7), (900, 40000, 20)])
+@pytest.mark.parametrize("dtype", [torch.float32, torch.bfloat16])
+def test_sparse_masks(keep, V, top, dtype):
+    """A grammar leaves a few tokens, strewn over the vocabulary: fewer in a part than there are alternatives."""
+    g = torch.Generator().manual_seed(keep + V)
+    x = torch.full((3, V), -math.inf, dtype=dtype)
+    for r in range(3):
+        at = torch.randperm(V, generator=g)[:keep]
+        x[r, at] = (torch.randn(keep, generator=g) * 3).to(dtype)
+    x[2] = torch.where(x[2] == -math.inf, x[2], 1.25)  # and all alike
+    check(x, [int((x[r] > -math.inf).nonzero()[keep // 2]) for r in range(3)], top)
+
+
+@pytest.mark.parametrize("top", [1, 20, 64])
+def test_the_top_of_the_row_in_few_threads(top):
+    """The largest logits at a stride of a thread's elements, and in one run of ids."""
+    V = 100000
+    x = logits(3, V, torch.float32, 31, scale=1.0)
+    x[0, ::1024] = 50 + torch.arange(0, 98).float() / 7
+    x[1, 40000:42500] = 60 - torch.arange(2500).float() / 100
+    x[2] = -torch.arange(V).float() / 1000
+    check(x, [1024, 41000, 99999], top)
+
+
 def test_tokens_at_masked_places():
     x = logits(3, 300, torch.float32, 1)
     x[0, 10] = -math.inf
