@@ -147,11 +147,21 @@ def _ptr(t):
     return t.data_ptr()
 
 
+_raw_stream = None
+
+
 def _stream(stream):
-    import torch
-    if stream is None:
-        stream = torch.cuda.current_stream()
-    return stream.cuda_stream if hasattr(stream, "cuda_stream") else int(stream)
+    """The cudaStream_t of a torch stream, an integer, or the current stream (None)."""
+    global _raw_stream
+    if stream is not None:
+        return stream.cuda_stream if hasattr(stream, "cuda_stream") else int(stream)
+    if _raw_stream is None:
+        import torch
+        # the current stream's handle without a Stream object around it (3 us on a Grace core), where torch has it
+        raw = getattr(torch._C, "_cuda_getCurrentRawStream", None)
+        device = torch.cuda.current_device
+        _raw_stream = (lambda: raw(device())) if raw else (lambda: torch.cuda.current_stream().cuda_stream)
+    return _raw_stream()
 
 
 _BF16 = None
@@ -334,11 +344,23 @@ def _want(ok: bool, where: str):
         raise MTPError(9, where)
 
 
+_torch = None
+
+
+def _t():
+    """torch, imported with the first call that needs it."""
+    global _torch
+    if _torch is None:
+        import torch
+        _torch = torch
+    return _torch
+
+
 def _whole(where: str, *tensors, n=None):
     """Contiguous int32 tensors (None passes), of n elements if n is given."""
+    i32 = _t().int32
     for t in tensors:
-        if t is not None and (t.element_size() != 4 or t.is_floating_point() or not t.is_contiguous()
-                              or (n is not None and t.numel() != n)):
+        if t is not None and (t.dtype is not i32 or not t.is_contiguous() or (n is not None and t.numel() != n)):
             raise MTPError(9, where)
 
 
@@ -380,10 +402,13 @@ def kv_page_plan(cover, keep, new, table, free, cover_out, start, slot, pos, pag
 
 def _dtype_q4(where: str, *tensors) -> int:
     """The dtype code of tensors of one type, fp32 or bf16."""
-    import torch
-    dt = tensors[0].dtype
-    _want(dt in (torch.bfloat16, torch.float32) and all(t.dtype == dt for t in tensors), where)
-    return MTP_DTYPE_BF16 if dt == torch.bfloat16 else MTP_DTYPE_F32
+    torch, dt = _t(), tensors[0].dtype
+    if dt is not torch.bfloat16 and dt is not torch.float32:
+        raise MTPError(9, where)
+    for t in tensors:
+        if t.dtype is not dt:
+            raise MTPError(9, where)
+    return MTP_DTYPE_BF16 if dt is torch.bfloat16 else MTP_DTYPE_F32
 
 
 def kv_q4_append(cache: PagedCache, k, v, slot, status=None, stream=None):
@@ -410,8 +435,7 @@ def kv_q4_read(cache: PagedCache, slot, k, v, status=None, stream=None):
 
 def kv_q4_attend_workspace_bytes(cache: PagedCache, n_q: int, max_q: int, dtype) -> int:
     """dtype: the queries' torch dtype."""
-    import torch
-    return lib().kv_q4_attend_workspace_bytes(cache.ref, n_q, max_q, MTP_DTYPE_BF16 if dtype == torch.bfloat16
+    return lib().kv_q4_attend_workspace_bytes(cache.ref, n_q, max_q, MTP_DTYPE_BF16 if dtype is _t().bfloat16
                                               else MTP_DTYPE_F32)
 
 
@@ -423,7 +447,7 @@ def kv_q4_attend(cache: PagedCache, q, table, start, length, out, workspace, max
     tokens, n_q, dh = q.shape
     rows, max_pages = table.shape
     _want(dh == cache.c.head_dim and q.stride(2) == 1 and out.shape == q.shape and out.is_contiguous()
-          and (lse is None or (lse.element_size() == 4 and lse.numel() == tokens * n_q and lse.is_contiguous())),
+          and (lse is None or (lse.dtype is _t().float32 and lse.numel() == tokens * n_q and lse.is_contiguous())),
           "kv_q4_attend")
     _whole("kv_q4_attend", table, start, length)
     _want(start.numel() == rows + 1 and length.numel() == rows, "kv_q4_attend")
@@ -449,9 +473,10 @@ def spec_logprobs(logits, tok, logprob, workspace, rank=None, entropy=None, top_
     top = 0 if top_id is None else top_id.shape[1]
     _whole("spec_logprobs", tok, rank, n=n)
     _whole("spec_logprobs", top_id, n=n * top)
+    f32 = _t().float32
     for t, size in ((logprob, n), (entropy, n), (top_lp, n * top)):
-        _want(t is None or (t.element_size() == 4 and t.is_floating_point() and t.is_contiguous() and t.numel() == size),
-              "spec_logprobs")
+        if t is not None and (t.dtype is not f32 or not t.is_contiguous() or t.numel() != size):
+            raise MTPError(9, "spec_logprobs")
     _want(logits.stride(1) == 1 and (top_id is None) == (top_lp is None)
           and workspace.numel() * workspace.element_size() >= lib().spec_logprobs_workspace_bytes(n, V, top),
           "spec_logprobs")

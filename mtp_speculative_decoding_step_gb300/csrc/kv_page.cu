@@ -29,6 +29,7 @@ namespace {
 
 constexpr int kPlanThreads = 512;
 constexpr int kPlanMaxRows = 4096;
+constexpr int kNo = 1 << 30;   // (pages of a row stay below 2^27)
 constexpr int kPlanTokens = 4 * kPlanThreads;  // packed positions per block and turn
 
 struct PlanArgs {
@@ -37,23 +38,25 @@ struct PlanArgs {
   int32_t *table, *free_pages, *cover_out, *start, *slot, *pos, *status;
 };
 
-// One row's lengths, checked.
+// One row's lengths, checked. (32-bit throughout: a row's capacity is below
+// 2^31, and two counts below that add up below 2^32.)
 struct PlanRow {
   int held, want, fresh;  // fresh: appended positions that the packing counts
   int fault;              // 0, or 1 << status
-  long long total;
+  int keep, total;
 };
 
 __device__ __forceinline__ PlanRow plan_row(const PlanArgs& a, int r) {
   PlanRow p;
-  const long long cap = (long long)a.page * a.max_pages;
-  const int c = a.cover[r], k = a.keep[r], n = a.fresh[r];
-  const long long cc = min(max((long long)c, 0LL), cap);
-  p.held = (int)((cc + a.page - 1) / a.page);
-  p.total = (long long)k + n;
+  const unsigned cap = (unsigned)a.page * a.max_pages, page = a.page;
+  const int c = __ldg(a.cover + r), k = __ldg(a.keep + r), n = __ldg(a.fresh + r);
+  const unsigned cc = min((unsigned)max(c, 0), cap), total = (unsigned)k + (unsigned)n;
+  p.held = (int)((cc + page - 1) / page);
+  p.keep = k;
+  p.total = (int)total;
   p.fresh = max(n, 0);
-  p.fault = c != cc || k < 0 || k > c || n < 0 ? 1 << MTP_ERR_BAD_ARG : (p.total > cap ? 1 << MTP_ERR_KV_CAPACITY : 0);
-  p.want = p.fault ? p.held : (int)((p.total + a.page - 1) / a.page);
+  p.fault = c != (int)cc || k < 0 || k > c || n < 0 ? 1 << MTP_ERR_BAD_ARG : (total > cap ? 1 << MTP_ERR_KV_CAPACITY : 0);
+  p.want = p.fault ? p.held : (int)((total + page - 1) / page);
   return p;
 }
 
@@ -103,7 +106,8 @@ __global__ void __launch_bounds__(kPlanThreads) k_page_plan(const PlanArgs a) {
   int* s_start = s_dyn;               // [rows] first packed position
   int* s_take = s_start + a.rows;     // [rows] pages taken before the row
   int* s_rel = s_take + a.rows;       // [rows] pages given back before the row
-  uint8_t* s_no = reinterpret_cast<uint8_t*>(s_rel + a.rows);  // [rows] refused
+  int* s_keep = s_rel + a.rows;       // [rows] positions kept
+  int* s_held = s_keep + a.rows;      // [rows] pages held, bit 30: refused
   __shared__ long long s_w[2][2][kPlanThreads / 32];
   __shared__ int s_fault, s_granted;
   const int t = threadIdx.x;
@@ -116,8 +120,9 @@ __global__ void __launch_bounds__(kPlanThreads) k_page_plan(const PlanArgs a) {
   const int per = (a.rows + kPlanThreads - 1) / kPlanThreads;
   const int r0 = min(t * per, a.rows), r1 = min(r0 + per, a.rows);
   long long v[2] = {0, 0}, tot[2];
+  PlanRow p;  // (with a row a thread at most, made once)
   for (int r = r0; r < r1; ++r) {
-    const PlanRow p = plan_row(a, r);
+    p = plan_row(a, r);
     v[0] += p.fresh;
     v[1] += p.held;
   }
@@ -128,14 +133,17 @@ __global__ void __launch_bounds__(kPlanThreads) k_page_plan(const PlanArgs a) {
   long long at = v[0];
   int fault = 0;
   v[0] = v[1] = 0;
+  bool no = false;
   for (int r = r0; r < r1; ++r) {
-    const PlanRow p = plan_row(a, r);
+    if (per > 1) p = plan_row(a, r);
     s_start[r] = (int)min(at, (long long)a.max_tokens);
     at += p.fresh;
     const bool fits = at <= a.max_tokens;
-    s_no[r] = p.fault || broken || !fits;
+    no = p.fault || broken || !fits;
+    s_keep[r] = p.keep;
+    s_held[r] = p.held | (no ? kNo : 0);
     fault |= p.fault | (broken || !fits ? 1 << MTP_ERR_BAD_ARG : 0);
-    if (!s_no[r]) {
+    if (!no) {
       v[0] += max(0, p.want - p.held);
       v[1] += max(0, p.held - p.want);
     }
@@ -146,15 +154,19 @@ __global__ void __launch_bounds__(kPlanThreads) k_page_plan(const PlanArgs a) {
   long long tk = v[0], rl = v[1];
   int granted = 0;
   for (int r = r0; r < r1; ++r) {
-    const PlanRow p = plan_row(a, r);
+    if (per > 1) {
+      p = plan_row(a, r);
+      no = s_held[r] & kNo;
+    }
     s_take[r] = (int)tk;
     s_rel[r] = (int)rl;
-    if (!s_no[r]) {
+    if (!no) {
       const int take = max(0, p.want - p.held);
       rl += max(0, p.held - p.want);
       tk += take;
       if (take && tk > top) {  // as is every later taker
-        s_no[r] = 1;
+        no = true;
+        s_held[r] = p.held | kNo;
         fault |= 1 << MTP_ERR_KV_CAPACITY;
       } else if (take) {
         granted = (int)tk;
@@ -163,7 +175,7 @@ __global__ void __launch_bounds__(kPlanThreads) k_page_plan(const PlanArgs a) {
     if (blockIdx.x == 0) {
       a.start[r] = s_start[r];
       // (cover and cover_out do not overlap: other blocks still read cover)
-      a.cover_out[r] = s_no[r] ? min(max(a.cover[r], 0), a.page * a.max_pages) : (int)p.total;
+      a.cover_out[r] = no ? min(max(a.cover[r], 0), a.page * a.max_pages) : p.total;
     }
   }
   if (blockIdx.x == 0 && t == 0) a.start[a.rows] = n_tok;
@@ -182,8 +194,9 @@ __global__ void __launch_bounds__(kPlanThreads) k_page_plan(const PlanArgs a) {
   auto taken = [&](int k) {
     if (k < sum_rel) {
       const int r = last_le(s_rel, a.rows, k);
-      const PlanRow p = plan_row(a, r);
-      return checked(a.table[(long long)r * a.max_pages + p.want + (k - s_rel[r])]);
+      // (a row that gives pages back is not refused)
+      const int want = (s_keep[r] + __ldg(a.fresh + r) + a.page - 1) / a.page;
+      return checked(a.table[(long long)r * a.max_pages + want + (k - s_rel[r])]);
     }
     return checked(a.free_pages[top - 1 - k]);
   };
@@ -193,8 +206,7 @@ __global__ void __launch_bounds__(kPlanThreads) k_page_plan(const PlanArgs a) {
   // onto the stack
   for (long long k = gt; k < n_take; k += nt) {
     const int r = last_le(s_take, a.rows, (int)k);
-    const PlanRow p = plan_row(a, r);
-    a.table[(long long)r * a.max_pages + p.held + ((int)k - s_take[r])] = taken((int)k);
+    a.table[(long long)r * a.max_pages + s_held[r] + ((int)k - s_take[r])] = taken((int)k);
   }
   for (long long k = n_take + gt; k < sum_rel; k += nt) a.free_pages[top - 1 - k] = taken((int)k);
 
@@ -202,9 +214,7 @@ __global__ void __launch_bounds__(kPlanThreads) k_page_plan(const PlanArgs a) {
   for (long long b = 4 * gt; b < a.max_tokens; b += 4 * nt) {
     int slot[4], pos[4];
     int r = b < n_tok ? last_le(s_start, a.rows, (int)b) : 0;
-    int r_have = -1, at_have = -1, id_have = -1;
-    PlanRow p;
-    bool no = true;
+    int r_have = -1, at_have = -1, id_have = -1, keep = 0, held = 0;
 #pragma unroll
     for (int j = 0; j < 4; ++j) {
       const int i = (int)b + j;
@@ -212,16 +222,16 @@ __global__ void __launch_bounds__(kPlanThreads) k_page_plan(const PlanArgs a) {
       if (i >= n_tok) continue;
       while (r + 1 < a.rows && s_start[r + 1] <= i) ++r;
       if (r != r_have) {
-        p = plan_row(a, r);
-        no = s_no[r];
+        keep = s_keep[r];
+        held = s_held[r];
         r_have = r;
         at_have = -1;
       }
-      pos[j] = a.keep[r] + (i - s_start[r]);
-      if (no) continue;
+      pos[j] = keep + (i - s_start[r]);
+      if (held & kNo) continue;
       const int at = pos[j] / a.page;
       if (at != at_have) {
-        id_have = at < p.held ? checked(a.table[(long long)r * a.max_pages + at]) : taken(s_take[r] + (at - p.held));
+        id_have = at < held ? checked(a.table[(long long)r * a.max_pages + at]) : taken(s_take[r] + (at - held));
         at_have = at;
       }
       if (id_have >= 0) slot[j] = id_have * a.page + (pos[j] - at * a.page);
@@ -258,7 +268,7 @@ extern "C" mtp_status kv_page_plan(mtp_stream stream, int32_t rows, int32_t page
   if (d_cover_out < d_cover + rows && d_cover < d_cover_out + rows) return MTP_ERR_BAD_ARG;
   PlanArgs a{rows, page, max_pages, n_pages, max_tokens, d_cover, d_keep, d_new, d_table, d_free, d_cover_out,
              d_start, d_slot, d_pos, d_status};
-  const int smem = 13 * rows;  // at 4096 rows more than the default limit
+  const int smem = 20 * rows;  // at 4096 rows more than the default limit
   {
     static std::mutex mu;
     static bool set[kMaxDevices] = {};
@@ -267,7 +277,7 @@ extern "C" mtp_status kv_page_plan(mtp_stream stream, int32_t rows, int32_t page
     if (dev < 0 || dev >= kMaxDevices) dev = 0;
     std::lock_guard<std::mutex> lock(mu);
     if (!set[dev]) {
-      if (cudaFuncSetAttribute(k_page_plan, cudaFuncAttributeMaxDynamicSharedMemorySize, 13 * kPlanMaxRows) != cudaSuccess) {
+      if (cudaFuncSetAttribute(k_page_plan, cudaFuncAttributeMaxDynamicSharedMemorySize, 20 * kPlanMaxRows) != cudaSuccess) {
         cudaGetLastError();
         return MTP_ERR_CUDA;
       }

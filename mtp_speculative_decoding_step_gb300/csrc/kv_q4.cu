@@ -1,10 +1,15 @@
 // Append to and read from the paged 4-bit KV cache (kv_q4_append, kv_q4_read).
 //
 // Rounding of 16 elements y = x 2^-exp: scale = e4m3(max|y| / 6), code = the
-// e2m1 value nearest to |y| / scale. No quotient is formed for the codes: the
-// seven borders between neighbouring values, times the scale, are exact in fp32
-// (three significant bits times four), so comparing |y| with them gives the
-// exact nearest value, ties to the even code.
+// e2m1 value nearest to |y| / scale, ties to the even code. The seven borders
+// between neighbouring values, times the scale, are exact in fp32 (three
+// significant bits times four).
+//   fp32 input: |y| is compared with them, which is exact; a quotient could
+//     round onto a border that |y| only comes near.
+//   bf16 input: |y| (8 bits) is either on a border or 2^-9 of it away, so the
+//     correctly rounded quotient q = y r + (y - (y r) b) r, r = 1 / b (one
+//     Newton step on the product) is on a border exactly where y is, and the
+//     conversion instruction's rounding to nearest even is the definition's.
 //
 // One thread per 16 elements: its loads are one or two sectors, its eight code
 // bytes and one scale byte lie next to its neighbours'. HBM-bound: a bf16 value
@@ -102,14 +107,35 @@ __global__ void __launch_bounds__(kQ4Threads) k_q4_append(const __grid_constant_
   asm("cvt.rn.satfinite.e4m3x2.f32 %0, %1, %2;" : "=h"(sc) : "f"(0.f), "f"(amax / 6.f));
   const float s = f16x2_to_f(e4m3x2_to_f16x2(sc)).x;
   uint32_t code[2] = {0, 0};
+  if (DT == MTP_DTYPE_BF16) {
+    const float rs = __frcp_rn(s);
 #pragma unroll
-  for (int i = 0; i < 16; ++i) {
-    const float m = fabsf(x[i]);
-    // borders .25 .75 1.25 1.75 2.5 3.5 5; on a border the even code
-    uint32_t c = (m > 0.25f * s) + (m >= 0.75f * s) + (m > 1.25f * s) + (m >= 1.75f * s) + (m > 2.5f * s) +
-                 (m >= 3.5f * s) + (m > 5.f * s);
-    c |= (__float_as_uint(x[i]) >> 31) << 3;
-    code[i >> 3] |= c << (4 * (i & 7));
+    for (int w = 0; w < 2; ++w) {
+      float q[8];
+#pragma unroll
+      for (int i = 0; i < 8; ++i) {
+        const float y = x[8 * w + i], q0 = y * rs;
+        q[i] = copysignf(fmaf(fmaf(-q0, s, y), rs, q0), y);  // (-0 stays -0)
+      }
+      asm("{\n\t.reg .b8 b0, b1, b2, b3;\n\t"
+          "cvt.rn.satfinite.e2m1x2.f32 b0, %2, %1;\n\t"
+          "cvt.rn.satfinite.e2m1x2.f32 b1, %4, %3;\n\t"
+          "cvt.rn.satfinite.e2m1x2.f32 b2, %6, %5;\n\t"
+          "cvt.rn.satfinite.e2m1x2.f32 b3, %8, %7;\n\t"
+          "mov.b32 %0, {b0, b1, b2, b3};\n\t}"
+          : "=r"(code[w])
+          : "f"(q[0]), "f"(q[1]), "f"(q[2]), "f"(q[3]), "f"(q[4]), "f"(q[5]), "f"(q[6]), "f"(q[7]));
+    }
+  } else {
+#pragma unroll
+    for (int i = 0; i < 16; ++i) {
+      const float m = fabsf(x[i]);
+      // borders .25 .75 1.25 1.75 2.5 3.5 5; on a border the even code
+      uint32_t c = (m > 0.25f * s) + (m >= 0.75f * s) + (m > 1.25f * s) + (m >= 1.75f * s) + (m > 2.5f * s) +
+                   (m >= 3.5f * s) + (m > 5.f * s);
+      c |= (__float_as_uint(x[i]) >> 31) << 3;
+      code[i >> 3] |= c << (4 * (i & 7));
+    }
   }
   uint8_t scale = (uint8_t)sc;
   if (!finite) {
@@ -161,16 +187,17 @@ __global__ void __launch_bounds__(kQ4Threads) k_q4_read(const __grid_constant__ 
     const uint8_t* row = a.cache[kv] + (((long long)(slot / a.page) * a.n_kv + head) * a.page + slot % a.page) * kRow;
     const uint32_t* c = reinterpret_cast<const uint32_t*>(row + 8 * b);
     const uint32_t sc = row[DH / 2 + b];
-    const float s = f16x2_to_f(e4m3x2_to_f16x2(sc)).x * pow2i(head_exp(a.exp[kv], head));
+    const uint32_t s2 = e4m3x2_to_f16x2(sc * 0x0101u);
+    const float up = pow2i(head_exp(a.exp[kv], head));
 #pragma unroll
     for (int w = 0; w < 2; ++w) {
       uint32_t h[4];
       e2m1x8_to_f16(c[w], h);
 #pragma unroll
       for (int j = 0; j < 4; ++j) {
-        const float2 f = f16x2_to_f(h[j]);
-        v[8 * w + 2 * j] = f.x * s;
-        v[8 * w + 2 * j + 1] = f.y * s;
+        const float2 f = f16x2_to_f(hmul2_bits(h[j], s2));
+        v[8 * w + 2 * j] = f.x * up;
+        v[8 * w + 2 * j + 1] = f.y * up;
       }
     }
   }
@@ -183,7 +210,7 @@ __global__ void __launch_bounds__(kQ4Threads) k_q4_read(const __grid_constant__ 
       uint32_t u[4];
 #pragma unroll
       for (int j = 0; j < 4; ++j)
-        u[j] = (uint32_t)f_to_bf16(v[8 * w + 2 * j]) | ((uint32_t)f_to_bf16(v[8 * w + 2 * j + 1]) << 16);
+        asm("cvt.rn.bf16x2.f32 %0, %1, %2;" : "=r"(u[j]) : "f"(v[8 * w + 2 * j + 1]), "f"(v[8 * w + 2 * j]));
       o[w] = make_uint4(u[0], u[1], u[2], u[3]);
     }
   } else {

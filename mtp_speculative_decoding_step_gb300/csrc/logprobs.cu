@@ -521,12 +521,12 @@ __global__ void __launch_bounds__(kLpThreads + 32, kLpBlocksPerSM) k_lp_part(con
   if (tid == 0) a.heads[at] = make_uint4((uint32_t)known, (uint32_t)(known >> 32), (uint32_t)n, 0u);
 }
 
-constexpr int kLpJoinThreads = 128;
+constexpr int kLpJoinThreads = 256;
 constexpr int kLpLive = 1024;
 
 __global__ void __launch_bounds__(kLpJoinThreads) k_lp_join(const __grid_constant__ LpArgs a, int dt) {
   __shared__ unsigned long long s_live[kLpLive], s_bound;
-  __shared__ int s_n;
+  __shared__ int s_n, s_cnt[kLpMaxParts];
   __shared__ float s_red[4][kLpJoinThreads / 32];
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, r = blockIdx.x, P = a.parts, top = a.top;
   if (tid == 0) {
@@ -544,6 +544,7 @@ __global__ void __launch_bounds__(kLpJoinThreads) k_lp_join(const __grid_constan
     if (top > 0) {
       const uint4 h = a.heads[(long long)r * P + p];
       bound = max(bound, (unsigned long long)h.y << 32 | h.x);
+      s_cnt[p] = min((int)h.z, kLpList);
     }
     s.add(LpSum{f.x, f.y, f.z});
     before += __float_as_int(f.w);
@@ -591,10 +592,20 @@ __global__ void __launch_bounds__(kLpJoinThreads) k_lp_join(const __grid_constan
     a.top_id[(long long)r * top + rank] = (int32_t)(0xFFFFFFFFu - (uint32_t)k);
     a.top_lp[(long long)r * top + rank] = (key_value(k) - s.m) - ls;
   };
-  auto keys = [&](auto&& f) {
-    for (int p = warp; p < P; p += kLpJoinThreads / 32) {
-      const int n = min((int)a.heads[(long long)r * P + p].z, kLpList);
-      for (int i = lane; i < n; i += 32) f(a.keys[((long long)r * P + p) * kLpList + i]);
+  auto keys = [&](auto&& f) {  // eight threads per part's list, four keys each in flight
+#pragma unroll 1
+    for (int p = tid >> 3; p < P; p += kLpJoinThreads / 8) {
+      const unsigned long long* list = a.keys + ((long long)r * P + p) * kLpList;
+      const int n = s_cnt[p];
+#pragma unroll 1
+      for (int i = tid & 7; i < n; i += 32) {
+        unsigned long long k[4];
+#pragma unroll
+        for (int c = 0; c < 4; ++c) k[c] = i + 8 * c < n ? list[i + 8 * c] : 0ull;
+#pragma unroll
+        for (int c = 0; c < 4; ++c)
+          if (k[c]) f(k[c]);
+      }
     }
   };
   auto collect = [&]() {
@@ -639,8 +650,7 @@ __global__ void __launch_bounds__(kLpJoinThreads) k_lp_join(const __grid_constan
     keys([&](unsigned long long k) {
       int rank = 0;
       for (int p = 0; p < P; ++p) {
-        const int m = min((int)a.heads[(long long)r * P + p].z, kLpList);
-        for (int i = 0; i < m; ++i) rank += a.keys[((long long)r * P + p) * kLpList + i] > k;
+        for (int i = 0; i < s_cnt[p]; ++i) rank += a.keys[((long long)r * P + p) * kLpList + i] > k;
       }
       if (rank < top) put(k, rank);
     });

@@ -68,6 +68,32 @@ def test_append_writes_the_reference_bytes(T, nkv, dh, page, layout, dtype):
         assert torch.equal(val.to(dtype).double(), val)  # the values are exact in either type
 
 
+def test_bf16_quotients_agree_with_the_comparisons():
+    """bf16 input is rounded through a quotient, fp32 input by exact comparisons: the same bytes for the same values, at
+    every scale, on every border, one bf16 step to either side of it, and over random values."""
+    scales = torch.arange(1, 127, dtype=torch.uint8).view(torch.float8_e4m3fn).float()  # every finite scale above 0
+    borders = torch.tensor([0.25, 0.75, 1.25, 1.75, 2.5, 3.5, 5.0])
+    on = (scales[:, None] * borders).to(torch.bfloat16)
+    bits = on.view(torch.int16)
+    near = torch.stack([on, (bits + 1).view(torch.bfloat16), (bits - 1).view(torch.bfloat16)], -1).flatten(1)  # [126, 21]
+    top = (scales * 6).to(torch.bfloat16)[:, None]  # makes the block's scale
+    rows = torch.cat([torch.cat([top, near[:, :15]], 1), torch.cat([top, near[:, 6:]], 1)], 1)  # two blocks of 16
+    rows = torch.cat([rows, -rows], 1).reshape(126, 1, 64)
+    g = torch.Generator().manual_seed(8)
+    noise = (torch.randn((4096, 1, 64), generator=g) * torch.exp(3 * torch.randn((4096, 1, 1), generator=g))).to(torch.bfloat16)
+    x = torch.cat([rows, noise]).cuda()
+    T = x.shape[0]
+    slot = torch.arange(T, dtype=torch.int32, device="cuda")
+    got = []
+    for y in (x, x.float()):
+        k, v, cache = new_cache(-(-T // 16), 1, 16, 64)
+        m.kv_q4_append(cache, y, y, slot)
+        got.append((k, v))
+    assert torch.equal(got[0][0], got[1][0]) and torch.equal(got[0][1], got[1][1])
+    raw, _ = q4_ref.quantize(x[:126].cpu())
+    assert torch.equal(got[0][0].cpu().reshape(-1, 1, 36)[:126], raw)
+
+
 def test_nonfinite_blocks_read_back_as_nan_and_are_reported():
     k, v = inputs(4, 2, 64, torch.bfloat16, 3), inputs(4, 2, 64, torch.bfloat16, 4)
     k[1, 0, 5], v[2, 1, 63], v[3, 0, 16] = float("nan"), float("inf"), -float("inf")
