@@ -9,7 +9,7 @@ namespace mtp {
 
 namespace {
 
-constexpr int kJoinThreads = 256;
+constexpr int kJoinThreads = 128;  // small blocks: most find nothing to do
 
 // Block (b, y): the query tile that block b of the attention began and did not
 // end; blocks b + 1 to `last` hold the rest of it. Row by row (y, y + gridDim.y,
@@ -46,7 +46,7 @@ __global__ void __launch_bounds__(kJoinThreads) k_q4_join(const __grid_constant_
     for (int w = 0; w < kJoinThreads / 32; ++w) m = fmaxf(m, s_red[0][w]);
     float l = 0.f;
     float4 o = make_float4(0.f, 0.f, 0.f, 0.f);
-    for (int p0 = 0; p0 < parts; p0 += kJoinThreads) {  // (one turn up to 256 blocks)
+    for (int p0 = 0; p0 < parts; p0 += kJoinThreads) {
       if (p0 + tid < parts) {
         const float2 ml = a.part_ml[at(p0 + tid)];
         const float w = ml.x == -INFINITY ? (ml.y == 0.f ? 0.f : 1.f) : exp2f(ml.x - m);
@@ -54,7 +54,7 @@ __global__ void __launch_bounds__(kJoinThreads) k_q4_join(const __grid_constant_
         l = fmaf(w, ml.y, l);
       }
       __syncthreads();
-#pragma unroll 4
+#pragma unroll 8
       for (int p = grp; p < min(parts - p0, kJoinThreads); p += kG) {
         const float w = s_w[p];
         const float4 v = reinterpret_cast<const float4*>(a.part_o + at(p0 + p) * DH)[d4];
@@ -75,11 +75,11 @@ __global__ void __launch_bounds__(kJoinThreads) k_q4_join(const __grid_constant_
 #pragma unroll
     for (int w = 0; w < kJoinThreads / 32; ++w) l += s_red[1][w];
     const long long dst = (long long)(a0 + f / G) * a.n_q + me.y * G + f % G;
-    if (tid < DH) {
+    for (int d = tid; d < DH; d += kJoinThreads) {
       float y = 0.f;
 #pragma unroll
-      for (int g = 0; g < kG; ++g) y += reinterpret_cast<const float*>(s_o[g])[tid];
-      store_elem(a.out, DT, dst * DH + tid, l != 0.f ? y * (up / l) : 0.f);
+      for (int g = 0; g < kG; ++g) y += reinterpret_cast<const float*>(s_o[g])[d];
+      store_elem(a.out, DT, dst * DH + d, l != 0.f ? y * (up / l) : 0.f);
     }
     if (tid == 0 && a.lse) a.lse[dst] = l != 0.f ? (m + log2f(l)) * 0.693147181f : -INFINITY;
   }

@@ -458,12 +458,13 @@ __global__ void __launch_bounds__(kAttnThreads, 1) k_q4_attn(const __grid_consta
     if (lane < 2) a.part_meta[2 * blockIdx.x + lane] = make_int4(0, 0, 0, 0);
     const int per = (a.rows + 31) / 32, r0 = min(lane * per, a.rows), r1 = min(r0 + per, a.rows);
     long long sum = 0;
-    int a0 = 0, n = 0, L = 0;
+    int a0 = 0, n = 0, L = 0, ph = 0;
 #pragma unroll 1
     for (int r = r0; r < r1; ++r) {
       walk.row(r, a0, n, L);
       if (blockIdx.x == 0 && L != a.len[r]) flag_status(a.status, MTP_ERR_BAD_ARG);
-      sum += (long long)walk.per_head(n, L) * a.n_kv;
+      ph = walk.per_head(n, L);
+      sum += (long long)ph * a.n_kv;
     }
     long long inc = sum;
 #pragma unroll
@@ -477,11 +478,16 @@ __global__ void __launch_bounds__(kAttnThreads, 1) k_q4_attn(const __grid_consta
     const int nb = (int)max(1LL, min((long long)gridDim.x, all)), b = blockIdx.x;
     long long q = 0;
     unsigned rem = 0;
+    if (all >> 32 == 0) {
+      q = (unsigned)all / (unsigned)nb;
+      rem = (unsigned)all - (unsigned)q * nb;
+    } else {
 #pragma unroll 1
-    for (int d = 48; d >= 0; d -= 16) {  // all / nb, 16 bits a step (nb < 2^16)
-      const unsigned part = rem << 16 | (unsigned)(all >> d & 0xFFFF), x = part / (unsigned)nb;
-      q = q << 16 | x;
-      rem = part - x * nb;
+      for (int d = 48; d >= 0; d -= 16) {  // 16 bits a step (nb < 2^16)
+        const unsigned part = rem << 16 | (unsigned)(all >> d & 0xFFFF), x = part / (unsigned)nb;
+        q = q << 16 | x;
+        rem = part - x * nb;
+      }
     }
     const int more = (int)rem;
     const long long w0 = b < nb ? b * q + min(b, more) : all;
@@ -494,11 +500,14 @@ __global__ void __launch_bounds__(kAttnThreads, 1) k_q4_attn(const __grid_consta
     a0 = __shfl_sync(0xFFFFFFFFu, a0, owner);  // (the last row that the lane looked at: its only one, mostly)
     n = __shfl_sync(0xFFFFFFFFu, n, owner);
     L = __shfl_sync(0xFFFFFFFFu, L, owner);
+    ph = __shfl_sync(0xFFFFFFFFu, ph, owner);
     if (left > 0) {
 #pragma unroll 1
       for (;; ++r) {
-        if (per > 1) walk.row(r, a0, n, L);
-        const int ph = walk.per_head(n, L);
+        if (per > 1) {
+          walk.row(r, a0, n, L);
+          ph = walk.per_head(n, L);
+        }
         if (w0 < at + (long long)ph * a.n_kv) {
           const unsigned x = (unsigned)(w0 - at);  // (a row has fewer than 2^32 tasks)
           g = (int)(x / (unsigned)ph);
@@ -1157,6 +1166,11 @@ __global__ void __launch_bounds__(kAttnThreads, 1) k_q4_attn(const __grid_consta
       if (!whole && sg == 0 && me == 0)
         a.part_meta[slot] = make_int4(s.r, s.g, s.j, begins ? s.last : -1);
       group_sync(bar);
+      constexpr int kOut = NC < 16 ? 8 : 16;  // columns of O at a time
+      auto load_o = [](uint32_t t, float* o) {
+        if constexpr (kOut == 8) tc::tmem_ld8(t, o);
+        else tc::tmem_ld16(t, o);
+      };
       auto put = [](void* out, long long at, float y) {
         if (WIDE) static_cast<float*>(out)[at] = y;
         else static_cast<__nv_bfloat16*>(out)[at] = __float2bfloat16_rn(y);
@@ -1165,36 +1179,36 @@ __global__ void __launch_bounds__(kAttnThreads, 1) k_q4_attn(const __grid_consta
 #pragma unroll 1
         for (int mb = 0; mb < S::MB; ++mb)
 #pragma unroll 1
-          for (int c = 0; c < NC; c += 8) {
-            float o[8];
-            tc::tmem_ld8(tmem + S::cO + mb * N + c0 + c + lanes, o);
+          for (int c = 0; c < NC; c += kOut) {
+            float o[kOut];
+            load_o(tmem + S::cO + mb * N + c0 + c + lanes, o);
             if (WIDE) {
-              float o2[8];
-              tc::tmem_ld8(tmem + S::cO + mb * N + N / 2 + c0 + c + lanes, o2);
+              float o2[kOut];
+              load_o(tmem + S::cO + mb * N + N / 2 + c0 + c + lanes, o2);
 #pragma unroll
-              for (int e = 0; e < 8; ++e) o[e] += o2[e];
+              for (int e = 0; e < kOut; ++e) o[e] += o2[e];
             }
             const int d = mb * 128 + 32 * quarter + lane;
             if (M.nan_run[run & 1] == run + 1) {
               uint32_t nan = 0;
 #pragma unroll 1
-              for (int e = 0; e < 8; ++e)
+              for (int e = 0; e < kOut; ++e)
                 nan |= (uint32_t)sees_nan<DH / 16>(s.first, s.tile, nt, s.p0, s.p1, M.nan_bits[run & 1], d / 16,
                                                    M.lim[c0 + c + e], a.window) << e;
 #pragma unroll
-              for (int e = 0; e < 8; ++e)
+              for (int e = 0; e < kOut; ++e)
                 if (nan >> e & 1) o[e] = __int_as_float(0x7FC00000);
             }
             if (whole) {
 #pragma unroll
-              for (int e = 0; e < 8; ++e) {
+              for (int e = 0; e < kOut; ++e) {
                 const int dst = M.dst[c0 + c + e];
                 if (dst >= 0) put(a.out, (long long)dst * DH + d, o[e] * M.f[c0 + c + e]);
               }
             } else {
               float* p = a.part_o + ((long long)slot * S::RT + c0 + c) * DH + d;
 #pragma unroll
-              for (int e = 0; e < 8; ++e) p[e * DH] = o[e];
+              for (int e = 0; e < kOut; ++e) p[e * DH] = o[e];
             }
           }
       }

@@ -670,7 +670,7 @@ int lp_parts(int n, int V) {
   int best = 1;
   double least = 0;
   for (int p = 1; p <= most; ++p) {
-    const double cost = (double)(((long long)n * p + slots - 1) / slots) * ((double)V / p + 8000.0) + 30.0 * p;
+    const double cost = (double)(((long long)n * p + slots - 1) / slots) * ((double)V / p + 8000.0) + 110.0 * p;
     if (p == 1 || cost < least) {
       least = cost;
       best = p;
