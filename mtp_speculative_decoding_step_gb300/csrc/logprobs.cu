@@ -8,15 +8,24 @@
 // k_lp_part: a row is cut into parts, one block each. A thread keeps its own
 // running (m, S, T); when m grows by d, S and T become f S and f (T - d S) with
 // f = e^-d. Alternatives: at least k elements reach the k-th largest of the
-// maxima that groups of threads saw, so only threads whose own maximum reaches
-// that bound look at their elements again (from L2) and collect what does: some
-// 25 elements for k = 20. A collection that overflows is cut to its k best as it
-// goes. Elements go by 64-bit keys (value descending, id ascending), so ties
-// need no care anywhere.
-// k_lp_join: a block per row adds up the parts and merges their k keys.
+// maxima that groups of threads saw. A thread also keeps its maxima over eight
+// stretches of the part, so that only stretches whose maximum reaches that
+// bound are looked at again (from L2), a vector per lane: some 25 elements for
+// k = 20. A collection that overflows is cut to its k best as it goes. Elements
+// go by 64-bit keys (value descending, id ascending), so ties need no care
+// anywhere.
+// k_lp_join: a block per row adds up the parts and merges their lists.
 //
-// HBM-bound for many rows: 9 instructions an element, one of them an exponential.
+// Bound by issue and, at a part's end, by latency: 14 instructions an element
+// (one an exponential, at 16 a cycle and SM), then some 8,000 cycles for the
+// alternatives, which four blocks an SM hide only in part. 256 rows of 152,064
+// fp32 logits with 20 alternatives: 42 us, 3.7 TB/s; without any 37 us; 1001
+// rows of 32,769 bf16 logits with 8: 33 us; 3 rows of 152,064 with 5: 10 us.
+// One block per SM slot for all its rows' parts (copies running on into the
+// next part) was slower, 50 and 46 us: its loop needs registers that four
+// blocks an SM do not have.
 #include <algorithm>
+#include <climits>
 
 #include "common.cuh"
 #include "kernels.h"
@@ -31,6 +40,7 @@ constexpr int kLpMaxTop = 64;
 constexpr int kLpCap = 1024;        // collected keys of a block
 constexpr int kLpList = 128;        // keys that a part hands on
 constexpr int kLpMaxParts = 128;
+constexpr int kLpCells = 8;
 constexpr int kLpStages = 4;
 constexpr int kLpStage = 8192;      // bytes: two 16-byte vectors a thread
 constexpr unsigned kLpWaitLimit = 1u << 20;
@@ -96,6 +106,21 @@ struct LpSum {
   }
 };
 
+// The sum over the first `lanes` lanes of a warp (a power of two; in lane 0):
+// the largest m first, then plain sums.
+__device__ __forceinline__ void lp_warp_add(LpSum& s, int& before, int lanes) {
+  float m = s.m;
+#pragma unroll
+  for (int o = lanes / 2; o > 0; o >>= 1) m = fmaxf(m, __shfl_xor_sync(0xFFFFFFFFu, m, o));
+  if (s.m < m) s.raise(m);
+#pragma unroll
+  for (int o = lanes / 2; o > 0; o >>= 1) {
+    s.S += __shfl_xor_sync(0xFFFFFFFFu, s.S, o);
+    s.T += __shfl_xor_sync(0xFFFFFFFFu, s.T, o);
+    before += __shfl_xor_sync(0xFFFFFFFFu, before, o);
+  }
+}
+
 // Two fp32 values side by side (one instruction for both).
 __device__ __forceinline__ uint64_t pair(float a, float b) {
   uint64_t d;
@@ -135,11 +160,14 @@ struct LpShared {
     alignas(128) uint8_t ring[kLpStages][kLpStage];
     unsigned long long key[2][kLpCap];  // collected keys, and those left of them (once the ring is done)
   };
+  float cell[kLpCells][kLpThreads];   // the threads' maxima over stretches of the part
+  int n_list[kLpThreads / 32];
+  uint16_t list[kLpThreads / 32][32 * kLpCells];  // a warp's cells that may hold alternatives: cell * 32 + lane
   alignas(16) unsigned long long group[128];
   unsigned long long bound, kth;
   uint64_t full[kLpStages], empty[kLpStages];
-  int n, n_live, fail;
-  float red[4][kLpThreads / 32];
+  int n, n_live;
+  float4 sums[kLpThreads / 32];
 };
 
 // Barrier of the 256 threads that compute.
@@ -164,19 +192,19 @@ __device__ __forceinline__ void kth_bound(LpShared& sh, unsigned long long v, in
   v = max(v, __shfl_xor_sync(0xFFFFFFFFu, v, 1));
   if (g == 4) v = max(v, __shfl_xor_sync(0xFFFFFFFFu, v, 2));
   if (tid % g == 0) sh.group[tid / g] = v;
+  if (tid == 0) sh.kth = 0;
   lp_sync();
-  // a group's rank, counted by its g threads a slice each
-  const int me = tid / g, share = ng / g, from = tid % g * share;
-  const unsigned long long mine = sh.group[me];
+  // a group's rank, counted by its g threads, every g-th pair each (side by side in the banks)
+  const unsigned long long mine = sh.group[tid / g];
   int before = 0;
 #pragma unroll 4
-  for (int i = from; i < from + share; i += 2) {
+  for (int i = tid % g * 2; i < ng; i += 2 * g) {
     const ulonglong2 o = *reinterpret_cast<const ulonglong2*>(&sh.group[i]);
-    before += (o.x > mine || (o.x == mine && i < me)) + (o.y > mine || (o.y == mine && i + 1 < me));
+    before += (o.x > mine) + (o.y > mine);
   }
   before += __shfl_xor_sync(0xFFFFFFFFu, before, 1);
   if (g == 4) before += __shfl_xor_sync(0xFFFFFFFFu, before, 2);
-  if (before == top - 1) sh.kth = mine;
+  if (before == top - 1 && mine) sh.kth = mine;  // (keys differ; 0: the group saw nothing)
   lp_sync();
 }
 
@@ -228,7 +256,8 @@ __global__ void __launch_bounds__(kLpThreads + 32, kLpBlocksPerSM) k_lp_part(con
   const int v0 = (int)((long long)n_vec * part / a.parts), v1 = (int)((long long)n_vec * (part + 1) / a.parts);
   const uint8_t* body = row + head * (16 / W);
   if (tid == 0) {
-    sh.n = sh.fail = 0;
+    sh.n = 0;
+    for (int i = 0; i < kLpThreads / 32; ++i) sh.n_list[i] = 0;
     for (int i = 0; i < kLpStages; ++i) {
       mbar_init(smem_u32(&sh.full[i]), 1);
       mbar_init(smem_u32(&sh.empty[i]), kLpThreads / 32);
@@ -245,10 +274,7 @@ __global__ void __launch_bounds__(kLpThreads + 32, kLpBlocksPerSM) k_lp_part(con
     for (int i = 0; i < kLpStages; ++i) last[i] = -1;
 #pragma unroll 1
     for (int v = v0; v < v1; v += kVecs) {
-      if (round > 0 && !mbar_wait(smem_u32(&sh.empty[st]), (round - 1) & 1, kLpWaitLimit)) {
-        sh.fail = 1;
-        break;
-      }
+      if (round > 0 && !mbar_wait(smem_u32(&sh.empty[st]), (round - 1) & 1, kLpWaitLimit)) break;
       if (tid == kLpThreads) {
         const uint32_t bytes = min(kVecs, v1 - v) * 16;
         mbar_expect_tx(smem_u32(&sh.full[st]), bytes);
@@ -263,10 +289,17 @@ __global__ void __launch_bounds__(kLpThreads + 32, kLpBlocksPerSM) k_lp_part(con
         ++round;
       }
     }
-    if (sh.fail)  // copies in flight land before the block's shared memory goes
+    // (copies land before the block's shared memory goes, whatever the others do)
 #pragma unroll
-      for (int i = 0; i < kLpStages; ++i)
-        if (last[i] >= 0) mbar_wait(smem_u32(&sh.full[i]), last[i] & 1, kLpWaitLimit);
+    for (int i = 0; i < kLpStages; ++i)
+      if (last[i] >= 0) mbar_wait(smem_u32(&sh.full[i]), last[i] & 1, kLpWaitLimit);
+    __syncwarp();
+    asm volatile("barrier.cta.sync.aligned 2, 288;" ::: "memory");
+    const float4 f = sh.sums[tid & 7];
+    LpSum s{f.x, f.y, f.z};
+    int before = __float_as_int(f.w);
+    lp_warp_add(s, before, 8);
+    if (tid == kLpThreads) a.sums[(long long)r * a.parts + part] = make_float4(s.m, s.S, s.T, __int_as_float(before));
     return;
   }
   const int t = a.tok[r];
@@ -298,13 +331,16 @@ __global__ void __launch_bounds__(kLpThreads + 32, kLpBlocksPerSM) k_lp_part(con
 
   float seen = -INFINITY;  // the largest of the vectors, and the first one that had it
   int seen_at = v0;
+  const int cell_len = ((v1 - v0 + kVecs - 1) / kVecs + kLpCells - 1) / kLpCells;  // batches of a cell
+  int cell_at = 0, n_cells = 0;
+  float cell_max = -INFINITY;
   uint64_t S2 = 0, T2 = 0;  // even and odd elements' sums
   int st = 0, phase = 0;
   bool ok = true;
 #pragma unroll 1
   for (int v = v0; v < v1; v += kVecs) {
     const bool whole = v + kVecs <= v1;
-    ok = mbar_wait(smem_u32(&sh.full[st]), phase, kLpWaitLimit) && ok;
+    ok = ok && mbar_wait(smem_u32(&sh.full[st]), phase, kLpWaitLimit);
     uint4 w[Q];
 #pragma unroll
     for (int q = 0; q < Q; ++q) w[q] = reinterpret_cast<const uint4*>(sh.ring[st])[q * kLpThreads + tid];
@@ -345,6 +381,12 @@ __global__ void __launch_bounds__(kLpThreads + 32, kLpBlocksPerSM) k_lp_part(con
         s.raise(top);
       }
     }
+    cell_max = fmaxf(cell_max, top);
+    if (++cell_at == cell_len) {
+      sh.cell[n_cells++][tid] = cell_max;
+      cell_max = -INFINITY;
+      cell_at = 0;
+    }
     const int id0 = head + v * W, id1 = id0 + kVecs * W;
     const bool mixed = id0 <= t && t < id1;
     const float m = s.m == -INFINITY ? 0.f : s.m, over = mixed ? INFINITY : (id1 <= t ? below : xt);
@@ -384,44 +426,16 @@ __global__ void __launch_bounds__(kLpThreads + 32, kLpBlocksPerSM) k_lp_part(con
     }
   }
   fold(s, S2, T2);
-  if (!ok) {
-    flag_status(a.status, MTP_ERR_TIMEOUT);
-    sh.fail = 1;
-  }
+  if (cell_at > 0) sh.cell[n_cells++][tid] = cell_max;
+  if (!ok) flag_status(a.status, MTP_ERR_TIMEOUT);
 
-  // the block's sums
+  // the warps' sums; the copying warp adds them up
   const int lane = tid & 31, warp = tid >> 5;
-#pragma unroll
-  for (int o = 16; o > 0; o >>= 1) {
-    LpSum x;
-    x.m = __shfl_xor_sync(0xFFFFFFFFu, s.m, o);
-    x.S = __shfl_xor_sync(0xFFFFFFFFu, s.S, o);
-    x.T = __shfl_xor_sync(0xFFFFFFFFu, s.T, o);
-    s.add(x);
-    before += __shfl_xor_sync(0xFFFFFFFFu, before, o);
-  }
-  if (lane == 0) {
-    sh.red[0][warp] = s.m;
-    sh.red[1][warp] = s.S;
-    sh.red[2][warp] = s.T;
-    sh.red[3][warp] = __int_as_float(before);
-  }
-  lp_sync();
+  lp_warp_add(s, before, 32);
+  if (lane == 0) sh.sums[warp] = make_float4(s.m, s.S, s.T, __int_as_float(before));
+  __syncwarp();
+  asm volatile("barrier.cta.arrive.aligned 2, 288;" ::: "memory");
   const long long at = (long long)r * a.parts + part;
-  if (warp == 0) {
-    s = lane < kLpThreads / 32 ? LpSum{sh.red[0][lane], sh.red[1][lane], sh.red[2][lane]} : LpSum{-INFINITY, 0.f, 0.f};
-    before = lane < kLpThreads / 32 ? __float_as_int(sh.red[3][lane]) : 0;
-#pragma unroll
-    for (int o = kLpThreads / 64; o > 0; o >>= 1) {
-      LpSum x;
-      x.m = __shfl_xor_sync(0xFFFFFFFFu, s.m, o);
-      x.S = __shfl_xor_sync(0xFFFFFFFFu, s.S, o);
-      x.T = __shfl_xor_sync(0xFFFFFFFFu, s.T, o);
-      s.add(x);
-      before += __shfl_xor_sync(0xFFFFFFFFu, before, o);
-    }
-    if (lane == 0) a.sums[at] = make_float4(s.m, s.S, s.T, __int_as_float(before));
-  }
   if (a.top == 0) return;
 
   // the alternatives (`each` hands the thread's elements of batch v on)
@@ -449,34 +463,49 @@ __global__ void __launch_bounds__(kLpThreads + 32, kLpBlocksPerSM) k_lp_part(con
     return at < kLpCap;
   };
   if (lone >= bound && lone) push(lone);
-  // threads that may hold some: their elements, by the whole warp (a lane per
-  // vector), four threads' loads in flight
-  unsigned who = __ballot_sync(0xFFFFFFFFu, best >= bound && seen >= least && seen > -INFINITY);
+  // cells that may hold some (where their maximum is the bound's value, some id
+  // is before its), and then those cells' elements again, a vector per lane
+  const float reach = fmaxf(least, -3.402823466e38f);
+  uint16_t* list = sh.list[warp];
+  if (best >= bound && seen >= reach) {
+    const int last_id = bound ? (int)(0xFFFFFFFFu - (uint32_t)bound) : INT_MAX;
+    unsigned in = 0;
+    int id = head + (v0 + tid) * W;
+#pragma unroll
+    for (int c = 0; c < kLpCells; ++c, id += cell_len * kVecs * W) {
+      const float x = c < n_cells ? sh.cell[c][tid] : -INFINITY;
+      in |= (x > reach || (x == reach && id <= last_id)) << c;
+    }
+    int to = atomicAdd(&sh.n_list[warp], __popc(in));
+    for (; in; in &= in - 1) list[to++] = (uint16_t)((__ffs(in) - 1) * 32 + lane);
+  }
+  __syncwarp();
+  const unsigned per_cell = cell_len * Q, items = sh.n_list[warp] * per_cell;
+  const unsigned inverse = 0xFFFFFFFFu / per_cell + 1;  // i / per_cell = the product's high half: i per_cell < 2^32
 #pragma unroll 1
-  while (who) {
-    int from[4];
+  for (unsigned i0 = lane; i0 < items; i0 += 128) {
+    uint4 u4[4];
+    int at[4];
 #pragma unroll
     for (int c = 0; c < 4; ++c) {
-      from[c] = who ? v0 + (tid & ~31) + __ffs(who) - 1 : v1;
-      who &= who - 1;
+      const unsigned i = i0 + 32 * c, k = __umulhi(i, inverse);
+      at[c] = v1;
+      if (i < items) {
+        const int e = list[k];
+        at[c] = v0 + (e >> 5) * cell_len * kVecs + (int)(i - k * per_cell) * kLpThreads + (tid & ~31) + (e & 31);
+      }
+      if (at[c] < v1) u4[c] = __ldg(reinterpret_cast<const uint4*>(body) + at[c]);
     }
-#pragma unroll 1
-    for (int step = (tid & 31) * kLpThreads; v0 + step < v1; step += 32 * kLpThreads) {
-      uint4 u4[4];
 #pragma unroll
-      for (int c = 0; c < 4; ++c)
-        if (from[c] + step < v1) u4[c] = __ldg(reinterpret_cast<const uint4*>(body) + from[c] + step);
+    for (int c = 0; c < 4; ++c) {
+      if (at[c] >= v1) continue;
+      const uint32_t u[4] = {u4[c].x, u4[c].y, u4[c].z, u4[c].w};
 #pragma unroll
-      for (int c = 0; c < 4; ++c) {
-        if (from[c] + step >= v1) continue;
-        const uint32_t u[4] = {u4[c].x, u4[c].y, u4[c].z, u4[c].w};
-#pragma unroll
-        for (int e = 0; e < W; ++e) {
-          const float x = W == 8 ? ((e & 1) ? bf16hi(u[e / 2]) : bf16lo(u[e / 2])) : __uint_as_float(u[W == 8 ? 0 : e]);
-          if (x >= least && x > -INFINITY) {
-            const unsigned long long k = lp_key(x, head + (from[c] + step) * W + e);
-            if (k >= bound) push(k);
-          }
+      for (int e = 0; e < W; ++e) {
+        const float x = W == 8 ? ((e & 1) ? bf16hi(u[e / 2]) : bf16lo(u[e / 2])) : __uint_as_float(u[W == 8 ? 0 : e]);
+        if (x >= reach) {
+          const unsigned long long k = lp_key(x, head + at[c] * W + e);
+          if (k >= bound) push(k);
         }
       }
     }
@@ -533,8 +562,7 @@ __global__ void __launch_bounds__(kLpJoinThreads) k_lp_join(const __grid_constan
     s_bound = 1ull;
     s_n = 0;
   }
-  pdl_wait();
-  pdl_trigger();
+  pdl_wait();  // (no early trigger: the next call's blocks, four to an SM, would find less room beside these)
   __syncthreads();
   LpSum s{-INFINITY, 0.f, 0.f};
   int before = 0;
