@@ -10,11 +10,13 @@ namespace mtp {
 namespace {
 
 constexpr int kJoinThreads = 128;  // small blocks: most find nothing to do
+constexpr int kJoinFew = 4;        // parts that one warp joins by itself
 
 // Block (b, y): the query tile that block b of the attention began and did not
 // end; blocks b + 1 to `last` hold the rest of it. Row by row (y, y + gridDim.y,
 // ...): the parts' weights, one thread per part, then their sum, a group of
-// DH / 4 threads per part.
+// DH / 4 threads per part. A few parts (prompts: two) are a warp's work, four
+// rows at a time without barriers.
 template <int DH, int DT>
 __global__ void __launch_bounds__(kJoinThreads) k_q4_join(const __grid_constant__ Q4AttnArgs a, int RT) {
   constexpr int kG = kJoinThreads / (DH / 4);
@@ -29,15 +31,67 @@ __global__ void __launch_bounds__(kJoinThreads) k_q4_join(const __grid_constant_
   const int a0 = min(max(a.start[me.x], 0), a.tokens);
   const int n = min(max(a.start[me.x + 1], a0), a.tokens) - a0;
   const float up = pow2i(head_exp(a.v_exp, me.y));
+  // a part that saw nothing has m = -inf and the sum 0; one whose scores were
+  // all NaN has m = -inf and the sum NaN
+  auto at = [&](int p, int j) { return (long long)(2 * (b + p) + (p == 0)) * RT + j; };
+  auto weight = [](float2 ml, float m) { return ml.x == -INFINITY ? (ml.y == 0.f ? 0.f : 1.f) : exp2f(ml.x - m); };
+  auto place = [&](int f) { return (long long)(a0 + f / G) * a.n_q + me.y * G + f % G; };
+  if (parts <= kJoinFew) {
+    for (int j = blockIdx.y + gridDim.y * warp; j < RT; j += gridDim.y * (kJoinThreads / 32)) {
+      const int f = me.z * RT + j;
+      if (f >= n * G) return;
+      float2 ml[kJoinFew];
+      float4 v[kJoinFew][(DH + 127) / 128];
+#pragma unroll
+      for (int p = 0; p < kJoinFew; ++p) {
+        ml[p] = p < parts ? a.part_ml[at(p, j)] : make_float2(-INFINITY, 0.f);
+#pragma unroll
+        for (int i = 0; i < (DH + 127) / 128; ++i)
+          if (p < parts && lane < DH / 4) v[p][i] = reinterpret_cast<const float4*>(a.part_o + at(p, j) * DH)[32 * i + lane];
+      }
+      float m = ml[0].x, l = 0.f, w[kJoinFew];
+#pragma unroll
+      for (int p = 1; p < kJoinFew; ++p) m = fmaxf(m, ml[p].x);
+#pragma unroll
+      for (int p = 0; p < kJoinFew; ++p) {
+        w[p] = weight(ml[p], m);
+        l = fmaf(w[p], ml[p].y, l);
+      }
+      const float scale = l != 0.f ? up / l : 0.f;
+      const long long dst = place(f);
+#pragma unroll
+      for (int i = 0; i < (DH + 127) / 128; ++i) {
+        float4 o = make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll
+        for (int p = 0; p < kJoinFew; ++p)
+          if (w[p] != 0.f && p < parts) {
+            o.x = fmaf(w[p], v[p][i].x, o.x);
+            o.y = fmaf(w[p], v[p][i].y, o.y);
+            o.z = fmaf(w[p], v[p][i].z, o.z);
+            o.w = fmaf(w[p], v[p][i].w, o.w);
+          }
+        if (l == 0.f) o = make_float4(0.f, 0.f, 0.f, 0.f);
+        if (lane >= DH / 4) continue;
+        if (DT == MTP_DTYPE_F32) {
+          reinterpret_cast<float4*>(static_cast<float*>(a.out) + dst * DH)[32 * i + lane] =
+              make_float4(o.x * scale, o.y * scale, o.z * scale, o.w * scale);
+        } else {
+          uint2 u;
+          asm("cvt.rn.bf16x2.f32 %0, %1, %2;" : "=r"(u.x) : "f"(o.y * scale), "f"(o.x * scale));
+          asm("cvt.rn.bf16x2.f32 %0, %1, %2;" : "=r"(u.y) : "f"(o.w * scale), "f"(o.z * scale));
+          reinterpret_cast<uint2*>(static_cast<uint16_t*>(a.out) + dst * DH)[32 * i + lane] = u;
+        }
+      }
+      if (lane == 0 && a.lse) a.lse[dst] = l != 0.f ? (m + log2f(l)) * 0.693147181f : -INFINITY;
+    }
+    return;
+  }
   const int grp = tid / (DH / 4), d4 = tid % (DH / 4);
   for (int j = blockIdx.y; j < RT; j += gridDim.y) {
     const int f = me.z * RT + j;
     if (f >= n * G) return;
-    // a part that saw nothing has m = -inf and the sum 0; one whose scores were
-    // all NaN has m = -inf and the sum NaN
-    auto at = [&](int p) { return (long long)(2 * (b + p) + (p == 0)) * RT + j; };
     float m = -INFINITY;
-    for (int p = tid; p < parts; p += kJoinThreads) m = fmaxf(m, a.part_ml[at(p)].x);
+    for (int p = tid; p < parts; p += kJoinThreads) m = fmaxf(m, a.part_ml[at(p, j)].x);
     m = warp_max(m);
     __syncthreads();
     if (lane == 0) s_red[0][warp] = m;
@@ -48,8 +102,8 @@ __global__ void __launch_bounds__(kJoinThreads) k_q4_join(const __grid_constant_
     float4 o = make_float4(0.f, 0.f, 0.f, 0.f);
     for (int p0 = 0; p0 < parts; p0 += kJoinThreads) {
       if (p0 + tid < parts) {
-        const float2 ml = a.part_ml[at(p0 + tid)];
-        const float w = ml.x == -INFINITY ? (ml.y == 0.f ? 0.f : 1.f) : exp2f(ml.x - m);
+        const float2 ml = a.part_ml[at(p0 + tid, j)];
+        const float w = weight(ml, m);
         s_w[tid] = w;
         l = fmaf(w, ml.y, l);
       }
@@ -57,7 +111,7 @@ __global__ void __launch_bounds__(kJoinThreads) k_q4_join(const __grid_constant_
 #pragma unroll 8
       for (int p = grp; p < min(parts - p0, kJoinThreads); p += kG) {
         const float w = s_w[p];
-        const float4 v = reinterpret_cast<const float4*>(a.part_o + at(p0 + p) * DH)[d4];
+        const float4 v = reinterpret_cast<const float4*>(a.part_o + at(p0 + p, j) * DH)[d4];
         if (w != 0.f) {
           o.x = fmaf(w, v.x, o.x);
           o.y = fmaf(w, v.y, o.y);
@@ -74,7 +128,7 @@ __global__ void __launch_bounds__(kJoinThreads) k_q4_join(const __grid_constant_
     l = 0.f;
 #pragma unroll
     for (int w = 0; w < kJoinThreads / 32; ++w) l += s_red[1][w];
-    const long long dst = (long long)(a0 + f / G) * a.n_q + me.y * G + f % G;
+    const long long dst = place(f);
     for (int d = tid; d < DH; d += kJoinThreads) {
       float y = 0.f;
 #pragma unroll
@@ -147,7 +201,9 @@ mtp_status kv_q4_attend(mtp_stream stream, const kv_q4_cache* c, int32_t rows, i
       c->head_dim == 64    ? (wide ? k_q4_join<64, MTP_DTYPE_F32> : k_q4_join<64, MTP_DTYPE_BF16>)
       : c->head_dim == 128 ? (wide ? k_q4_join<128, MTP_DTYPE_F32> : k_q4_join<128, MTP_DTYPE_BF16>)
                            : (wide ? k_q4_join<256, MTP_DTYPE_F32> : k_q4_join<256, MTP_DTYPE_BF16>);
-  e = launch_pdl(join, dim3(blocks, std::min(rt, 32)), dim3(kJoinThreads), 0, s, a, rt);
+  // (rows of a query tile that are used, as far as the caller knows)
+  const int used = (int)std::min<long long>(std::min(rt, 32), (long long)max_q * (n_q / c->n_kv));
+  e = launch_pdl(join, dim3(blocks, used), dim3(kJoinThreads), 0, s, a, rt);
   count_launch();
   return e == cudaSuccess ? MTP_OK : MTP_ERR_CUDA;
 }
