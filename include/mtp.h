@@ -400,7 +400,7 @@ mtp_status kv_page_plan(mtp_stream stream, int32_t rows, int32_t page, int32_t m
  *       strides in elements (a slice of a fused q/k/v projection will do)
  *   d_slot [tokens]: kv_page_plan's; -1 skips the position, any other value
  *       outside [0, n_pages * page) skips it and sets 1 << MTP_ERR_BAD_ARG in
- *       d_status. Two positions with the same slot leave either's row.
+ *       d_status. Two positions with the same slot leave bytes of both.
  * Rounding, per 16 elements y = x * 2^-exp: scale = e4m3(max|y| / 6) (fp32
  * quotient, to nearest even, at most 448), code = the e2m1 value nearest to
  * |y| / scale (exact, the even code when two are as near, 6 beyond 6); a zero
@@ -438,7 +438,9 @@ mtp_status kv_q4_read(mtp_stream stream, const kv_q4_cache* cache, int32_t token
  * of 2^-31 of it.
  * A page entry outside [0, n_pages) sets 1 << MTP_ERR_BAD_ARG in d_status and
  * its positions are not read; a bounded wait that ran out sets
- * 1 << MTP_ERR_TIMEOUT. Errors: BAD_ARG.
+ * 1 << MTP_ERR_TIMEOUT. Errors: BAD_ARG (rows outside 1..4096, n_q above 1024 or
+ * no multiple of n_kv, tokens * n_q or max_pages * page of 2^31 and more, d_q not
+ * aligned to its type, d_out or d_workspace not to 16 bytes, a null pointer).
  */
 size_t kv_q4_attend_workspace_bytes(const kv_q4_cache* cache, int32_t n_q, int32_t max_q, int32_t dtype);
 mtp_status kv_q4_attend(mtp_stream stream, const kv_q4_cache* cache, int32_t rows, int32_t n_q, int32_t tokens,
@@ -465,8 +467,10 @@ mtp_status kv_q4_attend(mtp_stream stream, const kv_q4_cache* cache, int32_t row
  * Logits of -inf are masked tokens; a row with nothing else gives -inf (0 for
  * entropy). A NaN or +inf sets 1 << MTP_ERR_NONFINITE; the row's outputs then
  * carry no meaning, ids stay in range. d_workspace:
- * spec_logprobs_workspace_bytes(n, vocab, top) bytes, 16-byte aligned.
- * Errors: BAD_ARG.
+ * spec_logprobs_workspace_bytes(n, vocab, top) bytes, 16-byte aligned. A bounded
+ * wait that ran out sets 1 << MTP_ERR_TIMEOUT. Errors: BAD_ARG (n above 65535,
+ * vocab outside 1..2^20, top above 64, a row_stride below vocab, d_logits not
+ * aligned to its type, a null pointer).
  */
 size_t spec_logprobs_workspace_bytes(int32_t n, int32_t vocab, int32_t top);
 mtp_status spec_logprobs(mtp_stream stream, int32_t n, int32_t vocab, const void* d_logits, int64_t row_stride,

@@ -9,6 +9,7 @@ device tensors (PyTorch supplies device memory and streams only).
 from __future__ import annotations
 
 import ctypes
+import functools
 import os
 
 import numpy as np
@@ -374,6 +375,7 @@ class PagedCache:
     def __init__(self, c, keep):
         self.c = c
         self.ref = ctypes.byref(c)
+        self.n_kv, self.head_dim = c.n_kv, c.head_dim  # (a field of the structure costs 0.1 us a read)
         self._keep = keep
 
 
@@ -413,9 +415,8 @@ def _dtype_q4(where: str, *tensors) -> int:
 
 def kv_q4_append(cache: PagedCache, k, v, slot, status=None, stream=None):
     """k, v: [tokens, n_kv, head_dim], fp32 or bf16, the last dimension contiguous; slot [tokens] int32."""
-    c = cache.c
-    shape = (slot.numel(), c.n_kv, c.head_dim)
-    _want(tuple(k.shape) == shape and tuple(v.shape) == shape and k.stride(2) == 1 and v.stride(2) == 1, "kv_q4_append")
+    shape = (slot.numel(), cache.n_kv, cache.head_dim)
+    _want(k.shape == shape and v.shape == shape and k.stride(2) == 1 and v.stride(2) == 1, "kv_q4_append")
     _whole("kv_q4_append", slot)
     rc = lib().kv_q4_append(_stream(stream), cache.ref, shape[0], _ptr(k), k.stride(0), k.stride(1), _ptr(v), v.stride(0),
                             v.stride(1), _dtype_q4("kv_q4_append", k, v), _ptr(slot), _ptr(status))
@@ -424,19 +425,29 @@ def kv_q4_append(cache: PagedCache, k, v, slot, status=None, stream=None):
 
 def kv_q4_read(cache: PagedCache, slot, k, v, status=None, stream=None):
     """slot [tokens] int32; k, v: [tokens, n_kv, head_dim] out, contiguous, fp32 or bf16."""
-    c = cache.c
-    shape = (slot.numel(), c.n_kv, c.head_dim)
-    _want(tuple(k.shape) == shape and tuple(v.shape) == shape and k.is_contiguous() and v.is_contiguous(), "kv_q4_read")
+    shape = (slot.numel(), cache.n_kv, cache.head_dim)
+    _want(k.shape == shape and v.shape == shape and k.is_contiguous() and v.is_contiguous(), "kv_q4_read")
     _whole("kv_q4_read", slot)
     rc = lib().kv_q4_read(_stream(stream), cache.ref, shape[0], _ptr(slot), _ptr(k), _ptr(v),
                           _dtype_q4("kv_q4_read", k, v), _ptr(status))
     _check(rc, "kv_q4_read")
 
 
+@functools.lru_cache(maxsize=1024)
+def _attend_bytes(n_kv: int, head_dim: int, n_q: int, max_q: int, dt: int) -> int:
+    # a function of sizes alone, asked for by every call that checks its workspace
+    c = Q4Cache(None, None, None, None, n_kv, head_dim, 16, 1)
+    return lib().kv_q4_attend_workspace_bytes(ctypes.byref(c), n_q, max_q, dt)
+
+
+@functools.lru_cache(maxsize=1024)
+def _logprobs_bytes(n: int, vocab: int, top: int) -> int:
+    return lib().spec_logprobs_workspace_bytes(n, vocab, top)
+
+
 def kv_q4_attend_workspace_bytes(cache: PagedCache, n_q: int, max_q: int, dtype) -> int:
     """dtype: the queries' torch dtype."""
-    return lib().kv_q4_attend_workspace_bytes(cache.ref, n_q, max_q, MTP_DTYPE_BF16 if dtype is _t().bfloat16
-                                              else MTP_DTYPE_F32)
+    return _attend_bytes(cache.n_kv, cache.head_dim, n_q, max_q, MTP_DTYPE_BF16 if dtype is _t().bfloat16 else MTP_DTYPE_F32)
 
 
 def kv_q4_attend(cache: PagedCache, q, table, start, length, out, workspace, max_q: int, scale: float, window: int = 0,
@@ -446,14 +457,13 @@ def kv_q4_attend(cache: PagedCache, q, table, start, length, out, workspace, max
     kv_q4_attend_workspace_bytes(cache, n_q, max_q, q.dtype) bytes."""
     tokens, n_q, dh = q.shape
     rows, max_pages = table.shape
-    _want(dh == cache.c.head_dim and q.stride(2) == 1 and out.shape == q.shape and out.is_contiguous()
+    _want(dh == cache.head_dim and q.stride(2) == 1 and out.shape == q.shape and out.is_contiguous()
           and (lse is None or (lse.dtype is _t().float32 and lse.numel() == tokens * n_q and lse.is_contiguous())),
           "kv_q4_attend")
     _whole("kv_q4_attend", table, start, length)
     _want(start.numel() == rows + 1 and length.numel() == rows, "kv_q4_attend")
     dt = _dtype_q4("kv_q4_attend", q, out)
-    _want(workspace.numel() * workspace.element_size()
-          >= lib().kv_q4_attend_workspace_bytes(cache.ref, n_q, max_q, dt), "kv_q4_attend")
+    _want(workspace.nbytes >= _attend_bytes(cache.n_kv, dh, n_q, max_q, dt), "kv_q4_attend")
     rc = lib().kv_q4_attend(_stream(stream), cache.ref, rows, n_q, tokens, _ptr(q), q.stride(0), q.stride(1), dt,
                             _ptr(table), max_pages, _ptr(start), _ptr(length), max_q, scale, window, _ptr(out), _ptr(lse),
                             _ptr(status), _ptr(workspace))
@@ -478,8 +488,7 @@ def spec_logprobs(logits, tok, logprob, workspace, rank=None, entropy=None, top_
         if t is not None and (t.dtype is not f32 or not t.is_contiguous() or t.numel() != size):
             raise MTPError(9, "spec_logprobs")
     _want(logits.stride(1) == 1 and (top_id is None) == (top_lp is None)
-          and workspace.numel() * workspace.element_size() >= lib().spec_logprobs_workspace_bytes(n, V, top),
-          "spec_logprobs")
+          and workspace.nbytes >= _logprobs_bytes(n, V, top), "spec_logprobs")
     rc = lib().spec_logprobs(_stream(stream), n, V, _ptr(logits), logits.stride(0), _dtype_q4("spec_logprobs", logits),
                              _ptr(tok), top, _ptr(logprob), _ptr(rank), _ptr(entropy), _ptr(top_id), _ptr(top_lp),
                              _ptr(status), _ptr(workspace))
