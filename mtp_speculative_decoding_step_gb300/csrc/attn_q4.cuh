@@ -298,7 +298,7 @@ struct Shape {
   static_assert(VS >= 1 && KS <= kMost && VS <= kMost && KS + VS <= kRoom && cEnd <= 512 && (SG == 2 || (KS % 2 == 0 && VS % 2 == 0)), "shape");
 };
 
-constexpr int kRuns = 4;
+constexpr int kRuns = 8;
 
 // Small state of a block.
 template <int DH>
@@ -454,6 +454,7 @@ __global__ void __launch_bounds__(kAttnThreads, 1) k_q4_attn(const __grid_consta
   pdl_trigger();
 
   // the shares in turn: `next` waits for share `k` and hands it out, `done` gives its slot back
+  // (after the share, when the words that `next` loaded have all been used)
   auto next = [&](uint32_t k, Run& s) {
     if (!wait(&M.run_full[k % kRuns], (k / kRuns) & 1, fail)) return false;
     s = M.run[k % kRuns];
@@ -681,8 +682,6 @@ __global__ void __launch_bounds__(kAttnThreads, 1) k_q4_attn(const __grid_consta
       if (!ok) break;
       const int nt = __shfl_sync(0xFFFFFFFFu, M.run[k % kRuns].nt, 0);
       flags = __shfl_sync(0xFFFFFFFFu, M.run[k % kRuns].flags, 0);
-      if (lane == 0) done(k);
-      __syncwarp();
       if (nt == 0) break;
       // With two buffers S runs two tiles ahead of P.V: a tile's softmax has
       // the other tile's products to hide behind. (The softmax that fills P of
@@ -716,6 +715,8 @@ __global__ void __launch_bounds__(kAttnThreads, 1) k_q4_attn(const __grid_consta
         }
       }
       it += nt;
+      if (lane == 0) done(k);
+      __syncwarp();
     }
     if (!ok) {  // what was issued ends before its operands and tensor memory go
       mma_commit_elect(smem_u32(&M.drain));
@@ -768,8 +769,6 @@ __global__ void __launch_bounds__(kAttnThreads, 1) k_q4_attn(const __grid_consta
       const uint8_t* row = live ? base + S::oRawK + st * S::kRaw + tid * S::kRow : M.zero;
       uint32_t code[4 * kKC], sc[(kKC + 1) / 2];
       load_row(row, row + DH / 2, code, sc);
-      __syncwarp();
-      if (lane == 0) mbar_arrive(smem_u32(&M.rawk_empty[st]));
       if (round > 0 && !wait(&M.k_empty[b], (round - 1) & 1, fail)) return false;
       tc_fence_after();
 #pragma unroll
@@ -778,6 +777,10 @@ __global__ void __launch_bounds__(kAttnThreads, 1) k_q4_attn(const __grid_consta
         expand(code + 4 * c, sc[c / 2] >> (16 * (c & 1)), x);
         tmem_st_rows16(tmem + S::cK + b * S::KC + c * 16 + ((uint32_t)(32 * quarter) << 16), x);
       }
+      // (the stage goes back once its words have been used: an arrival right behind
+      // the loads does not wait for them, and a copy that hits L2 overtook them)
+      __syncwarp();
+      if (lane == 0) mbar_arrive(smem_u32(&M.rawk_empty[st]));
       tc_wait_st();
       tc_fence_before();
       __syncwarp();
@@ -798,10 +801,6 @@ __global__ void __launch_bounds__(kAttnThreads, 1) k_q4_attn(const __grid_consta
         const uint8_t* row = live ? base + S::oRawV + st * S::kRaw + tr * S::kRow : M.zero;
         uint32_t code[kD / 8], sc[(kD / 32 + 1) / 2];
         load_row(row + part * (kD / 2), row + DH / 2 + part * (kD / 16), code, sc);
-        if (h == 1) {
-          __syncwarp();
-          if (lane == 0) mbar_arrive(smem_u32(&M.rawv_empty[st]));
-        }
         const uint32_t vs = i % S::VB * 2 + h;
         if (i >= S::VB && !wait(&M.v_empty[(i - S::VB & 1) * 2 + h], (i - S::VB) / 2 & 1, fail)) return false;
         if (edge) {
@@ -833,6 +832,10 @@ __global__ void __launch_bounds__(kAttnThreads, 1) k_q4_attn(const __grid_consta
                          "r"(x[4 * w]), "r"(x[4 * w + 1]), "r"(x[4 * w + 2]), "r"(x[4 * w + 3])
                          : "memory");
         }
+        if (h == 1) {  // (as K's: after the words' last use)
+          __syncwarp();
+          if (lane == 0) mbar_arrive(smem_u32(&M.rawv_empty[st]));
+        }
         fence_async();
         __syncwarp();
         if (lane == 0) mbar_arrive(smem_u32(&M.v_full[vs]));
@@ -850,7 +853,6 @@ __global__ void __launch_bounds__(kAttnThreads, 1) k_q4_attn(const __grid_consta
       ok = next(k, s);
       __syncwarp();
       if (!ok) break;
-      if (lane == 0) done(k);
 #pragma unroll 1
       for (int i = 0; i <= s.nt && ok; ++i) {
         const bool flush = i == s.nt;  // after the last tile, its V
@@ -866,6 +868,8 @@ __global__ void __launch_bounds__(kAttnThreads, 1) k_q4_attn(const __grid_consta
         iv = it;
         it += !flush;
       }
+      if (lane == 0) done(k);
+      __syncwarp();
     }
   } else if (warp >= kSoftWarp) {
     // ---------------------------------------------------------- softmax
@@ -883,7 +887,6 @@ __global__ void __launch_bounds__(kAttnThreads, 1) k_q4_attn(const __grid_consta
     for (; !(s.flags & 4); ++run) {
       ok = next(run, s);
       if (group_any(bar, !ok)) break;
-      if (lane == 0) done(run);
       if (s.nt == 0) break;
       const int nt = s.nt;
       const bool begins = s.flags & 1, ends = s.flags & 2;
@@ -1226,6 +1229,7 @@ __global__ void __launch_bounds__(kAttnThreads, 1) k_q4_attn(const __grid_consta
       }
       tc_fence_before();
       group_sync(bar);
+      if (lane == 0) done(run);
     }
   }
 
