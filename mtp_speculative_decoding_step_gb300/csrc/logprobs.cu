@@ -344,12 +344,6 @@ __global__ void __launch_bounds__(kLpThreads + 32, kLpBlocksPerSM) k_lp_part(con
     uint4 w[Q];
 #pragma unroll
     for (int q = 0; q < Q; ++q) w[q] = reinterpret_cast<const uint4*>(sh.ring[st])[q * kLpThreads + tid];
-    __syncwarp();
-    if ((tid & 31) == 0) mbar_arrive(smem_u32(&sh.empty[st]));
-    if (++st == kLpStages) {
-      st = 0;
-      phase ^= 1;
-    }
     if (!whole) {
 #pragma unroll
       for (int q = 0; q < Q; ++q)
@@ -371,7 +365,16 @@ __global__ void __launch_bounds__(kLpThreads + 32, kLpBlocksPerSM) k_lp_part(con
       for (int e = 1; e < W; ++e) most[q] = fmaxf(most[q], elem(q, e));
       top = fmaxf(top, most[q]);
     }
-    if (top > seen) {
+    // The stage goes back by the lane that the vote names: it hangs on every word
+    // loaded. (An arrival right behind the loads does not wait for them, and the
+    // next copy could overtake them.)
+    const bool higher = top > seen;
+    if ((tid & 31) == (__any_sync(0xFFFFFFFFu, higher) ? 0 : 1)) mbar_arrive(smem_u32(&sh.empty[st]));
+    if (++st == kLpStages) {
+      st = 0;
+      phase ^= 1;
+    }
+    if (higher) {
       seen = top;
 #pragma unroll
       for (int q = Q - 1; q >= 0; --q)
