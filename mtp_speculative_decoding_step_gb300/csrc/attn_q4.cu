@@ -143,7 +143,10 @@ __global__ void __launch_bounds__(kJoinThreads) k_q4_join(const __grid_constant_
 // Columns of the products: the query rows of a position block on one KV head,
 // twice for fp32 queries, rounded up to 16, 32, 64 or 128 (fp32: 64). A wider
 // tile than its rows fill costs MMA and softmax time, a narrower one reads and
-// dequantises the cache again for every further tile. WIDTHS
+// dequantises the cache again for every further tile. Times in us with 16, 32,
+// 64 and 128 columns: 18 rows of one sequence 17.0, 15.0, 17.4, 19.5; 24 of
+// eight 55.7, 38.2, 46.6, 58.7; 4 of 64 63.8, 71.3, 92.8, 114.5; 9000 and 12288
+// (prompts) 2784, 1529, 982, 711.
 int columns(int n_q, int n_kv, int max_q, bool wide) {
   const long long rows = (long long)max_q * (n_q / n_kv) * (wide ? 2 : 1);
   return rows <= 16 ? 16 : (rows <= 32 ? 32 : (rows <= 64 || wide ? 64 : 128));

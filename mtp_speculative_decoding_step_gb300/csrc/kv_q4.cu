@@ -10,6 +10,7 @@
 //     correctly rounded quotient q = y r + (y - (y r) b) r, r = 1 / b (one
 //     Newton step on the product) is on a border exactly where y is, and the
 //     conversion instruction's rounding to nearest even is the definition's.
+//     (By comparisons as fp32, the prompt below took 63 us instead of 39.)
 //
 // One thread per 16 elements: its loads are one or two sectors, its eight code
 // bytes and one scale byte lie next to its neighbours'. A bf16 value is 2 bytes

@@ -16,9 +16,10 @@
 // anywhere.
 // k_lp_join: a block per row adds up the parts and merges their lists.
 //
-// Bound by issue and, at a part's end, by latency: 14 instructions an element
-// (one an exponential, at 16 a cycle and SM), then some 8,000 cycles for the
-// alternatives, which four blocks an SM hide only in part. 256 rows of 152,064
+// Bound by issue (70 % of its rate: 23 instructions an element, the
+// alternatives' included, one an exponential at 16 a cycle and SM) and, at a
+// part's end, by latency: some 8,000 cycles for the alternatives, which four
+// blocks an SM hide only in part. 256 rows of 152,064
 // fp32 logits with 20 alternatives: 42 us, 3.7 TB/s; without any 37 us; 1001
 // rows of 32,769 bf16 logits with 8: 33 us; 3 rows of 152,064 with 5: 10 us.
 // One block per SM slot for all its rows' parts (copies running on into the
@@ -694,7 +695,8 @@ __global__ void __launch_bounds__(kLpJoinThreads) k_lp_join(const __grid_constan
 
 // Parts per row: the count with the least (waves of resident blocks) x (a
 // part's elements + a block's fixed cost, counted in elements), the join's cost
-// per part added. Many rows: whole waves; few rows: short parts.
+// per part added. Many rows: whole waves; few rows: short parts. (256 rows of
+// 152,064: 2 parts 43 us, 7 parts 54.)
 int lp_parts(int n, int V) {
   const long long slots = (long long)kLpBlocksPerSM * device_sm_count();
   const int most = std::min(kLpMaxParts, std::max(1, V / 2048));
