@@ -332,7 +332,7 @@ __global__ void __launch_bounds__(kLpThreads + 32, kLpBlocksPerSM) k_lp_part(con
 
   float seen = -INFINITY;  // the largest of the vectors, and the first one that had it
   int seen_at = v0;
-  const int cell_len = ((v1 - v0 + kVecs - 1) / kVecs + kLpCells - 1) / kLpCells;  // batches of a cell
+  const int cell_len = max(1, ((v1 - v0 + kVecs - 1) / kVecs + kLpCells - 1) / kLpCells);  // batches of a cell
   int cell_at = 0, n_cells = 0;
   float cell_max = -INFINITY;
   uint64_t S2 = 0, T2 = 0;  // even and odd elements' sums
