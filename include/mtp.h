@@ -436,6 +436,8 @@ mtp_status kv_q4_read(mtp_stream stream, const kv_q4_cache* cache, int32_t token
  * fp32 q as two f16 parts (22 bits). The softmax weights are f16 (11 bits;
  * fp32 q: two parts, 22 bits) down to 2^-21 of the largest, below that in steps
  * of 2^-31 of it.
+ * The tensor core's sums drop the bits past fp32's: over the 1024 (fp32 q) or
+ * 16,384 positions at most that it sums up at a time, 4e-6 or 7e-5 of the sum.
  * A page entry outside [0, n_pages) sets 1 << MTP_ERR_BAD_ARG in d_status and
  * its positions are not read; a bounded wait that ran out sets
  * 1 << MTP_ERR_TIMEOUT. Errors: BAD_ARG (rows outside 1..4096, n_q above 1024 or

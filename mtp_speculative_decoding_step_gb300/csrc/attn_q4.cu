@@ -165,7 +165,8 @@ size_t kv_q4_attend_workspace_bytes(const kv_q4_cache* c, int32_t n_q, int32_t m
     return 0;
   const bool wide = dtype == MTP_DTYPE_F32;
   const size_t rt = (size_t)columns(n_q, c->n_kv, max_q, wide) / (wide ? 2 : 1), slots = 2 * (size_t)device_sm_count();
-  return slots * (sizeof(int4) + rt * (sizeof(float2) + sizeof(float) * c->head_dim));
+  // (the parts' O and, for long shares, one more per block)
+  return slots * (sizeof(int4) + rt * sizeof(float2)) + slots / 2 * 3 * rt * sizeof(float) * c->head_dim;
 }
 
 mtp_status kv_q4_attend(mtp_stream stream, const kv_q4_cache* c, int32_t rows, int32_t n_q, int32_t tokens,
@@ -190,9 +191,10 @@ mtp_status kv_q4_attend(mtp_stream stream, const kv_q4_cache* c, int32_t rows, i
   w += sizeof(int4) * 2 * blocks;
   float2* ml = reinterpret_cast<float2*>(w);
   w += sizeof(float2) * 2 * blocks * rt;
+  float* part_o = reinterpret_cast<float*>(w);
   Q4AttnArgs a{static_cast<const uint8_t*>(c->k), static_cast<const uint8_t*>(c->v), c->k_exp, c->v_exp, d_table,
                d_start, d_len, d_q, tok_stride, head_stride, d_out, d_lse, d_status, meta, ml,
-               reinterpret_cast<float*>(w), rows, n_q, c->n_kv, c->page, c->n_pages, max_pages, tokens, window, 0,
+               part_o, part_o + (size_t)2 * blocks * rt * c->head_dim, rows, n_q, c->n_kv, c->page, c->n_pages, max_pages, tokens, window, 0,
                scale};
   const uintptr_t bits = reinterpret_cast<uintptr_t>(d_q) | (uintptr_t)(tok_stride * es) | (uintptr_t)(head_stride * es);
   a.q_vec = (bits & 15) == 0;

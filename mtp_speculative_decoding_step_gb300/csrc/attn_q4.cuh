@@ -79,6 +79,7 @@ struct Q4AttnArgs {
   int4* part_meta;               // [2 * blocks] (row, head, query tile, block that ends it; -1 if it began elsewhere; 0 if none)
   float2* part_ml;               // [2 * blocks][rows of a tile] (m, sum)
   float* part_o;                 // [2 * blocks][rows of a tile][DH]
+  float* far_o;                  // [blocks][rows of a tile][DH]: O of a long share's tiles before the last kFar
   int rows, n_q, n_kv, page, n_pages, max_pages, tokens, window;
   int q_vec;                     // 16-byte loads of q are aligned
   float scale;
@@ -276,6 +277,11 @@ struct Shape {
   static constexpr int SG = N == 128 ? 2 : 1;            // softmax warpgroups
   static constexpr int NW = N / SG;                      // columns per softmax warpgroup
   static constexpr int NC = WIDE ? NW / 2 : NW;          // query rows per softmax warpgroup
+  // The tensor core's accumulation drops the bits past fp32's, 5e-7 of a sum per
+  // tile: after kFar tiles O moves to memory, where it is added with rounding. (2e-6
+  // of fp32 outputs are left then, 9e-5 of bf16's, whose own step is 40 times that;
+  // a row of 131,072 positions summed by one block had lost 8e-4.)
+  static constexpr int kFar = WIDE ? 8 : 128;
   static constexpr int MB = DH == 256 ? 2 : 1;           // M blocks of O^T (64 dims: duplicated rows)
   static constexpr int KC = DH / 2;                      // tensor-memory columns of a K operand
   static constexpr int SB = MB * N + 2 * N + 2 * KC <= 512 ? 2 : 1;  // S and K buffers
@@ -285,7 +291,7 @@ struct Shape {
   static constexpr int kRaw = kT * kRow;                 // a tile's rows of K or V
   static constexpr int VB = DH == 256 ? 1 : 2;           // V tiles in shared memory
   static constexpr int kV = kT * DH * 2, kQ = N * DH * 2, kP = N * kT * 2;  // (SB buffers of P)
-  static constexpr int kMetaBytes = 8192;
+  static constexpr int kMetaBytes = 8704;
   static constexpr int kRoom = (227 * 1024 - kMetaBytes - VB * kV - kQ - SB * kP) / kRaw;
   // ring stages; even counts for two dequantising groups, so that each group
   // meets every phase of its stages' barriers
@@ -315,6 +321,7 @@ struct Meta {
   Run run[kRuns];                    // the shares, written by one warp ahead of the other roles
   alignas(16) float cm[128][2];      // per query row: c, m
   float f[128];                      // per query row: factor of a moved m, then 1 / sum
+  float far[128];                    // per query row: the m of what is in far_o
   alignas(16) int lim[128];          // per query row: its position
   int dst[128];                      // per query row: row of out and lse, or -1
   float red[4][128];                 // per warp of a softmax group and query row
@@ -324,7 +331,7 @@ struct Meta {
   uint32_t nan_run[2];               // by the run's parity: 1 + the last run that noted something in nan_bits
   uint32_t nan_bits[2][4][DH / 16][4];  // edge tile, 16 dimensions: positions whose V is NaN there
 };
-static_assert(sizeof(Meta<256>) <= 8192, "meta");
+static_assert(sizeof(Meta<256>) <= 8704, "meta");
 
 __device__ __forceinline__ __half2 as_half2(uint32_t u) { return *reinterpret_cast<const __half2*>(&u); }
 __device__ __forceinline__ uint32_t as_bits(__half2 h) { return *reinterpret_cast<const uint32_t*>(&h); }
@@ -394,6 +401,54 @@ __device__ __noinline__ bool sees_nan(int first, int t0, int cnt, int p0, int p1
     }
   }
   return false;
+}
+
+// A softmax group's O of the tiles since the last call, added to what far_o has
+// of those before (`first`: nothing), or back from there at the share's `end`.
+// Out of line with all its addresses: few shares come here, and the loop over
+// tiles needs the registers (with them inside, prompts took 760 us, not 713).
+template <int DH, int N, bool WIDE>
+__device__ __noinline__ void add_far(const Q4AttnArgs* a, Meta<DH>* M, int sg, bool first, bool end) {
+  using S = Shape<DH, N, WIDE>;
+  const int me = threadIdx.x & 127, quarter = me >> 5, c0 = sg * S::NC;
+  if (me < S::NC) {
+    const int col = c0 + me;
+    const float was = M->far[col], m = M->cm[col][1];
+    M->f[col] = first ? 0.f : (was == m ? 1.f : (was == kUnset ? 0.f : ex2(was - m)));
+    M->far[col] = m;
+  }
+  group_sync(1 + sg);
+  if (DH == 64 && quarter >= 2) return;  // (duplicated rows)
+  const uint32_t t0 = M->tmem + S::cO + c0 + ((uint32_t)(32 * quarter) << 16);
+  float* p0 = a->far_o + ((long long)blockIdx.x * S::RT + c0) * DH + me;
+#pragma unroll 1
+  for (int mb = 0; mb < S::MB; ++mb)
+#pragma unroll 1
+    for (int c = 0; c < S::NC; c += 8) {
+      const uint32_t t = t0 + mb * N + c;
+      float* p = p0 + c * DH + mb * 128;
+      float o[8];
+      tc::tmem_ld8(t, o);
+      if (WIDE && !end) {
+        float o2[8];
+        tc::tmem_ld8(t + N / 2, o2);
+#pragma unroll
+        for (int e = 0; e < 8; ++e) o[e] += o2[e];
+      }
+#pragma unroll
+      for (int e = 0; e < 8; ++e)
+        if (!first) o[e] = fmaf(p[e * DH], M->f[c0 + c + e], o[e]);
+      if (end) {
+        asm volatile("tcgen05.st.sync.aligned.32x32b.x8.b32 [%8], {%0,%1,%2,%3,%4,%5,%6,%7};" ::"r"(__float_as_uint(o[0])),
+                     "r"(__float_as_uint(o[1])), "r"(__float_as_uint(o[2])), "r"(__float_as_uint(o[3])),
+                     "r"(__float_as_uint(o[4])), "r"(__float_as_uint(o[5])), "r"(__float_as_uint(o[6])),
+                     "r"(__float_as_uint(o[7])), "r"(t));
+      } else {
+#pragma unroll
+        for (int e = 0; e < 8; ++e) p[e * DH] = o[e];
+      }
+    }
+  if (end) tc_wait_st();
 }
 
 template <int DH, int N, bool WIDE>
@@ -707,7 +762,7 @@ __global__ void __launch_bounds__(kAttnThreads, 1) k_q4_attn(const __grid_consta
           if (!ok) break;
           issue_s(n);
         }
-        ok = wait(&M.p_full[t % S::SB], t / S::SB & 1, fail) && issue_pv(t, i == 0);
+        ok = wait(&M.p_full[t % S::SB], t / S::SB & 1, fail) && issue_pv(t, i % S::kFar == 0);
         if (S::SB == 2 && more && ok) {
           ok = wait(&M.k_full[n % S::SB], n / S::SB & 1, fail);
           tc_fence_after();
@@ -974,6 +1029,12 @@ __global__ void __launch_bounds__(kAttnThreads, 1) k_q4_attn(const __grid_consta
 
       bool broken = false;
       for (int i = 0; i < nt; ++i, ++it) {
+        if (i > 0 && i % S::kFar == 0) {  // the tiles before: P.V of tile i starts O anew
+          ok = wait(&M.p_empty[(it - 1) % S::SB], (it - 1) / S::SB & 1, fail) && ok;
+          if (group_any(bar, !ok)) { broken = true; break; }
+          tc_fence_after();
+          add_far<DH, N, WIDE>(&a, &M, sg, i == S::kFar, false);
+        }
         const uint32_t sb = it % S::SB;
         ok = wait(&M.s_full[sb], (it / S::SB) & 1, fail) && ok;
         tc_fence_after();
@@ -1156,6 +1217,7 @@ __global__ void __launch_bounds__(kAttnThreads, 1) k_q4_attn(const __grid_consta
       ok = wait(&M.p_empty[(it - 1) % S::SB], (it - 1) / S::SB & 1, fail) && ok;
       if (group_any(bar, !ok)) break;
       tc_fence_after();
+      if (nt > S::kFar) add_far<DH, N, WIDE>(&a, &M, sg, false, true);
 #pragma unroll
       for (int b = 0; b < 2 * NB; ++b) {
         float y = sum[b];

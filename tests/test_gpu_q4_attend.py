@@ -299,3 +299,34 @@ def test_a_repeated_call_gives_the_same_bits(nq, nkv, dh, page, hint, dtype):
     first = call(c, 1 / math.sqrt(dh), max_q=hint)
     for i, (out, lse) in enumerate(outs):
         assert torch.equal(lse.cpu(), first[1]) and torch.equal(out.cpu(), first[0]), i
+
+
+@pytest.mark.parametrize("dtype,times", [(torch.float32, 1), (torch.float32, 16), (torch.bfloat16, 16)])
+@pytest.mark.parametrize("nq,nkv,dh", HEADS)
+def test_long_sums_stay_accurate(nq, nkv, dh, dtype, times):
+    """A block sums thousands of positions of positive values by itself (152 rows), the same pages over and over, so
+    that the result is that of one turn. The bound on an element: as `check`'s, with a sum over the tiles
+    of a share that loses at most 8 steps of 2^-23 a tile for 8 (fp32) or 128 (bf16) tiles and half a step of
+    2^-24 for every 8 or 128 tiles after that."""
+    page, n_pages, rows = 128, 24, 152
+    g = torch.Generator().manual_seed(dh)
+    kc, vc = (q4_ref.quantize(x)[0].reshape(n_pages, nkv, page, -1) for x in (
+        torch.randn((n_pages * nkv, page, dh), generator=g), torch.randn((n_pages * nkv, page, dh), generator=g).abs()))
+    q = torch.randn((3, nq, dh), generator=g).to(dtype)
+    c = dict(kc=kc, vc=vc, table=[list(range(n_pages))] * 3, start=[0, 1, 2, 3], length=[n_pages * page] * 3, q=q, k_exp=None, v_exp=None)
+    scale = 1 / math.sqrt(dh)
+    ref, rlse, spread, reach, _ = q4_ref.attend(q.double(), kc, vc, c["table"], c["start"], c["length"], scale, 0, None, None)
+    c.update(table=[list(range(n_pages)) * times] * rows, start=list(range(rows + 1)), length=[n_pages * page * times] * rows,
+             q=q.repeat(51, 1, 1)[:rows])
+    out, lse, status = call(c, scale)
+    assert status == 0
+    wide = dtype == torch.float32
+    far, tiles = (8, n_pages * times) if wide else (128, n_pages * times)
+    lost = 8 * min(far, tiles) * 2.0 ** -23 + tiles / far * 2.0 ** -24
+    d = ((2.0 ** -21 if wide else 2.0 ** -16) + dh * 2.0 ** -24) * reach
+    rel = 2 * d + 2.0 ** -21 + (2.0 ** -22 if wide else 2.0 ** -11)
+    tol = ref.abs() * (2.0 ** -24 if wide else 2.0 ** -8) + (rel[..., None] + lost) * spread * (1 + 2.0 ** -8)
+    ltol = d + 2.0 ** -20 + (rlse.abs() + math.log(times)) * 2.0 ** -23 + tiles * 2.0 ** -24
+    for r in range(rows):
+        assert ((out[r].double() - ref[r % 3]).abs() <= tol[r % 3]).all(), r
+        assert ((lse[r].double() - rlse[r % 3] - math.log(times)).abs() <= ltol[r % 3]).all(), r
