@@ -34,7 +34,7 @@
 // within 2^21 of the largest to 11 bits.
 //
 // What bounds it, and what it measured (24 query heads on 4 KV heads of 256):
-//   prompts (two rows of 1500 and 2048 queries near 8192): 690 us, 950 TFLOP/s,
+//   prompts (two rows of 1500 and 2048 queries near 8192): 690 us, 945 TFLOP/s,
 //     the tensor pipe active 47 %; the dequantising group (one beside the 128
 //     columns' softmax) and the softmax share the issue slots
 //   8 rows of 4 queries, 1k to 16k positions: 38 us, 2.3 TB/s. A tile takes 2450
