@@ -523,7 +523,9 @@ __global__ void __launch_bounds__(kAttnThreads, 1) k_q4_attn(const __grid_consta
     // owns an equal stretch of them. The rows' task counts are scanned, rows
     // in consecutive groups per lane.
     const Walk walk{&a, a.n_q / a.n_kv, S::RT};
-    if (lane < 2) a.part_meta[2 * blockIdx.x + lane] = make_int4(0, 0, 0, 0);
+    // (by the lane that hands out the shares, so that its arrival orders these
+    // stores before those of the warps that take a share)
+    if (lane == 0) a.part_meta[2 * blockIdx.x] = a.part_meta[2 * blockIdx.x + 1] = make_int4(0, 0, 0, 0);
     const int per = (a.rows + 31) / 32, r0 = min(lane * per, a.rows), r1 = min(r0 + per, a.rows);
     long long sum = 0;
     int a0 = 0, n = 0, L = 0, ph = 0;
