@@ -115,9 +115,9 @@ struct Walk {
   int G, RT;       // query heads per KV head, query rows per tile
 
   __device__ void row(int r, int& a0, int& n, int& L) const {
-    a0 = min(max(__ldg(a->start + r), 0), a->tokens);
-    n = min(max(__ldg(a->start + r + 1), a0), a->tokens) - a0;
-    L = min(max(__ldg(a->len + r), 0), a->max_pages * a->page);
+    a0 = min(max(a->start[r], 0), a->tokens);
+    n = min(max(a->start[r + 1], a0), a->tokens) - a0;
+    L = min(max(a->len[r], 0), a->max_pages * a->page);
   }
   __device__ int tiles(int n) const { return (n * G + RT - 1) / RT; }
   __device__ void span(int n, int L, int j, int& lo, int& end, int& t0, int& cnt) const {
@@ -659,7 +659,7 @@ __global__ void __launch_bounds__(kAttnThreads, 1) k_q4_attn(const __grid_consta
       auto places = [&](int g) {
         const int q = 4 * g + (lane >> 3), p0 = (lane & 7) * ps, t0 = (s.tile + q) * kT + p0;
         if (p0 >= kT || q >= s.nt || t0 >= s.end || t0 + ps <= s.lo) return -1LL;
-        const int page = t0 / a.page, id = __ldg(tab + page);
+        const int page = t0 / a.page, id = tab[page];
         if (id >= 0 && id < a.n_pages) return (((long long)id * a.n_kv + s.g) * a.page + (t0 - page * a.page)) * S::kRow;
         flag_status(a.status, MTP_ERR_BAD_ARG);
         return -1LL;

@@ -38,6 +38,17 @@ __device__ __forceinline__ uint4 ldg_stream(const void* p) {
   return r;
 }
 
+// The same for data that an earlier kernel of a chain with programmatic
+// serialisation may still be writing when this one starts: not the read-only
+// path, whose data has to stay as it is while the kernel runs. After pdl_wait.
+__device__ __forceinline__ uint4 ld_stream(const void* p) {
+  uint4 r;
+  asm volatile("ld.global.L1::no_allocate.v4.u32 {%0,%1,%2,%3}, [%4];"
+               : "=r"(r.x), "=r"(r.y), "=r"(r.z), "=r"(r.w)
+               : "l"(p));
+  return r;
+}
+
 // Store with release semantics at system scope: writes ordered before it (by
 // this thread, or by threads synchronised with it) are visible to the host
 // before the stored value is.

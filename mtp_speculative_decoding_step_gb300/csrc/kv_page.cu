@@ -52,7 +52,7 @@ struct PlanRow {
 __device__ __forceinline__ PlanRow plan_row(const PlanArgs& a, int r) {
   PlanRow p;
   const unsigned cap = (unsigned)a.page * a.max_pages, page = a.page;
-  const int c = __ldg(a.cover + r), k = __ldg(a.keep + r), n = __ldg(a.fresh + r);
+  const int c = a.cover[r], k = a.keep[r], n = a.fresh[r];
   const unsigned cc = min((unsigned)max(c, 0), cap), total = (unsigned)k + (unsigned)n;
   p.held = (int)((cc + page - 1) / page);
   p.keep = k;
@@ -198,7 +198,7 @@ __global__ void __launch_bounds__(kPlanThreads) k_page_plan(const PlanArgs a) {
     if (k < sum_rel) {
       const int r = last_le(s_rel, a.rows, k);
       // (a row that gives pages back is not refused)
-      const int want = (s_keep[r] + __ldg(a.fresh + r) + a.page - 1) / a.page;
+      const int want = (s_keep[r] + a.fresh[r] + a.page - 1) / a.page;
       return checked(a.table[(long long)r * a.max_pages + want + (k - s_rel[r])]);
     }
     return checked(a.free_pages[top - 1 - k]);

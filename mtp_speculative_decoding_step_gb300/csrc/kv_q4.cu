@@ -48,7 +48,7 @@ __device__ __forceinline__ void load16(const void* src, long long at, bool vec, 
     if (vec) {
 #pragma unroll
       for (int i = 0; i < 2; ++i) {
-        const uint4 w = ldg_stream(p + 8 * i);
+        const uint4 w = ld_stream(p + 8 * i);
         const uint32_t u[4] = {w.x, w.y, w.z, w.w};
 #pragma unroll
         for (int j = 0; j < 4; ++j) {
@@ -65,7 +65,7 @@ __device__ __forceinline__ void load16(const void* src, long long at, bool vec, 
     if (vec) {
 #pragma unroll
       for (int i = 0; i < 4; ++i) {
-        const uint4 w = ldg_stream(p + 4 * i);
+        const uint4 w = ld_stream(p + 4 * i);
         x[4 * i] = __uint_as_float(w.x);
         x[4 * i + 1] = __uint_as_float(w.y);
         x[4 * i + 2] = __uint_as_float(w.z);

@@ -448,7 +448,7 @@ __global__ void __launch_bounds__(kLpThreads + 32, kLpBlocksPerSM) k_lp_part(con
     for (int q = 0; q < Q; ++q) {
       const int i = v + q * kLpThreads + tid;
       if (i >= v1) continue;
-      const uint4 u4 = __ldg(reinterpret_cast<const uint4*>(body) + i);
+      const uint4 u4 = reinterpret_cast<const uint4*>(body)[i];
       const uint32_t u[4] = {u4.x, u4.y, u4.z, u4.w};
 #pragma unroll
       for (int e = 0; e < W; ++e)
@@ -498,7 +498,7 @@ __global__ void __launch_bounds__(kLpThreads + 32, kLpBlocksPerSM) k_lp_part(con
         const int e = list[k];
         at[c] = v0 + (e >> 5) * cell_len * kVecs + (int)(i - k * per_cell) * kLpThreads + (tid & ~31) + (e & 31);
       }
-      if (at[c] < v1) u4[c] = __ldg(reinterpret_cast<const uint4*>(body) + at[c]);
+      if (at[c] < v1) u4[c] = reinterpret_cast<const uint4*>(body)[at[c]];
     }
 #pragma unroll
     for (int c = 0; c < 4; ++c) {

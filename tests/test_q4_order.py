@@ -21,3 +21,14 @@ def test_partial_results_are_cleared_by_the_lane_that_hands_out_shares():
     shares = src[src.index("part_meta[2 * blockIdx.x"):]
     gives = re.findall(r"if \(([^)]*lane == 0)\) \{[^}]*mbar_arrive\(smem_u32\(&M\.run_full", shares)
     assert gives == ["left == 0 && lane == 0", "lane == 0"]
+
+
+def test_no_read_only_loads_in_kernels_that_start_before_their_predecessor_ends():
+    """These kernels are launched with programmatic serialisation: what they read (tables, lengths, K and V, logits) may
+    still be written between their start and griddepcontrol.wait. A load through the read-only path (ld.global.nc) is for
+    data that does not change while the kernel runs, and may be moved to before the wait."""
+    for name in ("kv_page.cu", "kv_q4.cu", "q4.cuh", "attn_q4.cu", "attn_q4.cuh", "logprobs.cu"):
+        assert not re.findall(r"__ldg|ldg_stream|global\.nc|__restrict__", source(name)), name
+    common = source("common.cuh")
+    body = common[common.index("uint4 ld_stream("):]
+    assert "ld.global.L1::no_allocate" in body[:body.index("}\n")]
