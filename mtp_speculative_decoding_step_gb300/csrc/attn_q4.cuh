@@ -328,8 +328,14 @@ struct Meta {
   alignas(16) uint8_t zero[144];     // a row of zeros, read in the place of positions out of sight
   uint32_t copied[2];                // tiles of K and of V whose copies were issued
   uint64_t drain;                    // the MMAs of a run that gave up
-  uint32_t nan_run[2];               // by the run's parity: 1 + the last run that noted something in nan_bits
-  uint32_t nan_bits[2][4][DH / 16][4];  // edge tile, 16 dimensions: positions whose V is NaN there
+  // Notes of NaN in V, in sets that the shares use in turn. V of a tile waits for
+  // the products of the tile as many before it as there are V buffers; shares
+  // have one tile at least, and those products wait for the softmax to have
+  // begun on their share. So a share's notes are still being read while V of the
+  // next one (one buffer) or of the next two is expanded, and no longer.
+  static constexpr int kNotes = Shape<DH, 16, false>::VB + 1;
+  uint32_t nan_run[kNotes];             // 1 + the last run that noted something in the set
+  uint32_t nan_bits[kNotes][4][DH / 16][4];  // edge tile, 16 dimensions: positions whose V is NaN there
 };
 static_assert(sizeof(Meta<256>) <= 8704, "meta");
 
@@ -484,7 +490,7 @@ __global__ void __launch_bounds__(kAttnThreads, 1) k_q4_attn(const __grid_consta
     mbar_init(smem_u32(&M.q_full), kSoftWarps);
     M.fail = 0;
     M.copied[0] = M.copied[1] = 0;
-    M.nan_run[0] = M.nan_run[1] = 0;
+    for (int i = 0; i < Meta<DH>::kNotes; ++i) M.nan_run[i] = 0;
     mbar_init(smem_u32(&M.drain), 1);
     for (int i = 0; i < kRuns; ++i) {
       mbar_init(smem_u32(&M.run_full[i]), 1);
@@ -861,9 +867,9 @@ __global__ void __launch_bounds__(kAttnThreads, 1) k_q4_attn(const __grid_consta
         const uint32_t vs = i % S::VB * 2 + h;
         if (i >= S::VB && !wait(&M.v_empty[(i - S::VB & 1) * 2 + h], (i - S::VB) / 2 & 1, fail)) return false;
         if (edge) {
-          // (the words hold an older share's notes, whose reader is done: the
-          // products of the share between are)
-          auto& notes = M.nan_bits[run & 1][sg.edge_index(tile)];
+          // (the words hold the notes of a share whose reader is done: see kNotes)
+          const uint32_t set = run % Meta<DH>::kNotes;
+          auto& notes = M.nan_bits[set][sg.edge_index(tile)];
           if (lane < kD / 16) notes[part * (kD / 16) + lane][tr >> 5] = 0;
           __syncwarp();
 #pragma unroll
@@ -874,7 +880,7 @@ __global__ void __launch_bounds__(kAttnThreads, 1) k_q4_attn(const __grid_consta
               const int q = (__ffs(nan) - 1) / 8;
               nan &= ~(0xFFu << (8 * q));
               atomicOr(&notes[part * (kD / 16) + 4 * w + q][tr >> 5], 1u << (tr & 31));
-              M.nan_run[run & 1] = run + 1;
+              M.nan_run[set] = run + 1;
             }
           }
         }
@@ -1268,11 +1274,12 @@ __global__ void __launch_bounds__(kAttnThreads, 1) k_q4_attn(const __grid_consta
               for (int e = 0; e < kOut; ++e) o[e] += o2[e];
             }
             const int d = mb * 128 + 32 * quarter + lane;
-            if (M.nan_run[run & 1] == run + 1) {
+            const uint32_t set = run % Meta<DH>::kNotes;
+            if (M.nan_run[set] == run + 1) {
               uint32_t nan = 0;
 #pragma unroll 1
               for (int e = 0; e < kOut; ++e)
-                nan |= (uint32_t)sees_nan<DH / 16>(s.first, s.tile, nt, s.p0, s.p1, M.nan_bits[run & 1], d / 16,
+                nan |= (uint32_t)sees_nan<DH / 16>(s.first, s.tile, nt, s.p0, s.p1, M.nan_bits[set], d / 16,
                                                    M.lim[c0 + c + e], a.window) << e;
 #pragma unroll
               for (int e = 0; e < kOut; ++e)
