@@ -370,12 +370,13 @@ size_t kv_q4_row_bytes(int32_t head_dim);
  *   d_free [n_pages] in/out: the free pages, a stack of
  *       n_free = n_pages - sum_r held entries (every page is a row's or free).
  *   d_cover_out [rows] out: keep + new, the d_cover of the next call and the
- *       cache length that kv_q4_attend takes; d_cover where the row is refused.
- *       Must not overlap d_cover.
+ *       cache length that kv_q4_attend takes; d_cover (held to the table's
+ *       positions) where the row is refused.
  *   d_start [rows + 1] out: the rows' appended positions are packed, row r's at
  *       [start[r], start[r + 1]).
  *   d_slot, d_pos [max_tokens] out: slot and position of every packed position;
  *       -1 past the last one, and d_slot -1 for a refused row.
+ * No output may overlap d_cover, d_keep or d_new, which are read until the end.
  * Order: pages given back go onto the stack from the last row's last page to
  * the first row's first, then pages are taken off it from the first row on, so
  * a plan that undoes another leaves the stack as it was. The lengths are inputs
@@ -387,7 +388,8 @@ size_t kv_q4_row_bytes(int32_t head_dim);
  * positions pass max_tokens; d_slot is -1 (and BAD_ARG set) also where an entry
  * of the table or of the stack is no page. d_status may be NULL.
  * Errors: BAD_ARG (rows outside 1..4096, page not a multiple of 16,
- * rows * max_pages or n_pages * page of 2^31 and more, a null pointer).
+ * rows * max_pages or n_pages * page of 2^31 and more, a null pointer, an output
+ * over a length array).
  */
 mtp_status kv_page_plan(mtp_stream stream, int32_t rows, int32_t page, int32_t max_pages, int32_t n_pages,
                         int32_t max_tokens, const int32_t* d_cover, const int32_t* d_keep, const int32_t* d_new,

@@ -177,7 +177,6 @@ __global__ void __launch_bounds__(kPlanThreads) k_page_plan(const PlanArgs a) {
     }
     if (blockIdx.x == 0) {
       a.start[r] = s_start[r];
-      // (cover and cover_out do not overlap: other blocks still read cover)
       a.cover_out[r] = no ? min(max(a.cover[r], 0), a.page * a.max_pages) : p.total;
     }
   }
@@ -268,7 +267,13 @@ extern "C" mtp_status kv_page_plan(mtp_stream stream, int32_t rows, int32_t page
   if (!d_cover || !d_keep || !d_new || !d_table || !d_free || !d_cover_out || !d_start ||
       (max_tokens > 0 && (!d_slot || !d_pos)))
     return MTP_ERR_BAD_ARG;
-  if (d_cover_out < d_cover + rows && d_cover < d_cover_out + rows) return MTP_ERR_BAD_ARG;
+  // blocks read the lengths to the end while others write
+  const struct { const int32_t* p; long long n; } written[] = {
+      {d_table, (long long)rows * max_pages}, {d_free, n_pages}, {d_cover_out, rows}, {d_start, rows + 1},
+      {d_slot, max_tokens}, {d_pos, max_tokens}};
+  for (const int32_t* in : {d_cover, d_keep, d_new})
+    for (const auto& w : written)
+      if (w.p < in + rows && in < w.p + w.n) return MTP_ERR_BAD_ARG;
   PlanArgs a{rows, page, max_pages, n_pages, max_tokens, d_cover, d_keep, d_new, d_table, d_free, d_cover_out,
              d_start, d_slot, d_pos, d_status};
   const int smem = 20 * rows;  // at 4096 rows more than the default limit
