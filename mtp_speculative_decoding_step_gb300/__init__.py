@@ -433,21 +433,29 @@ def kv_q4_read(cache: PagedCache, slot, k, v, status=None, stream=None):
     _check(rc, "kv_q4_read")
 
 
+def _device() -> int:
+    """The current device's index, -1 before torch has set CUDA up (the library then looks at the first device)."""
+    cuda = _t().cuda
+    return cuda.current_device() if cuda.is_initialized() else -1
+
+
+# Workspace sizes depend on the call's sizes and the current device's SM count, and are asked for by every call that
+# checks its workspace.
 @functools.lru_cache(maxsize=1024)
-def _attend_bytes(n_kv: int, head_dim: int, n_q: int, max_q: int, dt: int) -> int:
-    # a function of sizes alone, asked for by every call that checks its workspace
+def _attend_bytes(device: int, n_kv: int, head_dim: int, n_q: int, max_q: int, dt: int) -> int:
     c = Q4Cache(None, None, None, None, n_kv, head_dim, 16, 1)
     return lib().kv_q4_attend_workspace_bytes(ctypes.byref(c), n_q, max_q, dt)
 
 
 @functools.lru_cache(maxsize=1024)
-def _logprobs_bytes(n: int, vocab: int, top: int) -> int:
+def _logprobs_bytes(device: int, n: int, vocab: int, top: int) -> int:
     return lib().spec_logprobs_workspace_bytes(n, vocab, top)
 
 
 def kv_q4_attend_workspace_bytes(cache: PagedCache, n_q: int, max_q: int, dtype) -> int:
     """dtype: the queries' torch dtype."""
-    return _attend_bytes(cache.n_kv, cache.head_dim, n_q, max_q, MTP_DTYPE_BF16 if dtype is _t().bfloat16 else MTP_DTYPE_F32)
+    return _attend_bytes(_device(), cache.n_kv, cache.head_dim, n_q, max_q,
+                         MTP_DTYPE_BF16 if dtype is _t().bfloat16 else MTP_DTYPE_F32)
 
 
 def kv_q4_attend(cache: PagedCache, q, table, start, length, out, workspace, max_q: int, scale: float, window: int = 0,
@@ -463,7 +471,7 @@ def kv_q4_attend(cache: PagedCache, q, table, start, length, out, workspace, max
     _whole("kv_q4_attend", table, start, length)
     _want(start.numel() == rows + 1 and length.numel() == rows, "kv_q4_attend")
     dt = _dtype_q4("kv_q4_attend", q, out)
-    _want(workspace.nbytes >= _attend_bytes(cache.n_kv, dh, n_q, max_q, dt), "kv_q4_attend")
+    _want(workspace.nbytes >= _attend_bytes(_device(), cache.n_kv, dh, n_q, max_q, dt), "kv_q4_attend")
     rc = lib().kv_q4_attend(_stream(stream), cache.ref, rows, n_q, tokens, _ptr(q), q.stride(0), q.stride(1), dt,
                             _ptr(table), max_pages, _ptr(start), _ptr(length), max_q, scale, window, _ptr(out), _ptr(lse),
                             _ptr(status), _ptr(workspace))
@@ -488,7 +496,7 @@ def spec_logprobs(logits, tok, logprob, workspace, rank=None, entropy=None, top_
         if t is not None and (t.dtype is not f32 or not t.is_contiguous() or t.numel() != size):
             raise MTPError(9, "spec_logprobs")
     _want(logits.stride(1) == 1 and (top_id is None) == (top_lp is None)
-          and workspace.nbytes >= _logprobs_bytes(n, V, top), "spec_logprobs")
+          and workspace.nbytes >= _logprobs_bytes(_device(), n, V, top), "spec_logprobs")
     rc = lib().spec_logprobs(_stream(stream), n, V, _ptr(logits), logits.stride(0), _dtype_q4("spec_logprobs", logits),
                              _ptr(tok), top, _ptr(logprob), _ptr(rank), _ptr(entropy), _ptr(top_id), _ptr(top_lp),
                              _ptr(status), _ptr(workspace))
