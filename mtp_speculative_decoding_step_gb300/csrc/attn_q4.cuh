@@ -59,11 +59,11 @@
 #include "common.cuh"
 #include "kernels.h"
 #include "q4.cuh"
+#include "q4_walk.h"
 #include "tc_common.cuh"
 
 namespace mtp {
 
-constexpr int kT = 128;          // positions per tile
 constexpr int kAttnThreads = 512;
 constexpr float kUnset = -INFINITY;
 constexpr unsigned kQ4WaitLimit = 1u << 20;  // polls: 4 s, where a tile takes about a microsecond
@@ -83,66 +83,6 @@ struct Q4AttnArgs {
   int rows, n_q, n_kv, page, n_pages, max_pages, tokens, window;
   int q_vec;                     // 16-byte loads of q are aligned
   float scale;
-};
-
-// ------------------------------------------------------------ task walk
-
-// A block's share of one (row, KV head, query tile). Query row f of the row's
-// position-major order is (position f / G, head f % G of the KV head's G); tile
-// j holds f in [j RT, (j + 1) RT).
-struct Run {
-  int r, g, j;         // row, KV head, query tile
-  int a0, n, pos;      // first packed position, positions, the first one's place in the cache
-  int lo, end;         // cached positions that some query row sees: [lo, end)
-  int first, tile, nt; // the query tile's first 128-position tile; this share's tiles
-  int p0, p1;          // places of the first and the last query row
-  int flags;           // 1: begins here, 2: ends here, 4: the block's last share
-  int last;            // the block that ends it
-
-  // whether some (row, position) pair of a tile may be out of sight
-  __device__ bool edge(int t, int window) const {
-    return t * kT + kT - 1 > p0 || (window > 0 && t * kT <= p1 - window);
-  }
-  // its number among the edge tiles: p0 and p1 lie less than kT apart, so two
-  // tiles at most hold a causal border, and two a window's
-  __device__ int edge_index(int t) const {
-    return t * kT + kT - 1 > p0 ? min(max(t - p0 / kT, 0), 1) : 2 + min(t - first, 1);
-  }
-};
-
-struct Walk {
-  const Q4AttnArgs* a;
-  int G, RT;       // query heads per KV head, query rows per tile
-
-  __device__ void row(int r, int& a0, int& n, int& L) const {
-    a0 = min(max(a->start[r], 0), a->tokens);
-    n = min(max(a->start[r + 1], a0), a->tokens) - a0;
-    L = min(max(a->len[r], 0), a->max_pages * a->page);
-  }
-  __device__ int tiles(int n) const { return (n * G + RT - 1) / RT; }
-  __device__ void span(int n, int L, int j, int& lo, int& end, int& t0, int& cnt) const {
-    const int i0 = j * RT / G, i1 = (min(n * G, (j + 1) * RT) - 1) / G;
-    end = max(L - n + i1 + 1, 0);
-    lo = a->window > 0 ? max(0, L - n + i0 - a->window + 1) : 0;
-    t0 = 0;
-    cnt = 1;  // one tile at least: rows that see nothing are written too
-    if (lo < end) {
-      t0 = lo / kT;
-      cnt = (end - 1) / kT - t0 + 1;
-    } else {
-      end = lo;
-    }
-  }
-  __device__ int per_head(int n, int L) const {
-    int sum = 0;
-#pragma unroll 1
-    for (int j = 0; j < tiles(n); ++j) {
-      int lo, end, t0, cnt;
-      span(n, L, j, lo, end, t0, cnt);
-      sum += cnt;
-    }
-    return sum;
-  }
 };
 
 // ------------------------------------------------------------ PTX
@@ -528,19 +468,20 @@ __global__ void __launch_bounds__(kAttnThreads, 1) k_q4_attn(const __grid_consta
     // Every (row, KV head, query tile, 128-position tile) is a task; each block
     // owns an equal stretch of them. The rows' task counts are scanned, rows
     // in consecutive groups per lane.
-    const Walk walk{&a, a.n_q / a.n_kv, S::RT};
+    const Walk<Q4AttnArgs> walk{&a, a.n_q / a.n_kv, S::RT};
     // (by the lane that hands out the shares, so that its arrival orders these
     // stores before those of the warps that take a share)
     if (lane == 0) a.part_meta[2 * blockIdx.x] = a.part_meta[2 * blockIdx.x + 1] = make_int4(0, 0, 0, 0);
     const int per = (a.rows + 31) / 32, r0 = min(lane * per, a.rows), r1 = min(r0 + per, a.rows);
     long long sum = 0;
-    int a0 = 0, n = 0, L = 0, ph = 0;
+    int a0 = 0, n = 0, L = 0;
+    long long ph = 0;
 #pragma unroll 1
     for (int r = r0; r < r1; ++r) {
       walk.row(r, a0, n, L);
       if (blockIdx.x == 0 && L != a.len[r]) flag_status(a.status, MTP_ERR_BAD_ARG);
       ph = walk.per_head(n, L);
-      sum += (long long)ph * a.n_kv;
+      sum += ph * a.n_kv;
     }
     long long inc = sum;
 #pragma unroll
@@ -572,7 +513,8 @@ __global__ void __launch_bounds__(kAttnThreads, 1) k_q4_attn(const __grid_consta
     const unsigned who = __ballot_sync(0xFFFFFFFFu, left > 0 && inc - sum <= w0 && w0 < inc);
     const int owner = who ? __ffs(who) - 1 : 0;
     long long at = __shfl_sync(0xFFFFFFFFu, inc - sum, owner);
-    int r = __shfl_sync(0xFFFFFFFFu, r0, owner), g = 0, j = 0, o = 0;
+    int r = __shfl_sync(0xFFFFFFFFu, r0, owner), g = 0, j = 0;
+    long long o = 0;
     a0 = __shfl_sync(0xFFFFFFFFu, a0, owner);  // (the last row that the lane looked at: its only one, mostly)
     n = __shfl_sync(0xFFFFFFFFu, n, owner);
     L = __shfl_sync(0xFFFFFFFFu, L, owner);
@@ -584,13 +526,11 @@ __global__ void __launch_bounds__(kAttnThreads, 1) k_q4_attn(const __grid_consta
           walk.row(r, a0, n, L);
           ph = walk.per_head(n, L);
         }
-        if (w0 < at + (long long)ph * a.n_kv) {
-          const unsigned x = (unsigned)(w0 - at);  // (a row has fewer than 2^32 tasks)
-          g = (int)(x / (unsigned)ph);
-          o = (int)(x % (unsigned)ph);
+        if (w0 < at + ph * a.n_kv) {
+          walk.find(w0 - at, ph, g, o);
           break;
         }
-        at += (long long)ph * a.n_kv;
+        at += ph * a.n_kv;
       }
     }
     bool found = false;
@@ -619,8 +559,8 @@ __global__ void __launch_bounds__(kAttnThreads, 1) k_q4_attn(const __grid_consta
       s.pos = L - n;
       s.p0 = s.pos + j * S::RT / walk.G;
       s.p1 = s.pos + (min(n * walk.G, (j + 1) * S::RT) - 1) / walk.G;
-      s.tile = s.first + o;
-      s.nt = (int)min((long long)(cnt - o), left);
+      s.tile = s.first + (int)o;
+      s.nt = (int)min(cnt - o, left);
       s.flags = (o == 0 ? 1 : 0) | (o + s.nt == cnt ? 2 : 0) | (s.nt == left ? 4 : 0);
       s.last = b;
 #pragma unroll 1
