@@ -32,7 +32,7 @@ struct Run {
 
   // whether some (row, position) pair of a tile may be out of sight
   Q4_WALK bool edge(int t, int window) const {
-    return t * kT + kT - 1 > p0 || (window > 0 && t * kT <= p1 - window);
+    return t * kT + kT - 1 > p0 || (window > 0 && t * kT <= max(p1, -1) - window);
   }
   // its number among the edge tiles: p0 and p1 lie less than kT apart, so two
   // tiles at most hold a causal border, and two a window's
@@ -56,7 +56,8 @@ struct Walk {
   Q4_WALK void span(int n, int L, int j, int& lo, int& end, int& t0, int& cnt) const {
     const int i0 = j * RT / G, i1 = (min(n * G, (j + 1) * RT) - 1) / G;
     end = max(L - n + i1 + 1, 0);
-    lo = a->window > 0 ? max(0, L - n + i0 - a->window + 1) : 0;
+    // (from 0 at the least before the window goes off: a first place below 0 less a window near 2^31 would wrap)
+    lo = a->window > 0 ? max(0, max(0, L - n + i0 + 1) - a->window) : 0;
     t0 = 0;
     cnt = 1;  // one tile at least: rows that see nothing are written too
     if (lo < end) {

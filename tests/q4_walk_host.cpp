@@ -23,3 +23,19 @@ void walk_find(long long x, long long ph, int* g, long long* o) {
 }
 
 }  // extern "C"
+
+extern "C" {
+
+void walk_span(int n, int L, int G, int RT, int window, int j, int* out) {
+  const Args a{nullptr, nullptr, n, 1, 1, window};
+  mtp::Walk<Args>{&a, G, RT}.span(n, L, j, out[0], out[1], out[2], out[3]);
+}
+
+int walk_edge(int p0, int p1, int t, int window) {
+  mtp::Run s{};
+  s.p0 = p0;
+  s.p1 = p1;
+  return s.edge(t, window);
+}
+
+}  // extern "C"

@@ -51,3 +51,23 @@ def test_a_task_is_found_in_its_head(walk, ph):
         g, o = ctypes.c_int(-1), ctypes.c_longlong(-1)
         walk.walk_find(x, ph, ctypes.byref(g), ctypes.byref(o))
         assert (g.value, o.value) == divmod(x, ph), x
+
+
+LIMIT = (1 << 31) - 1
+
+
+@pytest.mark.parametrize("n,L,G,RT", SHAPES + [(5, 2, 1, 16), (40, 10, 4, 16), (130, 128, 6, 32), (3, 0, 1, 16), (4096, 4000, 2, 128)])
+@pytest.mark.parametrize("window", [0, 1, 7, 4096, 1 << 30, LIMIT - 40, LIMIT - 1, LIMIT])
+def test_visible_positions_of_query_tiles(walk, n, L, G, RT, window):
+    """Also for rows with more queries than cached positions, whose first places are negative."""
+    got = (ctypes.c_int * 4)()
+    for j, (lo, end, cnt) in enumerate(spans(n, L, G, RT, window)):
+        walk.walk_span(n, L, G, RT, window, j, got)
+        if lo < end:
+            assert list(got) == [lo, end, lo // 128, cnt]
+        else:
+            assert got[0] == got[1] and got[3] == 1
+        p0, p1 = L - n + j * RT // G, L - n + (min(n * G, (j + 1) * RT) - 1) // G
+        for t in range(min(got[2], 1 << 20), min(got[2], 1 << 20) + cnt):
+            out_of_sight = 128 * t + 127 > p0 or (window > 0 and 128 * t <= p1 - window)
+            assert bool(walk.walk_edge(p0, p1, t, window)) == out_of_sight
