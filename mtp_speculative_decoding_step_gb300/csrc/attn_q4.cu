@@ -32,8 +32,9 @@ __global__ void __launch_bounds__(kJoinThreads) k_q4_join(const __grid_constant_
   const int a0 = min(max(a.start[me.x], 0), a.tokens);
   const int n = min(max(a.start[me.x + 1], a0), a.tokens) - a0;
   const float up = pow2i(head_exp(a.v_exp, me.y));
-  // a part that saw nothing has m = -inf and the sum 0; one whose scores were
-  // all NaN has m = -inf and the sum NaN
+  // a part that saw nothing has m = -inf, the sum 0 and O = 0; one whose scores
+  // were all NaN has m = -inf and the sum NaN. Parts whose weight is 0 are added
+  // too: 0 x NaN is NaN, as where one block sums all of the row.
   auto at = [&](int p, int j) { return (long long)(2 * (b + p) + (p == 0)) * RT + j; };
   auto weight = [](float2 ml, float m) { return ml.x == -INFINITY ? (ml.y == 0.f ? 0.f : 1.f) : exp2f(ml.x - m); };
   auto place = [&](int f) { return (long long)(a0 + f / G) * a.n_q + me.y * G + f % G; };
@@ -65,7 +66,7 @@ __global__ void __launch_bounds__(kJoinThreads) k_q4_join(const __grid_constant_
         float4 o = make_float4(0.f, 0.f, 0.f, 0.f);
 #pragma unroll
         for (int p = 0; p < kJoinFew; ++p)
-          if (w[p] != 0.f && p < parts) {
+          if (p < parts) {
             o.x = fmaf(w[p], v[p][i].x, o.x);
             o.y = fmaf(w[p], v[p][i].y, o.y);
             o.z = fmaf(w[p], v[p][i].z, o.z);
@@ -113,12 +114,10 @@ __global__ void __launch_bounds__(kJoinThreads) k_q4_join(const __grid_constant_
       for (int p = grp; p < min(parts - p0, kJoinThreads); p += kG) {
         const float w = s_w[p];
         const float4 v = reinterpret_cast<const float4*>(a.part_o + at(p0 + p, j) * DH)[d4];
-        if (w != 0.f) {
-          o.x = fmaf(w, v.x, o.x);
-          o.y = fmaf(w, v.y, o.y);
-          o.z = fmaf(w, v.z, o.z);
-          o.w = fmaf(w, v.w, o.w);
-        }
+        o.x = fmaf(w, v.x, o.x);
+        o.y = fmaf(w, v.y, o.y);
+        o.z = fmaf(w, v.z, o.z);
+        o.w = fmaf(w, v.w, o.w);
       }
       __syncthreads();
     }

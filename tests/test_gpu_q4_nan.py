@@ -54,3 +54,24 @@ def test_blocks_with_many_one_tile_shares(dh, group, hint, dtype):
                        int(torch.randint(0, dh // 16, (1,), generator=g)))
     nan = check_nan(c, 1 / math.sqrt(dh), calls=3, max_q=hint)
     assert nan.any() and (~nan).any()
+
+
+@pytest.mark.parametrize("dtype", [torch.bfloat16, torch.float32])
+@pytest.mark.parametrize("nq,nkv,dh", [(4, 2, 64), (8, 2, 128), (24, 4, 256)])
+@pytest.mark.parametrize("rows,kv", [(1, 300), (1, 2000), (1, 9000), (170, 300)])
+def test_nan_of_no_weight_shows_however_the_row_is_split(rows, kv, nq, nkv, dh, dtype):
+    """All weight of a row lies in its newest tile, 2^-200 of it and less elsewhere, and NaN in the oldest. By the formula
+    0 x NaN is NaN: a block that sums both tiles shows it, and so has a join of several blocks' parts to."""
+    c = build(rows, [2] * rows, [kv] * rows, nq, nkv, dh, 16, dtype, 33, exps=False)
+    c["q"] = c["q"].abs() + 1
+    for r in range(rows):
+        for p in range(-(-kv // 16)):
+            # codes 1.0 and one scale for all: the scores of a page are equal, 0 but on the last one
+            c["kc"][c["table"][r][p], :, :, : dh // 2] = 0x22
+            c["kc"][c["table"][r][p], :, : kv - 16 * p, dh // 2:] = q4_ref.e4m3_code(
+                torch.tensor(16.0 if 16 * p + 16 >= kv else 0.0, dtype=torch.float64)).item()
+        for h in range(nkv):
+            poison(c, r, 5, h, h)
+    # (16 sum q >= 16 dh, so that page's scores are 150 and more, 2^216 times the others' weight)
+    nan = check_nan(c, 150 / (16 * dh))
+    assert nan[:, :, :].any(-1).all() and (~nan).any()
