@@ -18,6 +18,7 @@
 // together 39 us for 172 MB, 4.4 TB/s; the append is at two thirds of the issue
 // rate (18.9 M instructions for 33.6 M values), the read is HBM-bound.
 #include <algorithm>
+#include <cfloat>
 
 #include "common.cuh"
 #include "kernels.h"
@@ -102,9 +103,14 @@ __global__ void __launch_bounds__(kQ4Threads) k_q4_append(const __grid_constant_
   bool finite = true;
 #pragma unroll
   for (int i = 0; i < 16; ++i) {
-    x[i] *= down;
     finite &= isfinite(x[i]);
+    x[i] *= down;
     amax = fmaxf(amax, fabsf(x[i]));
+  }
+  if (finite && amax == INFINITY) {  // past fp32's range by the exponent alone: as large as it gets, 6 x 448
+    amax = FLT_MAX;
+#pragma unroll
+    for (int i = 0; i < 16; ++i) x[i] = fminf(fmaxf(x[i], -FLT_MAX), FLT_MAX);
   }
   uint16_t sc;
   asm("cvt.rn.satfinite.e4m3x2.f32 %0, %1, %2;" : "=h"(sc) : "f"(0.f), "f"(amax / 6.f));
