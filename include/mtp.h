@@ -409,7 +409,8 @@ mtp_status kv_page_plan(mtp_stream stream, int32_t rows, int32_t page, int32_t m
  * scale gives zero codes. 16 elements with a NaN or an infinity among them are
  * stored as NaN (scale 0x7F) and set 1 << MTP_ERR_NONFINITE.
  * kv_q4_read — the values of slots, [tokens][n_kv][head_dim] contiguous in
- * dtype; zeros where d_slot skips. Errors of both: BAD_ARG.
+ * dtype, d_k and d_v 16-byte aligned; zeros where d_slot skips. Errors of both:
+ * BAD_ARG.
  */
 mtp_status kv_q4_append(mtp_stream stream, const kv_q4_cache* cache, int32_t tokens, const void* d_k,
                         int64_t k_tok_stride, int64_t k_head_stride, const void* d_v, int64_t v_tok_stride,
@@ -425,7 +426,10 @@ mtp_status kv_q4_read(mtp_stream stream, const kv_q4_cache* cache, int32_t token
  * with window > 0 only the last `window` of those. Per query head (n_q / n_kv
  * of them share a KV head):
  *   s_j = scale * q . k_j,  out = sum_j softmax(s)_j v_j,  lse = log sum_j exp(s_j)
- * A query that sees nothing gets zeros and lse = -inf.
+ * A query that sees nothing gets zeros and lse = -inf. A NaN in a K row that a
+ * query sees makes its outputs on that head NaN, one in V its 16 dimensions;
+ * positions out of sight may hold anything. Rows of d_out and d_lse outside
+ * [start[0], start[rows]) are not written.
  *   d_q: element (t, head, i) at t * tok_stride + head * head_stride + i
  *   d_out [tokens][n_q][head_dim] contiguous in dtype; d_lse [tokens][n_q] float
  *       (optional)
@@ -434,7 +438,7 @@ mtp_status kv_q4_read(mtp_stream stream, const kv_q4_cache* cache, int32_t token
  *       kernel's shape. Rows that have more are still computed.
  *   d_workspace: kv_q4_attend_workspace_bytes(...) bytes, 16-byte aligned.
  * Scores and sums are fp32. q enters as f16 after a power-of-two scaling per
- * query and head (exact for bf16 but for elements 2^-16 below the largest);
+ * query and head (exact for bf16 but for elements 2^-30 below the largest);
  * fp32 q as two f16 parts (22 bits). The softmax weights are f16 (11 bits;
  * fp32 q: two parts, 22 bits) down to 2^-21 of the largest, below that in steps
  * of 2^-31 of it.

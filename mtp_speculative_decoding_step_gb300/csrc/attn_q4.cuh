@@ -33,17 +33,28 @@
 // weights up to 2^15 and, 2^-14 being its smallest normal number, rounds all
 // within 2^21 of the largest to 11 bits.
 //
-// What bounds it, and what it measured (24 query heads on 4 KV heads of 256):
-//   prompts (two rows of 1500 and 2048 queries near 8192): 690 us, 945 TFLOP/s,
-//     the tensor pipe active 47 %; the dequantising group (one beside the 128
-//     columns' softmax) and the softmax share the issue slots
-//   8 rows of 4 queries, 1k to 16k positions: 38 us, 2.3 TB/s. A tile takes 2450
-//     cycles of a block, 1900 of them shared-memory traffic (raw rows in and
-//     out, V's f16 tile written by threads and read by the MMA, P)
-//   64 rows of one query, 2 KV heads of 128, pages of 16: 63 us, 2.4 TB/s
-//   1 row of 3 queries, 4096 positions (one tile a block): 15 us with the join,
-//     all latency: shares 2700 cycles, page look-up and copy 2900, the two
-//     products and the softmax between 3700, O 3300
+// What it measured (24 query heads on 4 KV heads of 256), and what is known of
+// what bounds it:
+//   prompts (two rows of 1500 and 2048 queries near 8192): 690 us, 950 TFLOP/s.
+//     The tensor pipe is active 47 %, the issue slots 42 %: neither is full. With
+//     128 columns tensor memory has room for one S and one K, so that expansion,
+//     S, softmax and P.V of a block take turns
+//   8 rows of 4 queries, 1k to 16k positions: 38 us, 2.3 TB/s. A block has 15.4
+//     tiles of 2450 cycles, 20 us (1900 of the 2450 are shared-memory traffic: raw
+//     rows in and out, V's f16 tile written by threads and read by the MMA, P);
+//     the rest is a share's start, its drain of O and the join, not told apart
+//   64 rows of one query, 2 KV heads of 128, pages of 16: 61 us, 2.4 TB/s. A
+//     block has 54 tiles, 2200 cycles each with the starts and the join, where
+//     shared memory accounts for 890 and the issue slots are 47 % busy: which wait
+//     limits it is not known
+//   1 row of 3 queries, 4096 positions (one tile a block): 14.4 us with the join,
+//     one after another: shares 2700 cycles, page look-up and copy 2900, the two
+//     products and the softmax between 3700, O 3300, together 6.5 us; a launch and
+//     the join are some 4 more, and what is left of the 14.4 is not accounted for
+//   fp32 queries, the same four: 1960, 46, 64 and 15 us
+//   many short rows (8 query heads on 2 of 128): 512 of up to 1023 positions 62 us,
+//     4096 of up to 127 282 us. Every block reads all rows' lengths, 32 at a time,
+//     which at 4096 rows is 128 dependent steps; not measured by itself
 //
 // fp32 queries: q and the weights each enter as two f16 parts in separate
 // columns (22 bits), N / 2 rows a tile.

@@ -15,11 +15,13 @@
 // so the blocks need no order among them. Each block redoes the row scan (12
 // bytes per row from L2) rather than wait for another block or launch.
 //
-// Bound by latency: the scan, one binary search and two dependent loads; a
-// block's lengths, its table rows and its stack entries are one load each.
-// 8 rows of 4 positions: 5.7 us in a graph, of which a launch is about 2; 512
-// rows and 512,000 positions: 9.4 us (8.4 MB, 0.9 TB/s), half of it the scan that
-// each block repeats.
+// Few rows are bound by latency: the scan, one binary search and two dependent
+// loads; a block's lengths, its table rows and its stack entries are one load
+// each. 8 rows of 4 positions: 4.3 us in a graph of such calls, of which a launch
+// is about 2. Many rows with prompts are bound by instructions (5.7 M a call,
+// the issue slots 62 % busy): the 64-bit scans that each block repeats, and the
+// divisions and selects of each position. 512 rows and 512,000 positions: 9.0 us
+// (8.4 MB, 0.9 TB/s).
 #include <algorithm>
 #include <mutex>
 

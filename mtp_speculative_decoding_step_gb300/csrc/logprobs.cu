@@ -695,8 +695,9 @@ __global__ void __launch_bounds__(kLpJoinThreads) k_lp_join(const __grid_constan
 
 // Parts per row: the count with the least (waves of resident blocks) x (a
 // part's elements + a block's fixed cost, counted in elements), the join's cost
-// per part added. Many rows: whole waves; few rows: short parts. (256 rows of
-// 152,064: 2 parts 43 us, 7 parts 54.)
+// per part added. Many rows: whole waves; few rows: short parts. (The constants
+// were tried at one size alone (256 rows of 152,064: 8000 gives 2 parts
+// and 43 us, 1000 to 4000 give 7 parts and 54; the 110 was not varied.)
 int lp_parts(int n, int V) {
   const long long slots = (long long)kLpBlocksPerSM * device_sm_count();
   const int most = std::min(kLpMaxParts, std::max(1, V / 2048));
