@@ -6,7 +6,7 @@ to the committed cache, where a round drafts a tree instead of a chain:
   rope     per-head norms of queries and keys, the rotation by position, and the
            append of K and V to the paged 4-bit cache (kv_q4_append_rope)
   prompt   causal attention of whole packed prompts over unrounded K and V
-           (attend_prompt)
+           (kv_attend_prompt)
   plan     positions and ancestor masks of trees from their parents (kv_tree_plan)
   tree     attention of a tree's nodes over the cache and their ancestors
            (kv_q4_attend_tree)
@@ -357,8 +357,8 @@ def _prompt(s):
         import mtp_speculative_decoding_step_gb300 as m
         b = s["buf"]
         if not b:
-            b["ws"] = torch.empty(m.attend_prompt_workspace_bytes(s["q"].shape[0], c["rows"]), dtype=torch.uint8, device=DEV)
-        m.attend_prompt(s["q"], s["k"], s["v"], s["start"], s["out"], b["ws"], s["max_len"], scale=s["scale"], window=c["window"], lse=s["lse"])
+            b["ws"] = torch.empty(m.kv_attend_prompt_workspace_bytes(s["q"].shape[0], c["rows"]), dtype=torch.uint8, device=DEV)
+        m.kv_attend_prompt(s["q"], s["k"], s["v"], s["start"], s["out"], b["ws"], s["max_len"], scale=s["scale"], window=c["window"], lse=s["lse"])
         return {"out": s["out"], "lse": s["lse"]}
     nq, nkv, L = c["n_q"], c["n_kv"], s["max_len"]
     G, start = nq // nkv, s["start"]
