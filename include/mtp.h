@@ -458,6 +458,164 @@ mtp_status kv_q4_attend(mtp_stream stream, const kv_q4_cache* cache, int32_t row
                         void* d_workspace);
 
 /*
+ * ------------------------------------------------ trees of drafts, prompts
+ *
+ * A round that drafts a tree verifies all of its nodes at once: they are
+ * appended to the cache like a block of positions (kv_page_plan with
+ * d_new = the node counts, kv_q4_append_rope with the nodes' positions), each
+ * attends the row's committed prefix and its own ancestors, and of the path
+ * that the target confirms the rows are moved together behind the prefix.
+ * Node 0 of a row is the last committed token; a node's parent comes before it.
+ */
+#define MTP_TREE_MAX 128  /* nodes of a row */
+#define MTP_MAX_CACHES 64 /* layers of one kv_q4_tree_commit */
+#define MTP_ROPE_MAX 128  /* rotated pairs */
+
+/* Frequencies of a rotation by position, in turns per position (units of
+ * 2^-64), caller-owned host memory. */
+typedef struct {
+  int32_t rot_dim; /* the first rot_dim dimensions are rotated: pairs (i, i + rot_dim / 2) */
+  uint64_t turn[MTP_ROPE_MAX];
+} mtp_rope;
+
+/* Fill *out: pair i turns by theta^(-2i/rot_dim) radians a position, or by
+ * h_freq[i] where h_freq is given (rot_dim / 2 of them, finite; scaled
+ * rotations). Host only. Errors: BAD_ARG (rot_dim odd or outside 0..256, theta
+ * not positive or not finite). */
+mtp_status mtp_rope_init(int32_t rot_dim, double theta, const double* h_freq, mtp_rope* out);
+
+/*
+ * kv_q4_append_rope — norms, rotation and append of a projection's rows.
+ * Queries and keys: y = x / sqrt(mean x^2 + eps) * w over the head (without
+ * d_q_norm or d_k_norm: y = x), then the pairs (y_i, y_{i + rot_dim / 2}) turned
+ * by d_pos * frequency i, as exactly at far positions as at near ones. Queries
+ * go to d_q_out, keys to the cache and, unless it is NULL, to d_k_out; values go
+ * to the cache as they are. The cache's 4 bits are rounded (as by kv_q4_append)
+ * from keys that are good to 2^-30, not from d_k_out.
+ *   d_q, d_k, d_v: element (t, head, i) at t * tok_stride + head * head_stride + i,
+ *       strides in elements (slices of a fused projection will do), dtype each
+ *   d_q_norm, d_k_norm [head_dim] float, 16-byte aligned, applied as they are
+ *       (with the +1 of a raw-HF checkpoint added); NULL = no norm
+ *   d_pos, d_slot [tokens]: a position below 0 is padding: its rows of the outputs
+ *       are zeros and nothing is appended. d_slot -1 appends nothing; any other
+ *       slot outside the cache, or a slot beside a position below 0, sets
+ *       1 << MTP_ERR_BAD_ARG in d_status and appends nothing.
+ *   d_q_out [tokens][n_q][head_dim], d_k_out [tokens][n_kv][head_dim] (optional)
+ *       contiguous in dtype, 16-byte aligned. Each may be its own input where that
+ *       is contiguous; any other overlap is refused.
+ * 16 elements of K or V with a NaN or an infinity are stored as NaN and set
+ * 1 << MTP_ERR_NONFINITE. Squares are summed in fp32. Errors: BAD_ARG (n_q
+ * outside 1..1024, rot_dim above head_dim, eps negative or not finite,
+ * tokens * (n_q + 2 n_kv) near 2^31, an input not aligned to its type, a null
+ * pointer, an overlap).
+ */
+mtp_status kv_q4_append_rope(mtp_stream stream, const kv_q4_cache* cache, int32_t tokens, int32_t n_q,
+                             const void* d_q, int64_t q_tok_stride, int64_t q_head_stride, const void* d_k,
+                             int64_t k_tok_stride, int64_t k_head_stride, const void* d_v, int64_t v_tok_stride,
+                             int64_t v_head_stride, int32_t dtype, const float* d_q_norm, const float* d_k_norm,
+                             float eps, const mtp_rope* rope, const int32_t* d_pos, const int32_t* d_slot,
+                             void* d_q_out, void* d_k_out, int32_t* d_status);
+
+/*
+ * kv_tree_plan — positions and ancestor masks of trees, once for all layers.
+ * Row r has n = start[r + 1] - start[r] <= MTP_TREE_MAX nodes, which stand at
+ * the cached positions len[r] - n .. len[r] - 1.
+ *   d_parent [tokens]: the parent's number within the row, below the node's own;
+ *       -1 where the node hangs on the prefix
+ *   d_pos [tokens] out: len - n + depth (for the rotation, and for a window)
+ *   d_mask [tokens][MTP_TREE_MAX / 32] out, 16-byte aligned: bit a of a node's
+ *       mask is node a, its ancestors and itself; with window > 0 only the last
+ *       `window` of them
+ * A node with an invalid parent and its descendants get position -1, an empty
+ * mask and 1 << MTP_ERR_BAD_ARG in d_status, as do all nodes of a row with too
+ * many of them or with len < n. Entries outside [start[0], start[rows]) are not
+ * written. Errors: BAD_ARG (rows outside 1..4096, a null or unaligned pointer,
+ * an output over an input).
+ */
+mtp_status kv_tree_plan(mtp_stream stream, int32_t rows, int32_t tokens, const int32_t* d_parent,
+                        const int32_t* d_start, const int32_t* d_len, int32_t window, int32_t* d_pos, int32_t* d_mask,
+                        int32_t* d_status);
+
+/*
+ * kv_q4_attend_tree — kv_q4_attend for the nodes of trees: query i of row r sees
+ * the prefix [0, len - n), with window > 0 from position d_pos - window + 1 on,
+ * and the nodes whose bits its mask has (kv_tree_plan's, or any other set;
+ * bits from n on mean nothing). Arguments, arithmetic and workspace
+ * (kv_q4_attend_workspace_bytes) as there.
+ *   d_mask [tokens][MTP_TREE_MAX / 32], 16-byte aligned
+ *   d_pos [tokens]: needed with window > 0 only; held to [len - n, len - 1]
+ * A row of more than MTP_TREE_MAX nodes sets 1 << MTP_ERR_BAD_ARG in d_status,
+ * and its outputs are not written. Errors: kv_q4_attend's, and BAD_ARG for max_q
+ * above MTP_TREE_MAX, d_mask null or unaligned, a window without d_pos.
+ */
+mtp_status kv_q4_attend_tree(mtp_stream stream, const kv_q4_cache* cache, int32_t rows, int32_t n_q, int32_t tokens,
+                             const void* d_q, int64_t tok_stride, int64_t head_stride, int32_t dtype,
+                             const int32_t* d_table, int32_t max_pages, const int32_t* d_start, const int32_t* d_len,
+                             const int32_t* d_mask, const int32_t* d_pos, int32_t max_q, float scale, int32_t window,
+                             void* d_out, float* d_lse, int32_t* d_status, void* d_workspace);
+
+/*
+ * kv_q4_tree_commit — the confirmed path of each row's tree, moved together in
+ * every layer's cache. The path starts at node 0; behind a node follows its
+ * lowest-numbered child whose token is the target's choice after that node, as
+ * long as there is one and the path is shorter than max_path. With a choice
+ * drawn from the target's distribution at every node the committed tokens
+ * follow that distribution; with its argmax the verify is greedy.
+ *   caches [n_caches] (host, at most MTP_MAX_CACHES): the layers, which share the
+ *       block table and have one shape; two that overlap are refused. 0 = the
+ *       path only (d_table may then be NULL)
+ *   d_parent, d_tok, d_choice [tokens]: per node its parent (kv_tree_plan), its
+ *       token, and the token that the target puts behind it
+ *   d_n_acc [rows] out: accepted drafts, path length - 1 (0 for a row without nodes)
+ *   d_out_tok [rows][max_path] out: the committed tokens, d_choice along the
+ *       path (the accepted drafts, then the target's own), then -1
+ *   d_path [rows][max_path] out (optional): the path's nodes, then -1
+ *   d_keep [rows] out: len - n + path length, kv_page_plan's d_keep
+ * The cached rows of path node k go to place k, position len - n + k. Moves
+ * whose table entry is no page are left out and set 1 << MTP_ERR_BAD_ARG in
+ * d_status, as does a parent that is not below its node (which then is nobody's
+ * child); rows with too many nodes, or len outside [n, max_pages * page], also set
+ * it, move nothing, have no path and keep len. A second call on the same
+ * tree would move rows that have moved. Errors: BAD_ARG (rows outside 1..4096,
+ * max_path outside 1..MTP_TREE_MAX, a null pointer, overlapping outputs).
+ */
+mtp_status kv_q4_tree_commit(mtp_stream stream, const kv_q4_cache* caches, int32_t n_caches, int32_t rows,
+                             int32_t tokens, const int32_t* d_table, int32_t max_pages, const int32_t* d_start,
+                             const int32_t* d_len, const int32_t* d_parent, const int32_t* d_tok,
+                             const int32_t* d_choice, int32_t max_path, int32_t* d_n_acc, int32_t* d_out_tok,
+                             int32_t* d_keep, int32_t* d_path, int32_t* d_status);
+
+/*
+ * kv_attend_prompt — causal attention of whole prompts over their own keys and
+ * values, unrounded (the cache then serves what follows them). Row r holds
+ * positions [start[r], start[r + 1]) of the packed tokens; its i-th query sees
+ * the positions up to its own, with window > 0 only the last `window` of them:
+ *   s_ij = scale * q_i . k_j,  out_i = sum_j softmax(s_i)_j v_j,  lse_i = log sum_j exp(s_ij)
+ *   d_q, d_k, d_v: element (t, head, i) at t * tok_stride + head * head_stride + i
+ *       (slices of a fused projection will do); bases and strides multiples of
+ *       16 bytes
+ *   d_out [tokens][n_q][head_dim] contiguous in dtype, 16-byte aligned;
+ *   d_lse [tokens][n_q] float (optional)
+ *   max_len: the most positions of a row, as the caller knows it, for the launch's
+ *       shape only: rows that have more are still computed
+ *   d_workspace: kv_attend_prompt_workspace_bytes(tokens, rows), 16-byte aligned
+ * Positions that a query does not see may hold anything; what it does see and is
+ * NaN or infinite shows in its outputs. Rows of d_out and d_lse outside
+ * [start[0], start[rows]) are not written. Scores, sums and outputs are
+ * accumulated in fp32; with bf16 the softmax weights are rounded to bf16 for the
+ * product with V (off by at most 2^-8 of each). A bounded wait that ran out sets
+ * 1 << MTP_ERR_TIMEOUT in d_status. Errors: BAD_ARG (rows outside 1..4096, n_q
+ * outside 1..1024 or no multiple of n_kv, head_dim not 64, 128 or 256, tokens *
+ * n_q of 2^31 and more, a null or unaligned pointer, an output over an input).
+ */
+size_t kv_attend_prompt_workspace_bytes(int32_t tokens, int32_t rows);
+mtp_status kv_attend_prompt(mtp_stream stream, int32_t rows, int32_t n_q, int32_t n_kv, int32_t head_dim, int32_t tokens,
+                         const void* d_q, int64_t q_tok_stride, int64_t q_head_stride, const void* d_k,
+                         int64_t k_tok_stride, int64_t k_head_stride, const void* d_v, int64_t v_tok_stride,
+                         int64_t v_head_stride, int32_t dtype, const int32_t* d_start, int32_t max_len, float scale,
+                         int32_t window, void* d_out, float* d_lse, int32_t* d_status, void* d_workspace);
+
+/*
  * spec_logprobs — log probabilities of given tokens under raw logits (no
  * transforms), with their ranks, the entropy and the likeliest alternatives.
  *   d_logits [n] rows of vocab logits (dtype), row_stride elements apart: for

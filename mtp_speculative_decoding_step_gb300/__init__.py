@@ -37,6 +37,8 @@ EXPORTS = (
     "mtp_depth_ctl_state", "mtp_set_draft_head", "mtp_test_verify_stall",
     "kv_q4_row_bytes", "kv_page_plan", "kv_q4_append", "kv_q4_read", "kv_q4_attend_workspace_bytes",
     "kv_q4_attend", "spec_logprobs_workspace_bytes", "spec_logprobs",
+    "mtp_rope_init", "kv_q4_append_rope", "kv_tree_plan", "kv_q4_attend_tree", "kv_q4_tree_commit",
+    "kv_attend_prompt_workspace_bytes", "kv_attend_prompt",
 )
 
 
@@ -72,6 +74,13 @@ class Q4Cache(ctypes.Structure):
     _fields_ = [("k", ctypes.c_void_p), ("v", ctypes.c_void_p), ("k_exp", ctypes.c_void_p),
                 ("v_exp", ctypes.c_void_p), ("n_kv", ctypes.c_int32), ("head_dim", ctypes.c_int32),
                 ("page", ctypes.c_int32), ("n_pages", ctypes.c_int32)]
+
+
+MTP_TREE_MAX, MTP_MAX_CACHES, MTP_ROPE_MAX = 128, 64, 128
+
+
+class Rope(ctypes.Structure):
+    _fields_ = [("rot_dim", ctypes.c_int32), ("turn", ctypes.c_uint64 * MTP_ROPE_MAX)]
 
 
 _lib = None
@@ -126,10 +135,23 @@ def lib():
         L.spec_logprobs_workspace_bytes.argtypes = [i32, i32, i32]
         L.spec_logprobs_workspace_bytes.restype = sz
         L.spec_logprobs.argtypes = [vp, i32, i32, vp, i64, i32, vp, i32] + [vp] * 7
+        f32 = ctypes.c_float
+        L.mtp_rope_init.argtypes = [i32, ctypes.c_double, ctypes.POINTER(ctypes.c_double), ctypes.POINTER(Rope)]
+        L.kv_q4_append_rope.argtypes = [vp, cache, i32, i32, vp, i64, i64, vp, i64, i64, vp, i64, i64, i32, vp, vp, f32,
+                                        ctypes.POINTER(Rope), vp, vp, vp, vp, vp]
+        L.kv_tree_plan.argtypes = [vp, i32, i32, vp, vp, vp, i32, vp, vp, vp]
+        L.kv_q4_attend_tree.argtypes = [vp, cache, i32, i32, i32, vp, i64, i64, i32, vp, i32, vp, vp, vp, vp, i32, f32, i32,
+                                        vp, vp, vp, vp]
+        L.kv_q4_tree_commit.argtypes = [vp, cache, i32, i32, i32, vp, i32, vp, vp, vp, vp, vp, i32] + [vp] * 5
+        L.kv_attend_prompt_workspace_bytes.argtypes = [i32, i32]
+        L.kv_attend_prompt_workspace_bytes.restype = sz
+        L.kv_attend_prompt.argtypes = [vp, i32, i32, i32, i32, i32, vp, i64, i64, vp, i64, i64, vp, i64, i64, i32, vp, i32,
+                                       f32, i32, vp, vp, vp, vp]
         for name in ("mtp_load", "mtp_free", "mtp_get_lengths", "mtp_set_lengths", "mtp_flush", "mtp_draft",
                      "spec_verify", "spec_verify_noalloc", "kv_rollback", "mtp_profile_enable",
                      "mtp_profile_read", "mtp_test_verify_stall", "kv_page_plan", "kv_q4_append", "kv_q4_read",
-                     "kv_q4_attend", "spec_logprobs"):
+                     "kv_q4_attend", "spec_logprobs", "mtp_rope_init", "kv_q4_append_rope", "kv_tree_plan",
+                     "kv_q4_attend_tree", "kv_q4_tree_commit", "kv_attend_prompt"):
             getattr(L, name).restype = ctypes.c_int
         _lib = L
     return _lib
@@ -452,6 +474,11 @@ def _logprobs_bytes(device: int, n: int, vocab: int, top: int) -> int:
     return lib().spec_logprobs_workspace_bytes(n, vocab, top)
 
 
+@functools.lru_cache(maxsize=1024)
+def _prompt_bytes(tokens: int, rows: int) -> int:
+    return lib().kv_attend_prompt_workspace_bytes(tokens, rows)
+
+
 def kv_q4_attend_workspace_bytes(cache: PagedCache, n_q: int, max_q: int, dtype) -> int:
     """dtype: the queries' torch dtype."""
     return _attend_bytes(_device(), cache.n_kv, cache.head_dim, n_q, max_q,
@@ -501,6 +528,133 @@ def spec_logprobs(logits, tok, logprob, workspace, rank=None, entropy=None, top_
                              _ptr(tok), top, _ptr(logprob), _ptr(rank), _ptr(entropy), _ptr(top_id), _ptr(top_lp),
                              _ptr(status), _ptr(workspace))
     _check(rc, "spec_logprobs")
+
+
+def mtp_rope(rot_dim: int, theta: float = 10000.0, freq=None) -> Rope:
+    """Frequencies of a rotation over the first rot_dim dimensions: theta^(-2i/rot_dim) radians a position, or freq[i]."""
+    out = Rope()
+    f = None
+    if freq is not None:
+        _want(len(freq) == rot_dim // 2, "mtp_rope_init")
+        f = (ctypes.c_double * max(len(freq), 1))(*[float(x) for x in freq])
+    _check(lib().mtp_rope_init(int(rot_dim), float(theta), f, ctypes.byref(out)), "mtp_rope_init")
+    return out
+
+
+def _f32(where: str, *tensors, n):
+    """Contiguous float32 tensors of n elements (None passes)."""
+    f32 = _t().float32
+    for t in tensors:
+        if t is not None and (t.dtype is not f32 or not t.is_contiguous() or t.numel() != n):
+            raise MTPError(9, where)
+
+
+def kv_q4_append_rope(cache: PagedCache, q, k, v, rope: Rope, pos, slot, q_out, k_out=None, q_norm=None, k_norm=None,
+                      eps: float = 1e-6, status=None, stream=None):
+    """q [tokens, n_q, head_dim], k, v [tokens, n_kv, head_dim], fp32 or bf16, the last dimension contiguous; pos, slot
+    [tokens] int32; q_out, k_out: contiguous like q and k (k_out optional); q_norm, k_norm [head_dim] float (None: no norm);
+    rope: mtp_rope(...). See kv_q4_append_rope in include/mtp.h."""
+    tokens, n_q, dh = q.shape
+    shape = (tokens, cache.n_kv, cache.head_dim)
+    _want(k.shape == shape and v.shape == shape and dh == cache.head_dim and q.stride(2) == 1 and k.stride(2) == 1
+          and v.stride(2) == 1 and q_out.shape == q.shape and q_out.is_contiguous()
+          and (k_out is None or (k_out.shape == shape and k_out.is_contiguous())), "kv_q4_append_rope")
+    _whole("kv_q4_append_rope", pos, slot, n=tokens)
+    _f32("kv_q4_append_rope", q_norm, k_norm, n=dh)
+    dt = _dtype_q4("kv_q4_append_rope", q, k, v, q_out) if k_out is None else _dtype_q4("kv_q4_append_rope", q, k, v, q_out, k_out)
+    rc = lib().kv_q4_append_rope(_stream(stream), cache.ref, tokens, n_q, _ptr(q), q.stride(0), q.stride(1), _ptr(k),
+                                 k.stride(0), k.stride(1), _ptr(v), v.stride(0), v.stride(1), dt, _ptr(q_norm), _ptr(k_norm),
+                                 eps, ctypes.byref(rope), _ptr(pos), _ptr(slot), _ptr(q_out), _ptr(k_out), _ptr(status))
+    _check(rc, "kv_q4_append_rope")
+
+
+def kv_tree_plan(parent, start, length, pos, mask, window: int = 0, status=None, stream=None):
+    """parent, pos [tokens], start [rows + 1], length [rows], mask [tokens, MTP_TREE_MAX / 32], all int32. See kv_tree_plan
+    in include/mtp.h."""
+    tokens, rows = parent.numel(), length.numel()
+    _whole("kv_tree_plan", parent, pos, n=tokens)
+    _whole("kv_tree_plan", mask, n=tokens * (MTP_TREE_MAX // 32))
+    _whole("kv_tree_plan", start, n=rows + 1)
+    _whole("kv_tree_plan", length)
+    rc = lib().kv_tree_plan(_stream(stream), rows, tokens, _ptr(parent), _ptr(start), _ptr(length), window, _ptr(pos),
+                            _ptr(mask), _ptr(status))
+    _check(rc, "kv_tree_plan")
+
+
+def kv_q4_attend_tree(cache: PagedCache, q, table, start, length, mask, out, workspace, max_q: int, scale: float,
+                      window: int = 0, pos=None, lse=None, status=None, stream=None):
+    """kv_q4_attend for trees: mask [tokens, MTP_TREE_MAX / 32] and pos [tokens] (with a window) int32, kv_tree_plan's;
+    the other arguments as there."""
+    tokens, n_q, dh = q.shape
+    rows, max_pages = table.shape
+    _want(dh == cache.head_dim and q.stride(2) == 1 and out.shape == q.shape and out.is_contiguous(), "kv_q4_attend_tree")
+    _f32("kv_q4_attend_tree", lse, n=tokens * n_q)
+    _whole("kv_q4_attend_tree", table)
+    _whole("kv_q4_attend_tree", start, n=rows + 1)
+    _whole("kv_q4_attend_tree", length, n=rows)
+    _whole("kv_q4_attend_tree", mask, n=tokens * (MTP_TREE_MAX // 32))
+    _whole("kv_q4_attend_tree", pos, n=tokens)
+    dt = _dtype_q4("kv_q4_attend_tree", q, out)
+    _want(workspace.nbytes >= _attend_bytes(_device(), cache.n_kv, dh, n_q, max_q, dt), "kv_q4_attend_tree")
+    rc = lib().kv_q4_attend_tree(_stream(stream), cache.ref, rows, n_q, tokens, _ptr(q), q.stride(0), q.stride(1), dt,
+                                 _ptr(table), max_pages, _ptr(start), _ptr(length), _ptr(mask), _ptr(pos), max_q, scale,
+                                 window, _ptr(out), _ptr(lse), _ptr(status), _ptr(workspace))
+    _check(rc, "kv_q4_attend_tree")
+
+
+class PagedCaches:
+    """The layers of one kv_q4_tree_commit: an array of kv_q4_cache and the tensors it points to."""
+
+    def __init__(self, caches):
+        self.n = len(caches)
+        self.c = (Q4Cache * max(self.n, 1))(*[x.c for x in caches])
+        self._keep = list(caches)
+
+
+def kv_q4_caches(caches) -> PagedCaches:
+    """caches: the layers' PagedCache objects, of one shape, at most MTP_MAX_CACHES."""
+    return PagedCaches(caches)
+
+
+def kv_q4_tree_commit(caches: PagedCaches, table, start, length, parent, tok, choice, n_acc, out_tok, keep, path=None,
+                      status=None, stream=None):
+    """table [rows, max_pages], start [rows + 1], length, n_acc, keep [rows], parent, tok, choice [tokens], out_tok and
+    path [rows, max_path], all int32. See kv_q4_tree_commit in include/mtp.h."""
+    rows, max_path = out_tok.shape
+    tokens, max_pages = parent.numel(), 1 if table is None else table.shape[1]
+    _want(table is None or table.shape[0] == rows, "kv_q4_tree_commit")
+    _whole("kv_q4_tree_commit", table, out_tok)
+    _whole("kv_q4_tree_commit", start, n=rows + 1)
+    _whole("kv_q4_tree_commit", length, n_acc, keep, n=rows)
+    _whole("kv_q4_tree_commit", parent, tok, choice, n=tokens)
+    _whole("kv_q4_tree_commit", path, n=rows * max_path)
+    rc = lib().kv_q4_tree_commit(_stream(stream), caches.c, caches.n, rows, tokens, _ptr(table), max_pages, _ptr(start),
+                                 _ptr(length), _ptr(parent), _ptr(tok), _ptr(choice), max_path, _ptr(n_acc), _ptr(out_tok),
+                                 _ptr(keep), _ptr(path), _ptr(status))
+    _check(rc, "kv_q4_tree_commit")
+
+
+def kv_attend_prompt_workspace_bytes(tokens: int, rows: int) -> int:
+    return lib().kv_attend_prompt_workspace_bytes(tokens, rows)
+
+
+def kv_attend_prompt(q, k, v, start, out, workspace, max_len: int, scale: float, window: int = 0, lse=None, status=None,
+                     stream=None):
+    """q [tokens, n_q, head_dim], k, v [tokens, n_kv, head_dim], fp32 or bf16, the last dimension contiguous, 16-byte aligned
+    rows; start [rows + 1] int32; out like q, contiguous; lse [tokens, n_q] float; workspace:
+    kv_attend_prompt_workspace_bytes(tokens, rows) bytes. See kv_attend_prompt in include/mtp.h."""
+    tokens, n_q, dh = q.shape
+    rows, n_kv = start.numel() - 1, k.shape[1]
+    _want(k.shape == (tokens, n_kv, dh) and v.shape == k.shape and q.stride(2) == 1 and k.stride(2) == 1 and v.stride(2) == 1
+          and out.shape == q.shape and out.is_contiguous(), "kv_attend_prompt")
+    _f32("kv_attend_prompt", lse, n=tokens * n_q)
+    _whole("kv_attend_prompt", start)
+    dt = _dtype_q4("kv_attend_prompt", q, k, v, out)
+    _want(workspace.nbytes >= _prompt_bytes(tokens, rows), "kv_attend_prompt")
+    rc = lib().kv_attend_prompt(_stream(stream), rows, n_q, n_kv, dh, tokens, _ptr(q), q.stride(0), q.stride(1), _ptr(k),
+                                k.stride(0), k.stride(1), _ptr(v), v.stride(0), v.stride(1), dt, _ptr(start), max_len, scale,
+                                window, _ptr(out), _ptr(lse), _ptr(status), _ptr(workspace))
+    _check(rc, "kv_attend_prompt")
 
 
 PROFILE_KINDS = ("fc", "qkv", "qkv_post", "attention", "o_proj", "gate_up", "down", "lm_head", "sample",

@@ -1,0 +1,308 @@
+// Causal attention of whole packed prompts over unrounded keys and values
+// (kv_attend_prompt).
+//
+//   s_ij = scale q_i . k_j,  out_i = sum_j softmax(s_i)_j v_j,  j <= i (and > i - window)
+//
+// in one pass over the keys with the running maximum and sum of each query.
+#include <algorithm>
+#include <cmath>
+#include <mutex>
+
+#include "common.cuh"
+#include "kernels.h"
+#include "prompt_tiles.h"
+
+namespace mtp {
+
+namespace {
+
+struct PromptArgs {
+  const void *q, *k, *v;
+  long long ts[3], hs[3];  // strides of Q, K, V in elements
+  const int32_t* start;
+  void* out;
+  float* lse;
+  int32_t* status;
+  int rows, n_q, n_kv, tokens, window;
+  float scale;
+};
+
+// The row and the query tile of tile number x, counted from the last row's last
+// tile (a row's later tiles are its longest); false past the first. By a whole
+// warp, rows in consecutive groups per lane.
+__device__ __forceinline__ bool find_tile(const PromptArgs& a, int tile, int x, int& a0, int& n, int& j) {
+  const int lane = threadIdx.x & 31, per = (a.rows + 31) / 32, r0 = min(lane * per, a.rows), r1 = min(r0 + per, a.rows);
+  int sum = 0, b0, m;
+#pragma unroll 4
+  for (int r = r0; r < r1; ++r) {
+    prompt_row(a.start, a.tokens, r, b0, m);
+    sum += prompt_tiles(m, tile);
+  }
+  int inc = sum;
+#pragma unroll
+  for (int o = 1; o < 32; o <<= 1) {
+    const int u = __shfl_up_sync(0xFFFFFFFFu, inc, o);
+    if (lane >= o) inc += u;
+  }
+  const int all = __shfl_sync(0xFFFFFFFFu, inc, 31);
+  if (x >= all) return false;
+  x = all - 1 - x;
+  const int owner = __ffs(__ballot_sync(0xFFFFFFFFu, inc - sum <= x && x < inc)) - 1;
+  int at = __shfl_sync(0xFFFFFFFFu, inc - sum, owner), r = __shfl_sync(0xFFFFFFFFu, r0, owner);
+  for (;; ++r) {
+    prompt_row(a.start, a.tokens, r, a0, n);
+    const int t = prompt_tiles(n, tile);
+    if (x < at + t) break;
+    at += t;
+  }
+  j = x - at;
+  return true;
+}
+
+// ------------------------------------------------------------ CUDA cores
+
+constexpr int kSimtRows = 64, kSimtKeys = 32, kSimtThreads = 256;
+
+template <int DH>
+constexpr int simt_smem() { return ((kSimtRows + 2 * kSimtKeys) * (DH + 4) + kSimtRows * (kSimtKeys + 4)) * 4; }
+
+// 64 queries of a head against 32 keys at a time, all in fp32. Thread (ty, tx)
+// of 16 x 16 has the scores of 4 queries with 2 keys, then 4 queries' outputs
+// in DH / 16 dimensions: 32 products per 8 shared-memory accesses of a warp,
+// which is what the multiply-add units and shared memory sustain together.
+template <int DH, int DT>
+__global__ void __launch_bounds__(kSimtThreads) k_prompt_simt(const __grid_constant__ PromptArgs a) {
+  constexpr int kS = DH + 4, kPS = kSimtKeys + 4, kD = DH / 64;
+  extern __shared__ __align__(16) float smem[];
+  float *sq = smem, *sk = sq + kSimtRows * kS, *sv = sk + kSimtKeys * kS, *sp = sv + kSimtKeys * kS;
+  __shared__ int s_at[4];
+  pdl_wait();
+  pdl_trigger();
+  const int tid = threadIdx.x, tx = tid & 15, ty = tid >> 4, h = blockIdx.x % a.n_q, g = h / (a.n_q / a.n_kv);
+  if (tid < 32) {
+    int a0 = 0, n = 0, j = 0;
+    const bool some = find_tile(a, kSimtRows, blockIdx.x / a.n_q, a0, n, j);
+    if (tid == 0) {
+      s_at[0] = a0;
+      s_at[1] = some ? n : 0;
+      s_at[2] = j;
+    }
+  }
+  __syncthreads();
+  const int a0 = s_at[0], n = s_at[1], i0 = s_at[2] * kSimtRows;
+  if (n == 0) return;
+  const int rows = min(n - i0, kSimtRows);
+  auto stage = [&](float* dst, int side, const void* src, int head, int first, int count, int most) {
+    for (int e = tid; e < most * (DH / 4); e += kSimtThreads) {
+      const int r = e / (DH / 4), d = e % (DH / 4) * 4;
+      float4 x = make_float4(0.f, 0.f, 0.f, 0.f);
+      if (r < count) {
+        const long long at = (long long)(a0 + first + r) * a.ts[side] + (long long)head * a.hs[side] + d;
+        if (DT == MTP_DTYPE_F32) {
+          x = *reinterpret_cast<const float4*>(static_cast<const float*>(src) + at);
+        } else {
+          const uint2 w = *reinterpret_cast<const uint2*>(static_cast<const uint16_t*>(src) + at);
+          x = make_float4(bf16lo(w.x), bf16hi(w.x), bf16lo(w.y), bf16hi(w.y));
+        }
+      }
+      *reinterpret_cast<float4*>(dst + r * kS + d) = x;
+    }
+  };
+  stage(sq, 0, a.q, h, i0, rows, kSimtRows);
+  const float c = a.scale * 1.44269504f;
+  float m[4], l[4], o[4][kD][4];
+#pragma unroll
+  for (int r = 0; r < 4; ++r) {
+    m[r] = -INFINITY;
+    l[r] = 0.f;
+#pragma unroll
+    for (int d = 0; d < kD; ++d)
+#pragma unroll
+      for (int e = 0; e < 4; ++e) o[r][d][e] = 0.f;
+  }
+  const int first = a.window > 0 ? max(0, i0 + 1 - a.window) / kSimtKeys * kSimtKeys : 0, last = i0 + rows;
+  for (int t0 = first; t0 < last; t0 += kSimtKeys) {
+    __syncthreads();
+    stage(sk, 1, a.k, g, t0, min(n - t0, kSimtKeys), kSimtKeys);
+    stage(sv, 2, a.v, g, t0, min(n - t0, kSimtKeys), kSimtKeys);
+    __syncthreads();
+    float s[4][2];
+#pragma unroll
+    for (int r = 0; r < 4; ++r) s[r][0] = s[r][1] = 0.f;
+#pragma unroll 4
+    for (int d = 0; d < DH; d += 4) {
+      float4 qv[4], kv[2];
+#pragma unroll
+      for (int r = 0; r < 4; ++r) qv[r] = *reinterpret_cast<const float4*>(sq + (4 * ty + r) * kS + d);
+#pragma unroll
+      for (int b = 0; b < 2; ++b) kv[b] = *reinterpret_cast<const float4*>(sk + (tx + 16 * b) * kS + d);
+#pragma unroll
+      for (int r = 0; r < 4; ++r)
+#pragma unroll
+        for (int b = 0; b < 2; ++b)
+          s[r][b] = fmaf(qv[r].x, kv[b].x, fmaf(qv[r].y, kv[b].y, fmaf(qv[r].z, kv[b].z, fmaf(qv[r].w, kv[b].w, s[r][b]))));
+    }
+    const bool edge = t0 + kSimtKeys > i0 + 1 || (a.window > 0 && t0 <= i0 + kSimtRows - 1 - a.window);
+#pragma unroll
+    for (int r = 0; r < 4; ++r) {
+      const int i = i0 + 4 * ty + r;
+      bool gone[2];
+#pragma unroll
+      for (int b = 0; b < 2; ++b) {
+        const int t = t0 + tx + 16 * b;
+        gone[b] = t > i || (a.window > 0 && t <= i - a.window);
+        s[r][b] = gone[b] ? -INFINITY : s[r][b] * c;
+      }
+      float mx = fmaxf(s[r][0], s[r][1]);
+#pragma unroll
+      for (int w = 1; w < 16; w <<= 1) mx = fmaxf(mx, __shfl_xor_sync(0xFFFFFFFFu, mx, w));
+      const float nm = fmaxf(m[r], mx), from = nm == -INFINITY ? 0.f : nm;
+      const float f = m[r] == nm ? 1.f : exp2f(m[r] - from);
+      float sum = 0.f;
+#pragma unroll
+      for (int b = 0; b < 2; ++b) {
+        const float p = exp2f(s[r][b] - from);
+        if (!gone[b]) sum += p;
+        sp[(4 * ty + r) * kPS + tx + 16 * b] = gone[b] ? -1.f : p;  // (-1: out of sight, whatever V holds there)
+      }
+#pragma unroll
+      for (int w = 1; w < 16; w <<= 1) sum += __shfl_xor_sync(0xFFFFFFFFu, sum, w);
+      l[r] = fmaf(l[r], f, sum);
+      m[r] = nm;
+#pragma unroll
+      for (int d = 0; d < kD; ++d)
+#pragma unroll
+        for (int e = 0; e < 4; ++e) o[r][d][e] *= f;
+    }
+    __syncwarp();  // (a query's 16 threads are one warp's)
+    auto add = [&](auto edges) {
+#pragma unroll 2
+      for (int t = 0; t < kSimtKeys; t += 4) {
+        float4 p[4];
+#pragma unroll
+        for (int r = 0; r < 4; ++r) p[r] = *reinterpret_cast<const float4*>(sp + (4 * ty + r) * kPS + t);
+#pragma unroll
+        for (int u = 0; u < 4; ++u) {
+          float pu[4];
+#pragma unroll
+          for (int r = 0; r < 4; ++r) pu[r] = u == 0 ? p[r].x : (u == 1 ? p[r].y : (u == 2 ? p[r].z : p[r].w));
+#pragma unroll
+          for (int d = 0; d < kD; ++d) {
+            const float4 v = *reinterpret_cast<const float4*>(sv + (t + u) * kS + 64 * d + 4 * tx);
+#pragma unroll
+            for (int r = 0; r < 4; ++r) {
+              if (decltype(edges)::value && pu[r] < 0.f) continue;
+              o[r][d][0] = fmaf(pu[r], v.x, o[r][d][0]);
+              o[r][d][1] = fmaf(pu[r], v.y, o[r][d][1]);
+              o[r][d][2] = fmaf(pu[r], v.z, o[r][d][2]);
+              o[r][d][3] = fmaf(pu[r], v.w, o[r][d][3]);
+            }
+          }
+        }
+      }
+    };
+    if (edge) add(std::true_type{});
+    else add(std::false_type{});
+  }
+#pragma unroll
+  for (int r = 0; r < 4; ++r) {
+    const int i = i0 + 4 * ty + r;
+    if (i >= n) continue;
+    const long long at = (long long)(a0 + i) * a.n_q + h;
+    const float f = l[r] != 0.f ? 1.f / l[r] : 0.f;
+    if (tx == 0 && a.lse) a.lse[at] = l[r] != 0.f ? (m[r] + log2f(l[r])) * 0.693147181f : -INFINITY;
+#pragma unroll
+    for (int d = 0; d < kD; ++d) {
+      const float y[4] = {o[r][d][0] * f, o[r][d][1] * f, o[r][d][2] * f, o[r][d][3] * f};
+      const long long to = at * DH + 64 * d + 4 * tx;
+      if (DT == MTP_DTYPE_F32) {
+        *reinterpret_cast<float4*>(static_cast<float*>(a.out) + to) = make_float4(y[0], y[1], y[2], y[3]);
+      } else {
+        uint2 w;
+        asm("cvt.rn.bf16x2.f32 %0, %1, %2;" : "=r"(w.x) : "f"(y[1]), "f"(y[0]));
+        asm("cvt.rn.bf16x2.f32 %0, %1, %2;" : "=r"(w.y) : "f"(y[3]), "f"(y[2]));
+        *reinterpret_cast<uint2*>(static_cast<uint16_t*>(a.out) + to) = w;
+      }
+    }
+  }
+}
+
+// A kernel's dynamic shared memory limit, raised once per device.
+template <typename K>
+cudaError_t raise_smem(K k, int bytes, bool (&set)[kMaxDevices], std::mutex& mu) {
+  int dev = 0;
+  cudaGetDevice(&dev);
+  if (dev < 0 || dev >= kMaxDevices) dev = 0;
+  std::lock_guard<std::mutex> lock(mu);
+  if (set[dev]) return cudaSuccess;
+  const cudaError_t e = cudaFuncSetAttribute(k, cudaFuncAttributeMaxDynamicSharedMemorySize, bytes);
+  if (e != cudaSuccess) cudaGetLastError();
+  else set[dev] = true;
+  return e;
+}
+
+template <int DH, int DT>
+cudaError_t launch_simt(const PromptArgs& a, cudaStream_t s) {
+  static std::mutex mu;
+  static bool set[kMaxDevices] = {};
+  const cudaError_t e = raise_smem(k_prompt_simt<DH, DT>, simt_smem<DH>(), set, mu);
+  if (e != cudaSuccess) return e;
+  count_launch();
+  return launch_pdl(k_prompt_simt<DH, DT>, dim3((unsigned)(prompt_most_tiles(a.tokens, a.rows, kSimtRows) * a.n_q)),
+                    dim3(kSimtThreads), simt_smem<DH>(), s, a);
+}
+
+}  // namespace
+}  // namespace mtp
+
+using namespace mtp;
+
+extern "C" {
+
+size_t kv_attend_prompt_workspace_bytes(int32_t tokens, int32_t rows) {
+  if (tokens < 0 || rows < 1 || rows > 4096) return 0;
+  return 16;
+}
+
+mtp_status kv_attend_prompt(mtp_stream stream, int32_t rows, int32_t n_q, int32_t n_kv, int32_t head_dim,
+                            int32_t tokens, const void* d_q, int64_t q_tok_stride, int64_t q_head_stride,
+                            const void* d_k, int64_t k_tok_stride, int64_t k_head_stride, const void* d_v,
+                            int64_t v_tok_stride, int64_t v_head_stride, int32_t dtype, const int32_t* d_start,
+                            int32_t max_len, float scale, int32_t window, void* d_out, float* d_lse,
+                            int32_t* d_status, void* d_workspace) {
+  if (rows < 1 || rows > 4096 || n_kv < 1 || n_q < 1 || n_q > 1024 || n_q % n_kv != 0 ||
+      (head_dim != 64 && head_dim != 128 && head_dim != 256) || tokens < 0 || (long long)tokens * n_q >= (1LL << 31) ||
+      max_len < 1 || window < 0 || !std::isfinite(scale) || (dtype != MTP_DTYPE_BF16 && dtype != MTP_DTYPE_F32))
+    return MTP_ERR_BAD_ARG;
+  if (tokens == 0) return MTP_OK;
+  if (!d_q || !d_k || !d_v || !d_start || !d_out || !d_workspace) return MTP_ERR_BAD_ARG;
+  const int es = dtype == MTP_DTYPE_BF16 ? 2 : 4;
+  PromptArgs a{d_q, d_k, d_v, {q_tok_stride, k_tok_stride, v_tok_stride}, {q_head_stride, k_head_stride, v_head_stride},
+               d_start, d_out, d_lse, d_status, rows, n_q, n_kv, tokens, window, scale};
+  uintptr_t bits = reinterpret_cast<uintptr_t>(d_q) | reinterpret_cast<uintptr_t>(d_k) | reinterpret_cast<uintptr_t>(d_v) |
+                   reinterpret_cast<uintptr_t>(d_out) | reinterpret_cast<uintptr_t>(d_workspace);
+  for (int i = 0; i < 3; ++i) bits |= (uintptr_t)(a.ts[i] * es) | (uintptr_t)(a.hs[i] * es);
+  if ((bits & 15) != 0) return MTP_ERR_BAD_ARG;
+  // an output over an input would be read after it is written
+  const void* in[3] = {d_q, d_k, d_v};
+  for (int i = 0; i < 3; ++i) {
+    long long lo = 0, hi = head_dim;
+    for (const long long far : {(tokens - 1) * a.ts[i], ((i == 0 ? n_q : n_kv) - 1) * a.hs[i]}) {
+      lo += std::min(far, 0LL);
+      hi += std::max(far, 0LL);
+    }
+    const uint8_t *p = static_cast<const uint8_t*>(in[i]) + lo * es, *q = static_cast<const uint8_t*>(in[i]) + hi * es;
+    const uint8_t *o = static_cast<const uint8_t*>(d_out), *z = reinterpret_cast<const uint8_t*>(d_lse);
+    if (o < q && p < o + (size_t)tokens * n_q * head_dim * es) return MTP_ERR_BAD_ARG;
+    if (z && z < q && p < z + (size_t)tokens * n_q * 4) return MTP_ERR_BAD_ARG;
+  }
+  cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
+  cudaError_t e;
+  if (dtype == MTP_DTYPE_F32)
+    e = head_dim == 64 ? launch_simt<64, MTP_DTYPE_F32>(a, s) : head_dim == 128 ? launch_simt<128, MTP_DTYPE_F32>(a, s) : launch_simt<256, MTP_DTYPE_F32>(a, s);
+  else
+    e = head_dim == 64 ? launch_simt<64, MTP_DTYPE_BF16>(a, s) : head_dim == 128 ? launch_simt<128, MTP_DTYPE_BF16>(a, s) : launch_simt<256, MTP_DTYPE_BF16>(a, s);
+  return e == cudaSuccess ? MTP_OK : MTP_ERR_CUDA;
+}
+
+}  // extern "C"

@@ -1,4 +1,4 @@
-// kv_q4_attend: checks, the choice of the kernel's shape, and the join of the
+// kv_q4_attend and kv_q4_attend_tree: checks, the choice of the kernel's shape, and the join of the
 // partial results of query tiles that more than one block worked on.
 #include <algorithm>
 #include <cmath>
@@ -168,11 +168,12 @@ size_t kv_q4_attend_workspace_bytes(const kv_q4_cache* c, int32_t n_q, int32_t m
   return slots * (sizeof(int4) + rt * sizeof(float2)) + slots / 2 * 3 * rt * sizeof(float) * c->head_dim;
 }
 
-mtp_status kv_q4_attend(mtp_stream stream, const kv_q4_cache* c, int32_t rows, int32_t n_q, int32_t tokens,
-                        const void* d_q, int64_t tok_stride, int64_t head_stride, int32_t dtype,
-                        const int32_t* d_table, int32_t max_pages, const int32_t* d_start, const int32_t* d_len,
-                        int32_t max_q, float scale, int32_t window, void* d_out, float* d_lse, int32_t* d_status,
-                        void* d_workspace) {
+// Both entry points; d_mask makes the queries a tree's nodes.
+static mtp_status attend(mtp_stream stream, const kv_q4_cache* c, int32_t rows, int32_t n_q, int32_t tokens,
+                         const void* d_q, int64_t tok_stride, int64_t head_stride, int32_t dtype,
+                         const int32_t* d_table, int32_t max_pages, const int32_t* d_start, const int32_t* d_len,
+                         const int32_t* d_mask, const int32_t* d_place, int32_t max_q, float scale, int32_t window,
+                         void* d_out, float* d_lse, int32_t* d_status, void* d_workspace) {
   if (!q4_cache_ok(c) || rows < 1 || rows > 4096 || n_q < 1 || n_q > 1024 || n_q % c->n_kv != 0 || tokens < 0 ||
       (long long)tokens * n_q >= (1LL << 31) || max_pages < 1 || (long long)max_pages * c->page >= (1LL << 31) ||
       max_q < 1 || window < 0 || !std::isfinite(scale) || (dtype != MTP_DTYPE_BF16 && dtype != MTP_DTYPE_F32))
@@ -194,13 +195,14 @@ mtp_status kv_q4_attend(mtp_stream stream, const kv_q4_cache* c, int32_t rows, i
   Q4AttnArgs a{static_cast<const uint8_t*>(c->k), static_cast<const uint8_t*>(c->v), c->k_exp, c->v_exp, d_table,
                d_start, d_len, d_q, tok_stride, head_stride, d_out, d_lse, d_status, meta, ml,
                part_o, part_o + (size_t)2 * blocks * rt * c->head_dim, rows, n_q, c->n_kv, c->page, c->n_pages, max_pages, tokens, window, 0,
-               scale};
+               scale, d_mask, d_place};
   const uintptr_t bits = reinterpret_cast<uintptr_t>(d_q) | (uintptr_t)(tok_stride * es) | (uintptr_t)(head_stride * es);
   a.q_vec = (bits & 15) == 0;
   cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
-  cudaError_t e = c->head_dim == 64    ? launch_q4_attn_64(a, n, wide, blocks, s)
-                  : c->head_dim == 128 ? launch_q4_attn_128(a, n, wide, blocks, s)
-                                       : launch_q4_attn_256(a, n, wide, blocks, s);
+  auto launch = c->head_dim == 64    ? (d_mask ? launch_q4_tree_64 : launch_q4_attn_64)
+                : c->head_dim == 128 ? (d_mask ? launch_q4_tree_128 : launch_q4_attn_128)
+                                     : (d_mask ? launch_q4_tree_256 : launch_q4_attn_256);
+  cudaError_t e = launch(a, n, wide, blocks, s);
   if (e != cudaSuccess) return MTP_ERR_CUDA;
   void (*join)(Q4AttnArgs, int) =
       c->head_dim == 64    ? (wide ? k_q4_join<64, MTP_DTYPE_F32> : k_q4_join<64, MTP_DTYPE_BF16>)
@@ -211,6 +213,26 @@ mtp_status kv_q4_attend(mtp_stream stream, const kv_q4_cache* c, int32_t rows, i
   e = launch_pdl(join, dim3(blocks, used), dim3(kJoinThreads), 0, s, a, rt);
   count_launch();
   return e == cudaSuccess ? MTP_OK : MTP_ERR_CUDA;
+}
+
+mtp_status kv_q4_attend(mtp_stream stream, const kv_q4_cache* c, int32_t rows, int32_t n_q, int32_t tokens,
+                        const void* d_q, int64_t tok_stride, int64_t head_stride, int32_t dtype,
+                        const int32_t* d_table, int32_t max_pages, const int32_t* d_start, const int32_t* d_len,
+                        int32_t max_q, float scale, int32_t window, void* d_out, float* d_lse, int32_t* d_status,
+                        void* d_workspace) {
+  return attend(stream, c, rows, n_q, tokens, d_q, tok_stride, head_stride, dtype, d_table, max_pages, d_start, d_len,
+                nullptr, nullptr, max_q, scale, window, d_out, d_lse, d_status, d_workspace);
+}
+
+mtp_status kv_q4_attend_tree(mtp_stream stream, const kv_q4_cache* c, int32_t rows, int32_t n_q, int32_t tokens,
+                             const void* d_q, int64_t tok_stride, int64_t head_stride, int32_t dtype,
+                             const int32_t* d_table, int32_t max_pages, const int32_t* d_start, const int32_t* d_len,
+                             const int32_t* d_mask, const int32_t* d_pos, int32_t max_q, float scale, int32_t window,
+                             void* d_out, float* d_lse, int32_t* d_status, void* d_workspace) {
+  if (max_q > kTreeMost) return MTP_ERR_BAD_ARG;
+  if (tokens > 0 && (!d_mask || (reinterpret_cast<uintptr_t>(d_mask) & 15) != 0 || (window > 0 && !d_pos))) return MTP_ERR_BAD_ARG;
+  return attend(stream, c, rows, n_q, tokens, d_q, tok_stride, head_stride, dtype, d_table, max_pages, d_start, d_len,
+                d_mask, window > 0 ? d_pos : nullptr, max_q, scale, window, d_out, d_lse, d_status, d_workspace);
 }
 
 }  // extern "C"

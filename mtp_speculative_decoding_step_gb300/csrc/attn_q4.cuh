@@ -94,6 +94,7 @@ struct Q4AttnArgs {
   int rows, n_q, n_kv, page, n_pages, max_pages, tokens, window;
   int q_vec;                     // 16-byte loads of q are aligned
   float scale;
+  const int32_t *mask, *place;   // trees: bits of the nodes that a query sees; its position (NULL: no window)
 };
 
 // ------------------------------------------------------------ PTX
@@ -221,7 +222,7 @@ __device__ __forceinline__ bool group_any(int id, bool p) {
 
 constexpr int least(int a, int b) { return a < b ? a : b; }
 
-template <int DH, int N, bool WIDE>
+template <int DH, int N, bool WIDE, bool TREE = false>
 struct Shape {
   static constexpr int kRow = q4_row_bytes(DH);
   static constexpr int RT = WIDE ? N / 2 : N;            // query rows per tile
@@ -242,8 +243,8 @@ struct Shape {
   static constexpr int kRaw = kT * kRow;                 // a tile's rows of K or V
   static constexpr int VB = DH == 256 ? 1 : 2;           // V tiles in shared memory
   static constexpr int kV = kT * DH * 2, kQ = N * DH * 2, kP = N * kT * 2;  // (SB buffers of P)
-  static constexpr int kMetaBytes = 8704;
-  static constexpr int kRoom = (227 * 1024 - kMetaBytes - VB * kV - kQ - SB * kP) / kRaw;
+  static constexpr int kMetaBytes = 8704, kTreeBytes = TREE ? 128 * 16 : 0;  // (masks of a tile's query rows)
+  static constexpr int kRoom = (227 * 1024 - kMetaBytes - kTreeBytes - VB * kV - kQ - SB * kP) / kRaw;
   // ring stages; even counts for two dequantising groups, so that each group
   // meets every phase of its stages' barriers
   static constexpr int kMost = 8;
@@ -251,7 +252,7 @@ struct Shape {
   static constexpr int VS = least(kMost, SG == 2 ? kRoom / 2 : (kRoom - KS) / 2 * 2);  // V waits longer than K
   static constexpr int oV = 0, oQ = VB * kV, oP = oQ + kQ, oRawK = oP + SB * kP, oRawV = oRawK + KS * kRaw;
   static constexpr int oMeta = (oRawV + VS * kRaw + 127) / 128 * 128;
-  static constexpr int kSmem = oMeta + kMetaBytes;
+  static constexpr int oTree = oMeta + kMetaBytes, kSmem = oTree + kTreeBytes;
   static_assert(VS >= 1 && KS <= kMost && VS <= kMost && KS + VS <= kRoom && cEnd <= 512 && (SG == 2 || (KS % 2 == 0 && VS % 2 == 0)), "shape");
 };
 
@@ -338,10 +339,10 @@ __device__ __forceinline__ bool wait(uint64_t* bar, uint32_t parity, volatile in
 __device__ __forceinline__ void pin(uint32_t& x) { asm volatile("" : "+r"(x)); }
 
 // Whether a query at `pos` sees a position of an edge tile whose V is NaN in
-// 16-dimension block b.
-template <int B>
+// 16-dimension block b. (Trees: `mask` has the query's bits of the n positions from base on.)
+template <int B, bool TREE>
 __device__ __noinline__ bool sees_nan(int first, int t0, int cnt, int p0, int p1, const uint32_t (*bits)[B][4], int b, int pos,
-                                      int window) {
+                                      int window, const uint32_t* mask, int base, int n) {
   Run s;
   s.first = first;
   s.p0 = p0;
@@ -353,7 +354,11 @@ __device__ __noinline__ bool sees_nan(int first, int t0, int cnt, int p0, int p1
       while (m) {
         const int t = tile * kT + 32 * w + __ffs(m) - 1;
         m &= m - 1;
-        if (t <= pos && (window == 0 || pos - t < window)) return true;
+        if (TREE && t >= base) {
+          if (t - base < n && (mask[(t - base) >> 5] >> ((t - base) & 31) & 1)) return true;
+        } else if (t <= pos && (window == 0 || pos - t < window)) {
+          return true;
+        }
       }
     }
   }
@@ -364,9 +369,9 @@ __device__ __noinline__ bool sees_nan(int first, int t0, int cnt, int p0, int p1
 // of those before (`first`: nothing), or back from there at the share's `end`.
 // Out of line with all its addresses: few shares come here, and the loop over
 // tiles needs the registers (with them inside, prompts took 760 us, not 713).
-template <int DH, int N, bool WIDE>
+template <int DH, int N, bool WIDE, bool TREE>
 __device__ __noinline__ void add_far(const Q4AttnArgs* a, Meta<DH>* M, int sg, bool first, bool end) {
-  using S = Shape<DH, N, WIDE>;
+  using S = Shape<DH, N, WIDE, TREE>;
   const int me = threadIdx.x & 127, quarter = me >> 5, c0 = sg * S::NC;
   if (me < S::NC) {
     const int col = c0 + me;
@@ -408,9 +413,9 @@ __device__ __noinline__ void add_far(const Q4AttnArgs* a, Meta<DH>* M, int sg, b
   if (end) tc_wait_st();
 }
 
-template <int DH, int N, bool WIDE>
+template <int DH, int N, bool WIDE, bool TREE>
 __global__ void __launch_bounds__(kAttnThreads, 1) k_q4_attn(const __grid_constant__ Q4AttnArgs a) {
-  using S = Shape<DH, N, WIDE>;
+  using S = Shape<DH, N, WIDE, TREE>;
   extern __shared__ __align__(1024) uint8_t smem_raw[];  // (swizzled operands go by address bits 7 to 9)
   uint8_t* const base = smem_raw;
   auto& M = *reinterpret_cast<Meta<DH>*>(base + S::oMeta);
@@ -479,7 +484,7 @@ __global__ void __launch_bounds__(kAttnThreads, 1) k_q4_attn(const __grid_consta
     // Every (row, KV head, query tile, 128-position tile) is a task; each block
     // owns an equal stretch of them. The rows' task counts are scanned, rows
     // in consecutive groups per lane.
-    const Walk<Q4AttnArgs> walk{&a, a.n_q / a.n_kv, S::RT};
+    const Walk<Q4AttnArgs, TREE> walk{&a, a.n_q / a.n_kv, S::RT};
     // (by the lane that hands out the shares, so that its arrival orders these
     // stores before those of the warps that take a share)
     if (lane == 0) a.part_meta[2 * blockIdx.x] = a.part_meta[2 * blockIdx.x + 1] = make_int4(0, 0, 0, 0);
@@ -491,6 +496,7 @@ __global__ void __launch_bounds__(kAttnThreads, 1) k_q4_attn(const __grid_consta
     for (int r = r0; r < r1; ++r) {
       walk.row(r, a0, n, L);
       if (blockIdx.x == 0 && L != a.len[r]) flag_status(a.status, MTP_ERR_BAD_ARG);
+      if (TREE && blockIdx.x == 0 && min(a.start[r + 1], a.tokens) - a0 > kTreeMost) flag_status(a.status, MTP_ERR_BAD_ARG);
       ph = walk.per_head(n, L);
       sum += ph * a.n_kv;
     }
@@ -568,8 +574,8 @@ __global__ void __launch_bounds__(kAttnThreads, 1) k_q4_attn(const __grid_consta
       s.a0 = a0;
       s.n = n;
       s.pos = L - n;
-      s.p0 = s.pos + j * S::RT / walk.G;
-      s.p1 = s.pos + (min(n * walk.G, (j + 1) * S::RT) - 1) / walk.G;
+      s.p0 = TREE ? s.pos - 1 : s.pos + j * S::RT / walk.G;
+      s.p1 = TREE ? s.pos + n - 1 : s.pos + (min(n * walk.G, (j + 1) * S::RT) - 1) / walk.G;
       s.tile = s.first + (int)o;
       s.nt = (int)min(cnt - o, left);
       s.flags = (o == 0 ? 1 : 0) | (o + s.nt == cnt ? 2 : 0) | (s.nt == left ? 4 : 0);
@@ -897,6 +903,16 @@ __global__ void __launch_bounds__(kAttnThreads, 1) k_q4_attn(const __grid_consta
     bool ok = true;  // (a warp that fails leaves with its group, at a vote)
     Run s;
     s.flags = 0;
+    uint4* const tree = reinterpret_cast<uint4*>(base + S::oTree);
+    // whether a position is out of sight of the query of column `col`, whose place is `lim`
+    const unsigned w = a.window > 0 ? (unsigned)a.window : 0x80000000u;
+    auto hidden = [&](int t, int lim, int col) {
+      if constexpr (TREE) {
+        const int d = t - s.pos;
+        if (d >= 0) return !((unsigned)d < (unsigned)kTreeMost && (reinterpret_cast<const uint32_t*>(&tree[col])[d >> 5] >> (d & 31) & 1));
+      }
+      return (unsigned)(lim - t) >= w;
+    };
 #pragma unroll 1
     for (; !(s.flags & 4); ++run) {
       ok = next(run, s);
@@ -974,6 +990,20 @@ __global__ void __launch_bounds__(kAttnThreads, 1) k_q4_attn(const __grid_consta
             M.cm[j][0] = ldexpf(a.scale * 1.44269504f, kexp - (13 - ex));
             M.cm[j][1] = kUnset;
             M.lim[j] = real ? s.pos + i : -1;
+            if constexpr (TREE) {
+              uint4 m = make_uint4(0u, 0u, 0u, 0u);
+              if (real) {
+                m = reinterpret_cast<const uint4*>(a.mask)[s.a0 + i];
+                // bits of nodes that the row does not have
+                const int n = s.n;
+                m.x &= n >= 32 ? ~0u : (1u << n) - 1;
+                m.y &= n >= 64 ? ~0u : (n > 32 ? (1u << (n - 32)) - 1 : 0u);
+                m.z &= n >= 96 ? ~0u : (n > 64 ? (1u << (n - 64)) - 1 : 0u);
+                m.w &= n >= 128 ? ~0u : (n > 96 ? (1u << (n - 96)) - 1 : 0u);
+                M.lim[j] = a.place ? min(max(a.place[s.a0 + i], s.pos), s.pos + n - 1) : s.pos + n - 1;
+              }
+              tree[j] = m;
+            }
             M.dst[j] = real ? (s.a0 + i) * a.n_q + h : -1;
           }
         }
@@ -992,7 +1022,7 @@ __global__ void __launch_bounds__(kAttnThreads, 1) k_q4_attn(const __grid_consta
           ok = wait(&M.p_empty[(it - 1) % S::SB], (it - 1) / S::SB & 1, fail) && ok;
           if (group_any(bar, !ok)) { broken = true; break; }
           tc_fence_after();
-          add_far<DH, N, WIDE>(&a, &M, sg, i == S::kFar, false);
+          add_far<DH, N, WIDE, TREE>(&a, &M, sg, i == S::kFar, false);
         }
         const uint32_t sb = it % S::SB;
         ok = wait(&M.s_full[sb], (it / S::SB) & 1, fail) && ok;
@@ -1041,13 +1071,12 @@ __global__ void __launch_bounds__(kAttnThreads, 1) k_q4_attn(const __grid_consta
             }
             if (edge) {
               const int2 lim = *reinterpret_cast<const int2*>(&M.lim[c0 + 8 * b + pr]);
-              const unsigned w = a.window > 0 ? (unsigned)a.window : 0x80000000u;
 #pragma unroll
               for (int k = 0; k < 4; ++k) {
                 const int t = t0 + 32 * quarter + 8 * k + (lane >> 2);
                 uint32_t &x0 = v[k >> 1][4 * b + 2 * (k & 1)], &x1 = v[k >> 1][4 * b + 2 * (k & 1) + 1];
-                if ((unsigned)(lim.x - t) >= w) x0 = 0xFF800000u;  // -inf: out of sight
-                if ((unsigned)(lim.y - t) >= w) x1 = 0xFF800000u;
+                if (hidden(t, lim.x, c0 + 8 * b + pr)) x0 = 0xFF800000u;  // -inf
+                if (hidden(t, lim.y, c0 + 8 * b + pr + 1)) x1 = 0xFF800000u;
               }
             }
 #pragma unroll
@@ -1062,7 +1091,6 @@ __global__ void __launch_bounds__(kAttnThreads, 1) k_q4_attn(const __grid_consta
           for (int b = 0; b < NB; ++b) {
             const float4 cm = *reinterpret_cast<const float4*>(&M.cm[c0 + 8 * b + pr][0]);
             const int2 lim = *reinterpret_cast<const int2*>(&M.lim[c0 + 8 * b + pr]);
-            const unsigned w = a.window > 0 ? (unsigned)a.window : 0x80000000u;
             float y0 = -INFINITY, y1 = -INFINITY;
             uint32_t r[2][4], u[2][4];
 #pragma unroll
@@ -1084,8 +1112,8 @@ __global__ void __launch_bounds__(kAttnThreads, 1) k_q4_attn(const __grid_consta
                 z0 += __uint_as_float(u[k >> 1][e]);
                 z1 += __uint_as_float(u[k >> 1][e + 1]);
               }
-              if (!edge || (unsigned)(lim.x - t) < w) y0 = fmaxf(y0, z0 * cm.x);
-              if (!edge || (unsigned)(lim.y - t) < w) y1 = fmaxf(y1, z1 * cm.z);
+              if (!edge || !hidden(t, lim.x, c0 + 8 * b + pr)) y0 = fmaxf(y0, z0 * cm.x);
+              if (!edge || !hidden(t, lim.y, c0 + 8 * b + pr + 1)) y1 = fmaxf(y1, z1 * cm.z);
             }
 #pragma unroll
             for (int o = 4; o < 32; o <<= 1) {
@@ -1176,7 +1204,7 @@ __global__ void __launch_bounds__(kAttnThreads, 1) k_q4_attn(const __grid_consta
       ok = wait(&M.p_empty[(it - 1) % S::SB], (it - 1) / S::SB & 1, fail) && ok;
       if (group_any(bar, !ok)) break;
       tc_fence_after();
-      if (nt > S::kFar) add_far<DH, N, WIDE>(&a, &M, sg, false, true);
+      if (nt > S::kFar) add_far<DH, N, WIDE, TREE>(&a, &M, sg, false, true);
 #pragma unroll
       for (int b = 0; b < 2 * NB; ++b) {
         float y = sum[b];
@@ -1230,8 +1258,10 @@ __global__ void __launch_bounds__(kAttnThreads, 1) k_q4_attn(const __grid_consta
               uint32_t nan = 0;
 #pragma unroll 1
               for (int e = 0; e < kOut; ++e)
-                nan |= (uint32_t)sees_nan<DH / 16>(s.first, s.tile, nt, s.p0, s.p1, M.nan_bits[set], d / 16,
-                                                   M.lim[c0 + c + e], a.window) << e;
+                nan |= (uint32_t)sees_nan<DH / 16, TREE>(s.first, s.tile, nt, s.p0, s.p1, M.nan_bits[set], d / 16,
+                                                         M.lim[c0 + c + e], a.window,
+                                                         TREE ? reinterpret_cast<const uint32_t*>(&tree[c0 + c + e]) : nullptr,
+                                                         s.pos, s.n) << e;
 #pragma unroll
               for (int e = 0; e < kOut; ++e)
                 if (nan >> e & 1) o[e] = __int_as_float(0x7FC00000);
@@ -1273,10 +1303,10 @@ __global__ void __launch_bounds__(kAttnThreads, 1) k_q4_attn(const __grid_consta
     asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, %1;" ::"r"(tmem), "r"(S::kCols) : "memory");
 }
 
-template <int DH, int N, bool WIDE>
+template <int DH, int N, bool WIDE, bool TREE>
 cudaError_t launch_q4_attn_t(const Q4AttnArgs& a, int blocks, cudaStream_t s) {
-  using S = Shape<DH, N, WIDE>;
-  auto k = k_q4_attn<DH, N, WIDE>;
+  using S = Shape<DH, N, WIDE, TREE>;
+  auto k = k_q4_attn<DH, N, WIDE, TREE>;
   {
     // the dynamic shared memory limit, raised once per device
     static std::mutex mu;
@@ -1298,22 +1328,25 @@ cudaError_t launch_q4_attn_t(const Q4AttnArgs& a, int blocks, cudaStream_t s) {
   return launch_pdl(k, dim3(blocks), dim3(kAttnThreads), (size_t)S::kSmem, s, a);
 }
 
-template <int DH>
+template <int DH, bool TREE>
 cudaError_t launch_q4_attn(const Q4AttnArgs& a, int n, bool wide, int blocks, cudaStream_t s) {
   if (wide) {
-    if (n == 16) return launch_q4_attn_t<DH, 16, true>(a, blocks, s);
-    if (n == 32) return launch_q4_attn_t<DH, 32, true>(a, blocks, s);
-    return launch_q4_attn_t<DH, 64, true>(a, blocks, s);
+    if (n == 16) return launch_q4_attn_t<DH, 16, true, TREE>(a, blocks, s);
+    if (n == 32) return launch_q4_attn_t<DH, 32, true, TREE>(a, blocks, s);
+    return launch_q4_attn_t<DH, 64, true, TREE>(a, blocks, s);
   }
-  if (n == 16) return launch_q4_attn_t<DH, 16, false>(a, blocks, s);
-  if (n == 32) return launch_q4_attn_t<DH, 32, false>(a, blocks, s);
-  if (n == 64) return launch_q4_attn_t<DH, 64, false>(a, blocks, s);
-  return launch_q4_attn_t<DH, 128, false>(a, blocks, s);
+  if (n == 16) return launch_q4_attn_t<DH, 16, false, TREE>(a, blocks, s);
+  if (n == 32) return launch_q4_attn_t<DH, 32, false, TREE>(a, blocks, s);
+  if (n == 64) return launch_q4_attn_t<DH, 64, false, TREE>(a, blocks, s);
+  return launch_q4_attn_t<DH, 128, false, TREE>(a, blocks, s);
 }
 
-// One head dimension's kernels each (their own translation units).
+// One head dimension's kernels each, blocks of positions and trees (their own translation units).
 cudaError_t launch_q4_attn_64(const Q4AttnArgs& a, int n, bool wide, int blocks, cudaStream_t s);
 cudaError_t launch_q4_attn_128(const Q4AttnArgs& a, int n, bool wide, int blocks, cudaStream_t s);
 cudaError_t launch_q4_attn_256(const Q4AttnArgs& a, int n, bool wide, int blocks, cudaStream_t s);
+cudaError_t launch_q4_tree_64(const Q4AttnArgs& a, int n, bool wide, int blocks, cudaStream_t s);
+cudaError_t launch_q4_tree_128(const Q4AttnArgs& a, int n, bool wide, int blocks, cudaStream_t s);
+cudaError_t launch_q4_tree_256(const Q4AttnArgs& a, int n, bool wide, int blocks, cudaStream_t s);
 
 }  // namespace mtp

@@ -4,7 +4,7 @@
 namespace mtp {
 
 cudaError_t launch_q4_attn_128(const Q4AttnArgs& a, int n, bool wide, int blocks, cudaStream_t s) {
-  return launch_q4_attn<128>(a, n, wide, blocks, s);
+  return launch_q4_attn<128, false>(a, n, wide, blocks, s);
 }
 
 }  // namespace mtp

@@ -1,0 +1,641 @@
+// What a target's attention layer does between its projection and its
+// attention, in one pass (kv_q4_append_rope): norms of queries and keys per
+// head, the rotation by position, queries (and on request keys) out, K and V
+// into the paged 4-bit cache.
+//
+//   y = x rsqrt(mean(x^2) + eps) w                     (w: optional, with the norm)
+//   (z_i, z_{i+h}) = (y_i c - y_{i+h} s, y_{i+h} c + y_i s),  h = rot / 2, i < h
+//   c, s = cos, sin (pos f_i); dimensions from rot on pass through
+//
+// Angles. f_i is held as a fraction of a turn in units of 2^-64, so pos f_i
+// modulo a turn is one wrapping 64-bit product, exact but for f_i's own rounding
+// (2^-53 of it): position 2^20 turns as exactly as position 1. The nearest 64th of
+// a turn comes off and is looked up, the rest (0.05 radians at most) goes through
+// the first terms of the sine's and cosine's series; the two are joined by the
+// addition theorems. Everything is held in two floats, good to 2^-32.
+//
+// Keys go through the norm and the rotation in two floats each, because what is
+// kept of them is discrete: with results off by 2^-24 one of some 3 million
+// elements falls on the other side of a 4-bit border than the exact one. What
+// is compared with the borders is rounded to odd, so that no value that is not
+// on a border is taken for one that is. Queries, which are only rounded, are
+// fp32.
+//
+// Layout. A row of dh elements is dh / 8 lanes' work. A lane holds two runs of
+// four elements, A and B, such that a rotated pair is in one lane: A at 4 l and
+// B at h + 4 l for the first h / 4 lanes, the halves of what is not rotated in
+// the same way for the others. The sum of squares and the maxima of 16 elements
+// (four neighbouring lanes) are the only exchanges. That needs rot % 32 == 0 and
+// 4-element alignment; every other call takes the general kernel, which stages
+// a row in shared memory.
+//
+// V is what kv_q4_append makes of it, bit for bit.
+#include <algorithm>
+#include <cfloat>
+#include <cmath>
+
+#include "common.cuh"
+#include "kernels.h"
+#include "q4.cuh"
+
+namespace mtp {
+
+namespace {
+
+constexpr int kRopeThreads = 256;  // of the general kernel
+constexpr int kMostWarps = 12;     // of a block of the other, the one that makes the angles among them
+constexpr int kBatch = 4;          // rows of queries a group of lanes takes, loaded together
+
+struct RopeArgs {
+  const void* x[3];            // Q, K, V
+  long long ts[3], hs[3];      // strides in elements
+  void *q_out, *k_out;
+  const float* norm[2];        // of Q, K
+  uint8_t* cache[2];
+  const int32_t* exp[2];
+  const int32_t *pos, *slot;
+  int32_t* status;
+  int tokens, n_q, n_kv, page, n_slots;
+  int q_parts, parts;          // warps per position: those of its queries, all
+  float eps;
+  float2 quarter[17];          // cos of the 64ths of a turn up to a quarter, in two floats
+  mtp_rope rope;
+};
+
+// ------------------------------------------------------------ two floats
+
+// A value as hi + lo.
+struct Two {
+  float hi, lo;
+};
+
+__device__ __forceinline__ Two two_sum(float a, float b) {
+  const float s = __fadd_rn(a, b), t = __fsub_rn(s, a);
+  return {s, __fadd_rn(__fsub_rn(a, __fsub_rn(s, t)), __fsub_rn(b, t))};
+}
+
+// a b, plus c (small beside it), with hi the nearest float.
+__device__ __forceinline__ Two two_prod(float a, float b, float c) {
+  const float p = __fmul_rn(a, b);
+  return {p, __fadd_rn(__fmaf_rn(a, b, -p), c)};
+}
+
+// a c - b s; the low parts' products of low parts are left out (2^-48).
+__device__ __forceinline__ Two turn_one(Two a, Two b, float ch, float cl, float sh, float sl) {
+  const Two p = two_prod(a.hi, ch, __fmaf_rn(a.hi, cl, a.lo * ch)), q = two_prod(b.hi, sh, __fmaf_rn(b.hi, sl, b.lo * sh));
+  const Two r = two_sum(p.hi, -q.hi);
+  return {r.hi, __fadd_rn(r.lo, __fsub_rn(p.lo, q.lo))};
+}
+
+// The nearest float. (Where an infinity made the low part a NaN, the high one.)
+__device__ __forceinline__ float nearest(Two z) {
+  const float y = z.hi + z.lo;
+  return y == y ? y : z.hi;
+}
+
+// The value rounded to odd in 12 bits: cut off, with its last bit set where
+// something was. So it lies on the same side of any number of 11 bits or fewer as
+// the value, or on it as the value does.
+__device__ __forceinline__ float to_odd(Two z) {
+  const float y = nearest(z), rest = __fadd_rn(__fsub_rn(z.hi, y), z.lo);
+  // (a rest that points to 0 takes a step of y off before the cut; not finite: as it is)
+  const uint32_t u = __float_as_uint(y) - (rest * y < 0.f ? 1u : 0u);
+  return __uint_as_float((u & 0xFFFFF000u) | ((u & 0xFFFu) != 0 || (rest != 0.f && y != 0.f) ? 0x1000u : 0u));
+}
+
+struct CosSin {
+  float ch, cl, sh, sl;
+};
+
+// cos and sin of pos x turn.
+__device__ __forceinline__ CosSin turn_cs(int pos, uint64_t turn, const float2* quarter) {
+  const uint64_t p = (uint64_t)(uint32_t)pos * turn;
+  const uint32_t k = (uint32_t)((p + (1ull << 57)) >> 58) & 63;
+  const int64_t r = (int64_t)(p - ((uint64_t)k << 58));  // a 128th of a turn at most
+  // in radians: 2 pi = 6.28318548 - 1.74845553e-7 in two floats
+  const float rh = (float)r * 0x1p-64f, rl = (float)(r - (int64_t)(float)r) * 0x1p-64f;
+  const Two d = two_prod(rh, 6.28318548f, __fmaf_rn(rh, -1.74845553e-7f, rl * 6.28318548f));
+  const float d2 = d.hi * d.hi;
+  const float cc = d2 * __fmaf_rn(d2, -1.f / 24, 0.5f);                                     // 1 - cos
+  const float sl = __fmaf_rn(d.hi * d2, __fmaf_rn(d2, 1.f / 120, -1.f / 6), d.lo);          // sin - d.hi
+  const float2 C = quarter[k & 15], S = quarter[16 - (k & 15)];
+  const Two t = two_prod(S.x, d.hi, __fmaf_rn(S.x, sl, S.y * d.hi)), u = two_prod(C.x, d.hi, __fmaf_rn(C.x, sl, C.y * d.hi));
+  const Two a = two_sum(C.x, -t.hi), b = two_sum(S.x, u.hi);
+  const float al = a.lo + (C.y - t.lo - C.x * cc), bl = b.lo + (S.y + u.lo - S.x * cc);
+  const float ch = a.hi + al, cl = al - (ch - a.hi), sh = b.hi + bl, sl2 = bl - (sh - b.hi);
+  switch (k >> 4) {
+    case 0: return {ch, cl, sh, sl2};
+    case 1: return {-sh, -sl2, ch, cl};
+    case 2: return {-ch, -cl, -sh, -sl2};
+    default: return {sh, sl2, -ch, -cl};
+  }
+}
+
+// 1 / sqrt(sum / dh + eps): one Newton step on the instruction's result.
+__device__ __forceinline__ Two root(Two sum, float inv_dh, float eps) {
+  Two m = two_sum(sum.hi * inv_dh, eps);  // (inv_dh: a power of two)
+  m.lo = fmaf(sum.lo, inv_dh, m.lo);
+  const float r = rsqrtf(m.hi + m.lo);
+  const Two t = two_prod(r, r, 0.f);
+  const float e = __fmaf_rn(-m.hi, t.hi, 1.f) - m.hi * t.lo - m.lo * t.hi, c = 0.5f * r * e;
+  return {r, isfinite(c) ? c : 0.f};
+}
+
+// x r w, w optional.
+__device__ __forceinline__ Two scaled(float x, Two r, float w) {
+  const Two p = two_prod(r.hi, w, r.lo * w);
+  return two_prod(x, p.hi, x * p.lo);
+}
+
+// The e4m3 scale of 16 elements whose largest magnitude is amax, and its value.
+// (The correctly rounded quotient by 6: one correction of the product.)
+__device__ __forceinline__ uint32_t scale4(float amax, float& s) {
+  constexpr float kSixth = 1.f / 6.f;
+  const float q0 = amax * kSixth, q = fmaf(fmaf(-q0, 6.f, amax), kSixth, q0);
+  uint16_t sc;
+  asm("cvt.rn.satfinite.e4m3x2.f32 %0, %1, %2;" : "=h"(sc) : "f"(0.f), "f"(q));
+  s = f16x2_to_f(e4m3x2_to_f16x2(sc)).x;
+  return sc & 0xFFu;
+}
+
+// The correctly rounded quotient of y by the block scale s, rs near 1 / s. A y of 12
+// bits or fewer is on a border between two codes (3 bits times the scale's 4) or 2^-12
+// of it away, so the quotient is on a border exactly where y is.
+__device__ __forceinline__ float over(float y, float s, float rs) {
+  const float m = fminf(fabsf(y), 8.f * s), q = m * rs;  // (the largest code is 6; a quotient past fp32's range has none)
+  return copysignf(fmaf(fmaf(-q, s, m), rs, q), y);      // (-0 stays -0)
+}
+
+__device__ __forceinline__ uint32_t codes4(const float (&q)[4]) {
+  uint16_t c;
+  asm("{\n\t.reg .b8 b0, b1;\n\t"
+      "cvt.rn.satfinite.e2m1x2.f32 b0, %2, %1;\n\t"
+      "cvt.rn.satfinite.e2m1x2.f32 b1, %4, %3;\n\t"
+      "mov.b16 %0, {b0, b1};\n\t}"
+      : "=h"(c)
+      : "f"(q[0]), "f"(q[1]), "f"(q[2]), "f"(q[3]));
+  return c;
+}
+
+// Four elements as they are in memory, and as fp32.
+template <int DT>
+struct Raw4 {
+  uint32_t w[DT == MTP_DTYPE_BF16 ? 2 : 4];
+};
+
+template <int DT>
+__device__ __forceinline__ Raw4<DT> load4(const void* src, long long at) {
+  Raw4<DT> r;
+  if constexpr (DT == MTP_DTYPE_BF16) {
+    asm volatile("ld.global.L1::no_allocate.v2.u32 {%0,%1}, [%2];"
+                 : "=r"(r.w[0]), "=r"(r.w[1])
+                 : "l"(static_cast<const uint16_t*>(src) + at));
+  } else {
+    const uint4 u = ld_stream(static_cast<const float*>(src) + at);
+    r.w[0] = u.x, r.w[1] = u.y, r.w[2] = u.z, r.w[3] = u.w;
+  }
+  return r;
+}
+
+template <int DT>
+__device__ __forceinline__ void widen4(const Raw4<DT>& r, float (&x)[4]) {
+  if constexpr (DT == MTP_DTYPE_BF16) {
+    x[0] = bf16lo(r.w[0]), x[1] = bf16hi(r.w[0]), x[2] = bf16lo(r.w[1]), x[3] = bf16hi(r.w[1]);
+  } else {
+#pragma unroll
+    for (int e = 0; e < 4; ++e) x[e] = __uint_as_float(r.w[e]);
+  }
+}
+
+template <int DT>
+__device__ __forceinline__ void store4(void* dst, long long at, const float (&x)[4]) {
+  if (DT == MTP_DTYPE_BF16) {
+    uint2 w;
+    asm("cvt.rn.bf16x2.f32 %0, %1, %2;" : "=r"(w.x) : "f"(x[1]), "f"(x[0]));
+    asm("cvt.rn.bf16x2.f32 %0, %1, %2;" : "=r"(w.y) : "f"(x[3]), "f"(x[2]));
+    *reinterpret_cast<uint2*>(static_cast<uint16_t*>(dst) + at) = w;
+  } else {
+    *reinterpret_cast<float4*>(static_cast<float*>(dst) + at) = make_float4(x[0], x[1], x[2], x[3]);
+  }
+}
+
+// Where a head's row goes in the cache, in rows.
+__device__ __forceinline__ long long cache_row(const RopeArgs& a, int head, int slot) {
+  const int pg = slot / a.page;
+  return ((long long)pg * a.n_kv + head) * a.page + (slot - pg * a.page);
+}
+
+// The slot of a position that is appended, -1 else.
+__device__ __forceinline__ int slot_of(const RopeArgs& a, int t, int pos, bool tell) {
+  const int slot = a.slot[t];
+  if (slot == -1 || (slot >= 0 && slot < a.n_slots && pos >= 0)) return slot;
+  if (tell) flag_status(a.status, MTP_ERR_BAD_ARG);
+  return -1;
+}
+
+// 16 elements of 12 bits at most, a group of four lanes, 4 each, at their head's exponent:
+// the codes of a lane's elements, and the block's scale (0x7F, NaN, where one of the
+// elements is not finite: the row shows what it was given). By whole warps.
+__device__ __forceinline__ uint32_t quantize4(const float (&y)[4], int exp, uint32_t& sc) {
+  uint32_t mx = 0;  // (magnitudes as whole numbers: an infinity or a NaN is the largest)
+#pragma unroll
+  for (int e = 0; e < 4; ++e) mx = max(mx, __float_as_uint(y[e]) & 0x7FFFFFFFu);
+#pragma unroll
+  for (int o = 1; o < 4; o <<= 1) mx = max(mx, __shfl_xor_sync(0xFFFFFFFFu, mx, o));
+  float s;
+  sc = scale4(fminf(__uint_as_float(mx) * pow2i(-exp), FLT_MAX), s);
+  s *= pow2i(exp);  // the scale at the elements' size: exact
+  float rs, q[4];
+  asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(rs) : "f"(s));
+#pragma unroll
+  for (int e = 0; e < 4; ++e) q[e] = over(y[e], s, rs);
+  const uint32_t code = codes4(q);
+  if (mx >= 0x7F800000u) sc = 0x7F;
+  return sc == 0 || sc == 0x7F ? 0u : code;
+}
+
+// Queries of up to kBatch x (32 / kLanes) heads.
+template <int DH, int DT>
+__device__ __forceinline__ void rope_queries(const RopeArgs& a, const float (&A)[kBatch][4], const float (&B)[kBatch][4], float4 wa4,
+                                             float4 wb4, bool norm, const CosSin* cs, bool mine, int t, int pos, int h0, int ea, int eb) {
+  constexpr int kLanes = DH / 8, kGroups = 32 / kLanes;
+  const float wa[4] = {wa4.x, wa4.y, wa4.z, wa4.w}, wb[4] = {wb4.x, wb4.y, wb4.z, wb4.w};
+  // z = r (x w c - x' w' s): the weights go into the factors, once for all heads
+  float fa[4], ga[4], fb[4], gb[4];
+#pragma unroll
+  for (int e = 0; e < 4; ++e) {
+    const float c = mine ? cs[e].ch : 1.f, s = mine ? cs[e].sh : 0.f;
+    fa[e] = wa[e] * c;
+    ga[e] = wb[e] * s;
+    fb[e] = wb[e] * c;
+    gb[e] = wa[e] * s;
+  }
+  const long long at = ((long long)t * a.n_q + h0) * DH;
+#pragma unroll
+  for (int u = 0; u < kBatch; ++u) {
+    const bool head = h0 + u * kGroups < a.n_q;
+    float r = 1.f;
+    if (norm) {
+      float sum = 0.f;
+#pragma unroll
+      for (int e = 0; e < 4; ++e) sum = fmaf(A[u][e], A[u][e], fmaf(B[u][e], B[u][e], sum));
+#pragma unroll
+      for (int o = 1; o < kLanes; o <<= 1) sum += __shfl_xor_sync(0xFFFFFFFFu, sum, o);
+      r = rsqrtf(fmaf(sum, 1.f / DH, a.eps));
+    }
+    float ya[4], yb[4];
+#pragma unroll
+    for (int e = 0; e < 4; ++e) {
+      // (what is not turned takes nothing from the other run, whose infinity times 0 would show)
+      const float x = mine ? A[u][e] * gb[e] : 0.f, y = mine ? B[u][e] * ga[e] : 0.f;
+      ya[e] = r * fmaf(A[u][e], fa[e], -y);
+      yb[e] = r * fmaf(B[u][e], fb[e], x);
+    }
+    if (pos < 0) {
+#pragma unroll
+      for (int e = 0; e < 4; ++e) ya[e] = yb[e] = 0.f;
+    }
+    if (head) {
+      store4<DT>(a.q_out, at + u * kGroups * DH + ea, ya);
+      store4<DT>(a.q_out, at + u * kGroups * DH + eb, yb);
+    }
+  }
+}
+
+// Keys, in two floats, and values of 32 / kLanes heads.
+template <int DH, int DT>
+__device__ __forceinline__ void rope_keys(const RopeArgs& a, float (&A)[4], float (&B)[4], float (&VA)[4], float (&VB)[4], float4 wa4,
+                                          float4 wb4, bool norm, const CosSin* cs, bool mine, int t, int pos, int h0, int ea, int eb,
+                                          bool tell) {
+  constexpr int kLanes = DH / 8, kRow = q4_row_bytes(DH);
+  const float wa[4] = {wa4.x, wa4.y, wa4.z, wa4.w}, wb[4] = {wb4.x, wb4.y, wb4.z, wb4.w};
+  const bool head = h0 < a.n_kv;
+  const int slot = slot_of(a, t, pos, tell);
+  Two ka[4], kb[4];
+  if (norm) {
+    Two sum = {0.f, 0.f};
+#pragma unroll
+    for (int e = 0; e < 8; ++e) {
+      const float x = e < 4 ? A[e & 3] : B[e & 3];
+      const Two p = two_prod(x, x, 0.f), n = two_sum(sum.hi, p.hi);
+      sum = {n.hi, n.lo + (sum.lo + p.lo)};
+    }
+#pragma unroll
+    for (int o = 1; o < kLanes; o <<= 1) {
+      const float hi = __shfl_xor_sync(0xFFFFFFFFu, sum.hi, o), lo = __shfl_xor_sync(0xFFFFFFFFu, sum.lo, o);
+      const Two n = two_sum(sum.hi, hi);
+      sum = {n.hi, n.lo + (sum.lo + lo)};
+    }
+    const Two r = root(sum, 1.f / DH, a.eps);
+#pragma unroll
+    for (int e = 0; e < 4; ++e) {
+      ka[e] = scaled(A[e], r, wa[e]);
+      kb[e] = scaled(B[e], r, wb[e]);
+    }
+  } else {
+#pragma unroll
+    for (int e = 0; e < 4; ++e) {
+      ka[e] = {A[e], 0.f};
+      kb[e] = {B[e], 0.f};
+    }
+  }
+  if (mine) {
+#pragma unroll
+    for (int e = 0; e < 4; ++e) {
+      const CosSin c = cs[e];
+      const Two x = ka[e], y = kb[e];
+      ka[e] = turn_one(x, y, c.ch, c.cl, c.sh, c.sl);
+      kb[e] = turn_one(y, x, c.ch, c.cl, -c.sh, -c.sl);
+    }
+  }
+  if (a.k_out && head) {
+    float ya[4], yb[4];
+#pragma unroll
+    for (int e = 0; e < 4; ++e) {
+      ya[e] = pos < 0 ? 0.f : nearest(ka[e]);
+      yb[e] = pos < 0 ? 0.f : nearest(kb[e]);
+    }
+    const long long at = ((long long)t * a.n_kv + h0) * DH;
+    store4<DT>(a.k_out, at + ea, ya);
+    store4<DT>(a.k_out, at + eb, yb);
+  }
+  if (slot < 0) return;  // (the same for the warp)
+  const long long to = (head ? cache_row(a, h0, slot) : 0) * kRow;
+#pragma unroll
+  for (int side = 0; side < 2; ++side) {
+    float ya[4], yb[4];
+#pragma unroll
+    for (int e = 0; e < 4; ++e) {
+      // (bf16 has 8 bits)
+      ya[e] = side == 0 ? to_odd(ka[e]) : (DT == MTP_DTYPE_BF16 ? VA[e] : to_odd({VA[e], 0.f}));
+      yb[e] = side == 0 ? to_odd(kb[e]) : (DT == MTP_DTYPE_BF16 ? VB[e] : to_odd({VB[e], 0.f}));
+    }
+    const int exp = head ? head_exp(a.exp[side], h0) : 0;
+    uint32_t sa, sb;
+    const uint32_t ca = quantize4(ya, exp, sa), cb = quantize4(yb, exp, sb);
+    if (head) {
+      uint8_t* row = a.cache[side] + to;
+      *reinterpret_cast<uint16_t*>(row + ea / 2) = (uint16_t)ca;
+      *reinterpret_cast<uint16_t*>(row + eb / 2) = (uint16_t)cb;
+      if ((ea & 15) == 0) row[DH / 2 + ea / 16] = (uint8_t)sa;
+      if ((eb & 15) == 0) row[DH / 2 + eb / 16] = (uint8_t)sb;
+      if (sa == 0x7F || sb == 0x7F) flag_status(a.status, MTP_ERR_NONFINITE);
+    }
+  }
+}
+
+// Blocks stay and take positions in turn. One warp makes the next position's
+// angles, the others take kBatch x (32 / kLanes) heads of the queries or 32 /
+// kLanes heads of the keys and values at a time; a warp's next rows are on their
+// way while it works on those it has.
+template <int DH, int DT>
+__global__ void __launch_bounds__(32 * kMostWarps, 2) k_rope_rows(const __grid_constant__ RopeArgs a) {
+  constexpr int kLanes = DH / 8, kGroups = 32 / kLanes, kRow = q4_row_bytes(DH);
+  __shared__ CosSin s_cs[2][DH / 2];
+  __shared__ uint64_t s_turn[DH / 2];
+  __shared__ float2 s_quarter[17];
+  const int lane = threadIdx.x & 31, l = lane % kLanes, grp = lane / kLanes;
+  const int warp = __shfl_sync(0xFFFFFFFFu, (int)threadIdx.x >> 5, 0), workers = (blockDim.x >> 5) - 1;
+  const int half = a.rope.rot_dim / 2, turned = half / 4, rest = (DH - a.rope.rot_dim) / 2;
+  const bool mine = l < turned;
+  const int ea = mine ? 4 * l : 2 * half + 4 * (l - turned), eb = mine ? half + 4 * l : ea + rest;
+  if (threadIdx.x < 17) s_quarter[threadIdx.x] = a.quarter[threadIdx.x];
+  for (int i = threadIdx.x; i < half; i += blockDim.x) s_turn[i] = a.rope.turn[i];
+  __syncthreads();
+  pdl_wait();
+  pdl_trigger();
+  auto angles = [&](int t, int first, int step) {
+    const int pos = max(a.pos[t], 0);
+    for (int i = first; i < half; i += step) s_cs[t / gridDim.x & 1][i] = turn_cs(pos, s_turn[i], s_quarter);
+  };
+  if (warp == workers) {
+    if ((int)blockIdx.x < a.tokens) angles(blockIdx.x, lane, 32);
+    for (int t = blockIdx.x; t < a.tokens; t += gridDim.x) {
+      __syncthreads();  // the angles of t are there, those of the position before are no longer needed
+      if (t + (int)gridDim.x < a.tokens) angles(t + gridDim.x, lane, 32);
+    }
+    return;
+  }
+  Raw4<DT> ra[kBatch], rb[kBatch];
+  auto fetch = [&](int t, int part) {
+    const bool is_q = part < a.q_parts;
+    const int h0 = is_q ? part * kBatch * kGroups + grp : (part - a.q_parts) * kGroups + grp, heads = is_q ? a.n_q : a.n_kv;
+#pragma unroll
+    for (int u = 0; u < kBatch; ++u) {
+      const int side = is_q ? 0 : 1 + u, h = is_q ? h0 + u * kGroups : h0;
+      if (h < heads && (is_q || u < 2)) {
+        const long long at = (long long)t * a.ts[side] + (long long)h * a.hs[side];
+        ra[u] = load4<DT>(a.x[side], at + ea);
+        rb[u] = load4<DT>(a.x[side], at + eb);
+      }
+    }
+  };
+  if ((int)blockIdx.x < a.tokens && warp < a.parts) fetch(blockIdx.x, warp);
+#pragma unroll 1
+  for (int t = blockIdx.x; t < a.tokens; t += gridDim.x) {
+    const int pos = a.pos[t];
+    __syncthreads();
+    const CosSin* cs = s_cs[t / gridDim.x & 1] + 4 * l;
+#pragma unroll 1
+    for (int part = warp; part < a.parts; part += workers) {
+      const bool is_q = part < a.q_parts;
+      const int h0 = is_q ? part * kBatch * kGroups + grp : (part - a.q_parts) * kGroups + grp;
+      float A[kBatch][4], B[kBatch][4];
+#pragma unroll
+      for (int u = 0; u < kBatch; ++u) {
+        widen4<DT>(ra[u], A[u]);
+        widen4<DT>(rb[u], B[u]);
+      }
+      if (part + workers < a.parts) fetch(t, part + workers);
+      else if (t + (int)gridDim.x < a.tokens) fetch(t + gridDim.x, warp);
+      const float* w = a.norm[is_q ? 0 : 1];
+      float4 wa = make_float4(1.f, 1.f, 1.f, 1.f), wb = wa;
+      if (w) {
+        wa = *reinterpret_cast<const float4*>(w + ea);
+        wb = *reinterpret_cast<const float4*>(w + eb);
+      }
+      if (is_q) rope_queries<DH, DT>(a, A, B, wa, wb, w != nullptr, cs, mine, t, pos, h0, ea, eb);
+      else rope_keys<DH, DT>(a, A[0], B[0], A[1], B[1], wa, wb, w != nullptr, cs, mine, t, pos, h0, ea, eb, part == a.q_parts && lane == 0);
+    }
+  }
+}
+
+// Any rotated width and any strides: a warp per (position, head), the row in
+// shared memory. Lane l has elements l, l + 32, ... of the row, so neighbouring
+// lanes read neighbouring elements; 16 of them are half a warp.
+template <int DH, int DT>
+__global__ void __launch_bounds__(kRopeThreads) k_rope_any(const __grid_constant__ RopeArgs a) {
+  constexpr int kRow = q4_row_bytes(DH), kN = DH / 32;
+  __shared__ Two s_row[kRopeThreads / 32][DH];
+  __shared__ float2 s_quarter[17];
+  pdl_wait();
+  pdl_trigger();
+  if (threadIdx.x < 17) s_quarter[threadIdx.x] = a.quarter[threadIdx.x];
+  __syncthreads();
+  const int lane = threadIdx.x & 31, heads = a.n_q + 2 * a.n_kv;
+  const int item = blockIdx.x * (kRopeThreads / 32) + (threadIdx.x >> 5);
+  if (item >= a.tokens * heads) return;
+  const int t = item / heads, h = item - t * heads;
+  const int side = h < a.n_q ? 0 : (h < a.n_q + a.n_kv ? 1 : 2), g = h - (side == 0 ? 0 : (side == 1 ? a.n_q : a.n_q + a.n_kv));
+  const int pos = a.pos[t], slot = side > 0 ? slot_of(a, t, pos, h == heads - 1 && lane == 0) : -1, half = a.rope.rot_dim / 2;
+  Two* row_s = s_row[threadIdx.x >> 5];
+  const long long from = (long long)t * a.ts[side] + (long long)g * a.hs[side];
+  const float* w = side < 2 ? a.norm[side] : nullptr;
+  float x[kN];
+  Two sum = {0.f, 0.f};
+#pragma unroll
+  for (int i = 0; i < kN; ++i) {
+    x[i] = load_elem(a.x[side], DT, from + 32 * i + lane);
+    const Two p = two_prod(x[i], x[i], 0.f), n = two_sum(sum.hi, p.hi);
+    sum = {n.hi, n.lo + (sum.lo + p.lo)};
+  }
+#pragma unroll
+  for (int o = 1; o < 32; o <<= 1) {
+    const float hi = __shfl_xor_sync(0xFFFFFFFFu, sum.hi, o), lo = __shfl_xor_sync(0xFFFFFFFFu, sum.lo, o);
+    const Two n = two_sum(sum.hi, hi);
+    sum = {n.hi, n.lo + (sum.lo + lo)};
+  }
+  const Two r = root(sum, 1.f / DH, a.eps);
+#pragma unroll
+  for (int i = 0; i < kN; ++i) row_s[32 * i + lane] = w ? scaled(x[i], r, w[32 * i + lane]) : Two{x[i], 0.f};
+  __syncwarp();
+  if (side < 2 && pos > 0) {
+#pragma unroll 1
+    for (int i = lane; i < half; i += 32) {
+      const CosSin c = turn_cs(pos, a.rope.turn[i], s_quarter);
+      const Two u = row_s[i], v = row_s[half + i];
+      row_s[i] = turn_one(u, v, c.ch, c.cl, c.sh, c.sl);
+      row_s[half + i] = turn_one(v, u, c.ch, c.cl, -c.sh, -c.sl);
+    }
+  }
+  __syncwarp();
+  void* out = side == 0 ? a.q_out : (side == 1 ? a.k_out : nullptr);
+  const long long to = ((long long)t * (side == 0 ? a.n_q : a.n_kv) + g) * DH;
+  const int exp = side > 0 ? head_exp(a.exp[side - 1], g) : 0;
+  const long long row_at = slot >= 0 ? cache_row(a, g, slot) * kRow : 0;
+#pragma unroll
+  for (int i = 0; i < kN; ++i) {
+    const Two z = row_s[32 * i + lane];
+    if (out) store_elem(out, DT, to + 32 * i + lane, pos >= 0 ? nearest(z) : 0.f);
+    if (slot < 0) continue;  // (the same for the warp)
+    const float y = to_odd(z);
+    uint32_t mx = __float_as_uint(y) & 0x7FFFFFFFu;
+#pragma unroll
+    for (int o = 1; o < 16; o <<= 1) mx = max(mx, __shfl_xor_sync(0xFFFFFFFFu, mx, o));
+    float sv, rs;
+    uint32_t sc = scale4(fminf(__uint_as_float(mx) * pow2i(-exp), FLT_MAX), sv);
+    sv *= pow2i(exp);
+    asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(rs) : "f"(sv));
+    const float q[4] = {over(y, sv, rs), 0.f, 0.f, 0.f};
+    uint32_t code = sc != 0 ? codes4(q) : 0u;
+    if (mx >= 0x7F800000u) {
+      sc = 0x7F;
+      code = 0;
+      if ((lane & 15) == 0) flag_status(a.status, MTP_ERR_NONFINITE);
+    }
+    code |= __shfl_down_sync(0xFFFFFFFFu, code, 1) << 4;
+    uint8_t* row = a.cache[side - 1] + row_at;
+    if ((lane & 1) == 0) row[16 * i + lane / 2] = (uint8_t)code;
+    if ((lane & 15) == 0) row[DH / 2 + 2 * i + lane / 16] = (uint8_t)sc;
+  }
+}
+
+// Whether two ranges of bytes meet without being the same.
+bool cross(const void* a, size_t na, const void* b, size_t nb) {
+  const uint8_t *p = static_cast<const uint8_t*>(a), *q = static_cast<const uint8_t*>(b);
+  return p && q && p < q + nb && q < p + na;
+}
+
+}  // namespace
+}  // namespace mtp
+
+using namespace mtp;
+
+extern "C" {
+
+mtp_status mtp_rope_init(int32_t rot_dim, double theta, const double* h_freq, mtp_rope* out) {
+  if (!out || rot_dim < 0 || rot_dim > 2 * MTP_ROPE_MAX || rot_dim % 2 != 0) return MTP_ERR_BAD_ARG;
+  if (!h_freq && !(theta > 0.0 && std::isfinite(theta))) return MTP_ERR_BAD_ARG;
+  mtp_rope r = {};
+  r.rot_dim = rot_dim;
+  for (int i = 0; i < rot_dim / 2; ++i) {
+    const double f = h_freq ? h_freq[i] : std::pow(theta, -2.0 * i / rot_dim);
+    if (!std::isfinite(f)) return MTP_ERR_BAD_ARG;
+    double turn = f / 6.283185307179586476925286766559;
+    turn -= std::floor(turn);  // in [0, 1]; 1 where a tiny negative one rounds up
+    r.turn[i] = turn < 1.0 ? (uint64_t)std::ldexp(turn, 64) : 0;  // (a double below 1 times 2^64 fits)
+  }
+  *out = r;
+  return MTP_OK;
+}
+
+mtp_status kv_q4_append_rope(mtp_stream stream, const kv_q4_cache* c, int32_t tokens, int32_t n_q, const void* d_q,
+                             int64_t q_tok_stride, int64_t q_head_stride, const void* d_k, int64_t k_tok_stride,
+                             int64_t k_head_stride, const void* d_v, int64_t v_tok_stride, int64_t v_head_stride,
+                             int32_t dtype, const float* d_q_norm, const float* d_k_norm, float eps,
+                             const mtp_rope* rope, const int32_t* d_pos, const int32_t* d_slot, void* d_q_out,
+                             void* d_k_out, int32_t* d_status) {
+  if (!q4_cache_ok(c) || tokens < 0 || n_q < 1 || n_q > 1024 || (dtype != MTP_DTYPE_BF16 && dtype != MTP_DTYPE_F32) ||
+      (long long)tokens * (n_q + 2 * c->n_kv) >= (1LL << 31) - kRopeThreads || !rope || rope->rot_dim < 0 || rope->rot_dim > c->head_dim || rope->rot_dim % 2 != 0 || !(eps >= 0.f) || !std::isfinite(eps))
+    return MTP_ERR_BAD_ARG;
+  if (tokens == 0) return MTP_OK;
+  if (!d_q || !d_k || !d_v || !d_pos || !d_slot || !d_q_out) return MTP_ERR_BAD_ARG;
+  const int es = dtype == MTP_DTYPE_BF16 ? 2 : 4, dh = c->head_dim;
+  auto bits = [](const void* p) { return reinterpret_cast<uintptr_t>(p); };
+  if (((bits(d_q) | bits(d_k) | bits(d_v)) & (es - 1)) != 0 || ((bits(d_q_out) | bits(d_k_out) | bits(d_q_norm) | bits(d_k_norm)) & 15) != 0)
+    return MTP_ERR_BAD_ARG;
+  RopeArgs a{{d_q, d_k, d_v}, {q_tok_stride, k_tok_stride, v_tok_stride}, {q_head_stride, k_head_stride, v_head_stride},
+             d_q_out, d_k_out, {d_q_norm, d_k_norm}, {static_cast<uint8_t*>(c->k), static_cast<uint8_t*>(c->v)},
+             {c->k_exp, c->v_exp}, d_pos, d_slot, d_status, tokens, n_q, c->n_kv, c->page, c->n_pages * c->page, 1, 1, eps, {},
+             *rope};
+  for (int i = 0; i <= 16; ++i) {
+    const double x = i < 16 ? std::cos(i * (6.283185307179586476925286766559 / 64)) : 0.0;
+    a.quarter[i].x = (float)x;
+    a.quarter[i].y = (float)(x - a.quarter[i].x);
+  }
+  // an output may be its own input, laid out the same; any other overlap would be read after it is written
+  const void* in[3] = {d_q, d_k, d_v};
+  const int heads[3] = {n_q, c->n_kv, c->n_kv};
+  const void* out[2] = {d_q_out, d_k_out};
+  for (int o = 0; o < 2; ++o) {
+    const size_t bytes = (size_t)tokens * heads[o] * dh * es;
+    for (int i = 0; i < 3; ++i) {
+      if (!out[o] || (i == o && in[i] == out[o] && (tokens == 1 || a.ts[i] == (long long)heads[i] * dh) && (heads[i] == 1 || a.hs[i] == dh))) continue;
+      long long lo = 0, hi = dh;  // the input's range of elements (strides may be negative)
+      for (const long long far : {(tokens - 1) * a.ts[i], (heads[i] - 1) * a.hs[i]}) {
+        lo += std::min(far, 0LL);
+        hi += std::max(far, 0LL);
+      }
+      if (cross(out[o], bytes, static_cast<const uint8_t*>(in[i]) + lo * es, (size_t)(hi - lo) * es)) return MTP_ERR_BAD_ARG;
+    }
+  }
+  if (cross(d_q_out, (size_t)tokens * n_q * dh * es, d_k_out, d_k_out ? (size_t)tokens * c->n_kv * dh * es : 0)) return MTP_ERR_BAD_ARG;
+  uintptr_t align = bits(d_q) | bits(d_k) | bits(d_v);
+  for (int i = 0; i < 3; ++i) align |= (uintptr_t)(a.ts[i] * es) | (uintptr_t)(a.hs[i] * es);
+  const int all = n_q + 2 * c->n_kv;
+  const bool fast = rope->rot_dim % 32 == 0 && (align & (4 * es - 1)) == 0;
+  cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
+  void (*k)(RopeArgs);
+  long long blocks;
+  int threads = kRopeThreads;
+  if (fast) {
+    const int groups = 256 / dh;
+    a.q_parts = (n_q + kBatch * groups - 1) / (kBatch * groups);
+    a.parts = a.q_parts + (c->n_kv + groups - 1) / groups;
+    threads = 32 * std::min(a.parts + 1, kMostWarps);
+    blocks = std::min<long long>(tokens, (long long)device_sm_count() * (24 * 32 / threads));  // (80 registers a thread)
+    k = dtype == MTP_DTYPE_BF16
+            ? (dh == 64 ? k_rope_rows<64, MTP_DTYPE_BF16> : (dh == 128 ? k_rope_rows<128, MTP_DTYPE_BF16> : k_rope_rows<256, MTP_DTYPE_BF16>))
+            : (dh == 64 ? k_rope_rows<64, MTP_DTYPE_F32> : (dh == 128 ? k_rope_rows<128, MTP_DTYPE_F32> : k_rope_rows<256, MTP_DTYPE_F32>));
+  } else {
+    blocks = ((long long)tokens * all + kRopeThreads / 32 - 1) / (kRopeThreads / 32);
+    k = dtype == MTP_DTYPE_BF16
+            ? (dh == 64 ? k_rope_any<64, MTP_DTYPE_BF16> : (dh == 128 ? k_rope_any<128, MTP_DTYPE_BF16> : k_rope_any<256, MTP_DTYPE_BF16>))
+            : (dh == 64 ? k_rope_any<64, MTP_DTYPE_F32> : (dh == 128 ? k_rope_any<128, MTP_DTYPE_F32> : k_rope_any<256, MTP_DTYPE_F32>));
+  }
+  count_launch();
+  const cudaError_t e = launch_pdl(k, dim3((unsigned)blocks), dim3(threads), 0, s, a);
+  return e == cudaSuccess ? MTP_OK : MTP_ERR_CUDA;
+}
+
+}  // extern "C"

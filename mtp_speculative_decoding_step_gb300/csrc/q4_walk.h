@@ -17,6 +17,7 @@ using std::min;
 #endif
 
 constexpr int kT = 128;  // positions per tile
+constexpr int kTreeMost = 128;  // nodes of a tree: less than kT apart, as edge_index() needs them
 
 // A block's share of one (row, KV head, query tile). Query row f of the row's
 // position-major order is (position f / G, head f % G of the KV head's G); tile
@@ -26,7 +27,7 @@ struct Run {
   int a0, n, pos;      // first packed position, positions, the first one's place in the cache
   int lo, end;         // cached positions that some query row sees: [lo, end)
   int first, tile, nt; // the query tile's first 128-position tile; this share's tiles
-  int p0, p1;          // places of the first and the last query row
+  int p0, p1;          // places of the first and the last query row (trees: the prefix's last place, the row's last)
   int flags;           // 1: begins here, 2: ends here, 4: the block's last share
   int last;            // the block that ends it
 
@@ -41,8 +42,10 @@ struct Run {
   }
 };
 
-// Args: start, len, tokens, max_pages, page, window of the call.
-template <class Args>
+// Args: start, len, tokens, max_pages, page, window of the call. TREE: a row's
+// queries are the nodes of a tree at its last n positions; any of them may see
+// any other, and each the prefix before them, from its own position's window on.
+template <class Args, bool TREE = false>
 struct Walk {
   const Args* a;
   int G, RT;       // query heads per KV head, query rows per tile
@@ -50,11 +53,12 @@ struct Walk {
   Q4_WALK void row(int r, int& a0, int& n, int& L) const {
     a0 = min(max(a->start[r], 0), a->tokens);
     n = min(max(a->start[r + 1], a0), a->tokens) - a0;
+    if (TREE && n > kTreeMost) n = 0;  // (refused)
     L = min(max(a->len[r], 0), a->max_pages * a->page);
   }
   Q4_WALK int tiles(int n) const { return (n * G + RT - 1) / RT; }
   Q4_WALK void span(int n, int L, int j, int& lo, int& end, int& t0, int& cnt) const {
-    const int i0 = j * RT / G, i1 = (min(n * G, (j + 1) * RT) - 1) / G;
+    const int i0 = TREE ? 0 : j * RT / G, i1 = TREE ? n - 1 : (min(n * G, (j + 1) * RT) - 1) / G;
     end = max(L - n + i1 + 1, 0);
     // (from 0 at the least before the window goes off: a first place below 0 less a window near 2^31 would wrap)
     lo = a->window > 0 ? max(0, max(0, L - n + i0 + 1) - a->window) : 0;
