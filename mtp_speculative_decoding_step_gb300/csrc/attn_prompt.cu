@@ -1,5 +1,5 @@
 // Causal attention of whole packed prompts over unrounded keys and values
-// (kv_attend_prompt).
+// (kv_attend_prompt): checks, and the fp32 kernel. (bf16: attn_prompt_tc.cu.)
 //
 //   s_ij = scale q_i . k_j,  out_i = sum_j softmax(s_i)_j v_j,  j <= i (and > i - window)
 //
@@ -8,6 +8,7 @@
 #include <cmath>
 #include <mutex>
 
+#include "attn_prompt.h"
 #include "common.cuh"
 #include "kernels.h"
 #include "prompt_tiles.h"
@@ -15,49 +16,6 @@
 namespace mtp {
 
 namespace {
-
-struct PromptArgs {
-  const void *q, *k, *v;
-  long long ts[3], hs[3];  // strides of Q, K, V in elements
-  const int32_t* start;
-  void* out;
-  float* lse;
-  int32_t* status;
-  int rows, n_q, n_kv, tokens, window;
-  float scale;
-};
-
-// The row and the query tile of tile number x, counted from the last row's last
-// tile (a row's later tiles are its longest); false past the first. By a whole
-// warp, rows in consecutive groups per lane.
-__device__ __forceinline__ bool find_tile(const PromptArgs& a, int tile, int x, int& a0, int& n, int& j) {
-  const int lane = threadIdx.x & 31, per = (a.rows + 31) / 32, r0 = min(lane * per, a.rows), r1 = min(r0 + per, a.rows);
-  int sum = 0, b0, m;
-#pragma unroll 4
-  for (int r = r0; r < r1; ++r) {
-    prompt_row(a.start, a.tokens, r, b0, m);
-    sum += prompt_tiles(m, tile);
-  }
-  int inc = sum;
-#pragma unroll
-  for (int o = 1; o < 32; o <<= 1) {
-    const int u = __shfl_up_sync(0xFFFFFFFFu, inc, o);
-    if (lane >= o) inc += u;
-  }
-  const int all = __shfl_sync(0xFFFFFFFFu, inc, 31);
-  if (x >= all) return false;
-  x = all - 1 - x;
-  const int owner = __ffs(__ballot_sync(0xFFFFFFFFu, inc - sum <= x && x < inc)) - 1;
-  int at = __shfl_sync(0xFFFFFFFFu, inc - sum, owner), r = __shfl_sync(0xFFFFFFFFu, r0, owner);
-  for (;; ++r) {
-    prompt_row(a.start, a.tokens, r, a0, n);
-    const int t = prompt_tiles(n, tile);
-    if (x < at + t) break;
-    at += t;
-  }
-  j = x - at;
-  return true;
-}
 
 // ------------------------------------------------------------ CUDA cores
 
@@ -70,7 +28,7 @@ constexpr int simt_smem() { return ((kSimtRows + 2 * kSimtKeys) * (DH + 4) + kSi
 // of 16 x 16 has the scores of 4 queries with 2 keys, then 4 queries' outputs
 // in DH / 16 dimensions: 32 products per 8 shared-memory accesses of a warp,
 // which is what the multiply-add units and shared memory sustain together.
-template <int DH, int DT>
+template <int DH>
 __global__ void __launch_bounds__(kSimtThreads) k_prompt_simt(const __grid_constant__ PromptArgs a) {
   constexpr int kS = DH + 4, kPS = kSimtKeys + 4, kD = DH / 64;
   extern __shared__ __align__(16) float smem[];
@@ -81,7 +39,7 @@ __global__ void __launch_bounds__(kSimtThreads) k_prompt_simt(const __grid_const
   const int tid = threadIdx.x, tx = tid & 15, ty = tid >> 4, h = blockIdx.x % a.n_q, g = h / (a.n_q / a.n_kv);
   if (tid < 32) {
     int a0 = 0, n = 0, j = 0;
-    const bool some = find_tile(a, kSimtRows, blockIdx.x / a.n_q, a0, n, j);
+    const bool some = find_tile(a, 1, kSimtRows, blockIdx.x / a.n_q, a0, n, j);
     if (tid == 0) {
       s_at[0] = a0;
       s_at[1] = some ? n : 0;
@@ -98,12 +56,7 @@ __global__ void __launch_bounds__(kSimtThreads) k_prompt_simt(const __grid_const
       float4 x = make_float4(0.f, 0.f, 0.f, 0.f);
       if (r < count) {
         const long long at = (long long)(a0 + first + r) * a.ts[side] + (long long)head * a.hs[side] + d;
-        if (DT == MTP_DTYPE_F32) {
-          x = *reinterpret_cast<const float4*>(static_cast<const float*>(src) + at);
-        } else {
-          const uint2 w = *reinterpret_cast<const uint2*>(static_cast<const uint16_t*>(src) + at);
-          x = make_float4(bf16lo(w.x), bf16hi(w.x), bf16lo(w.y), bf16hi(w.y));
-        }
+        x = *reinterpret_cast<const float4*>(static_cast<const float*>(src) + at);
       }
       *reinterpret_cast<float4*>(dst + r * kS + d) = x;
     }
@@ -215,14 +168,7 @@ __global__ void __launch_bounds__(kSimtThreads) k_prompt_simt(const __grid_const
     for (int d = 0; d < kD; ++d) {
       const float y[4] = {o[r][d][0] * f, o[r][d][1] * f, o[r][d][2] * f, o[r][d][3] * f};
       const long long to = at * DH + 64 * d + 4 * tx;
-      if (DT == MTP_DTYPE_F32) {
-        *reinterpret_cast<float4*>(static_cast<float*>(a.out) + to) = make_float4(y[0], y[1], y[2], y[3]);
-      } else {
-        uint2 w;
-        asm("cvt.rn.bf16x2.f32 %0, %1, %2;" : "=r"(w.x) : "f"(y[1]), "f"(y[0]));
-        asm("cvt.rn.bf16x2.f32 %0, %1, %2;" : "=r"(w.y) : "f"(y[3]), "f"(y[2]));
-        *reinterpret_cast<uint2*>(static_cast<uint16_t*>(a.out) + to) = w;
-      }
+      *reinterpret_cast<float4*>(static_cast<float*>(a.out) + to) = make_float4(y[0], y[1], y[2], y[3]);
     }
   }
 }
@@ -241,14 +187,14 @@ cudaError_t raise_smem(K k, int bytes, bool (&set)[kMaxDevices], std::mutex& mu)
   return e;
 }
 
-template <int DH, int DT>
+template <int DH>
 cudaError_t launch_simt(const PromptArgs& a, cudaStream_t s) {
   static std::mutex mu;
   static bool set[kMaxDevices] = {};
-  const cudaError_t e = raise_smem(k_prompt_simt<DH, DT>, simt_smem<DH>(), set, mu);
+  const cudaError_t e = raise_smem(k_prompt_simt<DH>, simt_smem<DH>(), set, mu);
   if (e != cudaSuccess) return e;
   count_launch();
-  return launch_pdl(k_prompt_simt<DH, DT>, dim3((unsigned)(prompt_most_tiles(a.tokens, a.rows, kSimtRows) * a.n_q)),
+  return launch_pdl(k_prompt_simt<DH>, dim3((unsigned)(prompt_most_tiles(a.tokens, a.rows, 1, kSimtRows) * a.n_q)),
                     dim3(kSimtThreads), simt_smem<DH>(), s, a);
 }
 
@@ -298,10 +244,8 @@ mtp_status kv_attend_prompt(mtp_stream stream, int32_t rows, int32_t n_q, int32_
   }
   cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
   cudaError_t e;
-  if (dtype == MTP_DTYPE_F32)
-    e = head_dim == 64 ? launch_simt<64, MTP_DTYPE_F32>(a, s) : head_dim == 128 ? launch_simt<128, MTP_DTYPE_F32>(a, s) : launch_simt<256, MTP_DTYPE_F32>(a, s);
-  else
-    e = head_dim == 64 ? launch_simt<64, MTP_DTYPE_BF16>(a, s) : head_dim == 128 ? launch_simt<128, MTP_DTYPE_BF16>(a, s) : launch_simt<256, MTP_DTYPE_BF16>(a, s);
+  if (dtype == MTP_DTYPE_BF16) e = launch_prompt_tc(a, head_dim, s);
+  else e = head_dim == 64 ? launch_simt<64>(a, s) : (head_dim == 128 ? launch_simt<128>(a, s) : launch_simt<256>(a, s));
   return e == cudaSuccess ? MTP_OK : MTP_ERR_CUDA;
 }
 

@@ -71,13 +71,12 @@
 #include "kernels.h"
 #include "q4.cuh"
 #include "q4_walk.h"
-#include "tc_common.cuh"
+#include "tc_attn.cuh"
 
 namespace mtp {
 
 constexpr int kAttnThreads = 512;
 constexpr float kUnset = -INFINITY;
-constexpr unsigned kQ4WaitLimit = 1u << 20;  // polls: 4 s, where a tile takes about a microsecond
 
 struct Q4AttnArgs {
   const uint8_t *kc, *vc;
@@ -96,127 +95,6 @@ struct Q4AttnArgs {
   float scale;
   const int32_t *mask, *place;   // trees: bits of the nodes that a query sees; its position (NULL: no window)
 };
-
-// ------------------------------------------------------------ PTX
-
-__device__ __forceinline__ uint64_t sdesc_mn(uint32_t addr, uint32_t lbo) {
-  // M-major operand in 128B-swizzled atoms of 64 elements x 8 k: `lbo` bytes
-  // between atoms along M, 1024 between groups of eight k
-  uint64_t d = 0;
-  d |= (uint64_t)((addr >> 4) & 0x3FFF);
-  d |= (uint64_t)((lbo >> 4) & 0x3FFF) << 16;
-  d |= (uint64_t)(1024 >> 4) << 32;
-  d |= (uint64_t)1 << 46;
-  d |= (uint64_t)2 << 61;
-  return d;
-}
-
-// kind::f16 with f16 operands and fp32 accumulators; `a_mn`: A is M-major
-__host__ __device__ constexpr uint32_t idesc_f16(int m, int n, bool a_mn) {
-  return (1u << 4) | ((a_mn ? 1u : 0u) << 15) | ((uint32_t)(n >> 3) << 17) | ((uint32_t)(m >> 4) << 24);
-}
-
-// Issued by a converged warp, one lane elected in the instruction's own
-// predicate: operands that are the same for the warp then live in uniform
-// registers. (A branch on one lane costs moves into them for every MMA: 54
-// cycles each where the tensor core needs 20 to 40 at N = 32.)
-__device__ __forceinline__ void mma_f16_ss(uint32_t d, uint64_t a, uint64_t b, uint32_t idesc, uint32_t acc) {
-  asm volatile(
-      "{\n\t.reg .pred p, q;\n\t"
-      "elect.sync _|q, 0xffffffff;\n\t"
-      "setp.ne.b32 p, %4, 0;\n\t"
-      "@q tcgen05.mma.cta_group::1.kind::f16 [%0], %1, %2, %3, p;\n\t}" ::"r"(d),
-      "l"(a), "l"(b), "r"(idesc), "r"(acc)
-      : "memory");
-}
-__device__ __forceinline__ void mma_f16_ts(uint32_t d, uint32_t a, uint64_t b, uint32_t idesc, uint32_t acc) {
-  asm volatile(
-      "{\n\t.reg .pred p, q;\n\t"
-      "elect.sync _|q, 0xffffffff;\n\t"
-      "setp.ne.b32 p, %4, 0;\n\t"
-      "@q tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, p;\n\t}" ::"r"(d),
-      "r"(a), "l"(b), "r"(idesc), "r"(acc)
-      : "memory");
-}
-__device__ __forceinline__ void mma_commit_elect(uint32_t bar) {
-  asm volatile(
-      "{\n\t.reg .pred q;\n\t"
-      "elect.sync _|q, 0xffffffff;\n\t"
-      "@q tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.b64 [%0];\n\t}" ::"r"(bar)
-      : "memory");
-}
-
-__device__ __forceinline__ void tc_fence_before() { asm volatile("tcgen05.fence::before_thread_sync;" ::: "memory"); }
-__device__ __forceinline__ void tc_fence_after() { asm volatile("tcgen05.fence::after_thread_sync;" ::: "memory"); }
-__device__ __forceinline__ void tc_wait_ld() { asm volatile("tcgen05.wait::ld.sync.aligned;" ::: "memory"); }
-__device__ __forceinline__ void tc_wait_st() { asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory"); }
-__device__ __forceinline__ void fence_async() { asm volatile("fence.proxy.async.shared::cta;" ::: "memory"); }
-
-// 16 lanes x 8 C columns in the MMA fragment layout: registers 4b..4b+3 hold
-// (row l/4, columns 8b + 2(l%4), +1) and the same of row l/4 + 8.
-template <int C>
-__device__ __forceinline__ void tmem_ld_frag(uint32_t t, uint32_t* r);
-template <>
-__device__ __forceinline__ void tmem_ld_frag<1>(uint32_t t, uint32_t* r) {
-  asm volatile("tcgen05.ld.sync.aligned.16x256b.x1.b32 {%0,%1,%2,%3}, [%4];"
-               : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]) : "r"(t));
-}
-template <>
-__device__ __forceinline__ void tmem_ld_frag<2>(uint32_t t, uint32_t* r) {
-  asm volatile("tcgen05.ld.sync.aligned.16x256b.x2.b32 {%0,%1,%2,%3,%4,%5,%6,%7}, [%8];"
-               : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7])
-               : "r"(t));
-}
-template <>
-__device__ __forceinline__ void tmem_ld_frag<4>(uint32_t t, uint32_t* r) {
-  asm volatile("tcgen05.ld.sync.aligned.16x256b.x4.b32 {%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15}, [%16];"
-               : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7]),
-                 "=r"(r[8]), "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]), "=r"(r[14]), "=r"(r[15])
-               : "r"(t));
-}
-template <>
-__device__ __forceinline__ void tmem_ld_frag<8>(uint32_t t, uint32_t* r) {
-  tmem_ld_frag<4>(t, r);
-  tmem_ld_frag<4>(t + 32, r + 16);
-}
-
-__device__ __forceinline__ void tmem_st_rows16(uint32_t t, const uint32_t (&r)[16]) {
-  asm volatile("tcgen05.st.sync.aligned.32x32b.x16.b32 [%16], {%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15};" ::"r"(r[0]),
-               "r"(r[1]), "r"(r[2]), "r"(r[3]), "r"(r[4]), "r"(r[5]), "r"(r[6]), "r"(r[7]), "r"(r[8]), "r"(r[9]),
-               "r"(r[10]), "r"(r[11]), "r"(r[12]), "r"(r[13]), "r"(r[14]), "r"(r[15]), "r"(t));
-}
-
-__device__ __forceinline__ void stmatrix_x4_t(uint32_t addr, uint32_t a, uint32_t b, uint32_t c, uint32_t d) {
-  asm volatile("stmatrix.sync.aligned.m8n8.x4.trans.shared.b16 [%0], {%1,%2,%3,%4};" ::"r"(addr), "r"(a), "r"(b),
-               "r"(c), "r"(d)
-               : "memory");
-}
-
-__device__ __forceinline__ float ex2(float x) {
-  float y;
-  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
-  return y;
-}
-__device__ __forceinline__ uint32_t pack_f16(float lo, float hi) {
-  uint32_t d;
-  asm("cvt.rn.f16x2.f32 %0, %1, %2;" : "=r"(d) : "f"(hi), "f"(lo));
-  return d;
-}
-
-// Barrier over the 128 threads of a softmax warpgroup, and a vote over them.
-__device__ __forceinline__ void group_sync(int id) { asm volatile("barrier.cta.sync.aligned %0, 128;" ::"r"(id) : "memory"); }
-__device__ __forceinline__ bool group_any(int id, bool p) {
-  uint32_t any;
-  asm volatile(
-      "{\n\t.reg .pred p, q;\n\t"
-      "setp.ne.b32 p, %2, 0;\n\t"
-      "barrier.cta.red.or.aligned.pred q, %1, 128, p;\n\t"
-      "selp.u32 %0, 1, 0, q;\n\t}"
-      : "=r"(any)
-      : "r"(id), "r"((uint32_t)p)
-      : "memory");
-  return any != 0;
-}
 
 // ------------------------------------------------------------ shape
 
@@ -319,24 +197,6 @@ __device__ __forceinline__ void load_words(const uint8_t* p, uint32_t (&w)[NW]) 
     for (int i = 0; i < NW; ++i) w[i] = reinterpret_cast<const uint32_t*>(p)[i];
   }
 }
-
-// Bounded wait that gives up as soon as another role has failed. For whole,
-// converged warps: a ready wait costs some 80 cycles then, 230 where one lane
-// looks for the others, and lanes that wait for barriers of their own slow
-// every role threefold.
-__device__ __forceinline__ bool wait(uint64_t* bar, uint32_t parity, volatile int* fail) {
-  const uint32_t b = smem_u32(bar);
-#pragma unroll 1
-  for (unsigned i = 0; i < kQ4WaitLimit; ++i) {
-    if (mbar_try(b, parity)) return true;
-    if ((i & 1023) == 1023 && *fail) return false;
-  }
-  *fail = 1;
-  return false;
-}
-
-// Keeps a value read from tensor memory behind the wait that completes it.
-__device__ __forceinline__ void pin(uint32_t& x) { asm volatile("" : "+r"(x)); }
 
 // Whether a query at `pos` sees a position of an edge tile whose V is NaN in
 // 16-dimension block b. (Trees: `mask` has the query's bits of the n positions from base on.)
@@ -740,7 +600,7 @@ __global__ void __launch_bounds__(kAttnThreads, 1) k_q4_attn(const __grid_consta
     }
     if (!ok) {  // what was issued ends before its operands and tensor memory go
       mma_commit_elect(smem_u32(&M.drain));
-      mbar_wait(smem_u32(&M.drain), 0, kQ4WaitLimit);
+      mbar_wait(smem_u32(&M.drain), 0, kAttnWaitLimit);
     }
     __syncwarp();
   } else if (warp >= 4 && warp < kSoftWarp) {
@@ -1293,9 +1153,9 @@ __global__ void __launch_bounds__(kAttnThreads, 1) k_q4_attn(const __grid_consta
       flag_status(a.status, MTP_ERR_TIMEOUT);
       // let copies still in flight land before the shared memory is released
       for (uint32_t i = 0; i < (uint32_t)S::KS && i < M.copied[0]; ++i)
-        mbar_wait(smem_u32(&M.rawk_full[i]), ((M.copied[0] - 1 - i) / S::KS) & 1, kQ4WaitLimit);
+        mbar_wait(smem_u32(&M.rawk_full[i]), ((M.copied[0] - 1 - i) / S::KS) & 1, kAttnWaitLimit);
       for (uint32_t i = 0; i < (uint32_t)S::VS && i < M.copied[1]; ++i)
-        mbar_wait(smem_u32(&M.rawv_full[i]), ((M.copied[1] - 1 - i) / S::VS) & 1, kQ4WaitLimit);
+        mbar_wait(smem_u32(&M.rawv_full[i]), ((M.copied[1] - 1 - i) / S::VS) & 1, kAttnWaitLimit);
     }
   }
   __syncthreads();

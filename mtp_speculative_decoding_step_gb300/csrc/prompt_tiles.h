@@ -21,13 +21,14 @@ PROMPT_TILES void prompt_row(const int* start, int tokens, int r, int& a0, int& 
   n = min(max(start[r + 1], a0), tokens) - a0;
 }
 
-// Query tiles of a row, `tile` positions each.
+// Query tiles of n query rows, `tile` each.
 PROMPT_TILES int prompt_tiles(int n, int tile) { return (n + tile - 1) / tile; }
 
-// Blocks that hold all rows' query tiles, whatever their lengths are: a row's
-// last tile may be short, so rows add one each at the most.
-inline long long prompt_most_tiles(int tokens, int rows, int tile) {
-  return (long long)tokens / tile + (tokens < rows ? tokens : rows);
+// Blocks that hold all rows' query tiles of `tile` query rows, G a position,
+// whatever the rows' lengths are: a row's last tile may be short, so rows add one
+// each at the most.
+inline long long prompt_most_tiles(int tokens, int rows, int G, int tile) {
+  return (long long)tokens * G / tile + (tokens < rows ? tokens : rows);
 }
 
 }  // namespace mtp
