@@ -14,6 +14,7 @@ struct PromptArgs {
   int32_t* status;
   int rows, n_q, n_kv, tokens, window;
   float scale;
+  int group;  // bf16: heads to a query tile
 };
 
 // The row and the query tile (`tile` rows of G a position) of tile number x, counted from the last row's last
@@ -48,6 +49,6 @@ __device__ __forceinline__ bool find_tile(const PromptArgs& a, int G, int tile, 
   return true;
 }
 
-cudaError_t launch_prompt_tc(const PromptArgs& a, int head_dim, cudaStream_t s);
+cudaError_t launch_prompt_tc(PromptArgs a, int head_dim, cudaStream_t s);
 
 }  // namespace mtp

@@ -3,20 +3,23 @@
 //   S[128 queries][128 keys] = Q . K^T       Q, K in shared memory
 //   O[128 queries][DH]      += P . V         P = 2^(c s - m) in tensor memory, V in shared memory
 //
-// The query rows of one KV head are taken position-major (row f is position f / G,
-// head f % G of the G that share the KV head), 256 of them to a unit, which reads
-// its keys once: two query tiles of 128 in one block (DH <= 128), or one each in the
-// two blocks of a cluster (DH = 256, where O takes half of tensor memory), which
-// copy half of every tile each, to both. 12 warps:
+// The query rows of the heads that share a KV head are taken position-major, a
+// query tile being as many whole positions as 128 rows hold. Two query tiles are
+// a unit, which reads its keys once: both in one block (DH <= 128), or one each in
+// the two blocks of a cluster (DH = 256, where O takes half of tensor memory), which
+// copy half of every tile of K and V each, to both. Blocks stay and take units in turn,
+// the longest first. 12 warps:
 //   warps 0-7   softmax: two groups of 128 threads, thread = query row. An item is a
 //               query tile's 128 keys; items alternate between two places for S in
 //               tensor memory, group s has place s. With two query tiles a group has
 //               a tile of its own; with one, the groups take the keys in turn and
 //               hand the running maximum on
-//   warp 8      copies (TMA) K and V tiles through a ring in the order of their use
+//   warp 8      finds the units; copies (TMA) Q, and K and V through a ring in the order
+//               of their use
 //   warp 9      issues the MMAs: S of item k + 2 behind P.V of item k
-//   warps 10-11 clean V where some query of the unit does not see a position: 0
-//               times what stands there has to be 0
+//   warps 10-11 clean V of what is not finite where some query of the unit does not see
+//               a position: 0 times it has to be 0. (What such queries do see of it is
+//               added at the end.)
 // P is written as bf16 over its S (the tensor core reads it from there), off by at
 // most 2^-8 of each weight; their sum is taken of the fp32 weights. The running maximum is
 // lazy: O is rescaled only when a row's maximum has grown by 2^8, by the warp whose
@@ -25,6 +28,7 @@
 #include <algorithm>
 #include <cfloat>
 #include <mutex>
+#include <type_traits>
 
 #include "attn_prompt.h"
 #include "kernels.h"
@@ -36,8 +40,6 @@ namespace mtp {
 namespace {
 
 constexpr int kPromptThreads = 384;
-constexpr int kUnit = 256;  // query rows that share their keys
-
 // A warp's 32 rows (lane = row) of 32 columns.
 __device__ __forceinline__ void tmem_ld_rows32(uint32_t t, uint32_t* r) {
   asm volatile(
@@ -51,6 +53,60 @@ __device__ __forceinline__ void tmem_st_rows32(uint32_t t, const uint32_t* r) {
       "tcgen05.st.sync.aligned.32x32b.x32.b32 [%32], {%0, %1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, %15, %16, %17, %18, %19, %20, %21, %22, %23, %24, %25, %26, %27, %28, %29, %30, %31};" ::"r"(r[0]), "r"(r[1]), "r"(r[2]), "r"(r[3]), "r"(r[4]), "r"(r[5]), "r"(r[6]), "r"(r[7]), "r"(r[8]), "r"(r[9]), "r"(r[10]), "r"(r[11]), "r"(r[12]), "r"(r[13]), "r"(r[14]), "r"(r[15]), "r"(r[16]), "r"(r[17]), "r"(r[18]), "r"(r[19]), "r"(r[20]), "r"(r[21]), "r"(r[22]), "r"(r[23]), "r"(r[24]), "r"(r[25]), "r"(r[26]), "r"(r[27]), "r"(r[28]), "r"(r[29]), "r"(r[30]), "r"(r[31]),
       "r"(t)
       : "memory");
+}
+
+__device__ __forceinline__ float max3(float a, float b, float c) {
+  float d;
+  asm("max.f32 %0, %1, %2, %3;" : "=f"(d) : "f"(a), "f"(b), "f"(c));
+  return d;
+}
+
+// Two fp32 operations in one instruction.
+__device__ __forceinline__ void fma2(float& x, float& y, float c, float d) {
+  asm("{\n\t.reg .b64 s, t, u;\n\t"
+      "mov.b64 s, {%0, %1};\n\t"
+      "mov.b64 t, {%2, %2};\n\t"
+      "mov.b64 u, {%3, %3};\n\t"
+      "fma.rn.f32x2 s, s, t, u;\n\t"
+      "mov.b64 {%0, %1}, s;\n\t}"
+      : "+f"(x), "+f"(y)
+      : "f"(c), "f"(d));
+}
+__device__ __forceinline__ void add2(float& x, float& y, float u, float v) {
+  asm("{\n\t.reg .b64 s, t;\n\t"
+      "mov.b64 s, {%0, %1};\n\t"
+      "mov.b64 t, {%2, %3};\n\t"
+      "add.rn.f32x2 s, s, t;\n\t"
+      "mov.b64 {%0, %1}, s;\n\t}"
+      : "+f"(x), "+f"(y)
+      : "f"(u), "f"(v));
+}
+
+// Eight words a lane that belong to one of four columns of two each: lane q of four neighbouring ones gets column q of
+// all four (its words 2 j, 2 j + 1: lane j's).
+__device__ __forceinline__ void transpose4(uint32_t (&w)[8], int lane) {
+#pragma unroll
+  for (int bit = 1; bit < 4; bit <<= 1) {
+    const bool up = lane & bit;
+#pragma unroll
+    for (int c = 0; c < 4; ++c) {
+      if (c & bit) continue;
+#pragma unroll
+      for (int e = 0; e < 2; ++e) {
+        uint32_t &x = w[2 * c + e], &y = w[2 * (c | bit) + e];
+        const uint32_t got = __shfl_xor_sync(0xFFFFFFFFu, up ? x : y, bit);
+        if (up) x = got;
+        else y = got;
+      }
+    }
+  }
+}
+
+// 32 bytes, one sector.
+__device__ __forceinline__ void st_global32(void* p, const uint32_t (&w)[8]) {
+  asm volatile("st.global.v8.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8};" ::"l"(p), "r"(w[0]), "r"(w[1]), "r"(w[2]), "r"(w[3]), "r"(w[4]),
+               "r"(w[5]), "r"(w[6]), "r"(w[7])
+               : "memory");
 }
 
 __device__ __forceinline__ void st_shared16(uint32_t addr, uint4 v) {
@@ -112,7 +168,7 @@ struct PromptShape {
   static constexpr int NS = DH == 64 ? 8 : 5;     // ring stages
   static constexpr int kQ = QT * 128 * DH * 2, kStage = 128 * DH * 2 / CPT;
   static constexpr int oRing = kQ, oMeta = oRing + NS * kStage;
-  static constexpr int kMeta = 2048, kSmem = oMeta + kMeta;
+  static constexpr int kMeta = 3072, kSmem = oMeta + kMeta;
   static constexpr uint32_t cS = 0, cO = 256;     // columns of tensor memory: S at 0 and 128, O from 256 on
   static_assert(kSmem <= 227 * 1024, "shared memory");
   // stages of K of tile j, and of V, in the order of their use: S of the first item(s), then P.V of item k and S of item k + 2
@@ -120,60 +176,141 @@ struct PromptShape {
   __device__ static int v_at(int j, int nt) { return (DH == 256 ? min(j + 2, nt) + j : 2 * j + 1) * CPT; }
 };
 
-struct PromptMeta {
-  uint64_t full[8], empty[8], s_full[2], p_full[2], pv_done[2], m_full[2][4], q_full, v_go, v_ok, drain;
-  uint32_t tmem, copied;
-  int fail, nan;
-  int unit[4];   // first packed position of the row, its positions, the unit's first query row
-  float m[128];  // one query tile: the running maxima
+// A unit: a row's positions, a group of heads, and the unit's number in the row.
+struct Unit {
+  int a0, n, grp, j;
 };
-static_assert(sizeof(PromptMeta) <= 2048, "meta");
+
+// Unit x of the order in which blocks take them (`per` positions each): a row's
+// later units are its longest, so units go by their number in the row, the highest
+// first, at each number all rows that have one, for each all groups of heads. False
+// behind the last. By a whole warp. (The number is looked for by halving: F(j), the
+// units with numbers from j on, falls as j rises.)
+__device__ __forceinline__ bool find_unit(const PromptArgs& a, int per, long long x, Unit& u) {
+  const int lane = threadIdx.x & 31, groups = a.n_q / a.group;
+  const long long y = x / groups;
+  u.grp = (int)(x - y * groups);
+  constexpr int kOwn = 4;  // rows a lane keeps
+  int own[kOwn], most = 0;
+#pragma unroll
+  for (int q = 0; q < kOwn; ++q) {
+    const int r = lane + 32 * q;
+    int a0, n = 0;
+    if (r < a.rows) prompt_row(a.start, a.tokens, r, a0, n);
+    own[q] = (n + per - 1) / per;
+    most = max(most, own[q]);
+  }
+  auto units_of = [&](int r) {
+    int a0, n;
+    prompt_row(a.start, a.tokens, r, a0, n);
+    return (n + per - 1) / per;
+  };
+  for (int r = lane + 32 * kOwn; r < a.rows; r += 32) most = max(most, units_of(r));
+  most = __reduce_max_sync(0xFFFFFFFFu, most);
+  auto from = [&](int j) {  // (units of a call: below 2^31)
+    int sum = 0;
+#pragma unroll
+    for (int q = 0; q < kOwn; ++q) sum += max(0, own[q] - j);
+    for (int r = lane + 32 * kOwn; r < a.rows; r += 32) sum += max(0, units_of(r) - j);
+    return __reduce_add_sync(0xFFFFFFFFu, sum);
+  };
+  if (y >= from(0)) return false;
+  int lo = 0, hi = most;  // F(lo) > y >= F(hi)
+  while (hi - lo > 1) {
+    const int mid = (lo + hi) >> 1;
+    if (from(mid) > y) lo = mid;
+    else hi = mid;
+  }
+  u.j = lo;
+  int left = (int)y - from(lo + 1);  // the so manieth row with more than lo units
+  for (int r0 = 0; r0 < a.rows; r0 += 32) {
+    int a0 = 0, n = 0;
+    if (r0 + lane < a.rows) prompt_row(a.start, a.tokens, r0 + lane, a0, n);
+    const unsigned has = __ballot_sync(0xFFFFFFFFu, (n + per - 1) / per > lo);
+    if (left < __popc(has)) {
+      const int src = __fns(has, 0, left + 1);
+      u.a0 = __shfl_sync(0xFFFFFFFFu, a0, src);
+      u.n = __shfl_sync(0xFFFFFFFFu, n, src);
+      return true;
+    }
+    left -= __popc(has);
+  }
+  return false;
+}
+
+constexpr int kUnits = 4;  // units handed out ahead
+
+struct PromptMeta {
+  uint64_t full[8], empty[8], s_full[2], p_full[2][2], pv_done[2], m_full[2][4], q_full, q_empty, o_empty[2], v_go, v_ok, drain;
+  uint64_t unit_full[kUnits], unit_empty[kUnits];
+  Unit unit[kUnits];
+  uint32_t tmem, copied;
+  int fail;
+  int nan[kUnits];     // 1 + the last unit of this slot that had something cleaned out of V that one of its queries may see
+  float m[128];        // one query tile: the running maxima
+  float l[2][128];     // the groups' sums
+};
+static_assert(sizeof(PromptMeta) <= 3072, "meta");
+
+// x with what was cleaned out of V in dimension d and the query of row `dst` of the output sees. (Rare and slow.)
+__device__ __noinline__ float add_cleaned(const PromptArgs& a, const Unit& u, int p0, int p1, long long dst, int d, float x) {
+  if (dst < 0) return x;
+  const int pos = (int)(dst / a.n_q) - u.a0, head = u.grp * a.group / (a.n_q / a.n_kv);
+  const uint16_t* v = static_cast<const uint16_t*>(a.v) + (long long)u.a0 * a.ts[2] + (long long)head * a.hs[2] + d;
+  for (int t = a.window > 0 ? max(0, pos - (a.window - 1)) : 0; t <= pos; ++t) {
+    if (t <= p0 && (a.window == 0 || t > p1 - a.window)) {
+      t = p0;  // (all queries of the unit see it and what follows up to here: V was left as it was)
+      continue;
+    }
+    const float y = bf16_to_f(v[t * a.ts[2]]);
+    if (!isfinite(y)) x += y;
+  }
+  return x;
+}
 
 template <int DH>
 __global__ void __launch_bounds__(kPromptThreads, 1)
-    k_prompt_tc(const __grid_constant__ PromptArgs a, const __grid_constant__ CUtensorMap mk, const __grid_constant__ CUtensorMap mv) {
+    k_prompt_tc(const __grid_constant__ PromptArgs a, const __grid_constant__ CUtensorMap mq, const __grid_constant__ CUtensorMap mk,
+                const __grid_constant__ CUtensorMap mv) {
   using S = PromptShape<DH>;
   constexpr int CL = S::CL;
   extern __shared__ __align__(1024) uint8_t smem_raw[];
   auto& M = *reinterpret_cast<PromptMeta*>(smem_raw + S::oMeta);
   const uint32_t sm = smem_u32(smem_raw);
   const int warp = __shfl_sync(0xFFFFFFFFu, (int)threadIdx.x >> 5, 0), lane = threadIdx.x & 31;
-  const int G = a.n_q / a.n_kv, rank = CL == 1 ? 0 : (int)(blockIdx.x & 1), x = blockIdx.x / CL, g = x % a.n_kv;
+  const int G = a.group, rank = CL == 1 ? 0 : (int)(blockIdx.x & 1);
+  const int PT = 128 / G;  // positions of a query tile
   volatile int* fail = &M.fail;
   auto wait_all = [&](uint64_t* bar, uint32_t parity) { return __all_sync(0xFFFFFFFFu, wait(bar, parity, fail)) != 0; };
 
-  if (threadIdx.x == 32) {
+  if (threadIdx.x == 0) {
     for (int i = 0; i < 8; ++i) {
       mbar_init(smem_u32(&M.full[i]), 1);
       mbar_init(smem_u32(&M.empty[i]), CL);
     }
     for (int i = 0; i < 2; ++i) {
       mbar_init(smem_u32(&M.s_full[i]), 1);
-      mbar_init(smem_u32(&M.p_full[i]), 4);
+      for (int h = 0; h < 2; ++h) mbar_init(smem_u32(&M.p_full[i][h]), 4);
       mbar_init(smem_u32(&M.pv_done[i]), 1);
+      mbar_init(smem_u32(&M.o_empty[i]), 4);
       for (int w = 0; w < 4; ++w) mbar_init(smem_u32(&M.m_full[i][w]), 1);
     }
-    mbar_init(smem_u32(&M.q_full), 8);
+    mbar_init(smem_u32(&M.q_full), 1);
+    mbar_init(smem_u32(&M.q_empty), 1);
     mbar_init(smem_u32(&M.v_go), 1);
     mbar_init(smem_u32(&M.v_ok), 2);
     mbar_init(smem_u32(&M.drain), 1);
-    M.fail = M.nan = 0;
+    for (int i = 0; i < kUnits; ++i) {
+      mbar_init(smem_u32(&M.unit_full[i]), 1);
+      mbar_init(smem_u32(&M.unit_empty[i]), 11);  // the warps but the one that hands them out
+      M.nan[i] = 0;
+    }
+    M.fail = 0;
     M.copied = 0;
     asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
   }
+  // (tensor memory after the kernels before this one have given theirs back, and before a dependent kernel may take some)
   pdl_wait();
-  if (warp == 0) {
-    int a0 = 0, n = 0, j = 0;
-    const bool some = find_tile(a, G, kUnit, x / a.n_kv, a0, n, j);
-    if (lane == 0) {
-      M.unit[0] = a0;
-      M.unit[1] = some ? n : 0;
-      M.unit[2] = j * kUnit;
-    }
-  }
-  __syncthreads();
-  const int a0 = M.unit[0], n = M.unit[1], f0 = M.unit[2];
-  if (n == 0) return;  // (both blocks of a cluster)
   if (warp == 0) {
     asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], 512;" ::"r"(smem_u32(&M.tmem)) : "memory");
     asm volatile("tcgen05.relinquish_alloc_permit.cta_group::1.sync.aligned;" ::: "memory");
@@ -182,70 +319,125 @@ __global__ void __launch_bounds__(kPromptThreads, 1)
   __syncthreads();
   if (CL > 1) cluster_sync();  // the other block's barriers are there
   tc_fence_after();
-  pdl_trigger();  // (with tensor memory in hand: a dependent kernel may take what is left of it before it waits for this one)
+  pdl_trigger();
   const uint32_t tmem = M.tmem;
-  // positions of the unit's first and last query row, and its tiles of 128 keys
-  const int p0 = f0 / G, p1 = (min(n * G, f0 + kUnit) - 1) / G;
-  const int t_first = a.window > 0 ? max(0, p0 - (a.window - 1)) / 128 : 0, nt = p1 / 128 + 1 - t_first;
-  const int items = nt * S::QT;
-  // whether some query of rows at positions q0 to q1 does not see some position of a tile
-  auto edge = [&](int j, int q0, int q1) {
-    const int t0 = (t_first + j) * 128;
-    return t0 + 127 > q0 || (a.window > 0 && t0 <= q1 - a.window);
+
+  // what a unit asks for: positions p0 to p1 of its queries, tiles of 128 keys from t_first on
+  struct Span {
+    int p0, p1, t_first, nt;
+  };
+  auto span = [&](const Unit& u) {
+    Span s;
+    s.p0 = u.j * 2 * PT;
+    s.p1 = min(u.n, s.p0 + 2 * PT) - 1;
+    s.t_first = a.window > 0 ? max(0, s.p0 - (a.window - 1)) / 128 : 0;
+    s.nt = s.p1 / 128 + 1 - s.t_first;
+    return s;
+  };
+  // whether some query at positions q0 to q1 does not see some position of the tile from t0 on
+  auto edge = [&](int t0, int q0, int q1) { return t0 + 127 > q0 || (a.window > 0 && t0 <= q1 - a.window); };
+  // steps of 16 keys of a tile that some query of the unit sees
+  auto steps = [&](const Span& s, int t0, int& lo, int& hi) {
+    hi = min(8, (s.p1 - t0) / 16 + 1);
+    lo = a.window > 0 ? max(0, max(0, s.p0 - (a.window - 1)) - t0) / 16 : 0;
+  };
+  // unit number i of this block; false behind the last
+  auto take = [&](int i, Unit& u) {
+    if (!wait_all(&M.unit_full[i % kUnits], i / kUnits & 1)) return false;
+    u = M.unit[i % kUnits];
+    __syncwarp();
+    if (lane == 0) mbar_arrive(smem_u32(&M.unit_empty[i % kUnits]));
+    return u.n > 0;
   };
 
   if (warp == 8) {
-    // ---------------------------------------------------------- copies
-    if (lane == 0) {
-      int at = 0;
-      bool ok = true;
-      auto tile = [&](const CUtensorMap* map, int j, bool is_v) {
+    // ---------------------------------------------------------- units, copies
+    int at = 0;
+    bool ok = true;
+    Unit u;
+    auto tile = [&](const CUtensorMap* map, int head, int pos, bool is_v) {
 #pragma unroll 1
-        for (int c = 0; c < S::CPT && ok; ++c, ++at) {
-          const int st = at % S::NS, round = at / S::NS;
-          if (round > 0 && !(ok = wait(&M.empty[st], (round - 1) & 1, fail))) return;
-          const uint32_t bar = smem_u32(&M.full[st]), dst = sm + S::oRing + st * S::kStage;
-          mbar_expect_tx(bar, S::kStage);
-          M.copied = at + 1;
-          const int pos = a0 + (t_first + j) * 128;
-          if constexpr (DH == 256) {
-            // K: 128 positions of half the dimensions; V: 64 positions of all. Half of it from each block
-            if (!is_v) {
-              tma_box<CL>(dst + rank * 16384, map, (2 * c + rank) * 64, g, pos, bar);
-            } else {
-              for (int b = 2 * rank; b < 2 * rank + 2; ++b) tma_box<CL>(dst + b * 8192, map, b * 64, g, pos + 64 * c, bar);
-            }
+      for (int c = 0; c < S::CPT && ok; ++c, ++at) {
+        const int st = at % S::NS, round = at / S::NS;
+        if (round > 0 && !(ok = wait(&M.empty[st], (round - 1) & 1, fail))) return;
+        const uint32_t bar = smem_u32(&M.full[st]), dst = sm + S::oRing + st * S::kStage;
+        mbar_expect_tx(bar, S::kStage);
+        M.copied = at + 1;
+        if constexpr (DH == 256) {
+          // K: 128 positions of half the dimensions; V: 64 positions of all. Half of it from each block
+          if (!is_v) {
+            tma_box<CL>(dst + rank * 16384, map, (2 * c + rank) * 64, head, pos, bar);
           } else {
-            for (int b = 0; b < DH / 64; ++b) tma_box<CL>(dst + b * 16384, map, b * 64, g, pos, bar);
+            for (int b = 2 * rank; b < 2 * rank + 2; ++b) tma_box<CL>(dst + b * 8192, map, b * 64, head, pos + 64 * c, bar);
           }
-        }
-      };
-      if (DH == 256) {
-        tile(&mk, 0, false);
-        if (nt > 1) tile(&mk, 1, false);
-        for (int j = 0; j < nt && ok; ++j) {
-          tile(&mv, j, true);
-          if (j + 2 < nt) tile(&mk, j + 2, false);
-        }
-      } else {
-        for (int j = 0; j < nt && ok; ++j) {
-          tile(&mk, j, false);
-          tile(&mv, j, true);
+        } else {
+          for (int b = 0; b < DH / 64; ++b) tma_box<CL>(dst + b * 16384, map, b * 64, head, pos, bar);
         }
       }
-      // the last arrivals on this block's barriers, the other block's among them
-      for (int i = max(0, at - S::NS); i < at && ok; ++i) ok = wait(&M.empty[i % S::NS], i / S::NS & 1, fail);
+    };
+    // unit i of this block, found and handed out; false behind the last
+    auto hand_out = [&](int i, Unit& u) {
+      // there and back: who has the longest unit of one turn has the shortest of the next
+      const int blocks = gridDim.x / CL, b = blockIdx.x / CL;
+      if (!find_unit(a, 2 * PT, (long long)i * blocks + (i & 1 ? blocks - 1 - b : b), u)) u.n = 0;
+      if (i >= kUnits && !wait_all(&M.unit_empty[i % kUnits], (i / kUnits - 1) & 1)) return false;
+      if (lane == 0) {
+        M.unit[i % kUnits] = u;
+        mbar_arrive(smem_u32(&M.unit_full[i % kUnits]));
+      }
+      return u.n > 0;
+    };
+    Unit ahead;
+    bool some = hand_out(0, ahead);
+#pragma unroll 1
+    for (int i = 0; some; ++i) {
+      u = ahead;
+      some = hand_out(i + 1, ahead);  // (before the copies of this one, which wait for room)
+      if (lane == 0) {
+        const Span s = span(u);
+        if (i > 0) ok = wait(&M.q_empty, (i - 1) & 1, fail);
+        if (ok) {
+          mbar_expect_tx(smem_u32(&M.q_full), S::QT * (DH / 64) * PT * G * 128);
+          for (int q = 0; q < S::QT; ++q)
+            for (int b = 0; b < DH / 64; ++b)
+              tma_box<1>(sm + q * 128 * DH * 2 + b * 16384, &mq, b * 64, u.grp * G, u.a0 + s.p0 + (CL == 2 ? rank : q) * PT, smem_u32(&M.q_full));
+        }
+        const int head = u.grp * G / (a.n_q / a.n_kv), pos = u.a0 + s.t_first * 128;
+        if (DH == 256) {
+          if (ok) tile(&mk, head, pos, false);
+          if (s.nt > 1 && ok) tile(&mk, head, pos + 128, false);
+#pragma unroll 1
+          for (int j = 0; j < s.nt && ok; ++j) {
+            tile(&mv, head, pos + 128 * j, true);
+            if (j + 2 < s.nt && ok) tile(&mk, head, pos + 128 * (j + 2), false);
+          }
+        } else {
+#pragma unroll 1
+          for (int j = 0; j < s.nt && ok; ++j) {
+            tile(&mk, head, pos + 128 * j, false);
+            if (ok) tile(&mv, head, pos + 128 * j, true);
+          }
+        }
+      }
+      ok = __shfl_sync(0xFFFFFFFFu, ok, 0);
+      if (!ok) break;
     }
+    // the last arrivals on this block's barriers, the other block's among them
+    if (lane == 0)
+      for (int i = max(0, at - S::NS); i < at && ok; ++i) ok = wait(&M.empty[i % S::NS], i / S::NS & 1, fail);
     __syncwarp();
   } else if (warp == 9) {
     // ---------------------------------------------------------- MMAs
     constexpr uint32_t idS = idesc_bf(128, 128, false), idO = idesc_bf(128, DH, true);
     const uint32_t tm = __shfl_sync(0xFFFFFFFFu, tmem, 0);
     const uint64_t dq = tc::sdesc(sm);
-    int edges = 0;  // tiles whose V was cleaned
-    bool ok = wait_all(&M.q_full, 0);
+    int edges = 0, base = 0, items = 0;  // tiles whose V was cleaned; ring stages and items before the unit
+    int done[2] = {0, 0};                // items of each place before the unit
+    bool ok = true;
+    Unit u;
+    Span sp = {};
     auto issue_s = [&](int k) {
-      const int j = S::QT == 2 ? k >> 1 : k, slot = k & 1, at = S::k_at(j);
+      const int j = S::QT == 2 ? k >> 1 : k, slot = k & 1, at = base + S::k_at(j);
 #pragma unroll 1
       for (int c = 0; c < S::CPT; ++c) {
         const int st = (at + c) % S::NS;
@@ -255,16 +447,16 @@ __global__ void __launch_bounds__(kPromptThreads, 1)
         const uint64_t da = dq + (S::QT == 2 ? slot * (128 * DH * 2 / 16) : 0) + c * (DH / S::CPT / 64) * 1024;
 #pragma unroll
         for (int e = 0; e < DH / S::CPT / 16; ++e)
-          mma_f16_ss(tm + S::cS + slot * 128, da + (e >> 2) * 1024 + (e & 3) * 2, dk + (e >> 2) * 1024 + (e & 3) * 2, idS,
-                        (c | e) > 0 ? 1u : 0u);
+          mma_f16_ss(tm + S::cS + slot * 128, da + (e >> 2) * 1024 + (e & 3) * 2, dk + (e >> 2) * 1024 + (e & 3) * 2, idS, (c | e) > 0 ? 1u : 0u);
         if (S::QT == 1 || slot == 1) commit_all<CL>(smem_u32(&M.empty[st]));
       }
       mma_commit_elect(smem_u32(&M.s_full[slot]));
+      if (k == items - 1) mma_commit_elect(smem_u32(&M.q_empty));
       return true;
     };
-    auto issue_pv = [&](int k) {
-      const int j = S::QT == 2 ? k >> 1 : k, slot = k & 1, at = S::v_at(j, nt);
-      const bool first = S::QT == 1 || slot == 0, clean = first && edge(j, p0, p1);
+    auto issue_pv = [&](int i, int k) {
+      const int j = S::QT == 2 ? k >> 1 : k, slot = k & 1, at = base + S::v_at(j, sp.nt), t0 = (sp.t_first + j) * 128;
+      const bool first = S::QT == 1 || slot == 0, clean = first && edge(t0, sp.p0, sp.p1);
       if (first) {
 #pragma unroll 1
         for (int c = 0; c < S::CPT; ++c)
@@ -272,28 +464,52 @@ __global__ void __launch_bounds__(kPromptThreads, 1)
         if (clean && lane == 0) mbar_arrive(smem_u32(&M.v_go));
         __syncwarp();
       }
-      if (!wait_all(&M.p_full[slot], k >> 1 & 1)) return false;
-      if (clean && !wait_all(&M.v_ok, edges++ & 1)) return false;
-      tc_fence_after();
+      if (i > 0 && k < S::QT) {  // O of the unit before has been read
+        if (!wait_all(&M.o_empty[slot], (i - 1) & 1)) return false;
+        if (S::QT == 1 && !wait_all(&M.o_empty[1], (i - 1) & 1)) return false;
+      }
+      int lo, hi;
+      steps(sp, t0, lo, hi);
+      uint32_t acc = k >= S::QT ? 1u : 0u;
+      const uint32_t d = tm + S::cO + (S::QT == 2 ? slot * DH : 0), p = tm + S::cS + slot * 128;
 #pragma unroll 1
-      for (int c = 0; c < S::CPT; ++c) {
-        const int st = (at + c) % S::NS;
-        const uint64_t dv = sdesc_mn(sm + S::oRing + st * S::kStage, 16384 / S::CPT);
+      for (int c = 0; c < 2; ++c) {  // 64 keys
+        if (!wait_all(&M.p_full[slot][c], (done[slot] + (k >> 1)) & 1)) return false;
+        if (clean && c == 0 && !wait_all(&M.v_ok, edges++ & 1)) return false;
+        tc_fence_after();
+        const int st = (at + (S::CPT == 2 ? c : 0)) % S::NS;
+        const uint64_t dv = sdesc_mn(sm + S::oRing + st * S::kStage, 16384 / S::CPT) + (S::CPT == 2 ? 0 : c * 512);
+        if (lo <= 4 * c && hi >= 4 * c + 4) {
 #pragma unroll
-        for (int e = 0; e < 8 / S::CPT; ++e)
-          mma_f16_ts(tm + S::cO + (S::QT == 2 ? slot * DH : 0), tm + S::cS + slot * 128 + (c * (8 / S::CPT) + e) * 8, dv + e * 128, idO,
-                        k >= S::QT || (c | e) > 0 ? 1u : 0u);
-        if (S::QT == 1 || slot == 1) commit_all<CL>(smem_u32(&M.empty[st]));
+          for (int e = 0; e < 4; ++e) mma_f16_ts(d, p + c * 32 + e * 8, dv + e * 128, idO, e > 0 ? 1u : acc);
+          acc = 1u;
+        } else {
+#pragma unroll 1
+          for (int e = max(0, lo - 4 * c); e < min(4, hi - 4 * c); ++e) {
+            mma_f16_ts(d, p + c * 32 + e * 8, dv + e * 128, idO, acc);
+            acc = 1u;
+          }
+        }
+        if ((S::QT == 1 || slot == 1) && (S::CPT == 2 || c == 1)) commit_all<CL>(smem_u32(&M.empty[st]));
       }
       mma_commit_elect(smem_u32(&M.pv_done[slot]));
       return true;
     };
-    ok = ok && issue_s(0);
-    if (items > 1) ok = ok && issue_s(1);
 #pragma unroll 1
-    for (int k = 0; k < items && ok; ++k) {
-      ok = issue_pv(k);
-      if (ok && k + 2 < items) ok = issue_s(k + 2);
+    for (int i = 0; ok && take(i, u); ++i) {
+      sp = span(u);
+      items = sp.nt * S::QT;
+      ok = wait_all(&M.q_full, i & 1);
+      tc_fence_after();
+      ok = ok && issue_s(0) && (items < 2 || issue_s(1));
+#pragma unroll 1
+      for (int k = 0; k < items && ok; ++k) {
+        ok = issue_pv(i, k);
+        if (ok && k + 2 < items) ok = issue_s(k + 2);
+      }
+      base += 2 * sp.nt * S::CPT;
+      done[0] += (items + 1) / 2;
+      done[1] += items / 2;
     }
     // what was issued ends before its operands and tensor memory go
     mma_commit_elect(smem_u32(&M.drain));
@@ -302,223 +518,244 @@ __global__ void __launch_bounds__(kPromptThreads, 1)
   } else if (warp >= 10) {
     // ---------------------------------------------------------- V of edge tiles
     const int me = threadIdx.x - 320;
-    constexpr int kSegs = DH / 8;  // 16-byte pieces of a position
-    int edges = 0;
+    constexpr int kSegs = DH / 8, kRows = 128 / S::CPT;  // 16-byte pieces of a position, positions of a stage
+    int edges = 0, base = 0;
+    bool ok = true;
+    Unit u;
 #pragma unroll 1
-    for (int j = 0; j < nt; ++j) {
-      if (!edge(j, p0, p1)) continue;
-      // (told by the MMA warp, which has seen all stages of the ring in turn)
-      if (!wait_all(&M.v_go, edges++ & 1)) break;
-      const int t0 = (t_first + j) * 128, at = S::v_at(j, nt);
+    for (int i = 0; ok && take(i, u); ++i) {
+      const Span sp = span(u);
 #pragma unroll 1
-      for (int c = 0; c < S::CPT; ++c) {
-        const int st = (at + c) % S::NS;
-        const uint32_t base = sm + S::oRing + st * S::kStage;
-        constexpr int kRows = 128 / S::CPT;
-        // positions that all queries of the unit see lie between those that some do not
-        for (int i = me; i < kRows * kSegs; i += 64) {
-          const int r = i / kSegs, e = i % kSegs, t = t0 + c * kRows + r;
-          if (t <= p0 && (a.window == 0 || t > p1 - a.window)) continue;
-          const uint32_t addr = base + (e >> 3) * (kRows * 128) + r * 128 + (e & 7) * 16;
-          if (t > p1 || (a.window > 0 && t <= p0 - a.window)) {
-            st_shared16(addr, make_uint4(0u, 0u, 0u, 0u));
-            continue;
-          }
-          uint4 v;
-          asm volatile("ld.shared.v4.b32 {%0, %1, %2, %3}, [%4];" : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w) : "r"(addr));
-          uint32_t w[4] = {v.x, v.y, v.z, v.w}, bad = 0;
+      for (int j = 0; j < sp.nt; ++j) {
+        const int t0 = (sp.t_first + j) * 128, at = base + S::v_at(j, sp.nt);
+        if (!edge(t0, sp.p0, sp.p1)) continue;
+        // (told by the MMA warp, which has seen all stages of the ring in turn)
+        if (!(ok = wait_all(&M.v_go, edges++ & 1))) break;
+        int lo, hi;
+        steps(sp, t0, lo, hi);
+        bool found = false;
+        // positions [r0, r1) of the tile without what is not finite
+        auto clean = [&](int r0, int r1) {
+          // a thread has a piece of every 64 / kSegs th position
+          const int q = me % kSegs, step = 64 / kSegs;
+#pragma unroll 1
+          for (int c = 0; c < S::CPT; ++c) {
+            const uint32_t to = sm + S::oRing + (at + c) % S::NS * S::kStage + (q >> 3) * (kRows * 128) + (q & 7) * 16;
+            const int end = min(r1, (c + 1) * kRows) - c * kRows;
+#pragma unroll 1
+            for (int r = max(r0, c * kRows) - c * kRows + me / kSegs; r < end; r += 4 * step) {
+              uint4 v[4];
 #pragma unroll
-          for (int q = 0; q < 4; ++q) {
-            const uint32_t lo = (w[q] & 0x7F80u) == 0x7F80u ? 0xFFFFu : 0u, hi = (w[q] & 0x7F800000u) == 0x7F800000u ? 0xFFFF0000u : 0u;
-            bad |= lo | hi;
-            w[q] &= ~(lo | hi);
+              for (int x = 0; x < 4; ++x)
+                asm volatile("ld.shared.v4.b32 {%0, %1, %2, %3}, [%4];"
+                             : "=r"(v[x].x), "=r"(v[x].y), "=r"(v[x].z), "=r"(v[x].w)
+                             : "r"(to + min(r + x * step, end - 1) * 128));
+              // an exponent of all ones carries into its sign's place
+              auto odd = [](uint32_t w) { return ((w & 0x7F807F80u) + 0x00800080u) & 0x80008000u; };
+#pragma unroll
+              for (int x = 0; x < 4; ++x)
+                if (odd(v[x].x) | odd(v[x].y) | odd(v[x].z) | odd(v[x].w)) {  // (a piece that two threads have: both store the same)
+                  uint32_t w[4] = {v[x].x, v[x].y, v[x].z, v[x].w};
+#pragma unroll
+                  for (int y = 0; y < 4; ++y) w[y] &= ~((odd(w[y]) >> 15) * 0xFFFFu);
+                  const int rx = min(r + x * step, end - 1), t = t0 + c * kRows + rx;
+                  st_shared16(to + rx * 128, make_uint4(w[0], w[1], w[2], w[3]));
+                  found |= t <= sp.p1 && !(a.window > 0 && t <= sp.p0 - a.window);
+                }
+            }
           }
-          if (bad) {
-            M.nan = 1;
-            st_shared16(addr, make_uint4(w[0], w[1], w[2], w[3]));
-          }
-        }
+        };
+        const int low = a.window > 0 ? min(16 * hi, max(16 * lo, sp.p1 - a.window + 1 - t0)) : 16 * lo;
+        clean(16 * lo, low);
+        clean(max(low, max(16 * lo, sp.p0 + 1 - t0)), 16 * hi);
+        if (found) M.nan[i % kUnits] = i + 1;
+        fence_async();
+        __syncwarp();
+        if (lane == 0) mbar_arrive(smem_u32(&M.v_ok));
       }
-      fence_async();
-      __syncwarp();
-      if (lane == 0) mbar_arrive(smem_u32(&M.v_ok));
+      base += 2 * sp.nt * S::CPT;
     }
   } else {
     // ---------------------------------------------------------- softmax
     const int slot = warp >> 2, quarter = warp & 3, row = threadIdx.x & 127;
     const uint32_t lanes = (uint32_t)(32 * quarter) << 16;
-    const int fq = f0 + (CL == 2 ? rank : slot) * 128;  // the query tile's first row
-    // ---- queries to swizzled shared memory, negated for a negative scale
-    {
-      constexpr int kPer = DH / 8;                       // 16-byte pieces of a row
-      const uint32_t flip = a.scale < 0.f ? 0x80008000u : 0u;
-      const int r0 = S::QT == 2 ? 32 * quarter : 16 * warp, rows = S::QT == 2 ? 32 : 16;
-#pragma unroll 4
-      for (int i = lane; i < rows * kPer; i += 32) {
-        const int r = r0 + i / kPer, e = i % kPer, f = fq + r;
-        uint4 v = make_uint4(0u, 0u, 0u, 0u);
-        if (f < n * G) {
-          const int p = f / G, h = g * G + f - p * G;
-          v = ld_stream(static_cast<const uint16_t*>(a.q) + (long long)(a0 + p) * a.ts[0] + (long long)h * a.hs[0] + 8 * e);
-          v.x ^= flip, v.y ^= flip, v.z ^= flip, v.w ^= flip;
-        }
-        st_shared16(sm + (S::QT == 2 ? slot * 128 * DH * 2 : 0) + (e >> 3) * 16384 + r * 128 + (((e & 7) ^ (r & 7)) << 4), v);
-      }
-      fence_async();
-      __syncwarp();
-      if (lane == 0) mbar_arrive(smem_u32(&M.q_full));
-    }
-    const int f = fq + row;
-    const bool real = f < n * G;
-    const int pos = real ? f / G : -1;
-    const int q0 = fq / G, q1 = (min(n * G, fq + 128) - 1) / G;
     const unsigned win = a.window > 0 ? (unsigned)a.window : 0x80000000u;
     // (above 0: -inf times 0 would be no weight)
     const float c = fmaxf(fabsf(a.scale) * 1.44269504f, FLT_MIN);
-    float m = -INFINITY, l = 0.f;
+    const int in_pos = row / G, in_head = row - in_pos * G;  // the row's place in a query tile
+    int done[2] = {0, 0};
     bool ok = true;
+    Unit u;
 #pragma unroll 1
-    for (int k = slot; k < items; k += 2) {
-      const int j = S::QT == 2 ? k >> 1 : k;
-      ok = wait_all(&M.s_full[slot], k >> 1 & 1);
-      if (!ok) break;
-      tc_fence_after();
-      uint32_t s[128];
-#pragma unroll
-      for (int q = 0; q < 4; ++q) tmem_ld_rows32(tmem + S::cS + slot * 128 + 32 * q + lanes, s + 32 * q);
-      tc_wait_ld();
-#pragma unroll
-      for (int e = 0; e < 128; ++e) pin(s[e]);
-      if (edge(j, q0, q1)) {
-        const int rel = pos - (t_first + j) * 128;
-#pragma unroll
-        for (int e = 0; e < 128; ++e)
-          if ((unsigned)(rel - e) >= win) s[e] = 0xFF800000u;  // -inf: out of sight
-      }
-      float mx[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
-#pragma unroll
-      for (int e = 0; e < 128; e += 4)
-#pragma unroll
-        for (int q = 0; q < 4; ++q) mx[q] = fmaxf(mx[q], __uint_as_float(s[e + q]));
-      const float top = fmaxf(fmaxf(mx[0], mx[1]), fmaxf(mx[2], mx[3])) * c;
-      // the maximum so far; one that moves takes O with it
-      float was = m;
-      if (S::QT == 1 && k > 0) {
-        ok = wait_all(&M.m_full[slot ^ 1][quarter], (k - 1) >> 1 & 1);
+    for (int i = 0; ok && take(i, u); ++i) {
+      const Span sp = span(u);
+      const int items = sp.nt * S::QT;
+      const int q0 = sp.p0 + (CL == 2 ? rank : slot) * PT, q1 = min(u.n, q0 + PT) - 1;  // the query tile's positions
+      const bool real = in_pos < PT && q0 + in_pos < u.n;
+      const int pos = real ? q0 + in_pos : -1;
+      float m = -INFINITY, l = 0.f;
+#pragma unroll 1
+      for (int k = slot; k < items; k += 2) {
+        const int t0 = (sp.t_first + (S::QT == 2 ? k >> 1 : k)) * 128;
+        ok = wait_all(&M.s_full[slot], (done[slot] + (k >> 1)) & 1);
         if (!ok) break;
-        was = M.m[row];
-      }
-      const float now = top > was + 8.f || was == -INFINITY ? fmaxf(top, was) : was;
-      if (S::QT == 1) {
-        M.m[row] = now;
-        __syncwarp();
-        if (lane == 0) mbar_arrive(smem_u32(&M.m_full[slot][quarter]));
-      }
-      const bool moved = now != was && was != -INFINITY;
-      if (now != m) l = m == -INFINITY ? 0.f : l * ex2(m - now);
-      m = now;
-      if (__any_sync(0xFFFFFFFFu, moved)) {
-        if (S::QT == 1) {  // (with a tile of its own, S of this item came behind P.V of the last)
-          ok = wait_all(&M.pv_done[slot ^ 1], (k - 1) >> 1 & 1);
-          if (!ok) break;
-          tc_fence_after();
-        }
-        const float fac = moved ? ex2(was - now) : 1.f;
-#pragma unroll 1
-        for (int d = 0; d < DH; d += 16) {
-          const uint32_t t = tmem + S::cO + (S::QT == 2 ? slot * DH : 0) + d + lanes;
-          float o[16];
-          tc::tmem_ld16(t, o);
-          uint32_t u[16];
+        tc_fence_after();
+        uint32_t s[128];
 #pragma unroll
-          for (int e = 0; e < 16; ++e) u[e] = __float_as_uint(o[e] * fac);
-          tmem_st_rows16(t, u);
-        }
-      }
-      const float base = m == -INFINITY ? 0.f : m;
-      float sum[4] = {0.f, 0.f, 0.f, 0.f};
-#pragma unroll
-      for (int h = 0; h < 2; ++h) {
-        uint32_t w[32];
-#pragma unroll
-        for (int e = 0; e < 32; ++e) {
-          const float u = ex2(fmaf(__uint_as_float(s[64 * h + 2 * e]), c, -base)), v = ex2(fmaf(__uint_as_float(s[64 * h + 2 * e + 1]), c, -base));
-          sum[e & 1] += u;
-          sum[2 + (e & 1)] += v;
-          w[e] = pack_bf16(u, v);
-        }
-        tmem_st_rows32(tmem + S::cS + slot * 128 + 32 * h + lanes, w);
-      }
-      l += (sum[0] + sum[1]) + (sum[2] + sum[3]);
-      tc_wait_st();
-      tc_fence_before();
-      __syncwarp();
-      if (lane == 0) mbar_arrive(smem_u32(&M.p_full[slot]));
-    }
-    // ---- O of this query tile
-    int c0 = 0, cn = DH;
-    if (ok) {
-      const int last = S::QT == 2 ? items - 2 + slot : items - 1;
-      // (in turn: a parity tells only neighbouring phases apart)
-      ok = (last < 2 || wait_all(&M.pv_done[last & 1], ((last >> 1) - 1) & 1)) && wait_all(&M.pv_done[last & 1], last >> 1 & 1);
-      tc_fence_after();
-    }
-    if (S::QT == 1) {  // the groups' sums, then half of the dimensions each
-      float2* ml = reinterpret_cast<float2*>(smem_raw);  // (Q has been read)
-      ml[slot * 128 + row] = make_float2(m, l);
-      asm volatile("barrier.cta.sync.aligned 1, 256;" ::: "memory");
-      const float2 o = ml[(slot ^ 1) * 128 + row];
-      const float top = fmaxf(m, o.x);
-      l = (m == -INFINITY ? l : l * ex2(m - top)) + (o.x == -INFINITY ? o.y : o.y * ex2(o.x - top));
-      m = top;
-      c0 = slot * (DH / 2);
-      cn = DH / 2;
-    }
-    if (ok) {
-      const float r = l != 0.f ? 1.f / l : 0.f;
-      const long long dst = real ? (long long)(a0 + pos) * a.n_q + g * G + (f - pos * G) : 0;
-      if (real && a.lse && c0 == 0) a.lse[dst] = l != 0.f ? (m + log2f(l)) * 0.693147181f : -INFINITY;
-      const bool nan = *reinterpret_cast<volatile int*>(&M.nan) != 0;
-#pragma unroll 1
-      for (int d = c0; d < c0 + cn; d += 32) {
-        uint32_t o[32];
-        tmem_ld_rows32(tmem + S::cO + (S::QT == 2 ? slot * DH : 0) + d + lanes, o);
+        for (int q = 0; q < 4; ++q) tmem_ld_rows32(tmem + S::cS + slot * 128 + 32 * q + lanes, s + 32 * q);
         tc_wait_ld();
 #pragma unroll
-        for (int e = 0; e < 32; ++e) {
-          pin(o[e]);
-          o[e] = l != 0.f ? __float_as_uint(__uint_as_float(o[e]) * r) : 0u;
-        }
-        if (nan && real) {  // what was cleaned out of V and this query sees
-          const int lo = a.window > 0 ? max(0, pos - (a.window - 1)) : 0;
-#pragma unroll 1
-          for (int t = lo; t <= pos; ++t) {
-            if (t <= p0 && (a.window == 0 || t > p1 - a.window)) {
-              t = p0;  // (all queries of the unit see it and what follows up to here: V was left as it was)
-              continue;
-            }
-            const uint16_t* v = static_cast<const uint16_t*>(a.v) + (long long)(a0 + t) * a.ts[2] + (long long)g * a.hs[2] + d;
-#pragma unroll 1
-            for (int q = 0; q < 32; ++q) {
-              const float y = bf16_to_f(v[q]);
-              if (isfinite(y)) continue;
+        for (int e = 0; e < 128; ++e) pin(s[e]);
+        if (a.scale < 0.f) {
 #pragma unroll
-              for (int e = 0; e < 32; ++e)
-                if (e == q) o[e] = __float_as_uint(__uint_as_float(o[e]) + y);
-            }
+          for (int e = 0; e < 128; ++e) s[e] ^= 0x80000000u;
+        }
+        if (edge(t0, q0, q1)) {
+          const int rel = pos - t0;
+#pragma unroll
+          for (int e = 0; e < 128; ++e)
+            if ((unsigned)(rel - e) >= win) s[e] = 0xFF800000u;  // -inf: out of sight
+        }
+        float mx[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
+#pragma unroll
+        for (int e = 0; e < 128; e += 8)
+#pragma unroll
+          for (int q = 0; q < 4; ++q) mx[q] = max3(mx[q], __uint_as_float(s[e + 2 * q]), __uint_as_float(s[e + 2 * q + 1]));
+        const float top = fmaxf(fmaxf(mx[0], mx[1]), fmaxf(mx[2], mx[3])) * c;
+        // the maximum so far; one that moves takes O with it
+        float was = m;
+        if (S::QT == 1 && k > 0) {
+          ok = wait_all(&M.m_full[slot ^ 1][quarter], (done[slot ^ 1] + ((k - 1) >> 1)) & 1);
+          if (!ok) break;
+          was = M.m[row];
+        }
+        const float now = top > was + 8.f || was == -INFINITY ? fmaxf(top, was) : was;
+        if (S::QT == 1) {
+          M.m[row] = now;
+          __syncwarp();
+          if (lane == 0) mbar_arrive(smem_u32(&M.m_full[slot][quarter]));
+        }
+        const bool moved = now != was && was != -INFINITY;
+        if (now != m) l = m == -INFINITY ? 0.f : l * ex2(m - now);
+        m = now;
+        if (__any_sync(0xFFFFFFFFu, moved)) {
+          if (S::QT == 1) {  // (with a tile of its own, S of this item came behind P.V of the last)
+            ok = wait_all(&M.pv_done[slot ^ 1], (done[slot ^ 1] + ((k - 1) >> 1)) & 1);
+            if (!ok) break;
+            tc_fence_after();
+          }
+          const float fac = moved ? ex2(was - now) : 1.f;
+#pragma unroll 1
+          for (int d = 0; d < DH; d += 16) {
+            const uint32_t t = tmem + S::cO + (S::QT == 2 ? slot * DH : 0) + d + lanes;
+            float o[16];
+            tc::tmem_ld16(t, o);
+            uint32_t x[16];
+#pragma unroll
+            for (int e = 0; e < 16; ++e) x[e] = __float_as_uint(o[e] * fac);
+            tmem_st_rows16(t, x);
           }
         }
-        if (real) {
-          uint4* p = reinterpret_cast<uint4*>(static_cast<uint16_t*>(a.out) + dst * DH + d);
+        const float base = m == -INFINITY ? 0.f : m;
+        float sum[4] = {0.f, 0.f, 0.f, 0.f};
 #pragma unroll
-          for (int e = 0; e < 4; ++e) {
-            uint32_t u[4];
+        for (int h = 0; h < 2; ++h) {
+          uint32_t w[32];
 #pragma unroll
-            for (int q = 0; q < 4; ++q) u[q] = pack_bf16(__uint_as_float(o[8 * e + 2 * q]), __uint_as_float(o[8 * e + 2 * q + 1]));
-            p[e] = make_uint4(u[0], u[1], u[2], u[3]);
+          for (int e = 0; e < 32; ++e) {
+            float x = __uint_as_float(s[64 * h + 2 * e]), y = __uint_as_float(s[64 * h + 2 * e + 1]);
+            fma2(x, y, c, -base);
+            x = ex2(x);
+            y = ex2(y);
+            add2(sum[2 * (e & 1)], sum[2 * (e & 1) + 1], x, y);
+            w[e] = pack_bf16(x, y);
           }
+          tmem_st_rows32(tmem + S::cS + slot * 128 + 32 * h + lanes, w);
+          tc_wait_st();
+          tc_fence_before();
+          __syncwarp();
+          if (lane == 0) mbar_arrive(smem_u32(&M.p_full[slot][h]));
         }
+        l += (sum[0] + sum[1]) + (sum[2] + sum[3]);
       }
+      // ---- O of this query tile
+      int c0 = 0;
+      constexpr int kDims = S::QT == 2 ? DH : DH / 2;
+      if (S::QT == 1) {  // the groups' sums, then half of the dimensions each
+        asm volatile("barrier.cta.sync.aligned 1, 256;" ::: "memory");
+        const float top = M.m[row];
+        l = m == -INFINITY ? l : l * ex2(m - top);
+        M.l[slot][row] = l;
+        asm volatile("barrier.cta.sync.aligned 1, 256;" ::: "memory");
+        l += M.l[slot ^ 1][row];
+        m = top;
+        c0 = slot * kDims;
+      }
+      if (ok) {
+        // (the phase before is over: S of the last item, which this group or the other one has seen, came behind that P.V)
+        const int last = S::QT == 2 ? items - 2 + slot : items - 1;
+        ok = wait_all(&M.pv_done[last & 1], (done[last & 1] + (last >> 1)) & 1);
+        tc_fence_after();
+      }
+      done[0] += (items + 1) / 2;
+      done[1] += items / 2;
+      if (!ok) break;
+      const float r = l != 0.f ? 1.f / l : 0.f;
+      const long long dst = real ? (long long)(u.a0 + pos) * a.n_q + u.grp * G + in_head : -1;
+      if (real && a.lse && c0 == 0) a.lse[dst] = l != 0.f ? (m + log2f(l)) * 0.693147181f : -INFINITY;
+      // rows to dimensions four lanes at a time: a store is eight whole lines
+      float rr[4];
+      long long to[4];  // the lane's rows: lane / 4 + 8 y of the warp's 32
+#pragma unroll
+      for (int y = 0; y < 4; ++y) {
+        rr[y] = __shfl_sync(0xFFFFFFFFu, r, (lane >> 2) + 8 * y);
+        to[y] = __shfl_sync(0xFFFFFFFFu, dst, (lane >> 2) + 8 * y);
+      }
+      const int nan = *reinterpret_cast<volatile int*>(&M.nan[i % kUnits]) == i + 1;
+      auto put = [&](auto slow) {
+#pragma unroll 1
+        for (int d = c0; d < c0 + kDims; d += 64) {
+          uint32_t o[2][2][16];  // 16 rows, 32 dimensions
+#pragma unroll
+          for (int hh = 0; hh < 2; ++hh)
+#pragma unroll
+            for (int q = 0; q < 2; ++q)
+              tmem_ld_frag<4>(tmem + S::cO + (S::QT == 2 ? slot * DH : 0) + d + 32 * q + lanes + ((uint32_t)(16 * hh) << 16), o[hh][q]);
+          tc_wait_ld();
+#pragma unroll
+          for (int hh = 0; hh < 2; ++hh)
+#pragma unroll
+            for (int q = 0; q < 2; ++q)
+#pragma unroll
+              for (int e = 0; e < 16; ++e) pin(o[hh][q][e]);
+          if (d + 64 >= c0 + kDims) {  // O may be written again
+            tc_fence_before();
+            __syncwarp();
+            if (lane == 0) mbar_arrive(smem_u32(&M.o_empty[slot]));
+          }
+#pragma unroll
+          for (int y = 0; y < 4; ++y) {
+            uint32_t w[8];
+#pragma unroll
+            for (int b = 0; b < 8; ++b) {  // dimensions 8 b + 2 (lane % 4), + 1 of the row
+              float x[2];
+#pragma unroll
+              for (int e = 0; e < 2; ++e) {
+                x[e] = __uint_as_float(o[y >> 1][b >> 2][4 * (b & 3) + 2 * (y & 1) + e]);
+                x[e] = rr[y] != 0.f ? x[e] * rr[y] : 0.f;
+                if (decltype(slow)::value) x[e] = add_cleaned(a, u, sp.p0, sp.p1, to[y], d + 8 * b + 2 * (lane & 3) + e, x[e]);
+              }
+              w[b] = pack_bf16(x[0], x[1]);
+            }
+            transpose4(w, lane);
+            // words 2 j, 2 j + 1 are lane j's of blocks 2 (lane % 4), + 1
+            const uint32_t v[8] = {w[0], w[2], w[4], w[6], w[1], w[3], w[5], w[7]};
+            if (to[y] >= 0) st_global32(static_cast<uint16_t*>(a.out) + to[y] * DH + d + 16 * (lane & 3), v);
+          }
+        }
+      };
+      if (nan) put(std::true_type{});
+      else put(std::false_type{});
     }
   }
 
@@ -529,6 +766,8 @@ __global__ void __launch_bounds__(kPromptThreads, 1)
     // let copies still in flight land before the shared memory is released
     for (uint32_t i = 0; i < (uint32_t)S::NS && i < M.copied; ++i)
       mbar_wait(smem_u32(&M.full[(M.copied - 1 - i) % S::NS]), ((M.copied - 1 - i) / S::NS) & 1, kAttnWaitLimit);
+    mbar_wait(smem_u32(&M.q_full), 0, kAttnWaitLimit);
+    mbar_wait(smem_u32(&M.q_full), 1, kAttnWaitLimit);
   }
   __syncthreads();
   if (CL > 1) cluster_sync();  // the other block's copies and arrivals end here too
@@ -536,24 +775,25 @@ __global__ void __launch_bounds__(kPromptThreads, 1)
   if (warp == 0) asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, 512;" ::"r"(tmem) : "memory");
 }
 
-// K or V as (head dimension, head, position), boxes of 64 x 1 x `rows`.
-bool head_map(CUtensorMap* m, const void* p, int dh, int heads, int tokens, long long hs, long long ts, int rows) {
+// Q, K or V as (head dimension, head, position), boxes of 64 x `per` x `rows`.
+bool head_map(CUtensorMap* m, const void* p, int dh, int heads, int tokens, long long hs, long long ts, int per, int rows) {
   auto enc = tc::get_encode();
   if (!enc) return false;
   cuuint64_t dims[3] = {(cuuint64_t)dh, (cuuint64_t)heads, (cuuint64_t)tokens};
   // (the stride of a dimension of one is any that the encoder takes)
   cuuint64_t strides[2] = {(cuuint64_t)(heads > 1 ? hs : dh) * 2, (cuuint64_t)(tokens > 1 ? ts : (long long)dh * heads) * 2};
-  cuuint32_t box[3] = {64, 1, (cuuint32_t)rows}, one[3] = {1, 1, 1};
+  cuuint32_t box[3] = {64, (cuuint32_t)per, (cuuint32_t)rows}, one[3] = {1, 1, 1};
   return enc(m, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 3, const_cast<void*>(p), dims, strides, box, one, CU_TENSOR_MAP_INTERLEAVE_NONE,
              CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
 template <int DH>
-cudaError_t launch(const PromptArgs& a, cudaStream_t s) {
+cudaError_t launch(PromptArgs a, cudaStream_t s) {
   using S = PromptShape<DH>;
-  CUtensorMap mk, mv;
-  if (!head_map(&mk, a.k, DH, a.n_kv, a.tokens, a.hs[1], a.ts[1], 128) ||
-      !head_map(&mv, a.v, DH, a.n_kv, a.tokens, a.hs[2], a.ts[2], DH == 256 ? 64 : 128))
+  CUtensorMap mq, mk, mv;
+  if (!head_map(&mq, a.q, DH, a.n_q, a.tokens, a.hs[0], a.ts[0], a.group, 128 / a.group) ||
+      !head_map(&mk, a.k, DH, a.n_kv, a.tokens, a.hs[1], a.ts[1], 1, 128) ||
+      !head_map(&mv, a.v, DH, a.n_kv, a.tokens, a.hs[2], a.ts[2], 1, DH == 256 ? 64 : 128))
     return cudaErrorInvalidValue;
   static std::mutex mu;
   static bool set[kMaxDevices] = {};
@@ -571,9 +811,9 @@ cudaError_t launch(const PromptArgs& a, cudaStream_t s) {
       set[dev] = true;
     }
   }
-  const int G = a.n_q / a.n_kv;
+  const long long units = prompt_most_tiles(a.tokens, a.rows, 1, 2 * (128 / a.group)) * (a.n_q / a.group);
   cudaLaunchConfig_t cfg = {};
-  cfg.gridDim = dim3((unsigned)(prompt_most_tiles(a.tokens, a.rows, G, kUnit) * a.n_kv * S::CL));
+  cfg.gridDim = dim3((unsigned)std::min<long long>(units, device_sm_count() / S::CL) * S::CL);
   cfg.blockDim = dim3(kPromptThreads);
   cfg.dynamicSmemBytes = S::kSmem;
   cfg.stream = s;
@@ -586,12 +826,15 @@ cudaError_t launch(const PromptArgs& a, cudaStream_t s) {
   cfg.attrs = at;
   cfg.numAttrs = S::CL > 1 ? 2 : 1;
   count_launch();
-  return cudaLaunchKernelEx(&cfg, k_prompt_tc<DH>, a, mk, mv);
+  return cudaLaunchKernelEx(&cfg, k_prompt_tc<DH>, a, mq, mk, mv);
 }
 
 }  // namespace
 
-cudaError_t launch_prompt_tc(const PromptArgs& a, int head_dim, cudaStream_t s) {
+cudaError_t launch_prompt_tc(PromptArgs a, int head_dim, cudaStream_t s) {
+  // heads to a query tile: all that share a KV head, or their largest divisor that fits
+  const int G = a.n_q / a.n_kv;
+  for (a.group = std::min(G, 128); G % a.group != 0;) --a.group;
   return head_dim == 64 ? launch<64>(a, s) : (head_dim == 128 ? launch<128>(a, s) : launch<256>(a, s));
 }
 
