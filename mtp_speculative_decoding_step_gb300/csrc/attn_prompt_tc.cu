@@ -166,13 +166,13 @@ struct PromptShape {
   static constexpr int CL = DH == 256 ? 2 : 1;    // blocks of a unit
   static constexpr int CPT = DH == 256 ? 2 : 1;   // ring stages of a tile of K or V
   static constexpr int NS = DH == 64 ? 8 : 5;     // ring stages
+  static constexpr int kHalves = DH == 64 ? 1 : 2;  // P is given on in one piece or in two (64 dimensions' products are too short to wait twice)
   static constexpr int kQ = QT * 128 * DH * 2, kStage = 128 * DH * 2 / CPT;
   static constexpr int oRing = kQ, oMeta = oRing + NS * kStage;
   static constexpr int kMeta = 3072, kSmem = oMeta + kMeta;
   static constexpr uint32_t cS = 0, cO = 256;     // columns of tensor memory: S at 0 and 128, O from 256 on
   static_assert(kSmem <= 227 * 1024, "shared memory");
-  // stages of K of tile j, and of V, in the order of their use: S of the first item(s), then P.V of item k and S of item k + 2
-  __device__ static int k_at(int j) { return (DH == 256 ? j + max(0, j - 1) : 2 * j) * CPT; }
+  // a unit's stage of V of tile j, in the order of use: S of the first item(s), then P.V of item k and S of item k + 2
   __device__ static int v_at(int j, int nt) { return (DH == 256 ? min(j + 2, nt) + j : 2 * j + 1) * CPT; }
 };
 
@@ -281,7 +281,7 @@ __global__ void __launch_bounds__(kPromptThreads, 1)
   const int G = a.group, rank = CL == 1 ? 0 : (int)(blockIdx.x & 1);
   const int PT = 128 / G;  // positions of a query tile
   volatile int* fail = &M.fail;
-  auto wait_all = [&](uint64_t* bar, uint32_t parity) { return __all_sync(0xFFFFFFFFu, wait(bar, parity, fail)) != 0; };
+  auto ready = [&](uint64_t* bar, uint32_t parity) { return wait(bar, parity, fail); };
 
   if (threadIdx.x == 0) {
     for (int i = 0; i < 8; ++i) {
@@ -343,7 +343,7 @@ __global__ void __launch_bounds__(kPromptThreads, 1)
   };
   // unit number i of this block; false behind the last
   auto take = [&](int i, Unit& u) {
-    if (!wait_all(&M.unit_full[i % kUnits], i / kUnits & 1)) return false;
+    if (!ready(&M.unit_full[i % kUnits], i / kUnits & 1)) return false;
     u = M.unit[i % kUnits];
     __syncwarp();
     if (lane == 0) mbar_arrive(smem_u32(&M.unit_empty[i % kUnits]));
@@ -380,7 +380,7 @@ __global__ void __launch_bounds__(kPromptThreads, 1)
       // there and back: who has the longest unit of one turn has the shortest of the next
       const int blocks = gridDim.x / CL, b = blockIdx.x / CL;
       if (!find_unit(a, 2 * PT, (long long)i * blocks + (i & 1 ? blocks - 1 - b : b), u)) u.n = 0;
-      if (i >= kUnits && !wait_all(&M.unit_empty[i % kUnits], (i / kUnits - 1) & 1)) return false;
+      if (i >= kUnits && !ready(&M.unit_empty[i % kUnits], (i / kUnits - 1) & 1)) return false;
       if (lane == 0) {
         M.unit[i % kUnits] = u;
         mbar_arrive(smem_u32(&M.unit_full[i % kUnits]));
@@ -428,88 +428,155 @@ __global__ void __launch_bounds__(kPromptThreads, 1)
     __syncwarp();
   } else if (warp == 9) {
     // ---------------------------------------------------------- MMAs
+    // (by one warp in one order: while the tensor core has one item's products, the other's softmax runs; two warps, an
+    // item each, fell into step with each other and took a quarter longer. The waits between the products cost some 80
+    // cycles each, so there are no more of them than the order needs.)
     constexpr uint32_t idS = idesc_bf(128, 128, false), idO = idesc_bf(128, DH, true);
     const uint32_t tm = __shfl_sync(0xFFFFFFFFu, tmem, 0);
     const uint64_t dq = tc::sdesc(sm);
-    int edges = 0, base = 0, items = 0;  // tiles whose V was cleaned; ring stages and items before the unit
-    int done[2] = {0, 0};                // items of each place before the unit
+    struct Ring {
+      int st, ph;
+      __device__ void next() {
+        if (++st == S::NS) {
+          st = 0;
+          ph ^= 1;
+        }
+      }
+    };
+    Ring ring = {0, 0};   // the next stage in the order of use
+    int edges = 0;        // tiles whose V was cleaned
+    int done[2] = {0, 0}; // items of each place so far
     bool ok = true;
     Unit u;
     Span sp = {};
-    auto issue_s = [&](int k) {
-      const int j = S::QT == 2 ? k >> 1 : k, slot = k & 1, at = base + S::k_at(j);
-#pragma unroll 1
-      for (int c = 0; c < S::CPT; ++c) {
-        const int st = (at + c) % S::NS;
-        if (!wait_all(&M.full[st], (at + c) / S::NS & 1)) return false;
-        tc_fence_after();
-        const uint64_t dk = tc::sdesc(sm + S::oRing + st * S::kStage);
-        const uint64_t da = dq + (S::QT == 2 ? slot * (128 * DH * 2 / 16) : 0) + c * (DH / S::CPT / 64) * 1024;
-#pragma unroll
-        for (int e = 0; e < DH / S::CPT / 16; ++e)
-          mma_f16_ss(tm + S::cS + slot * 128, da + (e >> 2) * 1024 + (e & 3) * 2, dk + (e >> 2) * 1024 + (e & 3) * 2, idS, (c | e) > 0 ? 1u : 0u);
-        if (S::QT == 1 || slot == 1) commit_all<CL>(smem_u32(&M.empty[st]));
-      }
-      mma_commit_elect(smem_u32(&M.s_full[slot]));
-      if (k == items - 1) mma_commit_elect(smem_u32(&M.q_empty));
-      return true;
+    auto full = [&](const Ring& r) {
+      ok = ready(&M.full[r.st], r.ph);
+      tc_fence_after();
+      return ok;
     };
-    auto issue_pv = [&](int i, int k) {
-      const int j = S::QT == 2 ? k >> 1 : k, slot = k & 1, at = base + S::v_at(j, sp.nt), t0 = (sp.t_first + j) * 128;
-      const bool first = S::QT == 1 || slot == 0, clean = first && edge(t0, sp.p0, sp.p1);
-      if (first) {
-#pragma unroll 1
-        for (int c = 0; c < S::CPT; ++c)
-          if (!wait_all(&M.full[(at + c) % S::NS], (at + c) / S::NS & 1)) return false;
-        if (clean && lane == 0) mbar_arrive(smem_u32(&M.v_go));
-        __syncwarp();
-      }
-      if (i > 0 && k < S::QT) {  // O of the unit before has been read
-        if (!wait_all(&M.o_empty[slot], (i - 1) & 1)) return false;
-        if (S::QT == 1 && !wait_all(&M.o_empty[1], (i - 1) & 1)) return false;
-      }
-      int lo, hi;
-      steps(sp, t0, lo, hi);
-      uint32_t acc = k >= S::QT ? 1u : 0u;
-      const uint32_t d = tm + S::cO + (S::QT == 2 ? slot * DH : 0), p = tm + S::cS + slot * 128;
-#pragma unroll 1
-      for (int c = 0; c < 2; ++c) {  // 64 keys
-        if (!wait_all(&M.p_full[slot][c], (done[slot] + (k >> 1)) & 1)) return false;
-        if (clean && c == 0 && !wait_all(&M.v_ok, edges++ & 1)) return false;
-        tc_fence_after();
-        const int st = (at + (S::CPT == 2 ? c : 0)) % S::NS;
-        const uint64_t dv = sdesc_mn(sm + S::oRing + st * S::kStage, 16384 / S::CPT) + (S::CPT == 2 ? 0 : c * 512);
-        if (lo <= 4 * c && hi >= 4 * c + 4) {
+    // S in place `slot` of query tile q and one stage of K, the tile's c-th
+    auto products_s = [&](int slot, int q, int c, int st) {
+      const uint64_t dk = tc::sdesc(sm + S::oRing + st * S::kStage);
+      const uint64_t da = dq + q * (128 * DH * 2 / 16) + c * (DH / S::CPT / 64) * 1024;
 #pragma unroll
-          for (int e = 0; e < 4; ++e) mma_f16_ts(d, p + c * 32 + e * 8, dv + e * 128, idO, e > 0 ? 1u : acc);
-          acc = 1u;
-        } else {
+      for (int e = 0; e < DH / S::CPT / 16; ++e)
+        mma_f16_ss(tm + S::cS + slot * 128, da + (e >> 2) * 1024 + (e & 3) * 2, dk + (e >> 2) * 1024 + (e & 3) * 2, idS, (c | e) > 0 ? 1u : 0u);
+    };
+    // P.V of the c-th 64 keys; st: their stage; [lo, hi): the tile's steps of 16 keys that count
+    auto products_o = [&](int slot, int c, int st, int lo, int hi, uint32_t& acc) {
+      const uint32_t d = tm + S::cO + (S::QT == 2 ? slot * DH : 0), p = tm + S::cS + slot * 128 + c * 32;
+      const uint64_t dv = sdesc_mn(sm + S::oRing + st * S::kStage, 16384 / S::CPT) + (S::CPT == 2 ? 0 : c * 512);
+      if (lo <= 4 * c && hi >= 4 * c + 4) {
+#pragma unroll
+        for (int e = 0; e < 4; ++e) mma_f16_ts(d, p + e * 8, dv + e * 128, idO, e > 0 ? 1u : acc);
+        acc = 1u;
+      } else {
 #pragma unroll 1
-          for (int e = max(0, lo - 4 * c); e < min(4, hi - 4 * c); ++e) {
-            mma_f16_ts(d, p + c * 32 + e * 8, dv + e * 128, idO, acc);
-            acc = 1u;
-          }
+        for (int e = max(0, lo - 4 * c); e < min(4, hi - 4 * c); ++e) {
+          mma_f16_ts(d, p + e * 8, dv + e * 128, idO, acc);
+          acc = 1u;
         }
-        if ((S::QT == 1 || slot == 1) && (S::CPT == 2 || c == 1)) commit_all<CL>(smem_u32(&M.empty[st]));
       }
-      mma_commit_elect(smem_u32(&M.pv_done[slot]));
-      return true;
+    };
+    auto weights = [&](int slot, int c) {
+      if (c == 0 && S::kHalves == 1) return true;
+      ok = ready(&M.p_full[slot][S::kHalves == 1 ? 0 : c], done[slot] & 1);
+      tc_fence_after();
+      return ok;
     };
 #pragma unroll 1
     for (int i = 0; ok && take(i, u); ++i) {
       sp = span(u);
-      items = sp.nt * S::QT;
-      ok = wait_all(&M.q_full, i & 1);
-      tc_fence_after();
-      ok = ok && issue_s(0) && (items < 2 || issue_s(1));
+      ok = ready(&M.q_full, i & 1);
+      if (!ok) break;
+      // one query tile: K of the first two tiles comes before V
+      const int lead = S::QT == 2 ? 1 : min(2, sp.nt);
 #pragma unroll 1
-      for (int k = 0; k < items && ok; ++k) {
-        ok = issue_pv(i, k);
-        if (ok && k + 2 < items) ok = issue_s(k + 2);
+      for (int j = 0; j < lead && ok; ++j) {
+#pragma unroll 1
+        for (int c = 0; c < S::CPT && full(ring); ++c) {
+          products_s(j, 0, c, ring.st);
+          if (S::QT == 2) {
+            mma_commit_elect(smem_u32(&M.s_full[0]));
+            products_s(1, 1, c, ring.st);
+          }
+          commit_all<CL>(smem_u32(&M.empty[ring.st]));
+          ring.next();
+        }
+        mma_commit_elect(smem_u32(&M.s_full[S::QT == 2 ? 1 : j]));
       }
-      base += 2 * sp.nt * S::CPT;
-      done[0] += (items + 1) / 2;
-      done[1] += items / 2;
+      if (ok && lead == sp.nt) mma_commit_elect(smem_u32(&M.q_empty));
+#pragma unroll 1
+      for (int j = 0; j < sp.nt && ok; ++j) {
+        const int t0 = (sp.t_first + j) * 128;
+        const bool clean = edge(t0, sp.p0, sp.p1);
+        int lo = 0, hi = 8;
+        const Ring v = ring;
+        if (!full(ring)) break;
+        ring.next();
+        if (clean) {  // (all of V, then the cleaners)
+          steps(sp, t0, lo, hi);
+          if (S::CPT == 2 && !full(ring)) break;
+          if (lane == 0) mbar_arrive(smem_u32(&M.v_go));
+          __syncwarp();
+        }
+        if (S::CPT == 2) ring.next();
+        const bool more = j + lead < sp.nt;  // (a tile of K left for S)
+        if constexpr (S::QT == 2) {
+          const Ring k = ring;
+#pragma unroll
+          for (int slot = 0; slot < 2; ++slot) {
+            if (i > 0 && j == 0 && !(ok = ready(&M.o_empty[slot], (i - 1) & 1))) break;  // O of the unit before has been read
+            uint32_t acc = j > 0 ? 1u : 0u;
+#pragma unroll
+            for (int c = 0; c < 2; ++c) {
+              if (!weights(slot, c)) break;
+              if (S::kHalves == 1 && c == 0) continue;
+              if (clean && slot == 0 && c == (S::kHalves == 1 ? 1 : 0) && !(ok = ready(&M.v_ok, edges++ & 1))) break;
+              if (S::kHalves == 1) products_o(slot, 0, v.st, lo, hi, acc);
+              products_o(slot, c, v.st, lo, hi, acc);
+            }
+            if (!ok) break;
+            ++done[slot];
+            if (slot == 1) commit_all<CL>(smem_u32(&M.empty[v.st]));
+            if (j + 1 == sp.nt) mma_commit_elect(smem_u32(&M.pv_done[slot]));
+            if (more) {
+              if (slot == 0 && !full(k)) break;
+              products_s(slot, slot, 0, k.st);
+              if (slot == 1) commit_all<CL>(smem_u32(&M.empty[k.st]));
+              mma_commit_elect(smem_u32(&M.s_full[slot]));
+            }
+          }
+          if (more) ring.next();
+        } else {
+          const int slot = j & 1;
+          if (i > 0 && j == 0 && !(ok = ready(&M.o_empty[0], (i - 1) & 1) && ready(&M.o_empty[1], (i - 1) & 1))) break;
+          uint32_t acc = j > 0 ? 1u : 0u;
+          Ring r = v;
+#pragma unroll
+          for (int c = 0; c < 2; ++c) {
+            if (!weights(slot, c)) break;
+            if (clean && c == 0 && !(ok = ready(&M.v_ok, edges++ & 1))) break;
+            if (!clean && c == 1 && !full(r)) break;
+            products_o(slot, c, r.st, lo, hi, acc);
+            commit_all<CL>(smem_u32(&M.empty[r.st]));
+            r.next();
+          }
+          if (!ok) break;
+          ++done[slot];
+          mma_commit_elect(smem_u32(&M.pv_done[slot]));
+          if (more) {
+#pragma unroll 1
+            for (int c = 0; c < S::CPT && full(ring); ++c) {
+              products_s(slot, 0, c, ring.st);
+              commit_all<CL>(smem_u32(&M.empty[ring.st]));
+              ring.next();
+            }
+            mma_commit_elect(smem_u32(&M.s_full[slot]));
+          }
+        }
+        if (more && j + lead + 1 == sp.nt) mma_commit_elect(smem_u32(&M.q_empty));
+      }
     }
     // what was issued ends before its operands and tensor memory go
     mma_commit_elect(smem_u32(&M.drain));
@@ -530,7 +597,7 @@ __global__ void __launch_bounds__(kPromptThreads, 1)
         const int t0 = (sp.t_first + j) * 128, at = base + S::v_at(j, sp.nt);
         if (!edge(t0, sp.p0, sp.p1)) continue;
         // (told by the MMA warp, which has seen all stages of the ring in turn)
-        if (!(ok = wait_all(&M.v_go, edges++ & 1))) break;
+        if (!(ok = ready(&M.v_go, edges++ & 1))) break;
         int lo, hi;
         steps(sp, t0, lo, hi);
         bool found = false;
@@ -597,7 +664,7 @@ __global__ void __launch_bounds__(kPromptThreads, 1)
 #pragma unroll 1
       for (int k = slot; k < items; k += 2) {
         const int t0 = (sp.t_first + (S::QT == 2 ? k >> 1 : k)) * 128;
-        ok = wait_all(&M.s_full[slot], (done[slot] + (k >> 1)) & 1);
+        ok = ready(&M.s_full[slot], (done[slot] + (k >> 1)) & 1);
         if (!ok) break;
         tc_fence_after();
         uint32_t s[128];
@@ -625,7 +692,7 @@ __global__ void __launch_bounds__(kPromptThreads, 1)
         // the maximum so far; one that moves takes O with it
         float was = m;
         if (S::QT == 1 && k > 0) {
-          ok = wait_all(&M.m_full[slot ^ 1][quarter], (done[slot ^ 1] + ((k - 1) >> 1)) & 1);
+          ok = ready(&M.m_full[slot ^ 1][quarter], (done[slot ^ 1] + ((k - 1) >> 1)) & 1);
           if (!ok) break;
           was = M.m[row];
         }
@@ -640,7 +707,7 @@ __global__ void __launch_bounds__(kPromptThreads, 1)
         m = now;
         if (__any_sync(0xFFFFFFFFu, moved)) {
           if (S::QT == 1) {  // (with a tile of its own, S of this item came behind P.V of the last)
-            ok = wait_all(&M.pv_done[slot ^ 1], (done[slot ^ 1] + ((k - 1) >> 1)) & 1);
+            ok = ready(&M.pv_done[slot ^ 1], (done[slot ^ 1] + ((k - 1) >> 1)) & 1);
             if (!ok) break;
             tc_fence_after();
           }
@@ -671,10 +738,11 @@ __global__ void __launch_bounds__(kPromptThreads, 1)
             w[e] = pack_bf16(x, y);
           }
           tmem_st_rows32(tmem + S::cS + slot * 128 + 32 * h + lanes, w);
+          if (h == 0 && S::kHalves == 1) continue;
           tc_wait_st();
           tc_fence_before();
           __syncwarp();
-          if (lane == 0) mbar_arrive(smem_u32(&M.p_full[slot][h]));
+          if (lane == 0) mbar_arrive(smem_u32(&M.p_full[slot][S::kHalves == 1 ? 0 : h]));
         }
         l += (sum[0] + sum[1]) + (sum[2] + sum[3]);
       }
@@ -693,8 +761,8 @@ __global__ void __launch_bounds__(kPromptThreads, 1)
       }
       if (ok) {
         // (the phase before is over: S of the last item, which this group or the other one has seen, came behind that P.V)
-        const int last = S::QT == 2 ? items - 2 + slot : items - 1;
-        ok = wait_all(&M.pv_done[last & 1], (done[last & 1] + (last >> 1)) & 1);
+        const int last = items - 1;
+        ok = S::QT == 2 ? ready(&M.pv_done[slot], i & 1) : ready(&M.pv_done[last & 1], (done[last & 1] + (last >> 1)) & 1);
         tc_fence_after();
       }
       done[0] += (items + 1) / 2;
