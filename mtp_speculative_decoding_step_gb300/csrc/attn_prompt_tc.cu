@@ -48,13 +48,6 @@ __device__ __forceinline__ void tmem_ld_rows32(uint32_t t, uint32_t* r) {
       : "r"(t));
 }
 
-__device__ __forceinline__ void tmem_st_rows32(uint32_t t, const uint32_t* r) {
-  asm volatile(
-      "tcgen05.st.sync.aligned.32x32b.x32.b32 [%32], {%0, %1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, %15, %16, %17, %18, %19, %20, %21, %22, %23, %24, %25, %26, %27, %28, %29, %30, %31};" ::"r"(r[0]), "r"(r[1]), "r"(r[2]), "r"(r[3]), "r"(r[4]), "r"(r[5]), "r"(r[6]), "r"(r[7]), "r"(r[8]), "r"(r[9]), "r"(r[10]), "r"(r[11]), "r"(r[12]), "r"(r[13]), "r"(r[14]), "r"(r[15]), "r"(r[16]), "r"(r[17]), "r"(r[18]), "r"(r[19]), "r"(r[20]), "r"(r[21]), "r"(r[22]), "r"(r[23]), "r"(r[24]), "r"(r[25]), "r"(r[26]), "r"(r[27]), "r"(r[28]), "r"(r[29]), "r"(r[30]), "r"(r[31]),
-      "r"(t)
-      : "memory");
-}
-
 __device__ __forceinline__ float max3(float a, float b, float c) {
   float d;
   asm("max.f32 %0, %1, %2, %3;" : "=f"(d) : "f"(a), "f"(b), "f"(c));
@@ -80,26 +73,6 @@ __device__ __forceinline__ void add2(float& x, float& y, float u, float v) {
       "mov.b64 {%0, %1}, s;\n\t}"
       : "+f"(x), "+f"(y)
       : "f"(u), "f"(v));
-}
-
-// Eight words a lane that belong to one of four columns of two each: lane q of four neighbouring ones gets column q of
-// all four (its words 2 j, 2 j + 1: lane j's).
-__device__ __forceinline__ void transpose4(uint32_t (&w)[8], int lane) {
-#pragma unroll
-  for (int bit = 1; bit < 4; bit <<= 1) {
-    const bool up = lane & bit;
-#pragma unroll
-    for (int c = 0; c < 4; ++c) {
-      if (c & bit) continue;
-#pragma unroll
-      for (int e = 0; e < 2; ++e) {
-        uint32_t &x = w[2 * c + e], &y = w[2 * (c | bit) + e];
-        const uint32_t got = __shfl_xor_sync(0xFFFFFFFFu, up ? x : y, bit);
-        if (up) x = got;
-        else y = got;
-      }
-    }
-  }
 }
 
 // 32 bytes, one sector.
@@ -251,6 +224,26 @@ struct PromptMeta {
   float l[2][128];     // the groups' sums
 };
 static_assert(sizeof(PromptMeta) <= 3072, "meta");
+
+// Eight words a lane that belong to one of four columns of two each: lane q of four neighbouring ones gets column q of
+// all four (its words 2 j, 2 j + 1: lane j's).
+__device__ __forceinline__ void transpose4(uint32_t (&w)[8], int lane) {
+#pragma unroll
+  for (int bit = 1; bit < 4; bit <<= 1) {
+    const bool up = lane & bit;
+#pragma unroll
+    for (int c = 0; c < 4; ++c) {
+      if (c & bit) continue;
+#pragma unroll
+      for (int e = 0; e < 2; ++e) {
+        uint32_t &x = w[2 * c + e], &y = w[2 * (c | bit) + e];
+        const uint32_t got = __shfl_xor_sync(0xFFFFFFFFu, up ? x : y, bit);
+        if (up) x = got;
+        else y = got;
+      }
+    }
+  }
+}
 
 // x with what was cleaned out of V in dimension d and the query of row `dst` of the output sees. (Rare and slow.)
 __device__ __noinline__ float add_cleaned(const PromptArgs& a, const Unit& u, int p0, int p1, long long dst, int d, float x) {
@@ -428,12 +421,23 @@ __global__ void __launch_bounds__(kPromptThreads, 1)
     __syncwarp();
   } else if (warp == 9) {
     // ---------------------------------------------------------- MMAs
-    // (by one warp in one order: while the tensor core has one item's products, the other's softmax runs; two warps, an
-    // item each, fell into step with each other and took a quarter longer. The waits between the products cost some 80
-    // cycles each, so there are no more of them than the order needs.)
+    // By one warp in one order: while the tensor core has one item's products, the other's softmax runs. (Two warps, an
+    // item each, fell into step with each other and took a quarter longer.) The waits between the products cost some 80
+    // cycles each, so there are no more of them than the order needs, and no branch depends on how one ended: what the
+    // compiler can see to be the same for the warp stays in uniform registers, where the MMAs take their operands from. A wait
+    // that ran out ends the role at the next unit.
     constexpr uint32_t idS = idesc_bf(128, 128, false), idO = idesc_bf(128, DH, true);
     const uint32_t tm = __shfl_sync(0xFFFFFFFFu, tmem, 0);
     const uint64_t dq = tc::sdesc(sm);
+    auto await = [&](uint64_t* bar, uint32_t parity) {
+      const uint32_t b = smem_u32(bar);
+#pragma unroll 1
+      for (unsigned i = 0; !mbar_try(b, parity); ++i) {
+        if (i == kAttnWaitLimit) *fail = 1;
+        if (i == kAttnWaitLimit || ((i & 63) == 63 && *fail)) break;
+      }
+      __syncwarp();
+    };
     struct Ring {
       int st, ph;
       __device__ void next() {
@@ -446,13 +450,9 @@ __global__ void __launch_bounds__(kPromptThreads, 1)
     Ring ring = {0, 0};   // the next stage in the order of use
     int edges = 0;        // tiles whose V was cleaned
     int done[2] = {0, 0}; // items of each place so far
-    bool ok = true;
-    Unit u;
-    Span sp = {};
     auto full = [&](const Ring& r) {
-      ok = ready(&M.full[r.st], r.ph);
+      await(&M.full[r.st], r.ph);
       tc_fence_after();
-      return ok;
     };
     // S in place `slot` of query tile q and one stage of K, the tile's c-th
     auto products_s = [&](int slot, int q, int c, int st) {
@@ -479,22 +479,25 @@ __global__ void __launch_bounds__(kPromptThreads, 1)
       }
     };
     auto weights = [&](int slot, int c) {
-      if (c == 0 && S::kHalves == 1) return true;
-      ok = ready(&M.p_full[slot][S::kHalves == 1 ? 0 : c], done[slot] & 1);
+      await(&M.p_full[slot][c], done[slot] & 1);
       tc_fence_after();
-      return ok;
     };
 #pragma unroll 1
-    for (int i = 0; ok && take(i, u); ++i) {
-      sp = span(u);
-      ok = ready(&M.q_full, i & 1);
-      if (!ok) break;
+    for (int i = 0;; ++i) {
+      Unit u;
+      const bool some = take(i, u) && !*fail;
+      if (__shfl_sync(0xFFFFFFFFu, (int)some, 0) == 0) break;
+      u.n = __shfl_sync(0xFFFFFFFFu, u.n, 0);
+      u.j = __shfl_sync(0xFFFFFFFFu, u.j, 0);
+      const Span sp = span(u);
+      await(&M.q_full, i & 1);
       // one query tile: K of the first two tiles comes before V
       const int lead = S::QT == 2 ? 1 : min(2, sp.nt);
 #pragma unroll 1
-      for (int j = 0; j < lead && ok; ++j) {
+      for (int j = 0; j < lead; ++j) {
 #pragma unroll 1
-        for (int c = 0; c < S::CPT && full(ring); ++c) {
+        for (int c = 0; c < S::CPT; ++c) {
+          full(ring);
           products_s(j, 0, c, ring.st);
           if (S::QT == 2) {
             mma_commit_elect(smem_u32(&M.s_full[0]));
@@ -505,18 +508,18 @@ __global__ void __launch_bounds__(kPromptThreads, 1)
         }
         mma_commit_elect(smem_u32(&M.s_full[S::QT == 2 ? 1 : j]));
       }
-      if (ok && lead == sp.nt) mma_commit_elect(smem_u32(&M.q_empty));
+      if (lead == sp.nt) mma_commit_elect(smem_u32(&M.q_empty));
 #pragma unroll 1
-      for (int j = 0; j < sp.nt && ok; ++j) {
+      for (int j = 0; j < sp.nt; ++j) {
         const int t0 = (sp.t_first + j) * 128;
         const bool clean = edge(t0, sp.p0, sp.p1);
         int lo = 0, hi = 8;
         const Ring v = ring;
-        if (!full(ring)) break;
+        full(ring);
         ring.next();
         if (clean) {  // (all of V, then the cleaners)
           steps(sp, t0, lo, hi);
-          if (S::CPT == 2 && !full(ring)) break;
+          if (S::CPT == 2) full(ring);
           if (lane == 0) mbar_arrive(smem_u32(&M.v_go));
           __syncwarp();
         }
@@ -526,22 +529,19 @@ __global__ void __launch_bounds__(kPromptThreads, 1)
           const Ring k = ring;
 #pragma unroll
           for (int slot = 0; slot < 2; ++slot) {
-            if (i > 0 && j == 0 && !(ok = ready(&M.o_empty[slot], (i - 1) & 1))) break;  // O of the unit before has been read
+            if (i > 0 && j == 0) await(&M.o_empty[slot], (i - 1) & 1);  // O of the unit before has been read
             uint32_t acc = j > 0 ? 1u : 0u;
 #pragma unroll
             for (int c = 0; c < 2; ++c) {
-              if (!weights(slot, c)) break;
-              if (S::kHalves == 1 && c == 0) continue;
-              if (clean && slot == 0 && c == (S::kHalves == 1 ? 1 : 0) && !(ok = ready(&M.v_ok, edges++ & 1))) break;
-              if (S::kHalves == 1) products_o(slot, 0, v.st, lo, hi, acc);
+              if (c < S::kHalves) weights(slot, c);
+              if (clean && slot == 0 && c == 0) await(&M.v_ok, edges++ & 1);
               products_o(slot, c, v.st, lo, hi, acc);
             }
-            if (!ok) break;
             ++done[slot];
             if (slot == 1) commit_all<CL>(smem_u32(&M.empty[v.st]));
             if (j + 1 == sp.nt) mma_commit_elect(smem_u32(&M.pv_done[slot]));
             if (more) {
-              if (slot == 0 && !full(k)) break;
+              if (slot == 0) full(k);
               products_s(slot, slot, 0, k.st);
               if (slot == 1) commit_all<CL>(smem_u32(&M.empty[k.st]));
               mma_commit_elect(smem_u32(&M.s_full[slot]));
@@ -550,24 +550,27 @@ __global__ void __launch_bounds__(kPromptThreads, 1)
           if (more) ring.next();
         } else {
           const int slot = j & 1;
-          if (i > 0 && j == 0 && !(ok = ready(&M.o_empty[0], (i - 1) & 1) && ready(&M.o_empty[1], (i - 1) & 1))) break;
+          if (i > 0 && j == 0) {
+            await(&M.o_empty[0], (i - 1) & 1);
+            await(&M.o_empty[1], (i - 1) & 1);
+          }
           uint32_t acc = j > 0 ? 1u : 0u;
           Ring r = v;
 #pragma unroll
           for (int c = 0; c < 2; ++c) {
-            if (!weights(slot, c)) break;
-            if (clean && c == 0 && !(ok = ready(&M.v_ok, edges++ & 1))) break;
-            if (!clean && c == 1 && !full(r)) break;
+            weights(slot, c);
+            if (clean && c == 0) await(&M.v_ok, edges++ & 1);
+            if (!clean && c == 1) full(r);
             products_o(slot, c, r.st, lo, hi, acc);
             commit_all<CL>(smem_u32(&M.empty[r.st]));
             r.next();
           }
-          if (!ok) break;
           ++done[slot];
           mma_commit_elect(smem_u32(&M.pv_done[slot]));
           if (more) {
 #pragma unroll 1
-            for (int c = 0; c < S::CPT && full(ring); ++c) {
+            for (int c = 0; c < S::CPT; ++c) {
+              full(ring);
               products_s(slot, 0, c, ring.st);
               commit_all<CL>(smem_u32(&M.empty[ring.st]));
               ring.next();
@@ -726,23 +729,26 @@ __global__ void __launch_bounds__(kPromptThreads, 1)
         const float base = m == -INFINITY ? 0.f : m;
         float sum[4] = {0.f, 0.f, 0.f, 0.f};
 #pragma unroll
-        for (int h = 0; h < 2; ++h) {
-          uint32_t w[32];
+        for (int h = 0; h < 4; ++h) {
+          uint32_t w[16];
+          if (h > 0)
 #pragma unroll
-          for (int e = 0; e < 32; ++e) {
-            float x = __uint_as_float(s[64 * h + 2 * e]), y = __uint_as_float(s[64 * h + 2 * e + 1]);
+            for (int e = 32 * h; e < 32 * h + 32; ++e) pin(s[e]);
+#pragma unroll
+          for (int e = 0; e < 16; ++e) {
+            float x = __uint_as_float(s[32 * h + 2 * e]), y = __uint_as_float(s[32 * h + 2 * e + 1]);
             fma2(x, y, c, -base);
             x = ex2(x);
             y = ex2(y);
             add2(sum[2 * (e & 1)], sum[2 * (e & 1) + 1], x, y);
             w[e] = pack_bf16(x, y);
           }
-          tmem_st_rows32(tmem + S::cS + slot * 128 + 32 * h + lanes, w);
-          if (h == 0 && S::kHalves == 1) continue;
+          tmem_st_rows16(tmem + S::cS + slot * 128 + 16 * h + lanes, w);
+          if ((h & 1) == 0 || (h == 1 && S::kHalves == 1)) continue;
           tc_wait_st();
           tc_fence_before();
           __syncwarp();
-          if (lane == 0) mbar_arrive(smem_u32(&M.p_full[slot][S::kHalves == 1 ? 0 : h]));
+          if (lane == 0) mbar_arrive(smem_u32(&M.p_full[slot][S::kHalves == 1 ? 0 : h >> 1]));
         }
         l += (sum[0] + sum[1]) + (sum[2] + sum[3]);
       }
