@@ -14,12 +14,12 @@
 // the first terms of the sine's and cosine's series; the two are joined by the
 // addition theorems. Everything is held in two floats, good to 2^-32.
 //
-// Keys go through the norm and the rotation in two floats each, because what is
-// kept of them is discrete: with results off by 2^-24 one of some 3 million
-// elements falls on the other side of a 4-bit border than the exact one. What
-// is compared with the borders is rounded to odd, so that no value that is not
-// on a border is taken for one that is. Queries, which are only rounded, are
-// fp32.
+// What is kept of a key is discrete: with results off by 2^-22 some of a few million
+// elements fall on the other side of a 4-bit border than the exact ones. So a
+// row of keys that comes so near a border, of a code or of a scale, that fp32 cannot
+// tell the side (one of 30) is taken again in two floats per value, and rounded to
+// odd before it is compared, so that no value that is not on a border is taken for
+// one that is. Queries, which are only rounded, are fp32.
 //
 // Layout. A row of dh elements is dh / 8 lanes' work. A lane holds two runs of
 // four elements, A and B, such that a rotated pair is in one lane: A at 4 l and
@@ -43,7 +43,7 @@ namespace mtp {
 namespace {
 
 constexpr int kRopeThreads = 256;  // of the general kernel
-constexpr int kMostWarps = 12;     // of a block of the other, the one that makes the angles among them
+constexpr int kMostWarps = 10;     // of a block of the other
 constexpr int kBatch = 4;          // rows of queries a group of lanes takes, loaded together
 
 struct RopeArgs {
@@ -233,86 +233,80 @@ __device__ __forceinline__ int slot_of(const RopeArgs& a, int t, int pos, bool t
   return -1;
 }
 
-// 16 elements of 12 bits at most, a group of four lanes, 4 each, at their head's exponent:
-// the codes of a lane's elements, and the block's scale (0x7F, NaN, where one of the
-// elements is not finite: the row shows what it was given). By whole warps.
-__device__ __forceinline__ uint32_t quantize4(const float (&y)[4], int exp, uint32_t& sc) {
+// Codes and scale of 16 elements, a group of four lanes, 4 each, at their head's exponent: `mx` is the largest
+// magnitude's bits (0x7F, NaN, where one of the elements is not finite: the row shows what it was given).
+struct Block4 {
+  float s, rs;  // the scale at the elements' size and its inverse
+  uint32_t sc;
+};
+
+__device__ __forceinline__ uint32_t most4(const float (&y)[4]) {
   uint32_t mx = 0;  // (magnitudes as whole numbers: an infinity or a NaN is the largest)
 #pragma unroll
   for (int e = 0; e < 4; ++e) mx = max(mx, __float_as_uint(y[e]) & 0x7FFFFFFFu);
 #pragma unroll
   for (int o = 1; o < 4; o <<= 1) mx = max(mx, __shfl_xor_sync(0xFFFFFFFFu, mx, o));
-  float s;
-  sc = scale4(fminf(__uint_as_float(mx) * pow2i(-exp), FLT_MAX), s);
-  s *= pow2i(exp);  // the scale at the elements' size: exact
-  float rs, q[4];
-  asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(rs) : "f"(s));
+  return mx;
+}
+
+__device__ __forceinline__ Block4 block4(uint32_t mx, float down, float up) {
+  Block4 b;
+  b.sc = scale4(fminf(__uint_as_float(mx) * down, FLT_MAX), b.s);
+  b.s *= up;  // exact
+  asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(b.rs) : "f"(b.s));
+  if (mx >= 0x7F800000u) b.sc = 0x7F;
+  return b;
+}
+
+// Elements of 12 bits at most. By whole warps.
+__device__ __forceinline__ uint32_t quantize4(const float (&y)[4], float down, float up, uint32_t& sc) {
+  const Block4 b = block4(most4(y), down, up);
+  float q[4];
 #pragma unroll
-  for (int e = 0; e < 4; ++e) q[e] = over(y[e], s, rs);
+  for (int e = 0; e < 4; ++e) q[e] = over(y[e], b.s, b.rs);
   const uint32_t code = codes4(q);
-  if (mx >= 0x7F800000u) sc = 0x7F;
+  sc = b.sc;
   return sc == 0 || sc == 0x7F ? 0u : code;
 }
 
-// Queries of up to kBatch x (32 / kLanes) heads.
-template <int DH, int DT>
-__device__ __forceinline__ void rope_queries(const RopeArgs& a, const float (&A)[kBatch][4], const float (&B)[kBatch][4], float4 wa4,
-                                             float4 wb4, bool norm, const CosSin* cs, bool mine, int t, int pos, int h0, int ea, int eb) {
-  constexpr int kLanes = DH / 8, kGroups = 32 / kLanes;
-  const float wa[4] = {wa4.x, wa4.y, wa4.z, wa4.w}, wb[4] = {wb4.x, wb4.y, wb4.z, wb4.w};
-  // z = r (x w c - x' w' s): the weights go into the factors, once for all heads
-  float fa[4], ga[4], fb[4], gb[4];
+// fp32 elements off by at most err each: `near` where a code's border or the scale's may lie between them and the exact
+// ones. Borders between codes are at 1, 3, 5, 7, 10, 14 and 20 quarters of the scale. By whole warps.
+// `exact`: they are what they are.
+__device__ __forceinline__ uint32_t quantize4_near(const float (&y)[4], const float (&err)[4], float down, float up, bool exact, uint32_t& sc,
+                                                   bool& near) {
+  float off = 0.f;
+#pragma unroll
+  for (int e = 0; e < 4; ++e) off = fmaxf(off, err[e]);
+#pragma unroll
+  for (int o = 1; o < 4; o <<= 1) off = fmaxf(off, __shfl_xor_sync(0xFFFFFFFFu, off, o));
+  const uint32_t mx = most4(y);
+  const Block4 b = block4(mx, down, up);
+  float other;
+  const float top = __uint_as_float(mx);
+  near = scale4(fminf((top + off) * down, FLT_MAX), other) != scale4(fminf(fmaxf(top - off, 0.f) * down, FLT_MAX), other);
+  float q[4];
 #pragma unroll
   for (int e = 0; e < 4; ++e) {
-    const float c = mine ? cs[e].ch : 1.f, s = mine ? cs[e].sh : 0.f;
-    fa[e] = wa[e] * c;
-    ga[e] = wb[e] * s;
-    fb[e] = wb[e] * c;
-    gb[e] = wa[e] * s;
+    q[e] = y[e] * b.rs;
+    const float t = fabsf(q[e]) * 4.f, whole = rintf(t);
+    // (the quotient itself is off by 2^-22 of at most 24 quarters; what is not finite has no side)
+    near |= fabsf(t - whole) <= fmaf(err[e] * b.rs, 4.f, 0x1p-17f) && t < 24.f && !exact;
+    if (exact) q[e] = over(to_odd({y[e], 0.f}), b.s, b.rs);
   }
-  const long long at = ((long long)t * a.n_q + h0) * DH;
-#pragma unroll
-  for (int u = 0; u < kBatch; ++u) {
-    const bool head = h0 + u * kGroups < a.n_q;
-    float r = 1.f;
-    if (norm) {
-      float sum = 0.f;
-#pragma unroll
-      for (int e = 0; e < 4; ++e) sum = fmaf(A[u][e], A[u][e], fmaf(B[u][e], B[u][e], sum));
-#pragma unroll
-      for (int o = 1; o < kLanes; o <<= 1) sum += __shfl_xor_sync(0xFFFFFFFFu, sum, o);
-      r = rsqrtf(fmaf(sum, 1.f / DH, a.eps));
-    }
-    float ya[4], yb[4];
-#pragma unroll
-    for (int e = 0; e < 4; ++e) {
-      // (what is not turned takes nothing from the other run, whose infinity times 0 would show)
-      const float x = mine ? A[u][e] * gb[e] : 0.f, y = mine ? B[u][e] * ga[e] : 0.f;
-      ya[e] = r * fmaf(A[u][e], fa[e], -y);
-      yb[e] = r * fmaf(B[u][e], fb[e], x);
-    }
-    if (pos < 0) {
-#pragma unroll
-      for (int e = 0; e < 4; ++e) ya[e] = yb[e] = 0.f;
-    }
-    if (head) {
-      store4<DT>(a.q_out, at + u * kGroups * DH + ea, ya);
-      store4<DT>(a.q_out, at + u * kGroups * DH + eb, yb);
-    }
-  }
+  const uint32_t code = codes4(q);
+  sc = b.sc;
+  near = near && sc != 0x7F;
+  return sc == 0 || sc == 0x7F ? 0u : code;
 }
 
-// Keys, in two floats, and values of 32 / kLanes heads.
-template <int DH, int DT>
-__device__ __forceinline__ void rope_keys(const RopeArgs& a, float (&A)[4], float (&B)[4], float (&VA)[4], float (&VB)[4], float4 wa4,
-                                          float4 wb4, bool norm, const CosSin* cs, bool mine, int t, int pos, int h0, int ea, int eb,
-                                          bool tell) {
-  constexpr int kLanes = DH / 8, kRow = q4_row_bytes(DH);
-  const float wa[4] = {wa4.x, wa4.y, wa4.z, wa4.w}, wb[4] = {wb4.x, wb4.y, wb4.z, wb4.w};
-  const bool head = h0 < a.n_kv;
-  const int slot = slot_of(a, t, pos, tell);
+// A warp's keys in two floats: A and B of row `u` as they came, at the factors' place `cs`; codes of both runs (low and high
+// half) and scales (a byte each). Out of line: few rows come here, and the others need the registers.
+template <int DH>
+__device__ __noinline__ uint2 exact_keys(float4 A4, float4 B4, const float* w, int ea, int eb, float eps, const CosSin* cs, bool mine, int exp) {
+  constexpr int kLanes = DH / 8;
+  const float A[4] = {A4.x, A4.y, A4.z, A4.w}, B[4] = {B4.x, B4.y, B4.z, B4.w};
   Two ka[4], kb[4];
-  if (norm) {
+  if (w) {
     Two sum = {0.f, 0.f};
 #pragma unroll
     for (int e = 0; e < 8; ++e) {
@@ -326,11 +320,11 @@ __device__ __forceinline__ void rope_keys(const RopeArgs& a, float (&A)[4], floa
       const Two n = two_sum(sum.hi, hi);
       sum = {n.hi, n.lo + (sum.lo + lo)};
     }
-    const Two r = root(sum, 1.f / DH, a.eps);
+    const Two r = root(sum, 1.f / DH, eps);
 #pragma unroll
     for (int e = 0; e < 4; ++e) {
-      ka[e] = scaled(A[e], r, wa[e]);
-      kb[e] = scaled(B[e], r, wb[e]);
+      ka[e] = scaled(A[e], r, w[ea + e]);
+      kb[e] = scaled(B[e], r, w[eb + e]);
     }
   } else {
 #pragma unroll
@@ -348,54 +342,243 @@ __device__ __forceinline__ void rope_keys(const RopeArgs& a, float (&A)[4], floa
       kb[e] = turn_one(y, x, c.ch, c.cl, -c.sh, -c.sl);
     }
   }
-  if (a.k_out && head) {
-    float ya[4], yb[4];
+  __syncwarp();
+  float ya[4], yb[4];
+#pragma unroll
+  for (int e = 0; e < 4; ++e) {
+    ya[e] = to_odd(ka[e]);
+    yb[e] = to_odd(kb[e]);
+  }
+  uint32_t sa, sb;
+  const uint32_t ca = quantize4(ya, pow2i(-exp), pow2i(exp), sa), cb = quantize4(yb, pow2i(-exp), pow2i(exp), sb);
+  return make_uint2(ca | cb << 16, sa | sb << 8);
+}
+
+// Codes of two runs and their scales to the cache row at byte `to`.
+template <int DH>
+__device__ __forceinline__ void store_codes(const RopeArgs& a, int side, long long to, int ea, int eb, uint32_t ca, uint32_t cb, uint32_t sa, uint32_t sb) {
+  uint8_t* row = a.cache[side] + to;
+  *reinterpret_cast<uint16_t*>(row + ea / 2) = (uint16_t)ca;
+  *reinterpret_cast<uint16_t*>(row + eb / 2) = (uint16_t)cb;
+  if ((ea & 15) == 0) row[DH / 2 + ea / 16] = (uint8_t)sa;
+  if ((eb & 15) == 0) row[DH / 2 + eb / 16] = (uint8_t)sb;
+  if (sa == 0x7F || sb == 0x7F) flag_status(a.status, MTP_ERR_NONFINITE);
+}
+
+// Two fp32 values for one instruction.
+struct Pair {
+  unsigned long long v;
+};
+__device__ __forceinline__ Pair pair(float x, float y) {
+  Pair p;
+  asm("mov.b64 %0, {%1, %2};" : "=l"(p.v) : "f"(x), "f"(y));
+  return p;
+}
+__device__ __forceinline__ float2 both(Pair p) {
+  float2 f;
+  asm("mov.b64 {%0, %1}, %2;" : "=f"(f.x), "=f"(f.y) : "l"(p.v));
+  return f;
+}
+__device__ __forceinline__ Pair mul2(Pair a, Pair b) {
+  Pair p;
+  asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(p.v) : "l"(a.v), "l"(b.v));
+  return p;
+}
+__device__ __forceinline__ Pair fma2(Pair a, Pair b, Pair c) {
+  Pair p;
+  asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(p.v) : "l"(a.v), "l"(b.v), "l"(c.v));
+  return p;
+}
+
+// Sums of four rows over kLanes lanes: a lane gets that of row 2 (lane & 1) + (lane >> 1 & 1).
+template <int kLanes>
+__device__ __forceinline__ float sum_rows(const float (&s)[4], int lane) {
+  const bool b0 = lane & 1, b1 = lane & 2;
+  float u = b0 ? s[2] : s[0], v = b0 ? s[3] : s[1];
+  u += __shfl_xor_sync(0xFFFFFFFFu, b0 ? s[0] : s[2], 1);
+  v += __shfl_xor_sync(0xFFFFFFFFu, b0 ? s[1] : s[3], 1);
+  float w = b1 ? v : u;
+  w += __shfl_xor_sync(0xFFFFFFFFu, b1 ? u : v, 2);
+#pragma unroll
+  for (int o = 4; o < kLanes; o <<= 1) w += __shfl_xor_sync(0xFFFFFFFFu, w, o);
+  return w;
+}
+
+// A row's two runs as pairs.
+template <int DT>
+__device__ __forceinline__ void runs(const Raw4<DT>& x, const Raw4<DT>& y, Pair (&A)[2], Pair (&B)[2]) {
+  float u[4], v[4];
+  widen4<DT>(x, u);
+  widen4<DT>(y, v);
+  A[0] = pair(u[0], u[1]), A[1] = pair(u[2], u[3]);
+  B[0] = pair(v[0], v[1]), B[1] = pair(v[2], v[3]);
+}
+
+__device__ __forceinline__ float square(const Pair (&A)[2], const Pair (&B)[2]) {
+  const float2 s = both(fma2(A[0], A[0], fma2(A[1], A[1], fma2(B[0], B[0], mul2(B[1], B[1])))));
+  return s.x + s.y;
+}
+
+// z = r (x w c - x' w' s): the weights go into the factors, once for all heads of an item.
+struct Factors {
+  Pair fa[2], fb[2], ga[2], gb[2];
+  __device__ __forceinline__ Factors(float4 wa, float4 wb, const CosSin* cs, bool mine) {
+    const float va[4] = {wa.x, wa.y, wa.z, wa.w}, vb[4] = {wb.x, wb.y, wb.z, wb.w};
+    float c[4], s[4];
 #pragma unroll
     for (int e = 0; e < 4; ++e) {
-      ya[e] = pos < 0 ? 0.f : nearest(ka[e]);
-      yb[e] = pos < 0 ? 0.f : nearest(kb[e]);
+      c[e] = mine ? cs[e].ch : 1.f;
+      s[e] = mine ? cs[e].sh : 0.f;
+    }
+#pragma unroll
+    for (int e = 0; e < 2; ++e) {
+      fa[e] = pair(va[2 * e] * c[2 * e], va[2 * e + 1] * c[2 * e + 1]);
+      fb[e] = pair(vb[2 * e] * c[2 * e], vb[2 * e + 1] * c[2 * e + 1]);
+      ga[e] = pair(-vb[2 * e] * s[2 * e], -vb[2 * e + 1] * s[2 * e + 1]);
+      gb[e] = pair(va[2 * e] * s[2 * e], va[2 * e + 1] * s[2 * e + 1]);
+    }
+  }
+  // what run x brings to the other one (nothing where nothing is turned: an infinity times 0 would show)
+  __device__ __forceinline__ static void cross(const Pair (&x)[2], const Pair (&g)[2], bool mine, Pair (&y)[2]) {
+#pragma unroll
+    for (int e = 0; e < 2; ++e) {
+      y[e] = mul2(x[e], g[e]);
+      y[e].v = mine ? y[e].v : 0ull;
+    }
+  }
+  __device__ __forceinline__ static void turn(const Pair (&x)[2], const Pair (&f)[2], const Pair (&y)[2], float r, float (&z)[4]) {
+    const Pair r2 = pair(r, r);
+    const float2 u = both(mul2(fma2(x[0], f[0], y[0]), r2)), v = both(mul2(fma2(x[1], f[1], y[1]), r2));
+    z[0] = u.x, z[1] = u.y, z[2] = v.x, z[3] = v.y;
+  }
+};
+
+// Queries of up to kBatch x (32 / kLanes) heads.
+template <int DH, int DT>
+__device__ __forceinline__ void rope_queries(const RopeArgs& a, const Raw4<DT> (&ra)[kBatch], const Raw4<DT> (&rb)[kBatch], const Factors& F, bool norm,
+                                             bool mine, int t, int pos, int h0, int ea, int eb, int lane) {
+  constexpr int kLanes = DH / 8, kGroups = 32 / kLanes;
+  const long long at = ((long long)t * a.n_q + h0) * DH;
+  if (pos < 0) {  // padding
+    const float none[4] = {0.f, 0.f, 0.f, 0.f};
+    for (int u = 0; u < kBatch && h0 + u * kGroups < a.n_q; ++u) {
+      store4<DT>(a.q_out, at + u * kGroups * DH + ea, none);
+      store4<DT>(a.q_out, at + u * kGroups * DH + eb, none);
+    }
+    return;
+  }
+  Pair A[kBatch][2], B[kBatch][2];
+  float sq[kBatch], r = 1.f;
+#pragma unroll
+  for (int u = 0; u < kBatch; ++u) {
+    runs<DT>(ra[u], rb[u], A[u], B[u]);
+    sq[u] = square(A[u], B[u]);
+  }
+  if (norm) r = rsqrtf(fmaf(sum_rows<kLanes>(sq, lane), 1.f / DH, a.eps));
+#pragma unroll
+  for (int u = 0; u < kBatch; ++u) {
+    const float ru = norm ? __shfl_sync(0xFFFFFFFFu, r, (lane & ~3) | (u >> 1) | ((u & 1) << 1)) : 1.f;
+    Pair x[2], y[2];
+    float ya[4], yb[4];
+    Factors::cross(B[u], F.ga, mine, x);
+    Factors::cross(A[u], F.gb, mine, y);
+    Factors::turn(A[u], F.fa, x, ru, ya);
+    Factors::turn(B[u], F.fb, y, ru, yb);
+    if (h0 + u * kGroups < a.n_q) {
+      store4<DT>(a.q_out, at + u * kGroups * DH + ea, ya);
+      store4<DT>(a.q_out, at + u * kGroups * DH + eb, yb);
+    }
+  }
+}
+
+// Keys and values of 32 / kLanes heads.
+template <int DH, int DT>
+__device__ __forceinline__ void rope_keys(const RopeArgs& a, const Raw4<DT> (&ra)[kBatch], const Raw4<DT> (&rb)[kBatch], const Factors& F, const float* w,
+                                          const CosSin* cs, bool mine, int t, int pos, int h0, int ea, int eb, bool tell) {
+  constexpr int kLanes = DH / 8;
+  const bool head = h0 < a.n_kv;
+  const int slot = slot_of(a, t, pos, tell);
+  Pair A[2], B[2], x[2], y[2];
+  runs<DT>(ra[0], rb[0], A, B);
+  float r = 1.f;
+  if (w) {
+    float sum = square(A, B);
+#pragma unroll
+    for (int o = 1; o < kLanes; o <<= 1) sum += __shfl_xor_sync(0xFFFFFFFFu, sum, o);
+    r = rsqrtf(fmaf(sum, 1.f / DH, a.eps));
+  }
+  float ya[4], yb[4];
+  Factors::cross(B, F.ga, mine, x);
+  Factors::cross(A, F.gb, mine, y);
+  Factors::turn(A, F.fa, x, r, ya);
+  Factors::turn(B, F.fb, y, r, yb);
+  if (slot >= 0) {  // (the same for the warp)
+    // off by 2^-19 of (|x w c| + |x' w' s|) r at most: the sum's 13 roundings, half of which reach its root, the root's two
+    // steps, and a step or two each of the factors, products and their sum
+    const float step = r * 0x1p-19f;
+    float da[4], db[4];
+#pragma unroll
+    for (int e = 0; e < 2; ++e) {
+      const float2 p = both(mul2(A[e], F.fa[e])), q = both(x[e]), v = both(mul2(B[e], F.fb[e])), z = both(y[e]);
+      da[2 * e] = step * (fabsf(p.x) + fabsf(q.x)), da[2 * e + 1] = step * (fabsf(p.y) + fabsf(q.y));
+      db[2 * e] = step * (fabsf(v.x) + fabsf(z.x)), db[2 * e + 1] = step * (fabsf(v.y) + fabsf(z.y));
+    }
+    const int exp = head ? head_exp(a.exp[0], h0) : 0;
+    const bool exact = !w && !mine;  // neither scaled nor turned
+    if (exact) {
+#pragma unroll
+      for (int e = 0; e < 4; ++e) da[e] = db[e] = 0.f;
+    }
+    uint32_t sa, sb;
+    bool na, nb;
+    uint32_t ca = quantize4_near(ya, da, pow2i(-exp), pow2i(exp), exact, sa, na), cb = quantize4_near(yb, db, pow2i(-exp), pow2i(exp), exact, sb, nb);
+    if (__any_sync(0xFFFFFFFFu, (na || nb) && head)) {
+      const float2 p = both(A[0]), q = both(A[1]), v = both(B[0]), z = both(B[1]);
+      const uint2 again = exact_keys<DH>(make_float4(p.x, p.y, q.x, q.y), make_float4(v.x, v.y, z.x, z.y), w, ea, eb, a.eps, cs, mine, exp);
+      ca = again.x & 0xFFFFu;
+      cb = again.x >> 16;
+      sa = again.y & 0xFFu;
+      sb = again.y >> 8;
+    }
+    const long long to = head ? cache_row(a, h0, slot) * q4_row_bytes(DH) : 0;
+    if (head) store_codes<DH>(a, 0, to, ea, eb, ca, cb, sa, sb);
+    float va[4], vb[4];
+    widen4<DT>(ra[1], va);
+    widen4<DT>(rb[1], vb);
+    if (DT != MTP_DTYPE_BF16) {  // (bf16 has 8 bits)
+#pragma unroll
+      for (int e = 0; e < 4; ++e) {
+        va[e] = to_odd({va[e], 0.f});
+        vb[e] = to_odd({vb[e], 0.f});
+      }
+    }
+    const int vexp = head ? head_exp(a.exp[1], h0) : 0;
+    ca = quantize4(va, pow2i(-vexp), pow2i(vexp), sa);
+    cb = quantize4(vb, pow2i(-vexp), pow2i(vexp), sb);
+    if (head) store_codes<DH>(a, 1, to, ea, eb, ca, cb, sa, sb);
+  }
+  if (a.k_out && head) {
+    if (pos < 0) {
+#pragma unroll
+      for (int e = 0; e < 4; ++e) ya[e] = yb[e] = 0.f;
     }
     const long long at = ((long long)t * a.n_kv + h0) * DH;
     store4<DT>(a.k_out, at + ea, ya);
     store4<DT>(a.k_out, at + eb, yb);
   }
-  if (slot < 0) return;  // (the same for the warp)
-  const long long to = (head ? cache_row(a, h0, slot) : 0) * kRow;
-#pragma unroll
-  for (int side = 0; side < 2; ++side) {
-    float ya[4], yb[4];
-#pragma unroll
-    for (int e = 0; e < 4; ++e) {
-      // (bf16 has 8 bits)
-      ya[e] = side == 0 ? to_odd(ka[e]) : (DT == MTP_DTYPE_BF16 ? VA[e] : to_odd({VA[e], 0.f}));
-      yb[e] = side == 0 ? to_odd(kb[e]) : (DT == MTP_DTYPE_BF16 ? VB[e] : to_odd({VB[e], 0.f}));
-    }
-    const int exp = head ? head_exp(a.exp[side], h0) : 0;
-    uint32_t sa, sb;
-    const uint32_t ca = quantize4(ya, exp, sa), cb = quantize4(yb, exp, sb);
-    if (head) {
-      uint8_t* row = a.cache[side] + to;
-      *reinterpret_cast<uint16_t*>(row + ea / 2) = (uint16_t)ca;
-      *reinterpret_cast<uint16_t*>(row + eb / 2) = (uint16_t)cb;
-      if ((ea & 15) == 0) row[DH / 2 + ea / 16] = (uint8_t)sa;
-      if ((eb & 15) == 0) row[DH / 2 + eb / 16] = (uint8_t)sb;
-      if (sa == 0x7F || sb == 0x7F) flag_status(a.status, MTP_ERR_NONFINITE);
-    }
-  }
 }
 
-// Blocks stay and take positions in turn. One warp makes the next position's
-// angles, the others take kBatch x (32 / kLanes) heads of the queries or 32 /
-// kLanes heads of the keys and values at a time; a warp's next rows are on their
-// way while it works on those it has.
+// Blocks stay and take two positions at a time, whose angles were made while the two before were worked on. An item is
+// kBatch x (32 / kLanes) heads of the queries, or 32 / kLanes heads of the keys and values, which take longer: a warp that
+// has those at one position has queries at the other. Its next rows are on their way while it works on those it has.
 template <int DH, int DT>
 __global__ void __launch_bounds__(32 * kMostWarps, 2) k_rope_rows(const __grid_constant__ RopeArgs a) {
-  constexpr int kLanes = DH / 8, kGroups = 32 / kLanes, kRow = q4_row_bytes(DH);
-  __shared__ CosSin s_cs[2][DH / 2];
+  constexpr int kLanes = DH / 8, kGroups = 32 / kLanes;
+  __shared__ CosSin s_cs[4][DH / 2];
   __shared__ uint64_t s_turn[DH / 2];
   __shared__ float2 s_quarter[17];
   const int lane = threadIdx.x & 31, l = lane % kLanes, grp = lane / kLanes;
-  const int warp = __shfl_sync(0xFFFFFFFFu, (int)threadIdx.x >> 5, 0), workers = (blockDim.x >> 5) - 1;
+  const int warp = __shfl_sync(0xFFFFFFFFu, (int)threadIdx.x >> 5, 0), warps = blockDim.x >> 5;
   const int half = a.rope.rot_dim / 2, turned = half / 4, rest = (DH - a.rope.rot_dim) / 2;
   const bool mine = l < turned;
   const int ea = mine ? 4 * l : 2 * half + 4 * (l - turned), eb = mine ? half + 4 * l : ea + rest;
@@ -404,20 +587,24 @@ __global__ void __launch_bounds__(32 * kMostWarps, 2) k_rope_rows(const __grid_c
   __syncthreads();
   pdl_wait();
   pdl_trigger();
-  auto angles = [&](int t, int first, int step) {
-    const int pos = max(a.pos[t], 0);
-    for (int i = first; i < half; i += step) s_cs[t / gridDim.x & 1][i] = turn_cs(pos, s_turn[i], s_quarter);
-  };
-  if (warp == workers) {
-    if ((int)blockIdx.x < a.tokens) angles(blockIdx.x, lane, 32);
-    for (int t = blockIdx.x; t < a.tokens; t += gridDim.x) {
-      __syncthreads();  // the angles of t are there, those of the position before are no longer needed
-      if (t + (int)gridDim.x < a.tokens) angles(t + gridDim.x, lane, 32);
+  const int step = gridDim.x, parts = a.parts;
+  // of the block's positions k and k + 1
+  auto angles = [&](int k) {
+    for (int i = threadIdx.x; i < 2 * half; i += blockDim.x) {
+      const int y = i >= half, t = blockIdx.x + (k + y) * step;
+      if (t < a.tokens) s_cs[(k + y) & 3][i - y * half] = turn_cs(max(a.pos[t], 0), s_turn[i - y * half], s_quarter);
     }
-    return;
-  }
+  };
+  // a warp's i-th item of position k
+  auto part_of = [&](int k, int i) {
+    const int p = i + (k & 1 ? parts / 2 : 0);
+    return p < parts ? p : p - parts;
+  };
   Raw4<DT> ra[kBatch], rb[kBatch];
-  auto fetch = [&](int t, int part) {
+  auto fetch = [&](int k, int i) {
+    const int t = blockIdx.x + k * step;
+    if (t >= a.tokens || i >= parts) return;
+    const int part = part_of(k, i);
     const bool is_q = part < a.q_parts;
     const int h0 = is_q ? part * kBatch * kGroups + grp : (part - a.q_parts) * kGroups + grp, heads = is_q ? a.n_q : a.n_kv;
 #pragma unroll
@@ -430,113 +617,132 @@ __global__ void __launch_bounds__(32 * kMostWarps, 2) k_rope_rows(const __grid_c
       }
     }
   };
-  if ((int)blockIdx.x < a.tokens && warp < a.parts) fetch(blockIdx.x, warp);
+  fetch(0, warp);
+  angles(0);
 #pragma unroll 1
-  for (int t = blockIdx.x; t < a.tokens; t += gridDim.x) {
+  for (int k = 0;; ++k) {
+    const int t = blockIdx.x + k * step;
+    if (t >= a.tokens) break;
+    if ((k & 1) == 0) __syncthreads();
     const int pos = a.pos[t];
-    __syncthreads();
-    const CosSin* cs = s_cs[t / gridDim.x & 1] + 4 * l;
+    const CosSin* cs = s_cs[k & 3] + 4 * l;
 #pragma unroll 1
-    for (int part = warp; part < a.parts; part += workers) {
+    for (int i = warp; i < parts; i += warps) {
+      const int part = part_of(k, i);
       const bool is_q = part < a.q_parts;
       const int h0 = is_q ? part * kBatch * kGroups + grp : (part - a.q_parts) * kGroups + grp;
-      float A[kBatch][4], B[kBatch][4];
+      Raw4<DT> xa[kBatch], xb[kBatch];
 #pragma unroll
       for (int u = 0; u < kBatch; ++u) {
-        widen4<DT>(ra[u], A[u]);
-        widen4<DT>(rb[u], B[u]);
+        xa[u] = ra[u];
+        xb[u] = rb[u];
       }
-      if (part + workers < a.parts) fetch(t, part + workers);
-      else if (t + (int)gridDim.x < a.tokens) fetch(t + gridDim.x, warp);
+      if (i + warps < parts) fetch(k, i + warps);
+      else fetch(k + 1, warp);
       const float* w = a.norm[is_q ? 0 : 1];
       float4 wa = make_float4(1.f, 1.f, 1.f, 1.f), wb = wa;
       if (w) {
         wa = *reinterpret_cast<const float4*>(w + ea);
         wb = *reinterpret_cast<const float4*>(w + eb);
       }
-      if (is_q) rope_queries<DH, DT>(a, A, B, wa, wb, w != nullptr, cs, mine, t, pos, h0, ea, eb);
-      else rope_keys<DH, DT>(a, A[0], B[0], A[1], B[1], wa, wb, w != nullptr, cs, mine, t, pos, h0, ea, eb, part == a.q_parts && lane == 0);
+      const Factors F(wa, wb, cs, mine);
+      if (is_q) rope_queries<DH, DT>(a, xa, xb, F, w != nullptr, mine, t, pos, h0, ea, eb, lane);
+      else rope_keys<DH, DT>(a, xa, xb, F, w, cs, mine, t, pos, h0, ea, eb, part == a.q_parts && lane == 0);
     }
+    if (k & 1) angles(k + 1);
   }
 }
 
-// Any rotated width and any strides: a warp per (position, head), the row in
-// shared memory. Lane l has elements l, l + 32, ... of the row, so neighbouring
-// lanes read neighbouring elements; 16 of them are half a warp.
+// Any rotated width and any strides: a block per position, whose angles it makes once, a warp per head, the row in shared
+// memory. Lane l has elements l, l + 32, ... of the row, so neighbouring lanes read neighbouring elements; 16 of them are
+// half a warp. Keys in two floats, all of them.
 template <int DH, int DT>
 __global__ void __launch_bounds__(kRopeThreads) k_rope_any(const __grid_constant__ RopeArgs a) {
   constexpr int kRow = q4_row_bytes(DH), kN = DH / 32;
   __shared__ Two s_row[kRopeThreads / 32][DH];
+  __shared__ CosSin s_cs[DH / 2];
   __shared__ float2 s_quarter[17];
   pdl_wait();
   pdl_trigger();
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, heads = a.n_q + 2 * a.n_kv, t = blockIdx.x, half = a.rope.rot_dim / 2;
+  const int pos = a.pos[t];
   if (threadIdx.x < 17) s_quarter[threadIdx.x] = a.quarter[threadIdx.x];
   __syncthreads();
-  const int lane = threadIdx.x & 31, heads = a.n_q + 2 * a.n_kv;
-  const int item = blockIdx.x * (kRopeThreads / 32) + (threadIdx.x >> 5);
-  if (item >= a.tokens * heads) return;
-  const int t = item / heads, h = item - t * heads;
-  const int side = h < a.n_q ? 0 : (h < a.n_q + a.n_kv ? 1 : 2), g = h - (side == 0 ? 0 : (side == 1 ? a.n_q : a.n_q + a.n_kv));
-  const int pos = a.pos[t], slot = side > 0 ? slot_of(a, t, pos, h == heads - 1 && lane == 0) : -1, half = a.rope.rot_dim / 2;
-  Two* row_s = s_row[threadIdx.x >> 5];
-  const long long from = (long long)t * a.ts[side] + (long long)g * a.hs[side];
-  const float* w = side < 2 ? a.norm[side] : nullptr;
-  float x[kN];
-  Two sum = {0.f, 0.f};
-#pragma unroll
-  for (int i = 0; i < kN; ++i) {
-    x[i] = load_elem(a.x[side], DT, from + 32 * i + lane);
-    const Two p = two_prod(x[i], x[i], 0.f), n = two_sum(sum.hi, p.hi);
-    sum = {n.hi, n.lo + (sum.lo + p.lo)};
-  }
-#pragma unroll
-  for (int o = 1; o < 32; o <<= 1) {
-    const float hi = __shfl_xor_sync(0xFFFFFFFFu, sum.hi, o), lo = __shfl_xor_sync(0xFFFFFFFFu, sum.lo, o);
-    const Two n = two_sum(sum.hi, hi);
-    sum = {n.hi, n.lo + (sum.lo + lo)};
-  }
-  const Two r = root(sum, 1.f / DH, a.eps);
-#pragma unroll
-  for (int i = 0; i < kN; ++i) row_s[32 * i + lane] = w ? scaled(x[i], r, w[32 * i + lane]) : Two{x[i], 0.f};
-  __syncwarp();
-  if (side < 2 && pos > 0) {
+  for (int i = threadIdx.x; i < half; i += kRopeThreads) s_cs[i] = turn_cs(max(pos, 0), a.rope.turn[i], s_quarter);
+  __syncthreads();
+  const int slot = slot_of(a, t, pos, threadIdx.x == 0);
+  Two* row_s = s_row[warp];
+  float* flat = reinterpret_cast<float*>(row_s);
 #pragma unroll 1
-    for (int i = lane; i < half; i += 32) {
-      const CosSin c = turn_cs(pos, a.rope.turn[i], s_quarter);
-      const Two u = row_s[i], v = row_s[half + i];
-      row_s[i] = turn_one(u, v, c.ch, c.cl, c.sh, c.sl);
-      row_s[half + i] = turn_one(v, u, c.ch, c.cl, -c.sh, -c.sl);
-    }
-  }
-  __syncwarp();
-  void* out = side == 0 ? a.q_out : (side == 1 ? a.k_out : nullptr);
-  const long long to = ((long long)t * (side == 0 ? a.n_q : a.n_kv) + g) * DH;
-  const int exp = side > 0 ? head_exp(a.exp[side - 1], g) : 0;
-  const long long row_at = slot >= 0 ? cache_row(a, g, slot) * kRow : 0;
+  for (int h = warp; h < heads; h += kRopeThreads / 32) {
+    const int side = h < a.n_q ? 0 : (h < a.n_q + a.n_kv ? 1 : 2), g = h - (side == 0 ? 0 : (side == 1 ? a.n_q : a.n_q + a.n_kv));
+    const long long from = (long long)t * a.ts[side] + (long long)g * a.hs[side];
+    const float* w = side < 2 ? a.norm[side] : nullptr;
+    float x[kN];
 #pragma unroll
-  for (int i = 0; i < kN; ++i) {
-    const Two z = row_s[32 * i + lane];
-    if (out) store_elem(out, DT, to + 32 * i + lane, pos >= 0 ? nearest(z) : 0.f);
-    if (slot < 0) continue;  // (the same for the warp)
-    const float y = to_odd(z);
-    uint32_t mx = __float_as_uint(y) & 0x7FFFFFFFu;
+    for (int i = 0; i < kN; ++i) x[i] = load_elem(a.x[side], DT, from + 32 * i + lane);
+    __syncwarp();
+    if (side == 1) {
+      Two sum = {0.f, 0.f};
 #pragma unroll
-    for (int o = 1; o < 16; o <<= 1) mx = max(mx, __shfl_xor_sync(0xFFFFFFFFu, mx, o));
-    float sv, rs;
-    uint32_t sc = scale4(fminf(__uint_as_float(mx) * pow2i(-exp), FLT_MAX), sv);
-    sv *= pow2i(exp);
-    asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(rs) : "f"(sv));
-    const float q[4] = {over(y, sv, rs), 0.f, 0.f, 0.f};
-    uint32_t code = sc != 0 ? codes4(q) : 0u;
-    if (mx >= 0x7F800000u) {
-      sc = 0x7F;
-      code = 0;
-      if ((lane & 15) == 0) flag_status(a.status, MTP_ERR_NONFINITE);
+      for (int i = 0; i < kN; ++i) {
+        const Two p = two_prod(x[i], x[i], 0.f), n = two_sum(sum.hi, p.hi);
+        sum = {n.hi, n.lo + (sum.lo + p.lo)};
+      }
+#pragma unroll
+      for (int o = 1; o < 32; o <<= 1) {
+        const float hi = __shfl_xor_sync(0xFFFFFFFFu, sum.hi, o), lo = __shfl_xor_sync(0xFFFFFFFFu, sum.lo, o);
+        const Two n = two_sum(sum.hi, hi);
+        sum = {n.hi, n.lo + (sum.lo + lo)};
+      }
+      const Two r = root(sum, 1.f / DH, a.eps);
+#pragma unroll
+      for (int i = 0; i < kN; ++i) row_s[32 * i + lane] = w ? scaled(x[i], r, w[32 * i + lane]) : Two{x[i], 0.f};
+      __syncwarp();
+      for (int i = lane; i < half; i += 32) {
+        const CosSin c = s_cs[i];
+        const Two u = row_s[i], v = row_s[half + i];
+        row_s[i] = turn_one(u, v, c.ch, c.cl, c.sh, c.sl);
+        row_s[half + i] = turn_one(v, u, c.ch, c.cl, -c.sh, -c.sl);
+      }
+      __syncwarp();
+    } else if (side == 0) {
+      float sum = 0.f;
+#pragma unroll
+      for (int i = 0; i < kN; ++i) sum = fmaf(x[i], x[i], sum);
+      const float r = w ? rsqrtf(fmaf(warp_sum(sum), 1.f / DH, a.eps)) : 1.f;
+#pragma unroll
+      for (int i = 0; i < kN; ++i) flat[32 * i + lane] = w ? x[i] * (r * w[32 * i + lane]) : x[i];
+      __syncwarp();
+      for (int i = lane; i < half; i += 32) {
+        const float c = s_cs[i].ch, s = s_cs[i].sh, u = flat[i], v = flat[half + i];
+        flat[i] = fmaf(u, c, -(v * s));
+        flat[half + i] = fmaf(v, c, u * s);
+      }
+      __syncwarp();
     }
-    code |= __shfl_down_sync(0xFFFFFFFFu, code, 1) << 4;
-    uint8_t* row = a.cache[side - 1] + row_at;
-    if ((lane & 1) == 0) row[16 * i + lane / 2] = (uint8_t)code;
-    if ((lane & 15) == 0) row[DH / 2 + 2 * i + lane / 16] = (uint8_t)sc;
+    void* out = side == 0 ? a.q_out : (side == 1 ? a.k_out : nullptr);
+    const long long to = ((long long)t * (side == 0 ? a.n_q : a.n_kv) + g) * DH;
+    const int exp = side > 0 ? head_exp(a.exp[side - 1], g) : 0;
+    const long long row_at = side > 0 && slot >= 0 ? cache_row(a, g, slot) * kRow : 0;
+#pragma unroll
+    for (int i = 0; i < kN; ++i) {
+      const Two z = side == 1 ? row_s[32 * i + lane] : Two{side == 0 ? flat[32 * i + lane] : x[i], 0.f};
+      if (out) store_elem(out, DT, to + 32 * i + lane, pos >= 0 ? nearest(z) : 0.f);
+      if (side == 0 || slot < 0) continue;  // (the same for the warp)
+      const float y = to_odd(z);
+      uint32_t mx = __float_as_uint(y) & 0x7FFFFFFFu;
+#pragma unroll
+      for (int o = 1; o < 16; o <<= 1) mx = max(mx, __shfl_xor_sync(0xFFFFFFFFu, mx, o));
+      const Block4 b = block4(mx, pow2i(-exp), pow2i(exp));
+      const float q[4] = {over(y, b.s, b.rs), 0.f, 0.f, 0.f};
+      uint32_t code = b.sc == 0 || b.sc == 0x7F ? 0u : codes4(q);
+      if (b.sc == 0x7F && (lane & 15) == 0) flag_status(a.status, MTP_ERR_NONFINITE);
+      code |= __shfl_down_sync(0xFFFFFFFFu, code, 1) << 4;
+      uint8_t* row = a.cache[side - 1] + row_at;
+      if ((lane & 1) == 0) row[16 * i + lane / 2] = (uint8_t)code;
+      if ((lane & 15) == 0) row[DH / 2 + 2 * i + lane / 16] = (uint8_t)b.sc;
+    }
   }
 }
 
@@ -612,7 +818,6 @@ mtp_status kv_q4_append_rope(mtp_stream stream, const kv_q4_cache* c, int32_t to
   if (cross(d_q_out, (size_t)tokens * n_q * dh * es, d_k_out, d_k_out ? (size_t)tokens * c->n_kv * dh * es : 0)) return MTP_ERR_BAD_ARG;
   uintptr_t align = bits(d_q) | bits(d_k) | bits(d_v);
   for (int i = 0; i < 3; ++i) align |= (uintptr_t)(a.ts[i] * es) | (uintptr_t)(a.hs[i] * es);
-  const int all = n_q + 2 * c->n_kv;
   const bool fast = rope->rot_dim % 32 == 0 && (align & (4 * es - 1)) == 0;
   cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
   void (*k)(RopeArgs);
@@ -622,13 +827,14 @@ mtp_status kv_q4_append_rope(mtp_stream stream, const kv_q4_cache* c, int32_t to
     const int groups = 256 / dh;
     a.q_parts = (n_q + kBatch * groups - 1) / (kBatch * groups);
     a.parts = a.q_parts + (c->n_kv + groups - 1) / groups;
-    threads = 32 * std::min(a.parts + 1, kMostWarps);
-    blocks = std::min<long long>(tokens, (long long)device_sm_count() * (24 * 32 / threads));  // (80 registers a thread)
+    const int warps = std::min(a.parts, kMostWarps);
+    threads = 32 * warps;
+    blocks = std::min<long long>(tokens, (long long)device_sm_count() * (2 * kMostWarps / warps));
     k = dtype == MTP_DTYPE_BF16
             ? (dh == 64 ? k_rope_rows<64, MTP_DTYPE_BF16> : (dh == 128 ? k_rope_rows<128, MTP_DTYPE_BF16> : k_rope_rows<256, MTP_DTYPE_BF16>))
             : (dh == 64 ? k_rope_rows<64, MTP_DTYPE_F32> : (dh == 128 ? k_rope_rows<128, MTP_DTYPE_F32> : k_rope_rows<256, MTP_DTYPE_F32>));
   } else {
-    blocks = ((long long)tokens * all + kRopeThreads / 32 - 1) / (kRopeThreads / 32);
+    blocks = tokens;
     k = dtype == MTP_DTYPE_BF16
             ? (dh == 64 ? k_rope_any<64, MTP_DTYPE_BF16> : (dh == 128 ? k_rope_any<128, MTP_DTYPE_BF16> : k_rope_any<256, MTP_DTYPE_BF16>))
             : (dh == 64 ? k_rope_any<64, MTP_DTYPE_F32> : (dh == 128 ? k_rope_any<128, MTP_DTYPE_F32> : k_rope_any<256, MTP_DTYPE_F32>));
