@@ -151,6 +151,27 @@ int columns(int n_q, int n_kv, int max_q, bool wide) {
   return rows <= 16 ? 16 : (rows <= 32 ? 32 : (rows <= 64 || wide ? 64 : 128));
 }
 
+// Trees: the query rows of one KV head are many (16 nodes of 6 heads fill 96 columns) and the rows of a call few, so
+// that wide tiles leave blocks without work, or with one tile and all of its start, drain and join. Estimated from what
+// was measured with 24 heads on 4 of 256, in us: a block's tiles at 1.25, 1.9 or 3.1 with 32, 64 or 128 columns, and 24,
+// 30 or 33 for the rest. Times with these: one row of 16 nodes at 4096 positions 27.8, 29.0, 33.4; of 33 nodes 29.1,
+// 41.4, 40.7; of 64 at 16,384 73.9, 74.3, 68.4; eight rows of 16 at 8192 71.4, 79.1, 68.3, of 33 157, 137, 128. The
+// lengths are taken to be what the block table holds; no more columns than the workspace has room for.
+int tree_columns(int widest, long long query_rows, long long heads, long long tiles, int blocks) {
+  constexpr float kTile[3] = {1.25f, 1.9f, 3.1f}, kRest[3] = {24.f, 30.f, 33.f};
+  int best = widest;
+  float least = INFINITY;
+  for (int i = 0, n = 32; n <= widest; ++i, n *= 2) {
+    const long long tasks = heads * tiles * ((query_rows + n - 1) / n);
+    const float t = (float)((tasks + blocks - 1) / blocks) * kTile[i] + kRest[i];
+    if (t < least) {
+      least = t;
+      best = n;
+    }
+  }
+  return best;
+}
+
 }  // namespace
 }  // namespace mtp
 
@@ -185,7 +206,12 @@ static mtp_status attend(mtp_stream stream, const kv_q4_cache* c, int32_t rows, 
       (reinterpret_cast<uintptr_t>(d_q) & (es - 1)) != 0 || (reinterpret_cast<uintptr_t>(d_out) & 15) != 0 ||
       (reinterpret_cast<uintptr_t>(d_workspace) & 15) != 0)
     return MTP_ERR_BAD_ARG;
-  const int blocks = device_sm_count(), n = columns(n_q, c->n_kv, max_q, wide), rt = n / (wide ? 2 : 1);
+  const int blocks = device_sm_count();
+  int n = columns(n_q, c->n_kv, max_q, wide);
+  if (d_mask)
+    n = tree_columns(n, (long long)max_q * (n_q / c->n_kv) * (wide ? 2 : 1), (long long)rows * c->n_kv,
+                     ((long long)max_pages * c->page + kT - 1) / kT, blocks);
+  const int rt = n / (wide ? 2 : 1);
   uint8_t* w = static_cast<uint8_t*>(d_workspace);
   int4* meta = reinterpret_cast<int4*>(w);
   w += sizeof(int4) * 2 * blocks;
