@@ -19,20 +19,30 @@ namespace {
 
 // ------------------------------------------------------------ CUDA cores
 
-constexpr int kSimtRows = 64, kSimtKeys = 32, kSimtThreads = 256;
+constexpr int kSimtRows = 64, kSimtThreads = 256;
 
 template <int DH>
-constexpr int simt_smem() { return ((kSimtRows + 2 * kSimtKeys) * (DH + 4) + kSimtRows * (kSimtKeys + 4)) * 4; }
+struct Simt {
+  static constexpr int kKeys = DH == 256 ? 32 : 64;  // of a tile; two tiles of K and V fit
+  static constexpr int kS = DH + 4, kPS = kKeys + 4;  // strides of rows, of P's
+  static constexpr int kTile = kKeys * kS;
+  static constexpr int kSmem = (kSimtRows * kS + 4 * kTile + kSimtRows * kPS) * 4;
+  static_assert(kSmem <= 227 * 1024, "shared memory");
+};
 
-// 64 queries of a head against 32 keys at a time, all in fp32. Thread (ty, tx)
-// of 16 x 16 has the scores of 4 queries with 2 keys, then 4 queries' outputs
-// in DH / 16 dimensions: 32 products per 8 shared-memory accesses of a warp,
-// which is what the multiply-add units and shared memory sustain together.
+// 16 bytes to shared memory asynchronously; zeros where there is nothing to copy.
+__device__ __forceinline__ void copy16(float* dst, const float* src, bool some) {
+  asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(smem_u32(dst)), "l"(src), "r"(some ? 16 : 0) : "memory");
+}
+
+// 64 queries of a head against 32 or 64 keys at a time, all in fp32; the next tile of K and V is copied meanwhile. Thread
+// (ty, tx) of 16 x 16 has the scores of 4 queries with kKeys / 16 keys, then 4 queries' outputs in DH / 16 dimensions.
 template <int DH>
 __global__ void __launch_bounds__(kSimtThreads) k_prompt_simt(const __grid_constant__ PromptArgs a) {
-  constexpr int kS = DH + 4, kPS = kSimtKeys + 4, kD = DH / 64;
+  using S = Simt<DH>;
+  constexpr int kD = DH / 64, kB = S::kKeys / 16;
   extern __shared__ __align__(16) float smem[];
-  float *sq = smem, *sk = sq + kSimtRows * kS, *sv = sk + kSimtKeys * kS, *sp = sv + kSimtKeys * kS;
+  float *sq = smem, *skv = sq + kSimtRows * S::kS, *sp = skv + 4 * S::kTile;
   __shared__ int s_at[4];
   pdl_wait();
   pdl_trigger();
@@ -53,15 +63,18 @@ __global__ void __launch_bounds__(kSimtThreads) k_prompt_simt(const __grid_const
   auto stage = [&](float* dst, int side, const void* src, int head, int first, int count, int most) {
     for (int e = tid; e < most * (DH / 4); e += kSimtThreads) {
       const int r = e / (DH / 4), d = e % (DH / 4) * 4;
-      float4 x = make_float4(0.f, 0.f, 0.f, 0.f);
-      if (r < count) {
-        const long long at = (long long)(a0 + first + r) * a.ts[side] + (long long)head * a.hs[side] + d;
-        x = *reinterpret_cast<const float4*>(static_cast<const float*>(src) + at);
-      }
-      *reinterpret_cast<float4*>(dst + r * kS + d) = x;
+      const long long at = (long long)(a0 + first + min(r, max(count, 1) - 1)) * a.ts[side] + (long long)head * a.hs[side] + d;
+      copy16(dst + r * S::kS + d, static_cast<const float*>(src) + at, r < count);
     }
   };
+  const int first = a.window > 0 ? max(0, i0 - (a.window - 1)) / S::kKeys * S::kKeys : 0, last = i0 + rows;
+  auto keys = [&](int t0, int buf) {
+    stage(skv + 2 * buf * S::kTile, 1, a.k, g, t0, min(n - t0, S::kKeys), S::kKeys);
+    stage(skv + (2 * buf + 1) * S::kTile, 2, a.v, g, t0, min(n - t0, S::kKeys), S::kKeys);
+    asm volatile("cp.async.commit_group;" ::: "memory");
+  };
   stage(sq, 0, a.q, h, i0, rows, kSimtRows);
+  keys(first, 0);
   const float c = a.scale * 1.44269504f;
   float m[4], l[4], o[4][kD][4];
 #pragma unroll
@@ -73,50 +86,57 @@ __global__ void __launch_bounds__(kSimtThreads) k_prompt_simt(const __grid_const
 #pragma unroll
       for (int e = 0; e < 4; ++e) o[r][d][e] = 0.f;
   }
-  const int first = a.window > 0 ? max(0, i0 + 1 - a.window) / kSimtKeys * kSimtKeys : 0, last = i0 + rows;
-  for (int t0 = first; t0 < last; t0 += kSimtKeys) {
+  int buf = 0;
+  for (int t0 = first; t0 < last; t0 += S::kKeys, buf ^= 1) {
+    if (t0 + S::kKeys < last) {
+      keys(t0 + S::kKeys, buf ^ 1);
+      asm volatile("cp.async.wait_group 1;" ::: "memory");
+    } else {
+      asm volatile("cp.async.wait_group 0;" ::: "memory");
+    }
     __syncthreads();
-    stage(sk, 1, a.k, g, t0, min(n - t0, kSimtKeys), kSimtKeys);
-    stage(sv, 2, a.v, g, t0, min(n - t0, kSimtKeys), kSimtKeys);
-    __syncthreads();
-    float s[4][2];
+    const float *sk = skv + 2 * buf * S::kTile, *sv = sk + S::kTile;
+    float s[4][kB];
 #pragma unroll
-    for (int r = 0; r < 4; ++r) s[r][0] = s[r][1] = 0.f;
+    for (int r = 0; r < 4; ++r)
+#pragma unroll
+      for (int b = 0; b < kB; ++b) s[r][b] = 0.f;
 #pragma unroll 4
     for (int d = 0; d < DH; d += 4) {
-      float4 qv[4], kv[2];
+      float4 qv[4], kv[kB];
 #pragma unroll
-      for (int r = 0; r < 4; ++r) qv[r] = *reinterpret_cast<const float4*>(sq + (4 * ty + r) * kS + d);
+      for (int r = 0; r < 4; ++r) qv[r] = *reinterpret_cast<const float4*>(sq + (4 * ty + r) * S::kS + d);
 #pragma unroll
-      for (int b = 0; b < 2; ++b) kv[b] = *reinterpret_cast<const float4*>(sk + (tx + 16 * b) * kS + d);
+      for (int b = 0; b < kB; ++b) kv[b] = *reinterpret_cast<const float4*>(sk + (tx + 16 * b) * S::kS + d);
 #pragma unroll
       for (int r = 0; r < 4; ++r)
 #pragma unroll
-        for (int b = 0; b < 2; ++b)
+        for (int b = 0; b < kB; ++b)
           s[r][b] = fmaf(qv[r].x, kv[b].x, fmaf(qv[r].y, kv[b].y, fmaf(qv[r].z, kv[b].z, fmaf(qv[r].w, kv[b].w, s[r][b]))));
     }
-    const bool edge = t0 + kSimtKeys > i0 + 1 || (a.window > 0 && t0 <= i0 + kSimtRows - 1 - a.window);
+    const bool edge = t0 + S::kKeys > i0 + 1 || (a.window > 0 && t0 <= i0 + kSimtRows - 1 - a.window);
 #pragma unroll
     for (int r = 0; r < 4; ++r) {
       const int i = i0 + 4 * ty + r;
-      bool gone[2];
+      bool gone[kB];
+      float mx = -INFINITY;
 #pragma unroll
-      for (int b = 0; b < 2; ++b) {
+      for (int b = 0; b < kB; ++b) {
         const int t = t0 + tx + 16 * b;
         gone[b] = t > i || (a.window > 0 && t <= i - a.window);
         s[r][b] = gone[b] ? -INFINITY : s[r][b] * c;
+        mx = fmaxf(mx, s[r][b]);
       }
-      float mx = fmaxf(s[r][0], s[r][1]);
 #pragma unroll
       for (int w = 1; w < 16; w <<= 1) mx = fmaxf(mx, __shfl_xor_sync(0xFFFFFFFFu, mx, w));
       const float nm = fmaxf(m[r], mx), from = nm == -INFINITY ? 0.f : nm;
       const float f = m[r] == nm ? 1.f : exp2f(m[r] - from);
       float sum = 0.f;
 #pragma unroll
-      for (int b = 0; b < 2; ++b) {
+      for (int b = 0; b < kB; ++b) {
         const float p = exp2f(s[r][b] - from);
         if (!gone[b]) sum += p;
-        sp[(4 * ty + r) * kPS + tx + 16 * b] = gone[b] ? -1.f : p;  // (-1: out of sight, whatever V holds there)
+        sp[(4 * ty + r) * S::kPS + tx + 16 * b] = gone[b] ? -1.f : p;  // (-1: out of sight, whatever V holds there)
       }
 #pragma unroll
       for (int w = 1; w < 16; w <<= 1) sum += __shfl_xor_sync(0xFFFFFFFFu, sum, w);
@@ -130,10 +150,10 @@ __global__ void __launch_bounds__(kSimtThreads) k_prompt_simt(const __grid_const
     __syncwarp();  // (a query's 16 threads are one warp's)
     auto add = [&](auto edges) {
 #pragma unroll 2
-      for (int t = 0; t < kSimtKeys; t += 4) {
+      for (int t = 0; t < S::kKeys; t += 4) {
         float4 p[4];
 #pragma unroll
-        for (int r = 0; r < 4; ++r) p[r] = *reinterpret_cast<const float4*>(sp + (4 * ty + r) * kPS + t);
+        for (int r = 0; r < 4; ++r) p[r] = *reinterpret_cast<const float4*>(sp + (4 * ty + r) * S::kPS + t);
 #pragma unroll
         for (int u = 0; u < 4; ++u) {
           float pu[4];
@@ -141,7 +161,7 @@ __global__ void __launch_bounds__(kSimtThreads) k_prompt_simt(const __grid_const
           for (int r = 0; r < 4; ++r) pu[r] = u == 0 ? p[r].x : (u == 1 ? p[r].y : (u == 2 ? p[r].z : p[r].w));
 #pragma unroll
           for (int d = 0; d < kD; ++d) {
-            const float4 v = *reinterpret_cast<const float4*>(sv + (t + u) * kS + 64 * d + 4 * tx);
+            const float4 v = *reinterpret_cast<const float4*>(sv + (t + u) * S::kS + 64 * d + 4 * tx);
 #pragma unroll
             for (int r = 0; r < 4; ++r) {
               if (decltype(edges)::value && pu[r] < 0.f) continue;
@@ -156,6 +176,7 @@ __global__ void __launch_bounds__(kSimtThreads) k_prompt_simt(const __grid_const
     };
     if (edge) add(std::true_type{});
     else add(std::false_type{});
+    __syncthreads();  // (before the copies of the tile after the next)
   }
 #pragma unroll
   for (int r = 0; r < 4; ++r) {
@@ -165,11 +186,9 @@ __global__ void __launch_bounds__(kSimtThreads) k_prompt_simt(const __grid_const
     const float f = l[r] != 0.f ? 1.f / l[r] : 0.f;
     if (tx == 0 && a.lse) a.lse[at] = l[r] != 0.f ? (m[r] + log2f(l[r])) * 0.693147181f : -INFINITY;
 #pragma unroll
-    for (int d = 0; d < kD; ++d) {
-      const float y[4] = {o[r][d][0] * f, o[r][d][1] * f, o[r][d][2] * f, o[r][d][3] * f};
-      const long long to = at * DH + 64 * d + 4 * tx;
-      *reinterpret_cast<float4*>(static_cast<float*>(a.out) + to) = make_float4(y[0], y[1], y[2], y[3]);
-    }
+    for (int d = 0; d < kD; ++d)
+      *reinterpret_cast<float4*>(static_cast<float*>(a.out) + at * DH + 64 * d + 4 * tx) =
+          make_float4(o[r][d][0] * f, o[r][d][1] * f, o[r][d][2] * f, o[r][d][3] * f);
   }
 }
 
@@ -191,11 +210,11 @@ template <int DH>
 cudaError_t launch_simt(const PromptArgs& a, cudaStream_t s) {
   static std::mutex mu;
   static bool set[kMaxDevices] = {};
-  const cudaError_t e = raise_smem(k_prompt_simt<DH>, simt_smem<DH>(), set, mu);
+  const cudaError_t e = raise_smem(k_prompt_simt<DH>, Simt<DH>::kSmem, set, mu);
   if (e != cudaSuccess) return e;
   count_launch();
   return launch_pdl(k_prompt_simt<DH>, dim3((unsigned)(prompt_most_tiles(a.tokens, a.rows, 1, kSimtRows) * a.n_q)),
-                    dim3(kSimtThreads), simt_smem<DH>(), s, a);
+                    dim3(kSimtThreads), Simt<DH>::kSmem, s, a);
 }
 
 }  // namespace
