@@ -36,7 +36,9 @@ __device__ __forceinline__ void copy16(float* dst, const float* src, bool some) 
 }
 
 // 64 queries of a head against 32 or 64 keys at a time, all in fp32; the next tile of K and V is copied meanwhile. Thread
-// (ty, tx) of 16 x 16 has the scores of 4 queries with kKeys / 16 keys, then 4 queries' outputs in DH / 16 dimensions.
+// (ty, tx) of 16 x 16 has the scores of 4 queries with kKeys / 16 keys, then 4 queries' outputs in DH / 16 dimensions: 8
+// loads of 16 bytes from shared memory per 64 products, which bound it. 1024 positions of 24 heads of 256: 440 us, 29
+// TFLOP/s; 3 rows of up to 131 of 4 heads of 64: 18 us, three tiles one after another.
 template <int DH>
 __global__ void __launch_bounds__(kSimtThreads) k_prompt_simt(const __grid_constant__ PromptArgs a) {
   using S = Simt<DH>;

@@ -56,6 +56,11 @@
 //     4096 of up to 127 282 us. Every block reads all rows' lengths, 32 at a time,
 //     which at 4096 rows is 128 dependent steps; not measured by itself
 //
+// Trees (TREE, kv_q4_attend_tree): the queries are the nodes of a tree at a row's last positions. The tiles that hold them
+// are edges, where a query's sight is a bit of its mask; everything before is the same. 8 rows of 20 to 33 nodes, 1k to 16k
+// positions: 127 us, 392 TFLOP/s: a block has 29 tiles of 128 columns at some 4600 cycles and two or three shares, whose
+// starts, drains (128 KB of O each) and join are the other half. One row of 16 nodes at 4096 positions: 27 us.
+//
 // fp32 queries: q and the weights each enter as two f16 parts in separate
 // columns (22 bits), N / 2 rows a tile.
 //

@@ -6,7 +6,8 @@
 // m_i the nodes at distances [0, 2^k) above i and j_i the one at 2^k,
 //   m_i |= m_{j_i},  j_i = j_{j_i}
 // so a chain of 128 takes seven steps where walking it takes 127 dependent
-// loads. A block per row, a thread per node; bound by latency.
+// loads. A block per row, a thread per node; bound by latency: 8 trees of 16 nodes
+// 1.8 us, 512 trees of up to 128 2.8 us, in a graph of such calls.
 //
 // Commit. next_i = the lowest child of i whose token is choice_i, found for all
 // nodes at once; the path is then one dependent load per node. The row of the
@@ -16,7 +17,8 @@
 // excludes; it may be one of an earlier node, so a thread takes its bytes of
 // all of the path's rows in order, reading ahead of its writes. Every block of
 // a row walks the path again (it is L2-resident and a few hundred cycles) and
-// takes a part of the layers, sides and heads: one launch for all layers.
+// takes a part of the layers, sides and heads: one launch for all layers. 8 rows
+// and one layer 3.3 us, 64 rows and 16 layers 4.6 us (4.8 MB).
 #include <algorithm>
 
 #include "common.cuh"
