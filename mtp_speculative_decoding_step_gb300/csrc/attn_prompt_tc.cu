@@ -47,6 +47,7 @@ namespace mtp {
 namespace {
 
 constexpr int kPromptThreads = 384;
+
 // A warp's 32 rows (lane = row) of 32 columns.
 __device__ __forceinline__ void tmem_ld_rows32(uint32_t t, uint32_t* r) {
   asm volatile(
@@ -140,6 +141,8 @@ __host__ __device__ constexpr uint32_t idesc_bf(int m, int n, bool b_mn) {
   return (1u << 4) | (1u << 7) | (1u << 10) | ((b_mn ? 1u : 0u) << 16) | ((uint32_t)(n >> 3) << 17) | ((uint32_t)(m >> 4) << 24);
 }
 
+constexpr int kMeta = 3 << 10;  // bytes of PromptMeta, rounded up
+
 template <int DH>
 struct PromptShape {
   static constexpr int QT = DH == 256 ? 1 : 2;    // query tiles of a block
@@ -149,7 +152,7 @@ struct PromptShape {
   static constexpr int kHalves = DH == 64 ? 1 : 2;  // P is given on in one piece or in two (64 dimensions' products are too short to wait twice)
   static constexpr int kQ = QT * 128 * DH * 2, kStage = 128 * DH * 2 / CPT;
   static constexpr int oRing = kQ, oMeta = oRing + NS * kStage;
-  static constexpr int kMeta = 3072, kSmem = oMeta + kMeta;
+  static constexpr int kSmem = oMeta + kMeta;
   static constexpr uint32_t cS = 0, cO = 256;     // columns of tensor memory: S at 0 and 128, O from 256 on
   static_assert(kSmem <= 227 * 1024, "shared memory");
   // a unit's stage of V of tile j, in the order of use: S of the first item(s), then P.V of item k and S of item k + 2
@@ -221,7 +224,7 @@ __device__ __forceinline__ bool find_unit(const PromptArgs& a, int per, long lon
 constexpr int kUnits = 4;  // units handed out ahead
 
 struct PromptMeta {
-  uint64_t full[8], empty[8], s_full[2], p_full[2][2], pv_done[2], m_full[2][4], q_full, q_empty, o_empty[2], v_go, v_ok, drain;
+  uint64_t full[8], empty[8], s_full[2], p_full[2][2], pv_done[2], m_full[2][4], l_full[2][4], q_full, q_empty, o_empty[2], v_go, v_ok, drain;
   uint64_t unit_full[kUnits], unit_empty[kUnits];
   Unit unit[kUnits];
   uint32_t tmem, copied;
@@ -230,7 +233,7 @@ struct PromptMeta {
   float m[128];        // one query tile: the running maxima
   float l[2][128];     // the groups' sums
 };
-static_assert(sizeof(PromptMeta) <= 3072, "meta");
+static_assert(sizeof(PromptMeta) <= kMeta, "meta");
 
 // Eight words a lane that belong to one of four columns of two each: lane q of four neighbouring ones gets column q of
 // all four (its words 2 j, 2 j + 1: lane j's).
@@ -293,7 +296,10 @@ __global__ void __launch_bounds__(kPromptThreads, 1)
       for (int h = 0; h < 2; ++h) mbar_init(smem_u32(&M.p_full[i][h]), 4);
       mbar_init(smem_u32(&M.pv_done[i]), 1);
       mbar_init(smem_u32(&M.o_empty[i]), 4);
-      for (int w = 0; w < 4; ++w) mbar_init(smem_u32(&M.m_full[i][w]), 1);
+      for (int w = 0; w < 4; ++w) {
+        mbar_init(smem_u32(&M.m_full[i][w]), 1);
+        mbar_init(smem_u32(&M.l_full[i][w]), 1);
+      }
     }
     mbar_init(smem_u32(&M.q_full), 1);
     mbar_init(smem_u32(&M.q_empty), 1);
@@ -763,11 +769,21 @@ __global__ void __launch_bounds__(kPromptThreads, 1)
       int c0 = 0;
       constexpr int kDims = S::QT == 2 ? DH : DH / 2;
       if (S::QT == 1) {  // the groups' sums, then half of the dimensions each
-        asm volatile("barrier.cta.sync.aligned 1, 256;" ::: "memory");
+        // Two warps have the same rows. Each says twice a unit where it is: that its maxima are written, that its sums
+        // are. (Not a barrier of the two groups: one that had left would keep the other for good.)
+        auto meet = [&](uint32_t parity) {
+          __syncwarp();
+          if (lane == 0) mbar_arrive(smem_u32(&M.l_full[slot][quarter]));
+          ok = ready(&M.l_full[slot ^ 1][quarter], parity);
+        };
+        if (!ok) break;
+        meet(0);
+        if (!ok) break;
         const float top = M.m[row];
         l = m == -INFINITY ? l : l * ex2(m - top);
         M.l[slot][row] = l;
-        asm volatile("barrier.cta.sync.aligned 1, 256;" ::: "memory");
+        meet(1);
+        if (!ok) break;
         l += M.l[slot ^ 1][row];
         m = top;
         c0 = slot * kDims;

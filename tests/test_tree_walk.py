@@ -111,3 +111,8 @@ def test_prompt_kernel_takes_tensor_memory_before_a_dependent_kernel_may():
     """A dependent kernel that allocates before its wait would hold what this one's later blocks need."""
     src = source("attn_prompt_tc.cu")
     assert src.index("pdl_wait();") < src.index("tcgen05.alloc") < src.index("pdl_trigger();")
+
+
+def test_prompt_kernel_waits_with_limits_only():
+    """A barrier of some of the warps would keep the others for good where one has left after a wait that ran out."""
+    assert not re.findall(r"barrier\.cta|bar\.sync|group_sync|group_any", source("attn_prompt_tc.cu"))
