@@ -593,12 +593,13 @@ mtp_status kv_q4_tree_commit(mtp_stream stream, const kv_q4_cache* caches, int32
  *   s_ij = scale * q_i . k_j,  out_i = sum_j softmax(s_i)_j v_j,  lse_i = log sum_j exp(s_ij)
  *   d_q, d_k, d_v: element (t, head, i) at t * tok_stride + head * head_stride + i
  *       (slices of a fused projection will do); bases and strides multiples of
- *       16 bytes
+ *       16 bytes, strides above 0 and below 2^40 bytes
  *   d_out [tokens][n_q][head_dim] contiguous in dtype, 16-byte aligned;
  *   d_lse [tokens][n_q] float (optional)
- *   max_len: the most positions of a row, as the caller knows it, for the launch's
- *       shape only: rows that have more are still computed
- *   d_workspace: kv_attend_prompt_workspace_bytes(tokens, rows), 16-byte aligned
+ *   max_len: the most positions of a row, as the caller knows it, at least 1. A hint:
+ *       rows that have more are still computed. The launch's shape does not need it now
+ *   d_workspace: kv_attend_prompt_workspace_bytes(tokens, rows), 16-byte aligned. The
+ *       kernels do not write it now, so calls may share one
  * Positions that a query does not see may hold anything; what it does see and is
  * NaN or infinite shows in its outputs. Rows of d_out and d_lse outside
  * [start[0], start[rows]) are not written. Scores, sums and outputs are

@@ -12,6 +12,7 @@
 #include "common.cuh"
 #include "kernels.h"
 #include "prompt_tiles.h"
+#include "ranges.h"
 
 namespace mtp {
 
@@ -248,21 +249,25 @@ mtp_status kv_attend_prompt(mtp_stream stream, int32_t rows, int32_t n_q, int32_
                d_start, d_out, d_lse, d_status, rows, n_q, n_kv, tokens, window, scale};
   uintptr_t bits = reinterpret_cast<uintptr_t>(d_q) | reinterpret_cast<uintptr_t>(d_k) | reinterpret_cast<uintptr_t>(d_v) |
                    reinterpret_cast<uintptr_t>(d_out) | reinterpret_cast<uintptr_t>(d_workspace);
-  for (int i = 0; i < 3; ++i) bits |= (uintptr_t)(a.ts[i] * es) | (uintptr_t)(a.hs[i] * es);
-  if ((bits & 15) != 0) return MTP_ERR_BAD_ARG;
+  for (int i = 0; i < 3; ++i) {
+    const long long heads = i == 0 ? n_q : n_kv;
+    // (the bf16 kernel's copies want strides above 0 and below 2^40 bytes; the same for both types)
+    if (tokens > 1 && (a.ts[i] <= 0 || a.ts[i] >= (1LL << 40) / es)) return MTP_ERR_BAD_ARG;
+    if (heads > 1 && (a.hs[i] <= 0 || a.hs[i] >= (1LL << 40) / es)) return MTP_ERR_BAD_ARG;
+    bits |= (uintptr_t)a.ts[i] * es | (uintptr_t)a.hs[i] * es;
+  }
+  if ((bits & 15) != 0 || ((reinterpret_cast<uintptr_t>(d_lse) | reinterpret_cast<uintptr_t>(d_start)) & 3) != 0) return MTP_ERR_BAD_ARG;
   // an output over an input would be read after it is written
+  const size_t n_out = (size_t)tokens * n_q * head_dim * es, n_lse = (size_t)tokens * n_q * 4, n_start = (size_t)(rows + 1) * 4;
   const void* in[3] = {d_q, d_k, d_v};
   for (int i = 0; i < 3; ++i) {
-    long long lo = 0, hi = head_dim;
-    for (const long long far : {(tokens - 1) * a.ts[i], ((i == 0 ? n_q : n_kv) - 1) * a.hs[i]}) {
-      lo += std::min(far, 0LL);
-      hi += std::max(far, 0LL);
-    }
-    const uint8_t *p = static_cast<const uint8_t*>(in[i]) + lo * es, *q = static_cast<const uint8_t*>(in[i]) + hi * es;
-    const uint8_t *o = static_cast<const uint8_t*>(d_out), *z = reinterpret_cast<const uint8_t*>(d_lse);
-    if (o < q && p < o + (size_t)tokens * n_q * head_dim * es) return MTP_ERR_BAD_ARG;
-    if (z && z < q && p < z + (size_t)tokens * n_q * 4) return MTP_ERR_BAD_ARG;
+    Bytes x;
+    if (!rows_range(in[i], tokens, a.ts[i], i == 0 ? n_q : n_kv, a.hs[i], head_dim, es, x) || cross(d_out, n_out, x.at, x.size) ||
+        cross(d_lse, n_lse, x.at, x.size))
+      return MTP_ERR_BAD_ARG;
   }
+  if (cross(d_out, n_out, d_start, n_start) || cross(d_lse, n_lse, d_start, n_start) || cross(d_out, n_out, d_lse, n_lse))
+    return MTP_ERR_BAD_ARG;
   cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
   cudaError_t e;
   if (dtype == MTP_DTYPE_BF16) e = launch_prompt_tc(a, head_dim, s);

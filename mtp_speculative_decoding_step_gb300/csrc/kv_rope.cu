@@ -42,6 +42,7 @@
 
 #include "common.cuh"
 #include "kernels.h"
+#include "ranges.h"
 #include "q4.cuh"
 
 namespace mtp {
@@ -752,12 +753,6 @@ __global__ void __launch_bounds__(kRopeThreads) k_rope_any(const __grid_constant
   }
 }
 
-// Whether two ranges of bytes meet without being the same.
-bool cross(const void* a, size_t na, const void* b, size_t nb) {
-  const uint8_t *p = static_cast<const uint8_t*>(a), *q = static_cast<const uint8_t*>(b);
-  return p && q && p < q + nb && q < p + na;
-}
-
 }  // namespace
 }  // namespace mtp
 
@@ -810,20 +805,19 @@ mtp_status kv_q4_append_rope(mtp_stream stream, const kv_q4_cache* c, int32_t to
   const int heads[3] = {n_q, c->n_kv, c->n_kv};
   const void* out[2] = {d_q_out, d_k_out};
   for (int o = 0; o < 2; ++o) {
-    const size_t bytes = (size_t)tokens * heads[o] * dh * es;
+    const size_t bytes = (size_t)tokens * heads[o] * dh * es, index = (size_t)tokens * 4, norm = (size_t)dh * 4;
+    if (cross(out[o], bytes, d_pos, index) || cross(out[o], bytes, d_slot, index) || cross(out[o], bytes, d_q_norm, norm) ||
+        cross(out[o], bytes, d_k_norm, norm))
+      return MTP_ERR_BAD_ARG;
     for (int i = 0; i < 3; ++i) {
       if (!out[o] || (i == o && in[i] == out[o] && (tokens == 1 || a.ts[i] == (long long)heads[i] * dh) && (heads[i] == 1 || a.hs[i] == dh))) continue;
-      long long lo = 0, hi = dh;  // the input's range of elements (strides may be negative)
-      for (const long long far : {(tokens - 1) * a.ts[i], (heads[i] - 1) * a.hs[i]}) {
-        lo += std::min(far, 0LL);
-        hi += std::max(far, 0LL);
-      }
-      if (cross(out[o], bytes, static_cast<const uint8_t*>(in[i]) + lo * es, (size_t)(hi - lo) * es)) return MTP_ERR_BAD_ARG;
+      Bytes x;
+      if (!rows_range(in[i], tokens, a.ts[i], heads[i], a.hs[i], dh, es, x) || cross(out[o], bytes, x.at, x.size)) return MTP_ERR_BAD_ARG;
     }
   }
   if (cross(d_q_out, (size_t)tokens * n_q * dh * es, d_k_out, d_k_out ? (size_t)tokens * c->n_kv * dh * es : 0)) return MTP_ERR_BAD_ARG;
   uintptr_t align = bits(d_q) | bits(d_k) | bits(d_v);
-  for (int i = 0; i < 3; ++i) align |= (uintptr_t)(a.ts[i] * es) | (uintptr_t)(a.hs[i] * es);
+  for (int i = 0; i < 3; ++i) align |= (uintptr_t)a.ts[i] * es | (uintptr_t)a.hs[i] * es;
   const bool fast = rope->rot_dim % 32 == 0 && (align & (4 * es - 1)) == 0;
   cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
   void (*k)(RopeArgs);

@@ -51,7 +51,10 @@ def _rope_args(**kw):
                                 dict(q_norm=FAKE + 4), dict(k_norm=FAKE + 8), dict(tokens=1 << 29),
                                 # overlaps: an output over another's input, over its own laid out otherwise, over the other output
                                 dict(q_out=2 * FAR), dict(k_out=3 * FAR), dict(q_out=FAR, qt=520), dict(q_out=FAR + 16), dict(k_out=5 * FAR + 64),
-                                dict(q=5 * FAR + 1024, qt=-512, q_out=5 * FAR)])
+                                dict(q=5 * FAR + 1024, qt=-512, q_out=5 * FAR),
+                                # over what says where rows go, over the norms; strides that no memory has
+                                dict(q_out=4 * FAR), dict(k_out=4 * FAR), dict(k_norm=6 * FAR), dict(q_norm=5 * FAR + 512),
+                                dict(qt=1 << 62), dict(kh=-(1 << 61)), dict(tokens=3, vt=(1 << 63) - 4)])
 def test_append_rope_refuses(L, kw):
     assert L.kv_q4_append_rope(*_rope_args(**kw)) == BAD
 
@@ -167,7 +170,11 @@ def _prompt_args(**kw):
                                 dict(tokens=-1), dict(tokens=1 << 29), dict(q=None), dict(k=None), dict(v=None), dict(start=None), dict(out=None),
                                 dict(ws=None), dict(dtype=2), dict(max_len=0), dict(scale=math.nan), dict(window=-1), dict(q=FAR + 8),
                                 dict(k=2 * FAR + 2), dict(qt=516), dict(vh=132), dict(out=5 * FAR + 8), dict(ws=7 * FAR + 8), dict(out=FAR),
-                                dict(out=2 * FAR + 512), dict(lse=3 * FAR), dict(q=5 * FAR + 9 * 1024, qt=-512)])
+                                dict(out=2 * FAR + 512), dict(lse=3 * FAR), dict(q=5 * FAR + 9 * 1024, qt=-512),
+                                # strides that the copies do not take, in either type
+                                dict(qt=0), dict(kh=0), dict(vt=-256), dict(kt=0, dtype=0), dict(vh=-128, dtype=0), dict(qt=1 << 39), dict(kt=1 << 38, dtype=0),
+                                dict(vt=1 << 62), dict(lse=6 * FAR + 2), dict(start=FAKE + 1), dict(out=FAKE - 1024), dict(lse=FAKE),
+                                dict(lse=5 * FAR + 64)])
 def test_prompt_refuses(L, kw):
     assert L.kv_attend_prompt(*_prompt_args(**kw)) == BAD
 
