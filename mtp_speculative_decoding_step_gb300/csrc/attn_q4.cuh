@@ -787,19 +787,19 @@ __global__ void __launch_bounds__(kAttnThreads, 1) k_q4_attn(const __grid_consta
       const bool begins = s.flags & 1, ends = s.flags & 2;
       // ---- queries: eight lanes per row, scaled by a power of two to [2^13, 2^14)
       const int kexp = head_exp(a.k_exp, s.g);
-#pragma unroll 1
-      for (int j0 = 4 * quarter; j0 < (NC + 15) / 16 * 16; j0 += 16) {
-        const int j = c0 + j0 + (lane >> 3), d0 = (lane & 7) * 8;  // its elements: d0 + 64 k .. + 7
-        const bool mine = j0 + (lane >> 3) < NC;
-        const int f = s.j * S::RT + j, i = f / G, h = s.g * G + f % G;
-        const bool real = mine && f < s.n * G;
-        const long long at = (long long)(s.a0 + i) * a.ts + (long long)h * a.hs + d0;
-        float x[DH / 8];
+      // all rows' loads first: one trip to memory a share, not one for every 16 rows (PLACEHOLDER)
+      constexpr int kTurns = (NC + 15) / 16, kWords = WIDE ? 8 : 4;
+      uint32_t raw[kTurns][DH / 64][kWords];
+#pragma unroll
+      for (int turn = 0; turn < kTurns; ++turn) {
+        const int j0 = 4 * quarter + 16 * turn + (lane >> 3), f = s.j * S::RT + c0 + j0, i = f / G, h = s.g * G + f % G;
+        const bool real = j0 < NC && f < s.n * G;
+        const long long at = (long long)(s.a0 + i) * a.ts + (long long)h * a.hs + (lane & 7) * 8;
 #pragma unroll
         for (int k = 0; k < DH / 64; ++k) {
-          uint32_t u[WIDE ? 8 : 4];
+          uint32_t(&u)[kWords] = raw[turn][k];
 #pragma unroll
-          for (int e = 0; e < (WIDE ? 8 : 4); ++e) u[e] = 0u;
+          for (int e = 0; e < kWords; ++e) u[e] = 0u;
           if (real) {
             const uint8_t* p = static_cast<const uint8_t*>(a.q) + (at + 64 * k) * (WIDE ? 4 : 2);
             if (a.q_vec) {
@@ -821,10 +821,39 @@ __global__ void __launch_bounds__(kAttnThreads, 1) k_q4_attn(const __grid_consta
                        ((uint32_t)reinterpret_cast<const uint16_t*>(p)[2 * e + 1] << 16);
             }
           }
+        }
+      }
+      if constexpr (TREE) {  // a thread per query row: its mask and its place
+        const int me = threadIdx.x & 127, f = s.j * S::RT + c0 + me, n = s.n;
+        if (me < NC) {
+          uint4 m = make_uint4(0u, 0u, 0u, 0u);
+          int lim = -1;
+          if (f < n * G) {
+            m = reinterpret_cast<const uint4*>(a.mask)[s.a0 + f / G];
+            lim = a.place ? min(max(a.place[s.a0 + f / G], s.pos), s.pos + n - 1) : s.pos + n - 1;
+            // bits of nodes that the row does not have
+            m.x &= n >= 32 ? ~0u : (1u << n) - 1;
+            m.y &= n >= 64 ? ~0u : (n > 32 ? (1u << (n - 32)) - 1 : 0u);
+            m.z &= n >= 96 ? ~0u : (n > 64 ? (1u << (n - 64)) - 1 : 0u);
+            m.w &= n >= 128 ? ~0u : (n > 96 ? (1u << (n - 96)) - 1 : 0u);
+          }
+          tree[c0 + me] = m;
+          M.lim[c0 + me] = lim;
+        }
+      }
+#pragma unroll
+      for (int turn = 0; turn < kTurns; ++turn) {
+        const int j0 = 4 * quarter + 16 * turn, j = c0 + j0 + (lane >> 3);
+        const bool mine = j0 + (lane >> 3) < NC;
+        const int f = s.j * S::RT + j, i = f / G, h = s.g * G + f % G;
+        const bool real = mine && f < s.n * G;
+        float x[DH / 8];
+#pragma unroll
+        for (int k = 0; k < DH / 64; ++k)
 #pragma unroll
           for (int e = 0; e < 8; ++e)
-            x[8 * k + e] = WIDE ? __uint_as_float(u[WIDE ? e : 0]) : ((e & 1) ? bf16hi(u[e / 2]) : bf16lo(u[e / 2]));
-        }
+            x[8 * k + e] = WIDE ? __uint_as_float(raw[turn][k][WIDE ? e : 0])
+                                : ((e & 1) ? bf16hi(raw[turn][k][e / 2]) : bf16lo(raw[turn][k][e / 2]));
         float mx = 0.f;
 #pragma unroll
         for (int e = 0; e < DH / 8; ++e) mx = fmaxf(mx, fabsf(x[e]));
@@ -854,21 +883,7 @@ __global__ void __launch_bounds__(kAttnThreads, 1) k_q4_attn(const __grid_consta
           if ((lane & 7) == 0) {
             M.cm[j][0] = ldexpf(a.scale * 1.44269504f, kexp - (13 - ex));
             M.cm[j][1] = kUnset;
-            M.lim[j] = real ? s.pos + i : -1;
-            if constexpr (TREE) {
-              uint4 m = make_uint4(0u, 0u, 0u, 0u);
-              if (real) {
-                m = reinterpret_cast<const uint4*>(a.mask)[s.a0 + i];
-                // bits of nodes that the row does not have
-                const int n = s.n;
-                m.x &= n >= 32 ? ~0u : (1u << n) - 1;
-                m.y &= n >= 64 ? ~0u : (n > 32 ? (1u << (n - 32)) - 1 : 0u);
-                m.z &= n >= 96 ? ~0u : (n > 64 ? (1u << (n - 64)) - 1 : 0u);
-                m.w &= n >= 128 ? ~0u : (n > 96 ? (1u << (n - 96)) - 1 : 0u);
-                M.lim[j] = a.place ? min(max(a.place[s.a0 + i], s.pos), s.pos + n - 1) : s.pos + n - 1;
-              }
-              tree[j] = m;
-            }
+            if (!TREE) M.lim[j] = real ? s.pos + i : -1;
             M.dst[j] = real ? (s.a0 + i) * a.n_q + h : -1;
           }
         }
