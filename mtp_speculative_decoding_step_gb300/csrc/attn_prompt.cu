@@ -20,14 +20,16 @@ namespace {
 
 // ------------------------------------------------------------ CUDA cores
 
-constexpr int kSimtRows = 64, kSimtThreads = 256;
+constexpr int kSimtThreads = 256;
 
-template <int DH>
+// R: queries of a thread.
+template <int DH, int R>
 struct Simt {
+  static constexpr int kRows = 16 * R;  // queries of a block
   static constexpr int kKeys = DH == 256 ? 32 : 64;  // of a tile; two tiles of K and V fit
   static constexpr int kS = DH + 4, kPS = kKeys + 4;  // strides of rows, of P's
   static constexpr int kTile = kKeys * kS;
-  static constexpr int kSmem = (kSimtRows * kS + 4 * kTile + kSimtRows * kPS) * 4;
+  static constexpr int kSmem = (kRows * kS + 4 * kTile + kRows * kPS) * 4;
   static_assert(kSmem <= 227 * 1024, "shared memory");
 };
 
@@ -36,23 +38,23 @@ __device__ __forceinline__ void copy16(float* dst, const float* src, bool some) 
   asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(smem_u32(dst)), "l"(src), "r"(some ? 16 : 0) : "memory");
 }
 
-// 64 queries of a head against 32 or 64 keys at a time, all in fp32; the next tile of K and V is copied meanwhile. Thread
-// (ty, tx) of 16 x 16 has the scores of 4 queries with kKeys / 16 keys, then 4 queries' outputs in DH / 16 dimensions: 8
-// loads of 16 bytes from shared memory per 64 products, which bound it. 1024 positions of 24 heads of 256: 440 us, 29
-// TFLOP/s; 3 rows of up to 131 of 4 heads of 64: 18 us, three tiles one after another.
-template <int DH>
+// 16 R queries of a head against 32 or 64 keys at a time, all in fp32; the next tile of K and V is copied meanwhile. Thread
+// (ty, tx) of 16 x 16 has the scores of R queries with kKeys / 16 keys, then R queries' outputs in DH / 16 dimensions: 8
+// loads of 16 bytes from shared memory per 64 products with 4 queries, which bound it. 1024 positions of 24 heads of 256: 440
+// us, 29 TFLOP/s.
+template <int DH, int R>
 __global__ void __launch_bounds__(kSimtThreads) k_prompt_simt(const __grid_constant__ PromptArgs a) {
-  using S = Simt<DH>;
+  using S = Simt<DH, R>;
   constexpr int kD = DH / 64, kB = S::kKeys / 16;
   extern __shared__ __align__(16) float smem[];
-  float *sq = smem, *skv = sq + kSimtRows * S::kS, *sp = skv + 4 * S::kTile;
+  float *sq = smem, *skv = sq + S::kRows * S::kS, *sp = skv + 4 * S::kTile;
   __shared__ int s_at[4];
   pdl_wait();
   pdl_trigger();
   const int tid = threadIdx.x, tx = tid & 15, ty = tid >> 4, h = blockIdx.x % a.n_q, g = h / (a.n_q / a.n_kv);
   if (tid < 32) {
     int a0 = 0, n = 0, j = 0;
-    const bool some = find_tile(a, 1, kSimtRows, blockIdx.x / a.n_q, a0, n, j);
+    const bool some = find_tile(a, 1, S::kRows, blockIdx.x / a.n_q, a0, n, j);
     if (tid == 0) {
       s_at[0] = a0;
       s_at[1] = some ? n : 0;
@@ -60,9 +62,9 @@ __global__ void __launch_bounds__(kSimtThreads) k_prompt_simt(const __grid_const
     }
   }
   __syncthreads();
-  const int a0 = s_at[0], n = s_at[1], i0 = s_at[2] * kSimtRows;
+  const int a0 = s_at[0], n = s_at[1], i0 = s_at[2] * S::kRows;
   if (n == 0) return;
-  const int rows = min(n - i0, kSimtRows);
+  const int rows = min(n - i0, S::kRows);
   auto stage = [&](float* dst, int side, const void* src, int head, int first, int count, int most) {
     for (int e = tid; e < most * (DH / 4); e += kSimtThreads) {
       const int r = e / (DH / 4), d = e % (DH / 4) * 4;
@@ -76,12 +78,12 @@ __global__ void __launch_bounds__(kSimtThreads) k_prompt_simt(const __grid_const
     stage(skv + (2 * buf + 1) * S::kTile, 2, a.v, g, t0, min(n - t0, S::kKeys), S::kKeys);
     asm volatile("cp.async.commit_group;" ::: "memory");
   };
-  stage(sq, 0, a.q, h, i0, rows, kSimtRows);
+  stage(sq, 0, a.q, h, i0, rows, S::kRows);
   keys(first, 0);
   const float c = a.scale * 1.44269504f;
-  float m[4], l[4], o[4][kD][4];
+  float m[R], l[R], o[R][kD][4];
 #pragma unroll
-  for (int r = 0; r < 4; ++r) {
+  for (int r = 0; r < R; ++r) {
     m[r] = -INFINITY;
     l[r] = 0.f;
 #pragma unroll
@@ -99,28 +101,28 @@ __global__ void __launch_bounds__(kSimtThreads) k_prompt_simt(const __grid_const
     }
     __syncthreads();
     const float *sk = skv + 2 * buf * S::kTile, *sv = sk + S::kTile;
-    float s[4][kB];
+    float s[R][kB];
 #pragma unroll
-    for (int r = 0; r < 4; ++r)
+    for (int r = 0; r < R; ++r)
 #pragma unroll
       for (int b = 0; b < kB; ++b) s[r][b] = 0.f;
 #pragma unroll 4
     for (int d = 0; d < DH; d += 4) {
-      float4 qv[4], kv[kB];
+      float4 qv[R], kv[kB];
 #pragma unroll
-      for (int r = 0; r < 4; ++r) qv[r] = *reinterpret_cast<const float4*>(sq + (4 * ty + r) * S::kS + d);
+      for (int r = 0; r < R; ++r) qv[r] = *reinterpret_cast<const float4*>(sq + (R * ty + r) * S::kS + d);
 #pragma unroll
       for (int b = 0; b < kB; ++b) kv[b] = *reinterpret_cast<const float4*>(sk + (tx + 16 * b) * S::kS + d);
 #pragma unroll
-      for (int r = 0; r < 4; ++r)
+      for (int r = 0; r < R; ++r)
 #pragma unroll
         for (int b = 0; b < kB; ++b)
           s[r][b] = fmaf(qv[r].x, kv[b].x, fmaf(qv[r].y, kv[b].y, fmaf(qv[r].z, kv[b].z, fmaf(qv[r].w, kv[b].w, s[r][b]))));
     }
-    const bool edge = t0 + S::kKeys > i0 + 1 || (a.window > 0 && t0 <= i0 + kSimtRows - 1 - a.window);
+    const bool edge = t0 + S::kKeys > i0 + 1 || (a.window > 0 && t0 <= i0 + S::kRows - 1 - a.window);
 #pragma unroll
-    for (int r = 0; r < 4; ++r) {
-      const int i = i0 + 4 * ty + r;
+    for (int r = 0; r < R; ++r) {
+      const int i = i0 + R * ty + r;
       bool gone[kB];
       float mx = -INFINITY;
 #pragma unroll
@@ -139,7 +141,7 @@ __global__ void __launch_bounds__(kSimtThreads) k_prompt_simt(const __grid_const
       for (int b = 0; b < kB; ++b) {
         const float p = exp2f(s[r][b] - from);
         if (!gone[b]) sum += p;
-        sp[(4 * ty + r) * S::kPS + tx + 16 * b] = gone[b] ? -1.f : p;  // (-1: out of sight, whatever V holds there)
+        sp[(R * ty + r) * S::kPS + tx + 16 * b] = gone[b] ? -1.f : p;  // (-1: out of sight, whatever V holds there)
       }
 #pragma unroll
       for (int w = 1; w < 16; w <<= 1) sum += __shfl_xor_sync(0xFFFFFFFFu, sum, w);
@@ -154,19 +156,19 @@ __global__ void __launch_bounds__(kSimtThreads) k_prompt_simt(const __grid_const
     auto add = [&](auto edges) {
 #pragma unroll 2
       for (int t = 0; t < S::kKeys; t += 4) {
-        float4 p[4];
+        float4 p[R];
 #pragma unroll
-        for (int r = 0; r < 4; ++r) p[r] = *reinterpret_cast<const float4*>(sp + (4 * ty + r) * S::kPS + t);
+        for (int r = 0; r < R; ++r) p[r] = *reinterpret_cast<const float4*>(sp + (R * ty + r) * S::kPS + t);
 #pragma unroll
         for (int u = 0; u < 4; ++u) {
-          float pu[4];
+          float pu[R];
 #pragma unroll
-          for (int r = 0; r < 4; ++r) pu[r] = u == 0 ? p[r].x : (u == 1 ? p[r].y : (u == 2 ? p[r].z : p[r].w));
+          for (int r = 0; r < R; ++r) pu[r] = u == 0 ? p[r].x : (u == 1 ? p[r].y : (u == 2 ? p[r].z : p[r].w));
 #pragma unroll
           for (int d = 0; d < kD; ++d) {
             const float4 v = *reinterpret_cast<const float4*>(sv + (t + u) * S::kS + 64 * d + 4 * tx);
 #pragma unroll
-            for (int r = 0; r < 4; ++r) {
+            for (int r = 0; r < R; ++r) {
               if (decltype(edges)::value && pu[r] < 0.f) continue;
               o[r][d][0] = fmaf(pu[r], v.x, o[r][d][0]);
               o[r][d][1] = fmaf(pu[r], v.y, o[r][d][1]);
@@ -182,8 +184,8 @@ __global__ void __launch_bounds__(kSimtThreads) k_prompt_simt(const __grid_const
     __syncthreads();  // (before the copies of the tile after the next)
   }
 #pragma unroll
-  for (int r = 0; r < 4; ++r) {
-    const int i = i0 + 4 * ty + r;
+  for (int r = 0; r < R; ++r) {
+    const int i = i0 + R * ty + r;
     if (i >= n) continue;
     const long long at = (long long)(a0 + i) * a.n_q + h;
     const float f = l[r] != 0.f ? 1.f / l[r] : 0.f;
@@ -209,15 +211,29 @@ cudaError_t raise_smem(K k, int bytes, bool (&set)[kMaxDevices], std::mutex& mu)
   return e;
 }
 
-template <int DH>
+template <int DH, int R>
 cudaError_t launch_simt(const PromptArgs& a, cudaStream_t s) {
+  using S = Simt<DH, R>;
   static std::mutex mu;
   static bool set[kMaxDevices] = {};
-  const cudaError_t e = raise_smem(k_prompt_simt<DH>, Simt<DH>::kSmem, set, mu);
+  const cudaError_t e = raise_smem(k_prompt_simt<DH, R>, S::kSmem, set, mu);
   if (e != cudaSuccess) return e;
   count_launch();
-  return launch_pdl(k_prompt_simt<DH>, dim3((unsigned)(prompt_most_tiles(a.tokens, a.rows, 1, kSimtRows) * a.n_q)),
-                    dim3(kSimtThreads), Simt<DH>::kSmem, s, a);
+  return launch_pdl(k_prompt_simt<DH, R>, dim3((unsigned)(prompt_most_tiles(a.tokens, a.rows, 1, S::kRows) * a.n_q)),
+                    dim3(kSimtThreads), S::kSmem, s, a);
+}
+
+// Small query tiles where there are few: the block with a row's last queries has all of its keys, one tile after another, and a
+// tile of keys takes it a third of the time with 16 queries that it takes with 64. With 64, 32 and 16 queries, in us: 3 rows of
+// 131 of 4 heads of 64 (108 blocks of 16) 17.9, 13.5, 11.3; 300 positions of 8 heads of 128 (152) 45.0, 35.9, 29.4; 64 of 24
+// heads of 256 (120) 22.0, 16.2, 14.1; 256 of those (408; 216 of 32) 76, 56, 74; 4 rows of 200 of 8 of 128 (432; 232) 36.9,
+// 37.9, 40.7; 8 rows of 256 of 4 of 64 (544; 288) 23.4, 26.7, 34.3. The outputs are the same bits.
+template <int DH>
+cudaError_t launch_simt(const PromptArgs& a, cudaStream_t s) {
+  auto blocks = [&](int tile) { return prompt_most_tiles(a.tokens, a.rows, 1, tile) * a.n_q; };
+  if (blocks(16) <= device_sm_count()) return launch_simt<DH, 1>(a, s);
+  if (2 * blocks(32) <= 3 * device_sm_count()) return launch_simt<DH, 2>(a, s);
+  return launch_simt<DH, 4>(a, s);
 }
 
 }  // namespace

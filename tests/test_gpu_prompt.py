@@ -88,6 +88,14 @@ def test_windows(nq, nkv, dh, dtype, window):
     check(make([600, 5, 129, 333], nq, nkv, dh, dtype, window % 1000), 1 / math.sqrt(dh), window)
 
 
+@pytest.mark.parametrize("n,nq,nkv,dh", [([131, 1, 70], 4, 2, 64), ([17, 90], 8, 2, 128), ([64, 300], 3, 3, 256),
+                                         ([700], 4, 2, 64), ([33, 367], 8, 2, 128), ([900], 3, 1, 256)])
+@pytest.mark.parametrize("window", [0, 50])
+def test_few_queries_take_small_tiles(n, nq, nkv, dh, window):
+    """fp32: tiles of 16 queries where those are no more than the SMs, of 32 where those are few."""
+    check(make(n, nq, nkv, dh, torch.float32, dh + len(n)), 1 / math.sqrt(dh), window)
+
+
 def test_one_token():
     for dtype in (torch.bfloat16, torch.float32):
         c = make([1], 4, 2, 64, dtype, 3)
