@@ -555,16 +555,18 @@ def kv_q4_append_rope(cache: PagedCache, q, k, v, rope: Rope, pos, slot, q_out, 
     [tokens] int32; q_out, k_out: contiguous like q and k (k_out optional); q_norm, k_norm [head_dim] float (None: no norm);
     rope: mtp_rope(...). See kv_q4_append_rope in include/mtp.h."""
     tokens, n_q, dh = q.shape
+    qs, ks, vs = q.stride(), k.stride(), v.stride()
     shape = (tokens, cache.n_kv, cache.head_dim)
-    _want(k.shape == shape and v.shape == shape and dh == cache.head_dim and q.stride(2) == 1 and k.stride(2) == 1
-          and v.stride(2) == 1 and q_out.shape == q.shape and q_out.is_contiguous()
+    _want(k.shape == shape and v.shape == shape and dh == cache.head_dim and qs[2] == 1 and ks[2] == 1
+          and vs[2] == 1 and q_out.shape == q.shape and q_out.is_contiguous()
           and (k_out is None or (k_out.shape == shape and k_out.is_contiguous())), "kv_q4_append_rope")
     _whole("kv_q4_append_rope", pos, slot, n=tokens)
     _f32("kv_q4_append_rope", q_norm, k_norm, n=dh)
     dt = _dtype_q4("kv_q4_append_rope", q, k, v, q_out) if k_out is None else _dtype_q4("kv_q4_append_rope", q, k, v, q_out, k_out)
-    rc = lib().kv_q4_append_rope(_stream(stream), cache.ref, tokens, n_q, _ptr(q), q.stride(0), q.stride(1), _ptr(k),
-                                 k.stride(0), k.stride(1), _ptr(v), v.stride(0), v.stride(1), dt, _ptr(q_norm), _ptr(k_norm),
-                                 eps, ctypes.byref(rope), _ptr(pos), _ptr(slot), _ptr(q_out), _ptr(k_out), _ptr(status))
+    rc = lib().kv_q4_append_rope(_stream(stream), cache.ref, tokens, n_q, q.data_ptr(), qs[0], qs[1], k.data_ptr(),
+                                 ks[0], ks[1], v.data_ptr(), vs[0], vs[1], dt, _ptr(q_norm), _ptr(k_norm),
+                                 eps, ctypes.byref(rope), _ptr(pos), _ptr(slot), q_out.data_ptr(), _ptr(k_out),
+                                 _ptr(status))
     _check(rc, "kv_q4_append_rope")
 
 
@@ -576,7 +578,7 @@ def kv_tree_plan(parent, start, length, pos, mask, window: int = 0, status=None,
     _whole("kv_tree_plan", mask, n=tokens * (MTP_TREE_MAX // 32))
     _whole("kv_tree_plan", start, n=rows + 1)
     _whole("kv_tree_plan", length)
-    rc = lib().kv_tree_plan(_stream(stream), rows, tokens, _ptr(parent), _ptr(start), _ptr(length), window, _ptr(pos),
+    rc = lib().kv_tree_plan(_stream(stream), rows, tokens, parent.data_ptr(), _ptr(start), length.data_ptr(), window, _ptr(pos),
                             _ptr(mask), _ptr(status))
     _check(rc, "kv_tree_plan")
 
@@ -586,8 +588,9 @@ def kv_q4_attend_tree(cache: PagedCache, q, table, start, length, mask, out, wor
     """kv_q4_attend for trees: mask [tokens, MTP_TREE_MAX / 32] and pos [tokens] (with a window) int32, kv_tree_plan's;
     the other arguments as there."""
     tokens, n_q, dh = q.shape
+    qs = q.stride()
     rows, max_pages = table.shape
-    _want(dh == cache.head_dim and q.stride(2) == 1 and out.shape == q.shape and out.is_contiguous(), "kv_q4_attend_tree")
+    _want(dh == cache.head_dim and qs[2] == 1 and out.shape == q.shape and out.is_contiguous(), "kv_q4_attend_tree")
     _f32("kv_q4_attend_tree", lse, n=tokens * n_q)
     _whole("kv_q4_attend_tree", table)
     _whole("kv_q4_attend_tree", start, n=rows + 1)
@@ -596,9 +599,9 @@ def kv_q4_attend_tree(cache: PagedCache, q, table, start, length, mask, out, wor
     _whole("kv_q4_attend_tree", pos, n=tokens)
     dt = _dtype_q4("kv_q4_attend_tree", q, out)
     _want(workspace.nbytes >= _attend_bytes(_device(), cache.n_kv, dh, n_q, max_q, dt), "kv_q4_attend_tree")
-    rc = lib().kv_q4_attend_tree(_stream(stream), cache.ref, rows, n_q, tokens, _ptr(q), q.stride(0), q.stride(1), dt,
-                                 _ptr(table), max_pages, _ptr(start), _ptr(length), _ptr(mask), _ptr(pos), max_q, scale,
-                                 window, _ptr(out), _ptr(lse), _ptr(status), _ptr(workspace))
+    rc = lib().kv_q4_attend_tree(_stream(stream), cache.ref, rows, n_q, tokens, q.data_ptr(), qs[0], qs[1], dt,
+                                 table.data_ptr(), max_pages, _ptr(start), _ptr(length), _ptr(mask), _ptr(pos), max_q, scale,
+                                 window, out.data_ptr(), _ptr(lse), _ptr(status), workspace.data_ptr())
     _check(rc, "kv_q4_attend_tree")
 
 
@@ -629,8 +632,8 @@ def kv_q4_tree_commit(caches: PagedCaches, table, start, length, parent, tok, ch
     _whole("kv_q4_tree_commit", parent, tok, choice, n=tokens)
     _whole("kv_q4_tree_commit", path, n=rows * max_path)
     rc = lib().kv_q4_tree_commit(_stream(stream), caches.c, caches.n, rows, tokens, _ptr(table), max_pages, _ptr(start),
-                                 _ptr(length), _ptr(parent), _ptr(tok), _ptr(choice), max_path, _ptr(n_acc), _ptr(out_tok),
-                                 _ptr(keep), _ptr(path), _ptr(status))
+                                 _ptr(length), parent.data_ptr(), _ptr(tok), _ptr(choice), max_path, _ptr(n_acc),
+                                 out_tok.data_ptr(), _ptr(keep), _ptr(path), _ptr(status))
     _check(rc, "kv_q4_tree_commit")
 
 
@@ -644,16 +647,17 @@ def kv_attend_prompt(q, k, v, start, out, workspace, max_len: int, scale: float,
     rows; start [rows + 1] int32; out like q, contiguous; lse [tokens, n_q] float; workspace:
     kv_attend_prompt_workspace_bytes(tokens, rows) bytes. See kv_attend_prompt in include/mtp.h."""
     tokens, n_q, dh = q.shape
+    qs, ks, vs = q.stride(), k.stride(), v.stride()
     rows, n_kv = start.numel() - 1, k.shape[1]
-    _want(k.shape == (tokens, n_kv, dh) and v.shape == k.shape and q.stride(2) == 1 and k.stride(2) == 1 and v.stride(2) == 1
+    _want(k.shape == (tokens, n_kv, dh) and v.shape == k.shape and qs[2] == 1 and ks[2] == 1 and vs[2] == 1
           and out.shape == q.shape and out.is_contiguous(), "kv_attend_prompt")
     _f32("kv_attend_prompt", lse, n=tokens * n_q)
     _whole("kv_attend_prompt", start)
     dt = _dtype_q4("kv_attend_prompt", q, k, v, out)
     _want(workspace.nbytes >= _prompt_bytes(tokens, rows), "kv_attend_prompt")
-    rc = lib().kv_attend_prompt(_stream(stream), rows, n_q, n_kv, dh, tokens, _ptr(q), q.stride(0), q.stride(1), _ptr(k),
-                                k.stride(0), k.stride(1), _ptr(v), v.stride(0), v.stride(1), dt, _ptr(start), max_len, scale,
-                                window, _ptr(out), _ptr(lse), _ptr(status), _ptr(workspace))
+    rc = lib().kv_attend_prompt(_stream(stream), rows, n_q, n_kv, dh, tokens, q.data_ptr(), qs[0], qs[1], k.data_ptr(),
+                                ks[0], ks[1], v.data_ptr(), vs[0], vs[1], dt, start.data_ptr(), max_len, scale,
+                                window, out.data_ptr(), _ptr(lse), _ptr(status), workspace.data_ptr())
     _check(rc, "kv_attend_prompt")
 
 
