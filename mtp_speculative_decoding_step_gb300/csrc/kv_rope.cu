@@ -753,6 +753,18 @@ __global__ void __launch_bounds__(kRopeThreads) k_rope_any(const __grid_constant
   }
 }
 
+// cos(2 pi i / 64) in two floats, made once.
+struct Quarter {
+  float2 c[17];
+  Quarter() {
+    for (int i = 0; i <= 16; ++i) {
+      const double x = i < 16 ? std::cos(i * (6.283185307179586476925286766559 / 64)) : 0.0;
+      c[i].x = (float)x;
+      c[i].y = (float)(x - c[i].x);
+    }
+  }
+};
+
 }  // namespace
 }  // namespace mtp
 
@@ -795,11 +807,8 @@ mtp_status kv_q4_append_rope(mtp_stream stream, const kv_q4_cache* c, int32_t to
              d_q_out, d_k_out, {d_q_norm, d_k_norm}, {static_cast<uint8_t*>(c->k), static_cast<uint8_t*>(c->v)},
              {c->k_exp, c->v_exp}, d_pos, d_slot, d_status, tokens, n_q, c->n_kv, c->page, c->n_pages * c->page, 1, 1, eps, {},
              *rope};
-  for (int i = 0; i <= 16; ++i) {
-    const double x = i < 16 ? std::cos(i * (6.283185307179586476925286766559 / 64)) : 0.0;
-    a.quarter[i].x = (float)x;
-    a.quarter[i].y = (float)(x - a.quarter[i].x);
-  }
+  static const Quarter quarter;
+  std::copy(quarter.c, quarter.c + 17, a.quarter);
   // an output may be its own input, laid out the same; any other overlap would be read after it is written
   const void* in[3] = {d_q, d_k, d_v};
   const int heads[3] = {n_q, c->n_kv, c->n_kv};
