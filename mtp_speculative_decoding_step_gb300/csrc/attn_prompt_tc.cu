@@ -73,6 +73,15 @@ __device__ __forceinline__ void fma2(float& x, float& y, float c, float d) {
       : "+f"(x), "+f"(y)
       : "f"(c), "f"(d));
 }
+__device__ __forceinline__ void mul2(float& x, float& y, float c) {
+  asm("{\n\t.reg .b64 s, t;\n\t"
+      "mov.b64 s, {%0, %1};\n\t"
+      "mov.b64 t, {%2, %2};\n\t"
+      "mul.rn.f32x2 s, s, t;\n\t"
+      "mov.b64 {%0, %1}, s;\n\t}"
+      : "+f"(x), "+f"(y)
+      : "f"(c));
+}
 __device__ __forceinline__ void add2(float& x, float& y, float u, float v) {
   asm("{\n\t.reg .b64 s, t;\n\t"
       "mov.b64 s, {%0, %1};\n\t"
@@ -788,15 +797,7 @@ __global__ void __launch_bounds__(kPromptThreads, 1)
         m = top;
         c0 = slot * kDims;
       }
-      if (ok) {
-        // (the phase before is over: S of the last item, which this group or the other one has seen, came behind that P.V)
-        const int last = items - 1;
-        ok = S::QT == 2 ? ready(&M.pv_done[slot], i & 1) : ready(&M.pv_done[last & 1], (done[last & 1] + (last >> 1)) & 1);
-        tc_fence_after();
-      }
-      done[0] += (items + 1) / 2;
-      done[1] += items / 2;
-      if (!ok) break;
+      // (beside the last product: what the rows' sums give does not wait for it)
       const float r = l != 0.f ? 1.f / l : 0.f;
       const long long dst = real ? (long long)(u.a0 + pos) * a.n_q + u.grp * G + in_head : -1;
       if (real && a.lse && c0 == 0) a.lse[dst] = l != 0.f ? (m + log2f(l)) * 0.693147181f : -INFINITY;
@@ -808,7 +809,17 @@ __global__ void __launch_bounds__(kPromptThreads, 1)
         rr[y] = __shfl_sync(0xFFFFFFFFu, r, (lane >> 2) + 8 * y);
         to[y] = __shfl_sync(0xFFFFFFFFu, dst, (lane >> 2) + 8 * y);
       }
-      const int nan = *reinterpret_cast<volatile int*>(&M.nan[i % kUnits]) == i + 1;
+      if (ok) {
+        // (the phase before is over: S of the last item, which this group or the other one has seen, came behind that P.V)
+        const int last = items - 1;
+        ok = S::QT == 2 ? ready(&M.pv_done[slot], i & 1) : ready(&M.pv_done[last & 1], (done[last & 1] + (last >> 1)) & 1);
+        tc_fence_after();
+      }
+      done[0] += (items + 1) / 2;
+      done[1] += items / 2;
+      if (!ok) break;
+      // (or a row that nothing weighs in: its products may be 0 times NaN)
+      const bool nan = *reinterpret_cast<volatile int*>(&M.nan[i % kUnits]) == i + 1 || __any_sync(0xFFFFFFFFu, r == 0.f && dst >= 0);
       auto put = [&](auto slow) {
 #pragma unroll 1
         for (int d = c0; d < c0 + kDims; d += 64) {
@@ -839,9 +850,11 @@ __global__ void __launch_bounds__(kPromptThreads, 1)
 #pragma unroll
               for (int e = 0; e < 2; ++e) {
                 x[e] = __uint_as_float(o[y >> 1][b >> 2][4 * (b & 3) + 2 * (y & 1) + e]);
+                if (!decltype(slow)::value) continue;
                 x[e] = rr[y] != 0.f ? x[e] * rr[y] : 0.f;
-                if (decltype(slow)::value) x[e] = add_cleaned(a, u, sp.p0, sp.p1, to[y], d + 8 * b + 2 * (lane & 3) + e, x[e]);
+                x[e] = add_cleaned(a, u, sp.p0, sp.p1, to[y], d + 8 * b + 2 * (lane & 3) + e, x[e]);
               }
+              if (!decltype(slow)::value) mul2(x[0], x[1], rr[y]);
               w[b] = pack_bf16(x[0], x[1]);
             }
             transpose4(w, lane);
