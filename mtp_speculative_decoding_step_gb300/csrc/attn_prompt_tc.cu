@@ -26,12 +26,13 @@
 // rows they are. Every wait is bounded: on expiry the block raises the status
 // word, waits for its copies, frees its tensor memory and returns.
 //
-// What it measured: 8192 positions of 24 heads on 4 of 256 476 us, 1.73 PFLOP/s; of 32 on 8 of 128 316 us, 1.74 PFLOP/s; of
-// 32 on 4 of 64 290 us, 0.95 PFLOP/s. The tensor pipe is active 75 % (256 dimensions), shared memory 79 % on its side: S
+// What it measured: 8192 positions of 24 heads on 4 of 256 471 us, 1.75 PFLOP/s; of 32 on 8 of 128 316 us, 1.74 PFLOP/s; of
+// 32 on 4 of 64 278 us, 0.99 PFLOP/s. The tensor pipe is active 75 % (256 dimensions), shared memory 79 % on its side: S
 // reads 8 KB an MMA of 64 cycles and the copies write as much again. With 64 dimensions the softmax is longer than the
-// products. Short prompts are bound by a unit's beginning and end, some 4 us: the last product's wait, O's way out (3800
-// cycles) and the first softmax have no product beside them; 32 rows of 512 positions of 24 heads of 256 take 176 us (0.59
-// PFLOP/s), 32 rows of 1 to 2047 of 8 heads on 2 of 128 92 us (1.02).
+// products. Short prompts wait on one query tile's chain: with 512 positions of 128 dimensions a unit is 18,500 cycles, of
+// which the MMAs take 5300; the softmax of its 2.6 items 6700, waits for S between them 2500, the first S 1500, the last
+// product 1000, O's way out 4000. 32 rows of those take 104 us (0.66 PFLOP/s), of 24 heads of 256 166 us (0.62), 32 rows of
+// 1 to 2047 of 8 heads on 2 of 128 92 us (1.02).
 #include <algorithm>
 #include <cfloat>
 #include <mutex>

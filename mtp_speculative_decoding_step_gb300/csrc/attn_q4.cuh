@@ -58,8 +58,10 @@
 //
 // Trees (TREE, kv_q4_attend_tree): the queries are the nodes of a tree at a row's last positions. The tiles that hold them
 // are edges, where a query's sight is a bit of its mask; everything before is the same. 8 rows of 20 to 33 nodes, 1k to 16k
-// positions: 127 us, 392 TFLOP/s: a block has 29 tiles of 128 columns at some 4600 cycles and two or three shares, whose
-// starts, drains (128 KB of O each) and join are the other half. One row of 16 nodes at 4096 positions: 27 us.
+// positions: 123 us, 405 TFLOP/s. A block has 30 tiles of 128 columns at some 5000 cycles, of which the softmax is busy 3400
+// (S read, scaled and voted on 1840, weights 750, P^T stored 500), K and V are expanded in 3100 and the MMAs take 2050; a
+// move of the maxima costs 9000 more, one to four a share; a share's start and first maxima are 15,000, the join 10 us.
+// One row of 16 nodes at 4096 positions: 25 us, the join 6 of them.
 //
 // fp32 queries: q and the weights each enter as two f16 parts in separate
 // columns (22 bits), N / 2 rows a tile.
