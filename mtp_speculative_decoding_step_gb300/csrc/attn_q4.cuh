@@ -39,7 +39,7 @@
 //     The tensor pipe is active 47 %, the issue slots 42 %: neither is full. With
 //     128 columns tensor memory has room for one S and one K, so that expansion,
 //     S, softmax and P.V of a block take turns
-//   8 rows of 4 queries, 1k to 16k positions: 38 us, 2.3 TB/s. A block has 15.4
+//   8 rows of 4 queries, 1k to 16k positions: 36 us, 2.4 TB/s. A block has 15.4
 //     tiles of 2450 cycles, 20 us (1900 of the 2450 are shared-memory traffic: raw
 //     rows in and out, V's f16 tile written by threads and read by the MMA, P);
 //     the rest is a share's start, its drain of O and the join, not told apart
