@@ -499,7 +499,8 @@ mtp_status mtp_rope_init(int32_t rot_dim, double theta, const double* h_freq, mt
  *   d_pos, d_slot [tokens]: a position below 0 is padding: its rows of the outputs
  *       are zeros and nothing is appended. d_slot -1 appends nothing; any other
  *       slot outside the cache, or a slot beside a position below 0, sets
- *       1 << MTP_ERR_BAD_ARG in d_status and appends nothing.
+ *       1 << MTP_ERR_BAD_ARG in d_status and appends nothing. Two positions with
+ *       the same slot leave bytes of both.
  *   d_q_out [tokens][n_q][head_dim], d_k_out [tokens][n_kv][head_dim] (optional)
  *       contiguous in dtype, 16-byte aligned. Each may be its own input where that
  *       is contiguous; any other overlap is refused.
@@ -571,13 +572,14 @@ mtp_status kv_q4_attend_tree(mtp_stream stream, const kv_q4_cache* cache, int32_
  *       path (the accepted drafts, then the target's own), then -1
  *   d_path [rows][max_path] out (optional): the path's nodes, then -1
  *   d_keep [rows] out: len - n + path length, kv_page_plan's d_keep
- * The cached rows of path node k go to place k, position len - n + k. Moves
- * whose table entry is no page are left out and set 1 << MTP_ERR_BAD_ARG in
- * d_status, as does a parent that is not below its node (which then is nobody's
- * child); rows with too many nodes, or len outside [n, max_pages * page], also set
- * it, move nothing, have no path and keep len. A second call on the same
- * tree would move rows that have moved. Errors: BAD_ARG (rows outside 1..4096,
- * max_path outside 1..MTP_TREE_MAX, a null pointer, overlapping outputs).
+ * The cached rows of path node k go to place k, position len - n + k; no other
+ * row's table may name those pages. Moves whose table entry is no page are
+ * left out and set 1 << MTP_ERR_BAD_ARG in d_status, as does a parent that is
+ * not below its node (which then is nobody's child); rows with too many nodes,
+ * or len outside [n, max_pages * page], also set it, move nothing, have no
+ * path and keep len. A second call on the same tree would move rows that have
+ * moved. Errors: BAD_ARG (rows outside 1..4096, max_path outside
+ * 1..MTP_TREE_MAX, a null pointer, overlapping outputs).
  */
 mtp_status kv_q4_tree_commit(mtp_stream stream, const kv_q4_cache* caches, int32_t n_caches, int32_t rows,
                              int32_t tokens, const int32_t* d_table, int32_t max_pages, const int32_t* d_start,

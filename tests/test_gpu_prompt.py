@@ -199,6 +199,33 @@ def test_separate_and_padded_tensors_streams_and_graphs():
         assert torch.equal(out.cpu(), want)
 
 
+@pytest.mark.parametrize("nq,nkv,dh", [(256, 1, 64), (125, 1, 128), (129, 1, 64), (1021, 1, 64), (1024, 8, 256)])
+@pytest.mark.parametrize("dtype", [torch.bfloat16, torch.float32])
+def test_many_heads_to_a_kv_head(nq, nkv, dh, dtype):
+    """More than a query tile holds (parts of them that divide their number), one head at a time where that is prime."""
+    check(make([3, 0, 34], nq, nkv, dh, dtype, nq), 1 / math.sqrt(dh))
+
+
+@pytest.mark.parametrize("nq,nkv,dh", HEADS[:3])
+def test_two_calls_at_once(nq, nkv, dh):
+    """On two streams, one workspace between them."""
+    cs = [make([900, 5, 300], nq, nkv, dh, torch.bfloat16, 41), make([31, 700], nq, nkv, dh, torch.bfloat16, 42)]
+    want = [check(c, 0.08)[0] for c in cs]
+    ws = torch.empty(m.kv_attend_prompt_workspace_bytes(2000, 3), dtype=torch.uint8, device="cuda")
+    args = []
+    for c in cs:
+        q, k, v = parts(c, c["x"].cuda())
+        args.append((q, k, v, torch.tensor(c["start"], dtype=torch.int32, device="cuda"), torch.zeros(q.shape, dtype=q.dtype, device="cuda"), ws, 900))
+    streams = [torch.cuda.Stream(), torch.cuda.Stream()]
+    torch.cuda.synchronize()
+    for _ in range(20):
+        for a, s in zip(args, streams):
+            m.kv_attend_prompt(*a, scale=0.08, stream=s)
+    torch.cuda.synchronize()
+    for a, w in zip(args, want):
+        assert torch.equal(a[4].cpu(), w)
+
+
 def test_padded_batches_and_starts_out_of_range():
     """Positions before the first row and behind the last are left alone; starts out of range stay inside."""
     c = make([40, 50, 60, 30], 4, 2, 64, torch.bfloat16, 32)
