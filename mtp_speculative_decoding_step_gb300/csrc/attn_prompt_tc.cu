@@ -234,7 +234,7 @@ __device__ __forceinline__ bool find_unit(const PromptArgs& a, int per, long lon
 constexpr int kUnits = 4;  // units handed out ahead
 
 struct PromptMeta {
-  uint64_t full[8], empty[8], s_full[2], p_full[2][2], pv_done[2], m_full[2][4], l_full[2][4], q_full, q_empty, o_empty[2], v_go, v_ok, drain;
+  uint64_t full[8], empty[8], s_full[2], p_full[2][2], pv_done[2], m_full[2][4], l_full[kMeets], q_full, q_empty, o_empty[2], v_go, v_ok, drain;
   uint64_t unit_full[kUnits], unit_empty[kUnits];
   Unit unit[kUnits];
   uint32_t tmem, copied;
@@ -306,11 +306,9 @@ __global__ void __launch_bounds__(kPromptThreads, 1)
       for (int h = 0; h < 2; ++h) mbar_init(smem_u32(&M.p_full[i][h]), 4);
       mbar_init(smem_u32(&M.pv_done[i]), 1);
       mbar_init(smem_u32(&M.o_empty[i]), 4);
-      for (int w = 0; w < 4; ++w) {
-        mbar_init(smem_u32(&M.m_full[i][w]), 1);
-        mbar_init(smem_u32(&M.l_full[i][w]), 1);
-      }
+      for (int w = 0; w < 4; ++w) mbar_init(smem_u32(&M.m_full[i][w]), 1);
     }
+    for (int i = 0; i < kMeets; ++i) mbar_init(smem_u32(&M.l_full[i]), 1);
     mbar_init(smem_u32(&M.q_full), 1);
     mbar_init(smem_u32(&M.q_empty), 1);
     mbar_init(smem_u32(&M.v_go), 1);
@@ -781,10 +779,10 @@ __global__ void __launch_bounds__(kPromptThreads, 1)
       if (S::QT == 1) {  // the groups' sums, then half of the dimensions each
         // Two warps have the same rows. Each says twice a unit where it is: that its maxima are written, that its sums
         // are. (Not a barrier of the two groups: one that had left would keep the other for good.)
-        auto meet = [&](uint32_t parity) {
+        auto meet = [&](int time) {
           __syncwarp();
-          if (lane == 0) mbar_arrive(smem_u32(&M.l_full[slot][quarter]));
-          ok = ready(&M.l_full[slot ^ 1][quarter], parity);
+          if (lane == 0) mbar_arrive(smem_u32(&M.l_full[meet_barrier(time, slot, quarter)]));
+          ok = ready(&M.l_full[meet_barrier(time, slot ^ 1, quarter)], meet_parity(time, i));
         };
         if (!ok) break;
         meet(0);

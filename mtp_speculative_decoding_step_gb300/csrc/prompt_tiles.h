@@ -31,4 +31,14 @@ inline long long prompt_most_tiles(int tokens, int rows, int G, int tile) {
   return (long long)tokens * G / tile + (tokens < rows ? tokens : rows);
 }
 
+// Two warps (one of each group, `slot` 0 and 1) meet twice at the end of a unit: each arrives on a barrier of its own
+// (which counts to one) and waits for the other's. A warp goes on as soon as the other has arrived, which may not have
+// looked yet: were both times on one barrier, its second arrival could end the phase that the other still waits to see
+// ended, and each would wait for the other. With a barrier for each time, a warp is back at the first only behind the
+// second, where the other arrives after it has seen the first.
+constexpr int kMeets = 16;  // 2 times, 2 groups, 4 warps of a group
+PROMPT_TILES int meet_barrier(int time, int slot, int quarter) { return (time * 2 + slot) * 4 + quarter; }
+// The parity of the phase that the block's unit number `unit` ends there.
+PROMPT_TILES unsigned meet_parity(int /*time*/, int unit) { return unit & 1; }
+
 }  // namespace mtp
