@@ -284,6 +284,7 @@ mtp_status kv_attend_prompt(mtp_stream stream, int32_t rows, int32_t n_q, int32_
   }
   if (cross(d_out, n_out, d_start, n_start) || cross(d_lse, n_lse, d_start, n_start) || cross(d_out, n_out, d_lse, n_lse))
     return MTP_ERR_BAD_ARG;
+  a.out_whole = (reinterpret_cast<uintptr_t>(d_out) & 31) == 0;
   cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
   cudaError_t e;
   if (dtype == MTP_DTYPE_BF16) e = launch_prompt_tc(a, head_dim, s);

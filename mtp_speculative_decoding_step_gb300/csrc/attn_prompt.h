@@ -15,6 +15,7 @@ struct PromptArgs {
   int rows, n_q, n_kv, tokens, window;
   float scale;
   int group;  // bf16: heads to a query tile
+  int out_whole;  // bf16: every 32 bytes of an output row are one sector
 };
 
 // The row and the query tile (`tile` rows of G a position) of tile number x, counted from the last row's last
