@@ -4,11 +4,9 @@
 //   O[128 queries][DH]      += P . V         P = 2^(c s - m) in tensor memory, V in shared memory
 //
 // The query rows of the heads that share a KV head are taken position-major, a
-// query tile being as many whole positions as 128 rows hold. Two query tiles are
-// a unit, which reads its keys once: both in one block (DH <= 128), or one each in
-// the two blocks of a cluster (DH = 256, where O takes half of tensor memory), which
-// copy half of every tile of K and V each, to both. Blocks stay and take units in turn,
-// the longest first. 12 warps:
+// query tile being as many whole positions as 128 rows hold. A block takes a unit of
+// two query tiles, which reads its keys once, or of one (DH = 256, where O takes half
+// of tensor memory). Blocks stay and take units in turn, the longest first. 12 warps:
 //   warps 0-7   softmax: two groups of 128 threads, thread = query row. An item is a
 //               query tile's 128 keys; items alternate between two places for S in
 //               tensor memory, group s has place s. With two query tiles a group has
@@ -26,13 +24,17 @@
 // rows they are. Every wait is bounded: on expiry the block raises the status
 // word, waits for its copies, frees its tensor memory and returns.
 //
-// What it measured: 8192 positions of 24 heads on 4 of 256 471 us, 1.75 PFLOP/s; of 32 on 8 of 128 316 us, 1.74 PFLOP/s; of
-// 32 on 4 of 64 278 us, 0.99 PFLOP/s. The tensor pipe is active 75 % (256 dimensions), shared memory 79 % on its side: S
-// reads 8 KB an MMA of 64 cycles and the copies write as much again. With 64 dimensions the softmax is longer than the
-// products. Short prompts wait on one query tile's chain: with 512 positions of 128 dimensions a unit is 18,500 cycles, of
-// which the MMAs take 5300; the softmax of its 2.6 items 6700, waits for S between them 2500, the first S 1500, the last
-// product 1000, O's way out 4000. 32 rows of those take 104 us (0.66 PFLOP/s), of 24 heads of 256 166 us (0.62), 32 rows of
-// 1 to 2047 of 8 heads on 2 of 128 92 us (1.02).
+// Each block copies its own tiles, from L2 where another has the same. Two blocks of 256 dimensions that shared a unit's
+// keys, half of each tile copied by either to both, took 484 us where this takes 500 (24 heads on 4, 8192 positions), 330
+// where it takes 361 (8 prompts of 2048), and 80 where it takes 72 (64 of 128); but such copies have to stay within one
+// GPU's memory, which a call here says nothing about.
+//
+// What it measured: 8192 positions of 24 heads on 4 of 256 500 us, 1.65 PFLOP/s; of 32 on 8 of 128 311 us, 1.77 PFLOP/s; of
+// 32 on 4 of 64 278 us, 0.99 PFLOP/s. With 64 dimensions the softmax is longer than the products. Short prompts wait on one
+// query tile's chain: with 512 positions of 128 dimensions a unit is 18,500 cycles, of which the MMAs take 5300; the softmax
+// of its 2.6 items 6700, waits for S between them 2500, the first S 1500, the last product 1000, O's way out 4000. 32 rows of
+// those take 104 to 112 us (0.61 to 0.66 PFLOP/s), of 24 heads of 256 179 us (0.58), 32 rows of 1 to 2047 of 8 heads on 2 of
+// 128 92 us (1.02).
 #include <algorithm>
 #include <cfloat>
 #include <mutex>
@@ -110,40 +112,12 @@ __device__ __forceinline__ void st_shared16(uint32_t addr, uint4 v) {
   asm volatile("st.shared.v4.b32 [%0], {%1, %2, %3, %4};" ::"r"(addr), "r"(v.x), "r"(v.y), "r"(v.z), "r"(v.w) : "memory");
 }
 
-// A box of a tensor (head dimension, head, position) to this block's shared memory, or to both blocks' of the cluster.
-template <int CL>
+// A box of a tensor (head dimension, head, position) to shared memory.
 __device__ __forceinline__ void tma_box(uint32_t dst, const CUtensorMap* map, int x, int head, int pos, uint32_t bar) {
-  if constexpr (CL == 1) {
-    asm volatile(
-        "cp.async.bulk.tensor.3d.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1, {%2, %3, %4}], [%5];" ::"r"(dst),
-        "l"((uint64_t)map), "r"(x), "r"(head), "r"(pos), "r"(bar)
-        : "memory");
-  } else {
-    asm volatile(
-        "cp.async.bulk.tensor.3d.shared::cluster.global.mbarrier::complete_tx::bytes.multicast::cluster [%0], [%1, {%2, %3, %4}], [%5], "
-        "%6;" ::"r"(dst),
-        "l"((uint64_t)map), "r"(x), "r"(head), "r"(pos), "r"(bar), "h"((uint16_t)3)
-        : "memory");
-  }
-}
-
-// Arrives on the barrier at this place in this block, or in both blocks of the cluster, when the MMAs issued so far are done.
-template <int CL>
-__device__ __forceinline__ void commit_all(uint32_t bar) {
-  if constexpr (CL == 1) {
-    mma_commit_elect(bar);
-  } else {
-    asm volatile(
-        "{\n\t.reg .pred q;\n\t"
-        "elect.sync _|q, 0xffffffff;\n\t"
-        "@q tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.multicast::cluster.b64 [%0], %1;\n\t}" ::"r"(bar),
-        "h"((uint16_t)3)
-        : "memory");
-  }
-}
-
-__device__ __forceinline__ void cluster_sync() {
-  asm volatile("barrier.cluster.arrive.release.aligned;\n\tbarrier.cluster.wait.acquire.aligned;" ::: "memory");
+  asm volatile(
+      "cp.async.bulk.tensor.3d.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1, {%2, %3, %4}], [%5];" ::"r"(dst),
+      "l"((uint64_t)map), "r"(x), "r"(head), "r"(pos), "r"(bar)
+      : "memory");
 }
 
 __device__ __forceinline__ uint32_t pack_bf16(float lo, float hi) {
@@ -161,8 +135,7 @@ constexpr int kMeta = 3 << 10;  // bytes of PromptMeta, rounded up
 
 template <int DH>
 struct PromptShape {
-  static constexpr int QT = DH == 256 ? 1 : 2;    // query tiles of a block
-  static constexpr int CL = DH == 256 ? 2 : 1;    // blocks of a unit
+  static constexpr int QT = DH == 256 ? 1 : 2;    // query tiles of a unit
   static constexpr int CPT = DH == 256 ? 2 : 1;   // ring stages of a tile of K or V
   static constexpr int NS = DH == 64 ? 8 : 5;     // ring stages
   static constexpr int kHalves = DH == 64 ? 1 : 2;  // P is given on in one piece or in two (64 dimensions' products are too short to wait twice)
@@ -292,20 +265,19 @@ __global__ void __launch_bounds__(kPromptThreads, 1)
     k_prompt_tc(const __grid_constant__ PromptArgs a, const __grid_constant__ CUtensorMap mq, const __grid_constant__ CUtensorMap mk,
                 const __grid_constant__ CUtensorMap mv) {
   using S = PromptShape<DH>;
-  constexpr int CL = S::CL;
   extern __shared__ __align__(1024) uint8_t smem_raw[];
   auto& M = *reinterpret_cast<PromptMeta*>(smem_raw + S::oMeta);
   const uint32_t sm = smem_u32(smem_raw);
   const int warp = __shfl_sync(0xFFFFFFFFu, (int)threadIdx.x >> 5, 0), lane = threadIdx.x & 31;
-  const int G = a.group, rank = CL == 1 ? 0 : (int)(blockIdx.x & 1);
-  const int PT = 128 / G;  // positions of a query tile
+  const int G = a.group;
+  const int PT = 128 / G, per = S::QT * PT;  // positions of a query tile, of a unit
   volatile int* fail = &M.fail;
   auto ready = [&](uint64_t* bar, uint32_t parity) { return wait(bar, parity, fail); };
 
   if (threadIdx.x == 0) {
     for (int i = 0; i < 8; ++i) {
       mbar_init(smem_u32(&M.full[i]), 1);
-      mbar_init(smem_u32(&M.empty[i]), CL);
+      mbar_init(smem_u32(&M.empty[i]), 1);
     }
     for (int i = 0; i < 2; ++i) {
       mbar_init(smem_u32(&M.s_full[i]), 1);
@@ -337,7 +309,6 @@ __global__ void __launch_bounds__(kPromptThreads, 1)
   }
   tc_fence_before();
   __syncthreads();
-  if (CL > 1) cluster_sync();  // the other block's barriers are there
   tc_fence_after();
   pdl_trigger();
   const uint32_t tmem = M.tmem;
@@ -348,8 +319,8 @@ __global__ void __launch_bounds__(kPromptThreads, 1)
   };
   auto span = [&](const Unit& u) {
     Span s;
-    s.p0 = u.j * 2 * PT;
-    s.p1 = min(u.n, s.p0 + 2 * PT) - 1;
+    s.p0 = u.j * per;
+    s.p1 = min(u.n, s.p0 + per) - 1;
     s.t_first = a.window > 0 ? max(0, s.p0 - (a.window - 1)) / 128 : 0;
     s.nt = s.p1 / 128 + 1 - s.t_first;
     return s;
@@ -384,22 +355,22 @@ __global__ void __launch_bounds__(kPromptThreads, 1)
         mbar_expect_tx(bar, S::kStage);
         M.copied = at + 1;
         if constexpr (DH == 256) {
-          // K: 128 positions of half the dimensions; V: 64 positions of all. Half of it from each block
+          // K: 128 positions of half the dimensions; V: 64 positions of all
           if (!is_v) {
-            tma_box<CL>(dst + rank * 16384, map, (2 * c + rank) * 64, head, pos, bar);
+            for (int b = 0; b < 2; ++b) tma_box(dst + b * 16384, map, (2 * c + b) * 64, head, pos, bar);
           } else {
-            for (int b = 2 * rank; b < 2 * rank + 2; ++b) tma_box<CL>(dst + b * 8192, map, b * 64, head, pos + 64 * c, bar);
+            for (int b = 0; b < 4; ++b) tma_box(dst + b * 8192, map, b * 64, head, pos + 64 * c, bar);
           }
         } else {
-          for (int b = 0; b < DH / 64; ++b) tma_box<CL>(dst + b * 16384, map, b * 64, head, pos, bar);
+          for (int b = 0; b < DH / 64; ++b) tma_box(dst + b * 16384, map, b * 64, head, pos, bar);
         }
       }
     };
     // unit i of this block, found and handed out; false behind the last
     auto hand_out = [&](int i, Unit& u) {
       // there and back: who has the longest unit of one turn has the shortest of the next
-      const int blocks = gridDim.x / CL, b = blockIdx.x / CL;
-      if (!find_unit(a, 2 * PT, (long long)i * blocks + (i & 1 ? blocks - 1 - b : b), u)) u.n = 0;
+      const int blocks = gridDim.x, b = blockIdx.x;
+      if (!find_unit(a, per, (long long)i * blocks + (i & 1 ? blocks - 1 - b : b), u)) u.n = 0;
       if (i >= kUnits && !ready(&M.unit_empty[i % kUnits], (i / kUnits - 1) & 1)) return false;
       if (lane == 0) {
         M.unit[i % kUnits] = u;
@@ -420,7 +391,7 @@ __global__ void __launch_bounds__(kPromptThreads, 1)
           mbar_expect_tx(smem_u32(&M.q_full), S::QT * (DH / 64) * PT * G * 128);
           for (int q = 0; q < S::QT; ++q)
             for (int b = 0; b < DH / 64; ++b)
-              tma_box<1>(sm + q * 128 * DH * 2 + b * 16384, &mq, b * 64, u.grp * G, u.a0 + s.p0 + (CL == 2 ? rank : q) * PT, smem_u32(&M.q_full));
+              tma_box(sm + q * 128 * DH * 2 + b * 16384, &mq, b * 64, u.grp * G, u.a0 + s.p0 + q * PT, smem_u32(&M.q_full));
         }
         const int head = u.grp * G / (a.n_q / a.n_kv), pos = u.a0 + s.t_first * 128;
         if (DH == 256) {
@@ -442,7 +413,7 @@ __global__ void __launch_bounds__(kPromptThreads, 1)
       ok = __shfl_sync(0xFFFFFFFFu, ok, 0);
       if (!ok) break;
     }
-    // the last arrivals on this block's barriers, the other block's among them
+    // the last arrivals on this block's barriers
     if (lane == 0)
       for (int i = max(0, at - S::NS); i < at && ok; ++i) ok = wait(&M.empty[i % S::NS], i / S::NS & 1, fail);
     __syncwarp();
@@ -530,7 +501,7 @@ __global__ void __launch_bounds__(kPromptThreads, 1)
             mma_commit_elect(smem_u32(&M.s_full[0]));
             products_s(1, 1, c, ring.st);
           }
-          commit_all<CL>(smem_u32(&M.empty[ring.st]));
+          mma_commit_elect(smem_u32(&M.empty[ring.st]));
           ring.next();
         }
         mma_commit_elect(smem_u32(&M.s_full[S::QT == 2 ? 1 : j]));
@@ -565,12 +536,12 @@ __global__ void __launch_bounds__(kPromptThreads, 1)
               products_o(slot, c, v.st, lo, hi, acc);
             }
             ++done[slot];
-            if (slot == 1) commit_all<CL>(smem_u32(&M.empty[v.st]));
+            if (slot == 1) mma_commit_elect(smem_u32(&M.empty[v.st]));
             if (j + 1 == sp.nt) mma_commit_elect(smem_u32(&M.pv_done[slot]));
             if (more) {
               if (slot == 0) full(k);
               products_s(slot, slot, 0, k.st);
-              if (slot == 1) commit_all<CL>(smem_u32(&M.empty[k.st]));
+              if (slot == 1) mma_commit_elect(smem_u32(&M.empty[k.st]));
               mma_commit_elect(smem_u32(&M.s_full[slot]));
             }
           }
@@ -589,7 +560,7 @@ __global__ void __launch_bounds__(kPromptThreads, 1)
             if (clean && c == 0) await(&M.v_ok, edges++ & 1);
             if (!clean && c == 1) full(r);
             products_o(slot, c, r.st, lo, hi, acc);
-            commit_all<CL>(smem_u32(&M.empty[r.st]));
+            mma_commit_elect(smem_u32(&M.empty[r.st]));
             r.next();
           }
           ++done[slot];
@@ -599,7 +570,7 @@ __global__ void __launch_bounds__(kPromptThreads, 1)
             for (int c = 0; c < S::CPT; ++c) {
               full(ring);
               products_s(slot, 0, c, ring.st);
-              commit_all<CL>(smem_u32(&M.empty[ring.st]));
+              mma_commit_elect(smem_u32(&M.empty[ring.st]));
               ring.next();
             }
             mma_commit_elect(smem_u32(&M.s_full[slot]));
@@ -687,7 +658,7 @@ __global__ void __launch_bounds__(kPromptThreads, 1)
     for (int i = 0; ok && take(i, u); ++i) {
       const Span sp = span(u);
       const int items = sp.nt * S::QT;
-      const int q0 = sp.p0 + (CL == 2 ? rank : slot) * PT, q1 = min(u.n, q0 + PT) - 1;  // the query tile's positions
+      const int q0 = sp.p0 + (S::QT == 2 ? slot * PT : 0), q1 = min(u.n, q0 + PT) - 1;  // the query tile's positions
       const bool real = in_pos < PT && q0 + in_pos < u.n;
       const int pos = real ? q0 + in_pos : -1;
       float m = -INFINITY, l = 0.f;
@@ -885,7 +856,6 @@ __global__ void __launch_bounds__(kPromptThreads, 1)
     mbar_wait(smem_u32(&M.q_full), 1, kAttnWaitLimit);
   }
   __syncthreads();
-  if (CL > 1) cluster_sync();  // the other block's copies and arrivals end here too
   tc_fence_after();
   if (warp == 0) asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, 512;" ::"r"(tmem) : "memory");
 }
@@ -926,22 +896,10 @@ cudaError_t launch(PromptArgs a, cudaStream_t s) {
       set[dev] = true;
     }
   }
-  const long long units = prompt_most_tiles(a.tokens, a.rows, 1, 2 * (128 / a.group)) * (a.n_q / a.group);
-  cudaLaunchConfig_t cfg = {};
-  cfg.gridDim = dim3((unsigned)std::min<long long>(units, device_sm_count() / S::CL) * S::CL);
-  cfg.blockDim = dim3(kPromptThreads);
-  cfg.dynamicSmemBytes = S::kSmem;
-  cfg.stream = s;
-  cudaLaunchAttribute at[2];
-  at[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
-  at[0].val.programmaticStreamSerializationAllowed = 1;
-  at[1].id = cudaLaunchAttributeClusterDimension;
-  at[1].val.clusterDim.x = S::CL;
-  at[1].val.clusterDim.y = at[1].val.clusterDim.z = 1;
-  cfg.attrs = at;
-  cfg.numAttrs = S::CL > 1 ? 2 : 1;
+  const long long units = prompt_most_tiles(a.tokens, a.rows, 1, S::QT * (128 / a.group)) * (a.n_q / a.group);
   count_launch();
-  return cudaLaunchKernelEx(&cfg, k_prompt_tc<DH>, a, mq, mk, mv);
+  return launch_pdl(k_prompt_tc<DH>, dim3((unsigned)std::min<long long>(units, device_sm_count())), dim3(kPromptThreads), S::kSmem, s, a,
+                    mq, mk, mv);
 }
 
 }  // namespace
