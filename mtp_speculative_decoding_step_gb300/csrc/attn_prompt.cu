@@ -54,7 +54,7 @@ __global__ void __launch_bounds__(kSimtThreads) k_prompt_simt(const __grid_const
   const int tid = threadIdx.x, tx = tid & 15, ty = tid >> 4, h = blockIdx.x % a.n_q, g = h / (a.n_q / a.n_kv);
   if (tid < 32) {
     int a0 = 0, n = 0, j = 0;
-    const bool some = find_tile(a, 1, S::kRows, blockIdx.x / a.n_q, a0, n, j);
+    const bool some = find_tile(a, S::kRows, blockIdx.x / a.n_q, a0, n, j);
     if (tid == 0) {
       s_at[0] = a0;
       s_at[1] = some ? n : 0;

@@ -18,36 +18,28 @@ struct PromptArgs {
   int out_whole;  // bf16: every 32 bytes of an output row are one sector
 };
 
-// The row and the query tile (`tile` rows of G a position) of tile number x, counted from the last row's last
-// tile (a row's later tiles are its longest); false past the first. By a whole
-// warp, rows in consecutive groups per lane.
-__device__ __forceinline__ bool find_tile(const PromptArgs& a, int G, int tile, int x, int& a0, int& n, int& j) {
+// The row and the query tile (of `tile` positions) of tile number x, counted from the last row's last tile (a row's
+// later tiles are its longest); false past the first. By a whole warp, rows in consecutive groups per lane.
+__device__ __forceinline__ bool find_tile(const PromptArgs& a, int tile, int x, int& a0, int& n, int& j) {
   const int lane = threadIdx.x & 31, per = (a.rows + 31) / 32, r0 = min(lane * per, a.rows), r1 = min(r0 + per, a.rows);
-  int sum = 0, b0, m;
+  long long sum = 0;
+  int b0, m;
 #pragma unroll 4
   for (int r = r0; r < r1; ++r) {
     prompt_row(a.start, a.tokens, r, b0, m);
-    sum += prompt_tiles(m * G, tile);
+    sum += prompt_tiles(m, tile);
   }
-  int inc = sum;
+  long long inc = sum;
 #pragma unroll
   for (int o = 1; o < 32; o <<= 1) {
-    const int u = __shfl_up_sync(0xFFFFFFFFu, inc, o);
+    const long long u = __shfl_up_sync(0xFFFFFFFFu, inc, o);
     if (lane >= o) inc += u;
   }
-  const int all = __shfl_sync(0xFFFFFFFFu, inc, 31);
-  if (x >= all) return false;
-  x = all - 1 - x;
-  const int owner = __ffs(__ballot_sync(0xFFFFFFFFu, inc - sum <= x && x < inc)) - 1;
-  int at = __shfl_sync(0xFFFFFFFFu, inc - sum, owner), r = __shfl_sync(0xFFFFFFFFu, r0, owner);
-  for (;; ++r) {
-    prompt_row(a.start, a.tokens, r, a0, n);
-    const int t = prompt_tiles(n * G, tile);
-    if (x < at + t) break;
-    at += t;
-  }
-  j = x - at;
-  return true;
+  const long long all = __shfl_sync(0xFFFFFFFFu, inc, 31), y = all - 1 - x;
+  if (y < 0) return false;
+  const int owner = __ffs(__ballot_sync(0xFFFFFFFFu, inc - sum <= y && y < inc)) - 1;
+  const long long at = __shfl_sync(0xFFFFFFFFu, inc - sum, owner);
+  return prompt_tile_from(a.start, a.tokens, a.rows, tile, __shfl_sync(0xFFFFFFFFu, r0, owner), y - at, a0, n, j);
 }
 
 cudaError_t launch_prompt_tc(PromptArgs a, int head_dim, cudaStream_t s);

@@ -24,6 +24,21 @@ PROMPT_TILES void prompt_row(const int* start, int tokens, int r, int& a0, int& 
 // Query tiles of n query rows, `tile` each.
 PROMPT_TILES int prompt_tiles(int n, int tile) { return (n + tile - 1) / tile; }
 
+// The row and the query tile of tile number `left` of the rows from r on; false behind the last row. (64 bits: rows
+// whose starts go up and down hold the same positions many times.)
+PROMPT_TILES bool prompt_tile_from(const int* start, int tokens, int rows, int tile, int r, long long left, int& a0, int& n, int& j) {
+  for (; r < rows; ++r) {
+    prompt_row(start, tokens, r, a0, n);
+    const int t = prompt_tiles(n, tile);
+    if (left < t) {
+      j = (int)left;
+      return true;
+    }
+    left -= t;
+  }
+  return false;
+}
+
 // Blocks that hold all rows' query tiles of `tile` query rows, G a position,
 // whatever the rows' lengths are: a row's last tile may be short, so rows add one
 // each at the most.
