@@ -488,7 +488,7 @@ mtp_status mtp_rope_init(int32_t rot_dim, double theta, const double* h_freq, mt
  * kv_q4_append_rope — norms, rotation and append of a projection's rows.
  * Queries and keys: y = x / sqrt(mean x^2 + eps) * w over the head (without
  * d_q_norm or d_k_norm: y = x), then the pairs (y_i, y_{i + rot_dim / 2}) turned
- * by d_pos * frequency i, as exactly at far positions as at near ones. Queries
+ * by d_pos * frequency i, a frequency held to 2^-51 of itself. Queries
  * go to d_q_out, keys to the cache and, unless it is NULL, to d_k_out; values go
  * to the cache as they are. The cache's 4 bits are rounded (as by kv_q4_append)
  * from keys that are good to 2^-30, not from d_k_out.

@@ -194,7 +194,8 @@ int columns(int n_q, int n_kv, int max_q, bool wide) {
 // was measured with 24 heads on 4 of 256, in us: a block's tiles at 1.3, 1.66 or 2.27 with 32, 64 or 128 columns, and 20,
 // 28 or 32 for the rest. Times with these: one row of 16 nodes at 4096 positions 25.0, 28.6, 33.0; of 33 nodes 27.4,
 // 37.0, 39.8; of 64 at 16,384 72.5, 67.4, 58.7; eight rows of 16 at 8192 70.9, 73.4, 64.0, of 33 147, 117, 92. (Eight rows
-// of 33 of 8 heads on 2 of 128 are taken for equal: 56, 60, 62.) The lengths are taken to be what the block table holds;
+// of 33 of 8 heads on 2 of 128 are taken for equal: 56, 60, 62.) The lengths are taken to be what the block table holds
+// (with room for 37,376 positions or more one row of 16 nodes takes 128 columns, however short it is);
 // no more columns than the workspace has room for.
 int tree_columns(int widest, long long query_rows, long long heads, long long tiles, int blocks) {
   constexpr float kTile[3] = {1.3f, 1.66f, 2.27f}, kRest[3] = {20.f, 28.f, 32.f};

@@ -9,7 +9,7 @@
 //
 // Angles. f_i is held as a fraction of a turn in units of 2^-64, so pos f_i
 // modulo a turn is one wrapping 64-bit product, exact but for f_i's own rounding
-// (2^-53 of it): position 2^20 turns as exactly as position 1. The nearest 64th of
+// (2^-53 of it): at position 2^20 that is 2^-33 radians of the fastest pair. The nearest 64th of
 // a turn comes off and is looked up, the rest (0.05 radians at most) goes through
 // the first terms of the sine's and cosine's series; the two are joined by the
 // addition theorems. Everything is held in two floats, good to 2^-32.
